@@ -430,6 +430,129 @@ int sinkhorn_sparse_barycentric(sinkhorn_problem* p, double eps, const float* g,
                                 const float* f_hint, int32_t B, const int64_t* ptr,
                                 const int32_t* idx, float* T, float* grad);
 
+/* ---------------------------------------------------------------------------
+ * Attention between two sets of different length.
+ *
+ * The row softmax of an f-step and the weighted average of the barycentric
+ * projection in feature spaces of up to 128 dimensions, with inner-product
+ * scores, several heads and 16-bit types:
+ *   s_ij  = scale q_i . k_j + key_bias_j
+ *   lse_i = log sum_j exp(s_ij)
+ *   out_i = sum_j exp(s_ij - lse_i) v_j
+ * For the squared-Euclidean cost s ||x - y||^2 at eps this is the barycentric
+ * projection of the plan rows of x (for any d and any values in place of the
+ * target points) with q = x, k = y, scale = 2 s / eps and
+ * key_bias_j = log b_j + (g_j - s ||y_j||^2) / eps; the terms of x_i cancel.
+ * The weight that the keys gather under row weights a_i is then the plan's
+ * column marginal.
+ *
+ * Layout: q [batch][len_q][heads_q][d], k [batch][len_k][heads_kv][d],
+ * v [batch][len_k][heads_kv][dv], out and dout [batch][len_q][heads_q][dv],
+ * gradients as what they are gradients of; each by its strides in elements
+ * (batch, row, head), the last dimension contiguous. Inputs may have any
+ * strides >= 0 and any alignment (rows that are 16-byte aligned and a whole
+ * number of 16-byte chunks long are read 16 bytes at a time); the elements of
+ * an output may not overlap. Query head h reads key head
+ * h / (heads_q / heads_kv). lse is [batch][heads_q][len_q], gathered weights are
+ * [batch][heads_kv][len_k], row weights [batch][len_q], contiguous fp32.
+ *
+ * Masks. A key takes no part, whatever its k and v hold, when its index is at
+ * or behind key_lengths[batch], or its bias is -infinity or at most -1e30. A row
+ * without any key gives out = 0, lse = -infinity and no gradient. Rows at or
+ * behind query_lengths[batch] give the same, whatever they hold, and add to no
+ * gradient or weight. Lengths outside [0, len] are taken as the nearest bound.
+ * Anything non-finite elsewhere gives non-finite results.
+ *
+ * Arithmetic: scores, softmax statistics and all sums in fp32; with 16-bit
+ * types the weights (and in the backward pass their derivatives) are rounded
+ * to that type for the product that follows. fp32 products are fp32
+ * throughout. Results do not depend on scheduling: no atomics on floating
+ * point, splits are joined in a fixed order.
+ *
+ * All calls are asynchronous on `stream` (a hipStream_t of the current
+ * device), allocate nothing, keep no state and may be captured in a graph;
+ * a workspace must not be used by two calls that may run at the same time.
+ * ------------------------------------------------------------------------- */
+#define SINKHORN_F32 0
+#define SINKHORN_F16 1
+#define SINKHORN_BF16 2
+
+typedef struct {
+  int32_t dtype;              /* SINKHORN_F32, _F16 or _BF16: q, k, v, out and their gradients */
+  int32_t batch;
+  int32_t heads_q, heads_kv;  /* heads_q a multiple of heads_kv */
+  int32_t d, dv;              /* 1 .. 128 (SINKHORN_ERR_UNSUPPORTED above) */
+  int64_t len_q, len_k;       /* len_q * heads_q / heads_kv and len_k below 2^31 */
+  double scale;               /* finite and > 0 */
+  int64_t q_stride[3], k_stride[3], v_stride[3], out_stride[3];     /* elements: batch, row, head */
+  int64_t dout_stride[3], dq_stride[3], dk_stride[3], dv_stride[3]; /* backward only */
+  const float* key_bias;         /* device, nullable: [len_k] rows by bias_stride */
+  int64_t bias_stride[2];        /* elements: batch, key head (0: shared) */
+  const int32_t* query_lengths;  /* device [batch], nullable: len_q */
+  const int32_t* key_lengths;    /* device [batch], nullable: len_k */
+} sinkhorn_attention;
+
+/* Bytes of device workspace (16-byte aligned) that a call on `at` needs; may
+ * be 0. Host only. */
+#define SINKHORN_ATTEND 0         /* sinkhorn_cross_attention without mass_out */
+#define SINKHORN_ATTEND_MASS 1    /* sinkhorn_cross_attention with mass_out */
+#define SINKHORN_ATTEND_GRAD 2    /* sinkhorn_cross_attention_grad */
+#define SINKHORN_ATTENTION_MASS 3 /* sinkhorn_attention_mass */
+int sinkhorn_attention_workspace(const sinkhorn_attention* at, int32_t what, int64_t* bytes);
+
+/* Forward pass: out and lse. With mass_out also the weight each key gathers,
+ *   mass_out_j = mass_in_j + sum over rows i and the heads that share the key
+ *                of row_weight_i exp(s_ij - lse_i)
+ * (mass_in nullable: 0, and may be mass_out; row_weight nullable: 1). When all
+ * rows of a key head (len_q * heads_q / heads_kv) are at most 32, as for single
+ * tokens, the weight comes from the scores of the same pass and the keys are
+ * read once. out may not be an input. */
+int sinkhorn_cross_attention(const sinkhorn_attention* at, const void* q, const void* k,
+                             const void* v, void* out, float* lse, const float* row_weight,
+                             const float* mass_in, float* mass_out, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+/* Backward pass from the forward pass's out and lse and the gradient dout of
+ * out: dq, dk and dv (dk and dv summed over the rows and the heads that share
+ * a key head; zero for keys that take no part). key_bias is held fixed. */
+int sinkhorn_cross_attention_grad(const sinkhorn_attention* at, const void* q, const void* k,
+                                  const void* v, const void* out, const float* lse,
+                                  const void* dout, void* dq, void* dk, void* dv, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
+/* The gathered weight alone, from a forward pass's lse: mass_out as above. */
+int sinkhorn_attention_mass(const sinkhorn_attention* at, const void* q, const void* k,
+                            const float* lse, const float* row_weight, const float* mass_in,
+                            float* mass_out, void* workspace, int64_t workspace_bytes,
+                            void* stream);
+
+typedef struct {
+  int32_t dtype;
+  int32_t batch, heads;
+  int32_t d, dv;
+  int64_t len;             /* keys per batch entry and head, below 2^31 */
+  int64_t keep;            /* most keys that remain, >= 1 */
+  int64_t first, recent;   /* always kept; first + recent <= keep */
+  int64_t k_stride[3], v_stride[3];          /* elements: batch, row, head */
+  int64_t k_out_stride[3], v_out_stride[3];
+  const int32_t* key_lengths;  /* device [batch], nullable: len */
+} sinkhorn_cache;
+
+/* Eviction by gathered weight (columns pruned by their mass, as
+ * sinkhorn_sparsify prunes entries): for each batch entry and head, of the
+ * live keys the `first` first, the `recent` last and the heaviest of the
+ * others are kept, min(live, keep) in all, in their order. Equal weights: the
+ * lower index; a NaN counts as the lowest weight. With
+ * cap = min(keep, len): k_out and v_out (strided, room for cap rows) receive
+ * the kept rows, mass_out [batch][heads][cap] their weights and index_out
+ * [batch][heads][cap] the positions they had; lengths_out [batch] the number
+ * kept. Behind that number k_out and v_out are left as they were, mass_out is
+ * 0 and index_out -1. Outputs may not overlap inputs or each other. d and dv
+ * are not limited to 128. Asynchronous on `stream`; no workspace. */
+int sinkhorn_cache_evict(const sinkhorn_cache* cache, const void* k, const void* v,
+                         const float* mass, void* k_out, void* v_out, float* mass_out,
+                         int32_t* index_out, int32_t* lengths_out, void* stream);
+
 /* Measurement hook. `kinds` is a bit set of the kernels to time: every later
  * launch of a selected kernel carries two HIP events that its own dispatch
  * records at the kernel's start and end (hipExtLaunchKernelGGL), so the time

@@ -26,6 +26,10 @@ __all__ = [
     "Problem",
     "mean_sqeuclid",
     "morton_order",
+    "cross_attention",
+    "cross_attention_grad",
+    "attention_mass",
+    "cache_evict",
     "lib",
     "LIB_PATH",
     "OK",
@@ -141,6 +145,55 @@ class _MultiscaleReportC(ctypes.Structure):
     ]
 
 
+_i64x2 = _i64 * 2
+_i64x3 = _i64 * 3
+
+
+class _AttentionC(ctypes.Structure):
+    _fields_ = [
+        ("dtype", _i32),
+        ("batch", _i32),
+        ("heads_q", _i32),
+        ("heads_kv", _i32),
+        ("d", _i32),
+        ("dv", _i32),
+        ("len_q", _i64),
+        ("len_k", _i64),
+        ("scale", _f64),
+        ("q_stride", _i64x3),
+        ("k_stride", _i64x3),
+        ("v_stride", _i64x3),
+        ("out_stride", _i64x3),
+        ("dout_stride", _i64x3),
+        ("dq_stride", _i64x3),
+        ("dk_stride", _i64x3),
+        ("dv_stride", _i64x3),
+        ("key_bias", _p),
+        ("bias_stride", _i64x2),
+        ("query_lengths", _p),
+        ("key_lengths", _p),
+    ]
+
+
+class _CacheC(ctypes.Structure):
+    _fields_ = [
+        ("dtype", _i32),
+        ("batch", _i32),
+        ("heads", _i32),
+        ("d", _i32),
+        ("dv", _i32),
+        ("len", _i64),
+        ("keep", _i64),
+        ("first", _i64),
+        ("recent", _i64),
+        ("k_stride", _i64x3),
+        ("v_stride", _i64x3),
+        ("k_out_stride", _i64x3),
+        ("v_out_stride", _i64x3),
+        ("key_lengths", _p),
+    ]
+
+
 # name -> argtypes (every entry point declared in include/sinkhorn.h)
 _SIGS = {
     "sinkhorn_strerror": ([_i32], ctypes.c_char_p),
@@ -169,6 +222,11 @@ _SIGS = {
     "sinkhorn_solve_multiscale": ([_p, _p, _p, _p, _p], _i32),
     "sinkhorn_sample_indices": ([_i64, _i32, ctypes.c_uint64, ctypes.c_uint64, _p, _p], _i32),
     "sinkhorn_sampled_residual": ([_p, _f64, _p, _p, _i32, _i32, ctypes.c_uint64, _p, _p], _i32),
+    "sinkhorn_attention_workspace": ([_p, _i32, _p], _i32),
+    "sinkhorn_cross_attention": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
+    "sinkhorn_cross_attention_grad": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
+    "sinkhorn_attention_mass": ([_p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
+    "sinkhorn_cache_evict": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p], _i32),
     "sinkhorn_profile_enable": ([_p, _i32], _i32),
     "sinkhorn_profile_read": ([_p, _p, _p, _p], _i32),
     "sinkhorn_probe_issue_rate": ([_i32, _i32, _p, _p, _p, _p], _i32),
@@ -348,6 +406,261 @@ def device_memory(reset: bool = False):
     _check(lib().sinkhorn_device_memory(ctypes.byref(cur), ctypes.byref(peak), ctypes.byref(big),
                                         int(bool(reset))), "device_memory")
     return cur.value, peak.value, big.value
+
+
+# ---------------------------------------------------------------- attention between two sets
+_ATTN_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_ATTEND, _ATTEND_MASS, _ATTEND_GRAD, _ATTENTION_MASS = range(4)
+
+
+def _head_tensor(t, name, dtype=None, shape=None):
+    """A [batch, length, heads, width] tensor of one of the three element types
+    with a contiguous last dimension (the other strides are free)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in _ATTN_DTYPES:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [batch, length, heads, width]")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires grad: these calls record no graph; detach it or use torch.no_grad(), "
+                         "and take gradients from cross_attention_grad")
+    return t
+
+
+def _written(t, name):
+    """An output: no two of its elements may share memory."""
+    span = 1
+    for size, stride in sorted(((n, st) for n, st in zip(t.shape, t.stride()) if n > 1), key=lambda x: x[1]):
+        if stride < span:
+            raise ValueError(f"{name} has overlapping elements")
+        span = stride * size
+    return t
+
+
+def _plain(t, name, dtype, shape):
+    """A contiguous side argument (not necessarily on the device yet)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _same_device(first, others):
+    if first.device.type != "cuda":
+        raise ValueError("the arguments must be device tensors")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"the arguments are on different devices ({first.device}, {t.device})")
+
+
+def _strides3(t):
+    """Element strides of batch, length and head (0 where there is one)."""
+    return _i64x3(*[st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride()[:3])])
+
+
+def _attention(q, k, v, scale, key_bias, query_lengths, key_lengths):
+    _head_tensor(q, "q")
+    B, lq, hq, d = q.shape
+    _head_tensor(k, "k", q.dtype)
+    _, lk, hkv, _ = k.shape
+    if tuple(k.shape) != (B, lk, hkv, d):
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected ({B}, length, heads, {d})")
+    dv = d
+    if v is not None:
+        _head_tensor(v, "v", q.dtype)
+        dv = v.shape[3]
+        if tuple(v.shape) != (B, lk, hkv, dv):
+            raise ValueError(f"v has shape {tuple(v.shape)}, expected ({B}, {lk}, {hkv}, width)")
+    if hkv < 1 or hq < 1 or hq % hkv:
+        raise ValueError(f"{hq} query heads are no multiple of {hkv} key heads")
+    a = _AttentionC(dtype=_ATTN_DTYPES[q.dtype], batch=B, heads_q=hq, heads_kv=hkv, d=d, dv=dv, len_q=lq, len_k=lk,
+                    scale=1.0 / math.sqrt(max(d, 1)) if scale is None else float(scale),
+                    q_stride=_strides3(q), k_stride=_strides3(k))
+    if v is not None:
+        a.v_stride = _strides3(v)
+    if key_bias is not None:
+        if not isinstance(key_bias, torch.Tensor) or key_bias.dtype != torch.float32:
+            raise TypeError("key_bias must be a float32 tensor")
+        if key_bias.requires_grad and torch.is_grad_enabled():
+            raise ValueError("key_bias is held fixed and takes no gradient")
+        if tuple(key_bias.shape) not in ((B, lk), (B, hkv, lk)):
+            raise ValueError(f"key_bias has shape {tuple(key_bias.shape)}, expected ({B}, {lk}) or ({B}, {hkv}, {lk})")
+        if lk > 1 and key_bias.stride(-1) != 1:
+            raise ValueError("the last dimension of key_bias must be contiguous")
+        a.key_bias = key_bias.data_ptr()
+        a.bias_stride = _i64x2(key_bias.stride(0), key_bias.stride(1) if key_bias.dim() == 3 else 0)
+    if query_lengths is not None:
+        a.query_lengths = _plain(query_lengths, "query_lengths", torch.int32, (B,)).data_ptr()
+    if key_lengths is not None:
+        a.key_lengths = _plain(key_lengths, "key_lengths", torch.int32, (B,)).data_ptr()
+    return a
+
+
+def _workspace(a, what, device):
+    n = _i64()
+    _check(lib().sinkhorn_attention_workspace(ctypes.byref(a), what, ctypes.byref(n)), "attention_workspace")
+    return (torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None), n.value
+
+
+def _mass_args(a, row_weight, mass_in, mass_out):
+    B, hkv, lk = a.batch, a.heads_kv, a.len_k
+    if row_weight is not None:
+        _plain(row_weight, "row_weight", torch.float32, (B, a.len_q))
+    if mass_in is not None:
+        _plain(mass_in, "mass_in", torch.float32, (B, hkv, lk))
+    if mass_out is not None:
+        _plain(mass_out, "mass_out", torch.float32, (B, hkv, lk))
+
+
+def cross_attention(q, k, v, *, scale=None, key_bias=None, query_lengths=None, key_lengths=None, row_weight=None,
+                    mass_in=None, mass_out=None, out=None, lse=None):
+    """(out, lse): softmax(scale q.k + key_bias) v for q [B, Lq, Hq, d] against
+    k [B, Lk, Hkv, d] and v [B, Lk, Hkv, dv] (``sinkhorn_cross_attention``).
+
+    out [B, Lq, Hq, dv] has q's type, lse [B, Hq, Lq] is float32. Query head h
+    reads key head h // (Hq / Hkv). scale defaults to d ** -0.5. key_bias
+    (float32, [B, Lk] or [B, Hkv, Lk]) is added to the scores; a key whose bias
+    is <= -1e30 or whose index is >= key_lengths[b] (int32 [B]) takes no part. Rows
+    without keys and rows >= query_lengths[b] give out = 0, lse = -inf.
+
+    With mass_out (float32 [B, Hkv, Lk]) it also receives mass_in (same shape, may
+    be mass_out; default 0) plus the weight each key gathered over rows and
+    heads, rows weighted by row_weight (float32 [B, Lq], default 1).
+
+    For the squared-Euclidean cost at eps, q = x, k = y, scale = 2 s / eps and
+    key_bias = log b + (g - s |y|^2) / eps average v over the plan's rows."""
+    a = _attention(q, k, v, scale, key_bias, query_lengths, key_lengths)
+    B, lq, hq, _ = q.shape
+    shape = (B, lq, hq, v.shape[3])
+    if out is not None:
+        _written(_head_tensor(out, "out", q.dtype, shape), "out")
+    if lse is not None:
+        _plain(lse, "lse", torch.float32, (B, hq, lq))
+    if mass_out is None and (mass_in is not None or row_weight is not None):
+        raise ValueError("mass_in and row_weight need mass_out")
+    _mass_args(a, row_weight, mass_in, mass_out)
+    _same_device(q, (k, v, key_bias, query_lengths, key_lengths, row_weight, mass_in, mass_out, out, lse))
+    with torch.cuda.device(q.device):
+        out = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
+        lse = torch.empty((B, hq, lq), dtype=torch.float32, device=q.device) if lse is None else lse
+        a.out_stride = _strides3(out)
+        ws, n = _workspace(a, _ATTEND if mass_out is None else _ATTEND_MASS, q.device)
+        _check(lib().sinkhorn_cross_attention(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                              _ptr(row_weight), _ptr(mass_in), _ptr(mass_out), _ptr(ws), n,
+                                              _stream(q.device)), "cross_attention")
+    return out, lse
+
+
+def cross_attention_grad(dout, q, k, v, out, lse, *, scale=None, key_bias=None, query_lengths=None, key_lengths=None,
+                         dq=None, dk=None, dv=None):
+    """(dq, dk, dv) from dout, the gradient of out, and the out and lse that
+    cross_attention returned for the same arguments
+    (``sinkhorn_cross_attention_grad``). key_bias is held fixed."""
+    a = _attention(q, k, v, scale, key_bias, query_lengths, key_lengths)
+    B, lq, hq, _ = q.shape
+    shape = (B, lq, hq, v.shape[3])
+    _head_tensor(dout, "dout", q.dtype, shape)
+    _head_tensor(out, "out", q.dtype, shape)
+    _plain(lse, "lse", torch.float32, (B, hq, lq))
+    for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        if t is not None:
+            _written(_head_tensor(t, name, q.dtype, like.shape), name)
+    _same_device(q, (k, v, key_bias, query_lengths, key_lengths, dout, out, lse, dq, dk, dv))
+    with torch.cuda.device(q.device):
+        dq, dk, dv = (torch.empty(like.shape, dtype=q.dtype, device=q.device) if t is None else t
+                      for t, like in ((dq, q), (dk, k), (dv, v)))
+        a.out_stride, a.dout_stride = _strides3(out), _strides3(dout)
+        a.dq_stride, a.dk_stride, a.dv_stride = _strides3(dq), _strides3(dk), _strides3(dv)
+        ws, n = _workspace(a, _ATTEND_GRAD, q.device)
+        _check(lib().sinkhorn_cross_attention_grad(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                                   _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), n,
+                                                   _stream(q.device)), "cross_attention_grad")
+    return dq, dk, dv
+
+
+def attention_mass(q, k, lse, *, scale=None, key_bias=None, query_lengths=None, key_lengths=None, row_weight=None,
+                   mass_in=None, mass_out=None):
+    """The weight each key gathers, [B, Hkv, Lk] float32, from the lse of a
+    forward pass over the same arguments (``sinkhorn_attention_mass``): mass_in
+    (default 0) plus the sum over rows and heads of row_weight exp(s - lse)."""
+    a = _attention(q, k, None, scale, key_bias, query_lengths, key_lengths)
+    _plain(lse, "lse", torch.float32, (a.batch, a.heads_q, a.len_q))
+    _mass_args(a, row_weight, mass_in, mass_out)
+    _same_device(q, (k, key_bias, query_lengths, key_lengths, lse, row_weight, mass_in, mass_out))
+    with torch.cuda.device(q.device):
+        if mass_out is None:
+            mass_out = torch.empty((a.batch, a.heads_kv, a.len_k), dtype=torch.float32, device=q.device)
+        ws, n = _workspace(a, _ATTENTION_MASS, q.device)
+        _check(lib().sinkhorn_attention_mass(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(lse), _ptr(row_weight),
+                                             _ptr(mass_in), _ptr(mass_out), _ptr(ws), n, _stream(q.device)),
+               "attention_mass")
+    return mass_out
+
+
+def cache_evict(k, v, mass, keep: int, *, key_lengths=None, first: int = 0, recent: int = 0, k_out=None, v_out=None,
+                mass_out=None, index_out=None, lengths_out=None):
+    """Prune a cache by gathered weight (``sinkhorn_cache_evict``): of the live
+    keys of k [B, L, H, d], v [B, L, H, dv] keep the `first` first, the `recent`
+    last and the heaviest others by mass [B, H, L] (float32), `keep` in all, in
+    their order. Returns (k_out, v_out, mass_out, index_out, lengths_out): the
+    kept rows [B, C, H, .] with C = min(keep, L), their weights and old positions
+    [B, H, C] (0 and -1 behind the kept ones) and the counts [B] (int32). Rows of
+    k_out and v_out behind the kept ones are left as they were (zero in buffers
+    made here)."""
+    _head_tensor(k, "k")
+    B, n, h, d = k.shape
+    _head_tensor(v, "v", k.dtype)
+    dv = v.shape[3]
+    if tuple(v.shape) != (B, n, h, dv):
+        raise ValueError(f"v has shape {tuple(v.shape)}, expected ({B}, {n}, {h}, width)")
+    _plain(mass, "mass", torch.float32, (B, h, n))
+    keep, first, recent = int(keep), int(first), int(recent)
+    cap = min(keep, n)
+    if keep < 1:
+        raise ValueError("keep must be >= 1")
+    if key_lengths is not None:
+        _plain(key_lengths, "key_lengths", torch.int32, (B,))
+    if k_out is not None:
+        _written(_head_tensor(k_out, "k_out", k.dtype, (B, cap, h, d)), "k_out")
+    if v_out is not None:
+        _written(_head_tensor(v_out, "v_out", k.dtype, (B, cap, h, dv)), "v_out")
+    if mass_out is not None:
+        _plain(mass_out, "mass_out", torch.float32, (B, h, cap))
+    if index_out is not None:
+        _plain(index_out, "index_out", torch.int32, (B, h, cap))
+    if lengths_out is not None:
+        _plain(lengths_out, "lengths_out", torch.int32, (B,))
+    _same_device(k, (v, mass, key_lengths, k_out, v_out, mass_out, index_out, lengths_out))
+    with torch.cuda.device(k.device):
+        # without key_lengths every row of the outputs is written
+        new = torch.empty if key_lengths is None else torch.zeros
+        k_out = new((B, cap, h, d), dtype=k.dtype, device=k.device) if k_out is None else k_out
+        v_out = new((B, cap, h, dv), dtype=k.dtype, device=k.device) if v_out is None else v_out
+        if mass_out is None:
+            mass_out = torch.empty((B, h, cap), dtype=torch.float32, device=k.device)
+        if index_out is None:
+            index_out = torch.empty((B, h, cap), dtype=torch.int32, device=k.device)
+        if lengths_out is None:
+            lengths_out = torch.empty(B, dtype=torch.int32, device=k.device)
+        c = _CacheC(dtype=_ATTN_DTYPES[k.dtype], batch=B, heads=h, d=d, dv=dv, len=n, keep=keep, first=first,
+                    recent=recent, k_stride=_strides3(k), v_stride=_strides3(v), k_out_stride=_strides3(k_out),
+                    v_out_stride=_strides3(v_out), key_lengths=None if key_lengths is None else key_lengths.data_ptr())
+        _check(lib().sinkhorn_cache_evict(ctypes.byref(c), _ptr(k), _ptr(v), _ptr(mass), _ptr(k_out), _ptr(v_out),
+                                          _ptr(mass_out), _ptr(index_out), _ptr(lengths_out), _stream(k.device)),
+               "cache_evict")
+    return k_out, v_out, mass_out, index_out, lengths_out
 
 
 class Problem:

@@ -1,0 +1,376 @@
+// Cross attention, backward. With P = exp(s - lse) recomputed tile by tile and
+// D_r = dout_r . out_r:
+//   dV = P^T dout     dS = P o (dout V^T - D)     dQ = scale dS K     dK = scale dS^T Q
+// in two kernels without atomics, so results do not depend on the order of
+// workgroups: k_grad_q holds rows and runs over keys, k_grad_kv holds keys
+// and runs over the rows of every head that shares them (seven products in
+// place of the five that a single kernel with an atomic dQ would need).
+// Both take their tiles as the forward kernel does: scores with the held side
+// across, the other side down, so that the recomputed weights feed the next
+// product from their registers. When the held side does not fill the chip,
+// the other side is split over workgroups into fp32 partial sums, which
+// k_grad_join adds in a fixed order.
+#pragma once
+
+#include "attention.h"
+
+namespace sk {
+namespace attn {
+
+struct GradArgs {
+  Shape S;
+  int64_t os[3], dos[3], dqs[3], dks[3], dvs[3];
+  const void* out;
+  const void* dout;
+  const float* lse;
+  void* dq;
+  void* dk;
+  void* dv;
+  f32x2* stat;    // [batch * hkv][rows]: lse in log2 units (+inf: the row takes no part), D
+  float* part_q;  // [split][batch * hkv][rows][dp], nullable
+  float* part_k;  // [split][batch * hkv][lk][dp], nullable
+  float* part_v;  // [split][batch * hkv][lk][dvp], nullable
+  int32_t dp, dvp;
+  int32_t split_q, split_kv;
+  int64_t tiles_q, tiles_kv;
+  bool vec_q, vec_k, vec_v;  // dq, dk, dv may be written four elements at a time
+};
+
+// Row statistics: 16 lanes per row.
+template <class T>
+__global__ __launch_bounds__(256) void k_grad_stat(GradArgs A) {
+  const Shape& S = A.S;
+  const int64_t idx = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (idx >= (int64_t)S.batch * S.hkv * S.rows) return;
+  const int64_t pair = idx / S.rows, row = idx - pair * S.rows;
+  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
+  const int64_t qi = row / S.group;
+  const int qh = hk * S.group + (int)(row - qi * S.group);
+  const int ln = threadIdx.x & 15;
+  if (row >= live_rows(S, b)) {
+    if (ln == 0) A.stat[idx] = f32x2{kInf, 0.0f};
+    return;
+  }
+  const T* o = (const T*)A.out + b * A.os[0] + qi * A.os[1] + qh * A.os[2];
+  const T* g = (const T*)A.dout + b * A.dos[0] + qi * A.dos[1] + qh * A.dos[2];
+  float s = 0.0f;
+  for (int c = ln; c < S.dv; c += 16) s = fmaf((float)o[c], (float)g[c], s);
+#pragma unroll
+  for (int x = 8; x > 0; x >>= 1) s += __shfl_xor(s, x, 16);
+  if (ln == 0) {
+    const float e = A.lse[((int64_t)b * S.hq + qh) * S.lq + qi];
+    A.stat[idx] = f32x2{e == -kInf ? kInf : e * (float)kLog2e, s};
+  }
+}
+
+// Writes a transposed result (column: row `row` of the output, down: its
+// elements) either as a partial or rounded to T.
+template <class T, int NDB>
+__device__ __forceinline__ void write_cols(const f32x16 (&x)[NDB], float f, float* prow, int dp, T* orow, int d,
+                                           bool vec, int h) {
+#pragma unroll
+  for (int n = 0; n < NDB; ++n)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int c = 32 * n + 8 * g + 4 * h;
+      const f32x4 v = {f * x[n][4 * g], f * x[n][4 * g + 1], f * x[n][4 * g + 2], f * x[n][4 * g + 3]};
+      if (prow) {
+        if (c < dp) *(f32x4*)(prow + c) = v;
+      } else if (vec) {
+        store4<T, true>(orow, c, d, v);
+      } else {
+        store4<T, false>(orow, c, d, v);
+      }
+    }
+}
+
+// dQ: 4 waves of 32 rows, tiles of KT keys.
+template <class T, int DP, bool AL>
+__global__ __launch_bounds__(256) void k_grad_q(GradArgs A) {
+  using TL = Tile<T, DP>;
+  using V8 = typename Vec<T>::V8;
+  constexpr int KT = sizeof(T) == 2 ? 64 : 32, NT = 256, NS = DP / 16, NDB = DP / 32;
+  __shared__ __attribute__((aligned(16))) char tk[KT * TL::RB], tv[KT * TL::RB];
+  __shared__ __attribute__((aligned(16))) float sterm[KT];
+
+  const Shape& S = A.S;
+  const int64_t pairs = (int64_t)S.batch * S.hkv;
+  const int64_t item = xcd_item(pairs * A.tiles_q * A.split_q);
+  if (item >= pairs * A.tiles_q * A.split_q) return;
+  const int64_t pair = item / (A.tiles_q * A.split_q);
+  const int64_t rest = item - pair * (A.tiles_q * A.split_q);
+  const int64_t tile = rest / A.split_q;
+  const int split = (int)(rest - tile * A.split_q);
+  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int h = lane >> 5, r32 = lane & 31;
+
+  const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
+  const int64_t row0 = tile * 128, row = row0 + 32 * wave + r32;
+  const bool live = row < nrows;
+  const int64_t qi = row / S.group;
+  const int qh = hk * S.group + (int)(row - qi * S.group);
+  const int64_t ntiles = row0 < nrows ? (nkeys + KT - 1) / KT : 0;
+  const int64_t per = (ntiles + A.split_q - 1) / A.split_q;
+  const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
+
+  const T* kbase = (const T*)S.k + b * S.ks[0] + hk * S.ks[2];
+  const T* vbase = (const T*)S.v + b * S.vs[0] + hk * S.vs[2];
+  const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
+
+  V8 qf[NS], gf[NS];
+  {
+    const T* qrow = (const T*)S.q + b * S.qs[0] + qi * S.qs[1] + qh * S.qs[2];
+    const T* grow = (const T*)A.dout + b * A.dos[0] + qi * A.dos[1] + qh * A.dos[2];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      qf[s] = global_frag<T, AL>(qrow, live, s, h, S.d);
+      gf[s] = global_frag<T, AL>(grow, live, s, h, S.dv);
+    }
+  }
+  const f32x2 st = live ? A.stat[pair * S.rows + row] : f32x2{kInf, 0.0f};
+  f32x16 dq[NDB];
+#pragma unroll
+  for (int n = 0; n < NDB; ++n) dq[n] = zero16();
+
+  Stage<T, DP, KT, NT, AL> xk, xv;
+  float term = 0.0f;
+  if (t0 < t1) {
+    xk.load(kbase, S.ks[1], t0 * KT, nkeys, S.d, tid);
+    xv.load(vbase, S.vs[1], t0 * KT, nkeys, S.dv, tid);
+    if (tid < KT) term = column_term(bias, t0 * KT + tid, nkeys);
+  }
+  for (int64_t t = t0; t < t1; ++t) {
+    __syncthreads();
+    if (tid < KT) sterm[tid] = term;
+    __syncthreads();
+    xk.put_masked(tk, sterm, tid);
+    xv.put_masked(tv, sterm, tid);
+    __syncthreads();
+    if (t + 1 < t1) {
+      xk.load(kbase, S.ks[1], (t + 1) * KT, nkeys, S.d, tid);
+      xv.load(vbase, S.vs[1], (t + 1) * KT, nkeys, S.dv, tid);
+      if (tid < KT) term = column_term(bias, (t + 1) * KT + tid, nkeys);
+    }
+#pragma unroll
+    for (int n = 0; n < KT / 32; ++n) {
+      f32x16 p = zero16(), g = zero16();
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        p = mma(TL::row_frag(tk, 32 * n + r32, s, h), qf[s], p);
+        g = mma(TL::row_frag(tv, 32 * n + r32, s, h), gf[s], g);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 ct = *(const f32x4*)&sterm[32 * n + 8 * q + 4 * h];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 4 * q + e;
+          p[i] = ex2(fmaf(p[i], S.c, ct[e]) - st[0]) * (g[i] - st[1]);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const V8 ds = pack<T>(p, s);
+#pragma unroll
+        for (int x = 0; x < NDB; ++x) dq[x] = mma(TL::col_frag(tk, 32 * n + 16 * s, 32 * x, lane), ds, dq[x]);
+      }
+    }
+  }
+  if (row >= S.rows) return;
+  float* prow = A.part_q ? A.part_q + (((int64_t)split * pairs + pair) * S.rows + row) * A.dp : nullptr;
+  T* orow = (T*)A.dq + b * A.dqs[0] + qi * A.dqs[1] + qh * A.dqs[2];
+  write_cols<T, NDB>(dq, S.scale, prow, A.dp, orow, S.d, A.vec_q, h);
+}
+
+// dK and dV: 4 waves of 32 keys, tiles of RT rows.
+template <class T, int DP, bool AL>
+__global__ __launch_bounds__(256) void k_grad_kv(GradArgs A) {
+  using TL = Tile<T, DP>;
+  using V8 = typename Vec<T>::V8;
+  constexpr int RT = sizeof(T) == 2 ? 64 : 32, NT = 256, NS = DP / 16, NDB = DP / 32;
+  __shared__ __attribute__((aligned(16))) char tq[RT * TL::RB], tg[RT * TL::RB];
+  __shared__ __attribute__((aligned(16))) float slse[RT], sdot[RT];
+
+  const Shape& S = A.S;
+  const int64_t pairs = (int64_t)S.batch * S.hkv;
+  const int64_t item = xcd_item(pairs * A.tiles_kv * A.split_kv);
+  if (item >= pairs * A.tiles_kv * A.split_kv) return;
+  const int64_t pair = item / (A.tiles_kv * A.split_kv);
+  const int64_t rest = item - pair * (A.tiles_kv * A.split_kv);
+  const int64_t tile = rest / A.split_kv;
+  const int split = (int)(rest - tile * A.split_kv);
+  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int h = lane >> 5, r32 = lane & 31;
+
+  const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
+  const int64_t key0 = tile * 128, key = key0 + 32 * wave + r32;
+  const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
+  const float term = column_term(bias, key, nkeys);
+  const int64_t ntiles = key0 < nkeys ? (nrows + RT - 1) / RT : 0;
+  const int64_t per = (ntiles + A.split_kv - 1) / A.split_kv;
+  const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
+
+  V8 kf[NS], vf[NS];
+  {
+    const T* krow = (const T*)S.k + b * S.ks[0] + key * S.ks[1] + hk * S.ks[2];
+    const T* vrow = (const T*)S.v + b * S.vs[0] + key * S.vs[1] + hk * S.vs[2];
+    const bool live = term != -kInf;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      kf[s] = global_frag<T, AL>(krow, live, s, h, S.d);
+      vf[s] = global_frag<T, AL>(vrow, live, s, h, S.dv);
+    }
+  }
+  f32x16 dk[NDB], dv[NDB];
+#pragma unroll
+  for (int n = 0; n < NDB; ++n) {
+    dk[n] = zero16();
+    dv[n] = zero16();
+  }
+
+  constexpr int N = RT * TL::CPR / NT, STEP = NT / TL::CPR;
+  const int lc = tid % TL::CPR, lr = tid / TL::CPR;
+  const T* qbase = (const T*)S.q + b * S.qs[0];
+  const T* gbase = (const T*)A.dout + b * A.dos[0];
+  u32x4 xq[N], xg[N];
+  f32x2 st = {kInf, 0.0f};
+  auto load = [&](int64_t t) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int64_t row = t * RT + lr + n * STEP;
+      const bool live = row < nrows;
+      const int64_t qi = row / S.group;
+      const int qh = hk * S.group + (int)(row - qi * S.group);
+      xq[n] = live ? load_chunk<T, AL>(qbase + qi * S.qs[1] + qh * S.qs[2], lc, S.d) : u32x4{0, 0, 0, 0};
+      xg[n] = live ? load_chunk<T, AL>(gbase + qi * A.dos[1] + qh * A.dos[2], lc, S.dv) : u32x4{0, 0, 0, 0};
+    }
+    if (tid < RT) st = t * RT + tid < nrows ? A.stat[pair * S.rows + t * RT + tid] : f32x2{kInf, 0.0f};
+  };
+  if (t0 < t1) load(t0);
+  for (int64_t t = t0; t < t1; ++t) {
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      *(u32x4*)(tq + TL::at(lr + n * STEP, lc)) = xq[n];
+      *(u32x4*)(tg + TL::at(lr + n * STEP, lc)) = xg[n];
+    }
+    if (tid < RT) {
+      slse[tid] = st[0];
+      sdot[tid] = st[1];
+    }
+    __syncthreads();
+    if (t + 1 < t1) load(t + 1);
+#pragma unroll
+    for (int n = 0; n < RT / 32; ++n) {
+      f32x16 p = zero16(), g = zero16();
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        p = mma(TL::row_frag(tq, 32 * n + r32, s, h), kf[s], p);
+        g = mma(TL::row_frag(tg, 32 * n + r32, s, h), vf[s], g);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 le = *(const f32x4*)&slse[32 * n + 8 * q + 4 * h];
+        const f32x4 dd = *(const f32x4*)&sdot[32 * n + 8 * q + 4 * h];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 4 * q + e;
+          p[i] = ex2(fmaf(p[i], S.c, term) - le[e]);
+          g[i] = p[i] * (g[i] - dd[e]);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const V8 pw = pack<T>(p, s), ds = pack<T>(g, s);
+#pragma unroll
+        for (int x = 0; x < NDB; ++x) {
+          dv[x] = mma(TL::col_frag(tg, 32 * n + 16 * s, 32 * x, lane), pw, dv[x]);
+          dk[x] = mma(TL::col_frag(tq, 32 * n + 16 * s, 32 * x, lane), ds, dk[x]);
+        }
+      }
+    }
+  }
+  if (key >= S.lk) return;
+  const int64_t pi = ((int64_t)split * pairs + pair) * S.lk + key;
+  T* dkrow = (T*)A.dk + b * A.dks[0] + key * A.dks[1] + hk * A.dks[2];
+  T* dvrow = (T*)A.dv + b * A.dvs[0] + key * A.dvs[1] + hk * A.dvs[2];
+  write_cols<T, NDB>(dk, S.scale, A.part_k ? A.part_k + pi * A.dp : nullptr, A.dp, dkrow, S.d, A.vec_k, h);
+  write_cols<T, NDB>(dv, 1.0f, A.part_v ? A.part_v + pi * A.dvp : nullptr, A.dvp, dvrow, S.dv, A.vec_v, h);
+}
+
+// Adds the partial sums of one gradient in split order: 32 lanes per row.
+// Rows of dQ are packed (group > 1); rows of dK, dV are keys (group = 1).
+template <class T>
+__global__ __launch_bounds__(256) void k_grad_join(const float* part, int nsplit, int64_t pairs, int64_t rows,
+                                                   int32_t dp, int32_t hkv, int32_t group, T* out, int64_t s0,
+                                                   int64_t s1, int64_t s2, int32_t d, bool vec) {
+  const int64_t idx = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int c = 4 * (threadIdx.x & 31);
+  if (idx >= pairs * rows || c >= dp) return;
+  const int64_t pair = idx / rows, row = idx - pair * rows;
+  const int b = (int)(pair / hkv), hk = (int)(pair - (int64_t)b * hkv);
+  f32x4 x = {0, 0, 0, 0};
+  for (int s = 0; s < nsplit; ++s) {
+    const f32x4 v = *(const f32x4*)(part + (s * pairs * rows + idx) * dp + c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] += v[e];
+  }
+  const int64_t qi = row / group;
+  const int qh = hk * group + (int)(row - qi * group);
+  T* orow = out + b * s0 + qi * s1 + qh * s2;
+  if (vec)
+    store4<T, true>(orow, c, d, x);
+  else
+    store4<T, false>(orow, c, d, x);
+}
+
+template <class T, int DP, bool AL>
+void grad_launch(const GradArgs& A, hipStream_t st) {
+  const int64_t pairs = (int64_t)A.S.batch * A.S.hkv;
+  if (A.S.rows > 0) {
+    hipLaunchKernelGGL((k_grad_q<T, DP, AL>), grid1(xcd_blocks(pairs * A.tiles_q * A.split_q), 256), dim3(256), 0, st, A);
+    SK_LAUNCH_CHECK();
+  }
+  if (A.S.lk > 0) {
+    hipLaunchKernelGGL((k_grad_kv<T, DP, AL>), grid1(xcd_blocks(pairs * A.tiles_kv * A.split_kv), 256), dim3(256), 0,
+                       st, A);
+    SK_LAUNCH_CHECK();
+  }
+}
+
+// Instantiated once per element type (attend_grad_*.hip).
+template <class T>
+void attend_grad(const GradArgs& A, bool aligned, hipStream_t st) {
+  const int64_t pairs = (int64_t)A.S.batch * A.S.hkv;
+  if (A.S.rows > 0) {
+    hipLaunchKernelGGL((k_grad_stat<T>), grid1((pairs * A.S.rows + 15) / 16, 256), dim3(256), 0, st, A);
+    SK_LAUNCH_CHECK();
+  }
+  const bool wide = A.S.d > 64 || A.S.dv > 64;
+  if (wide) {
+    if (aligned)
+      grad_launch<T, 128, true>(A, st);
+    else
+      grad_launch<T, 128, false>(A, st);
+  } else {
+    if (aligned)
+      grad_launch<T, 64, true>(A, st);
+    else
+      grad_launch<T, 64, false>(A, st);
+  }
+  auto join = [&](const float* part, int nsplit, int64_t rows, int32_t dp, int32_t group, void* out, const int64_t* s,
+                  int32_t d, bool vec) {
+    if (!part || rows == 0) return;
+    hipLaunchKernelGGL((k_grad_join<T>), grid1((pairs * rows + 7) / 8, 256), dim3(256), 0, st, part, nsplit, pairs,
+                       rows, dp, A.S.hkv, group, (T*)out, s[0], s[1], s[2], d, vec);
+    SK_LAUNCH_CHECK();
+  };
+  join(A.part_q, A.split_q, A.S.rows, A.dp, A.S.group, A.dq, A.dqs, A.S.d, A.vec_q);
+  join(A.part_k, A.split_kv, A.S.lk, A.dp, 1, A.dk, A.dks, A.S.d, A.vec_k);
+  join(A.part_v, A.split_kv, A.S.lk, A.dvp, 1, A.dv, A.dvs, A.S.dv, A.vec_v);
+}
+
+}  // namespace attn
+}  // namespace sk

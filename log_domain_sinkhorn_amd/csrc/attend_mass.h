@@ -1,0 +1,145 @@
+// The attention weight that each key gathers over the rows and heads that
+// read it:  mass_out_j = mass_in_j + sum_r w_r exp(s_rj - lse_r).
+//
+// k_mass holds keys (a wave has 32 across) and runs over rows: one product and
+// one exponential per score, the sum over rows in a lane's own registers.
+// Rows are split over workgroups when the keys do not fill the chip; partial
+// sums are added in split order by k_mass_join. No atomics.
+//
+// For a single tile of rows (decoding) the forward kernel leaves its scores in
+// a workspace and k_mass_scores reads those: keys are then read once from
+// memory, by the forward pass.
+#pragma once
+
+#include "attention.h"
+
+namespace sk {
+namespace attn {
+
+struct MassArgs {
+  Shape S;
+  const float* lse;       // [batch][hq][lq]
+  const float* weight;    // [batch][lq], nullable: 1
+  const float* mass_in;   // [batch][hkv][lk], nullable: 0
+  float* mass_out;        // [batch][hkv][lk], may be mass_in
+  float* part;            // [split][batch * hkv][lk], nullable
+  int32_t nsplit;
+  int64_t tiles;
+  const float* scores;    // of the forward kernel (k_mass_scores)
+  int64_t score_ld;
+};
+
+// A row's log-sum-exp in log2 units (+inf: the row takes no part) and weight.
+__device__ __forceinline__ f32x2 mass_row(const MassArgs& A, int b, int hk, int64_t row, int64_t nrows) {
+  const Shape& S = A.S;
+  if (row >= nrows) return f32x2{kInf, 0.0f};
+  const int64_t qi = row / S.group;
+  const int qh = hk * S.group + (int)(row - qi * S.group);
+  const float e = A.lse[((int64_t)b * S.hq + qh) * S.lq + qi];
+  return f32x2{e == -kInf ? kInf : e * (float)kLog2e, A.weight ? A.weight[b * S.lq + qi] : 1.0f};
+}
+
+template <class T, int DP, bool AL>
+__global__ __launch_bounds__(256) void k_mass(MassArgs A) {
+  using TL = Tile<T, DP>;
+  using V8 = typename Vec<T>::V8;
+  constexpr int RT = 64, NT = 256, NS = DP / 16;
+  __shared__ __attribute__((aligned(16))) char tq[RT * TL::RB];
+  __shared__ __attribute__((aligned(16))) float slse[RT], sw[RT];
+
+  const Shape& S = A.S;
+  const int64_t pairs = (int64_t)S.batch * S.hkv;
+  const int64_t item = xcd_item(pairs * A.tiles * A.nsplit);
+  if (item >= pairs * A.tiles * A.nsplit) return;
+  const int64_t pair = item / (A.tiles * A.nsplit);
+  const int64_t rest = item - pair * (A.tiles * A.nsplit);
+  const int64_t tile = rest / A.nsplit;
+  const int split = (int)(rest - tile * A.nsplit);
+  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int h = lane >> 5, r32 = lane & 31;
+
+  const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
+  const int64_t key0 = tile * 128, key = key0 + 32 * wave + r32;
+  const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
+  const float term = column_term(bias, key, nkeys);
+  const int64_t ntiles = key0 < nkeys ? (nrows + RT - 1) / RT : 0;
+  const int64_t per = (ntiles + A.nsplit - 1) / A.nsplit;
+  const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
+
+  V8 kf[NS];
+  {
+    const T* krow = (const T*)S.k + b * S.ks[0] + key * S.ks[1] + hk * S.ks[2];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) kf[s] = global_frag<T, AL>(krow, term != -kInf, s, h, S.d);
+  }
+  constexpr int N = RT * TL::CPR / NT, STEP = NT / TL::CPR;
+  const int lc = tid % TL::CPR, lr = tid / TL::CPR;
+  const T* qbase = (const T*)S.q + b * S.qs[0];
+  u32x4 xq[N];
+  f32x2 st = {kInf, 0.0f};
+  auto load = [&](int64_t t) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int64_t row = t * RT + lr + n * STEP;
+      const int64_t qi = row / S.group;
+      const int qh = hk * S.group + (int)(row - qi * S.group);
+      xq[n] = row < nrows ? load_chunk<T, AL>(qbase + qi * S.qs[1] + qh * S.qs[2], lc, S.d) : u32x4{0, 0, 0, 0};
+    }
+    if (tid < RT) st = mass_row(A, b, hk, t * RT + tid, nrows);
+  };
+  float sum = 0.0f;
+  if (t0 < t1) load(t0);
+  for (int64_t t = t0; t < t1; ++t) {
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) *(u32x4*)(tq + TL::at(lr + n * STEP, lc)) = xq[n];
+    if (tid < RT) {
+      slse[tid] = st[0];
+      sw[tid] = st[1];
+    }
+    __syncthreads();
+    if (t + 1 < t1) load(t + 1);
+#pragma unroll
+    for (int n = 0; n < RT / 32; ++n) {
+      f32x16 p = zero16();
+#pragma unroll
+      for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tq, 32 * n + r32, s, h), kf[s], p);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 le = *(const f32x4*)&slse[32 * n + 8 * q + 4 * h];
+        const f32x4 w = *(const f32x4*)&sw[32 * n + 8 * q + 4 * h];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum = fmaf(w[e], ex2(fmaf(p[4 * q + e], S.c, term) - le[e]), sum);
+      }
+    }
+  }
+  sum = half_sum(sum);
+  if (h != 0 || key >= S.lk) return;
+  if (A.part)
+    A.part[((int64_t)split * pairs + pair) * S.lk + key] = sum;
+  else
+    A.mass_out[pair * S.lk + key] = (A.mass_in ? A.mass_in[pair * S.lk + key] : 0.0f) + sum;
+}
+
+// Instantiated once per element type (attend_mass_*.hip).
+template <class T>
+void attend_mass(const MassArgs& A, bool aligned, hipStream_t st) {
+  const int64_t pairs = (int64_t)A.S.batch * A.S.hkv;
+  const dim3 grid = grid1(xcd_blocks(pairs * A.tiles * A.nsplit), 256);
+  if (A.S.d > 64) {
+    if (aligned)
+      hipLaunchKernelGGL((k_mass<T, 128, true>), grid, dim3(256), 0, st, A);
+    else
+      hipLaunchKernelGGL((k_mass<T, 128, false>), grid, dim3(256), 0, st, A);
+  } else {
+    if (aligned)
+      hipLaunchKernelGGL((k_mass<T, 64, true>), grid, dim3(256), 0, st, A);
+    else
+      hipLaunchKernelGGL((k_mass<T, 64, false>), grid, dim3(256), 0, st, A);
+  }
+  SK_LAUNCH_CHECK();
+}
+
+}  // namespace attn
+}  // namespace sk

@@ -1,0 +1,182 @@
+"""Refusals of the attention operators, on the host: the binding's checks of
+types and shapes and the C ABI's checks before any device work."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import log_domain_sinkhorn_amd as sk
+
+BF = torch.bfloat16
+
+
+def _qkv(B=2, Lq=3, Hq=4, Hkv=2, Lk=5, d=8, dv=8, dtype=BF):
+    return (torch.zeros(B, Lq, Hq, d, dtype=dtype), torch.zeros(B, Lk, Hkv, d, dtype=dtype),
+            torch.zeros(B, Lk, Hkv, dv, dtype=dtype))
+
+
+@pytest.mark.parametrize("change", [
+    lambda a: a.update(q=a["q"].double()),
+    lambda a: a.update(k=a["k"].float()),
+    lambda a: a.update(q=[1.0]),
+    lambda a: a.update(key_bias=torch.zeros(2, 5, dtype=BF)),
+    lambda a: a.update(key_lengths=torch.ones(2, dtype=torch.int64)),
+    lambda a: a.update(mass_out=torch.zeros(2, 2, 5, dtype=torch.float64)),
+])
+def test_wrong_types(change):
+    q, k, v = _qkv()
+    a = dict(q=q, k=k, v=v)
+    change(a)
+    with pytest.raises(TypeError):
+        sk.cross_attention(**a)
+
+
+@pytest.mark.parametrize("change", [
+    lambda a: a.update(q=a["q"][0]),
+    lambda a: a.update(k=a["k"][:1]),
+    lambda a: a.update(k=a["k"][..., :4]),
+    lambda a: a.update(v=a["v"][:, :4]),
+    lambda a: a.update(v=a["v"][:, :, :1]),
+    lambda a: a.update(q=a["q"][:, :, :3]),
+    lambda a: a.update(q=a["q"].transpose(2, 3).contiguous().transpose(2, 3)),
+    lambda a: a.update(key_bias=torch.zeros(2, 6)),
+    lambda a: a.update(key_bias=torch.zeros(2, 1, 5)),
+    lambda a: a.update(key_bias=torch.zeros(5, 2).t()),
+    lambda a: a.update(key_lengths=torch.ones(3, dtype=torch.int32)),
+    lambda a: a.update(query_lengths=torch.ones(2, 1, dtype=torch.int32)),
+    lambda a: a.update(out=torch.zeros(2, 3, 4, 9, dtype=BF)),
+    lambda a: a.update(out=torch.zeros(1, 3, 4, 8, dtype=BF).expand(2, 3, 4, 8)),
+    lambda a: a.update(lse=torch.zeros(2, 3, 4)),
+    lambda a: a.update(mass_in=torch.zeros(2, 2, 5)),
+    lambda a: a.update(row_weight=torch.zeros(2, 3)),
+    lambda a: a.update(mass_out=torch.zeros(2, 4, 5)),
+    lambda a: a.update(q=a["q"].requires_grad_()),
+    lambda a: a.update(key_bias=torch.zeros(2, 5, requires_grad=True)),
+    lambda a: a,  # host tensors
+])
+def test_wrong_shapes_and_places(change):
+    q, k, v = _qkv()
+    a = dict(q=q, k=k, v=v)
+    change(a)
+    with pytest.raises(ValueError):
+        sk.cross_attention(**a)
+
+
+def test_gradient_and_weight_arguments():
+    q, k, v = _qkv()
+    out, lse = torch.zeros(2, 3, 4, 8, dtype=BF), torch.zeros(2, 4, 3)
+    for bad in (dict(dout=out.float()), dict(lse=lse.double())):
+        with pytest.raises(TypeError):
+            sk.cross_attention_grad(**{**dict(dout=out, q=q, k=k, v=v, out=out, lse=lse), **bad})
+    for bad in (dict(dout=out[:, :2]), dict(out=out[..., :4]), dict(lse=lse[:, :2]), dict(dk=q), dict()):
+        with pytest.raises(ValueError):
+            sk.cross_attention_grad(**{**dict(dout=out, q=q, k=k, v=v, out=out, lse=lse), **bad})
+    with pytest.raises(ValueError):
+        sk.attention_mass(q, k, lse[:, :1])
+
+
+@pytest.mark.parametrize("bad", [dict(keep=0), dict(mass=torch.zeros(2, 2, 4)), dict(v=torch.zeros(2, 4, 2, 8, dtype=BF)),
+                                 dict(k_out=torch.zeros(2, 4, 2, 8, dtype=BF)),
+                                 dict(index_out=torch.zeros(2, 2, 4, dtype=torch.int32)), dict()])
+def test_evict_arguments(bad):
+    _, k, v = _qkv()
+    with pytest.raises(ValueError):
+        sk.cache_evict(**{**dict(k=k, v=v, mass=torch.zeros(2, 2, 5), keep=3), **bad})
+
+
+def _desc(**kw):
+    a = sk._AttentionC(dtype=2, batch=2, heads_q=4, heads_kv=2, d=64, dv=64, len_q=3, len_k=1000, scale=0.125)
+    for n in ("q", "k", "v", "out", "dout", "dq", "dk", "dv"):
+        setattr(a, n + "_stride", sk._i64x3(1 << 20, 256, 64))
+    for n, x in kw.items():
+        setattr(a, n, x)
+    return a
+
+
+FAKE = ctypes.c_void_p(256)
+
+
+def _forward(a, q=FAKE, k=FAKE, v=FAKE, out=ctypes.c_void_p(512), lse=FAKE, w=None, mi=None, mo=None, ws=None, n=0):
+    return sk.lib().sinkhorn_cross_attention(ctypes.byref(a) if a is not None else None, q, k, v, out, lse, w, mi, mo, ws,
+                                             n, None)
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(dtype=3), b"dtype"), (dict(batch=-1), b"negative"), (dict(len_k=-1), b"negative"), (dict(heads_kv=3), b"multiple"),
+    (dict(heads_kv=0), b"multiple"), (dict(d=0), b"width"), (dict(len_k=1 << 31), b"2^31"), (dict(len_q=1 << 30), b"2^31"),
+    (dict(scale=0.0), b"scale"), (dict(scale=-1.0), b"scale"), (dict(scale=math.nan), b"scale"),
+    (dict(scale=math.inf), b"scale"), (dict(scale=1e-60), b"scale"), (dict(scale=1e39), b"scale"),
+    (dict(k_stride=sk._i64x3(1, -64, 1)), b"stride"),
+])
+def test_descriptions_are_refused(kw, word):
+    n = ctypes.c_int64()
+    a = _desc(**kw)
+    assert _forward(a) == sk.ERR_INVALID_ARG
+    assert word in sk.lib().sinkhorn_last_error()
+    assert sk.lib().sinkhorn_attention_workspace(ctypes.byref(a), 0, ctypes.byref(n)) == sk.ERR_INVALID_ARG
+
+
+def test_wide_heads_are_unsupported():
+    assert _forward(_desc(d=129)) == sk.ERR_UNSUPPORTED
+    assert _forward(_desc(dv=256)) == sk.ERR_UNSUPPORTED
+
+
+def test_null_pointers_aliases_and_workspaces():
+    L = sk.lib()
+    a = _desc()
+    assert _forward(None) == sk.ERR_INVALID_ARG
+    for kw in (dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(lse=None), dict(out=FAKE), dict(mi=FAKE),
+               dict(w=FAKE)):
+        assert _forward(a, **kw) == sk.ERR_INVALID_ARG, kw
+    need = ctypes.c_int64()
+    for what in range(4):
+        assert L.sinkhorn_attention_workspace(ctypes.byref(a), what, ctypes.byref(need)) == sk.OK
+    assert L.sinkhorn_attention_workspace(ctypes.byref(a), 4, ctypes.byref(need)) == sk.ERR_INVALID_ARG
+    assert L.sinkhorn_attention_workspace(ctypes.byref(a), 0, None) == sk.ERR_INVALID_ARG
+    assert L.sinkhorn_attention_workspace(ctypes.byref(a), 0, ctypes.byref(need)) == sk.OK
+    assert need.value > 0  # few rows against many keys: split
+    for ws, n in ((None, 0), (FAKE, need.value - 1), (ctypes.c_void_p(264), need.value)):
+        assert _forward(a, ws=ws, n=n) == sk.ERR_INVALID_ARG
+        assert b"workspace" in L.sinkhorn_last_error()
+    P = [FAKE] * 3
+    out, dout, dq, dk, dv = (ctypes.c_void_p(512 * i) for i in range(2, 7))
+    grad = lambda *x: L.sinkhorn_cross_attention_grad(ctypes.byref(a), *x, None, 0, None)  # noqa: E731
+    assert grad(*P, out, FAKE, dout, None, dk, dv) == sk.ERR_INVALID_ARG
+    assert grad(*P, out, FAKE, dout, dq, dq, dv) == sk.ERR_INVALID_ARG
+    assert grad(*P, out, FAKE, dout, dq, dk, dout) == sk.ERR_INVALID_ARG
+    assert grad(*P, out, FAKE, dout, dq, dk, dv) == sk.ERR_INVALID_ARG  # no workspace
+    assert b"workspace" in L.sinkhorn_last_error()
+    assert L.sinkhorn_attention_mass(ctypes.byref(a), FAKE, FAKE, FAKE, None, None, None, None, 0, None) == sk.ERR_INVALID_ARG
+    # nothing to do needs no device
+    a0 = _desc(batch=0)
+    assert _forward(a0) == sk.OK
+
+
+def _cache(**kw):
+    c = sk._CacheC(dtype=1, batch=1, heads=2, d=64, dv=64, len=100, keep=10, first=1, recent=2)
+    for n in ("k", "v", "k_out", "v_out"):
+        setattr(c, n + "_stride", sk._i64x3(12800, 128, 64))
+    for n, x in kw.items():
+        setattr(c, n, x)
+    return c
+
+
+def test_cache_descriptions_are_refused():
+    L = sk.lib()
+    p = [ctypes.c_void_p(4096 * i) for i in range(1, 9)]
+    call = lambda c, *x: L.sinkhorn_cache_evict(ctypes.byref(c) if c else None, *x, None)  # noqa: E731
+    assert call(None, *p) == sk.ERR_INVALID_ARG
+    for kw in (dict(dtype=7), dict(batch=-1), dict(heads=0), dict(len=-1), dict(len=1 << 31), dict(keep=0), dict(first=-1),
+               dict(recent=-1), dict(first=9, recent=2), dict(first=1 << 62, recent=1 << 62), dict(d=0),
+               dict(v_out_stride=sk._i64x3(1, -1, 1))):
+        assert call(_cache(**kw), *p) == sk.ERR_INVALID_ARG, kw
+    for i in range(8):
+        q = list(p)
+        q[i] = None
+        assert call(_cache(), *q) == sk.ERR_INVALID_ARG, i
+    for i, j in ((3, 0), (4, 1), (4, 3), (5, 2)):
+        q = list(p)
+        q[i] = q[j]
+        assert call(_cache(), *q) == sk.ERR_INVALID_ARG, (i, j)
+    assert call(_cache(batch=0), *([None] * 8)) == sk.OK

@@ -1,5 +1,5 @@
 // Cross attention, forward: out = softmax(scale q.k + bias) v row by row, in
-// one pass over the keys with a running maximum and sum, for the rows of one
+// one pass over the keys with a running reference and sum, for the rows of one
 // (batch entry, key head) pair.
 //
 // A wave holds 32 rows as the columns of transposed tiles: S^T = K Q^T (keys
@@ -7,9 +7,13 @@
 // registers and one exchange with the lane 32 away; the weights feed
 // O^T = V^T P^T from their registers. WQ waves take different rows of the
 // same keys and WK waves different keys of the same rows (joined through LDS
-// at the end): 4 x 1 for many rows, 1 x 4 when one tile of 32 rows holds them
+// at the end): 4 x 1 for many rows, 1 x WK when one tile of 32 rows holds them
 // all. The keys are split over workgroups when rows and heads alone do not fill
 // the chip; k_join then joins the partial results.
+//
+// Tiles of keys lie in two LDS buffers, one filled by loads to LDS while the
+// other is computed on: one barrier per tile and no staging registers, which
+// leaves two waves a SIMD whose matrix and vector work overlap.
 #pragma once
 
 #include "attention.h"
@@ -30,22 +34,31 @@ struct AttendArgs {
   int32_t nsplit;  // splits of the keys
   int64_t tiles;   // row tiles per pair
   bool vec;        // out may be written four elements at a time
+  int32_t unit;    // bytes a lane may load to LDS from q, k and v: 16, 4, or 2 (through registers)
 };
 
-template <class T, int DP, int WQ, int WK, int NB, bool AL>
-__global__ __launch_bounds__(64 * WQ * WK) void k_attend(AttendArgs A) {
+// Waves a SIMD that the LDS of a tile of `keys` keys of `row` bytes leaves room for.
+constexpr int attend_waves(int keys, int row) { return 4 * keys * row <= 72 * 1024 ? 2 : 1; }
+
+template <class T, int DP, int WQ, int WK, int NB, int CH>
+__global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)sizeof(T))) void k_attend(
+    AttendArgs A) {
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
   constexpr int NT = 64 * WQ * WK;
   constexpr int KT = 32 * NB * WK;  // keys per tile
   constexpr int NS = DP / 16, NDB = DP / 32;
+  using Ld = Loader<T, DP, KT, NT, CH>;
+  // fp32: scores in natural units, rounded once, and 2^(log2e s - m) with the
+  // product inside an fma: a weight is off by what its score's own rounding
+  // makes it. 16-bit types: log2 units from the start, one operation less.
+  constexpr bool kExact = sizeof(T) == 4;
+  constexpr float kTerm = kExact ? 1.0f : (float)kLog2e;
   constexpr int kTileBytes = KT * TL::RB;
-  constexpr int kJoinBytes = WK > 1 ? WK * 32 * DP * 4 : 0;
-  __shared__ __attribute__((aligned(16))) char sm[kJoinBytes > 2 * kTileBytes ? kJoinBytes : 2 * kTileBytes];
-  __shared__ __attribute__((aligned(16))) float sterm[KT];
+  static_assert(WK == 1 || WK * 32 * DP * 4 <= 4 * kTileBytes, "room to join the waves");
+  __shared__ __attribute__((aligned(16))) char sm[4 * kTileBytes];
+  __shared__ __attribute__((aligned(16))) float sterm[2][KT], sraw[3][KT];
   __shared__ f32x2 sml[WK > 1 ? WK * 32 : 1];
-  char* const sk_ = sm;
-  char* const sv_ = sm + kTileBytes;
 
   const Shape& S = A.S;
   const int64_t pairs = (int64_t)S.batch * S.hkv;
@@ -57,14 +70,14 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_attend(AttendArgs A) {
   const int split = (int)(rest - tile * A.nsplit);
   const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r32 = lane & 31;
   const int wq = wave % WQ, wk = wave / WQ;
 
   const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
   const int64_t row0 = tile * (32 * WQ);
   const int64_t row = row0 + 32 * wq + r32;
-  const bool live = row < nrows;
+  const bool live_row = row < nrows;
   const int64_t qi = row / S.group;
   const int qh = hk * S.group + (int)(row - qi * S.group);
 
@@ -77,114 +90,151 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_attend(AttendArgs A) {
   const T* vbase = (const T*)S.v + b * S.vs[0] + hk * S.vs[2];
   const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
 
+  Ld lk, lv;
+  lk.init(S.ks[1], S.d, wave, lane);
+  lv.init(S.vs[1], S.dv, wave, lane);
+  // Column terms. The biases of tile t are loaded to sraw[t % 3] during tile
+  // t - 2; during tile t - 1 they decide which rows are loaded and become the
+  // terms of sterm[t % 2].
+  auto fetch = [&](int64_t t) {
+    if (!bias || wave * 64 >= KT) return;
+    const int j = wave * 64 + lane;
+    dma_load<4>(dma_rsrc(bias + t * KT), lds_offset(sraw[(t - t0) % 3]) + wave * 256, t * KT + j < nkeys ? 4 * j : kOutside);
+  };
+  auto start = [&](int64_t t) {
+    const int buf = (int)(t - t0) & 1;
+    const float* raw = sraw[(t - t0) % 3];
+    const int64_t left = nkeys - t * KT;  // live keys from the tile's first on
+    if (tid < KT) {
+      float term = 0.0f;
+      if (bias) {
+        const float x = raw[tid];
+        term = x <= kMasked ? -kInf : x * kTerm;
+      }
+      sterm[buf][tid] = tid < left ? term : -kInf;
+    }
+    auto both = [&](auto&& live) {
+      lk.start(kbase + t * KT * S.ks[1], sm + buf * 2 * kTileBytes, live, S.d, wave, lane);
+      lv.start(vbase + t * KT * S.vs[1], sm + buf * 2 * kTileBytes + kTileBytes, live, S.dv, wave, lane);
+    };
+    if (bias)
+      both([&](int r) { return r < left && !(raw[r] <= kMasked); });
+    else if (left < KT)
+      both([&](int r) { return r < left; });
+    else
+      both([](int) { return true; });
+  };
+  auto land = [&](int64_t t) {
+    const int buf = (int)(t - t0) & 1;
+    lk.land(sm + buf * 2 * kTileBytes, wave, lane);
+    lv.land(sm + buf * 2 * kTileBytes + kTileBytes, wave, lane);
+  };
+  if (t0 < t1) {
+    if (bias) {
+      fetch(t0);
+      if (t0 + 1 < t1) fetch(t0 + 1);
+      dma_wait();
+      __syncthreads();
+    }
+    start(t0);
+    land(t0);
+  }
+
   V8 qf[NS];
   {
     const T* qrow = (const T*)S.q + b * S.qs[0] + qi * S.qs[1] + qh * S.qs[2];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) qf[s] = global_frag<T, AL>(qrow, live, s, h, S.d);
+    for (int s = 0; s < NS; ++s) qf[s] = global_frag<T, CH == 16>(qrow, live_row, s, h, S.d);
   }
   f32x16 o[NDB];
 #pragma unroll
   for (int n = 0; n < NDB; ++n) o[n] = zero16();
-  float m = -kInf, l = 0.0f;  // running maximum of the row; this lane's part of the sum
+  float m = -kInf, l = 0.0f;  // the row's reference (log2 units) and this lane's part of the sum
 
-  Stage<T, DP, KT, NT, AL> xk, xv;
-  float term = 0.0f;
-  if (t0 < t1) {
-    xk.load(kbase, S.ks[1], t0 * KT, nkeys, S.d, tid);
-    xv.load(vbase, S.vs[1], t0 * KT, nkeys, S.dv, tid);
-    if (tid < KT) term = column_term(bias, t0 * KT + tid, nkeys);
-  }
   for (int64_t t = t0; t < t1; ++t) {
-    // without a bias only a tile that the live keys end in has masked columns
-    const bool masked = bias != nullptr || (t + 1) * KT > nkeys;
-    __syncthreads();
-    if (tid < KT) sterm[tid] = term;
-    if (bias) {
-      __syncthreads();
-      xk.put_masked(sk_, sterm, tid);
-      xv.put_masked(sv_, sterm, tid);
-    } else {
-      xk.put(sk_, tid);
-      xv.put(sv_, tid);
-    }
+    const int buf = (int)(t - t0) & 1;
+    dma_wait();
     __syncthreads();
     if (t + 1 < t1) {
-      xk.load(kbase, S.ks[1], (t + 1) * KT, nkeys, S.d, tid);
-      xv.load(vbase, S.vs[1], (t + 1) * KT, nkeys, S.dv, tid);
-      if (tid < KT) term = column_term(bias, (t + 1) * KT + tid, nkeys);
+      start(t + 1);
+      if (t + 2 < t1) fetch(t + 2);
     }
-    f32x16 sc[NB];
+    const char* tk = sm + buf * 2 * kTileBytes;
+    const char* tv = tk + kTileBytes;
     const int kb0 = wk * 32 * NB;
+    // without a bias only the tile that the live keys end in has masked columns
+    const bool masked = bias != nullptr || (t + 1) * KT > nkeys;
+    f32x16 sc[NB];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       sc[n] = zero16();
 #pragma unroll
-      for (int s = 0; s < NS; ++s)
-        sc[n] = mma(TL::row_frag(sk_, kb0 + 32 * n + r32, s, h), qf[s], sc[n]);
+      for (int s = 0; s < NS; ++s) sc[n] = mma(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n]);
     }
-    float mx = -kInf;
-    if (masked) {
+    float f = kExact ? (float)kLog2e : S.c;  // to log2 units
+    if (kExact || masked || A.scores) {
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x4 ct = *(const f32x4*)&sterm[kb0 + 32 * n + 8 * g + 4 * h];
+          const f32x4 ct = *(const f32x4*)&sterm[buf][kb0 + 32 * n + 8 * g + 4 * h];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sc[n][4 * g + e] = fmaf(sc[n][4 * g + e], S.c, ct[e]);
-            mx = fmaxf(mx, sc[n][4 * g + e]);
+            const float x = sc[n][4 * g + e];
+            sc[n][4 * g + e] = kExact ? fmaf(x, S.scale, fmaf(x, S.scale_lo, ct[e])) : fmaf(x, S.c, ct[e]);
           }
         }
-    } else {
+      if (!kExact) f = 1.0f;
+      if (A.scores && row < S.rows) {
+        float* dst = A.scores + (pair * S.rows + row) * A.score_ld + t * KT + kb0;
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          sc[n][e] *= S.c;
-          mx = fmaxf(mx, sc[n][e]);
-        }
+          for (int g = 0; g < 4; ++g)
+            *(f32x4*)(dst + 32 * n + 8 * g + 4 * h) =
+                f32x4{sc[n][4 * g], sc[n][4 * g + 1], sc[n][4 * g + 2], sc[n][4 * g + 3]};
+      }
     }
-    if (A.scores && row < S.rows) {
-      float* dst = A.scores + (pair * S.rows + row) * A.score_ld + t * KT + kb0;
+    float mx = -kInf;
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *(f32x4*)(dst + 32 * n + 8 * g + 4 * h) =
-              f32x4{sc[n][4 * g], sc[n][4 * g + 1], sc[n][4 * g + 2], sc[n][4 * g + 3]};
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[n][e]);
+    mx = half_max(mx) * f;
+    // a new reference only where the maximum rose by more than 2^8: weights
+    // stay below 2^8 and the accumulators are seldom rescaled
+    if (__any(mx > m + 8.0f)) {
+      const float mn = fmaxf(m, mx);
+      const float a = mn == -kInf ? 1.0f : ex2(m - mn);
+      m = mn;
+      l *= a;
+#pragma unroll
+      for (int n = 0; n < NDB; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[n][e] *= a;
     }
-    const float mn = fmaxf(m, half_max(mx));
-    const float mu = mn == -kInf ? 0.0f : mn;  // a row with no live key yet: all weights 0
-    const float a = ex2(m - mu);
-    m = mn;
-    l *= a;
+    const float mu = m == -kInf ? 0.0f : m;  // a row with no live key yet: all weights 0
 #pragma unroll
-    for (int n = 0; n < NDB; ++n)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[n][e] *= a;
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        sc[n][e] = ex2(sc[n][e] - mu);
+        sc[n][e] = ex2(fmaf(sc[n][e], f, -mu));
         l += sc[n][e];
       }
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const V8 p = pack<T>(sc[n], s);
 #pragma unroll
-        for (int x = 0; x < NDB; ++x)
-          o[x] = mma(TL::col_frag(sv_, kb0 + 32 * n + 16 * s, 32 * x, lane), p, o[x]);
+        for (int x = 0; x < NDB; ++x) o[x] = mma(TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane), p, o[x]);
       }
-    }
+    if (t + 1 < t1) land(t + 1);
   }
   l = half_sum(l);
-  if (!live) {  // a row behind its sequence (its zero scores weigh nothing)
+  if (!live_row) {  // a row behind its sequence (its zero scores weigh nothing)
     m = -kInf;
     l = 0.0f;
-#pragma unroll
-    for (int n = 0; n < NDB; ++n) o[n] = zero16();
   }
 
   // the row's result, column group by column group: group index c4 of four
@@ -197,7 +247,7 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_attend(AttendArgs A) {
 #pragma unroll
     for (int x = 0; x < NDB; ++x)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) so[(wk * DP + 32 * x + 8 * (e >> 2) + 4 * h + (e & 3)) * 32 + r32] = o[x][e];
+      for (int e = 0; e < 16; ++e) so[(wk * DP + 32 * x + 8 * (e >> 2) + 4 * h + (e & 3)) * 32 + r32] = live_row ? o[x][e] : 0.0f;
     __syncthreads();
     // thread: row tid % 32, column groups tid / 32, + NT / 32, ...
     const int64_t jrow = row0 + (tid & 31);
@@ -241,7 +291,7 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_attend(AttendArgs A) {
       if (part)
         A.mlpart[((int64_t)split * pairs + pair) * S.rows + jrow] = f32x2{mm, ll};
       else
-        A.lse[((int64_t)b * S.hq + jh) * S.lq + ji] = ll == 0.0f ? -kInf : (mm + lg2(ll)) * (float)kLn2;
+        A.lse[((int64_t)b * S.hq + jh) * S.lq + ji] = log_sum(mm, ll);
     }
   } else {
     if (row >= S.rows) return;
@@ -253,7 +303,9 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_attend(AttendArgs A) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int c = 32 * n + 8 * g + 4 * h;
-        f32x4 x = {o[n][4 * g], o[n][4 * g + 1], o[n][4 * g + 2], o[n][4 * g + 3]};
+        f32x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = live_row ? o[n][4 * g + e] : 0.0f;
         if (part) {
           if (c < A.dvp) *(f32x4*)(A.opart + prow_i * A.dvp + c) = x;
         } else {
@@ -269,7 +321,7 @@ __global__ __launch_bounds__(64 * WQ * WK) void k_attend(AttendArgs A) {
       if (part)
         A.mlpart[prow_i] = f32x2{m, l};
       else
-        A.lse[((int64_t)b * S.hq + qh) * S.lq + qi] = l == 0.0f ? -kInf : (m + lg2(l)) * (float)kLn2;
+        A.lse[((int64_t)b * S.hq + qh) * S.lq + qi] = log_sum(m, l);
     }
   }
 }
@@ -309,34 +361,40 @@ __global__ __launch_bounds__(256) void k_join(AttendArgs A) {
     store4<T, true>(orow, c, S.dv, x);
   else
     store4<T, false>(orow, c, S.dv, x);
-  if (c == 0) A.lse[((int64_t)b * S.hq + qh) * S.lq + qi] = ll == 0.0f ? -kInf : (mm + lg2(ll)) * (float)kLn2;
+  if (c == 0) A.lse[((int64_t)b * S.hq + qh) * S.lq + qi] = log_sum(mm, ll);
 }
 
 // many: 128 rows per workgroup, else all rows in one tile of 32
-template <class T, int DP, bool AL>
+template <class T, int DP, int CH>
 void attend_launch(const AttendArgs& A, bool many, hipStream_t st) {
   const int64_t blocks = xcd_blocks((int64_t)A.S.batch * A.S.hkv * A.tiles * A.nsplit);
+  constexpr int WK = sizeof(T) == 2 ? 4 : 2;  // fp32: two buffers of 128 keys would not fit
   if (many)
-    hipLaunchKernelGGL((k_attend<T, DP, 4, 1, 2, AL>), grid1(blocks, 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_attend<T, DP, 4, 1, 2, CH>), grid1(blocks, 256), dim3(256), 0, st, A);
   else
-    hipLaunchKernelGGL((k_attend<T, DP, 1, 4, 1, AL>), grid1(blocks, 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_attend<T, DP, 1, WK, 1, CH>), grid1(blocks, 64 * WK), dim3(64 * WK), 0, st, A);
   SK_LAUNCH_CHECK();
 }
 
 // Instantiated once per element type (attend_*.hip).
 template <class T>
-void attend(const AttendArgs& A, bool many, bool aligned, hipStream_t st) {
+void attend(const AttendArgs& A, bool many, hipStream_t st) {
   const bool wide = A.S.d > 64 || A.S.dv > 64;
-  if (wide) {
-    if (aligned)
-      attend_launch<T, 128, true>(A, many, st);
+  if (A.unit == 16) {
+    if (wide)
+      attend_launch<T, 128, 16>(A, many, st);
     else
-      attend_launch<T, 128, false>(A, many, st);
+      attend_launch<T, 64, 16>(A, many, st);
+  } else if (A.unit == 4) {
+    if (wide)
+      attend_launch<T, 128, 4>(A, many, st);
+    else
+      attend_launch<T, 64, 4>(A, many, st);
   } else {
-    if (aligned)
-      attend_launch<T, 64, true>(A, many, st);
+    if (wide)
+      attend_launch<T, 128, 2>(A, many, st);
     else
-      attend_launch<T, 64, false>(A, many, st);
+      attend_launch<T, 64, 2>(A, many, st);
   }
   if (A.opart) {
     hipLaunchKernelGGL((k_join<T>), grid1(((int64_t)A.S.batch * A.S.hkv * A.S.rows + 7) / 8, 256), dim3(256), 0, st, A);

@@ -27,16 +27,18 @@ struct MassArgs {
   int64_t tiles;
   const float* scores;    // of the forward kernel (k_mass_scores)
   int64_t score_ld;
+  bool exact;             // scores in natural units (fp32), else log2 units
 };
 
-// A row's log-sum-exp in log2 units (+inf: the row takes no part) and weight.
-__device__ __forceinline__ f32x2 mass_row(const MassArgs& A, int b, int hk, int64_t row, int64_t nrows) {
+// A row's log-sum-exp (in log2 units unless `natural`) (+inf: the row takes no part) and weight.
+__device__ __forceinline__ f32x2 mass_row(const MassArgs& A, int b, int hk, int64_t row, int64_t nrows,
+                                          bool natural = false) {
   const Shape& S = A.S;
   if (row >= nrows) return f32x2{kInf, 0.0f};
   const int64_t qi = row / S.group;
   const int qh = hk * S.group + (int)(row - qi * S.group);
   const float e = A.lse[((int64_t)b * S.hq + qh) * S.lq + qi];
-  return f32x2{e == -kInf ? kInf : e * (float)kLog2e, A.weight ? A.weight[b * S.lq + qi] : 1.0f};
+  return f32x2{e == -kInf ? kInf : (natural ? e : e * (float)kLog2e), A.weight ? A.weight[b * S.lq + qi] : 1.0f};
 }
 
 template <class T, int DP, bool AL>

@@ -90,6 +90,11 @@ __device__ __forceinline__ float half_sum(float x) {
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x); }
 
+// Natural log-sum-exp from a log2 reference and the sum of 2^(t - reference).
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.0f ? -kInf : fmaf(m, (float)kLn2, lg2(l) * (float)kLn2);
+}
+
 // Eight registers of a result as a B operand (rounded to T: the weights are
 // rounded once, to nearest, before the product that consumes them).
 template <class T>
@@ -235,6 +240,138 @@ struct Stage {
   }
 };
 
+// The same straight from memory to LDS (buffer loads with an LDS destination:
+// no registers, no LDS writes by the waves), CH = 16 or 4 bytes a lane: 16 for
+// rows that are 16-byte aligned and a whole number of 16-byte chunks long, 4 for
+// any multiple of four bytes. A wave's instruction fills 64 CH bytes of LDS in
+// lane order, so the swizzle is applied to the address a lane fetches. Rows
+// that are not live, and what lies behind a row's width, get an offset behind
+// the buffer's end, for which the load puts zero. A tile may span at most
+// 2^31 bytes.
+constexpr uint32_t kOutside = 0x80000000u;
+
+// Written as assembly because the compiler waits for a load to LDS before any
+// LDS read that may alias it, so also before reads of the other buffer;
+// dma_wait() comes before the barrier behind which the data is read. The loads
+// have no destination register.
+template <int CH>
+__device__ __forceinline__ void dma_load(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds, uint32_t off) {
+  lds = __builtin_amdgcn_readfirstlane(lds);
+  if constexpr (CH == 16)
+    asm volatile(
+        "s_mov_b32 m0, %0\n"
+        "s_nop 0\n"
+        "buffer_load_dwordx4 %1, %2, 0 offen lds"
+        :
+        : "s"(lds), "v"(off), "s"(rsrc)
+        : "memory");
+  else
+    asm volatile(
+        "s_mov_b32 m0, %0\n"
+        "s_nop 0\n"
+        "buffer_load_dword %1, %2, 0 offen lds"
+        :
+        : "s"(lds), "v"(off), "s"(rsrc)
+        : "memory");
+}
+// base: the same for all lanes (the reads make that known to the compiler)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t dma_rsrc(const void* base) {
+  const uint64_t p = (uint64_t)base;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0, (int)kOutside, 0x00027000);
+}
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+}
+
+// Loader of the rows of a tile by the workgroup's NT threads: start(t, ...)
+// begins, land() finishes (staged loads only), dma_wait() and a barrier make
+// the tile readable. `wave` must be uniform.
+template <class T, int DP, int ROWS, int NT, int CH>
+struct Loader {
+  using TL = Tile<T, DP>;
+  static constexpr int UPR = TL::RB / CH;              // units per row
+  static constexpr int N = ROWS * UPR / NT;            // units per thread
+  static constexpr int RPI = UPR > 64 ? 1 : 64 / UPR;  // rows per instruction of a wave
+  static constexpr int IPR = UPR > 64 ? UPR / 64 : 1;  // instructions per row
+  static constexpr int NR = N / IPR;                   // different rows of a lane
+  static_assert(N * NT == ROWS * UPR && N >= IPR && N % IPR == 0, "tile and workgroup sizes");
+
+  uint32_t off[CH == 16 ? N : 1];  // byte offset of this lane's unit from the tile's start
+  uint32_t pitch;                  // bytes between rows
+
+  // tile row of this lane's units n * IPR ...
+  __device__ __forceinline__ static int row(int n, int wave, int lane) {
+    return (wave * NR + n) * RPI + (UPR >= 64 ? 0 : lane / UPR);
+  }
+  __device__ __forceinline__ void init(int64_t stride, int d, int wave, int lane) {
+    pitch = (uint32_t)(stride * (int64_t)sizeof(T));
+    if constexpr (CH == 16) {
+      static_assert(IPR == 1, "16-byte units: at most 64 a row");
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int r = row(n, wave, lane);
+        const int c = (lane % UPR) ^ TL::swz(r);
+        off[n] = c * TL::EPC < d ? r * pitch + 16 * c : kOutside;
+      }
+    }
+  }
+  // live(r): row r of the tile takes part
+  template <class F>
+  __device__ __forceinline__ void start(const T* base, char* t, F&& live, int d, int wave, int lane) {
+    const __amdgpu_buffer_rsrc_t rsrc = dma_rsrc(base);
+    const uint32_t lds = lds_offset(t) + wave * (N * 64 * CH);
+    // keeps the many offsets and masks of 4-byte units from being computed
+    // ahead of the loop over tiles and held in registers
+    uint32_t step = pitch;
+    if constexpr (CH == 4) asm volatile("" : "+s"(step), "+s"(d));
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      if constexpr (CH == 16) {
+        dma_load<16>(rsrc, lds + n * 1024, live(row(n, wave, lane)) ? off[n] : kOutside);
+      } else {
+        const int r = row(n, wave, lane);
+        const bool on = live(r);
+#pragma unroll
+        for (int i = 0; i < IPR; ++i) {
+          const int u = UPR > 64 ? lane + 64 * i : lane % UPR;     // 4-byte unit of the LDS row
+          const int w = (((u >> 2) ^ TL::swz(r)) << 2) + (u & 3);  // and of the row in memory
+          const bool in = on && w * 4 < d * (int)sizeof(T);
+          dma_load<4>(rsrc, lds + (n * IPR + i) * 256, in ? r * step + 4 * w : kOutside);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void land(char*, int, int) const {}
+};
+
+// Rows at odd addresses (CH = 2): element by element through registers, in
+// the same places.
+template <class T, int DP, int ROWS, int NT>
+struct Loader<T, DP, ROWS, NT, 2> {
+  using TL = Tile<T, DP>;
+  static constexpr int N = ROWS * TL::CPR / NT, NR = N, RPI = 64 / TL::CPR;
+  static_assert(N * NT == ROWS * TL::CPR && N >= 1, "tile and workgroup sizes");
+  u32x4 x[N];
+  int64_t pitch;
+
+  __device__ __forceinline__ static int row(int n, int wave, int lane) { return (wave * N + n) * RPI + lane / TL::CPR; }
+  __device__ __forceinline__ void init(int64_t stride, int, int, int) { pitch = stride; }
+  template <class F>
+  __device__ __forceinline__ void start(const T* base, char*, F&& live, int d, int wave, int lane) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      x[n] = live(row(n, wave, lane)) ? load_chunk<T, false>(base + row(n, wave, lane) * pitch, lane % TL::CPR, d)
+                                      : u32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void land(char* t, int wave, int lane) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) *(u32x4*)(t + TL::at(row(n, wave, lane), lane % TL::CPR)) = x[n];
+  }
+};
+
+__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // ---------------------------------------------------------------- arguments
 // One attention call as the kernels see it (strides in elements: batch, row,
 // head; the innermost dimension has stride 1).
@@ -250,8 +387,8 @@ struct Shape {
   int64_t bs[2];
   const int32_t* qlen;  // nullable
   const int32_t* klen;  // nullable
-  float scale;          // of the scores
-  float c;              // scale * log2(e)
+  float scale, scale_lo;  // of the scores: the fp32 value and what it misses
+  float c;                // scale * log2(e)
 };
 
 __device__ __forceinline__ int64_t live_keys(const Shape& S, int b) {

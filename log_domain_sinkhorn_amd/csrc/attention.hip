@@ -1,6 +1,8 @@
 // C ABI of the attention operators: argument checks, launch plans and
 // workspaces. The kernels are in attend.h (forward), attend_grad.h (backward)
 // and attend_mass.h (gathered weight), instantiated per element type.
+#include <initializer_list>
+
 #include "attend.h"
 #include "attend_grad.h"
 #include "attend_mass.h"
@@ -8,9 +10,9 @@
 namespace sk {
 namespace attn {
 
-extern template void attend<__bf16>(const AttendArgs&, bool, bool, hipStream_t);
-extern template void attend<_Float16>(const AttendArgs&, bool, bool, hipStream_t);
-extern template void attend<float>(const AttendArgs&, bool, bool, hipStream_t);
+extern template void attend<__bf16>(const AttendArgs&, bool, hipStream_t);
+extern template void attend<_Float16>(const AttendArgs&, bool, hipStream_t);
+extern template void attend<float>(const AttendArgs&, bool, hipStream_t);
 extern template void attend_grad<__bf16>(const GradArgs&, bool, hipStream_t);
 extern template void attend_grad<_Float16>(const GradArgs&, bool, hipStream_t);
 extern template void attend_grad<float>(const GradArgs&, bool, hipStream_t);
@@ -73,6 +75,25 @@ void check(const sinkhorn_attention* a) {
   require(a->bias_stride[0] >= 0 && a->bias_stride[1] >= 0, "negative stride");
 }
 
+struct Operand {
+  const void* p;
+  const int64_t* stride;
+  int64_t width;
+};
+
+// Bytes a lane may load to LDS at once from the rows of `ops`: 16, 4, or 2 for
+// a row that is not a multiple of four bytes (loaded through registers), as for
+// row strides of 2^23 bytes and more, with which a tile could span 2^31 bytes.
+int32_t load_unit(std::initializer_list<Operand> ops, int64_t size) {
+  bool by16 = true, by4 = true;
+  for (const Operand& o : ops) {
+    if (o.stride[1] * size >= (int64_t(1) << 23)) return 2;
+    by16 = by16 && rows_aligned(o.p, o.stride, o.width, size, 16);
+    by4 = by4 && rows_aligned(o.p, o.stride, o.width, size, 4);
+  }
+  return by16 ? 16 : (by4 ? 4 : 2);
+}
+
 Shape make_shape(const sinkhorn_attention* a, const void* q, const void* k, const void* v) {
   Shape S{};
   S.batch = a->batch;
@@ -98,6 +119,7 @@ Shape make_shape(const sinkhorn_attention* a, const void* q, const void* k, cons
   S.qlen = a->query_lengths;
   S.klen = a->key_lengths;
   S.scale = (float)a->scale;
+  S.scale_lo = (float)(a->scale - (double)S.scale);
   S.c = (float)(a->scale * kLog2e);
   return S;
 }
@@ -123,7 +145,7 @@ AttendPlan plan_attend(const sinkhorn_attention* a, bool mass) {
   const int64_t rows = a->len_q * (a->heads_q / a->heads_kv);
   p.many = rows > 32;
   p.tiles = ceil_div(rows, p.many ? 128 : 32);
-  p.nsplit = splits(pairs * p.tiles, ceil_div(a->len_k, p.many ? 64 : 128));
+  p.nsplit = splits(pairs * p.tiles, ceil_div(a->len_k, p.many || a->dtype == SINKHORN_F32 ? 64 : 128));
   p.partial = p.nsplit > 1;
   p.scores = mass && !p.many;
   const int64_t dvp = ceil_div(a->dv, 4) * 4;
@@ -218,9 +240,10 @@ __global__ __launch_bounds__(256) void k_mass_scores(MassArgs A) {
   const int64_t j = (blockIdx.x - pair * chunks) * 1024 + 4 * threadIdx.x;
   const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
   const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
-  if (threadIdx.x < 32) srow[threadIdx.x] = mass_row(A, b, hk, threadIdx.x, nrows);
+  if (threadIdx.x < 32) srow[threadIdx.x] = mass_row(A, b, hk, threadIdx.x, nrows, A.exact);
   __syncthreads();
   f32x4 x = {0, 0, 0, 0};
+  const float f = A.exact ? (float)kLog2e : 1.0f;
   if (j < nkeys) {
     // the forward kernel wrote whole tiles of the live keys
     const float* sc = A.scores + pair * S.rows * A.score_ld + j;
@@ -228,7 +251,7 @@ __global__ __launch_bounds__(256) void k_mass_scores(MassArgs A) {
       const f32x4 t = *(const f32x4*)(sc + r * A.score_ld);
       const f32x2 st = srow[r];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = fmaf(st[1], ex2(t[e] - st[0]), x[e]);
+      for (int e = 0; e < 4; ++e) x[e] = fmaf(st[1], ex2((t[e] - st[0]) * f), x[e]);
     }
   }
 #pragma unroll
@@ -321,14 +344,13 @@ int sinkhorn_cross_attention(const sinkhorn_attention* a, const void* q, const v
       A.score_ld = p.score_ld;
     }
     if (rows) {
-      const bool al = rows_aligned(q, a->q_stride, a->d, size, 16) && rows_aligned(k, a->k_stride, a->d, size, 16) &&
-                      rows_aligned(v, a->v_stride, a->dv, size, 16);
+      A.unit = load_unit({{q, a->q_stride, a->d}, {k, a->k_stride, a->d}, {v, a->v_stride, a->dv}}, size);
       if (a->dtype == SINKHORN_BF16)
-        attend<__bf16>(A, p.many, al, st);
+        attend<__bf16>(A, p.many, st);
       else if (a->dtype == SINKHORN_F16)
-        attend<_Float16>(A, p.many, al, st);
+        attend<_Float16>(A, p.many, st);
       else
-        attend<float>(A, p.many, al, st);
+        attend<float>(A, p.many, st);
     }
     if (mass) {
       MassArgs M{};
@@ -340,6 +362,7 @@ int sinkhorn_cross_attention(const sinkhorn_attention* a, const void* q, const v
       if (p.scores) {
         M.scores = A.scores;
         M.score_ld = A.score_ld;
+        M.exact = a->dtype == SINKHORN_F32;
         hipLaunchKernelGGL(k_mass_scores, grid1((int64_t)a->batch * a->heads_kv * ceil_div(a->len_k, 1024), 256),
                            dim3(256), 0, st, M);
         SK_LAUNCH_CHECK();

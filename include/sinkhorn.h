@@ -450,9 +450,9 @@ int sinkhorn_sparse_barycentric(sinkhorn_problem* p, double eps, const float* g,
  * v [batch][len_k][heads_kv][dv], out and dout [batch][len_q][heads_q][dv],
  * gradients as what they are gradients of; each by its strides in elements
  * (batch, row, head), the last dimension contiguous. Inputs may have any
- * strides >= 0 and any alignment (rows that are 16-byte aligned and a whole
- * number of 16-byte chunks long are read 16 bytes at a time); the elements of
- * an output may not overlap. Query head h reads key head
+ * strides >= 0 and any alignment (operands whose rows are not 16-byte aligned, or
+ * no whole number of 16 bytes long, are first copied into the workspace); the
+ * elements of an output may not overlap. Query head h reads key head
  * h / (heads_q / heads_kv). lse is [batch][heads_q][len_q], gathered weights are
  * [batch][heads_kv][len_k], row weights [batch][len_q], contiguous fp32.
  *
@@ -480,7 +480,7 @@ int sinkhorn_sparse_barycentric(sinkhorn_problem* p, double eps, const float* g,
 typedef struct {
   int32_t dtype;              /* SINKHORN_F32, _F16 or _BF16: q, k, v, out and their gradients */
   int32_t batch;
-  int32_t heads_q, heads_kv;  /* heads_q a multiple of heads_kv */
+  int32_t heads_q, heads_kv;  /* heads_q a multiple of heads_kv, at most 8192 */
   int32_t d, dv;              /* 1 .. 128 (SINKHORN_ERR_UNSUPPORTED above) */
   int64_t len_q, len_k;       /* len_q * heads_q / heads_kv and len_k below 2^31 */
   double scale;               /* finite and > 0 */
@@ -492,13 +492,16 @@ typedef struct {
   const int32_t* key_lengths;    /* device [batch], nullable: len_k */
 } sinkhorn_attention;
 
-/* Bytes of device workspace (16-byte aligned) that a call on `at` needs; may
- * be 0. Host only. */
+/* Bytes of device workspace (16-byte aligned) that a call on `at` with these
+ * operands needs; may be 0. Of q, k, v and dout only the addresses count (NULL
+ * stands for an aligned one; v and dout only where the call has them). Host
+ * only. */
 #define SINKHORN_ATTEND 0         /* sinkhorn_cross_attention without mass_out */
 #define SINKHORN_ATTEND_MASS 1    /* sinkhorn_cross_attention with mass_out */
 #define SINKHORN_ATTEND_GRAD 2    /* sinkhorn_cross_attention_grad */
 #define SINKHORN_ATTENTION_MASS 3 /* sinkhorn_attention_mass */
-int sinkhorn_attention_workspace(const sinkhorn_attention* at, int32_t what, int64_t* bytes);
+int sinkhorn_attention_workspace(const sinkhorn_attention* at, int32_t what, const void* q,
+                                 const void* k, const void* v, const void* dout, int64_t* bytes);
 
 /* Forward pass: out and lse. With mass_out also the weight each key gathers,
  *   mass_out_j = mass_in_j + sum over rows i and the heads that share the key

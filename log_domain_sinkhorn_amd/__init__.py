@@ -222,7 +222,7 @@ _SIGS = {
     "sinkhorn_solve_multiscale": ([_p, _p, _p, _p, _p], _i32),
     "sinkhorn_sample_indices": ([_i64, _i32, ctypes.c_uint64, ctypes.c_uint64, _p, _p], _i32),
     "sinkhorn_sampled_residual": ([_p, _f64, _p, _p, _i32, _i32, ctypes.c_uint64, _p, _p], _i32),
-    "sinkhorn_attention_workspace": ([_p, _i32, _p], _i32),
+    "sinkhorn_attention_workspace": ([_p, _i32, _p, _p, _p, _p, _p], _i32),
     "sinkhorn_cross_attention": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
     "sinkhorn_cross_attention_grad": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
     "sinkhorn_attention_mass": ([_p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
@@ -508,9 +508,10 @@ def _attention(q, k, v, scale, key_bias, query_lengths, key_lengths):
     return a
 
 
-def _workspace(a, what, device):
+def _workspace(a, what, device, q, k, v=None, dout=None):
     n = _i64()
-    _check(lib().sinkhorn_attention_workspace(ctypes.byref(a), what, ctypes.byref(n)), "attention_workspace")
+    _check(lib().sinkhorn_attention_workspace(ctypes.byref(a), what, _ptr(q), _ptr(k), _ptr(v), _ptr(dout),
+                                              ctypes.byref(n)), "attention_workspace")
     return (torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None), n.value
 
 
@@ -556,7 +557,7 @@ def cross_attention(q, k, v, *, scale=None, key_bias=None, query_lengths=None, k
         out = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
         lse = torch.empty((B, hq, lq), dtype=torch.float32, device=q.device) if lse is None else lse
         a.out_stride = _strides3(out)
-        ws, n = _workspace(a, _ATTEND if mass_out is None else _ATTEND_MASS, q.device)
+        ws, n = _workspace(a, _ATTEND if mass_out is None else _ATTEND_MASS, q.device, q, k, v)
         _check(lib().sinkhorn_cross_attention(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
                                               _ptr(row_weight), _ptr(mass_in), _ptr(mass_out), _ptr(ws), n,
                                               _stream(q.device)), "cross_attention")
@@ -583,7 +584,7 @@ def cross_attention_grad(dout, q, k, v, out, lse, *, scale=None, key_bias=None, 
                       for t, like in ((dq, q), (dk, k), (dv, v)))
         a.out_stride, a.dout_stride = _strides3(out), _strides3(dout)
         a.dq_stride, a.dk_stride, a.dv_stride = _strides3(dq), _strides3(dk), _strides3(dv)
-        ws, n = _workspace(a, _ATTEND_GRAD, q.device)
+        ws, n = _workspace(a, _ATTEND_GRAD, q.device, q, k, v, dout)
         _check(lib().sinkhorn_cross_attention_grad(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
                                                    _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), n,
                                                    _stream(q.device)), "cross_attention_grad")
@@ -602,7 +603,7 @@ def attention_mass(q, k, lse, *, scale=None, key_bias=None, query_lengths=None, 
     with torch.cuda.device(q.device):
         if mass_out is None:
             mass_out = torch.empty((a.batch, a.heads_kv, a.len_k), dtype=torch.float32, device=q.device)
-        ws, n = _workspace(a, _ATTENTION_MASS, q.device)
+        ws, n = _workspace(a, _ATTENTION_MASS, q.device, q, k)
         _check(lib().sinkhorn_attention_mass(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(lse), _ptr(row_weight),
                                              _ptr(mass_in), _ptr(mass_out), _ptr(ws), n, _stream(q.device)),
                "attention_mass")

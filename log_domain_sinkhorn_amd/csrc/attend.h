@@ -34,21 +34,22 @@ struct AttendArgs {
   int32_t nsplit;  // splits of the keys
   int64_t tiles;   // row tiles per pair
   bool vec;        // out may be written four elements at a time
-  int32_t unit;    // bytes a lane may load to LDS from q, k and v: 16, 4, or 2 (through registers)
 };
 
-// Waves a SIMD that the LDS of a tile of `keys` keys of `row` bytes leaves room for.
-constexpr int attend_waves(int keys, int row) { return 4 * keys * row <= 72 * 1024 ? 2 : 1; }
+// Waves a SIMD that the LDS of tiles of `keys` keys of `row` bytes leaves room
+// for, with `waves` of them in a workgroup.
+constexpr int attend_waves(int keys, int row, int waves) {
+  return 4 * keys * row <= 72 * 1024 && waves >= 4 ? 2 : 1;
+}
 
-template <class T, int DP, int WQ, int WK, int NB, int CH>
-__global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)sizeof(T))) void k_attend(
+template <class T, int DP, int WQ, int WK, int NB>
+__global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)sizeof(T), WQ * WK)) void k_attend(
     AttendArgs A) {
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
   constexpr int NT = 64 * WQ * WK;
   constexpr int KT = 32 * NB * WK;  // keys per tile
   constexpr int NS = DP / 16, NDB = DP / 32;
-  using Ld = Loader<T, DP, KT, NT, CH>;
   // fp32: scores in natural units, rounded once, and 2^(log2e s - m) with the
   // product inside an fma: a weight is off by what its score's own rounding
   // makes it. 16-bit types: log2 units from the start, one operation less.
@@ -90,45 +91,9 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)
   const T* vbase = (const T*)S.v + b * S.vs[0] + hk * S.vs[2];
   const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
 
-  Ld lk, lv;
-  lk.init(S.ks[1], S.d, wave, lane);
-  lv.init(S.vs[1], S.dv, wave, lane);
-  // Column terms. The biases of tile t are loaded to sraw[t % 3] during tile
-  // t - 2; during tile t - 1 they decide which rows are loaded and become the
-  // terms of sterm[t % 2].
-  auto fetch = [&](int64_t t) {
-    if (!bias || wave * 64 >= KT) return;
-    const int j = wave * 64 + lane;
-    dma_load<4>(dma_rsrc(bias + t * KT), lds_offset(sraw[(t - t0) % 3]) + wave * 256, t * KT + j < nkeys ? 4 * j : kOutside);
-  };
-  auto start = [&](int64_t t) {
-    const int buf = (int)(t - t0) & 1;
-    const float* raw = sraw[(t - t0) % 3];
-    const int64_t left = nkeys - t * KT;  // live keys from the tile's first on
-    if (tid < KT) {
-      float term = 0.0f;
-      if (bias) {
-        const float x = raw[tid];
-        term = x <= kMasked ? -kInf : x * kTerm;
-      }
-      sterm[buf][tid] = tid < left ? term : -kInf;
-    }
-    auto both = [&](auto&& live) {
-      lk.start(kbase + t * KT * S.ks[1], sm + buf * 2 * kTileBytes, live, S.d, wave, lane);
-      lv.start(vbase + t * KT * S.vs[1], sm + buf * 2 * kTileBytes + kTileBytes, live, S.dv, wave, lane);
-    };
-    if (bias)
-      both([&](int r) { return r < left && !(raw[r] <= kMasked); });
-    else if (left < KT)
-      both([&](int r) { return r < left; });
-    else
-      both([](int) { return true; });
-  };
-  auto land = [&](int64_t t) {
-    const int buf = (int)(t - t0) & 1;
-    lk.land(sm + buf * 2 * kTileBytes, wave, lane);
-    lv.land(sm + buf * 2 * kTileBytes + kTileBytes, wave, lane);
-  };
+  KeyTiles<T, DP, KT, NT> keys(S, wave, lane);
+  auto fetch = [&](int64_t t) { keys.fetch(bias, t, t - t0, nkeys, sraw, wave, lane); };
+  auto start = [&](int64_t t) { keys.start(S, kbase, vbase, bias, t, t - t0, nkeys, sm, sterm, sraw, kTerm, wave, lane); };
   if (t0 < t1) {
     if (bias) {
       fetch(t0);
@@ -137,14 +102,13 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)
       __syncthreads();
     }
     start(t0);
-    land(t0);
   }
 
   V8 qf[NS];
   {
     const T* qrow = (const T*)S.q + b * S.qs[0] + qi * S.qs[1] + qh * S.qs[2];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) qf[s] = global_frag<T, CH == 16>(qrow, live_row, s, h, S.d);
+    for (int s = 0; s < NS; ++s) qf[s] = global_frag<T>(qrow, live_row && t0 < t1, s, h, S.d);
   }
   f32x16 o[NDB];
 #pragma unroll
@@ -229,7 +193,6 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)
 #pragma unroll
         for (int x = 0; x < NDB; ++x) o[x] = mma(TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane), p, o[x]);
       }
-    if (t + 1 < t1) land(t + 1);
   }
   l = half_sum(l);
   if (!live_row) {  // a row behind its sequence (its zero scores weigh nothing)
@@ -365,37 +328,24 @@ __global__ __launch_bounds__(256) void k_join(AttendArgs A) {
 }
 
 // many: 128 rows per workgroup, else all rows in one tile of 32
-template <class T, int DP, int CH>
+template <class T, int DP>
 void attend_launch(const AttendArgs& A, bool many, hipStream_t st) {
   const int64_t blocks = xcd_blocks((int64_t)A.S.batch * A.S.hkv * A.tiles * A.nsplit);
   constexpr int WK = sizeof(T) == 2 ? 4 : 2;  // fp32: two buffers of 128 keys would not fit
   if (many)
-    hipLaunchKernelGGL((k_attend<T, DP, 4, 1, 2, CH>), grid1(blocks, 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_attend<T, DP, 4, 1, 2>), grid1(blocks, 256), dim3(256), 0, st, A);
   else
-    hipLaunchKernelGGL((k_attend<T, DP, 1, WK, 1, CH>), grid1(blocks, 64 * WK), dim3(64 * WK), 0, st, A);
+    hipLaunchKernelGGL((k_attend<T, DP, 1, WK, 1>), grid1(blocks, 64 * WK), dim3(64 * WK), 0, st, A);
   SK_LAUNCH_CHECK();
 }
 
 // Instantiated once per element type (attend_*.hip).
 template <class T>
 void attend(const AttendArgs& A, bool many, hipStream_t st) {
-  const bool wide = A.S.d > 64 || A.S.dv > 64;
-  if (A.unit == 16) {
-    if (wide)
-      attend_launch<T, 128, 16>(A, many, st);
-    else
-      attend_launch<T, 64, 16>(A, many, st);
-  } else if (A.unit == 4) {
-    if (wide)
-      attend_launch<T, 128, 4>(A, many, st);
-    else
-      attend_launch<T, 64, 4>(A, many, st);
-  } else {
-    if (wide)
-      attend_launch<T, 128, 2>(A, many, st);
-    else
-      attend_launch<T, 64, 2>(A, many, st);
-  }
+  if (A.S.d > 64 || A.S.dv > 64)
+    attend_launch<T, 128>(A, many, st);
+  else
+    attend_launch<T, 64>(A, many, st);
   if (A.opart) {
     hipLaunchKernelGGL((k_join<T>), grid1(((int64_t)A.S.batch * A.S.hkv * A.S.rows + 7) / 8, 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();

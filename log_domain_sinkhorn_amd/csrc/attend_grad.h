@@ -26,7 +26,8 @@ struct GradArgs {
   void* dq;
   void* dk;
   void* dv;
-  f32x2* stat;    // [batch * hkv][rows]: lse in log2 units (+inf: the row takes no part), D
+  f32x2* stat;       // [batch * hkv][rows_pad]: lse (+inf: the row takes no part), D
+  int64_t rows_pad;  // rows rounded up to 64
   float* part_q;  // [split][batch * hkv][rows][dp], nullable
   float* part_k;  // [split][batch * hkv][lk][dp], nullable
   float* part_v;  // [split][batch * hkv][lk][dvp], nullable
@@ -34,15 +35,17 @@ struct GradArgs {
   int32_t split_q, split_kv;
   int64_t tiles_q, tiles_kv;
   bool vec_q, vec_k, vec_v;  // dq, dk, dv may be written four elements at a time
+  bool stat_vec;             // out and dout may be read 16 bytes at a time
 };
 
-// Row statistics: 16 lanes per row.
+// Row statistics: 16 lanes per row. The lse is kept in natural units for fp32
+// and in log2 units for the 16-bit types.
 template <class T>
 __global__ __launch_bounds__(256) void k_grad_stat(GradArgs A) {
   const Shape& S = A.S;
   const int64_t idx = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  if (idx >= (int64_t)S.batch * S.hkv * S.rows) return;
-  const int64_t pair = idx / S.rows, row = idx - pair * S.rows;
+  if (idx >= (int64_t)S.batch * S.hkv * A.rows_pad) return;
+  const int64_t pair = idx / A.rows_pad, row = idx - pair * A.rows_pad;
   const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
   const int64_t qi = row / S.group;
   const int qh = hk * S.group + (int)(row - qi * S.group);
@@ -54,13 +57,36 @@ __global__ __launch_bounds__(256) void k_grad_stat(GradArgs A) {
   const T* o = (const T*)A.out + b * A.os[0] + qi * A.os[1] + qh * A.os[2];
   const T* g = (const T*)A.dout + b * A.dos[0] + qi * A.dos[1] + qh * A.dos[2];
   float s = 0.0f;
-  for (int c = ln; c < S.dv; c += 16) s = fmaf((float)o[c], (float)g[c], s);
+  if (A.stat_vec) {  // 16-byte chunks
+    constexpr int EPC = 16 / (int)sizeof(T);
+    for (int c = ln * EPC; c < S.dv; c += 16 * EPC) {
+      union {
+        u32x4 u;
+        T e[EPC];
+      } x, y;
+      x.u = *(const u32x4*)(o + c);
+      y.u = *(const u32x4*)(g + c);
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) s = fmaf((float)x.e[e], (float)y.e[e], s);
+    }
+  } else {
+    for (int c = ln; c < S.dv; c += 16) s = fmaf((float)o[c], (float)g[c], s);
+  }
 #pragma unroll
   for (int x = 8; x > 0; x >>= 1) s += __shfl_xor(s, x, 16);
   if (ln == 0) {
     const float e = A.lse[((int64_t)b * S.hq + qh) * S.lq + qi];
-    A.stat[idx] = f32x2{e == -kInf ? kInf : e * (float)kLog2e, s};
+    A.stat[idx] = e == -kInf ? f32x2{kInf, 0.0f} : f32x2{sizeof(T) == 4 ? e : e * (float)kLog2e, s};
   }
+}
+
+// exp(score - lse) of a product x, its column term and the row's lse.
+template <class T>
+__device__ __forceinline__ float weight(const Shape& S, float x, float term, float lse) {
+  if constexpr (sizeof(T) == 4)
+    return ex2((fmaf(x, S.scale, fmaf(x, S.scale_lo, term)) - lse) * (float)kLog2e);
+  else
+    return ex2(fmaf(x, S.c, term - lse));
 }
 
 // Writes a transposed result (column: row `row` of the output, down: its
@@ -84,14 +110,16 @@ __device__ __forceinline__ void write_cols(const f32x16 (&x)[NDB], float f, floa
     }
 }
 
-// dQ: 4 waves of 32 rows, tiles of KT keys.
-template <class T, int DP, bool AL>
-__global__ __launch_bounds__(256) void k_grad_q(GradArgs A) {
+// dQ: 4 waves of 32 rows, tiles of KT keys in two LDS buffers (as k_attend).
+template <class T, int DP>
+__global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(GradArgs A) {
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
-  constexpr int KT = sizeof(T) == 2 ? 64 : 32, NT = 256, NS = DP / 16, NDB = DP / 32;
-  __shared__ __attribute__((aligned(16))) char tk[KT * TL::RB], tv[KT * TL::RB];
-  __shared__ __attribute__((aligned(16))) float sterm[KT];
+  constexpr int KT = sizeof(T) * DP <= 256 ? 64 : 32, NT = 256, NS = DP / 16, NDB = DP / 32;
+  constexpr int kTileBytes = KT * TL::RB;
+  constexpr float kTerm = sizeof(T) == 4 ? 1.0f : (float)kLog2e;
+  __shared__ __attribute__((aligned(16))) char sm[4 * kTileBytes];
+  __shared__ __attribute__((aligned(16))) float sterm[2][KT], sraw[3][KT];
 
   const Shape& S = A.S;
   const int64_t pairs = (int64_t)S.batch * S.hkv;
@@ -102,12 +130,12 @@ __global__ __launch_bounds__(256) void k_grad_q(GradArgs A) {
   const int64_t tile = rest / A.split_q;
   const int split = (int)(rest - tile * A.split_q);
   const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r32 = lane & 31;
 
   const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
   const int64_t row0 = tile * 128, row = row0 + 32 * wave + r32;
-  const bool live = row < nrows;
+  const bool live_row = row < nrows;
   const int64_t qi = row / S.group;
   const int qh = hk * S.group + (int)(row - qi * S.group);
   const int64_t ntiles = row0 < nrows ? (nkeys + KT - 1) / KT : 0;
@@ -117,6 +145,18 @@ __global__ __launch_bounds__(256) void k_grad_q(GradArgs A) {
   const T* kbase = (const T*)S.k + b * S.ks[0] + hk * S.ks[2];
   const T* vbase = (const T*)S.v + b * S.vs[0] + hk * S.vs[2];
   const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
+  KeyTiles<T, DP, KT, NT> keys(S, wave, lane);
+  auto fetch = [&](int64_t t) { keys.fetch(bias, t, t - t0, nkeys, sraw, wave, lane); };
+  auto start = [&](int64_t t) { keys.start(S, kbase, vbase, bias, t, t - t0, nkeys, sm, sterm, sraw, kTerm, wave, lane); };
+  if (t0 < t1) {
+    if (bias) {
+      fetch(t0);
+      if (t0 + 1 < t1) fetch(t0 + 1);
+      dma_wait();
+      __syncthreads();
+    }
+    start(t0);
+  }
 
   V8 qf[NS], gf[NS];
   {
@@ -124,49 +164,39 @@ __global__ __launch_bounds__(256) void k_grad_q(GradArgs A) {
     const T* grow = (const T*)A.dout + b * A.dos[0] + qi * A.dos[1] + qh * A.dos[2];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      qf[s] = global_frag<T, AL>(qrow, live, s, h, S.d);
-      gf[s] = global_frag<T, AL>(grow, live, s, h, S.dv);
+      qf[s] = global_frag<T>(qrow, live_row && t0 < t1, s, h, S.d);
+      gf[s] = global_frag<T>(grow, live_row && t0 < t1, s, h, S.dv);
     }
   }
-  const f32x2 st = live ? A.stat[pair * S.rows + row] : f32x2{kInf, 0.0f};
+  const f32x2 st = live_row ? A.stat[pair * A.rows_pad + row] : f32x2{kInf, 0.0f};
   f32x16 dq[NDB];
 #pragma unroll
   for (int n = 0; n < NDB; ++n) dq[n] = zero16();
 
-  Stage<T, DP, KT, NT, AL> xk, xv;
-  float term = 0.0f;
-  if (t0 < t1) {
-    xk.load(kbase, S.ks[1], t0 * KT, nkeys, S.d, tid);
-    xv.load(vbase, S.vs[1], t0 * KT, nkeys, S.dv, tid);
-    if (tid < KT) term = column_term(bias, t0 * KT + tid, nkeys);
-  }
   for (int64_t t = t0; t < t1; ++t) {
-    __syncthreads();
-    if (tid < KT) sterm[tid] = term;
-    __syncthreads();
-    xk.put_masked(tk, sterm, tid);
-    xv.put_masked(tv, sterm, tid);
+    const int buf = (int)(t - t0) & 1;
+    dma_wait();
     __syncthreads();
     if (t + 1 < t1) {
-      xk.load(kbase, S.ks[1], (t + 1) * KT, nkeys, S.d, tid);
-      xv.load(vbase, S.vs[1], (t + 1) * KT, nkeys, S.dv, tid);
-      if (tid < KT) term = column_term(bias, (t + 1) * KT + tid, nkeys);
+      start(t + 1);
+      if (t + 2 < t1) fetch(t + 2);
     }
+    const char* tk = sm + buf * 2 * kTileBytes;
+    const char* tv = tk + kTileBytes;
 #pragma unroll
     for (int n = 0; n < KT / 32; ++n) {
       f32x16 p = zero16(), g = zero16();
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        p = mma(TL::row_frag(tk, 32 * n + r32, s, h), qf[s], p);
-        g = mma(TL::row_frag(tv, 32 * n + r32, s, h), gf[s], g);
-      }
+      for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tk, 32 * n + r32, s, h), qf[s], p);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) g = mma(TL::row_frag(tv, 32 * n + r32, s, h), gf[s], g);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const f32x4 ct = *(const f32x4*)&sterm[32 * n + 8 * q + 4 * h];
+        const f32x4 ct = *(const f32x4*)&sterm[buf][32 * n + 8 * q + 4 * h];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = 4 * q + e;
-          p[i] = ex2(fmaf(p[i], S.c, ct[e]) - st[0]) * (g[i] - st[1]);
+          p[i] = weight<T>(S, p[i], ct[e], st[0]) * (g[i] - st[1]);
         }
       }
 #pragma unroll
@@ -183,14 +213,15 @@ __global__ __launch_bounds__(256) void k_grad_q(GradArgs A) {
   write_cols<T, NDB>(dq, S.scale, prow, A.dp, orow, S.d, A.vec_q, h);
 }
 
-// dK and dV: 4 waves of 32 keys, tiles of RT rows.
-template <class T, int DP, bool AL>
-__global__ __launch_bounds__(256) void k_grad_kv(GradArgs A) {
+// dK and dV: 4 waves of 32 keys, tiles of RT rows in two LDS buffers.
+template <class T, int DP>
+__global__ __launch_bounds__(256, sizeof(T) * DP <= 128 ? 2 : 1) void k_grad_kv(GradArgs A) {
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
-  constexpr int RT = sizeof(T) == 2 ? 64 : 32, NT = 256, NS = DP / 16, NDB = DP / 32;
-  __shared__ __attribute__((aligned(16))) char tq[RT * TL::RB], tg[RT * TL::RB];
-  __shared__ __attribute__((aligned(16))) float slse[RT], sdot[RT];
+  constexpr int RT = sizeof(T) * DP <= 256 ? 64 : 32, NT = 256, NS = DP / 16, NDB = DP / 32;
+  constexpr int kTileBytes = RT * TL::RB;
+  __shared__ __attribute__((aligned(16))) char sm[4 * kTileBytes];
+  __shared__ __attribute__((aligned(16))) f32x2 sstat[2][RT];
 
   const Shape& S = A.S;
   const int64_t pairs = (int64_t)S.batch * S.hkv;
@@ -201,26 +232,37 @@ __global__ __launch_bounds__(256) void k_grad_kv(GradArgs A) {
   const int64_t tile = rest / A.split_kv;
   const int split = (int)(rest - tile * A.split_kv);
   const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r32 = lane & 31;
 
   const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
   const int64_t key0 = tile * 128, key = key0 + 32 * wave + r32;
   const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
-  const float term = column_term(bias, key, nkeys);
+  const float term = column_term(bias, key, nkeys, sizeof(T) == 4 ? 1.0f : (float)kLog2e);
   const int64_t ntiles = key0 < nkeys ? (nrows + RT - 1) / RT : 0;
   const int64_t per = (ntiles + A.split_kv - 1) / A.split_kv;
   const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
+
+  RowTiles<T, DP, RT, NT> rq(S, S.q, S.qs, b, hk, S.d, wave, lane), rg(S, A.dout, A.dos, b, hk, S.dv, wave, lane);
+  auto start = [&](int64_t t) {
+    const int buf = (int)(t - t0) & 1;
+    rq.start(S, t, nrows, sm + buf * 2 * kTileBytes, wave, lane);
+    rg.start(S, t, nrows, sm + buf * 2 * kTileBytes + kTileBytes, wave, lane);
+    // RT * 8 bytes of statistics (rows_pad covers the tile), 256 a wave
+    if (wave < RT / 32)
+      dma_load<4>(dma_rsrc(A.stat + pair * A.rows_pad + t * RT), lds_offset(sstat[buf]) + wave * 256, wave * 256 + 4 * lane);
+  };
+  if (t0 < t1) start(t0);
 
   V8 kf[NS], vf[NS];
   {
     const T* krow = (const T*)S.k + b * S.ks[0] + key * S.ks[1] + hk * S.ks[2];
     const T* vrow = (const T*)S.v + b * S.vs[0] + key * S.vs[1] + hk * S.vs[2];
-    const bool live = term != -kInf;
+    const bool live = term != -kInf && t0 < t1;  // no rows: nothing to read them for
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      kf[s] = global_frag<T, AL>(krow, live, s, h, S.d);
-      vf[s] = global_frag<T, AL>(vrow, live, s, h, S.dv);
+      kf[s] = global_frag<T>(krow, live, s, h, S.d);
+      vf[s] = global_frag<T>(vrow, live, s, h, S.dv);
     }
   }
   f32x16 dk[NDB], dv[NDB];
@@ -229,56 +271,29 @@ __global__ __launch_bounds__(256) void k_grad_kv(GradArgs A) {
     dk[n] = zero16();
     dv[n] = zero16();
   }
-
-  constexpr int N = RT * TL::CPR / NT, STEP = NT / TL::CPR;
-  const int lc = tid % TL::CPR, lr = tid / TL::CPR;
-  const T* qbase = (const T*)S.q + b * S.qs[0];
-  const T* gbase = (const T*)A.dout + b * A.dos[0];
-  u32x4 xq[N], xg[N];
-  f32x2 st = {kInf, 0.0f};
-  auto load = [&](int64_t t) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int64_t row = t * RT + lr + n * STEP;
-      const bool live = row < nrows;
-      const int64_t qi = row / S.group;
-      const int qh = hk * S.group + (int)(row - qi * S.group);
-      xq[n] = live ? load_chunk<T, AL>(qbase + qi * S.qs[1] + qh * S.qs[2], lc, S.d) : u32x4{0, 0, 0, 0};
-      xg[n] = live ? load_chunk<T, AL>(gbase + qi * A.dos[1] + qh * A.dos[2], lc, S.dv) : u32x4{0, 0, 0, 0};
-    }
-    if (tid < RT) st = t * RT + tid < nrows ? A.stat[pair * S.rows + t * RT + tid] : f32x2{kInf, 0.0f};
-  };
-  if (t0 < t1) load(t0);
   for (int64_t t = t0; t < t1; ++t) {
+    const int buf = (int)(t - t0) & 1;
+    dma_wait();
     __syncthreads();
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      *(u32x4*)(tq + TL::at(lr + n * STEP, lc)) = xq[n];
-      *(u32x4*)(tg + TL::at(lr + n * STEP, lc)) = xg[n];
-    }
-    if (tid < RT) {
-      slse[tid] = st[0];
-      sdot[tid] = st[1];
-    }
-    __syncthreads();
-    if (t + 1 < t1) load(t + 1);
+    if (t + 1 < t1) start(t + 1);
+    const char* tq = sm + buf * 2 * kTileBytes;
+    const char* tg = tq + kTileBytes;
 #pragma unroll
     for (int n = 0; n < RT / 32; ++n) {
       f32x16 p = zero16(), g = zero16();
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        p = mma(TL::row_frag(tq, 32 * n + r32, s, h), kf[s], p);
-        g = mma(TL::row_frag(tg, 32 * n + r32, s, h), vf[s], g);
-      }
+      for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tq, 32 * n + r32, s, h), kf[s], p);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x4 le = *(const f32x4*)&slse[32 * n + 8 * q + 4 * h];
-        const f32x4 dd = *(const f32x4*)&sdot[32 * n + 8 * q + 4 * h];
+      for (int s = 0; s < NS; ++s) g = mma(TL::row_frag(tg, 32 * n + r32, s, h), vf[s], g);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 4 * q + e;
-          p[i] = ex2(fmaf(p[i], S.c, term) - le[e]);
-          g[i] = p[i] * (g[i] - dd[e]);
+      for (int q = 0; q < 8; ++q) {
+        // two rows: {lse, D, lse, D}
+        const f32x4 w = *(const f32x4*)&sstat[buf][32 * n + 8 * (q >> 1) + 4 * h + 2 * (q & 1)];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = 2 * q + e;
+          p[i] = weight<T>(S, p[i], term, w[2 * e]);
+          g[i] = p[i] * (g[i] - w[2 * e + 1]);
         }
       }
 #pragma unroll
@@ -326,40 +341,31 @@ __global__ __launch_bounds__(256) void k_grad_join(const float* part, int nsplit
     store4<T, false>(orow, c, d, x);
 }
 
-template <class T, int DP, bool AL>
+template <class T, int DP>
 void grad_launch(const GradArgs& A, hipStream_t st) {
   const int64_t pairs = (int64_t)A.S.batch * A.S.hkv;
   if (A.S.rows > 0) {
-    hipLaunchKernelGGL((k_grad_q<T, DP, AL>), grid1(xcd_blocks(pairs * A.tiles_q * A.split_q), 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_grad_q<T, DP>), grid1(xcd_blocks(pairs * A.tiles_q * A.split_q), 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   }
   if (A.S.lk > 0) {
-    hipLaunchKernelGGL((k_grad_kv<T, DP, AL>), grid1(xcd_blocks(pairs * A.tiles_kv * A.split_kv), 256), dim3(256), 0,
-                       st, A);
+    hipLaunchKernelGGL((k_grad_kv<T, DP>), grid1(xcd_blocks(pairs * A.tiles_kv * A.split_kv), 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   }
 }
 
 // Instantiated once per element type (attend_grad_*.hip).
 template <class T>
-void attend_grad(const GradArgs& A, bool aligned, hipStream_t st) {
+void attend_grad(const GradArgs& A, hipStream_t st) {
   const int64_t pairs = (int64_t)A.S.batch * A.S.hkv;
   if (A.S.rows > 0) {
-    hipLaunchKernelGGL((k_grad_stat<T>), grid1((pairs * A.S.rows + 15) / 16, 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_grad_stat<T>), grid1((pairs * A.rows_pad + 15) / 16, 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   }
-  const bool wide = A.S.d > 64 || A.S.dv > 64;
-  if (wide) {
-    if (aligned)
-      grad_launch<T, 128, true>(A, st);
-    else
-      grad_launch<T, 128, false>(A, st);
-  } else {
-    if (aligned)
-      grad_launch<T, 64, true>(A, st);
-    else
-      grad_launch<T, 64, false>(A, st);
-  }
+  if (A.S.d > 64 || A.S.dv > 64)
+    grad_launch<T, 128>(A, st);
+  else
+    grad_launch<T, 64>(A, st);
   auto join = [&](const float* part, int nsplit, int64_t rows, int32_t dp, int32_t group, void* out, const int64_t* s,
                   int32_t d, bool vec) {
     if (!part || rows == 0) return;

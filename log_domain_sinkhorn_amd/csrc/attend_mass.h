@@ -30,24 +30,32 @@ struct MassArgs {
   bool exact;             // scores in natural units (fp32), else log2 units
 };
 
-// A row's log-sum-exp (in log2 units unless `natural`) (+inf: the row takes no part) and weight.
-__device__ __forceinline__ f32x2 mass_row(const MassArgs& A, int b, int hk, int64_t row, int64_t nrows,
-                                          bool natural = false) {
+// A row's log-sum-exp (+inf: the row takes no part) and weight. In log2 units
+// unless `natural`; what the fp32 product lse log2e rounds off goes into the
+// weight.
+__device__ __forceinline__ f32x2 mass_row(const MassArgs& A, int b, int hk, int64_t row, int64_t nrows, bool natural) {
   const Shape& S = A.S;
   if (row >= nrows) return f32x2{kInf, 0.0f};
   const int64_t qi = row / S.group;
   const int qh = hk * S.group + (int)(row - qi * S.group);
   const float e = A.lse[((int64_t)b * S.hq + qh) * S.lq + qi];
-  return f32x2{e == -kInf ? kInf : (natural ? e : e * (float)kLog2e), A.weight ? A.weight[b * S.lq + qi] : 1.0f};
+  const float w = A.weight ? A.weight[b * S.lq + qi] : 1.0f;
+  if (e == -kInf) return f32x2{kInf, w};
+  if (natural) return f32x2{e, w};
+  const float t = e * (float)kLog2e;
+  const float lost = fmaf(e, (float)kLog2e, -t) + e * (float)(kLog2e - (double)(float)kLog2e);
+  return f32x2{t, w * ex2(-lost)};
 }
 
-template <class T, int DP, bool AL>
-__global__ __launch_bounds__(256) void k_mass(MassArgs A) {
+template <class T, int DP>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A) {
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
   constexpr int RT = 64, NT = 256, NS = DP / 16;
-  __shared__ __attribute__((aligned(16))) char tq[RT * TL::RB];
-  __shared__ __attribute__((aligned(16))) float slse[RT], sw[RT];
+  constexpr bool kExact = sizeof(T) == 4;  // scores in natural units, rounded once
+  constexpr int kTileBytes = RT * TL::RB;
+  __shared__ __attribute__((aligned(16))) char sm[2 * kTileBytes];
+  __shared__ __attribute__((aligned(16))) f32x2 sstat[2][RT];
 
   const Shape& S = A.S;
   const int64_t pairs = (int64_t)S.batch * S.hkv;
@@ -58,61 +66,62 @@ __global__ __launch_bounds__(256) void k_mass(MassArgs A) {
   const int64_t tile = rest / A.nsplit;
   const int split = (int)(rest - tile * A.nsplit);
   const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r32 = lane & 31;
 
   const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
   const int64_t key0 = tile * 128, key = key0 + 32 * wave + r32;
   const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
-  const float term = column_term(bias, key, nkeys);
+  const float term = column_term(bias, key, nkeys, kExact ? 1.0f : (float)kLog2e);
   const int64_t ntiles = key0 < nkeys ? (nrows + RT - 1) / RT : 0;
   const int64_t per = (ntiles + A.nsplit - 1) / A.nsplit;
   const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
 
+  RowTiles<T, DP, RT, NT> rows(S, S.q, S.qs, b, hk, S.d, wave, lane);
+  f32x2 st = {kInf, 0.0f};
+  auto start = [&](int64_t t) { rows.start(S, t, nrows, sm + ((t - t0) & 1) * kTileBytes, wave, lane); };
+  auto stat = [&](int64_t t) {
+    if (tid < RT) st = mass_row(A, b, hk, t * RT + tid, nrows, kExact);
+  };
+  if (t0 < t1) {
+    start(t0);
+    stat(t0);
+    if (tid < RT) sstat[0][tid] = st;
+    if (t0 + 1 < t1) stat(t0 + 1);
+  }
   V8 kf[NS];
   {
     const T* krow = (const T*)S.k + b * S.ks[0] + key * S.ks[1] + hk * S.ks[2];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) kf[s] = global_frag<T, AL>(krow, term != -kInf, s, h, S.d);
+    for (int s = 0; s < NS; ++s) kf[s] = global_frag<T>(krow, term != -kInf && t0 < t1, s, h, S.d);
   }
-  constexpr int N = RT * TL::CPR / NT, STEP = NT / TL::CPR;
-  const int lc = tid % TL::CPR, lr = tid / TL::CPR;
-  const T* qbase = (const T*)S.q + b * S.qs[0];
-  u32x4 xq[N];
-  f32x2 st = {kInf, 0.0f};
-  auto load = [&](int64_t t) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int64_t row = t * RT + lr + n * STEP;
-      const int64_t qi = row / S.group;
-      const int qh = hk * S.group + (int)(row - qi * S.group);
-      xq[n] = row < nrows ? load_chunk<T, AL>(qbase + qi * S.qs[1] + qh * S.qs[2], lc, S.d) : u32x4{0, 0, 0, 0};
-    }
-    if (tid < RT) st = mass_row(A, b, hk, t * RT + tid, nrows);
-  };
   float sum = 0.0f;
-  if (t0 < t1) load(t0);
   for (int64_t t = t0; t < t1; ++t) {
+    const int buf = (int)(t - t0) & 1;
+    dma_wait();
     __syncthreads();
-#pragma unroll
-    for (int n = 0; n < N; ++n) *(u32x4*)(tq + TL::at(lr + n * STEP, lc)) = xq[n];
-    if (tid < RT) {
-      slse[tid] = st[0];
-      sw[tid] = st[1];
+    if (t + 1 < t1) {
+      if (tid < RT) sstat[buf ^ 1][tid] = st;
+      start(t + 1);
+      if (t + 2 < t1) stat(t + 2);
     }
-    __syncthreads();
-    if (t + 1 < t1) load(t + 1);
+    const char* tq = sm + buf * kTileBytes;
 #pragma unroll
     for (int n = 0; n < RT / 32; ++n) {
       f32x16 p = zero16();
 #pragma unroll
       for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tq, 32 * n + r32, s, h), kf[s], p);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x4 le = *(const f32x4*)&slse[32 * n + 8 * q + 4 * h];
-        const f32x4 w = *(const f32x4*)&sw[32 * n + 8 * q + 4 * h];
+      for (int q = 0; q < 8; ++q) {
+        // two rows: {lse, weight, lse, weight}
+        const f32x4 w = *(const f32x4*)&sstat[buf][32 * n + 8 * (q >> 1) + 4 * h + 2 * (q & 1)];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum = fmaf(w[e], ex2(fmaf(p[4 * q + e], S.c, term) - le[e]), sum);
+        for (int e = 0; e < 2; ++e) {
+          const float x = p[2 * q + e];
+          const float a = kExact ? (fmaf(x, S.scale, fmaf(x, S.scale_lo, term)) - w[2 * e]) * (float)kLog2e
+                                 : fmaf(x, S.c, term - w[2 * e]);
+          sum = fmaf(w[2 * e + 1], ex2(a), sum);
+        }
       }
     }
   }
@@ -126,20 +135,12 @@ __global__ __launch_bounds__(256) void k_mass(MassArgs A) {
 
 // Instantiated once per element type (attend_mass_*.hip).
 template <class T>
-void attend_mass(const MassArgs& A, bool aligned, hipStream_t st) {
-  const int64_t pairs = (int64_t)A.S.batch * A.S.hkv;
-  const dim3 grid = grid1(xcd_blocks(pairs * A.tiles * A.nsplit), 256);
-  if (A.S.d > 64) {
-    if (aligned)
-      hipLaunchKernelGGL((k_mass<T, 128, true>), grid, dim3(256), 0, st, A);
-    else
-      hipLaunchKernelGGL((k_mass<T, 128, false>), grid, dim3(256), 0, st, A);
-  } else {
-    if (aligned)
-      hipLaunchKernelGGL((k_mass<T, 64, true>), grid, dim3(256), 0, st, A);
-    else
-      hipLaunchKernelGGL((k_mass<T, 64, false>), grid, dim3(256), 0, st, A);
-  }
+void attend_mass(const MassArgs& A, hipStream_t st) {
+  const dim3 grid = grid1(xcd_blocks((int64_t)A.S.batch * A.S.hkv * A.tiles * A.nsplit), 256);
+  if (A.S.d > 64)
+    hipLaunchKernelGGL((k_mass<T, 128>), grid, dim3(256), 0, st, A);
+  else
+    hipLaunchKernelGGL((k_mass<T, 64>), grid, dim3(256), 0, st, A);
   SK_LAUNCH_CHECK();
 }
 

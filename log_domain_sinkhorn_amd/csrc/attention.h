@@ -168,30 +168,18 @@ struct Tile {
   }
 };
 
-// Chunk c of a row of d elements in memory, zero behind d. AL: rows and the
-// base are 16-byte aligned and d is a multiple of the chunk.
-template <class T, bool AL>
+// Chunk c of a row of d elements in memory (16-byte aligned, whole chunks),
+// zero behind d.
+template <class T>
 __device__ __forceinline__ u32x4 load_chunk(const T* row, int c, int d) {
   constexpr int EPC = 16 / (int)sizeof(T);
-  if constexpr (AL) {
-    if (c * EPC >= d) return u32x4{0, 0, 0, 0};
-    return *(const u32x4*)(row + c * EPC);
-  } else {
-    union {
-      T e[EPC];
-      u32x4 u;
-    } x;
-    x.u = u32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < EPC; ++e)
-      if (c * EPC + e < d) x.e[e] = row[c * EPC + e];
-    return x.u;
-  }
+  if (c * EPC >= d) return u32x4{0, 0, 0, 0};
+  return *(const u32x4*)(row + c * EPC);
 }
 
 // Operand fragment straight from memory: k = 16 s + 8 h + e of the row, zero
 // behind d or when the row is not live.
-template <class T, bool AL>
+template <class T>
 __device__ __forceinline__ typename Vec<T>::V8 global_frag(const T* row, bool live, int s, int h, int d) {
   constexpr int N = sizeof(T) / 2;  // chunks per fragment
   union {
@@ -199,61 +187,23 @@ __device__ __forceinline__ typename Vec<T>::V8 global_frag(const T* row, bool li
     typename Vec<T>::V8 v;
   } x;
 #pragma unroll
-  for (int n = 0; n < N; ++n)
-    x.u[n] = live ? load_chunk<T, AL>(row, (2 * s + h) * N + n, d) : u32x4{0, 0, 0, 0};
+  for (int n = 0; n < N; ++n) x.u[n] = live ? load_chunk<T>(row, (2 * s + h) * N + n, d) : u32x4{0, 0, 0, 0};
   return x.v;
 }
 
-// Rows [j0, j0 + ROWS) of a matrix, staged by the workgroup's NT threads
-// through registers into a Tile: issue the loads of the next tile, compute,
-// then put them down. Rows at or behind `count` become zero.
-template <class T, int DP, int ROWS, int NT, bool AL>
-struct Stage {
-  using TL = Tile<T, DP>;
-  static constexpr int N = ROWS * TL::CPR / NT;  // chunks per thread
-  static constexpr int STEP = NT / TL::CPR;      // rows between a thread's chunks
-  static_assert(N * NT == ROWS * TL::CPR && N >= 1, "tile and workgroup sizes");
-  u32x4 x[N];
-
-  __device__ __forceinline__ void load(const T* base, int64_t stride, int64_t j0, int64_t count, int d, int tid) {
-    const int c = tid % TL::CPR, r0 = tid / TL::CPR;
-    const T* p = base + (j0 + r0) * stride;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      x[n] = j0 + r0 + n * STEP < count ? load_chunk<T, AL>(p, c, d) : u32x4{0, 0, 0, 0};
-      p += STEP * stride;
-    }
-  }
-  __device__ __forceinline__ void put(char* t, int tid) const {
-    const int c = tid % TL::CPR, r0 = tid / TL::CPR;
-#pragma unroll
-    for (int n = 0; n < N; ++n) *(u32x4*)(t + TL::at(r0 + n * STEP, c)) = x[n];
-  }
-  // the same with the rows whose column term in LDS is -inf cleared
-  __device__ __forceinline__ void put_masked(char* t, const float* term, int tid) const {
-    const int c = tid % TL::CPR, r0 = tid / TL::CPR;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int r = r0 + n * STEP;
-      *(u32x4*)(t + TL::at(r, c)) = term[r] == -kInf ? u32x4{0, 0, 0, 0} : x[n];
-    }
-  }
-};
-
-// The same straight from memory to LDS (buffer loads with an LDS destination:
-// no registers, no LDS writes by the waves), CH = 16 or 4 bytes a lane: 16 for
-// rows that are 16-byte aligned and a whole number of 16-byte chunks long, 4 for
-// any multiple of four bytes. A wave's instruction fills 64 CH bytes of LDS in
-// lane order, so the swizzle is applied to the address a lane fetches. Rows
-// that are not live, and what lies behind a row's width, get an offset behind
-// the buffer's end, for which the load puts zero. A tile may span at most
-// 2^31 bytes.
+// Tiles go straight from memory to LDS (buffer loads with an LDS destination:
+// no registers, no LDS writes by the waves), 16 bytes a lane. A wave's
+// instruction fills 1 KB of LDS in lane order, so the swizzle is applied to
+// the chunk a lane fetches. Rows that take no part, and chunks behind a row's
+// width, get an offset behind the buffer's end, for which the load puts zero. A
+// tile spans less than 2^31 bytes (the host copies operands for which it
+// would not).
 constexpr uint32_t kOutside = 0x80000000u;
 
 // Written as assembly because the compiler waits for a load to LDS before any
 // LDS read that may alias it, so also before reads of the other buffer;
 // dma_wait() comes before the barrier behind which the data is read. The loads
-// have no destination register.
+// have no destination register. CH: bytes a lane, 16 or 4.
 template <int CH>
 __device__ __forceinline__ void dma_load(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds, uint32_t off) {
   lds = __builtin_amdgcn_readfirstlane(lds);
@@ -283,94 +233,39 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t dma_rsrc(const void* base) {
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
 }
+__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// Loader of the rows of a tile by the workgroup's NT threads: start(t, ...)
-// begins, land() finishes (staged loads only), dma_wait() and a barrier make
-// the tile readable. `wave` must be uniform.
-template <class T, int DP, int ROWS, int NT, int CH>
+// Loader of ROWS rows by the workgroup's NT threads. `wave` must be uniform.
+template <class T, int DP, int ROWS, int NT>
 struct Loader {
   using TL = Tile<T, DP>;
-  static constexpr int UPR = TL::RB / CH;              // units per row
-  static constexpr int N = ROWS * UPR / NT;            // units per thread
-  static constexpr int RPI = UPR > 64 ? 1 : 64 / UPR;  // rows per instruction of a wave
-  static constexpr int IPR = UPR > 64 ? UPR / 64 : 1;  // instructions per row
-  static constexpr int NR = N / IPR;                   // different rows of a lane
-  static_assert(N * NT == ROWS * UPR && N >= IPR && N % IPR == 0, "tile and workgroup sizes");
+  static constexpr int N = ROWS * TL::CPR / NT;  // chunks per thread
+  static constexpr int RPI = 64 / TL::CPR;       // rows per instruction of a wave
+  static_assert(N * NT == ROWS * TL::CPR && N >= 1 && RPI >= 1, "tile and workgroup sizes");
+  uint32_t off[N];  // byte offset of this lane's chunk from the tile's start
 
-  uint32_t off[CH == 16 ? N : 1];  // byte offset of this lane's unit from the tile's start
-  uint32_t pitch;                  // bytes between rows
-
-  // tile row of this lane's units n * IPR ...
-  __device__ __forceinline__ static int row(int n, int wave, int lane) {
-    return (wave * NR + n) * RPI + (UPR >= 64 ? 0 : lane / UPR);
-  }
-  __device__ __forceinline__ void init(int64_t stride, int d, int wave, int lane) {
-    pitch = (uint32_t)(stride * (int64_t)sizeof(T));
-    if constexpr (CH == 16) {
-      static_assert(IPR == 1, "16-byte units: at most 64 a row");
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const int r = row(n, wave, lane);
-        const int c = (lane % UPR) ^ TL::swz(r);
-        off[n] = c * TL::EPC < d ? r * pitch + 16 * c : kOutside;
-      }
-    }
-  }
-  // live(r): row r of the tile takes part
-  template <class F>
-  __device__ __forceinline__ void start(const T* base, char* t, F&& live, int d, int wave, int lane) {
-    const __amdgpu_buffer_rsrc_t rsrc = dma_rsrc(base);
-    const uint32_t lds = lds_offset(t) + wave * (N * 64 * CH);
-    // keeps the many offsets and masks of 4-byte units from being computed
-    // ahead of the loop over tiles and held in registers
-    uint32_t step = pitch;
-    if constexpr (CH == 4) asm volatile("" : "+s"(step), "+s"(d));
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      if constexpr (CH == 16) {
-        dma_load<16>(rsrc, lds + n * 1024, live(row(n, wave, lane)) ? off[n] : kOutside);
-      } else {
-        const int r = row(n, wave, lane);
-        const bool on = live(r);
-#pragma unroll
-        for (int i = 0; i < IPR; ++i) {
-          const int u = UPR > 64 ? lane + 64 * i : lane % UPR;     // 4-byte unit of the LDS row
-          const int w = (((u >> 2) ^ TL::swz(r)) << 2) + (u & 3);  // and of the row in memory
-          const bool in = on && w * 4 < d * (int)sizeof(T);
-          dma_load<4>(rsrc, lds + (n * IPR + i) * 256, in ? r * step + 4 * w : kOutside);
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ void land(char*, int, int) const {}
-};
-
-// Rows at odd addresses (CH = 2): element by element through registers, in
-// the same places.
-template <class T, int DP, int ROWS, int NT>
-struct Loader<T, DP, ROWS, NT, 2> {
-  using TL = Tile<T, DP>;
-  static constexpr int N = ROWS * TL::CPR / NT, NR = N, RPI = 64 / TL::CPR;
-  static_assert(N * NT == ROWS * TL::CPR && N >= 1, "tile and workgroup sizes");
-  u32x4 x[N];
-  int64_t pitch;
-
+  // tile row of this lane's chunk n
   __device__ __forceinline__ static int row(int n, int wave, int lane) { return (wave * N + n) * RPI + lane / TL::CPR; }
-  __device__ __forceinline__ void init(int64_t stride, int, int, int) { pitch = stride; }
+
+  // at(r): byte offset of row r of the tile
   template <class F>
-  __device__ __forceinline__ void start(const T* base, char*, F&& live, int d, int wave, int lane) {
+  __device__ __forceinline__ void place(F&& at, int d, int wave, int lane) {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      x[n] = live(row(n, wave, lane)) ? load_chunk<T, false>(base + row(n, wave, lane) * pitch, lane % TL::CPR, d)
-                                      : u32x4{0, 0, 0, 0};
+    for (int n = 0; n < N; ++n) {
+      const int r = row(n, wave, lane);
+      const int c = (lane % TL::CPR) ^ TL::swz(r);
+      off[n] = c * TL::EPC < d ? at(r) + 16 * c : kOutside;
+    }
   }
-  __device__ __forceinline__ void land(char* t, int wave, int lane) const {
+  // live(r): row r takes part
+  template <class F>
+  __device__ __forceinline__ void start(const T* base, char* t, F&& live, int wave, int lane) const {
+    const __amdgpu_buffer_rsrc_t rsrc = dma_rsrc(base);
+    const uint32_t lds = lds_offset(t) + wave * (N * 1024);
 #pragma unroll
-    for (int n = 0; n < N; ++n) *(u32x4*)(t + TL::at(row(n, wave, lane), lane % TL::CPR)) = x[n];
+    for (int n = 0; n < N; ++n) dma_load<16>(rsrc, lds + n * 1024, live(row(n, wave, lane)) ? off[n] : kOutside);
   }
 };
-
-__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // ---------------------------------------------------------------- arguments
 // One attention call as the kernels see it (strides in elements: batch, row,
@@ -378,6 +273,7 @@ __device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" :
 struct Shape {
   int32_t batch, hq, hkv, group;
   int32_t d, dv;
+  uint32_t group_mul;    // ceil(2^32 / group): x / group = (x group_mul) >> 32 while x group < 2^32; 0 for 1
   int64_t lq, lk, rows;  // rows = lq * group
   int64_t qs[3], ks[3], vs[3];
   const void* q;
@@ -402,13 +298,99 @@ __device__ __forceinline__ int64_t live_rows(const Shape& S, int b) {
   return (n < 0 ? 0 : (n > S.lq ? S.lq : n)) * S.group;
 }
 
-// Column term of key j in log2 units: -inf for a masked key.
-__device__ __forceinline__ float column_term(const float* bias, int64_t j, int64_t count) {
+// Rows of the packed (query, head) side: byte offset of row r of a tile that
+// starts at head `rem` of its first query.
+__device__ __forceinline__ uint32_t packed_row(const Shape& S, int r, int rem, uint32_t row_bytes, uint32_t head_bytes) {
+  const uint32_t x = (uint32_t)(r + rem);
+  if (S.group == 1) return x * row_bytes;
+  const uint32_t i = __umulhi(x, S.group_mul);
+  return i * row_bytes + (x - i * (uint32_t)S.group) * head_bytes;
+}
+
+// Column term of key j: its bias times `unit`, -inf for a masked key.
+__device__ __forceinline__ float column_term(const float* bias, int64_t j, int64_t count, float unit) {
   if (j >= count) return -kInf;
   if (!bias) return 0.0f;
   const float x = bias[j];
-  return x <= kMasked ? -kInf : x * (float)kLog2e;
+  return x <= kMasked ? -kInf : x * unit;
 }
+
+// Tiles of RT packed rows of q (or dout), by loads to LDS. Where the group
+// divides RT a lane's offsets are the same in every tile.
+template <class T, int DP, int RT, int NT>
+struct RowTiles {
+  Loader<T, DP, RT, NT> ld;
+  const T* base;
+  int64_t row_stride;
+  uint32_t row_bytes, head_bytes;
+  int d;
+
+  __device__ __forceinline__ RowTiles(const Shape& S, const void* p, const int64_t* s, int b, int hk, int d_, int wave,
+                                      int lane)
+      : base((const T*)p + b * s[0] + (int64_t)hk * S.group * s[2]), row_stride(s[1]),
+        row_bytes((uint32_t)(s[1] * sizeof(T))), head_bytes((uint32_t)(s[2] * sizeof(T))), d(d_) {
+    ld.place([&](int r) { return packed_row(S, r, 0, row_bytes, head_bytes); }, d, wave, lane);
+  }
+  __device__ __forceinline__ void start(const Shape& S, int64_t t, int64_t nrows, char* tile, int wave, int lane) {
+    const int64_t first = t * RT, qi = first / S.group;
+    const int rem = (int)(first - qi * S.group);
+    if (RT % S.group != 0)
+      ld.place([&](int r) { return packed_row(S, r, rem, row_bytes, head_bytes); }, d, wave, lane);
+    const int64_t left = nrows - first;
+    if (left >= RT)
+      ld.start(base + qi * row_stride, tile, [](int) { return true; }, wave, lane);
+    else
+      ld.start(base + qi * row_stride, tile, [&](int r) { return r < left; }, wave, lane);
+  }
+};
+
+// Tiles of KT keys: k and v in buffer (n & 1) of `sm` (k, then v), their column
+// terms in sterm[n & 1]; tile t is the n-th of the workgroup. Biases of tile n
+// are loaded to sraw[n % 3] during tile n - 2; during tile n - 1 they decide
+// which rows are loaded and become the column terms.
+template <class T, int DP, int KT, int NT>
+struct KeyTiles {
+  Loader<T, DP, KT, NT> lk, lv;
+  static constexpr int kTileBytes = KT * Tile<T, DP>::RB;
+
+  __device__ __forceinline__ KeyTiles(const Shape& S, int wave, int lane) {
+    const uint32_t kp = (uint32_t)(S.ks[1] * sizeof(T)), vp = (uint32_t)(S.vs[1] * sizeof(T));
+    lk.place([&](int r) { return r * kp; }, S.d, wave, lane);
+    lv.place([&](int r) { return r * vp; }, S.dv, wave, lane);
+  }
+  __device__ __forceinline__ void fetch(const float* bias, int64_t t, int64_t n, int64_t nkeys, float (*sraw)[KT],
+                                        int wave, int lane) const {
+    if (!bias || wave * 64 >= KT) return;
+    const int j = wave * 64 + lane;
+    dma_load<4>(dma_rsrc(bias + t * KT), lds_offset(sraw[n % 3]) + wave * 256,
+                j < KT && t * KT + j < nkeys ? 4 * j : kOutside);
+  }
+  __device__ __forceinline__ void start(const Shape& S, const T* kbase, const T* vbase, const float* bias, int64_t t,
+                                        int64_t n, int64_t nkeys, char* sm, float (*sterm)[KT], float (*sraw)[KT],
+                                        float unit, int wave, int lane) const {
+    const int buf = (int)n & 1, tid = wave * 64 + lane;
+    const float* raw = sraw[n % 3];
+    const int64_t left = nkeys - t * KT;  // live keys from the tile's first on
+    if (tid < KT) {
+      float term = 0.0f;
+      if (bias) {
+        const float x = raw[tid];
+        term = x <= kMasked ? -kInf : x * unit;
+      }
+      sterm[buf][tid] = tid < left ? term : -kInf;
+    }
+    auto both = [&](auto&& live) {
+      lk.start(kbase + t * KT * S.ks[1], sm + buf * 2 * kTileBytes, live, wave, lane);
+      lv.start(vbase + t * KT * S.vs[1], sm + buf * 2 * kTileBytes + kTileBytes, live, wave, lane);
+    };
+    if (bias)
+      both([&](int r) { return r < left && !(raw[r] <= kMasked); });
+    else if (left < KT)
+      both([&](int r) { return r < left; });
+    else
+      both([](int) { return true; });
+  }
+};
 
 // Workgroup index -> work item, such that each XCD (workgroups go to the 8
 // XCDs in turn) takes one contiguous run of items and neighbouring items,

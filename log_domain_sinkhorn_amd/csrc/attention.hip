@@ -1,7 +1,7 @@
 // C ABI of the attention operators: argument checks, launch plans and
 // workspaces. The kernels are in attend.h (forward), attend_grad.h (backward)
 // and attend_mass.h (gathered weight), instantiated per element type.
-#include <initializer_list>
+#include <algorithm>
 
 #include "attend.h"
 #include "attend_grad.h"
@@ -13,12 +13,12 @@ namespace attn {
 extern template void attend<__bf16>(const AttendArgs&, bool, hipStream_t);
 extern template void attend<_Float16>(const AttendArgs&, bool, hipStream_t);
 extern template void attend<float>(const AttendArgs&, bool, hipStream_t);
-extern template void attend_grad<__bf16>(const GradArgs&, bool, hipStream_t);
-extern template void attend_grad<_Float16>(const GradArgs&, bool, hipStream_t);
-extern template void attend_grad<float>(const GradArgs&, bool, hipStream_t);
-extern template void attend_mass<__bf16>(const MassArgs&, bool, hipStream_t);
-extern template void attend_mass<_Float16>(const MassArgs&, bool, hipStream_t);
-extern template void attend_mass<float>(const MassArgs&, bool, hipStream_t);
+extern template void attend_grad<__bf16>(const GradArgs&, hipStream_t);
+extern template void attend_grad<_Float16>(const GradArgs&, hipStream_t);
+extern template void attend_grad<float>(const GradArgs&, hipStream_t);
+extern template void attend_mass<__bf16>(const MassArgs&, hipStream_t);
+extern template void attend_mass<_Float16>(const MassArgs&, hipStream_t);
+extern template void attend_mass<float>(const MassArgs&, hipStream_t);
 
 namespace {
 
@@ -40,16 +40,31 @@ void require(bool ok, const char* what) {
   if (!ok) fail(SINKHORN_ERR_INVALID_ARG, what);
 }
 
-constexpr int64_t kFill = 512;  // workgroups that fill the chip: two for each of the 256 compute units
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Splits of the streamed side (`steps` tiles of it) for `blocks` workgroups:
-// one when they fill the chip by themselves.
-int32_t splits(int64_t blocks, int64_t steps) {
-  if (blocks <= 0 || blocks * 2 > kFill || steps <= 1) return 1;
-  const int64_t want = ceil_div(kFill, blocks);
-  return (int32_t)(want < steps ? want : steps);
+// Splits of the streamed side, `steps` tiles of it, for `blocks` workgroups of
+// which `slots` run at a time: the number with the least time in units of one
+// step, counting rounds of workgroups, two steps to begin and end each, and the
+// join (`join` steps and a little per split). `fine`: at least four rounds, so
+// that sequences of different lengths even out.
+int32_t splits(int64_t blocks, int64_t steps, int64_t slots, double join, bool fine) {
+  if (blocks <= 0 || steps <= 1 || blocks >= 4 * slots) return 1;
+  const int64_t most = std::min<int64_t>(steps, 512);
+  int32_t best = 1;
+  double least = 0.0;
+  for (int64_t n = 1; n <= most; ++n) {
+    const double rounds = (double)ceil_div(blocks * n, slots);
+    const double cost = rounds * (double)(ceil_div(steps, n) + 2) + (n > 1 ? join + 0.02 * (double)n : 0.0);
+    if (n == 1 || cost < least) {
+      least = cost;
+      best = (int32_t)n;
+    }
+  }
+  if (fine && best > 1) {
+    const int64_t n = std::min<int64_t>(ceil_div(4 * slots, blocks), std::max<int64_t>(1, steps / 8));
+    if (n > best) best = (int32_t)n;
+  }
+  return best;
 }
 
 int64_t elem_size(const sinkhorn_attention* a) { return a->dtype == SINKHORN_F32 ? 4 : 2; }
@@ -60,6 +75,7 @@ void check(const sinkhorn_attention* a) {
   require(a->batch >= 0 && a->len_q >= 0 && a->len_k >= 0, "negative size");
   require(a->heads_q >= 1 && a->heads_kv >= 1 && a->heads_q % a->heads_kv == 0,
           "heads_q must be a multiple of heads_kv");
+  if (a->heads_q > 8192) fail(SINKHORN_ERR_UNSUPPORTED, "more than 8192 heads");
   require(a->d >= 1 && a->dv >= 1, "head widths must be >= 1");
   if (a->d > kMaxD || a->dv > kMaxD) fail(SINKHORN_ERR_UNSUPPORTED, "head widths above 128");
   require(a->len_q * (a->heads_q / a->heads_kv) < (int64_t(1) << 31) && a->len_q < (int64_t(1) << 31) &&
@@ -75,26 +91,7 @@ void check(const sinkhorn_attention* a) {
   require(a->bias_stride[0] >= 0 && a->bias_stride[1] >= 0, "negative stride");
 }
 
-struct Operand {
-  const void* p;
-  const int64_t* stride;
-  int64_t width;
-};
-
-// Bytes a lane may load to LDS at once from the rows of `ops`: 16, 4, or 2 for
-// a row that is not a multiple of four bytes (loaded through registers), as for
-// row strides of 2^23 bytes and more, with which a tile could span 2^31 bytes.
-int32_t load_unit(std::initializer_list<Operand> ops, int64_t size) {
-  bool by16 = true, by4 = true;
-  for (const Operand& o : ops) {
-    if (o.stride[1] * size >= (int64_t(1) << 23)) return 2;
-    by16 = by16 && rows_aligned(o.p, o.stride, o.width, size, 16);
-    by4 = by4 && rows_aligned(o.p, o.stride, o.width, size, 4);
-  }
-  return by16 ? 16 : (by4 ? 4 : 2);
-}
-
-Shape make_shape(const sinkhorn_attention* a, const void* q, const void* k, const void* v) {
+Shape make_shape(const sinkhorn_attention* a) {
   Shape S{};
   S.batch = a->batch;
   S.hq = a->heads_q;
@@ -105,14 +102,12 @@ Shape make_shape(const sinkhorn_attention* a, const void* q, const void* k, cons
   S.lq = a->len_q;
   S.lk = a->len_k;
   S.rows = a->len_q * S.group;
+  S.group_mul = S.group > 1 ? (uint32_t)(((uint64_t(1) << 32) + S.group - 1) / S.group) : 0;
   for (int i = 0; i < 3; ++i) {
     S.qs[i] = a->q_stride[i];
     S.ks[i] = a->k_stride[i];
     S.vs[i] = a->v_stride[i];
   }
-  S.q = q;
-  S.k = k;
-  S.v = v;
   S.bias = a->key_bias;
   S.bs[0] = a->bias_stride[0];
   S.bs[1] = a->bias_stride[1];
@@ -129,89 +124,212 @@ void copy3(int64_t* dst, const int64_t* src) {
 }
 
 // ---------------------------------------------------------------- plans
+// Workspace layout: consecutive pieces of 256-byte multiples.
+struct Space {
+  int64_t bytes = 0;
+  int64_t take(int64_t n) {
+    const int64_t at = bytes;
+    bytes += ceil_div(n, 256) * 256;
+    return at;
+  }
+};
+
+// An operand that the kernels can not load 16 bytes a lane from is first
+// copied: rows at other addresses or of other widths, and strides with which a
+// tile could span 2^31 bytes. A copy is [batch][length][heads][width] with the
+// width rounded up to 16 bytes and zero behind d.
+struct Operand {
+  const void* p = nullptr;
+  int64_t stride[3] = {0, 0, 0};
+  int64_t len = 0;
+  int32_t heads = 0, d = 0, dp = 0;
+  bool copy = false;
+  int64_t at = 0;  // place of the copy in the workspace
+};
+
+Operand operand(const sinkhorn_attention* a, const void* p, const int64_t* stride, int64_t len, int32_t heads, int32_t d,
+                Space& ws) {
+  const int64_t size = elem_size(a);
+  Operand o;
+  o.p = p;
+  for (int i = 0; i < 3; ++i) o.stride[i] = stride[i];
+  o.len = len;
+  o.heads = heads;
+  o.d = d;
+  o.dp = (int32_t)(ceil_div(d * size, 16) * 16 / size);
+  o.copy = !rows_aligned(p, stride, d, size, 16) || stride[1] * size >= (int64_t(1) << 23) ||
+           stride[2] * size * heads >= (int64_t(1) << 30);
+  // keys of one head: its stride only moves the base
+  if (stride[1] * size < (int64_t(1) << 23) && rows_aligned(p, stride, d, size, 16) && heads == a->heads_kv &&
+      len == a->len_k)
+    o.copy = false;
+  if (o.copy) o.at = ws.take(size * a->batch * len * heads * o.dp);
+  return o;
+}
+
 struct AttendPlan {
-  bool many;       // 128 rows per workgroup (else all rows in tiles of 32)
-  bool partial;    // through partial results and k_join
-  bool scores;     // the scores are kept for the gathered weight
+  bool many;     // 128 rows per workgroup (else all rows in tiles of 32)
+  bool partial;  // through partial results and k_join
+  bool scores;   // the scores are kept for the gathered weight
   int32_t nsplit;
   int64_t tiles;
   int64_t score_ld;
-  int64_t ml_off, score_off, bytes;
+  Operand q, k, v;
+  int64_t o_off, ml_off, score_off, mass_off;
+  int32_t mass_split;
+  int64_t mass_tiles;
+  int64_t bytes;
 };
-
-AttendPlan plan_attend(const sinkhorn_attention* a, bool mass) {
-  AttendPlan p{};
-  const int64_t pairs = (int64_t)a->batch * a->heads_kv;
-  const int64_t rows = a->len_q * (a->heads_q / a->heads_kv);
-  p.many = rows > 32;
-  p.tiles = ceil_div(rows, p.many ? 128 : 32);
-  p.nsplit = splits(pairs * p.tiles, ceil_div(a->len_k, p.many || a->dtype == SINKHORN_F32 ? 64 : 128));
-  p.partial = p.nsplit > 1;
-  p.scores = mass && !p.many;
-  const int64_t dvp = ceil_div(a->dv, 4) * 4;
-  int64_t off = 0;
-  auto take = [&](int64_t bytes) {
-    const int64_t at = off;
-    off += ceil_div(bytes, 256) * 256;
-    return at;
-  };
-  if (p.partial) {
-    take(4 * p.nsplit * pairs * rows * dvp);
-    p.ml_off = take(8 * p.nsplit * pairs * rows);
-  }
-  if (p.scores) {
-    p.score_ld = ceil_div(a->len_k, 128) * 128;
-    p.score_off = take(4 * pairs * rows * p.score_ld);
-  }
-  p.bytes = off;
-  return p;
-}
-
-struct GradPlan {
-  int64_t tiles_q, tiles_kv;
-  int32_t split_q, split_kv;
-  int64_t pq_off, pk_off, pv_off, bytes;
-};
-
-GradPlan plan_grad(const sinkhorn_attention* a) {
-  GradPlan p{};
-  const int64_t pairs = (int64_t)a->batch * a->heads_kv;
-  const int64_t rows = a->len_q * (a->heads_q / a->heads_kv);
-  p.tiles_q = ceil_div(rows, 128);
-  p.tiles_kv = ceil_div(a->len_k, 128);
-  p.split_q = splits(pairs * p.tiles_q, ceil_div(a->len_k, 64));
-  p.split_kv = splits(pairs * p.tiles_kv, ceil_div(rows, 64));
-  const int64_t dp = ceil_div(a->d, 4) * 4, dvp = ceil_div(a->dv, 4) * 4;
-  int64_t off = 0;
-  auto take = [&](int64_t bytes) {
-    const int64_t at = off;
-    off += ceil_div(bytes, 256) * 256;
-    return at;
-  };
-  take(8 * pairs * rows);
-  if (p.split_q > 1) p.pq_off = take(4 * p.split_q * pairs * rows * dp);
-  if (p.split_kv > 1) {
-    p.pk_off = take(4 * p.split_kv * pairs * a->len_k * dp);
-    p.pv_off = take(4 * p.split_kv * pairs * a->len_k * dvp);
-  }
-  p.bytes = off;
-  return p;
-}
 
 struct MassPlan {
   int64_t tiles;
   int32_t nsplit;
-  int64_t bytes;
 };
 
-MassPlan plan_mass(const sinkhorn_attention* a) {
+bool wide(const sinkhorn_attention* a) { return a->d > 64 || a->dv > 64; }
+// steps of the streamed side that a join costs
+double join_steps(const sinkhorn_attention* a) { return a->dtype == SINKHORN_F32 ? 1.0 : 3.0; }
+
+MassPlan split_mass(const sinkhorn_attention* a) {
   MassPlan p{};
   const int64_t pairs = (int64_t)a->batch * a->heads_kv;
   const int64_t rows = a->len_q * (a->heads_q / a->heads_kv);
   p.tiles = ceil_div(a->len_k, 128);
-  p.nsplit = splits(pairs * p.tiles, ceil_div(rows, 64));
-  p.bytes = p.nsplit > 1 ? 4 * p.nsplit * pairs * a->len_k : 0;
+  p.nsplit = splits(pairs * p.tiles, ceil_div(rows, 64), 768, join_steps(a), false);
   return p;
+}
+
+AttendPlan plan_attend(const sinkhorn_attention* a, const void* q, const void* k, const void* v, bool mass) {
+  AttendPlan p{};
+  Space ws;
+  const bool f32 = a->dtype == SINKHORN_F32;
+  const int64_t pairs = (int64_t)a->batch * a->heads_kv;
+  const int64_t rows = a->len_q * (a->heads_q / a->heads_kv);
+  p.many = rows > 32;
+  p.tiles = ceil_div(rows, p.many ? 128 : 32);
+  const int64_t steps = ceil_div(a->len_k, p.many || f32 ? 64 : 128);
+  const int64_t slots = p.many ? (f32 && wide(a) ? 256 : 512) : (wide(a) ? 256 : 512);
+  p.nsplit = splits(pairs * p.tiles, steps, slots, join_steps(a), !p.many);
+  p.partial = p.nsplit > 1;
+  p.scores = mass && !p.many;
+  p.q = operand(a, q, a->q_stride, a->len_q, a->heads_q, a->d, ws);
+  p.k = operand(a, k, a->k_stride, a->len_k, a->heads_kv, a->d, ws);
+  p.v = operand(a, v, a->v_stride, a->len_k, a->heads_kv, a->dv, ws);
+  const int64_t after_copies = ws.bytes;
+  if (p.partial) {
+    p.o_off = ws.take(4 * p.nsplit * pairs * rows * ceil_div(a->dv, 4) * 4);
+    p.ml_off = ws.take(8 * p.nsplit * pairs * rows);
+  }
+  if (p.scores) {
+    p.score_ld = ceil_div(a->len_k, 128) * 128;
+    p.score_off = ws.take(4 * pairs * rows * p.score_ld);
+  } else if (mass) {
+    // the forward pass is done with its partial results by then
+    const MassPlan m = split_mass(a);
+    p.mass_split = m.nsplit;
+    p.mass_tiles = m.tiles;
+    if (m.nsplit > 1) {
+      Space two;
+      two.bytes = after_copies;
+      p.mass_off = two.take(4 * m.nsplit * pairs * a->len_k);
+      ws.bytes = std::max(ws.bytes, two.bytes);
+    }
+  }
+  p.bytes = ws.bytes;
+  return p;
+}
+
+struct GradPlan {
+  int64_t tiles_q, tiles_kv, rows_pad;
+  int32_t split_q, split_kv;
+  Operand q, k, v, dout;
+  int64_t stat_off, pq_off, pk_off, pv_off, bytes;
+};
+
+GradPlan plan_grad(const sinkhorn_attention* a, const void* q, const void* k, const void* v, const void* dout) {
+  GradPlan p{};
+  Space ws;
+  const bool f32 = a->dtype == SINKHORN_F32;
+  const int64_t pairs = (int64_t)a->batch * a->heads_kv;
+  const int64_t rows = a->len_q * (a->heads_q / a->heads_kv);
+  const int64_t step = f32 && wide(a) ? 32 : 64;
+  p.tiles_q = ceil_div(rows, 128);
+  p.tiles_kv = ceil_div(a->len_k, 128);
+  p.rows_pad = ceil_div(rows, 64) * 64;
+  p.split_q = splits(pairs * p.tiles_q, ceil_div(a->len_k, step), f32 && wide(a) ? 256 : 512, join_steps(a), false);
+  p.split_kv = splits(pairs * p.tiles_kv, ceil_div(rows, step), f32 || wide(a) ? 256 : 512, 2 * join_steps(a), false);
+  p.q = operand(a, q, a->q_stride, a->len_q, a->heads_q, a->d, ws);
+  p.k = operand(a, k, a->k_stride, a->len_k, a->heads_kv, a->d, ws);
+  p.v = operand(a, v, a->v_stride, a->len_k, a->heads_kv, a->dv, ws);
+  p.dout = operand(a, dout, a->dout_stride, a->len_q, a->heads_q, a->dv, ws);
+  const int64_t dp = ceil_div(a->d, 4) * 4, dvp = ceil_div(a->dv, 4) * 4;
+  p.stat_off = ws.take(8 * pairs * p.rows_pad);
+  if (p.split_q > 1) p.pq_off = ws.take(4 * p.split_q * pairs * rows * dp);
+  if (p.split_kv > 1) {
+    p.pk_off = ws.take(4 * p.split_kv * pairs * a->len_k * dp);
+    p.pv_off = ws.take(4 * p.split_kv * pairs * a->len_k * dvp);
+  }
+  p.bytes = ws.bytes;
+  return p;
+}
+
+struct WeightPlan {
+  MassPlan m;
+  Operand q, k;
+  int64_t part_off, bytes;
+};
+
+WeightPlan plan_mass(const sinkhorn_attention* a, const void* q, const void* k) {
+  WeightPlan p{};
+  Space ws;
+  p.m = split_mass(a);
+  p.q = operand(a, q, a->q_stride, a->len_q, a->heads_q, a->d, ws);
+  p.k = operand(a, k, a->k_stride, a->len_k, a->heads_kv, a->d, ws);
+  if (p.m.nsplit > 1) p.part_off = ws.take(4 * p.m.nsplit * (int64_t)a->batch * a->heads_kv * a->len_k);
+  p.bytes = ws.bytes;
+  return p;
+}
+
+// ---------------------------------------------------------------- copies
+// One 16-byte chunk of a copy per thread.
+template <class U>
+__global__ __launch_bounds__(256) void k_copy_rows(const U* src, int64_t s0, int64_t s1, int64_t s2, int64_t len,
+                                                   int32_t heads, int32_t d, int32_t chunks, int64_t total, u32x4* dst) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  constexpr int EPC = 16 / (int)sizeof(U);
+  const int64_t row = i / chunks;
+  const int c = (int)(i - row * chunks) * EPC;
+  const int64_t bl = row / heads, b = bl / len;
+  const U* p = src + b * s0 + (bl - b * len) * s1 + (row - bl * heads) * s2;
+  union {
+    U e[EPC];
+    u32x4 u;
+  } x;
+#pragma unroll
+  for (int e = 0; e < EPC; ++e) x.e[e] = c + e < d ? p[c + e] : (U)0;
+  dst[i] = x.u;
+}
+
+// The operand as the kernels read it: its address and strides, after the copy
+// if it needs one.
+const void* place(const sinkhorn_attention* a, const Operand& o, char* ws, int64_t* stride, hipStream_t st) {
+  for (int i = 0; i < 3; ++i) stride[i] = o.stride[i];
+  if (!o.copy || o.len == 0) return o.p;
+  const int64_t size = elem_size(a);
+  const int32_t chunks = (int32_t)(o.dp * size / 16);
+  const int64_t total = a->batch * o.len * o.heads * chunks;
+  if (size == 4)
+    hipLaunchKernelGGL((k_copy_rows<uint32_t>), grid1(ceil_div(total, 256), 256), dim3(256), 0, st, (const uint32_t*)o.p,
+                       o.stride[0], o.stride[1], o.stride[2], o.len, o.heads, o.d, chunks, total, (u32x4*)(ws + o.at));
+  else
+    hipLaunchKernelGGL((k_copy_rows<uint16_t>), grid1(ceil_div(total, 256), 256), dim3(256), 0, st, (const uint16_t*)o.p,
+                       o.stride[0], o.stride[1], o.stride[2], o.len, o.heads, o.d, chunks, total, (u32x4*)(ws + o.at));
+  SK_LAUNCH_CHECK();
+  stride[0] = o.len * o.heads * o.dp;
+  stride[1] = (int64_t)o.heads * o.dp;
+  stride[2] = o.dp;
+  return ws + o.at;
 }
 
 void check_workspace(const void* ws, int64_t have, int64_t need) {
@@ -263,14 +381,12 @@ __global__ __launch_bounds__(256) void k_mass_scores(MassArgs A) {
 }
 
 void run_mass(const sinkhorn_attention* a, MassArgs& A, hipStream_t st) {
-  const int64_t size = elem_size(a);
-  const bool al = rows_aligned(A.S.q, a->q_stride, a->d, size, 16) && rows_aligned(A.S.k, a->k_stride, a->d, size, 16);
   if (a->dtype == SINKHORN_BF16)
-    attend_mass<__bf16>(A, al, st);
+    attend_mass<__bf16>(A, st);
   else if (a->dtype == SINKHORN_F16)
-    attend_mass<_Float16>(A, al, st);
+    attend_mass<_Float16>(A, st);
   else
-    attend_mass<float>(A, al, st);
+    attend_mass<float>(A, st);
   if (A.part) {
     hipLaunchKernelGGL(k_mass_join, grid1(ceil_div((int64_t)A.S.batch * A.S.hkv * A.S.lk, 256), 256), dim3(256), 0, st,
                        A);
@@ -287,19 +403,16 @@ using namespace sk::attn;
 
 extern "C" {
 
-int sinkhorn_attention_workspace(const sinkhorn_attention* a, int32_t what, int64_t* bytes) {
+int sinkhorn_attention_workspace(const sinkhorn_attention* a, int32_t what, const void* q, const void* k, const void* v,
+                                 const void* dout, int64_t* bytes) {
   return guarded([&] {
     check(a);
     require(bytes != nullptr, "null pointer");
     switch (what) {
-      case SINKHORN_ATTEND: *bytes = plan_attend(a, false).bytes; break;
-      case SINKHORN_ATTEND_MASS: {
-        const int64_t x = plan_attend(a, true).bytes, y = plan_mass(a).bytes;
-        *bytes = x > y ? x : y;
-        break;
-      }
-      case SINKHORN_ATTEND_GRAD: *bytes = plan_grad(a).bytes; break;
-      case SINKHORN_ATTENTION_MASS: *bytes = plan_mass(a).bytes; break;
+      case SINKHORN_ATTEND: *bytes = plan_attend(a, q, k, v, false).bytes; break;
+      case SINKHORN_ATTEND_MASS: *bytes = plan_attend(a, q, k, v, true).bytes; break;
+      case SINKHORN_ATTEND_GRAD: *bytes = plan_grad(a, q, k, v, dout).bytes; break;
+      case SINKHORN_ATTENTION_MASS: *bytes = plan_mass(a, q, k).bytes; break;
       default: fail(SINKHORN_ERR_INVALID_ARG, "unknown workspace kind");
     }
     return SINKHORN_OK;
@@ -319,24 +432,26 @@ int sinkhorn_cross_attention(const sinkhorn_attention* a, const void* q, const v
             "mass_in and row_weight need mass_out");
     require(out == nullptr || (out != q && out != k && out != v), "output aliases an input");
     const bool mass = mass_out != nullptr && keys;
-    const AttendPlan p = plan_attend(a, mass);
-    const MassPlan mp = mass ? plan_mass(a) : MassPlan{};
-    const int64_t need = mass && mp.bytes > p.bytes ? mp.bytes : p.bytes;
-    check_workspace(workspace, workspace_bytes, need);
+    const AttendPlan p = plan_attend(a, q, k, v, mass);
+    check_workspace(workspace, workspace_bytes, p.bytes);
     const hipStream_t st = (hipStream_t)stream;
-    const int64_t size = elem_size(a);
     char* ws = (char*)workspace;
     AttendArgs A{};
-    A.S = make_shape(a, q, k, v);
+    A.S = make_shape(a);
+    if (rows) {
+      A.S.q = place(a, p.q, ws, A.S.qs, st);
+      A.S.k = place(a, p.k, ws, A.S.ks, st);
+      A.S.v = place(a, p.v, ws, A.S.vs, st);
+    }
     copy3(A.os, a->out_stride);
     A.out = out;
     A.lse = lse;
     A.dvp = (int32_t)(ceil_div(a->dv, 4) * 4);
     A.nsplit = p.nsplit;
     A.tiles = p.tiles;
-    A.vec = rows_aligned(out, a->out_stride, a->dv, size, 4 * size);
+    A.vec = rows_aligned(out, a->out_stride, a->dv, elem_size(a), 4 * elem_size(a));
     if (p.partial) {
-      A.opart = (float*)ws;
+      A.opart = (float*)(ws + p.o_off);
       A.mlpart = (f32x2*)(ws + p.ml_off);
     }
     if (p.scores) {
@@ -344,7 +459,6 @@ int sinkhorn_cross_attention(const sinkhorn_attention* a, const void* q, const v
       A.score_ld = p.score_ld;
     }
     if (rows) {
-      A.unit = load_unit({{q, a->q_stride, a->d}, {k, a->k_stride, a->d}, {v, a->v_stride, a->dv}}, size);
       if (a->dtype == SINKHORN_BF16)
         attend<__bf16>(A, p.many, st);
       else if (a->dtype == SINKHORN_F16)
@@ -367,10 +481,9 @@ int sinkhorn_cross_attention(const sinkhorn_attention* a, const void* q, const v
                            dim3(256), 0, st, M);
         SK_LAUNCH_CHECK();
       } else {
-        // the forward pass is done with the workspace by then
-        M.tiles = mp.tiles;
-        M.nsplit = mp.nsplit;
-        M.part = mp.nsplit > 1 ? (float*)ws : nullptr;
+        M.tiles = p.mass_tiles;
+        M.nsplit = p.mass_split;
+        M.part = p.mass_split > 1 ? (float*)(ws + p.mass_off) : nullptr;
         run_mass(a, M, st);
       }
     }
@@ -391,24 +504,33 @@ int sinkhorn_cross_attention_grad(const sinkhorn_attention* a, const void* q, co
     for (void* o : {dq, dk, dv})
       require(o == nullptr || (o != q && o != k && o != v && o != out && o != dout), "output aliases an input");
     require((!keys || dk != dv) && (!(rows && keys) || (dq != dk && dq != dv)), "outputs alias each other");
-    const GradPlan p = plan_grad(a);
+    const GradPlan p = plan_grad(a, q, k, v, dout);
     check_workspace(workspace, workspace_bytes, p.bytes);
+    const hipStream_t st = (hipStream_t)stream;
     const int64_t size = elem_size(a);
     char* ws = (char*)workspace;
     GradArgs A{};
-    A.S = make_shape(a, q, k, v);
+    A.S = make_shape(a);
     copy3(A.os, a->out_stride);
     copy3(A.dos, a->dout_stride);
+    if (rows && keys) {
+      A.S.q = place(a, p.q, ws, A.S.qs, st);
+      A.S.k = place(a, p.k, ws, A.S.ks, st);
+      A.S.v = place(a, p.v, ws, A.S.vs, st);
+      A.dout = place(a, p.dout, ws, A.dos, st);
+    } else {
+      A.dout = dout;  // only its products with out, which is 0
+    }
     copy3(A.dqs, a->dq_stride);
     copy3(A.dks, a->dk_stride);
     copy3(A.dvs, a->dv_stride);
     A.out = out;
-    A.dout = dout;
     A.lse = lse;
     A.dq = dq;
     A.dk = dk;
     A.dv = dv;
-    A.stat = (f32x2*)ws;
+    A.stat = (f32x2*)(ws + p.stat_off);
+    A.rows_pad = p.rows_pad;
     A.dp = (int32_t)(ceil_div(a->d, 4) * 4);
     A.dvp = (int32_t)(ceil_div(a->dv, 4) * 4);
     A.split_q = p.split_q;
@@ -423,16 +545,13 @@ int sinkhorn_cross_attention_grad(const sinkhorn_attention* a, const void* q, co
     A.vec_q = rows_aligned(dq, a->dq_stride, a->d, size, 4 * size);
     A.vec_k = rows_aligned(dk, a->dk_stride, a->d, size, 4 * size);
     A.vec_v = rows_aligned(dv, a->dv_stride, a->dv, size, 4 * size);
-    const bool al = rows_aligned(q, a->q_stride, a->d, size, 16) && rows_aligned(k, a->k_stride, a->d, size, 16) &&
-                    rows_aligned(v, a->v_stride, a->dv, size, 16) &&
-                    rows_aligned(dout, a->dout_stride, a->dv, size, 16);
-    const hipStream_t st = (hipStream_t)stream;
+    A.stat_vec = rows_aligned(out, A.os, a->dv, size, 16) && rows_aligned(A.dout, A.dos, a->dv, size, 16);
     if (a->dtype == SINKHORN_BF16)
-      attend_grad<__bf16>(A, al, st);
+      attend_grad<__bf16>(A, st);
     else if (a->dtype == SINKHORN_F16)
-      attend_grad<_Float16>(A, al, st);
+      attend_grad<_Float16>(A, st);
     else
-      attend_grad<float>(A, al, st);
+      attend_grad<float>(A, st);
     return SINKHORN_OK;
   });
 }
@@ -445,18 +564,24 @@ int sinkhorn_attention_mass(const sinkhorn_attention* a, const void* q, const vo
     if (a->batch == 0 || a->len_k == 0) return SINKHORN_OK;
     require(mass_out != nullptr, "null pointer");
     require(a->len_q == 0 || (q && k && lse), "null pointer");
-    const MassPlan p = plan_mass(a);
+    const WeightPlan p = plan_mass(a, q, k);
     check_workspace(workspace, workspace_bytes, p.bytes);
+    const hipStream_t st = (hipStream_t)stream;
+    char* ws = (char*)workspace;
     MassArgs M{};
-    M.S = make_shape(a, q, k, nullptr);
+    M.S = make_shape(a);
+    if (a->len_q > 0) {
+      M.S.q = place(a, p.q, ws, M.S.qs, st);
+      M.S.k = place(a, p.k, ws, M.S.ks, st);
+    }
     M.lse = lse;
     M.weight = row_weight;
     M.mass_in = mass_in;
     M.mass_out = mass_out;
-    M.tiles = p.tiles;
-    M.nsplit = p.nsplit;
-    M.part = p.nsplit > 1 ? (float*)workspace : nullptr;
-    run_mass(a, M, (hipStream_t)stream);
+    M.tiles = p.m.tiles;
+    M.nsplit = p.m.nsplit;
+    M.part = p.m.nsplit > 1 ? (float*)(ws + p.part_off) : nullptr;
+    run_mass(a, M, st);
     return SINKHORN_OK;
   });
 }

@@ -114,12 +114,13 @@ def test_descriptions_are_refused(kw, word):
     a = _desc(**kw)
     assert _forward(a) == sk.ERR_INVALID_ARG
     assert word in sk.lib().sinkhorn_last_error()
-    assert sk.lib().sinkhorn_attention_workspace(ctypes.byref(a), 0, ctypes.byref(n)) == sk.ERR_INVALID_ARG
+    assert sk.lib().sinkhorn_attention_workspace(ctypes.byref(a), 0, None, None, None, None, ctypes.byref(n)) == sk.ERR_INVALID_ARG
 
 
 def test_wide_heads_are_unsupported():
     assert _forward(_desc(d=129)) == sk.ERR_UNSUPPORTED
     assert _forward(_desc(dv=256)) == sk.ERR_UNSUPPORTED
+    assert _forward(_desc(heads_q=16384, heads_kv=8192)) == sk.ERR_UNSUPPORTED
 
 
 def test_null_pointers_aliases_and_workspaces():
@@ -131,11 +132,14 @@ def test_null_pointers_aliases_and_workspaces():
         assert _forward(a, **kw) == sk.ERR_INVALID_ARG, kw
     need = ctypes.c_int64()
     for what in range(4):
-        assert L.sinkhorn_attention_workspace(ctypes.byref(a), what, ctypes.byref(need)) == sk.OK
-    assert L.sinkhorn_attention_workspace(ctypes.byref(a), 4, ctypes.byref(need)) == sk.ERR_INVALID_ARG
-    assert L.sinkhorn_attention_workspace(ctypes.byref(a), 0, None) == sk.ERR_INVALID_ARG
-    assert L.sinkhorn_attention_workspace(ctypes.byref(a), 0, ctypes.byref(need)) == sk.OK
+        assert L.sinkhorn_attention_workspace(ctypes.byref(a), what, None, None, None, None, ctypes.byref(need)) == sk.OK
+    assert L.sinkhorn_attention_workspace(ctypes.byref(a), 4, None, None, None, None, ctypes.byref(need)) == sk.ERR_INVALID_ARG
+    assert L.sinkhorn_attention_workspace(ctypes.byref(a), 0, None, None, None, None, None) == sk.ERR_INVALID_ARG
+    assert L.sinkhorn_attention_workspace(ctypes.byref(a), 0, FAKE, FAKE, FAKE, None, ctypes.byref(need)) == sk.OK
     assert need.value > 0  # few rows against many keys: split
+    odd = ctypes.c_int64()
+    assert L.sinkhorn_attention_workspace(ctypes.byref(a), 0, FAKE, ctypes.c_void_p(258), FAKE, None, ctypes.byref(odd)) == sk.OK
+    assert odd.value == need.value + 2 * 2 * 1000 * 2 * 64  # a copy of k
     for ws, n in ((None, 0), (FAKE, need.value - 1), (ctypes.c_void_p(264), need.value)):
         assert _forward(a, ws=ws, n=n) == sk.ERR_INVALID_ARG
         assert b"workspace" in L.sinkhorn_last_error()

@@ -7,13 +7,15 @@
 // registers and one exchange with the lane 32 away; the weights feed
 // O^T = V^T P^T from their registers. WQ waves take different rows of the
 // same keys and WK waves different keys of the same rows (joined through LDS
-// at the end): 4 x 1 for many rows, 1 x WK when one tile of 32 rows holds them
+// at the end): 4 x 1 for many rows, 1 x 2 when one tile of 32 rows holds them
 // all. The keys are split over workgroups when rows and heads alone do not fill
 // the chip; k_join then joins the partial results.
 //
-// Tiles of keys lie in two LDS buffers, one filled by loads to LDS while the
-// other is computed on: one barrier per tile and no staging registers, which
-// leaves two waves a SIMD whose matrix and vector work overlap.
+// Tiles of keys lie in a ring of LDS buffers, filled by loads to LDS while an
+// earlier one is computed on: one barrier per tile and no staging registers,
+// which for many rows (two buffers) leaves two waves a SIMD whose matrix and
+// vector work overlap. With few rows memory is the bound: four buffers keep up
+// to 96 KB per compute unit in flight.
 #pragma once
 
 #include "attention.h"
@@ -36,14 +38,19 @@ struct AttendArgs {
   bool vec;        // out may be written four elements at a time
 };
 
-// Waves a SIMD that the LDS of tiles of `keys` keys of `row` bytes leaves room
-// for, with `waves` of them in a workgroup.
-constexpr int attend_waves(int keys, int row, int waves) {
-  return 4 * keys * row <= 72 * 1024 && waves >= 4 ? 2 : 1;
+// Few rows: waves of a workgroup, each with 32 keys of a tile, and tiles in LDS
+// for rows of `bytes` bytes: 144 KB, two thirds of it in flight.
+constexpr int few_waves(int64_t bytes) { return bytes <= 128 ? 6 : (bytes <= 256 ? 3 : 2); }
+constexpr int few_depth(int64_t bytes) { return bytes <= 256 ? 3 : 2; }
+
+// Waves a SIMD that LDS leaves room for: `depth` tiles of `keys` keys of `row`
+// bytes, `waves` waves in a workgroup.
+constexpr int attend_waves(int depth, int keys, int row, int waves) {
+  return waves / 4 * (2 * depth * keys * row <= 72 * 1024 ? 2 : 1) >= 2 ? 2 : 1;
 }
 
-template <class T, int DP, int WQ, int WK, int NB>
-__global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)sizeof(T), WQ * WK)) void k_attend(
+template <class T, int DP, int WQ, int WK, int NB, int D>
+__global__ __launch_bounds__(64 * WQ * WK, attend_waves(D, 32 * NB * WK, DP * (int)sizeof(T), WQ * WK)) void k_attend(
     AttendArgs A) {
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
@@ -55,10 +62,13 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)
   // makes it. 16-bit types: log2 units from the start, one operation less.
   constexpr bool kExact = sizeof(T) == 4;
   constexpr float kTerm = kExact ? 1.0f : (float)kLog2e;
-  constexpr int kTileBytes = KT * TL::RB;
-  static_assert(WK == 1 || WK * 32 * DP * 4 <= 4 * kTileBytes, "room to join the waves");
-  __shared__ __attribute__((aligned(16))) char sm[4 * kTileBytes];
-  __shared__ __attribute__((aligned(16))) float sterm[2][KT], sraw[3][KT];
+  using KeyT = KeyTiles<T, DP, KT, NT, D, (WK > 1)>;  // few rows: each key is read by one workgroup
+  constexpr int kJoinBytes = WK > 1 ? WK * 32 * DP * 4 : 0;
+  union Memory {
+    typename KeyT::Shared keys;
+    float join[kJoinBytes / 4 + 1];  // [WK][DP][32]
+  };
+  __shared__ Memory sm;
   __shared__ f32x2 sml[WK > 1 ? WK * 32 : 1];
 
   const Shape& S = A.S;
@@ -87,22 +97,8 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)
   const int64_t per = (ntiles + A.nsplit - 1) / A.nsplit;
   const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
 
-  const T* kbase = (const T*)S.k + b * S.ks[0] + hk * S.ks[2];
-  const T* vbase = (const T*)S.v + b * S.vs[0] + hk * S.vs[2];
-  const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
-
-  KeyTiles<T, DP, KT, NT> keys(S, wave, lane);
-  auto fetch = [&](int64_t t) { keys.fetch(bias, t, t - t0, nkeys, sraw, wave, lane); };
-  auto start = [&](int64_t t) { keys.start(S, kbase, vbase, bias, t, t - t0, nkeys, sm, sterm, sraw, kTerm, wave, lane); };
-  if (t0 < t1) {
-    if (bias) {
-      fetch(t0);
-      if (t0 + 1 < t1) fetch(t0 + 1);
-      dma_wait();
-      __syncthreads();
-    }
-    start(t0);
-  }
+  KeyT keys(sm.keys, S, b, hk, t0, t1, nkeys, kTerm, wave, lane);
+  keys.begin();
 
   V8 qf[NS];
   {
@@ -115,19 +111,11 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)
   for (int n = 0; n < NDB; ++n) o[n] = zero16();
   float m = -kInf, l = 0.0f;  // the row's reference (log2 units) and this lane's part of the sum
 
-  for (int64_t t = t0; t < t1; ++t) {
-    const int buf = (int)(t - t0) & 1;
-    dma_wait();
-    __syncthreads();
-    if (t + 1 < t1) {
-      start(t + 1);
-      if (t + 2 < t1) fetch(t + 2);
-    }
-    const char* tk = sm + buf * 2 * kTileBytes;
-    const char* tv = tk + kTileBytes;
+  for (int it = 0; it < keys.count; ++it) {
+    keys.next(it);
+    const char* const tk = keys.ktile(it);
+    const char* const tv = keys.vtile(it);
     const int kb0 = wk * 32 * NB;
-    // without a bias only the tile that the live keys end in has masked columns
-    const bool masked = bias != nullptr || (t + 1) * KT > nkeys;
     f32x16 sc[NB];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
@@ -136,12 +124,13 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)
       for (int s = 0; s < NS; ++s) sc[n] = mma(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n]);
     }
     float f = kExact ? (float)kLog2e : S.c;  // to log2 units
-    if (kExact || masked || A.scores) {
+    if (kExact || A.scores || keys.masked(it)) {
+      const float* const term = keys.term(it);
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x4 ct = *(const f32x4*)&sterm[buf][kb0 + 32 * n + 8 * g + 4 * h];
+          const f32x4 ct = *(const f32x4*)&term[kb0 + 32 * n + 8 * g + 4 * h];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float x = sc[n][4 * g + e];
@@ -150,7 +139,7 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)
         }
       if (!kExact) f = 1.0f;
       if (A.scores && row < S.rows) {
-        float* dst = A.scores + (pair * S.rows + row) * A.score_ld + t * KT + kb0;
+        float* dst = A.scores + (pair * S.rows + row) * A.score_ld + (t0 + it) * KT + kb0;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -204,7 +193,7 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)
   // columns, value x (not divided by the sum)
   const bool part = A.opart != nullptr;
   if constexpr (WK > 1) {
-    float* so = (float*)sm;  // [WK][DP][32]
+    float* const so = sm.join;
     __syncthreads();
     if (h == 0) sml[wk * 32 + r32] = f32x2{m, l};
 #pragma unroll
@@ -232,8 +221,9 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)
     T* orow = (T*)A.out + b * A.os[0] + ji * A.os[1] + jh * A.os[2];
     float* prow = part ? A.opart + (((int64_t)split * pairs + pair) * S.rows + jrow) * A.dvp : nullptr;
 #pragma unroll
-    for (int it = 0; it < DP * 8 / NT; ++it) {
+    for (int it = 0; it < (DP * 8 + NT - 1) / NT; ++it) {
       const int c = 4 * ((tid >> 5) + it * (NT / 32));
+      if (c >= DP) break;
       f32x4 x = {0, 0, 0, 0};
 #pragma unroll
       for (int w = 0; w < WK; ++w)
@@ -289,31 +279,81 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(32 * NB * WK, DP * (int)
   }
 }
 
-// Joins the splits of a row: 32 lanes per row, four columns a lane.
-template <class T>
+// Joins the splits of a row: 32 lanes per column group of four; GR groups of
+// lanes take every GR-th split and are added in a fixed order, 8 / GR rows per
+// workgroup. Few rows with many splits (decoding) take GR = 8: their loads are
+// then all in flight at once instead of one after the other (15 against 6 us
+// for 15 rows a head and 33 splits).
+template <class T, int GR>
 __global__ __launch_bounds__(256) void k_join(AttendArgs A) {
+  __shared__ f32x4 so[GR > 1 ? 256 : 1];
+  __shared__ f32x2 sml[GR > 1 ? 8 : 1];
   const Shape& S = A.S;
-  const int64_t pairs = (int64_t)S.batch * S.hkv;
-  const int64_t idx = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (idx >= pairs * S.rows) return;
-  const int64_t pair = idx / S.rows, row = idx - pair * S.rows;
-  const int c = 4 * (threadIdx.x & 31);
-  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
+  const int64_t n = (int64_t)S.batch * S.hkv * S.rows;  // rows in all
+  const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  const int64_t idx = (int64_t)blockIdx.x * (8 / GR) + grp / GR;
+  const bool live = idx < n;
+  const int c = 4 * lane;
+  // maximum over this group's splits, then over the groups
+  const int g = grp % GR;
   float mm = -kInf;
-  for (int s = 0; s < A.nsplit; ++s) mm = fmaxf(mm, A.mlpart[s * pairs * S.rows + idx][0]);
+  if (live)
+    for (int s = g + GR * lane; s < A.nsplit; s += GR * 32) mm = fmaxf(mm, A.mlpart[s * n + idx][0]);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor(mm, x, 32));
+  if constexpr (GR > 1) {
+    if (lane == 0) sml[grp][0] = mm;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < GR; ++k) mm = fmaxf(mm, sml[grp - g + k][0]);
+    __syncthreads();
+  }
   const float mu = mm == -kInf ? 0.0f : mm;
   float ll = 0.0f;
   f32x4 x = {0, 0, 0, 0};
-  for (int s = 0; s < A.nsplit; ++s) {
-    const f32x2 p = A.mlpart[s * pairs * S.rows + idx];
-    const float f = ex2(p[0] - mu);
-    ll = fmaf(f, p[1], ll);
-    if (c < A.dvp) {
-      const f32x4 o = *(const f32x4*)(A.opart + (s * pairs * S.rows + idx) * A.dvp + c);
+  if (live) {
+    int s = g;
+    for (; s + 3 * GR < A.nsplit; s += 4 * GR) {
+      f32x2 p[4];
+      f32x4 o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        p[k] = A.mlpart[(s + k * GR) * n + idx];
+        o[k] = c < A.dvp ? *(const f32x4*)(A.opart + ((s + k * GR) * n + idx) * A.dvp + c) : f32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = ex2(p[k][0] - mu);
+        ll = fmaf(f, p[k][1], ll);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = fmaf(f, o[k][e], x[e]);
+      }
+    }
+    for (; s < A.nsplit; s += GR) {
+      const f32x2 p = A.mlpart[s * n + idx];
+      const f32x4 o = c < A.dvp ? *(const f32x4*)(A.opart + (s * n + idx) * A.dvp + c) : f32x4{0, 0, 0, 0};
+      const float f = ex2(p[0] - mu);
+      ll = fmaf(f, p[1], ll);
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = fmaf(f, o[e], x[e]);
     }
   }
+  if constexpr (GR > 1) {
+    so[threadIdx.x] = x;
+    if (lane == 0) sml[grp][1] = ll;
+    __syncthreads();
+    if (g != 0) return;
+#pragma unroll
+    for (int k = 1; k < GR; ++k) {
+      const f32x4 y = so[threadIdx.x + 32 * k];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] += y[e];
+      ll += sml[grp + k][1];
+    }
+  }
+  if (!live) return;
+  const int64_t pair = idx / S.rows, row = idx - pair * S.rows;
+  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
   const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
 #pragma unroll
   for (int e = 0; e < 4; ++e) x[e] *= inv;
@@ -331,11 +371,11 @@ __global__ __launch_bounds__(256) void k_join(AttendArgs A) {
 template <class T, int DP>
 void attend_launch(const AttendArgs& A, bool many, hipStream_t st) {
   const int64_t blocks = xcd_blocks((int64_t)A.S.batch * A.S.hkv * A.tiles * A.nsplit);
-  constexpr int WK = sizeof(T) == 2 ? 4 : 2;  // fp32: two buffers of 128 keys would not fit
   if (many)
-    hipLaunchKernelGGL((k_attend<T, DP, 4, 1, 2>), grid1(blocks, 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_attend<T, DP, 4, 1, 2, 2>), grid1(blocks, 256), dim3(256), 0, st, A);
   else
-    hipLaunchKernelGGL((k_attend<T, DP, 1, WK, 1>), grid1(blocks, 64 * WK), dim3(64 * WK), 0, st, A);
+    hipLaunchKernelGGL((k_attend<T, DP, 1, few_waves(DP * sizeof(T)), 1, few_depth(DP * sizeof(T))>),
+                       grid1(blocks, 64 * few_waves(DP * sizeof(T))), dim3(64 * few_waves(DP * sizeof(T))), 0, st, A);
   SK_LAUNCH_CHECK();
 }
 
@@ -347,7 +387,11 @@ void attend(const AttendArgs& A, bool many, hipStream_t st) {
   else
     attend_launch<T, 64>(A, many, st);
   if (A.opart) {
-    hipLaunchKernelGGL((k_join<T>), grid1(((int64_t)A.S.batch * A.S.hkv * A.S.rows + 7) / 8, 256), dim3(256), 0, st, A);
+    const int64_t rows = (int64_t)A.S.batch * A.S.hkv * A.S.rows;
+    if (A.nsplit >= 8)
+      hipLaunchKernelGGL((k_join<T, 8>), grid1(rows, 256), dim3(256), 0, st, A);
+    else
+      hipLaunchKernelGGL((k_join<T, 1>), grid1((rows + 7) / 8, 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   }
 }

@@ -116,10 +116,8 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
   constexpr int KT = sizeof(T) * DP <= 256 ? 64 : 32, NT = 256, NS = DP / 16, NDB = DP / 32;
-  constexpr int kTileBytes = KT * TL::RB;
-  constexpr float kTerm = sizeof(T) == 4 ? 1.0f : (float)kLog2e;
-  __shared__ __attribute__((aligned(16))) char sm[4 * kTileBytes];
-  __shared__ __attribute__((aligned(16))) float sterm[2][KT], sraw[3][KT];
+  using KeyT = KeyTiles<T, DP, KT, NT, 2>;
+  __shared__ typename KeyT::Shared sm;
 
   const Shape& S = A.S;
   const int64_t pairs = (int64_t)S.batch * S.hkv;
@@ -142,21 +140,8 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
   const int64_t per = (ntiles + A.split_q - 1) / A.split_q;
   const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
 
-  const T* kbase = (const T*)S.k + b * S.ks[0] + hk * S.ks[2];
-  const T* vbase = (const T*)S.v + b * S.vs[0] + hk * S.vs[2];
-  const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
-  KeyTiles<T, DP, KT, NT> keys(S, wave, lane);
-  auto fetch = [&](int64_t t) { keys.fetch(bias, t, t - t0, nkeys, sraw, wave, lane); };
-  auto start = [&](int64_t t) { keys.start(S, kbase, vbase, bias, t, t - t0, nkeys, sm, sterm, sraw, kTerm, wave, lane); };
-  if (t0 < t1) {
-    if (bias) {
-      fetch(t0);
-      if (t0 + 1 < t1) fetch(t0 + 1);
-      dma_wait();
-      __syncthreads();
-    }
-    start(t0);
-  }
+  KeyT keys(sm, S, b, hk, t0, t1, nkeys, sizeof(T) == 4 ? 1.0f : (float)kLog2e, wave, lane);
+  keys.begin();
 
   V8 qf[NS], gf[NS];
   {
@@ -173,16 +158,11 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
 #pragma unroll
   for (int n = 0; n < NDB; ++n) dq[n] = zero16();
 
-  for (int64_t t = t0; t < t1; ++t) {
-    const int buf = (int)(t - t0) & 1;
-    dma_wait();
-    __syncthreads();
-    if (t + 1 < t1) {
-      start(t + 1);
-      if (t + 2 < t1) fetch(t + 2);
-    }
-    const char* tk = sm + buf * 2 * kTileBytes;
-    const char* tv = tk + kTileBytes;
+  for (int it = 0; it < keys.count; ++it) {
+    keys.next(it);
+    const char* const tk = keys.ktile(it);
+    const char* const tv = keys.vtile(it);
+    const float* const term = keys.term(it);
 #pragma unroll
     for (int n = 0; n < KT / 32; ++n) {
       f32x16 p = zero16(), g = zero16();
@@ -192,7 +172,7 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
       for (int s = 0; s < NS; ++s) g = mma(TL::row_frag(tv, 32 * n + r32, s, h), gf[s], g);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const f32x4 ct = *(const f32x4*)&sterm[buf][32 * n + 8 * q + 4 * h];
+        const f32x4 ct = *(const f32x4*)&term[32 * n + 8 * q + 4 * h];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = 4 * q + e;
@@ -273,7 +253,7 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 128 ? 2 : 1) void k_grad_kv(
   }
   for (int64_t t = t0; t < t1; ++t) {
     const int buf = (int)(t - t0) & 1;
-    dma_wait();
+    dma_wait<0>();
     __syncthreads();
     if (t + 1 < t1) start(t + 1);
     const char* tq = sm + buf * 2 * kTileBytes;

@@ -98,7 +98,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A
   float sum = 0.0f;
   for (int64_t t = t0; t < t1; ++t) {
     const int buf = (int)(t - t0) & 1;
-    dma_wait();
+    dma_wait<0>();
     __syncthreads();
     if (t + 1 < t1) {
       if (tid < RT) sstat[buf ^ 1][tid] = st;

@@ -203,11 +203,20 @@ constexpr uint32_t kOutside = 0x80000000u;
 // Written as assembly because the compiler waits for a load to LDS before any
 // LDS read that may alias it, so also before reads of the other buffer;
 // dma_wait() comes before the barrier behind which the data is read. The loads
-// have no destination register. CH: bytes a lane, 16 or 4.
-template <int CH>
+// have no destination register. CH: bytes a lane, 16 or 4. ONCE: the data is read
+// once (a non-temporal load, which leaves the caches to others).
+template <int CH, bool ONCE = false>
 __device__ __forceinline__ void dma_load(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds, uint32_t off) {
   lds = __builtin_amdgcn_readfirstlane(lds);
-  if constexpr (CH == 16)
+  if constexpr (CH == 16 && ONCE)
+    asm volatile(
+        "s_mov_b32 m0, %0\n"
+        "s_nop 0\n"
+        "buffer_load_dwordx4 %1, %2, 0 offen nt lds"
+        :
+        : "s"(lds), "v"(off), "s"(rsrc)
+        : "memory");
+  else if constexpr (CH == 16)
     asm volatile(
         "s_mov_b32 m0, %0\n"
         "s_nop 0\n"
@@ -233,10 +242,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t dma_rsrc(const void* base) {
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
 }
-__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Waits until at most N of the wave's memory operations are outstanding (they
+// complete in order, so all but the last N have).
+template <int N>
+__device__ __forceinline__ void dma_wait() {
+  static_assert(N >= 0 && N < 64, "vmcnt has six bits");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 // Loader of ROWS rows by the workgroup's NT threads. `wave` must be uniform.
-template <class T, int DP, int ROWS, int NT>
+template <class T, int DP, int ROWS, int NT, bool ONCE = false>
 struct Loader {
   using TL = Tile<T, DP>;
   static constexpr int N = ROWS * TL::CPR / NT;  // chunks per thread
@@ -263,7 +278,7 @@ struct Loader {
     const __amdgpu_buffer_rsrc_t rsrc = dma_rsrc(base);
     const uint32_t lds = lds_offset(t) + wave * (N * 1024);
 #pragma unroll
-    for (int n = 0; n < N; ++n) dma_load<16>(rsrc, lds + n * 1024, live(row(n, wave, lane)) ? off[n] : kOutside);
+    for (int n = 0; n < N; ++n) dma_load<16, ONCE>(rsrc, lds + n * 1024, live(row(n, wave, lane)) ? off[n] : kOutside);
   }
 };
 
@@ -344,44 +359,61 @@ struct RowTiles {
   }
 };
 
-// Tiles of KT keys: k and v in buffer (n & 1) of `sm` (k, then v), their column
-// terms in sterm[n & 1]; tile t is the n-th of the workgroup. Biases of tile n
-// are loaded to sraw[n % 3] during tile n - 2; during tile n - 1 they decide
-// which rows are loaded and become the column terms.
-template <class T, int DP, int KT, int NT>
+// The tiles of KT keys that a workgroup runs over, the n-th (n = 0 .. count - 1) from
+// tile t0 on, in a ring of D buffers (k, then v, in each): tile n + D - 1 is
+// started while tile n is computed on. Biases arrive D - 1 tiles before that,
+// in a ring of their own: when a tile is started they decide which of its rows
+// are loaded and become its column terms (times `unit`; -inf: masked).
+template <class T, int DP, int KT, int NT, int D, bool ONCE = false>
 struct KeyTiles {
-  Loader<T, DP, KT, NT> lk, lv;
+  using Ld = Loader<T, DP, KT, NT, ONCE>;
   static constexpr int kTileBytes = KT * Tile<T, DP>::RB;
+  static constexpr int kOps = 2 * Ld::N;  // loads of a wave per tile
+  struct Shared {
+    __attribute__((aligned(16))) char tiles[D][2][kTileBytes];
+    __attribute__((aligned(16))) float term[D][KT], raw[D][KT];
+  };
+  Ld lk, lv;
+  Shared& sm;
+  const T* k;
+  const T* v;
+  int64_t ks, vs;
+  const float* bias;
+  int64_t t0, nkeys;
+  int count, wave, lane;
+  float unit;
 
-  __device__ __forceinline__ KeyTiles(const Shape& S, int wave, int lane) {
-    const uint32_t kp = (uint32_t)(S.ks[1] * sizeof(T)), vp = (uint32_t)(S.vs[1] * sizeof(T));
+  __device__ __forceinline__ KeyTiles(Shared& sm_, const Shape& S, int b, int hk, int64_t first, int64_t last,
+                                      int64_t nkeys_, float unit_, int wave_, int lane_)
+      : sm(sm_), k((const T*)S.k + b * S.ks[0] + hk * S.ks[2]), v((const T*)S.v + b * S.vs[0] + hk * S.vs[2]),
+        ks(S.ks[1]), vs(S.vs[1]), bias(S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr), t0(first),
+        nkeys(nkeys_), count(last > first ? (int)(last - first) : 0), wave(wave_), lane(lane_), unit(unit_) {
+    const uint32_t kp = (uint32_t)(ks * sizeof(T)), vp = (uint32_t)(vs * sizeof(T));
     lk.place([&](int r) { return r * kp; }, S.d, wave, lane);
     lv.place([&](int r) { return r * vp; }, S.dv, wave, lane);
   }
-  __device__ __forceinline__ void fetch(const float* bias, int64_t t, int64_t n, int64_t nkeys, float (*sraw)[KT],
-                                        int wave, int lane) const {
-    if (!bias || wave * 64 >= KT) return;
+  __device__ __forceinline__ void fetch(int n) const {
     const int j = wave * 64 + lane;
-    dma_load<4>(dma_rsrc(bias + t * KT), lds_offset(sraw[n % 3]) + wave * 256,
-                j < KT && t * KT + j < nkeys ? 4 * j : kOutside);
+    if (!bias || n >= count || j >= KT) return;  // a lane that loads also writes: none behind the tile
+    const int64_t first = (t0 + n) * KT;
+    dma_load<4>(dma_rsrc(bias + first), lds_offset(sm.raw[n % D]) + wave * 256, first + j < nkeys ? 4 * j : kOutside);
   }
-  __device__ __forceinline__ void start(const Shape& S, const T* kbase, const T* vbase, const float* bias, int64_t t,
-                                        int64_t n, int64_t nkeys, char* sm, float (*sterm)[KT], float (*sraw)[KT],
-                                        float unit, int wave, int lane) const {
-    const int buf = (int)n & 1, tid = wave * 64 + lane;
-    const float* raw = sraw[n % 3];
-    const int64_t left = nkeys - t * KT;  // live keys from the tile's first on
+  __device__ __forceinline__ void start(int n) const {
+    if (n >= count) return;
+    const int buf = n % D, tid = wave * 64 + lane;
+    const float* raw = sm.raw[buf];
+    const int64_t first = (t0 + n) * KT, left = nkeys - first;  // live keys from the tile's first on
     if (tid < KT) {
       float term = 0.0f;
       if (bias) {
         const float x = raw[tid];
         term = x <= kMasked ? -kInf : x * unit;
       }
-      sterm[buf][tid] = tid < left ? term : -kInf;
+      sm.term[buf][tid] = tid < left ? term : -kInf;
     }
     auto both = [&](auto&& live) {
-      lk.start(kbase + t * KT * S.ks[1], sm + buf * 2 * kTileBytes, live, wave, lane);
-      lv.start(vbase + t * KT * S.vs[1], sm + buf * 2 * kTileBytes + kTileBytes, live, wave, lane);
+      lk.start(k + first * ks, sm.tiles[buf][0], live, wave, lane);
+      lv.start(v + first * vs, sm.tiles[buf][1], live, wave, lane);
     };
     if (bias)
       both([&](int r) { return r < left && !(raw[r] <= kMasked); });
@@ -390,6 +422,48 @@ struct KeyTiles {
     else
       both([](int) { return true; });
   }
+  // before the first tile
+  __device__ __forceinline__ void begin() const {
+    if (bias) {
+#pragma unroll
+      for (int n = 0; n < 2 * (D - 1) && n < D; ++n) fetch(n);
+      dma_wait<0>();
+      __syncthreads();
+    }
+#pragma unroll
+    for (int n = 0; n < D - 1; ++n) {
+      start(n);
+    }
+    if (bias && D > 2) {
+      // the rest of the biases that the first tiles' starts will want
+      __syncthreads();
+#pragma unroll
+      for (int n = D; n < 2 * (D - 1); ++n) fetch(n);
+      dma_wait<0>();
+    }
+  }
+  // makes tile n readable and starts the one D - 1 further on
+  __device__ __forceinline__ void next(int n) const {
+    // loads of the tiles after n are in flight; whatever else the wave has
+    // issued since only makes the wait longer
+    const int ahead = count - 1 - n;
+    if constexpr (D == 2)
+      dma_wait<0>();
+    else if (ahead >= D - 2)
+      dma_wait<(D - 2) * kOps>();
+    else if (D > 3 && ahead == 1)
+      dma_wait<kOps>();
+    else
+      dma_wait<0>();
+    __syncthreads();
+    fetch(n + 2 * (D - 1));
+    start(n + D - 1);
+  }
+  __device__ __forceinline__ const char* ktile(int n) const { return sm.tiles[n % D][0]; }
+  __device__ __forceinline__ const char* vtile(int n) const { return sm.tiles[n % D][1]; }
+  __device__ __forceinline__ const float* term(int n) const { return sm.term[n % D]; }
+  // does tile n have masked columns? (without a bias only where the live keys end)
+  __device__ __forceinline__ bool masked(int n) const { return bias != nullptr || (t0 + n + 1) * KT > nkeys; }
 };
 
 // Workgroup index -> work item, such that each XCD (workgroups go to the 8

@@ -207,9 +207,10 @@ AttendPlan plan_attend(const sinkhorn_attention* a, const void* q, const void* k
   const int64_t rows = a->len_q * (a->heads_q / a->heads_kv);
   p.many = rows > 32;
   p.tiles = ceil_div(rows, p.many ? 128 : 32);
-  const int64_t steps = ceil_div(a->len_k, p.many || f32 ? 64 : 128);
-  const int64_t slots = p.many ? (f32 && wide(a) ? 256 : 512) : (wide(a) ? 256 : 512);
-  p.nsplit = splits(pairs * p.tiles, steps, slots, join_steps(a), !p.many);
+  const int64_t keys = p.many ? 64 : 32 * few_waves((wide(a) ? 128 : 64) * elem_size(a));  // of a tile
+  const int64_t steps = ceil_div(a->len_k, keys);
+  const int64_t slots = !p.many || (f32 && wide(a)) ? 256 : 512;
+  p.nsplit = splits(pairs * p.tiles, steps, slots, p.many ? join_steps(a) : 7.0, !p.many);
   p.partial = p.nsplit > 1;
   p.scores = mass && !p.many;
   p.q = operand(a, q, a->q_stride, a->len_q, a->heads_q, a->d, ws);
@@ -221,7 +222,7 @@ AttendPlan plan_attend(const sinkhorn_attention* a, const void* q, const void* k
     p.ml_off = ws.take(8 * p.nsplit * pairs * rows);
   }
   if (p.scores) {
-    p.score_ld = ceil_div(a->len_k, 128) * 128;
+    p.score_ld = ceil_div(a->len_k, keys) * keys;
     p.score_off = ws.take(4 * pairs * rows * p.score_ld);
   } else if (mass) {
     // the forward pass is done with its partial results by then

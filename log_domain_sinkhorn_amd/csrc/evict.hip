@@ -6,8 +6,10 @@
 // k_evict_select (one workgroup per pair) finds the K-th largest weight by
 // radix selection on the weights' bits taken as ordered integers (8 bits a
 // pass, counts in LDS: integer sums, so the result is exact and does not depend
-// on the order of threads), then writes the kept indices in order with a scan;
-// keys that equal the threshold are taken from the lowest index up.
+// on the order of threads), then writes the kept indices in order; keys that
+// equal the threshold are taken from the lowest index up. Each pass takes
+// 16384 keys at a time, 16 loads of a thread in flight: one load at a time, the
+// passes are bound by the latency of memory.
 // k_evict_move copies the rows. The copy is bound by memory.
 #include "attention.h"
 
@@ -32,6 +34,8 @@ struct EvictArgs {
 };
 
 constexpr int kSelThreads = 1024;
+constexpr int kSelPer = 16;  // keys of a thread in flight
+constexpr int kSelChunk = kSelThreads * kSelPer;
 
 __device__ __forceinline__ int64_t evict_len(const EvictArgs& A, int b) {
   if (!A.klen) return A.len;
@@ -48,7 +52,7 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 
 __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
   __shared__ uint32_t hist[256];
-  __shared__ uint32_t swave[kSelThreads / 64];
+  __shared__ uint32_t swave[2][kSelThreads / 64];
   __shared__ uint32_t sdigit, sbefore;
   const int64_t pair = blockIdx.x;
   const int b = (int)(pair / A.heads);
@@ -77,9 +81,16 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
     for (int shift = 24; shift >= 0; shift -= 8) {
       if (tid < 256) hist[tid] = 0;
       __syncthreads();
-      for (int64_t j = lo + tid; j < hi; j += kSelThreads) {
-        const uint32_t u = order_key(w[j]);
-        if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1u);
+      for (int64_t j0 = lo; j0 < hi; j0 += kSelChunk) {
+        float x[kSelPer];
+        const int64_t j = j0 + tid;
+#pragma unroll
+        for (int i = 0; i < kSelPer; ++i) x[i] = j + i * kSelThreads < hi ? w[j + i * kSelThreads] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kSelPer; ++i) {
+          const uint32_t u = order_key(x[i]);
+          if (j + i * kSelThreads < hi && (u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1u);
+        }
       }
       __syncthreads();
       if (tid < 64) {
@@ -110,49 +121,58 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
       prefix |= sdigit << shift;
       mask |= 255u << shift;
       need -= sbefore;
-      __syncthreads();
     }
   }
-  // keys above `prefix` are kept, and the first `need` of those equal to it
+  // keys above `prefix` are kept, and the first `need` of those equal to it.
+  // A wave takes 1024 consecutive keys of a chunk, 64 at a time.
   const bool any = A.keep > A.first + A.recent;
   uint32_t nsel = 0, neq = 0;  // kept for sure, and equal, before this chunk
-  for (int64_t j0 = 0; j0 < n; j0 += kSelThreads) {
-    const int64_t j = j0 + tid;
-    uint32_t f = 0;  // low half: kept for sure; high half: equal to the threshold
-    float x = 0.0f;
-    if (j < n) {
-      x = w[j];
-      if (j < lo || j >= hi) {
-        f = 1;
-      } else if (any) {
-        const uint32_t u = order_key(x);
-        f = u > prefix ? 1u : (u == prefix ? 0x10000u : 0u);
-      }
-    }
-    uint32_t inc = f;
+  for (int64_t j0 = 0; j0 < n; j0 += kSelChunk) {
+    const int64_t jw = j0 + wave * (64 * kSelPer) + lane;
+    float x[kSelPer];
 #pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const uint32_t y = __shfl_up(inc, s);
-      if (lane >= s) inc += y;
+    for (int i = 0; i < kSelPer; ++i) x[i] = jw + 64 * i < n ? w[jw + 64 * i] : 0.0f;
+    uint64_t sel[kSelPer], eq[kSelPer];
+    uint32_t csel = 0, ceq = 0;
+#pragma unroll
+    for (int i = 0; i < kSelPer; ++i) {
+      const int64_t j = jw + 64 * i;
+      const bool always = j < n && (j < lo || j >= hi);
+      const bool mid = j < n && !always && any;
+      const uint32_t u = order_key(x[i]);
+      sel[i] = __ballot(always || (mid && u > prefix));
+      eq[i] = __ballot(mid && u == prefix);
+      csel += __popcll(sel[i]);
+      ceq += __popcll(eq[i]);
     }
-    if (lane == 63) swave[wave] = inc;
+    if (lane == 0) {
+      swave[0][wave] = csel;
+      swave[1][wave] = ceq;
+    }
     __syncthreads();
-    uint32_t base = 0, total = 0;
+    uint32_t s = nsel, q = neq;  // kept, and equal, before this wave's keys
     for (int k = 0; k < kSelThreads / 64; ++k) {
-      if (k < wave) base += swave[k];
-      total += swave[k];
-    }
-    const uint32_t ex = base + inc - f;
-    const uint32_t sel = nsel + (ex & 0xffffu), eq = neq + (ex >> 16);
-    if ((f & 1u) || ((f >> 16) && eq < need)) {
-      const int64_t pos = (int64_t)sel + (eq < need ? eq : need);
-      if (pos < A.cap) {
-        idx[pos] = (int32_t)j;
-        mo[pos] = x;
+      if (k < wave) {
+        s += swave[0][k];
+        q += swave[1][k];
       }
+      nsel += swave[0][k];
+      neq += swave[1][k];
     }
-    nsel += total & 0xffffu;
-    neq += total >> 16;
+    const uint64_t below = (uint64_t(1) << lane) - 1;
+#pragma unroll
+    for (int i = 0; i < kSelPer; ++i) {
+      const uint32_t es = s + __popcll(sel[i] & below), ee = q + __popcll(eq[i] & below);
+      if (((sel[i] >> lane) & 1) || (((eq[i] >> lane) & 1) && ee < need)) {
+        const int64_t pos = (int64_t)es + (ee < need ? ee : need);
+        if (pos < A.cap) {
+          idx[pos] = (int32_t)(jw + 64 * i);
+          mo[pos] = x[i];
+        }
+      }
+      s += __popcll(sel[i]);
+      q += __popcll(eq[i]);
+    }
     __syncthreads();
   }
 }

@@ -62,6 +62,7 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(D, 32 * NB * WK, DP * (i
   // makes it. 16-bit types: log2 units from the start, one operation less.
   constexpr bool kExact = sizeof(T) == 4;
   constexpr float kTerm = kExact ? 1.0f : (float)kLog2e;
+  static_assert(WK == 1 || (WQ == 1 && NB == 1), "few rows: one tile of 32, a wave's own 32 keys");
   using KeyT = KeyTiles<T, DP, KT, NT, D, (WK > 1)>;  // few rows: each key is read by one workgroup
   constexpr int kJoinBytes = WK > 1 ? WK * 32 * DP * 4 : 0;
   union Memory {
@@ -112,7 +113,8 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(D, 32 * NB * WK, DP * (i
   float m = -kInf, l = 0.0f;  // the row's reference (log2 units) and this lane's part of the sum
 
   for (int it = 0; it < keys.count; ++it) {
-    keys.next(it);
+    // each of the last two tiles stored its scores with an instruction at least
+    keys.template next<(D > 2 ? 2 : 0)>(it, D > 2 && A.scores && it >= 2);
     const char* const tk = keys.ktile(it);
     const char* const tv = keys.vtile(it);
     const int kb0 = wk * 32 * NB;
@@ -138,14 +140,21 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(D, 32 * NB * WK, DP * (i
           }
         }
       if (!kExact) f = 1.0f;
-      if (A.scores && row < S.rows) {
-        float* dst = A.scores + (pair * S.rows + row) * A.score_ld + (t0 + it) * KT + kb0;
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
+      if constexpr (WK > 1) {
+        if (A.scores) {
+          // Through this wave's own rows of the k tile, which it is done with, so
+          // that a row's 32 scores go out as one 128-byte line (four 32-byte
+          // pieces of a line each cost 60 of 350 us at 16 x 8 x 32768 keys).
+          char* const mine = const_cast<char*>(tk) + kb0 * TL::RB;
 #pragma unroll
           for (int g = 0; g < 4; ++g)
-            *(f32x4*)(dst + 32 * n + 8 * g + 4 * h) =
-                f32x4{sc[n][4 * g], sc[n][4 * g + 1], sc[n][4 * g + 2], sc[n][4 * g + 3]};
+            *(f32x4*)(mine + 128 * r32 + 16 * ((2 * g + h) ^ (r32 & 7))) =
+                f32x4{sc[0][4 * g], sc[0][4 * g + 1], sc[0][4 * g + 2], sc[0][4 * g + 3]};
+          float* const dst = A.scores + pair * S.rows * A.score_ld + (t0 + it) * KT + kb0;
+          for (int r = lane >> 3; r < (int)S.rows; r += 8)
+            *(f32x4*)(dst + r * A.score_ld + 4 * (lane & 7)) =
+                *(const f32x4*)(mine + 128 * r + 16 * ((lane & 7) ^ (r & 7)));
+        }
       }
     }
     float mx = -kInf;

@@ -442,13 +442,18 @@ struct KeyTiles {
       dma_wait<0>();
     }
   }
-  // makes tile n readable and starts the one D - 1 further on
-  __device__ __forceinline__ void next(int n) const {
-    // loads of the tiles after n are in flight; whatever else the wave has
-    // issued since only makes the wait longer
+  // Makes tile n readable and starts the one D - 1 further on. The loads of the
+  // tiles after n stay in flight, and of what else the wave has issued since
+  // the loads of tile n at least `stores` operations (0 or STORES), so that
+  // waiting for loads does not mean waiting for the caller's stores; any more
+  // than that only make the wait longer.
+  template <int STORES = 0>
+  __device__ __forceinline__ void next(int n, bool stores = false) const {
     const int ahead = count - 1 - n;
     if constexpr (D == 2)
       dma_wait<0>();
+    else if (ahead >= D - 2 && stores)
+      dma_wait<(D - 2) * kOps + STORES>();
     else if (ahead >= D - 2)
       dma_wait<(D - 2) * kOps>();
     else if (D > 3 && ahead == 1)

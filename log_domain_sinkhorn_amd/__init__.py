@@ -458,16 +458,39 @@ def _plain(t, name, dtype, shape):
 
 
 def _same_device(first, others):
-    if first.device.type != "cuda":
+    """The device's index."""
+    index = first.get_device()
+    if index < 0:
         raise ValueError("the arguments must be device tensors")
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"the arguments are on different devices ({first.device}, {t.device})")
+    return index
+
+
+# the current stream's handle without a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(index, where, fn, *args):
+    """fn(*args, current stream) with device `index` current."""
+    if torch.cuda.current_device() == index:
+        _check(fn(*args, _raw_stream(index)), where)
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, _raw_stream(index)), where)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _strides3(t):
     """Element strides of batch, length and head (0 where there is one)."""
-    return _i64x3(*[st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride()[:3])])
+    n0, n1, n2, _ = t.shape
+    s0, s1, s2, _ = t.stride()
+    return _i64x3(s0 if n0 > 1 else 0, s1 if n1 > 1 else 0, s2 if n2 > 1 else 0)
 
 
 def _attention(q, k, v, scale, key_bias, query_lengths, key_lengths):
@@ -485,9 +508,8 @@ def _attention(q, k, v, scale, key_bias, query_lengths, key_lengths):
             raise ValueError(f"v has shape {tuple(v.shape)}, expected ({B}, {lk}, {hkv}, width)")
     if hkv < 1 or hq < 1 or hq % hkv:
         raise ValueError(f"{hq} query heads are no multiple of {hkv} key heads")
-    a = _AttentionC(dtype=_ATTN_DTYPES[q.dtype], batch=B, heads_q=hq, heads_kv=hkv, d=d, dv=dv, len_q=lq, len_k=lk,
-                    scale=1.0 / math.sqrt(max(d, 1)) if scale is None else float(scale),
-                    q_stride=_strides3(q), k_stride=_strides3(k))
+    a = _AttentionC(_ATTN_DTYPES[q.dtype], B, hq, hkv, d, dv, lq, lk,
+                    1.0 / math.sqrt(max(d, 1)) if scale is None else float(scale), _strides3(q), _strides3(k))
     if v is not None:
         a.v_stride = _strides3(v)
     if key_bias is not None:
@@ -510,7 +532,7 @@ def _attention(q, k, v, scale, key_bias, query_lengths, key_lengths):
 
 def _workspace(a, what, device, q, k, v=None, dout=None):
     n = _i64()
-    _check(lib().sinkhorn_attention_workspace(ctypes.byref(a), what, _ptr(q), _ptr(k), _ptr(v), _ptr(dout),
+    _check(lib().sinkhorn_attention_workspace(ctypes.byref(a), what, _at(q), _at(k), _at(v), _at(dout),
                                               ctypes.byref(n)), "attention_workspace")
     return (torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None), n.value
 
@@ -552,15 +574,14 @@ def cross_attention(q, k, v, *, scale=None, key_bias=None, query_lengths=None, k
     if mass_out is None and (mass_in is not None or row_weight is not None):
         raise ValueError("mass_in and row_weight need mass_out")
     _mass_args(a, row_weight, mass_in, mass_out)
-    _same_device(q, (k, v, key_bias, query_lengths, key_lengths, row_weight, mass_in, mass_out, out, lse))
-    with torch.cuda.device(q.device):
-        out = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
-        lse = torch.empty((B, hq, lq), dtype=torch.float32, device=q.device) if lse is None else lse
-        a.out_stride = _strides3(out)
-        ws, n = _workspace(a, _ATTEND if mass_out is None else _ATTEND_MASS, q.device, q, k, v)
-        _check(lib().sinkhorn_cross_attention(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                                              _ptr(row_weight), _ptr(mass_in), _ptr(mass_out), _ptr(ws), n,
-                                              _stream(q.device)), "cross_attention")
+    index = _same_device(q, (k, v, key_bias, query_lengths, key_lengths, row_weight, mass_in, mass_out, out, lse))
+    device = q.device
+    out = torch.empty(shape, dtype=q.dtype, device=device) if out is None else out
+    lse = torch.empty((B, hq, lq), dtype=torch.float32, device=device) if lse is None else lse
+    a.out_stride = _strides3(out)
+    ws, n = _workspace(a, _ATTEND if mass_out is None else _ATTEND_MASS, device, q, k, v)
+    _launch(index, "cross_attention", lib().sinkhorn_cross_attention, ctypes.byref(a), q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), out.data_ptr(), lse.data_ptr(), _at(row_weight), _at(mass_in), _at(mass_out), _at(ws), n)
     return out, lse
 
 
@@ -578,16 +599,16 @@ def cross_attention_grad(dout, q, k, v, out, lse, *, scale=None, key_bias=None, 
     for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
         if t is not None:
             _written(_head_tensor(t, name, q.dtype, like.shape), name)
-    _same_device(q, (k, v, key_bias, query_lengths, key_lengths, dout, out, lse, dq, dk, dv))
-    with torch.cuda.device(q.device):
-        dq, dk, dv = (torch.empty(like.shape, dtype=q.dtype, device=q.device) if t is None else t
-                      for t, like in ((dq, q), (dk, k), (dv, v)))
-        a.out_stride, a.dout_stride = _strides3(out), _strides3(dout)
-        a.dq_stride, a.dk_stride, a.dv_stride = _strides3(dq), _strides3(dk), _strides3(dv)
-        ws, n = _workspace(a, _ATTEND_GRAD, q.device, q, k, v, dout)
-        _check(lib().sinkhorn_cross_attention_grad(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                                                   _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), n,
-                                                   _stream(q.device)), "cross_attention_grad")
+    index = _same_device(q, (k, v, key_bias, query_lengths, key_lengths, dout, out, lse, dq, dk, dv))
+    device = q.device
+    dq, dk, dv = (torch.empty(like.shape, dtype=q.dtype, device=device) if t is None else t
+                  for t, like in ((dq, q), (dk, k), (dv, v)))
+    a.out_stride, a.dout_stride = _strides3(out), _strides3(dout)
+    a.dq_stride, a.dk_stride, a.dv_stride = _strides3(dq), _strides3(dk), _strides3(dv)
+    ws, n = _workspace(a, _ATTEND_GRAD, device, q, k, v, dout)
+    _launch(index, "cross_attention_grad", lib().sinkhorn_cross_attention_grad, ctypes.byref(a), q.data_ptr(),
+            k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+            dv.data_ptr(), _at(ws), n)
     return dq, dk, dv
 
 
@@ -599,14 +620,12 @@ def attention_mass(q, k, lse, *, scale=None, key_bias=None, query_lengths=None, 
     a = _attention(q, k, None, scale, key_bias, query_lengths, key_lengths)
     _plain(lse, "lse", torch.float32, (a.batch, a.heads_q, a.len_q))
     _mass_args(a, row_weight, mass_in, mass_out)
-    _same_device(q, (k, key_bias, query_lengths, key_lengths, lse, row_weight, mass_in, mass_out))
-    with torch.cuda.device(q.device):
-        if mass_out is None:
-            mass_out = torch.empty((a.batch, a.heads_kv, a.len_k), dtype=torch.float32, device=q.device)
-        ws, n = _workspace(a, _ATTENTION_MASS, q.device, q, k)
-        _check(lib().sinkhorn_attention_mass(ctypes.byref(a), _ptr(q), _ptr(k), _ptr(lse), _ptr(row_weight),
-                                             _ptr(mass_in), _ptr(mass_out), _ptr(ws), n, _stream(q.device)),
-               "attention_mass")
+    index = _same_device(q, (k, key_bias, query_lengths, key_lengths, lse, row_weight, mass_in, mass_out))
+    if mass_out is None:
+        mass_out = torch.empty((a.batch, a.heads_kv, a.len_k), dtype=torch.float32, device=q.device)
+    ws, n = _workspace(a, _ATTENTION_MASS, q.device, q, k)
+    _launch(index, "attention_mass", lib().sinkhorn_attention_mass, ctypes.byref(a), q.data_ptr(), k.data_ptr(),
+            lse.data_ptr(), _at(row_weight), _at(mass_in), mass_out.data_ptr(), _at(ws), n)
     return mass_out
 
 
@@ -643,24 +662,23 @@ def cache_evict(k, v, mass, keep: int, *, key_lengths=None, first: int = 0, rece
         _plain(index_out, "index_out", torch.int32, (B, h, cap))
     if lengths_out is not None:
         _plain(lengths_out, "lengths_out", torch.int32, (B,))
-    _same_device(k, (v, mass, key_lengths, k_out, v_out, mass_out, index_out, lengths_out))
-    with torch.cuda.device(k.device):
-        # without key_lengths every row of the outputs is written
-        new = torch.empty if key_lengths is None else torch.zeros
-        k_out = new((B, cap, h, d), dtype=k.dtype, device=k.device) if k_out is None else k_out
-        v_out = new((B, cap, h, dv), dtype=k.dtype, device=k.device) if v_out is None else v_out
-        if mass_out is None:
-            mass_out = torch.empty((B, h, cap), dtype=torch.float32, device=k.device)
-        if index_out is None:
-            index_out = torch.empty((B, h, cap), dtype=torch.int32, device=k.device)
-        if lengths_out is None:
-            lengths_out = torch.empty(B, dtype=torch.int32, device=k.device)
-        c = _CacheC(dtype=_ATTN_DTYPES[k.dtype], batch=B, heads=h, d=d, dv=dv, len=n, keep=keep, first=first,
-                    recent=recent, k_stride=_strides3(k), v_stride=_strides3(v), k_out_stride=_strides3(k_out),
-                    v_out_stride=_strides3(v_out), key_lengths=None if key_lengths is None else key_lengths.data_ptr())
-        _check(lib().sinkhorn_cache_evict(ctypes.byref(c), _ptr(k), _ptr(v), _ptr(mass), _ptr(k_out), _ptr(v_out),
-                                          _ptr(mass_out), _ptr(index_out), _ptr(lengths_out), _stream(k.device)),
-               "cache_evict")
+    index = _same_device(k, (v, mass, key_lengths, k_out, v_out, mass_out, index_out, lengths_out))
+    device = k.device
+    # without key_lengths every row of the outputs is written
+    new = torch.empty if key_lengths is None else torch.zeros
+    k_out = new((B, cap, h, d), dtype=k.dtype, device=device) if k_out is None else k_out
+    v_out = new((B, cap, h, dv), dtype=k.dtype, device=device) if v_out is None else v_out
+    if mass_out is None:
+        mass_out = torch.empty((B, h, cap), dtype=torch.float32, device=device)
+    if index_out is None:
+        index_out = torch.empty((B, h, cap), dtype=torch.int32, device=device)
+    if lengths_out is None:
+        lengths_out = torch.empty(B, dtype=torch.int32, device=device)
+    c = _CacheC(_ATTN_DTYPES[k.dtype], B, h, d, dv, n, keep, first, recent, _strides3(k), _strides3(v), _strides3(k_out),
+                _strides3(v_out), _at(key_lengths))
+    _launch(index, "cache_evict", lib().sinkhorn_cache_evict, ctypes.byref(c), k.data_ptr(), v.data_ptr(),
+            mass.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), mass_out.data_ptr(), index_out.data_ptr(),
+            lengths_out.data_ptr())
     return k_out, v_out, mass_out, index_out, lengths_out
 
 

@@ -43,14 +43,8 @@ struct AttendArgs {
 constexpr int few_waves(int64_t bytes) { return bytes <= 128 ? 6 : (bytes <= 256 ? 3 : 2); }
 constexpr int few_depth(int64_t bytes) { return bytes <= 256 ? 3 : 2; }
 
-// Waves a SIMD that LDS leaves room for: `depth` tiles of `keys` keys of `row`
-// bytes, `waves` waves in a workgroup.
-constexpr int attend_waves(int depth, int keys, int row, int waves) {
-  return waves / 4 * (2 * depth * keys * row <= 72 * 1024 ? 2 : 1) >= 2 ? 2 : 1;
-}
-
-template <class T, int DP, int WQ, int WK, int NB, int D>
-__global__ __launch_bounds__(64 * WQ * WK, attend_waves(D, 32 * NB * WK, DP * (int)sizeof(T), WQ * WK)) void k_attend(
+template <class T, int DP, int WQ, int WK, int NB, int D, int OCC>
+__global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
     AttendArgs A) {
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
@@ -117,7 +111,7 @@ __global__ __launch_bounds__(64 * WQ * WK, attend_waves(D, 32 * NB * WK, DP * (i
     keys.template next<(D > 2 ? 2 : 0)>(it, D > 2 && A.scores && it >= 2);
     const char* const tk = keys.ktile(it);
     const char* const tv = keys.vtile(it);
-    const int kb0 = wk * 32 * NB;
+    const int kb0 = 32 * NB * wk;
     f32x16 sc[NB];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
@@ -380,11 +374,17 @@ __global__ __launch_bounds__(256) void k_join(AttendArgs A) {
 template <class T, int DP>
 void attend_launch(const AttendArgs& A, bool many, hipStream_t st) {
   const int64_t blocks = xcd_blocks((int64_t)A.S.batch * A.S.hkv * A.tiles * A.nsplit);
+  constexpr int RB = DP * (int)sizeof(T);
+  // many rows: two waves a SIMD (three for 64 columns of 16 bits); with fewer
+  // registers a wave spills, and half tiles cost more in what each tile
+  // repeats than they gain in occupancy (8192 x 16384 x 32 heads of 128:
+  // 2180 us against 5200)
+  constexpr int OCC = RB == 128 ? 3 : (RB == 256 ? 2 : 1);
   if (many)
-    hipLaunchKernelGGL((k_attend<T, DP, 4, 1, 2, 2>), grid1(blocks, 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_attend<T, DP, 4, 1, 2, 2, OCC>), grid1(blocks, 256), dim3(256), 0, st, A);
   else
-    hipLaunchKernelGGL((k_attend<T, DP, 1, few_waves(DP * sizeof(T)), 1, few_depth(DP * sizeof(T))>),
-                       grid1(blocks, 64 * few_waves(DP * sizeof(T))), dim3(64 * few_waves(DP * sizeof(T))), 0, st, A);
+    hipLaunchKernelGGL((k_attend<T, DP, 1, few_waves(RB), 1, few_depth(RB), RB == 128 ? 2 : 1>),
+                       grid1(blocks, 64 * few_waves(RB)), dim3(64 * few_waves(RB)), 0, st, A);
   SK_LAUNCH_CHECK();
 }
 

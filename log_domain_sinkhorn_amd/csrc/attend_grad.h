@@ -295,30 +295,44 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 128 ? 2 : 1) void k_grad_kv(
   write_cols<T, NDB>(dv, 1.0f, A.part_v ? A.part_v + pi * A.dvp : nullptr, A.dvp, dvrow, S.dv, A.vec_v, h);
 }
 
-// Adds the partial sums of one gradient in split order: 32 lanes per row.
-// Rows of dQ are packed (group > 1); rows of dK, dV are keys (group = 1).
+// Adds the partial sums of a gradient in split order: 32 lanes per row. Rows of
+// dQ are packed (group > 1); rows of dK, dV are keys (group = 1).
+struct GradJoin {
+  const float* part;
+  int64_t rows;
+  int32_t nsplit, dp, group, d;
+  void* out;
+  int64_t s[3];
+  bool vec;
+};
+struct GradJoins {
+  GradJoin g[3];
+  int64_t pairs;
+  int32_t hkv;
+};
+
 template <class T>
-__global__ __launch_bounds__(256) void k_grad_join(const float* part, int nsplit, int64_t pairs, int64_t rows,
-                                                   int32_t dp, int32_t hkv, int32_t group, T* out, int64_t s0,
-                                                   int64_t s1, int64_t s2, int32_t d, bool vec) {
+__global__ __launch_bounds__(256) void k_grad_join(GradJoins all) {
+  const GradJoin& J = all.g[blockIdx.y];
+  const int64_t n = all.pairs * J.rows;
   const int64_t idx = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int c = 4 * (threadIdx.x & 31);
-  if (idx >= pairs * rows || c >= dp) return;
-  const int64_t pair = idx / rows, row = idx - pair * rows;
-  const int b = (int)(pair / hkv), hk = (int)(pair - (int64_t)b * hkv);
+  if (idx >= n || c >= J.dp) return;
+  const int64_t pair = idx / J.rows, row = idx - pair * J.rows;
+  const int b = (int)(pair / all.hkv), hk = (int)(pair - (int64_t)b * all.hkv);
   f32x4 x = {0, 0, 0, 0};
-  for (int s = 0; s < nsplit; ++s) {
-    const f32x4 v = *(const f32x4*)(part + (s * pairs * rows + idx) * dp + c);
+  for (int s = 0; s < J.nsplit; ++s) {
+    const f32x4 v = *(const f32x4*)(J.part + (s * n + idx) * J.dp + c);
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] += v[e];
   }
-  const int64_t qi = row / group;
-  const int qh = hk * group + (int)(row - qi * group);
-  T* orow = out + b * s0 + qi * s1 + qh * s2;
-  if (vec)
-    store4<T, true>(orow, c, d, x);
+  const int64_t qi = row / J.group;
+  const int qh = hk * J.group + (int)(row - qi * J.group);
+  T* orow = (T*)J.out + b * J.s[0] + qi * J.s[1] + qh * J.s[2];
+  if (J.vec)
+    store4<T, true>(orow, c, J.d, x);
   else
-    store4<T, false>(orow, c, d, x);
+    store4<T, false>(orow, c, J.d, x);
 }
 
 template <class T, int DP>
@@ -346,16 +360,26 @@ void attend_grad(const GradArgs& A, hipStream_t st) {
     grad_launch<T, 128>(A, st);
   else
     grad_launch<T, 64>(A, st);
+  GradJoins all{};
+  all.pairs = pairs;
+  all.hkv = A.S.hkv;
+  unsigned n = 0;
+  int64_t most = 0;
   auto join = [&](const float* part, int nsplit, int64_t rows, int32_t dp, int32_t group, void* out, const int64_t* s,
                   int32_t d, bool vec) {
     if (!part || rows == 0) return;
-    hipLaunchKernelGGL((k_grad_join<T>), grid1((pairs * rows + 7) / 8, 256), dim3(256), 0, st, part, nsplit, pairs,
-                       rows, dp, A.S.hkv, group, (T*)out, s[0], s[1], s[2], d, vec);
-    SK_LAUNCH_CHECK();
+    all.g[n++] = GradJoin{part, rows, nsplit, dp, group, d, out, {s[0], s[1], s[2]}, vec};
+    most = rows > most ? rows : most;
   };
   join(A.part_q, A.split_q, A.S.rows, A.dp, A.S.group, A.dq, A.dqs, A.S.d, A.vec_q);
   join(A.part_k, A.split_kv, A.S.lk, A.dp, 1, A.dk, A.dks, A.S.d, A.vec_k);
   join(A.part_v, A.split_kv, A.S.lk, A.dvp, 1, A.dv, A.dvs, A.S.dv, A.vec_v);
+  if (n > 0) {
+    dim3 grid = grid1((pairs * most + 7) / 8, 256);
+    grid.y = n;
+    hipLaunchKernelGGL((k_grad_join<T>), grid, dim3(256), 0, st, all);
+    SK_LAUNCH_CHECK();
+  }
 }
 
 }  // namespace attn

@@ -250,17 +250,21 @@ __device__ __forceinline__ void dma_wait() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Loader of ROWS rows by the workgroup's NT threads. `wave` must be uniform.
+// Loader of ROWS rows by the workgroup's NT threads: instructions of 1 KB, the
+// waves in turn. `wave` must be uniform.
 template <class T, int DP, int ROWS, int NT, bool ONCE = false>
 struct Loader {
   using TL = Tile<T, DP>;
-  static constexpr int N = ROWS * TL::CPR / NT;  // chunks per thread
-  static constexpr int RPI = 64 / TL::CPR;       // rows per instruction of a wave
-  static_assert(N * NT == ROWS * TL::CPR && N >= 1 && RPI >= 1, "tile and workgroup sizes");
+  static constexpr int TOTAL = ROWS * TL::CPR / 64;        // instructions
+  static constexpr int NW = NT / 64;                       // waves
+  static constexpr int N = (TOTAL + NW - 1) / NW;          // instructions of a wave at most
+  static constexpr int RPI = 64 / TL::CPR;                 // rows per instruction
+  static_assert(TOTAL * 64 == ROWS * TL::CPR && RPI >= 1, "whole instructions");
   uint32_t off[N];  // byte offset of this lane's chunk from the tile's start
 
   // tile row of this lane's chunk n
-  __device__ __forceinline__ static int row(int n, int wave, int lane) { return (wave * N + n) * RPI + lane / TL::CPR; }
+  __device__ __forceinline__ static int row(int n, int wave, int lane) { return (n * NW + wave) * RPI + lane / TL::CPR; }
+  __device__ __forceinline__ static bool has(int n, int wave) { return TOTAL % NW == 0 || n * NW + wave < TOTAL; }
 
   // at(r): byte offset of row r of the tile
   template <class F>
@@ -276,9 +280,10 @@ struct Loader {
   template <class F>
   __device__ __forceinline__ void start(const T* base, char* t, F&& live, int wave, int lane) const {
     const __amdgpu_buffer_rsrc_t rsrc = dma_rsrc(base);
-    const uint32_t lds = lds_offset(t) + wave * (N * 1024);
+    const uint32_t lds = lds_offset(t) + wave * 1024;
 #pragma unroll
-    for (int n = 0; n < N; ++n) dma_load<16, ONCE>(rsrc, lds + n * 1024, live(row(n, wave, lane)) ? off[n] : kOutside);
+    for (int n = 0; n < N; ++n)
+      if (has(n, wave)) dma_load<16, ONCE>(rsrc, lds + n * NW * 1024, live(row(n, wave, lane)) ? off[n] : kOutside);
   }
 };
 
@@ -369,6 +374,7 @@ struct KeyTiles {
   using Ld = Loader<T, DP, KT, NT, ONCE>;
   static constexpr int kTileBytes = KT * Tile<T, DP>::RB;
   static constexpr int kOps = 2 * Ld::N;  // loads of a wave per tile
+  static_assert(D == 2 || Ld::TOTAL % Ld::NW == 0, "counted loads: the same of every wave");
   struct Shared {
     __attribute__((aligned(16))) char tiles[D][2][kTileBytes];
     __attribute__((aligned(16))) float term[D][KT], raw[D][KT];

@@ -2,6 +2,7 @@
 // workspaces. The kernels are in attend.h (forward), attend_grad.h (backward)
 // and attend_mass.h (gathered weight), instantiated per element type.
 #include <algorithm>
+#include <initializer_list>
 
 #include "attend.h"
 #include "attend_grad.h"
@@ -292,45 +293,78 @@ WeightPlan plan_mass(const sinkhorn_attention* a, const void* q, const void* k) 
 }
 
 // ---------------------------------------------------------------- copies
-// One 16-byte chunk of a copy per thread.
+struct Copy {
+  const void* src;
+  int64_t stride[3];
+  int64_t len, total;  // rows of a batch entry, 16-byte chunks of the copy
+  int32_t heads, d, chunks;
+  u32x4* dst;
+};
+struct Copies {
+  Copy c[4];
+};
+
+// One 16-byte chunk of a copy per thread; blockIdx.y: the operand.
 template <class U>
-__global__ __launch_bounds__(256) void k_copy_rows(const U* src, int64_t s0, int64_t s1, int64_t s2, int64_t len,
-                                                   int32_t heads, int32_t d, int32_t chunks, int64_t total, u32x4* dst) {
+__global__ __launch_bounds__(256) void k_copy_rows(Copies all) {
+  const Copy& o = all.c[blockIdx.y];
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= total) return;
+  if (i >= o.total) return;
   constexpr int EPC = 16 / (int)sizeof(U);
-  const int64_t row = i / chunks;
-  const int c = (int)(i - row * chunks) * EPC;
-  const int64_t bl = row / heads, b = bl / len;
-  const U* p = src + b * s0 + (bl - b * len) * s1 + (row - bl * heads) * s2;
+  const int64_t row = i / o.chunks;
+  const int c = (int)(i - row * o.chunks) * EPC;
+  const int64_t bl = row / o.heads, b = bl / o.len;
+  const U* p = (const U*)o.src + b * o.stride[0] + (bl - b * o.len) * o.stride[1] + (row - bl * o.heads) * o.stride[2];
   union {
     U e[EPC];
     u32x4 u;
   } x;
 #pragma unroll
-  for (int e = 0; e < EPC; ++e) x.e[e] = c + e < d ? p[c + e] : (U)0;
-  dst[i] = x.u;
+  for (int e = 0; e < EPC; ++e) x.e[e] = c + e < o.d ? p[c + e] : (U)0;
+  o.dst[i] = x.u;
 }
 
-// The operand as the kernels read it: its address and strides, after the copy
-// if it needs one.
-const void* place(const sinkhorn_attention* a, const Operand& o, char* ws, int64_t* stride, hipStream_t st) {
-  for (int i = 0; i < 3; ++i) stride[i] = o.stride[i];
-  if (!o.copy || o.len == 0) return o.p;
+// The operands as the kernels read them: addresses and strides, after the
+// copies that they need (in one launch).
+struct Placed {
+  const Operand* o;
+  const void** p;
+  int64_t* stride;
+};
+
+void place(const sinkhorn_attention* a, std::initializer_list<Placed> operands, char* ws, hipStream_t st) {
   const int64_t size = elem_size(a);
-  const int32_t chunks = (int32_t)(o.dp * size / 16);
-  const int64_t total = a->batch * o.len * o.heads * chunks;
+  Copies all{};
+  unsigned n = 0;
+  int64_t most = 0;
+  for (const Placed& x : operands) {
+    const Operand& o = *x.o;
+    *x.p = o.p;
+    for (int i = 0; i < 3; ++i) x.stride[i] = o.stride[i];
+    if (!o.copy || o.len == 0) continue;
+    Copy& c = all.c[n++];
+    c.src = o.p;
+    for (int i = 0; i < 3; ++i) c.stride[i] = o.stride[i];
+    c.len = o.len;
+    c.heads = o.heads;
+    c.d = o.d;
+    c.chunks = (int32_t)(o.dp * size / 16);
+    c.total = a->batch * o.len * o.heads * c.chunks;
+    c.dst = (u32x4*)(ws + o.at);
+    most = std::max(most, c.total);
+    *x.p = ws + o.at;
+    x.stride[0] = o.len * o.heads * o.dp;
+    x.stride[1] = (int64_t)o.heads * o.dp;
+    x.stride[2] = o.dp;
+  }
+  if (n == 0) return;
+  dim3 grid = grid1(ceil_div(most, 256), 256);
+  grid.y = n;
   if (size == 4)
-    hipLaunchKernelGGL((k_copy_rows<uint32_t>), grid1(ceil_div(total, 256), 256), dim3(256), 0, st, (const uint32_t*)o.p,
-                       o.stride[0], o.stride[1], o.stride[2], o.len, o.heads, o.d, chunks, total, (u32x4*)(ws + o.at));
+    hipLaunchKernelGGL((k_copy_rows<uint32_t>), grid, dim3(256), 0, st, all);
   else
-    hipLaunchKernelGGL((k_copy_rows<uint16_t>), grid1(ceil_div(total, 256), 256), dim3(256), 0, st, (const uint16_t*)o.p,
-                       o.stride[0], o.stride[1], o.stride[2], o.len, o.heads, o.d, chunks, total, (u32x4*)(ws + o.at));
+    hipLaunchKernelGGL((k_copy_rows<uint16_t>), grid, dim3(256), 0, st, all);
   SK_LAUNCH_CHECK();
-  stride[0] = o.len * o.heads * o.dp;
-  stride[1] = (int64_t)o.heads * o.dp;
-  stride[2] = o.dp;
-  return ws + o.at;
 }
 
 void check_workspace(const void* ws, int64_t have, int64_t need) {
@@ -439,11 +473,7 @@ int sinkhorn_cross_attention(const sinkhorn_attention* a, const void* q, const v
     char* ws = (char*)workspace;
     AttendArgs A{};
     A.S = make_shape(a);
-    if (rows) {
-      A.S.q = place(a, p.q, ws, A.S.qs, st);
-      A.S.k = place(a, p.k, ws, A.S.ks, st);
-      A.S.v = place(a, p.v, ws, A.S.vs, st);
-    }
+    if (rows) place(a, {{&p.q, &A.S.q, A.S.qs}, {&p.k, &A.S.k, A.S.ks}, {&p.v, &A.S.v, A.S.vs}}, ws, st);
     copy3(A.os, a->out_stride);
     A.out = out;
     A.lse = lse;
@@ -515,10 +545,8 @@ int sinkhorn_cross_attention_grad(const sinkhorn_attention* a, const void* q, co
     copy3(A.os, a->out_stride);
     copy3(A.dos, a->dout_stride);
     if (rows && keys) {
-      A.S.q = place(a, p.q, ws, A.S.qs, st);
-      A.S.k = place(a, p.k, ws, A.S.ks, st);
-      A.S.v = place(a, p.v, ws, A.S.vs, st);
-      A.dout = place(a, p.dout, ws, A.dos, st);
+      place(a, {{&p.q, &A.S.q, A.S.qs}, {&p.k, &A.S.k, A.S.ks}, {&p.v, &A.S.v, A.S.vs}, {&p.dout, &A.dout, A.dos}}, ws,
+            st);
     } else {
       A.dout = dout;  // only its products with out, which is 0
     }
@@ -571,10 +599,7 @@ int sinkhorn_attention_mass(const sinkhorn_attention* a, const void* q, const vo
     char* ws = (char*)workspace;
     MassArgs M{};
     M.S = make_shape(a);
-    if (a->len_q > 0) {
-      M.S.q = place(a, p.q, ws, M.S.qs, st);
-      M.S.k = place(a, p.k, ws, M.S.ks, st);
-    }
+    if (a->len_q > 0) place(a, {{&p.q, &M.S.q, M.S.qs}, {&p.k, &M.S.k, M.S.ks}}, ws, st);
     M.lse = lse;
     M.weight = row_weight;
     M.mass_in = mass_in;

@@ -125,7 +125,7 @@ def test_wide_heads_are_unsupported():
 
 def test_null_pointers_aliases_and_workspaces():
     L = sk.lib()
-    a = _desc()
+    a = _desc(len_k=1 << 16)
     assert _forward(None) == sk.ERR_INVALID_ARG
     for kw in (dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(lse=None), dict(out=FAKE), dict(mi=FAKE),
                dict(w=FAKE)):
@@ -139,7 +139,7 @@ def test_null_pointers_aliases_and_workspaces():
     assert need.value > 0  # few rows against many keys: split
     odd = ctypes.c_int64()
     assert L.sinkhorn_attention_workspace(ctypes.byref(a), 0, FAKE, ctypes.c_void_p(258), FAKE, None, ctypes.byref(odd)) == sk.OK
-    assert odd.value == need.value + 2 * 2 * 1000 * 2 * 64  # a copy of k
+    assert odd.value == need.value + 2 * 2 * (1 << 16) * 2 * 64  # a copy of k
     for ws, n in ((None, 0), (FAKE, need.value - 1), (ctypes.c_void_p(264), need.value)):
         assert _forward(a, ws=ws, n=n) == sk.ERR_INVALID_ARG
         assert b"workspace" in L.sinkhorn_last_error()

@@ -12,6 +12,8 @@
 // k_grad_join adds in a fixed order.
 #pragma once
 
+#include <type_traits>
+
 #include "attention.h"
 
 namespace sk {
@@ -26,7 +28,7 @@ struct GradArgs {
   void* dq;
   void* dk;
   void* dv;
-  f32x2* stat;       // [batch * hkv][rows_pad]: lse (+inf: the row takes no part), D
+  f32x2* stat;       // [batch * hkv][rows_pad]: minus lse (-inf: the row takes no part), D
   int64_t rows_pad;  // rows rounded up to 64
   float* part_q;  // [split][batch * hkv][rows][dp], nullable
   float* part_k;  // [split][batch * hkv][lk][dp], nullable
@@ -51,7 +53,7 @@ __global__ __launch_bounds__(256) void k_grad_stat(GradArgs A) {
   const int qh = hk * S.group + (int)(row - qi * S.group);
   const int ln = threadIdx.x & 15;
   if (row >= live_rows(S, b)) {
-    if (ln == 0) A.stat[idx] = f32x2{kInf, 0.0f};
+    if (ln == 0) A.stat[idx] = f32x2{-kInf, 0.0f};
     return;
   }
   const T* o = (const T*)A.out + b * A.os[0] + qi * A.os[1] + qh * A.os[2];
@@ -76,17 +78,18 @@ __global__ __launch_bounds__(256) void k_grad_stat(GradArgs A) {
   for (int x = 8; x > 0; x >>= 1) s += __shfl_xor(s, x, 16);
   if (ln == 0) {
     const float e = A.lse[((int64_t)b * S.hq + qh) * S.lq + qi];
-    A.stat[idx] = e == -kInf ? f32x2{kInf, 0.0f} : f32x2{sizeof(T) == 4 ? e : e * (float)kLog2e, s};
+    A.stat[idx] = e == -kInf ? f32x2{-kInf, 0.0f} : f32x2{sizeof(T) == 4 ? -e : -e * (float)kLog2e, s};
   }
 }
 
-// exp(score - lse) of a product x, its column term and the row's lse.
-template <class T>
-__device__ __forceinline__ float weight(const Shape& S, float x, float term, float lse) {
+// exp(score - lse) of a product x, its column term (if it has one) and minus the
+// row's lse.
+template <class T, bool TERM>
+__device__ __forceinline__ float weight(const Shape& S, float x, float term, float minus) {
   if constexpr (sizeof(T) == 4)
-    return ex2((fmaf(x, S.scale, fmaf(x, S.scale_lo, term)) - lse) * (float)kLog2e);
+    return ex2((fmaf(x, S.scale, fmaf(x, S.scale_lo, term)) + minus) * (float)kLog2e);
   else
-    return ex2(fmaf(x, S.c, term - lse));
+    return ex2(fmaf(x, S.c, TERM ? term + minus : minus));
 }
 
 // Writes a transposed result (column: row `row` of the output, down: its
@@ -153,7 +156,7 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
       gf[s] = global_frag<T>(grow, live_row && t0 < t1, s, h, S.dv);
     }
   }
-  const f32x2 st = live_row ? A.stat[pair * A.rows_pad + row] : f32x2{kInf, 0.0f};
+  const f32x2 st = live_row ? A.stat[pair * A.rows_pad + row] : f32x2{-kInf, 0.0f};
   f32x16 dq[NDB];
 #pragma unroll
   for (int n = 0; n < NDB; ++n) dq[n] = zero16();
@@ -163,6 +166,7 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
     const char* const tk = keys.ktile(it);
     const char* const tv = keys.vtile(it);
     const float* const term = keys.term(it);
+    const bool masked = keys.masked(it);
 #pragma unroll
     for (int n = 0; n < KT / 32; ++n) {
       f32x16 p = zero16(), g = zero16();
@@ -170,15 +174,22 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
       for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tk, 32 * n + r32, s, h), qf[s], p);
 #pragma unroll
       for (int s = 0; s < NS; ++s) g = mma(TL::row_frag(tv, 32 * n + r32, s, h), gf[s], g);
+      auto weights = [&](auto terms) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x4 ct = *(const f32x4*)&term[32 * n + 8 * q + 4 * h];
+        for (int q = 0; q < 4; ++q) {
+          f32x4 ct = {0, 0, 0, 0};
+          if constexpr (decltype(terms)::value) ct = *(const f32x4*)&term[32 * n + 8 * q + 4 * h];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 4 * q + e;
-          p[i] = weight<T>(S, p[i], ct[e], st[0]) * (g[i] - st[1]);
+          for (int e = 0; e < 4; ++e) {
+            const int i = 4 * q + e;
+            p[i] = weight<T, decltype(terms)::value>(S, p[i], ct[e], st[0]) * (g[i] - st[1]);
+          }
         }
-      }
+      };
+      if (masked)
+        weights(std::true_type{});
+      else
+        weights(std::false_type{});
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const V8 ds = pack<T>(p, s);
@@ -193,15 +204,26 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
   write_cols<T, NDB>(dq, S.scale, prow, A.dp, orow, S.d, A.vec_q, h);
 }
 
-// dK and dV: 4 waves of 32 keys, tiles of RT rows in two LDS buffers.
-template <class T, int DP>
-__global__ __launch_bounds__(256, sizeof(T) * DP <= 128 ? 2 : 1) void k_grad_kv(GradArgs A) {
+// dK and dV of 128 keys. Waves work in pairs on the same 32 keys: the first
+// computes S and the weights P and accumulates dV = P^T dout, the second computes
+// dout V^T and dS and accumulates dK = dS^T Q one tile of rows later, from the P
+// that its partner left in LDS (fp32, each lane's own registers). Either holds half of
+// the operands and accumulators, so two waves (and for 64 columns of 16 bits
+// four) fit a SIMD, whose matrix and vector work then overlap; one wave doing all
+// needs more than 256 registers at 128 columns and a SIMD to itself (4096 x
+// 8192 x 32 heads, bf16: 3.4 ms). Tiles of 32 rows in a ring of four: the
+// second wave's, the first's, and two being loaded (a tile is computed on in
+// less time than memory takes to answer).
+template <class T, int DP, int OCC>
+__global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
-  constexpr int RT = sizeof(T) * DP <= 256 ? 64 : 32, NT = 256, NS = DP / 16, NDB = DP / 32;
+  constexpr int RT = 32, NT = 512, NS = DP / 16, NDB = DP / 32;
+  constexpr int RING = sizeof(T) * DP > 256 ? 3 : 4;  // fp32 of 128 columns: no room for a fourth
   constexpr int kTileBytes = RT * TL::RB;
-  __shared__ __attribute__((aligned(16))) char sm[4 * kTileBytes];
-  __shared__ __attribute__((aligned(16))) f32x2 sstat[2][RT];
+  __shared__ __attribute__((aligned(16))) char sm[RING][2][kTileBytes];  // q, dout
+  __shared__ __attribute__((aligned(16))) f32x4 sp[2][4][4][64];      // P: [buffer][pair][registers][lane]
+  __shared__ __attribute__((aligned(16))) f32x2 sstat[RING][RT];
 
   const Shape& S = A.S;
   const int64_t pairs = (int64_t)S.batch * S.hkv;
@@ -214,85 +236,119 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 128 ? 2 : 1) void k_grad_kv(
   const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r32 = lane & 31;
+  const int wp = wave & 3;
+  const bool first = wave < 4;  // of its pair (waves w and w + 4 run on the same SIMD)
 
   const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
-  const int64_t key0 = tile * 128, key = key0 + 32 * wave + r32;
+  const int64_t key0 = tile * 128, key = key0 + 32 * wp + r32;
   const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
   const float term = column_term(bias, key, nkeys, sizeof(T) == 4 ? 1.0f : (float)kLog2e);
   const int64_t ntiles = key0 < nkeys ? (nrows + RT - 1) / RT : 0;
   const int64_t per = (ntiles + A.split_kv - 1) / A.split_kv;
   const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
+  const int count = t1 > t0 ? (int)(t1 - t0) : 0;
 
   RowTiles<T, DP, RT, NT> rq(S, S.q, S.qs, b, hk, S.d, wave, lane), rg(S, A.dout, A.dos, b, hk, S.dv, wave, lane);
-  auto start = [&](int64_t t) {
-    const int buf = (int)(t - t0) & 1;
-    rq.start(S, t, nrows, sm + buf * 2 * kTileBytes, wave, lane);
-    rg.start(S, t, nrows, sm + buf * 2 * kTileBytes + kTileBytes, wave, lane);
-    // RT * 8 bytes of statistics (rows_pad covers the tile), 256 a wave
-    if (wave < RT / 32)
-      dma_load<4>(dma_rsrc(A.stat + pair * A.rows_pad + t * RT), lds_offset(sstat[buf]) + wave * 256, wave * 256 + 4 * lane);
+  auto start = [&](int n) {
+    if (n >= count) return;
+    const int buf = n % RING;
+    rq.start(S, t0 + n, nrows, sm[buf][0], wave, lane);
+    rg.start(S, t0 + n, nrows, sm[buf][1], wave, lane);
+    // 32 rows of statistics, 8 bytes each (rows_pad covers the tile)
+    if (wave == 7) dma_load<4>(dma_rsrc(A.stat + pair * A.rows_pad + (t0 + n) * RT), lds_offset(sstat[buf]), 4 * lane);
   };
-  if (t0 < t1) start(t0);
-
-  V8 kf[NS], vf[NS];
+  using Ld = Loader<T, DP, RT, NT>;
+  V8 fr[NS];  // the keys' rows of k (first) or v (second)
   {
-    const T* krow = (const T*)S.k + b * S.ks[0] + key * S.ks[1] + hk * S.ks[2];
-    const T* vrow = (const T*)S.v + b * S.vs[0] + key * S.vs[1] + hk * S.vs[2];
-    const bool live = term != -kInf && t0 < t1;  // no rows: nothing to read them for
+    const T* row = first ? (const T*)S.k + b * S.ks[0] + key * S.ks[1] + hk * S.ks[2]
+                         : (const T*)S.v + b * S.vs[0] + key * S.vs[1] + hk * S.vs[2];
+    const bool live = term != -kInf && count > 0;  // no rows: nothing to read them for
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      kf[s] = global_frag<T>(krow, live, s, h, S.d);
-      vf[s] = global_frag<T>(vrow, live, s, h, S.dv);
-    }
+    for (int s = 0; s < NS; ++s) fr[s] = global_frag<T>(row, live, s, h, first ? S.d : S.dv);
   }
-  f32x16 dk[NDB], dv[NDB];
+  start(0);
+  if constexpr (RING > 3) start(1);
+  f32x16 acc[NDB];  // dV (first) or dK (second), transposed
 #pragma unroll
-  for (int n = 0; n < NDB; ++n) {
-    dk[n] = zero16();
-    dv[n] = zero16();
-  }
-  for (int64_t t = t0; t < t1; ++t) {
-    const int buf = (int)(t - t0) & 1;
-    dma_wait<0>();
+  for (int n = 0; n < NDB; ++n) acc[n] = zero16();
+
+  for (int it = 0; it <= count; ++it) {
+    // tile it has to be there; a wave's loads of tile it + 1 may be on their way
+    if (RING > 3 && it + 1 < count && Ld::has(Ld::N - 1, wave))
+      dma_wait<2 * Ld::N>();
+    else
+      dma_wait<0>();
     __syncthreads();
-    if (t + 1 < t1) start(t + 1);
-    const char* tq = sm + buf * 2 * kTileBytes;
-    const char* tg = tq + kTileBytes;
+    start(it + RING - 2);
+    if (first) {
+      if (it == count) break;  // no barrier follows
+      const char* const tq = sm[it % RING][0];
+      const char* const tg = sm[it % RING][1];
+      const f32x2* const stat = sstat[it % RING];
+      f32x16 p = zero16();
 #pragma unroll
-    for (int n = 0; n < RT / 32; ++n) {
-      f32x16 p = zero16(), g = zero16();
+      for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tq, r32, s, h), fr[s], p);
+      auto weights = [&](auto biased) {
 #pragma unroll
-      for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tq, 32 * n + r32, s, h), kf[s], p);
+        for (int q = 0; q < 8; ++q) {
+          const f32x4 w = *(const f32x4*)&stat[8 * (q >> 1) + 4 * h + 2 * (q & 1)];  // two rows: {-lse, D, -lse, D}
+          p[2 * q] = weight<T, decltype(biased)::value>(S, p[2 * q], term, w[0]);
+          p[2 * q + 1] = weight<T, decltype(biased)::value>(S, p[2 * q + 1], term, w[2]);
+        }
+      };
+      // without a bias the column term is 0 for every live key; what a key
+      // behind the sequence gathers is dropped below
+      if (bias)
+        weights(std::true_type{});
+      else
+        weights(std::false_type{});
 #pragma unroll
-      for (int s = 0; s < NS; ++s) g = mma(TL::row_frag(tg, 32 * n + r32, s, h), vf[s], g);
+      for (int q = 0; q < 4; ++q) sp[it & 1][wp][q][lane] = f32x4{p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]};
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        // two rows: {lse, D, lse, D}
-        const f32x4 w = *(const f32x4*)&sstat[buf][32 * n + 8 * (q >> 1) + 4 * h + 2 * (q & 1)];
+      for (int s = 0; s < 2; ++s) {
+        const V8 pw = pack<T>(p, s);
+#pragma unroll
+        for (int x = 0; x < NDB; ++x) acc[x] = mma(TL::col_frag(tg, 16 * s, 32 * x, lane), pw, acc[x]);
+      }
+    } else if (it > 0) {
+      const int last = it - 1;
+      const char* const tq = sm[last % RING][0];
+      const char* const tg = sm[last % RING][1];
+      const f32x2* const stat = sstat[last % RING];
+      f32x16 g = zero16();
+#pragma unroll
+      for (int s = 0; s < NS; ++s) g = mma(TL::row_frag(tg, r32, s, h), fr[s], g);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 p = sp[last & 1][wp][q][lane];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int i = 2 * q + e;
-          p[i] = weight<T>(S, p[i], term, w[2 * e]);
-          g[i] = p[i] * (g[i] - w[2 * e + 1]);
+          const f32x4 w = *(const f32x4*)&stat[8 * q + 4 * h + 2 * e];
+          g[4 * q + 2 * e] = p[2 * e] * (g[4 * q + 2 * e] - w[1]);
+          g[4 * q + 2 * e + 1] = p[2 * e + 1] * (g[4 * q + 2 * e + 1] - w[3]);
         }
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const V8 pw = pack<T>(p, s), ds = pack<T>(g, s);
+        const V8 ds = pack<T>(g, s);
 #pragma unroll
-        for (int x = 0; x < NDB; ++x) {
-          dv[x] = mma(TL::col_frag(tg, 32 * n + 16 * s, 32 * x, lane), pw, dv[x]);
-          dk[x] = mma(TL::col_frag(tq, 32 * n + 16 * s, 32 * x, lane), ds, dk[x]);
-        }
+        for (int x = 0; x < NDB; ++x) acc[x] = mma(TL::col_frag(tq, 16 * s, 32 * x, lane), ds, acc[x]);
       }
     }
   }
   if (key >= S.lk) return;
+  if (term == -kInf) {
+#pragma unroll
+    for (int n = 0; n < NDB; ++n) acc[n] = zero16();
+  }
   const int64_t pi = ((int64_t)split * pairs + pair) * S.lk + key;
-  T* dkrow = (T*)A.dk + b * A.dks[0] + key * A.dks[1] + hk * A.dks[2];
-  T* dvrow = (T*)A.dv + b * A.dvs[0] + key * A.dvs[1] + hk * A.dvs[2];
-  write_cols<T, NDB>(dk, S.scale, A.part_k ? A.part_k + pi * A.dp : nullptr, A.dp, dkrow, S.d, A.vec_k, h);
-  write_cols<T, NDB>(dv, 1.0f, A.part_v ? A.part_v + pi * A.dvp : nullptr, A.dvp, dvrow, S.dv, A.vec_v, h);
+  if (first) {
+    T* row = (T*)A.dv + b * A.dvs[0] + key * A.dvs[1] + hk * A.dvs[2];
+    write_cols<T, NDB>(acc, 1.0f, A.part_v ? A.part_v + pi * A.dvp : nullptr, A.dvp, row, S.dv, A.vec_v, h);
+  } else {
+    T* row = (T*)A.dk + b * A.dks[0] + key * A.dks[1] + hk * A.dks[2];
+    write_cols<T, NDB>(acc, S.scale, A.part_k ? A.part_k + pi * A.dp : nullptr, A.dp, row, S.d, A.vec_k, h);
+  }
 }
 
 // Adds the partial sums of a gradient in split order: 32 lanes per row. Rows of
@@ -343,7 +399,8 @@ void grad_launch(const GradArgs& A, hipStream_t st) {
     SK_LAUNCH_CHECK();
   }
   if (A.S.lk > 0) {
-    hipLaunchKernelGGL((k_grad_kv<T, DP>), grid1(xcd_blocks(pairs * A.tiles_kv * A.split_kv), 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_grad_kv<T, DP, (DP * sizeof(T) == 128 ? 4 : 2)>),
+                       grid1(xcd_blocks(pairs * A.tiles_kv * A.split_kv), 512), dim3(512), 0, st, A);
     SK_LAUNCH_CHECK();
   }
 }

@@ -11,6 +11,8 @@
 // memory, by the forward pass.
 #pragma once
 
+#include <type_traits>
+
 #include "attention.h"
 
 namespace sk {
@@ -78,10 +80,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A
   const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
 
   RowTiles<T, DP, RT, NT> rows(S, S.q, S.qs, b, hk, S.d, wave, lane);
-  f32x2 st = {kInf, 0.0f};
+  f32x2 st = {-kInf, 0.0f};  // of row tid: minus its lse, and its weight
   auto start = [&](int64_t t) { rows.start(S, t, nrows, sm + ((t - t0) & 1) * kTileBytes, wave, lane); };
   auto stat = [&](int64_t t) {
-    if (tid < RT) st = mass_row(A, b, hk, t * RT + tid, nrows, kExact);
+    if (tid < RT) {
+      st = mass_row(A, b, hk, t * RT + tid, nrows, kExact);
+      st[0] = -st[0];
+    }
   };
   if (t0 < t1) {
     start(t0);
@@ -106,26 +111,36 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A
       if (t + 2 < t1) stat(t + 2);
     }
     const char* tq = sm + buf * kTileBytes;
+    // without a bias the column term is 0 for every live key
+    auto tile = [&](auto biased) {
 #pragma unroll
-    for (int n = 0; n < RT / 32; ++n) {
-      f32x16 p = zero16();
+      for (int n = 0; n < RT / 32; ++n) {
+        f32x16 p = zero16();
 #pragma unroll
-      for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tq, 32 * n + r32, s, h), kf[s], p);
+        for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tq, 32 * n + r32, s, h), kf[s], p);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        // two rows: {lse, weight, lse, weight}
-        const f32x4 w = *(const f32x4*)&sstat[buf][32 * n + 8 * (q >> 1) + 4 * h + 2 * (q & 1)];
+        for (int q = 0; q < 8; ++q) {
+          // two rows: {-lse, weight, -lse, weight}
+          const f32x4 w = *(const f32x4*)&sstat[buf][32 * n + 8 * (q >> 1) + 4 * h + 2 * (q & 1)];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = p[2 * q + e];
-          const float a = kExact ? (fmaf(x, S.scale, fmaf(x, S.scale_lo, term)) - w[2 * e]) * (float)kLog2e
-                                 : fmaf(x, S.c, term - w[2 * e]);
-          sum = fmaf(w[2 * e + 1], ex2(a), sum);
+          for (int e = 0; e < 2; ++e) {
+            const float x = p[2 * q + e];
+            float a;
+            if constexpr (kExact)
+              a = (fmaf(x, S.scale, fmaf(x, S.scale_lo, term)) + w[2 * e]) * (float)kLog2e;
+            else
+              a = fmaf(x, S.c, decltype(biased)::value ? term + w[2 * e] : w[2 * e]);
+            sum = fmaf(w[2 * e + 1], ex2(a), sum);
+          }
         }
       }
-    }
+    };
+    if (bias)
+      tile(std::true_type{});
+    else
+      tile(std::false_type{});
   }
-  sum = half_sum(sum);
+  sum = term == -kInf ? 0.0f : half_sum(sum);
   if (h != 0 || key >= S.lk) return;
   if (A.part)
     A.part[((int64_t)split * pairs + pair) * S.lk + key] = sum;

@@ -3,13 +3,14 @@
 // of the rest, and move the kept rows of k, v and the weight to the front of
 // the output buffers in their order.
 //
-// k_evict_select (one workgroup per pair) finds the K-th largest weight by
+// k_evict_select (one workgroup per pair) finds the keep-th largest weight by
 // radix selection on the weights' bits taken as ordered integers (8 bits a
 // pass, counts in LDS: integer sums, so the result is exact and does not depend
 // on the order of threads), then writes the kept indices in order; keys that
-// equal the threshold are taken from the lowest index up. Each pass takes
-// 16384 keys at a time, 16 loads of a thread in flight: one load at a time, the
-// passes are bound by the latency of memory.
+// equal the threshold are taken from the lowest index up. Keys that are kept
+// in any case count as the highest. Up to 65536 keys stay in registers as such
+// integers over the passes; reading and converting them in each pass took 104 us
+// in place of 2x us at 65536 keys.
 // k_evict_move copies the rows. The copy is bound by memory.
 #include "attention.h"
 
@@ -34,8 +35,11 @@ struct EvictArgs {
 };
 
 constexpr int kSelThreads = 1024;
-constexpr int kSelPer = 16;  // keys of a thread in flight
+constexpr int kSelPer = 16;  // keys of a thread in a chunk
 constexpr int kSelChunk = kSelThreads * kSelPer;
+// Copies of the counts, by lane: equal weights (keys that gathered none) would
+// otherwise make a wave's additions to one counter wait for each other.
+constexpr int kCopies = 8;
 
 __device__ __forceinline__ int64_t evict_len(const EvictArgs& A, int b) {
   if (!A.klen) return A.len;
@@ -43,105 +47,126 @@ __device__ __forceinline__ int64_t evict_len(const EvictArgs& A, int b) {
   return n < 0 ? 0 : (n > A.len ? A.len : n);
 }
 
-// Weights as ordered integers: a NaN is the lowest, -0 equals +0.
+// Weights as ordered integers: a NaN is the lowest, -0 equals +0. Values below
+// kLowest and above that of +infinity stand for no weight.
+constexpr uint32_t kNone = 0u, kLowest = 2u, kAlways = 0xffffffffu;
 __device__ __forceinline__ uint32_t order_key(float x) {
-  if (x != x) return 0u;
   const uint32_t u = __float_as_uint(x + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t v = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return x != x ? kLowest : v;
 }
 
+// C: chunks of keys held in registers; 0: any number, read in each pass.
+template <int C>
 __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
-  __shared__ uint32_t hist[256];
+  __shared__ uint32_t hist[256][kCopies];
   __shared__ uint32_t swave[2][kSelThreads / 64];
   __shared__ uint32_t sdigit, sbefore;
   const int64_t pair = blockIdx.x;
   const int b = (int)(pair / A.heads);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t n = evict_len(A, b);
-  const int64_t left = n < A.keep ? n : A.keep;
+  const int n = (int)evict_len(A, b);
+  const int keep = (int)(A.keep < A.len ? A.keep : A.len);
+  const int left = n < keep ? n : keep;
   const float* w = A.mass + pair * A.len;
   int32_t* idx = A.index_out + pair * A.cap;
   float* mo = A.mass_out + pair * A.cap;
-  if (tid == 0 && pair == (int64_t)b * A.heads) A.lengths_out[b] = (int32_t)left;
-  for (int64_t j = left + tid; j < A.cap; j += kSelThreads) {
+  if (tid == 0 && pair == (int64_t)b * A.heads) A.lengths_out[b] = left;
+  for (int j = left + tid; j < (int)A.cap; j += kSelThreads) {
     idx[j] = -1;
     mo[j] = 0.0f;
   }
-  if (n <= A.keep) {
-    for (int64_t j = tid; j < n; j += kSelThreads) {
-      idx[j] = (int32_t)j;
+  if (n <= keep) {
+    for (int j = tid; j < n; j += kSelThreads) {
+      idx[j] = j;
       mo[j] = w[j];
     }
     return;
   }
-  const int64_t lo = A.first, hi = n - A.recent;
-  uint32_t need = (uint32_t)(A.keep - A.first - A.recent);  // of the middle; < hi - lo
-  uint32_t prefix = 0, mask = 0;
-  if (need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int64_t j0 = lo; j0 < hi; j0 += kSelChunk) {
-        float x[kSelPer];
-        const int64_t j = j0 + tid;
-#pragma unroll
-        for (int i = 0; i < kSelPer; ++i) x[i] = j + i * kSelThreads < hi ? w[j + i * kSelThreads] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < kSelPer; ++i) {
-          const uint32_t u = order_key(x[i]);
-          if (j + i * kSelThreads < hi && (u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1u);
-        }
-      }
-      __syncthreads();
-      if (tid < 64) {
-        // four bins a lane from the top down: lane 0 holds bins 255 .. 252
-        uint32_t c[4], s = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          c[e] = hist[255 - 4 * tid - e];
-          s += c[e];
-        }
-        uint32_t inc = s;
-#pragma unroll
-        for (int x = 1; x < 64; x <<= 1) {
-          const uint32_t y = __shfl_up(inc, x);
-          if (lane >= x) inc += y;
-        }
-        uint32_t before = inc - s;  // keys in higher bins
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (before < need && need <= before + c[e]) {
-            sdigit = 255 - 4 * tid - e;
-            sbefore = before;
-          }
-          before += c[e];
-        }
-      }
-      __syncthreads();
-      prefix |= sdigit << shift;
-      mask |= 255u << shift;
-      need -= sbefore;
-    }
-  }
-  // keys above `prefix` are kept, and the first `need` of those equal to it.
-  // A wave takes 1024 consecutive keys of a chunk, 64 at a time.
-  const bool any = A.keep > A.first + A.recent;
-  uint32_t nsel = 0, neq = 0;  // kept for sure, and equal, before this chunk
-  for (int64_t j0 = 0; j0 < n; j0 += kSelChunk) {
-    const int64_t jw = j0 + wave * (64 * kSelPer) + lane;
+  const int lo = (int)A.first, hi = n - (int)A.recent;
+  // a wave's keys of a chunk: 1024 consecutive ones, 64 at a time
+  const int base = wave * (64 * kSelPer) + lane;
+  auto read = [&](int chunk, uint32_t (&u)[kSelPer]) {
+    const int j0 = chunk * kSelChunk + base;
     float x[kSelPer];
 #pragma unroll
-    for (int i = 0; i < kSelPer; ++i) x[i] = jw + 64 * i < n ? w[jw + 64 * i] : 0.0f;
+    for (int i = 0; i < kSelPer; ++i) x[i] = j0 + 64 * i < n ? w[j0 + 64 * i] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSelPer; ++i) {
+      const int j = j0 + 64 * i;
+      u[i] = j >= n ? kNone : (j < lo || j >= hi ? kAlways : order_key(x[i]));
+    }
+  };
+  const int chunks = (n - 1) / kSelChunk + 1;
+  uint32_t held[C > 0 ? C : 1][kSelPer];
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) read(c, held[c]);
+  }
+  // f(chunk, keys) for every chunk
+  auto each = [&](auto&& f) {
+    if constexpr (C > 0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (c < chunks) f(c, held[c]);
+    } else {
+      for (int c = 0; c < chunks; ++c) {
+        read(c, held[0]);
+        f(c, held[0]);
+      }
+    }
+  };
+  uint32_t need = (uint32_t)keep;  // of the keys that agree with `prefix` in the bits of `mask`; fewer than there are
+  uint32_t prefix = 0, mask = 0;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256 * kCopies; i += kSelThreads) ((uint32_t*)hist)[i] = 0;
+    __syncthreads();
+    each([&](int, const uint32_t (&u)[kSelPer]) {
+#pragma unroll
+      for (int i = 0; i < kSelPer; ++i)
+        if ((u[i] & mask) == prefix) atomicAdd(&hist[(u[i] >> shift) & 255u][lane % kCopies], 1u);
+    });
+    __syncthreads();
+    if (tid < 64) {
+      // four bins a lane from the top down: lane 0 holds bins 255 .. 252
+      uint32_t c[4], s = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c[e] = 0;
+#pragma unroll
+        for (int k = 0; k < kCopies; ++k) c[e] += hist[255 - 4 * tid - e][k];
+        s += c[e];
+      }
+      uint32_t inc = s;
+#pragma unroll
+      for (int x = 1; x < 64; x <<= 1) {
+        const uint32_t y = __shfl_up(inc, x);
+        if (lane >= x) inc += y;
+      }
+      uint32_t before = inc - s;  // keys in higher bins
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (before < need && need <= before + c[e]) {
+          sdigit = 255 - 4 * tid - e;
+          sbefore = before;
+        }
+        before += c[e];
+      }
+    }
+    __syncthreads();
+    prefix |= sdigit << shift;
+    mask |= 255u << shift;
+    need -= sbefore;
+  }
+  // keys above `prefix` are kept, and the first `need` of those equal to it
+  uint32_t nsel = 0, neq = 0;  // kept for sure, and equal, before this chunk
+  each([&](int chunk, const uint32_t (&u)[kSelPer]) {
     uint64_t sel[kSelPer], eq[kSelPer];
     uint32_t csel = 0, ceq = 0;
 #pragma unroll
     for (int i = 0; i < kSelPer; ++i) {
-      const int64_t j = jw + 64 * i;
-      const bool always = j < n && (j < lo || j >= hi);
-      const bool mid = j < n && !always && any;
-      const uint32_t u = order_key(x[i]);
-      sel[i] = __ballot(always || (mid && u > prefix));
-      eq[i] = __ballot(mid && u == prefix);
+      sel[i] = __ballot(u[i] > prefix);
+      eq[i] = __ballot(u[i] == prefix);
       csel += __popcll(sel[i]);
       ceq += __popcll(eq[i]);
     }
@@ -151,6 +176,7 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
     }
     __syncthreads();
     uint32_t s = nsel, q = neq;  // kept, and equal, before this wave's keys
+#pragma unroll
     for (int k = 0; k < kSelThreads / 64; ++k) {
       if (k < wave) {
         s += swave[0][k];
@@ -160,21 +186,22 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
       neq += swave[1][k];
     }
     const uint64_t below = (uint64_t(1) << lane) - 1;
+    const int j0 = chunk * kSelChunk + base;
 #pragma unroll
     for (int i = 0; i < kSelPer; ++i) {
       const uint32_t es = s + __popcll(sel[i] & below), ee = q + __popcll(eq[i] & below);
       if (((sel[i] >> lane) & 1) || (((eq[i] >> lane) & 1) && ee < need)) {
-        const int64_t pos = (int64_t)es + (ee < need ? ee : need);
-        if (pos < A.cap) {
-          idx[pos] = (int32_t)(jw + 64 * i);
-          mo[pos] = x[i];
+        const uint32_t pos = es + (ee < need ? ee : need);
+        if (pos < (uint32_t)keep) {
+          idx[pos] = j0 + 64 * i;
+          mo[pos] = w[j0 + 64 * i];
         }
       }
       s += __popcll(sel[i]);
       q += __popcll(eq[i]);
     }
     __syncthreads();
-  }
+  });
 }
 
 // Copies the kept rows: UNIT bytes a thread and step, 32 rows per workgroup.
@@ -282,7 +309,13 @@ extern "C" int sinkhorn_cache_evict(const sinkhorn_cache* c, const void* k, cons
     }
     const hipStream_t st = (hipStream_t)stream;
     const int64_t pairs = (int64_t)c->batch * c->heads;
-    hipLaunchKernelGGL(k_evict_select, grid1(pairs, kSelThreads), dim3(kSelThreads), 0, st, A);
+    const dim3 all = grid1(pairs, kSelThreads);
+    if (c->len <= kSelChunk)
+      hipLaunchKernelGGL((k_evict_select<1>), all, dim3(kSelThreads), 0, st, A);
+    else if (c->len <= 4 * kSelChunk)
+      hipLaunchKernelGGL((k_evict_select<4>), all, dim3(kSelThreads), 0, st, A);
+    else
+      hipLaunchKernelGGL((k_evict_select<0>), all, dim3(kSelThreads), 0, st, A);
     SK_LAUNCH_CHECK();
     if (A.cap == 0) return SINKHORN_OK;
     A.blocks_per_pair = (A.cap + 31) / 32;

@@ -101,6 +101,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
 #pragma unroll
     for (int s = 0; s < NS; ++s) qf[s] = global_frag<T>(qrow, live_row && t0 < t1, s, h, S.d);
   }
+  loads_done();
   f32x16 o[NDB];
 #pragma unroll
   for (int n = 0; n < NDB; ++n) o[n] = zero16();

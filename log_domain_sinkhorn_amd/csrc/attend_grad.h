@@ -157,6 +157,7 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
     }
   }
   const f32x2 st = live_row ? A.stat[pair * A.rows_pad + row] : f32x2{-kInf, 0.0f};
+  loads_done();
   f32x16 dq[NDB];
 #pragma unroll
   for (int n = 0; n < NDB; ++n) dq[n] = zero16();
@@ -248,16 +249,16 @@ __global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
   const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
   const int count = t1 > t0 ? (int)(t1 - t0) : 0;
 
-  RowTiles<T, DP, RT, NT> rq(S, S.q, S.qs, b, hk, S.d, wave, lane), rg(S, A.dout, A.dos, b, hk, S.dv, wave, lane);
+  RowTiles<T, DP, RT, NT> rq(S, S.q, S.qs, b, hk, S.d, t0, nrows, wave, lane),
+      rg(S, A.dout, A.dos, b, hk, S.dv, t0, nrows, wave, lane);
   auto start = [&](int n) {
     if (n >= count) return;
     const int buf = n % RING;
-    rq.start(S, t0 + n, nrows, sm[buf][0], wave, lane);
-    rg.start(S, t0 + n, nrows, sm[buf][1], wave, lane);
+    rq.start(S, sm[buf][0], wave, lane);
+    rg.start(S, sm[buf][1], wave, lane);
     // 32 rows of statistics, 8 bytes each (rows_pad covers the tile)
     if (wave == 7) dma_load<4>(dma_rsrc(A.stat + pair * A.rows_pad + (t0 + n) * RT), lds_offset(sstat[buf]), 4 * lane);
   };
-  using Ld = Loader<T, DP, RT, NT>;
   V8 fr[NS];  // the keys' rows of k (first) or v (second)
   {
     const T* row = first ? (const T*)S.k + b * S.ks[0] + key * S.ks[1] + hk * S.ks[2]
@@ -266,22 +267,28 @@ __global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) fr[s] = global_frag<T>(row, live, s, h, first ? S.d : S.dv);
   }
+  loads_done();
   start(0);
   if constexpr (RING > 3) start(1);
   f32x16 acc[NDB];  // dV (first) or dK (second), transposed
 #pragma unroll
   for (int n = 0; n < NDB; ++n) acc[n] = zero16();
 
-  for (int it = 0; it <= count; ++it) {
-    // tile it has to be there; a wave's loads of tile it + 1 may be on their way
+  using Ld = Loader<T, DP, RT, NT>;
+  // Makes tile `it` readable and the weights of tile it - 1, and starts a tile.
+  // Both kinds of wave call it once for each it = 0 .. count.
+  auto next = [&](int it) {
+    // a wave's loads of tile it + 1 may be on their way
     if (RING > 3 && it + 1 < count && Ld::has(Ld::N - 1, wave))
       dma_wait<2 * Ld::N>();
     else
       dma_wait<0>();
     __syncthreads();
     start(it + RING - 2);
-    if (first) {
-      if (it == count) break;  // no barrier follows
+  };
+  if (first) {
+    for (int it = 0; it < count; ++it) {
+      next(it);
       const char* const tq = sm[it % RING][0];
       const char* const tg = sm[it % RING][1];
       const f32x2* const stat = sstat[it % RING];
@@ -310,17 +317,21 @@ __global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
 #pragma unroll
         for (int x = 0; x < NDB; ++x) acc[x] = mma(TL::col_frag(tg, 16 * s, 32 * x, lane), pw, acc[x]);
       }
-    } else if (it > 0) {
-      const int last = it - 1;
-      const char* const tq = sm[last % RING][0];
-      const char* const tg = sm[last % RING][1];
-      const f32x2* const stat = sstat[last % RING];
+    }
+    next(count);
+  } else {
+    next(0);
+    for (int it = 0; it < count; ++it) {
+      next(it + 1);
+      const char* const tq = sm[it % RING][0];
+      const char* const tg = sm[it % RING][1];
+      const f32x2* const stat = sstat[it % RING];
       f32x16 g = zero16();
 #pragma unroll
       for (int s = 0; s < NS; ++s) g = mma(TL::row_frag(tg, r32, s, h), fr[s], g);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const f32x4 p = sp[last & 1][wp][q][lane];
+        const f32x4 p = sp[it & 1][wp][q][lane];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const f32x4 w = *(const f32x4*)&stat[8 * q + 4 * h + 2 * e];

@@ -38,8 +38,8 @@ struct MassArgs {
 __device__ __forceinline__ f32x2 mass_row(const MassArgs& A, int b, int hk, int64_t row, int64_t nrows, bool natural) {
   const Shape& S = A.S;
   if (row >= nrows) return f32x2{kInf, 0.0f};
-  const int64_t qi = row / S.group;
-  const int qh = hk * S.group + (int)(row - qi * S.group);
+  const uint32_t qi = (uint32_t)row / (uint32_t)S.group;  // rows below 2^31
+  const int qh = hk * S.group + (int)((uint32_t)row - qi * S.group);
   const float e = A.lse[((int64_t)b * S.hq + qh) * S.lq + qi];
   const float w = A.weight ? A.weight[b * S.lq + qi] : 1.0f;
   if (e == -kInf) return f32x2{kInf, w};
@@ -79,9 +79,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A
   const int64_t per = (ntiles + A.nsplit - 1) / A.nsplit;
   const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
 
-  RowTiles<T, DP, RT, NT> rows(S, S.q, S.qs, b, hk, S.d, wave, lane);
+  RowTiles<T, DP, RT, NT> rows(S, S.q, S.qs, b, hk, S.d, t0, nrows, wave, lane);
   f32x2 st = {-kInf, 0.0f};  // of row tid: minus its lse, and its weight
-  auto start = [&](int64_t t) { rows.start(S, t, nrows, sm + ((t - t0) & 1) * kTileBytes, wave, lane); };
+  auto start = [&](int64_t t) { rows.start(S, sm + ((t - t0) & 1) * kTileBytes, wave, lane); };
   auto stat = [&](int64_t t) {
     if (tid < RT) {
       st = mass_row(A, b, hk, t * RT + tid, nrows, kExact);
@@ -100,6 +100,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A
 #pragma unroll
     for (int s = 0; s < NS; ++s) kf[s] = global_frag<T>(krow, term != -kInf && t0 < t1, s, h, S.d);
   }
+  loads_done();
   float sum = 0.0f;
   for (int64_t t = t0; t < t1; ++t) {
     const int buf = (int)(t - t0) & 1;

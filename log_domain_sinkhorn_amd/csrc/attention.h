@@ -250,6 +250,12 @@ __device__ __forceinline__ void dma_wait() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// Waits for all outstanding loads in a way that the compiler knows of. Behind
+// the loads of operands that stay in registers and before the first load to LDS:
+// the compiler would otherwise put its own wait for them into the loop over
+// tiles, and there wait for the tiles being loaded as well.
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt 0
+
 // Loader of ROWS rows by the workgroup's NT threads: instructions of 1 KB, the
 // waves in turn. `wave` must be uniform.
 template <class T, int DP, int ROWS, int NT, bool ONCE = false>
@@ -335,32 +341,41 @@ __device__ __forceinline__ float column_term(const float* bias, int64_t j, int64
   return x <= kMasked ? -kInf : x * unit;
 }
 
-// Tiles of RT packed rows of q (or dout), by loads to LDS. Where the group
-// divides RT a lane's offsets are the same in every tile.
+// Tiles of RT packed rows of q (or dout), by loads to LDS, one after the other
+// from tile t0 on. Where the group divides RT a lane's offsets are the same in
+// every tile.
 template <class T, int DP, int RT, int NT>
 struct RowTiles {
   Loader<T, DP, RT, NT> ld;
   const T* base;
-  int64_t row_stride;
+  int64_t row_stride, left;  // left: live rows from the next tile's first on
   uint32_t row_bytes, head_bytes;
-  int d;
+  int d, rem, step, step_rem;  // rem: the next tile's first head; a tile is `step` queries and `step_rem` heads long
 
-  __device__ __forceinline__ RowTiles(const Shape& S, const void* p, const int64_t* s, int b, int hk, int d_, int wave,
-                                      int lane)
-      : base((const T*)p + b * s[0] + (int64_t)hk * S.group * s[2]), row_stride(s[1]),
-        row_bytes((uint32_t)(s[1] * sizeof(T))), head_bytes((uint32_t)(s[2] * sizeof(T))), d(d_) {
+  __device__ __forceinline__ RowTiles(const Shape& S, const void* p, const int64_t* s, int b, int hk, int d_, int64_t t0,
+                                      int64_t nrows, int wave, int lane)
+      : row_stride(s[1]), left(nrows - t0 * RT), row_bytes((uint32_t)(s[1] * sizeof(T))),
+        head_bytes((uint32_t)(s[2] * sizeof(T))), d(d_), step(RT / S.group), step_rem(RT % S.group) {
+    const int64_t qi = t0 * RT / S.group;
+    rem = (int)(t0 * RT - qi * S.group);
+    base = (const T*)p + b * s[0] + (int64_t)hk * S.group * s[2] + qi * row_stride;
     ld.place([&](int r) { return packed_row(S, r, 0, row_bytes, head_bytes); }, d, wave, lane);
   }
-  __device__ __forceinline__ void start(const Shape& S, int64_t t, int64_t nrows, char* tile, int wave, int lane) {
-    const int64_t first = t * RT, qi = first / S.group;
-    const int rem = (int)(first - qi * S.group);
-    if (RT % S.group != 0)
+  // starts the next tile
+  __device__ __forceinline__ void start(const Shape& S, char* tile, int wave, int lane) {
+    if (step_rem != 0)
       ld.place([&](int r) { return packed_row(S, r, rem, row_bytes, head_bytes); }, d, wave, lane);
-    const int64_t left = nrows - first;
     if (left >= RT)
-      ld.start(base + qi * row_stride, tile, [](int) { return true; }, wave, lane);
+      ld.start(base, tile, [](int) { return true; }, wave, lane);
     else
-      ld.start(base + qi * row_stride, tile, [&](int r) { return r < left; }, wave, lane);
+      ld.start(base, tile, [&](int r) { return r < left; }, wave, lane);
+    left -= RT;
+    base += step * row_stride;
+    rem += step_rem;
+    if (rem >= S.group) {
+      rem -= S.group;
+      base += row_stride;
+    }
   }
 };
 

@@ -209,18 +209,19 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
 // computes S and the weights P and accumulates dV = P^T dout, the second computes
 // dout V^T and dS and accumulates dK = dS^T Q one tile of rows later, from the P
 // that its partner left in LDS (fp32, each lane's own registers). Either holds half of
-// the operands and accumulators, so two waves (and for 64 columns of 16 bits
-// four) fit a SIMD, whose matrix and vector work then overlap; one wave doing all
-// needs more than 256 registers at 128 columns and a SIMD to itself (4096 x
-// 8192 x 32 heads, bf16: 3.4 ms). Tiles of 32 rows in a ring of four: the
-// second wave's, the first's, and two being loaded (a tile is computed on in
-// less time than memory takes to answer).
-template <class T, int DP, int OCC>
-__global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
+// the operands and accumulators, so two waves fit a SIMD, whose matrix and vector
+// work then overlap; one wave doing all needs more than 256 registers at 128
+// columns and a SIMD to itself (4096 x 8192 x 32 heads, bf16: 3.4 ms against
+// 2.4). Tiles of 32 rows in a ring: the second
+// wave's, the first's, and those being loaded (a tile is computed on in less
+// time than memory takes to answer).
+template <class T, int DP>
+__global__ __launch_bounds__(512, 2) void k_grad_kv(GradArgs A) {
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
   constexpr int RT = 32, NT = 512, NS = DP / 16, NDB = DP / 32;
-  constexpr int RING = sizeof(T) * DP > 256 ? 3 : 4;  // fp32 of 128 columns: no room for a fourth
+  constexpr bool AHEAD = sizeof(T) * DP <= 256;  // registers for it
+  constexpr int RING = sizeof(T) * DP <= 256 ? 4 : 3;  // tiles in LDS: fp32 of 128 columns leaves no room for more
   constexpr int kTileBytes = RT * TL::RB;
   __shared__ __attribute__((aligned(16))) char sm[RING][2][kTileBytes];  // q, dout
   __shared__ __attribute__((aligned(16))) f32x4 sp[2][4][4][64];      // P: [buffer][pair][registers][lane]
@@ -257,7 +258,7 @@ __global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
     rq.start(S, sm[buf][0], wave, lane);
     rg.start(S, sm[buf][1], wave, lane);
     // 32 rows of statistics, 8 bytes each (rows_pad covers the tile)
-    if (wave == 7) dma_load<4>(dma_rsrc(A.stat + pair * A.rows_pad + (t0 + n) * RT), lds_offset(sstat[buf]), 4 * lane);
+    if (wave == 0) dma_load<4>(dma_rsrc(A.stat + pair * A.rows_pad + (t0 + n) * RT), lds_offset(sstat[buf]), 4 * lane);
   };
   V8 fr[NS];  // the keys' rows of k (first) or v (second)
   {
@@ -268,8 +269,8 @@ __global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
     for (int s = 0; s < NS; ++s) fr[s] = global_frag<T>(row, live, s, h, first ? S.d : S.dv);
   }
   loads_done();
-  start(0);
-  if constexpr (RING > 3) start(1);
+#pragma unroll
+  for (int n = 0; n < RING - 2; ++n) start(n);
   f32x16 acc[NDB];  // dV (first) or dK (second), transposed
 #pragma unroll
   for (int n = 0; n < NDB; ++n) acc[n] = zero16();
@@ -278,9 +279,13 @@ __global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
   // Makes tile `it` readable and the weights of tile it - 1, and starts a tile.
   // Both kinds of wave call it once for each it = 0 .. count.
   auto next = [&](int it) {
-    // a wave's loads of tile it + 1 may be on their way
-    if (RING > 3 && it + 1 < count && Ld::has(Ld::N - 1, wave))
-      dma_wait<2 * Ld::N>();
+    // the loads of the FLY tiles after it may be on their way
+    constexpr int FLY = RING - 3;
+    static_assert(Ld::N == 1 || Ld::TOTAL % Ld::NW == 0, "a wave has all of a tile's loads or none");
+    if (FLY > 0 && it + FLY < count && wave == 0)
+      dma_wait<FLY * (2 * Ld::N + 1)>();
+    else if (FLY > 0 && it + FLY < count && Ld::has(0, wave))
+      dma_wait<FLY * 2 * Ld::N>();
     else
       dma_wait<0>();
     __syncthreads();
@@ -292,9 +297,21 @@ __global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
       const char* const tq = sm[it % RING][0];
       const char* const tg = sm[it % RING][1];
       const f32x2* const stat = sstat[it % RING];
+      // all fragments on their way before the first product: left alone, the
+      // compiler reads one or two ahead and each product waits for LDS
+      V8 ra[NS], ca[2][NDB];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) ra[s] = TL::row_frag(tq, r32, s, h);
+      if constexpr (AHEAD) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int x = 0; x < NDB; ++x) ca[s][x] = TL::col_frag(tg, 16 * s, 32 * x, lane);
+        __builtin_amdgcn_sched_barrier(0);
+      }
       f32x16 p = zero16();
 #pragma unroll
-      for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tq, r32, s, h), fr[s], p);
+      for (int s = 0; s < NS; ++s) p = mma(ra[s], fr[s], p);
       auto weights = [&](auto biased) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -315,7 +332,8 @@ __global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
       for (int s = 0; s < 2; ++s) {
         const V8 pw = pack<T>(p, s);
 #pragma unroll
-        for (int x = 0; x < NDB; ++x) acc[x] = mma(TL::col_frag(tg, 16 * s, 32 * x, lane), pw, acc[x]);
+        for (int x = 0; x < NDB; ++x)
+          acc[x] = mma(AHEAD ? ca[s][x] : TL::col_frag(tg, 16 * s, 32 * x, lane), pw, acc[x]);
       }
     }
     next(count);
@@ -326,9 +344,19 @@ __global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
       const char* const tq = sm[it % RING][0];
       const char* const tg = sm[it % RING][1];
       const f32x2* const stat = sstat[it % RING];
+      V8 ra[NS], ca[2][NDB];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) ra[s] = TL::row_frag(tg, r32, s, h);
+      if constexpr (AHEAD) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int x = 0; x < NDB; ++x) ca[s][x] = TL::col_frag(tq, 16 * s, 32 * x, lane);
+        __builtin_amdgcn_sched_barrier(0);
+      }
       f32x16 g = zero16();
 #pragma unroll
-      for (int s = 0; s < NS; ++s) g = mma(TL::row_frag(tg, r32, s, h), fr[s], g);
+      for (int s = 0; s < NS; ++s) g = mma(ra[s], fr[s], g);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const f32x4 p = sp[it & 1][wp][q][lane];
@@ -343,7 +371,8 @@ __global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
       for (int s = 0; s < 2; ++s) {
         const V8 ds = pack<T>(g, s);
 #pragma unroll
-        for (int x = 0; x < NDB; ++x) acc[x] = mma(TL::col_frag(tq, 16 * s, 32 * x, lane), ds, acc[x]);
+        for (int x = 0; x < NDB; ++x)
+          acc[x] = mma(AHEAD ? ca[s][x] : TL::col_frag(tq, 16 * s, 32 * x, lane), ds, acc[x]);
       }
     }
   }
@@ -360,6 +389,126 @@ __global__ __launch_bounds__(512, OCC) void k_grad_kv(GradArgs A) {
     T* row = (T*)A.dk + b * A.dks[0] + key * A.dks[1] + hk * A.dks[2];
     write_cols<T, NDB>(acc, S.scale, A.part_k ? A.part_k + pi * A.dp : nullptr, A.dp, row, S.d, A.vec_k, h);
   }
+}
+
+// The same for 64 columns of 16 bits, where one wave holds both operands and
+// both accumulators of its 32 keys in less than 256 registers: 4 waves, tiles of
+// 64 rows in two LDS buffers, half the barriers and nothing passed between
+// waves (512 x 1000 x 16 heads x 8, bf16: 5x us against 60).
+template <class T, int DP>
+__global__ __launch_bounds__(256, 2) void k_grad_kv_one(GradArgs A) {
+  using TL = Tile<T, DP>;
+  using V8 = typename Vec<T>::V8;
+  constexpr int RT = 64, NT = 256, NS = DP / 16, NDB = DP / 32;
+  constexpr int kTileBytes = RT * TL::RB;
+  __shared__ __attribute__((aligned(16))) char sm[2][2][kTileBytes];  // q, dout
+  __shared__ __attribute__((aligned(16))) f32x2 sstat[2][RT];
+
+  const Shape& S = A.S;
+  const int64_t pairs = (int64_t)S.batch * S.hkv;
+  const int64_t item = xcd_item(pairs * A.tiles_kv * A.split_kv);
+  if (item >= pairs * A.tiles_kv * A.split_kv) return;
+  const int64_t pair = item / (A.tiles_kv * A.split_kv);
+  const int64_t rest = item - pair * (A.tiles_kv * A.split_kv);
+  const int64_t tile = rest / A.split_kv;
+  const int split = (int)(rest - tile * A.split_kv);
+  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5, r32 = lane & 31;
+
+  const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
+  const int64_t key0 = tile * 128, key = key0 + 32 * wave + r32;
+  const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
+  const float term = column_term(bias, key, nkeys, (float)kLog2e);
+  const int64_t ntiles = key0 < nkeys ? (nrows + RT - 1) / RT : 0;
+  const int64_t per = (ntiles + A.split_kv - 1) / A.split_kv;
+  const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
+  const int count = t1 > t0 ? (int)(t1 - t0) : 0;
+
+  RowTiles<T, DP, RT, NT> rq(S, S.q, S.qs, b, hk, S.d, t0, nrows, wave, lane),
+      rg(S, A.dout, A.dos, b, hk, S.dv, t0, nrows, wave, lane);
+  auto start = [&](int n) {
+    if (n >= count) return;
+    rq.start(S, sm[n & 1][0], wave, lane);
+    rg.start(S, sm[n & 1][1], wave, lane);
+    // 64 rows of statistics, 8 bytes each (rows_pad covers the tile)
+    if (wave < 2)
+      dma_load<4>(dma_rsrc(A.stat + pair * A.rows_pad + (t0 + n) * RT), lds_offset(sstat[n & 1]) + wave * 256,
+                  wave * 256 + 4 * lane);
+  };
+  V8 kf[NS], vf[NS];
+  {
+    const T* krow = (const T*)S.k + b * S.ks[0] + key * S.ks[1] + hk * S.ks[2];
+    const T* vrow = (const T*)S.v + b * S.vs[0] + key * S.vs[1] + hk * S.vs[2];
+    const bool live = term != -kInf && count > 0;  // no rows: nothing to read them for
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      kf[s] = global_frag<T>(krow, live, s, h, S.d);
+      vf[s] = global_frag<T>(vrow, live, s, h, S.dv);
+    }
+  }
+  loads_done();
+  start(0);
+  f32x16 dk[NDB], dv[NDB];
+#pragma unroll
+  for (int n = 0; n < NDB; ++n) {
+    dk[n] = zero16();
+    dv[n] = zero16();
+  }
+  for (int it = 0; it < count; ++it) {
+    dma_wait<0>();
+    __syncthreads();
+    start(it + 1);
+    const char* const tq = sm[it & 1][0];
+    const char* const tg = sm[it & 1][1];
+    const f32x2* const stat = sstat[it & 1];
+#pragma unroll
+    for (int n = 0; n < RT / 32; ++n) {
+      f32x16 p = zero16(), g = zero16();
+#pragma unroll
+      for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tq, 32 * n + r32, s, h), kf[s], p);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) g = mma(TL::row_frag(tg, 32 * n + r32, s, h), vf[s], g);
+      auto weights = [&](auto biased) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const f32x4 w = *(const f32x4*)&stat[32 * n + 8 * (q >> 1) + 4 * h + 2 * (q & 1)];  // {-lse, D, -lse, D}
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int i = 2 * q + e;
+            p[i] = weight<T, decltype(biased)::value>(S, p[i], term, w[2 * e]);
+            g[i] = p[i] * (g[i] - w[2 * e + 1]);
+          }
+        }
+      };
+      if (bias)
+        weights(std::true_type{});
+      else
+        weights(std::false_type{});  // as in k_grad_kv
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const V8 pw = pack<T>(p, s), ds = pack<T>(g, s);
+#pragma unroll
+        for (int x = 0; x < NDB; ++x) {
+          dv[x] = mma(TL::col_frag(tg, 32 * n + 16 * s, 32 * x, lane), pw, dv[x]);
+          dk[x] = mma(TL::col_frag(tq, 32 * n + 16 * s, 32 * x, lane), ds, dk[x]);
+        }
+      }
+    }
+  }
+  if (key >= S.lk) return;
+  if (term == -kInf) {
+#pragma unroll
+    for (int n = 0; n < NDB; ++n) {
+      dk[n] = zero16();
+      dv[n] = zero16();
+    }
+  }
+  const int64_t pi = ((int64_t)split * pairs + pair) * S.lk + key;
+  T* dkrow = (T*)A.dk + b * A.dks[0] + key * A.dks[1] + hk * A.dks[2];
+  T* dvrow = (T*)A.dv + b * A.dvs[0] + key * A.dvs[1] + hk * A.dvs[2];
+  write_cols<T, NDB>(dk, S.scale, A.part_k ? A.part_k + pi * A.dp : nullptr, A.dp, dkrow, S.d, A.vec_k, h);
+  write_cols<T, NDB>(dv, 1.0f, A.part_v ? A.part_v + pi * A.dvp : nullptr, A.dvp, dvrow, S.dv, A.vec_v, h);
 }
 
 // Adds the partial sums of a gradient in split order: 32 lanes per row. Rows of
@@ -410,8 +559,11 @@ void grad_launch(const GradArgs& A, hipStream_t st) {
     SK_LAUNCH_CHECK();
   }
   if (A.S.lk > 0) {
-    hipLaunchKernelGGL((k_grad_kv<T, DP, (DP * sizeof(T) == 128 ? 4 : 2)>),
-                       grid1(xcd_blocks(pairs * A.tiles_kv * A.split_kv), 512), dim3(512), 0, st, A);
+    const int64_t items = xcd_blocks(pairs * A.tiles_kv * A.split_kv);
+    if constexpr (DP * sizeof(T) == 128)
+      hipLaunchKernelGGL((k_grad_kv_one<T, DP>), grid1(items, 256), dim3(256), 0, st, A);
+    else
+      hipLaunchKernelGGL((k_grad_kv<T, DP>), grid1(items, 512), dim3(512), 0, st, A);
     SK_LAUNCH_CHECK();
   }
 }

@@ -259,7 +259,8 @@ GradPlan plan_grad(const sinkhorn_attention* a, const void* q, const void* k, co
   p.tiles_kv = ceil_div(a->len_k, 128);
   p.rows_pad = ceil_div(rows, 64) * 64;
   p.split_q = splits(pairs * p.tiles_q, ceil_div(a->len_k, step), f32 && wide(a) ? 256 : 512, join_steps(a), false);
-  p.split_kv = splits(pairs * p.tiles_kv, ceil_div(rows, 32), f32 || wide(a) ? 256 : 512, 4 * join_steps(a), false);
+  p.split_kv = f32 || wide(a) ? splits(pairs * p.tiles_kv, ceil_div(rows, 32), 256, 4 * join_steps(a), false)
+                              : splits(pairs * p.tiles_kv, ceil_div(rows, 64), 512, 2 * join_steps(a), false);
   p.q = operand(a, q, a->q_stride, a->len_q, a->heads_q, a->d, ws);
   p.k = operand(a, k, a->k_stride, a->len_k, a->heads_kv, a->d, ws);
   p.v = operand(a, v, a->v_stride, a->len_k, a->heads_kv, a->dv, ws);

@@ -551,10 +551,14 @@ typedef struct {
  * [batch][heads][cap] the positions they had; lengths_out [batch] the number
  * kept. Behind that number k_out and v_out are left as they were, mass_out is
  * 0 and index_out -1. Outputs may not overlap inputs or each other. d and dv
- * are not limited to 128. Asynchronous on `stream`; no workspace. */
+ * are not limited to 128. Asynchronous on `stream`. */
 int sinkhorn_cache_evict(const sinkhorn_cache* cache, const void* k, const void* v,
                          const float* mass, void* k_out, void* v_out, float* mass_out,
-                         int32_t* index_out, int32_t* lengths_out, void* stream);
+                         int32_t* index_out, int32_t* lengths_out, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace (16-byte aligned) that sinkhorn_cache_evict needs. Host only. */
+int sinkhorn_cache_workspace(const sinkhorn_cache* cache, int64_t* bytes);
 
 /* Measurement hook. `kinds` is a bit set of the kernels to time: every later
  * launch of a selected kernel carries two HIP events that its own dispatch

@@ -226,7 +226,8 @@ _SIGS = {
     "sinkhorn_cross_attention": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
     "sinkhorn_cross_attention_grad": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
     "sinkhorn_attention_mass": ([_p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
-    "sinkhorn_cache_evict": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p], _i32),
+    "sinkhorn_cache_evict": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
+    "sinkhorn_cache_workspace": ([_p, _p], _i32),
     "sinkhorn_profile_enable": ([_p, _i32], _i32),
     "sinkhorn_profile_read": ([_p, _p, _p, _p], _i32),
     "sinkhorn_probe_issue_rate": ([_i32, _i32, _p, _p, _p, _p], _i32),
@@ -676,9 +677,12 @@ def cache_evict(k, v, mass, keep: int, *, key_lengths=None, first: int = 0, rece
         lengths_out = torch.empty(B, dtype=torch.int32, device=device)
     c = _CacheC(_ATTN_DTYPES[k.dtype], B, h, d, dv, n, keep, first, recent, _strides3(k), _strides3(v), _strides3(k_out),
                 _strides3(v_out), _at(key_lengths))
+    size = _i64()
+    _check(lib().sinkhorn_cache_workspace(ctypes.byref(c), ctypes.byref(size)), "cache_workspace")
+    ws = torch.empty(size.value, dtype=torch.uint8, device=device) if size.value else None
     _launch(index, "cache_evict", lib().sinkhorn_cache_evict, ctypes.byref(c), k.data_ptr(), v.data_ptr(),
             mass.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), mass_out.data_ptr(), index_out.data_ptr(),
-            lengths_out.data_ptr())
+            lengths_out.data_ptr(), _at(ws), size.value)
     return k_out, v_out, mass_out, index_out, lengths_out
 
 

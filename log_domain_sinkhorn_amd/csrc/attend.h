@@ -115,11 +115,11 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
     const int kb0 = 32 * NB * wk;
     f32x16 sc[NB];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      sc[n] = zero16();
+    for (int n = 0; n < NB; ++n) sc[n] = zero16();
 #pragma unroll
-      for (int s = 0; s < NS; ++s) sc[n] = mma(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n]);
-    }
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) sc[n] = mma(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n]);
     float f = kExact ? (float)kLog2e : S.c;  // to log2 units
     if (kExact || A.scores || keys.masked(it)) {
       const float* const term = keys.term(it);

@@ -172,9 +172,10 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
     for (int n = 0; n < KT / 32; ++n) {
       f32x16 p = zero16(), g = zero16();
 #pragma unroll
-      for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tk, 32 * n + r32, s, h), qf[s], p);
-#pragma unroll
-      for (int s = 0; s < NS; ++s) g = mma(TL::row_frag(tv, 32 * n + r32, s, h), gf[s], g);
+      for (int s = 0; s < NS; ++s) {
+        p = mma(TL::row_frag(tk, 32 * n + r32, s, h), qf[s], p);
+        g = mma(TL::row_frag(tv, 32 * n + r32, s, h), gf[s], g);
+      }
       auto weights = [&](auto terms) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -466,9 +467,10 @@ __global__ __launch_bounds__(256, 2) void k_grad_kv_one(GradArgs A) {
     for (int n = 0; n < RT / 32; ++n) {
       f32x16 p = zero16(), g = zero16();
 #pragma unroll
-      for (int s = 0; s < NS; ++s) p = mma(TL::row_frag(tq, 32 * n + r32, s, h), kf[s], p);
-#pragma unroll
-      for (int s = 0; s < NS; ++s) g = mma(TL::row_frag(tg, 32 * n + r32, s, h), vf[s], g);
+      for (int s = 0; s < NS; ++s) {
+        p = mma(TL::row_frag(tq, 32 * n + r32, s, h), kf[s], p);
+        g = mma(TL::row_frag(tg, 32 * n + r32, s, h), vf[s], g);
+      }
       auto weights = [&](auto biased) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {

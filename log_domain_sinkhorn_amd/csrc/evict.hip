@@ -6,12 +6,14 @@
 // k_evict_select (one workgroup per pair) finds the keep-th largest weight by
 // radix selection on the weights' bits taken as ordered integers (8 bits a
 // pass, counts in LDS: integer sums, so the result is exact and does not depend
-// on the order of threads), then writes the kept indices in order; keys that
-// equal the threshold are taken from the lowest index up. Keys that are kept
-// in any case count as the highest. Up to 65536 keys stay in registers as such
-// integers over the passes; reading and converting them in each pass took 104 us
-// in place of 2x us at 65536 keys.
-// k_evict_move copies the rows. The copy is bound by memory.
+// on the order of threads). Keys that are kept in any case count as the highest;
+// of those that equal the threshold the lowest indices are kept. It then counts
+// the kept keys before every 256th one. Up to 65536 keys stay in registers as
+// ordered integers over the passes. One compute unit's vector work bounds it, so
+// all that can be done by others is: k_evict_move (one workgroup per 256 keys)
+// takes the threshold and those counts, finds its kept keys' places and copies
+// their rows, bound by memory (4 x 8 x 65536 keys to 16384, rows of 128 bf16: with
+// the places found by k_evict_select it took 78 us in place of 3x).
 #include "attention.h"
 
 namespace sk {
@@ -31,9 +33,12 @@ struct EvictArgs {
   char* dst[2];
   int64_t ss[2][3], ds[2][3];  // strides in bytes: batch, row, head
   int32_t width[2];            // row width in units of the copy
-  int64_t blocks_per_pair;
+  uint32_t* limit;   // [pairs][2] threshold, and how many keys equal to it are kept
+  uint32_t* before;  // [pairs][groups][2] kept for sure, and equal to the threshold, before a group
+  int64_t groups;    // of kGroup keys
 };
 
+constexpr int kGroup = 256;  // keys of a workgroup of k_evict_move
 constexpr int kSelThreads = 1024;
 constexpr int kSelPer = 16;  // keys of a thread in a chunk
 constexpr int kSelChunk = kSelThreads * kSelPer;
@@ -56,11 +61,18 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return x != x ? kLowest : v;
 }
 
+// Key j of n with weight x: the first `lo` and those from `hi` on are always kept.
+__device__ __forceinline__ uint32_t key_value(float x, int j, int n, int lo, int hi) {
+  return j >= n ? kNone : (j < lo || j >= hi ? kAlways : order_key(x));
+}
+
 // C: chunks of keys held in registers; 0: any number, read in each pass.
 template <int C>
 __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
+  constexpr int kSub = kSelChunk / kGroup;  // groups of a chunk: 64, four of a wave's
+  static_assert(kSub == 64 && kSelPer * 64 == 4 * kGroup, "a lane of one wave for each group");
   __shared__ uint32_t hist[256][kCopies];
-  __shared__ uint32_t swave[2][kSelThreads / 64];
+  __shared__ uint32_t scount[2][kSub];
   __shared__ uint32_t sdigit, sbefore;
   const int64_t pair = blockIdx.x;
   const int b = (int)(pair / A.heads);
@@ -68,21 +80,13 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
   const int n = (int)evict_len(A, b);
   const int keep = (int)(A.keep < A.len ? A.keep : A.len);
   const int left = n < keep ? n : keep;
-  const float* w = A.mass + pair * A.len;
-  int32_t* idx = A.index_out + pair * A.cap;
-  float* mo = A.mass_out + pair * A.cap;
   if (tid == 0 && pair == (int64_t)b * A.heads) A.lengths_out[b] = left;
   for (int j = left + tid; j < (int)A.cap; j += kSelThreads) {
-    idx[j] = -1;
-    mo[j] = 0.0f;
+    A.index_out[pair * A.cap + j] = -1;
+    A.mass_out[pair * A.cap + j] = 0.0f;
   }
-  if (n <= keep) {
-    for (int j = tid; j < n; j += kSelThreads) {
-      idx[j] = j;
-      mo[j] = w[j];
-    }
-    return;
-  }
+  if (n <= keep) return;  // all kept
+  const float* w = A.mass + pair * A.len;
   const int lo = (int)A.first, hi = n - (int)A.recent;
   // a wave's keys of a chunk: 1024 consecutive ones, 64 at a time
   const int base = wave * (64 * kSelPer) + lane;
@@ -92,10 +96,7 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
 #pragma unroll
     for (int i = 0; i < kSelPer; ++i) x[i] = j0 + 64 * i < n ? w[j0 + 64 * i] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < kSelPer; ++i) {
-      const int j = j0 + 64 * i;
-      u[i] = j >= n ? kNone : (j < lo || j >= hi ? kAlways : order_key(x[i]));
-    }
+    for (int i = 0; i < kSelPer; ++i) u[i] = key_value(x[i], j0 + 64 * i, n, lo, hi);
   };
   const int chunks = (n - 1) / kSelChunk + 1;
   uint32_t held[C > 0 ? C : 1][kSelPer];
@@ -159,69 +160,118 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
     need -= sbefore;
   }
   // keys above `prefix` are kept, and the first `need` of those equal to it
-  uint32_t nsel = 0, neq = 0;  // kept for sure, and equal, before this chunk
+  if (tid == 0) {
+    A.limit[2 * pair] = prefix;
+    A.limit[2 * pair + 1] = need;
+  }
+  uint32_t nsel = 0, neq = 0;  // before this chunk (the first wave's)
   each([&](int chunk, const uint32_t (&u)[kSelPer]) {
-    uint64_t sel[kSelPer], eq[kSelPer];
-    uint32_t csel = 0, ceq = 0;
 #pragma unroll
-    for (int i = 0; i < kSelPer; ++i) {
-      sel[i] = __ballot(u[i] > prefix);
-      eq[i] = __ballot(u[i] == prefix);
-      csel += __popcll(sel[i]);
-      ceq += __popcll(eq[i]);
-    }
-    if (lane == 0) {
-      swave[0][wave] = csel;
-      swave[1][wave] = ceq;
+    for (int g = 0; g < 4; ++g) {
+      uint32_t s = 0, q = 0;
+#pragma unroll
+      for (int i = 4 * g; i < 4 * g + 4; ++i) {
+        s += __popcll(__ballot(u[i] > prefix));
+        q += __popcll(__ballot(u[i] == prefix));
+      }
+      if (lane == 0) {
+        scount[0][4 * wave + g] = s;
+        scount[1][4 * wave + g] = q;
+      }
     }
     __syncthreads();
-    uint32_t s = nsel, q = neq;  // kept, and equal, before this wave's keys
+    if (wave == 0) {
+      const uint32_t s = scount[0][lane], q = scount[1][lane];
+      uint32_t is = s, iq = q;
 #pragma unroll
-    for (int k = 0; k < kSelThreads / 64; ++k) {
-      if (k < wave) {
-        s += swave[0][k];
-        q += swave[1][k];
-      }
-      nsel += swave[0][k];
-      neq += swave[1][k];
-    }
-    const uint64_t below = (uint64_t(1) << lane) - 1;
-    const int j0 = chunk * kSelChunk + base;
-#pragma unroll
-    for (int i = 0; i < kSelPer; ++i) {
-      const uint32_t es = s + __popcll(sel[i] & below), ee = q + __popcll(eq[i] & below);
-      if (((sel[i] >> lane) & 1) || (((eq[i] >> lane) & 1) && ee < need)) {
-        const uint32_t pos = es + (ee < need ? ee : need);
-        if (pos < (uint32_t)keep) {
-          idx[pos] = j0 + 64 * i;
-          mo[pos] = w[j0 + 64 * i];
+      for (int x = 1; x < 64; x <<= 1) {
+        const uint32_t ys = __shfl_up(is, x), yq = __shfl_up(iq, x);
+        if (lane >= x) {
+          is += ys;
+          iq += yq;
         }
       }
-      s += __popcll(sel[i]);
-      q += __popcll(eq[i]);
+      const int64_t group = (int64_t)chunk * kSub + lane;
+      if (group < A.groups) {
+        A.before[2 * (pair * A.groups + group)] = nsel + is - s;
+        A.before[2 * (pair * A.groups + group) + 1] = neq + iq - q;
+      }
+      nsel += __shfl(is, 63);
+      neq += __shfl(iq, 63);
     }
     __syncthreads();
   });
 }
 
-// Copies the kept rows: UNIT bytes a thread and step, 32 rows per workgroup.
+// Copies the kept rows of a group of keys, a unit U a thread and step.
 template <class U>
-__global__ __launch_bounds__(256) void k_evict_move(EvictArgs A) {
-  const int64_t pair = blockIdx.x / A.blocks_per_pair;
-  const int64_t r0 = (blockIdx.x - pair * A.blocks_per_pair) * 32;
+__global__ __launch_bounds__(kGroup) void k_evict_move(EvictArgs A) {
+  __shared__ int src[kGroup];
+  __shared__ uint32_t swave[2][kGroup / 64];
+  const int64_t pair = blockIdx.x / A.groups;
+  const int64_t group = blockIdx.x - pair * A.groups;
   const int b = (int)(pair / A.heads), hd = (int)(pair - (int64_t)b * A.heads);
-  const int64_t n = evict_len(A, b);
-  const int64_t left = n < A.cap ? n : A.cap;
-  const int rows = left - r0 < 32 ? (int)(left - r0) : 32;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = (int)evict_len(A, b), j0 = (int)(group * kGroup), j = j0 + tid;
+  if (j0 >= n) return;
+  const int keep = (int)(A.keep < A.len ? A.keep : A.len);
+  const float x = j < n ? A.mass[pair * A.len + j] : 0.0f;
+  bool kept = j < n;
+  int first = j0, place = tid, count = n - j0 < kGroup ? n - j0 : kGroup;  // place of the first kept key, of this among them
+  if (n > keep) {
+    const uint32_t limit = A.limit[2 * pair], need = A.limit[2 * pair + 1];
+    const uint32_t s0 = A.before[2 * (pair * A.groups + group)], q0 = A.before[2 * (pair * A.groups + group) + 1];
+    const uint32_t u = key_value(x, j, n, (int)A.first, n - (int)A.recent);
+    const uint64_t sel = __ballot(u > limit), eq = __ballot(u == limit);
+    if (lane == 0) {
+      swave[0][wave] = (uint32_t)__popcll(sel);
+      swave[1][wave] = (uint32_t)__popcll(eq);
+    }
+    __syncthreads();
+    uint32_t s = s0, q = q0, send = s0, qend = q0;
+#pragma unroll
+    for (int k = 0; k < kGroup / 64; ++k) {
+      if (k < wave) {
+        s += swave[0][k];
+        q += swave[1][k];
+      }
+      send += swave[0][k];
+      qend += swave[1][k];
+    }
+    const uint64_t below = (uint64_t(1) << lane) - 1;
+    s += (uint32_t)__popcll(sel & below);
+    q += (uint32_t)__popcll(eq & below);
+    kept = u > limit || (u == limit && q < need);
+    first = (int)(s0 + (q0 < need ? q0 : need));
+    place = (int)(s + (q < need ? q : need)) - first;
+    count = (int)(send + (qend < need ? qend : need)) - first;
+  }
+  if (kept) {
+    src[place] = j;
+    A.index_out[pair * A.cap + first + place] = j;
+    A.mass_out[pair * A.cap + first + place] = x;
+  }
+  __syncthreads();
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int w = A.width[t];
-    const char* src = A.src[t] + b * A.ss[t][0] + hd * A.ss[t][2];
-    char* dst = A.dst[t] + b * A.ds[t][0] + hd * A.ds[t][2];
-    for (int i = threadIdx.x; i < rows * w; i += 256) {
-      const int r = i / w, c = i - r * w;
-      const int64_t j = A.index_out[pair * A.cap + r0 + r];
-      ((U*)(dst + (r0 + r) * A.ds[t][1]))[c] = ((const U*)(src + j * A.ss[t][1]))[c];
+    const char* from = A.src[t] + b * A.ss[t][0] + hd * A.ss[t][2];
+    char* to = A.dst[t] + b * A.ds[t][0] + hd * A.ds[t][2] + first * A.ds[t][1];
+    // a thread's column(s) and first row; four rows in flight
+    const int wide = w < kGroup ? w : kGroup, step = kGroup / wide;
+    const int r0 = tid / wide;
+    if (r0 >= step) continue;
+    for (int c = tid - r0 * wide; c < w; c += wide) {
+      const U* p = (const U*)from + c;
+      for (int r = r0; r < count; r += 4 * step) {
+        U v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (r + i * step < count) v[i] = __builtin_nontemporal_load((const U*)((const char*)p + src[r + i * step] * A.ss[t][1]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (r + i * step < count) __builtin_nontemporal_store(v[i], (U*)(to + (r + i * step) * A.ds[t][1]) + c);
+      }
     }
   }
 }
@@ -244,17 +294,7 @@ void require(bool ok, const char* what) {
   if (!ok) fail(SINKHORN_ERR_INVALID_ARG, what);
 }
 
-}  // namespace
-}  // namespace attn
-}  // namespace sk
-
-using namespace sk;
-using namespace sk::attn;
-
-extern "C" int sinkhorn_cache_evict(const sinkhorn_cache* c, const void* k, const void* v, const float* mass,
-                                    void* k_out, void* v_out, float* mass_out, int32_t* index_out,
-                                    int32_t* lengths_out, void* stream) {
-  return guarded([&] {
+void check(const sinkhorn_cache* c) {
     require(c != nullptr, "null cache description");
     require(c->dtype == SINKHORN_F32 || c->dtype == SINKHORN_F16 || c->dtype == SINKHORN_BF16, "unknown dtype");
     require(c->batch >= 0 && c->heads >= 1 && c->len >= 0 && c->d >= 1 && c->dv >= 1, "bad sizes");
@@ -264,12 +304,44 @@ extern "C" int sinkhorn_cache_evict(const sinkhorn_cache* c, const void* k, cons
     for (int i = 0; i < 3; ++i)
       require(c->k_stride[i] >= 0 && c->v_stride[i] >= 0 && c->k_out_stride[i] >= 0 && c->v_out_stride[i] >= 0,
               "negative stride");
+}
+
+int64_t space(const sinkhorn_cache* c) {
+  return 8 * (int64_t)c->batch * c->heads * (1 + (c->len + kGroup - 1) / kGroup);
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace sk
+
+using namespace sk;
+using namespace sk::attn;
+
+extern "C" {
+
+int sinkhorn_cache_workspace(const sinkhorn_cache* c, int64_t* bytes) {
+  return guarded([&] {
+    check(c);
+    require(bytes != nullptr, "null pointer");
+    *bytes = space(c);
+    return SINKHORN_OK;
+  });
+}
+
+int sinkhorn_cache_evict(const sinkhorn_cache* c, const void* k, const void* v, const float* mass, void* k_out,
+                         void* v_out, float* mass_out, int32_t* index_out, int32_t* lengths_out, void* workspace,
+                         int64_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    check(c);
     if (c->batch == 0) return SINKHORN_OK;
     require(lengths_out != nullptr, "null pointer");
     if (c->len > 0) {
       require(k && v && mass && k_out && v_out && mass_out && index_out, "null pointer");
       require(k_out != k && v_out != v && k_out != v_out && mass_out != mass, "output aliases an input");
     }
+    require(workspace_bytes >= space(c) && (space(c) == 0 || workspace != nullptr),
+            "workspace too small (sinkhorn_cache_workspace)");
+    require((uintptr_t)workspace % 16 == 0, "workspace must be 16-byte aligned");
     const int64_t size = c->dtype == SINKHORN_F32 ? 4 : 2;
     EvictArgs A{};
     A.batch = c->batch;
@@ -309,6 +381,9 @@ extern "C" int sinkhorn_cache_evict(const sinkhorn_cache* c, const void* k, cons
     }
     const hipStream_t st = (hipStream_t)stream;
     const int64_t pairs = (int64_t)c->batch * c->heads;
+    A.groups = (c->len + kGroup - 1) / kGroup;
+    A.limit = (uint32_t*)workspace;
+    A.before = (uint32_t*)workspace + 2 * pairs;
     const dim3 all = grid1(pairs, kSelThreads);
     if (c->len <= kSelChunk)
       hipLaunchKernelGGL((k_evict_select<1>), all, dim3(kSelThreads), 0, st, A);
@@ -318,15 +393,16 @@ extern "C" int sinkhorn_cache_evict(const sinkhorn_cache* c, const void* k, cons
       hipLaunchKernelGGL((k_evict_select<0>), all, dim3(kSelThreads), 0, st, A);
     SK_LAUNCH_CHECK();
     if (A.cap == 0) return SINKHORN_OK;
-    A.blocks_per_pair = (A.cap + 31) / 32;
-    const dim3 grid = grid1(pairs * A.blocks_per_pair, 256);
+    const dim3 grid = grid1(pairs * A.groups, kGroup);
     switch (unit) {
-      case 16: hipLaunchKernelGGL((k_evict_move<u32x4>), grid, dim3(256), 0, st, A); break;
-      case 8: hipLaunchKernelGGL((k_evict_move<u32x2>), grid, dim3(256), 0, st, A); break;
-      case 4: hipLaunchKernelGGL((k_evict_move<uint32_t>), grid, dim3(256), 0, st, A); break;
-      default: hipLaunchKernelGGL((k_evict_move<uint16_t>), grid, dim3(256), 0, st, A); break;
+      case 16: hipLaunchKernelGGL((k_evict_move<u32x4>), grid, dim3(kGroup), 0, st, A); break;
+      case 8: hipLaunchKernelGGL((k_evict_move<u32x2>), grid, dim3(kGroup), 0, st, A); break;
+      case 4: hipLaunchKernelGGL((k_evict_move<uint32_t>), grid, dim3(kGroup), 0, st, A); break;
+      default: hipLaunchKernelGGL((k_evict_move<uint16_t>), grid, dim3(kGroup), 0, st, A); break;
     }
     SK_LAUNCH_CHECK();
     return SINKHORN_OK;
   });
 }
+
+}  // extern "C"

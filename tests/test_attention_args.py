@@ -169,7 +169,8 @@ def _cache(**kw):
 def test_cache_descriptions_are_refused():
     L = sk.lib()
     p = [ctypes.c_void_p(4096 * i) for i in range(1, 9)]
-    call = lambda c, *x: L.sinkhorn_cache_evict(ctypes.byref(c) if c else None, *x, None)  # noqa: E731
+    call = lambda c, *x, ws=p[7], n=1 << 20: L.sinkhorn_cache_evict(  # noqa: E731
+        ctypes.byref(c) if c else None, *x, ws, n, None)
     assert call(None, *p) == sk.ERR_INVALID_ARG
     for kw in (dict(dtype=7), dict(batch=-1), dict(heads=0), dict(len=-1), dict(len=1 << 31), dict(keep=0), dict(first=-1),
                dict(recent=-1), dict(first=9, recent=2), dict(first=1 << 62, recent=1 << 62), dict(d=0),
@@ -183,4 +184,10 @@ def test_cache_descriptions_are_refused():
         q = list(p)
         q[i] = q[j]
         assert call(_cache(), *q) == sk.ERR_INVALID_ARG, (i, j)
+    need = ctypes.c_int64()
+    assert L.sinkhorn_cache_workspace(ctypes.byref(_cache()), ctypes.byref(need)) == sk.OK and need.value > 0
+    assert L.sinkhorn_cache_workspace(ctypes.byref(_cache(keep=0)), ctypes.byref(need)) == sk.ERR_INVALID_ARG
+    assert L.sinkhorn_cache_workspace(ctypes.byref(_cache()), None) == sk.ERR_INVALID_ARG
+    for kw in (dict(ws=None), dict(n=need.value - 1), dict(ws=ctypes.c_void_p(4104))):
+        assert call(_cache(), *p, **kw) == sk.ERR_INVALID_ARG and b"workspace" in L.sinkhorn_last_error()
     assert call(_cache(batch=0), *([None] * 8)) == sk.OK

@@ -68,8 +68,8 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
 
   const Shape& S = A.S;
   const int64_t pairs = (int64_t)S.batch * S.hkv;
-  const int64_t item = xcd_item(pairs * A.tiles * A.nsplit);
-  if (item >= pairs * A.tiles * A.nsplit) return;
+  const int64_t item = xcd_item(pairs, A.tiles * A.nsplit);
+  if (item < 0) return;
   const int64_t pair = item / (A.tiles * A.nsplit);
   const int64_t rest = item - pair * (A.tiles * A.nsplit);
   const int64_t tile = rest / A.nsplit;
@@ -374,7 +374,7 @@ __global__ __launch_bounds__(256) void k_join(AttendArgs A) {
 // many: 128 rows per workgroup, else all rows in one tile of 32
 template <class T, int DP>
 void attend_launch(const AttendArgs& A, bool many, hipStream_t st) {
-  const int64_t blocks = xcd_blocks((int64_t)A.S.batch * A.S.hkv * A.tiles * A.nsplit);
+  const int64_t blocks = xcd_blocks((int64_t)A.S.batch * A.S.hkv, A.tiles * A.nsplit);
   constexpr int RB = DP * (int)sizeof(T);
   // many rows: two waves a SIMD (three for 64 columns of 16 bits); with fewer
   // registers a wave spills, and half tiles cost more in what each tile

@@ -124,8 +124,8 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
 
   const Shape& S = A.S;
   const int64_t pairs = (int64_t)S.batch * S.hkv;
-  const int64_t item = xcd_item(pairs * A.tiles_q * A.split_q);
-  if (item >= pairs * A.tiles_q * A.split_q) return;
+  const int64_t item = xcd_item(pairs, A.tiles_q * A.split_q);
+  if (item < 0) return;
   const int64_t pair = item / (A.tiles_q * A.split_q);
   const int64_t rest = item - pair * (A.tiles_q * A.split_q);
   const int64_t tile = rest / A.split_q;
@@ -230,8 +230,8 @@ __global__ __launch_bounds__(512, 2) void k_grad_kv(GradArgs A) {
 
   const Shape& S = A.S;
   const int64_t pairs = (int64_t)S.batch * S.hkv;
-  const int64_t item = xcd_item(pairs * A.tiles_kv * A.split_kv);
-  if (item >= pairs * A.tiles_kv * A.split_kv) return;
+  const int64_t item = xcd_item(pairs, A.tiles_kv * A.split_kv);
+  if (item < 0) return;
   const int64_t pair = item / (A.tiles_kv * A.split_kv);
   const int64_t rest = item - pair * (A.tiles_kv * A.split_kv);
   const int64_t tile = rest / A.split_kv;
@@ -407,8 +407,8 @@ __global__ __launch_bounds__(256, 2) void k_grad_kv_one(GradArgs A) {
 
   const Shape& S = A.S;
   const int64_t pairs = (int64_t)S.batch * S.hkv;
-  const int64_t item = xcd_item(pairs * A.tiles_kv * A.split_kv);
-  if (item >= pairs * A.tiles_kv * A.split_kv) return;
+  const int64_t item = xcd_item(pairs, A.tiles_kv * A.split_kv);
+  if (item < 0) return;
   const int64_t pair = item / (A.tiles_kv * A.split_kv);
   const int64_t rest = item - pair * (A.tiles_kv * A.split_kv);
   const int64_t tile = rest / A.split_kv;
@@ -557,11 +557,11 @@ template <class T, int DP>
 void grad_launch(const GradArgs& A, hipStream_t st) {
   const int64_t pairs = (int64_t)A.S.batch * A.S.hkv;
   if (A.S.rows > 0) {
-    hipLaunchKernelGGL((k_grad_q<T, DP>), grid1(xcd_blocks(pairs * A.tiles_q * A.split_q), 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_grad_q<T, DP>), grid1(xcd_blocks(pairs, A.tiles_q * A.split_q), 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   }
   if (A.S.lk > 0) {
-    const int64_t items = xcd_blocks(pairs * A.tiles_kv * A.split_kv);
+    const int64_t items = xcd_blocks(pairs, A.tiles_kv * A.split_kv);
     if constexpr (DP * sizeof(T) == 128)
       hipLaunchKernelGGL((k_grad_kv_one<T, DP>), grid1(items, 256), dim3(256), 0, st, A);
     else

@@ -61,8 +61,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A
 
   const Shape& S = A.S;
   const int64_t pairs = (int64_t)S.batch * S.hkv;
-  const int64_t item = xcd_item(pairs * A.tiles * A.nsplit);
-  if (item >= pairs * A.tiles * A.nsplit) return;
+  const int64_t item = xcd_item(pairs, A.tiles * A.nsplit);
+  if (item < 0) return;
   const int64_t pair = item / (A.tiles * A.nsplit);
   const int64_t rest = item - pair * (A.tiles * A.nsplit);
   const int64_t tile = rest / A.nsplit;
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A
 // Instantiated once per element type (attend_mass_*.hip).
 template <class T>
 void attend_mass(const MassArgs& A, hipStream_t st) {
-  const dim3 grid = grid1(xcd_blocks((int64_t)A.S.batch * A.S.hkv * A.tiles * A.nsplit), 256);
+  const dim3 grid = grid1(xcd_blocks((int64_t)A.S.batch * A.S.hkv, A.tiles * A.nsplit), 256);
   if (A.S.d > 64)
     hipLaunchKernelGGL((k_mass<T, 128>), grid, dim3(256), 0, st, A);
   else

@@ -492,14 +492,24 @@ struct KeyTiles {
   __device__ __forceinline__ bool masked(int n) const { return bias != nullptr || (t0 + n + 1) * KT > nkeys; }
 };
 
-// Workgroup index -> work item, such that each XCD (workgroups go to the 8
-// XCDs in turn) takes one contiguous run of items and neighbouring items,
-// which read the same keys, share its L2. Items at or behind `total`: none.
-__device__ __forceinline__ int64_t xcd_item(int64_t total) {
-  const int64_t per = (total + 7) >> 3;
-  return (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+// Workgroup index -> work item (pair * per + one of the pair's `per`), or -1.
+// Workgroups go to the 8 XCDs in turn, and those that read the same keys should
+// share one's L2. With pairs in multiples of 8 (or many) an XCD takes every
+// eighth pair, so that the heads of a short sequence do not all fall to one XCD;
+// otherwise it takes one contiguous run of the items.
+__host__ __device__ inline bool xcd_by_pair(int64_t pairs) { return pairs % 8 == 0 || pairs >= 64; }
+__device__ __forceinline__ int64_t xcd_item(int64_t pairs, int64_t per) {
+  const int64_t x = blockIdx.x & 7, i = blockIdx.x >> 3;
+  if (xcd_by_pair(pairs)) {
+    const int64_t p = i / per, pair = 8 * p + x;
+    return pair < pairs ? pair * per + (i - p * per) : -1;
+  }
+  const int64_t item = x * ((pairs * per + 7) >> 3) + i;
+  return i < ((pairs * per + 7) >> 3) && item < pairs * per ? item : -1;
 }
-inline int64_t xcd_blocks(int64_t total) { return ((total + 7) >> 3) << 3; }
+inline int64_t xcd_blocks(int64_t pairs, int64_t per) {
+  return xcd_by_pair(pairs) ? 8 * ((pairs + 7) / 8) * per : ((pairs * per + 7) >> 3) << 3;
+}
 
 // Four consecutive elements of a row in memory from fp32; VEC: aligned and d
 // a multiple of four.

@@ -43,14 +43,15 @@ struct AttendArgs {
 constexpr int few_waves(int64_t bytes) { return bytes <= 128 ? 6 : (bytes <= 256 ? 3 : 2); }
 constexpr int few_depth(int64_t bytes) { return bytes <= 256 ? 3 : 2; }
 
-template <class T, int DP, int WQ, int WK, int NB, int D, int OCC>
+template <class T, int W, int WQ, int WK, int NB, int D, int OCC>
 __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
     AttendArgs A) {
+  constexpr int DP = row_width(W);
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
   constexpr int NT = 64 * WQ * WK;
   constexpr int KT = 32 * NB * WK;  // keys per tile
-  constexpr int NS = DP / 16, NDB = DP / 32;
+  constexpr int NS = W / 16, NDB = W / 32;
   // fp32: scores in natural units, rounded once, and 2^(log2e s - m) with the
   // product inside an fma: a weight is off by what its score's own rounding
   // makes it. 16-bit types: log2 units from the start, one operation less.
@@ -58,10 +59,10 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
   constexpr float kTerm = kExact ? 1.0f : (float)kLog2e;
   static_assert(WK == 1 || (WQ == 1 && NB == 1), "few rows: one tile of 32, a wave's own 32 keys");
   using KeyT = KeyTiles<T, DP, KT, NT, D, (WK > 1)>;  // few rows: each key is read by one workgroup
-  constexpr int kJoinBytes = WK > 1 ? WK * 32 * DP * 4 : 0;
+  constexpr int kJoinBytes = WK > 1 ? WK * 32 * W * 4 : 0;
   union Memory {
     typename KeyT::Shared keys;
-    float join[kJoinBytes / 4 + 1];  // [WK][DP][32]
+    float join[kJoinBytes / 4 + 1];  // [WK][W][32]
   };
   __shared__ Memory sm;
   __shared__ f32x2 sml[WK > 1 ? WK * 32 : 1];
@@ -203,7 +204,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
 #pragma unroll
     for (int x = 0; x < NDB; ++x)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) so[(wk * DP + 32 * x + 8 * (e >> 2) + 4 * h + (e & 3)) * 32 + r32] = live_row ? o[x][e] : 0.0f;
+      for (int e = 0; e < 16; ++e) so[(wk * W + 32 * x + 8 * (e >> 2) + 4 * h + (e & 3)) * 32 + r32] = live_row ? o[x][e] : 0.0f;
     __syncthreads();
     // thread: row tid % 32, column groups tid / 32, + NT / 32, ...
     const int64_t jrow = row0 + (tid & 31);
@@ -225,14 +226,14 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
     T* orow = (T*)A.out + b * A.os[0] + ji * A.os[1] + jh * A.os[2];
     float* prow = part ? A.opart + (((int64_t)split * pairs + pair) * S.rows + jrow) * A.dvp : nullptr;
 #pragma unroll
-    for (int it = 0; it < (DP * 8 + NT - 1) / NT; ++it) {
+    for (int it = 0; it < (W * 8 + NT - 1) / NT; ++it) {
       const int c = 4 * ((tid >> 5) + it * (NT / 32));
-      if (c >= DP) break;
+      if (c >= W) break;
       f32x4 x = {0, 0, 0, 0};
 #pragma unroll
       for (int w = 0; w < WK; ++w)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = fmaf(f[w], so[(w * DP + c + e) * 32 + (tid & 31)], x[e]);
+        for (int e = 0; e < 4; ++e) x[e] = fmaf(f[w], so[(w * W + c + e) * 32 + (tid & 31)], x[e]);
       if (part) {
         if (c < A.dvp) *(f32x4*)(prow + c) = x;
       } else {
@@ -372,19 +373,19 @@ __global__ __launch_bounds__(256) void k_join(AttendArgs A) {
 }
 
 // many: 128 rows per workgroup, else all rows in one tile of 32
-template <class T, int DP>
+template <class T, int W>
 void attend_launch(const AttendArgs& A, bool many, hipStream_t st) {
   const int64_t blocks = xcd_blocks((int64_t)A.S.batch * A.S.hkv, A.tiles * A.nsplit);
-  constexpr int RB = DP * (int)sizeof(T);
-  // many rows: two waves a SIMD (three for 64 columns of 16 bits); with fewer
+  constexpr int RB = row_width(W) * (int)sizeof(T);
+  // many rows: two waves a SIMD (three for rows of 128 bytes); with fewer
   // registers a wave spills, and half tiles cost more in what each tile
   // repeats than they gain in occupancy (8192 x 16384 x 32 heads of 128:
   // 2180 us against 5200)
   constexpr int OCC = RB == 128 ? 3 : (RB == 256 ? 2 : 1);
   if (many)
-    hipLaunchKernelGGL((k_attend<T, DP, 4, 1, 2, 2, OCC>), grid1(blocks, 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_attend<T, W, 4, 1, 2, 2, OCC>), grid1(blocks, 256), dim3(256), 0, st, A);
   else
-    hipLaunchKernelGGL((k_attend<T, DP, 1, few_waves(RB), 1, few_depth(RB), RB == 128 ? 2 : 1>),
+    hipLaunchKernelGGL((k_attend<T, W, 1, few_waves(RB), 1, few_depth(RB), RB == 128 ? 2 : 1>),
                        grid1(blocks, 64 * few_waves(RB)), dim3(64 * few_waves(RB)), 0, st, A);
   SK_LAUNCH_CHECK();
 }
@@ -392,10 +393,7 @@ void attend_launch(const AttendArgs& A, bool many, hipStream_t st) {
 // Instantiated once per element type (attend_*.hip).
 template <class T>
 void attend(const AttendArgs& A, bool many, hipStream_t st) {
-  if (A.S.d > 64 || A.S.dv > 64)
-    attend_launch<T, 128>(A, many, st);
-  else
-    attend_launch<T, 64>(A, many, st);
+  by_width(A.S.d, A.S.dv, [&](auto w) { attend_launch<T, decltype(w)::value>(A, many, st); });
   if (A.opart) {
     const int64_t rows = (int64_t)A.S.batch * A.S.hkv * A.S.rows;
     if (A.nsplit >= 8)

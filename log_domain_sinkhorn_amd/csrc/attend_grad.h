@@ -114,11 +114,12 @@ __device__ __forceinline__ void write_cols(const f32x16 (&x)[NDB], float f, floa
 }
 
 // dQ: 4 waves of 32 rows, tiles of KT keys in two LDS buffers (as k_attend).
-template <class T, int DP>
-__global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(GradArgs A) {
+template <class T, int W>
+__global__ __launch_bounds__(256, sizeof(T) * row_width(W) <= 256 ? 2 : 1) void k_grad_q(GradArgs A) {
+  constexpr int DP = row_width(W);
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
-  constexpr int KT = sizeof(T) * DP <= 256 ? 64 : 32, NT = 256, NS = DP / 16, NDB = DP / 32;
+  constexpr int KT = sizeof(T) * DP <= 256 ? 64 : 32, NT = 256, NS = W / 16, NDB = W / 32;
   using KeyT = KeyTiles<T, DP, KT, NT, 2>;
   __shared__ typename KeyT::Shared sm;
 
@@ -216,11 +217,12 @@ __global__ __launch_bounds__(256, sizeof(T) * DP <= 256 ? 2 : 1) void k_grad_q(G
 // 2.4). Tiles of 32 rows in a ring: the second
 // wave's, the first's, and those being loaded (a tile is computed on in less
 // time than memory takes to answer).
-template <class T, int DP>
+template <class T, int W>
 __global__ __launch_bounds__(512, 2) void k_grad_kv(GradArgs A) {
+  constexpr int DP = row_width(W);
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
-  constexpr int RT = 32, NT = 512, NS = DP / 16, NDB = DP / 32;
+  constexpr int RT = 32, NT = 512, NS = W / 16, NDB = W / 32;
   constexpr bool AHEAD = sizeof(T) * DP <= 256;  // registers for it
   constexpr int RING = sizeof(T) * DP <= 256 ? 4 : 3;  // tiles in LDS: fp32 of 128 columns leaves no room for more
   constexpr int kTileBytes = RT * TL::RB;
@@ -396,11 +398,12 @@ __global__ __launch_bounds__(512, 2) void k_grad_kv(GradArgs A) {
 // both accumulators of its 32 keys in less than 256 registers: 4 waves, tiles of
 // 64 rows in two LDS buffers, half the barriers and nothing passed between
 // waves (512 x 1000 x 16 heads x 8, bf16: 5x us against 60).
-template <class T, int DP>
+template <class T, int W>
 __global__ __launch_bounds__(256, 2) void k_grad_kv_one(GradArgs A) {
+  constexpr int DP = row_width(W);
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
-  constexpr int RT = 64, NT = 256, NS = DP / 16, NDB = DP / 32;
+  constexpr int RT = 64, NT = 256, NS = W / 16, NDB = W / 32;
   constexpr int kTileBytes = RT * TL::RB;
   __shared__ __attribute__((aligned(16))) char sm[2][2][kTileBytes];  // q, dout
   __shared__ __attribute__((aligned(16))) f32x2 sstat[2][RT];
@@ -553,19 +556,19 @@ __global__ __launch_bounds__(256) void k_grad_join(GradJoins all) {
     store4<T, false>(orow, c, J.d, x);
 }
 
-template <class T, int DP>
+template <class T, int W>
 void grad_launch(const GradArgs& A, hipStream_t st) {
   const int64_t pairs = (int64_t)A.S.batch * A.S.hkv;
   if (A.S.rows > 0) {
-    hipLaunchKernelGGL((k_grad_q<T, DP>), grid1(xcd_blocks(pairs, A.tiles_q * A.split_q), 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_grad_q<T, W>), grid1(xcd_blocks(pairs, A.tiles_q * A.split_q), 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   }
   if (A.S.lk > 0) {
     const int64_t items = xcd_blocks(pairs, A.tiles_kv * A.split_kv);
-    if constexpr (DP * sizeof(T) == 128)
-      hipLaunchKernelGGL((k_grad_kv_one<T, DP>), grid1(items, 256), dim3(256), 0, st, A);
+    if constexpr (row_width(W) * sizeof(T) == 128)
+      hipLaunchKernelGGL((k_grad_kv_one<T, W>), grid1(items, 256), dim3(256), 0, st, A);
     else
-      hipLaunchKernelGGL((k_grad_kv<T, DP>), grid1(items, 512), dim3(512), 0, st, A);
+      hipLaunchKernelGGL((k_grad_kv<T, W>), grid1(items, 512), dim3(512), 0, st, A);
     SK_LAUNCH_CHECK();
   }
 }
@@ -578,10 +581,7 @@ void attend_grad(const GradArgs& A, hipStream_t st) {
     hipLaunchKernelGGL((k_grad_stat<T>), grid1((pairs * A.rows_pad + 15) / 16, 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   }
-  if (A.S.d > 64 || A.S.dv > 64)
-    grad_launch<T, 128>(A, st);
-  else
-    grad_launch<T, 64>(A, st);
+  by_width(A.S.d, A.S.dv, [&](auto w) { grad_launch<T, decltype(w)::value>(A, st); });
   GradJoins all{};
   all.pairs = pairs;
   all.hkv = A.S.hkv;

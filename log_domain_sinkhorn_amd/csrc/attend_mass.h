@@ -49,11 +49,12 @@ __device__ __forceinline__ f32x2 mass_row(const MassArgs& A, int b, int hk, int6
   return f32x2{t, w * ex2(-lost)};
 }
 
-template <class T, int DP>
+template <class T, int W>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A) {
+  constexpr int DP = row_width(W);
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
-  constexpr int RT = 64, NT = 256, NS = DP / 16;
+  constexpr int RT = 64, NT = 256, NS = W / 16;
   constexpr bool kExact = sizeof(T) == 4;  // scores in natural units, rounded once
   constexpr int kTileBytes = RT * TL::RB;
   __shared__ __attribute__((aligned(16))) char sm[2 * kTileBytes];
@@ -153,10 +154,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A
 template <class T>
 void attend_mass(const MassArgs& A, hipStream_t st) {
   const dim3 grid = grid1(xcd_blocks((int64_t)A.S.batch * A.S.hkv, A.tiles * A.nsplit), 256);
-  if (A.S.d > 64)
-    hipLaunchKernelGGL((k_mass<T, 128>), grid, dim3(256), 0, st, A);
-  else
-    hipLaunchKernelGGL((k_mass<T, 64>), grid, dim3(256), 0, st, A);
+  by_width(A.S.d, 1, [&](auto w) {
+    hipLaunchKernelGGL((k_mass<T, decltype(w)::value>), grid, dim3(256), 0, st, A);
+  });
   SK_LAUNCH_CHECK();
 }
 

@@ -19,6 +19,8 @@
 // {0..3}; the A operand is read from LDS in that order (col_frag).
 #pragma once
 
+#include <type_traits>
+
 #include "internal.h"
 
 namespace sk {
@@ -37,6 +39,20 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kMaxD = 128;         // largest head width
+// Head widths are computed on in units of 32 (W: 32, 64, 96 or 128 columns) and
+// held in LDS in rows of DP = 64 or 128.
+constexpr int row_width(int w) { return w <= 64 ? 64 : 128; }
+inline int head_width(int32_t d, int32_t dv) { return ((d > dv ? d : dv) + 31) / 32 * 32; }
+// f(std::integral_constant<int, W>) for the width of d and dv
+template <class F>
+void by_width(int32_t d, int32_t dv, F&& f) {
+  switch (head_width(d, dv)) {
+    case 32: f(std::integral_constant<int, 32>{}); break;
+    case 64: f(std::integral_constant<int, 64>{}); break;
+    case 96: f(std::integral_constant<int, 96>{}); break;
+    default: f(std::integral_constant<int, 128>{}); break;
+  }
+}
 constexpr float kMasked = -1e30f;  // a bias at or below this masks the key
 constexpr float kInf = __builtin_inff();
 

@@ -120,7 +120,8 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
 #pragma unroll
     for (int s = 0; s < NS; ++s)
 #pragma unroll
-      for (int n = 0; n < NB; ++n) sc[n] = mma(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n]);
+      for (int n = 0; n < NB; ++n) sc[n] = s + 2 < NS ? mma(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n])
+                           : mma_first(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n], S.d - 16 * s);
     float f = kExact ? (float)kLog2e : S.c;  // to log2 units
     if (kExact || A.scores || keys.masked(it)) {
       const float* const term = keys.term(it);

@@ -25,6 +25,8 @@ struct MassArgs {
   const float* mass_in;   // [batch][hkv][lk], nullable: 0
   float* mass_out;        // [batch][hkv][lk], may be mass_in
   float* part;            // [split][batch * hkv][lk], nullable
+  f32x2* stat;            // [batch * hkv][rows_pad]: minus lse (-inf: the row takes no part), weight
+  int64_t rows_pad;       // rows rounded up to 64
   int32_t nsplit;
   int64_t tiles;
   const float* scores;    // of the forward kernel (k_mass_scores)
@@ -50,7 +52,7 @@ __device__ __forceinline__ f32x2 mass_row(const MassArgs& A, int b, int hk, int6
 }
 
 template <class T, int W>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? (W == 96 ? 2 : 3) : 1) void k_mass(MassArgs A) {
   constexpr int DP = row_width(W);
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
@@ -81,20 +83,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A
   const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
 
   RowTiles<T, DP, RT, NT> rows(S, S.q, S.qs, b, hk, S.d, t0, nrows, wave, lane);
-  f32x2 st = {-kInf, 0.0f};  // of row tid: minus its lse, and its weight
-  auto start = [&](int64_t t) { rows.start(S, sm + ((t - t0) & 1) * kTileBytes, wave, lane); };
-  auto stat = [&](int64_t t) {
-    if (tid < RT) {
-      st = mass_row(A, b, hk, t * RT + tid, nrows, kExact);
-      st[0] = -st[0];
-    }
+  auto start = [&](int64_t t) {
+    const int buf = (int)(t - t0) & 1;
+    rows.start(S, sm + buf * kTileBytes, wave, lane);
+    // 64 rows of statistics, 8 bytes each (rows_pad covers the tile)
+    if (wave < 2)
+      dma_load<4>(dma_rsrc(A.stat + pair * A.rows_pad + t * RT), lds_offset(sstat[buf]) + wave * 256, wave * 256 + 4 * lane);
   };
-  if (t0 < t1) {
-    start(t0);
-    stat(t0);
-    if (tid < RT) sstat[0][tid] = st;
-    if (t0 + 1 < t1) stat(t0 + 1);
-  }
   V8 kf[NS];
   {
     const T* krow = (const T*)S.k + b * S.ks[0] + key * S.ks[1] + hk * S.ks[2];
@@ -102,16 +97,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void k_mass(MassArgs A
     for (int s = 0; s < NS; ++s) kf[s] = global_frag<T>(krow, term != -kInf && t0 < t1, s, h, S.d);
   }
   loads_done();
+  if (t0 < t1) start(t0);
   float sum = 0.0f;
   for (int64_t t = t0; t < t1; ++t) {
     const int buf = (int)(t - t0) & 1;
     dma_wait<0>();
     __syncthreads();
-    if (t + 1 < t1) {
-      if (tid < RT) sstat[buf ^ 1][tid] = st;
-      start(t + 1);
-      if (t + 2 < t1) stat(t + 2);
-    }
+    if (t + 1 < t1) start(t + 1);
     const char* tq = sm + buf * kTileBytes;
     // without a bias the column term is 0 for every live key
     auto tile = [&](auto biased) {

@@ -86,6 +86,22 @@ __device__ __forceinline__ f32x16 mma(f32x8 a, f32x8 b, f32x16 c) {
   return c;
 }
 
+// The same where only the first `left` of a lane's k matter (the rest is zero): a
+// wave of fp32 spends 64 cycles on each k, so the zeros behind a width that is
+// no multiple of 16 are left out (50 columns: 26 instructions in place of 32).
+template <class V>
+__device__ __forceinline__ f32x16 mma_first(V a, V b, f32x16 c, int left) {
+  if constexpr (sizeof(a[0]) == 4) {
+    if (left >= 8) return mma(a, b, c);
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < left) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  } else {
+    return mma(a, b, c);
+  }
+}
+
 __device__ __forceinline__ f32x16 zero16() {
   f32x16 z;
 #pragma unroll

@@ -168,6 +168,12 @@ Operand operand(const sinkhorn_attention* a, const void* p, const int64_t* strid
   return o;
 }
 
+struct MassPlan {
+  int64_t tiles, rows_pad;
+  int32_t nsplit;
+  int64_t stat_off, part_off;
+};
+
 struct AttendPlan {
   bool many;     // 128 rows per workgroup (else all rows in tiles of 32)
   bool partial;  // through partial results and k_join
@@ -176,28 +182,34 @@ struct AttendPlan {
   int64_t tiles;
   int64_t score_ld;
   Operand q, k, v;
-  int64_t o_off, ml_off, score_off, mass_off;
-  int32_t mass_split;
-  int64_t mass_tiles;
+  int64_t o_off, ml_off, score_off;
+  MassPlan mass;  // where the weight takes its own pass
   int64_t bytes;
 };
 
-struct MassPlan {
-  int64_t tiles;
-  int32_t nsplit;
-};
 
 bool wide(const sinkhorn_attention* a) { return a->d > 64 || a->dv > 64; }
 // steps of the streamed side that a join costs
 double join_steps(const sinkhorn_attention* a) { return a->dtype == SINKHORN_F32 ? 1.0 : 3.0; }
 
-MassPlan split_mass(const sinkhorn_attention* a) {
+MassPlan plan_weight(const sinkhorn_attention* a, Space& ws) {
   MassPlan p{};
   const int64_t pairs = (int64_t)a->batch * a->heads_kv;
   const int64_t rows = a->len_q * (a->heads_q / a->heads_kv);
   p.tiles = ceil_div(a->len_k, 128);
   p.nsplit = splits(pairs * p.tiles, ceil_div(rows, 64), 768, join_steps(a), false);
+  p.rows_pad = ceil_div(rows, 64) * 64;
+  p.stat_off = ws.take(8 * pairs * p.rows_pad);
+  if (p.nsplit > 1) p.part_off = ws.take(4 * p.nsplit * pairs * a->len_k);
   return p;
+}
+
+void use_plan(const MassPlan& p, char* ws, MassArgs& M) {
+  M.tiles = p.tiles;
+  M.rows_pad = p.rows_pad;
+  M.nsplit = p.nsplit;
+  M.stat = (f32x2*)(ws + p.stat_off);
+  M.part = p.nsplit > 1 ? (float*)(ws + p.part_off) : nullptr;
 }
 
 AttendPlan plan_attend(const sinkhorn_attention* a, const void* q, const void* k, const void* v, bool mass) {
@@ -227,15 +239,10 @@ AttendPlan plan_attend(const sinkhorn_attention* a, const void* q, const void* k
     p.score_off = ws.take(4 * pairs * rows * p.score_ld);
   } else if (mass) {
     // the forward pass is done with its partial results by then
-    const MassPlan m = split_mass(a);
-    p.mass_split = m.nsplit;
-    p.mass_tiles = m.tiles;
-    if (m.nsplit > 1) {
-      Space two;
-      two.bytes = after_copies;
-      p.mass_off = two.take(4 * m.nsplit * pairs * a->len_k);
-      ws.bytes = std::max(ws.bytes, two.bytes);
-    }
+    Space two;
+    two.bytes = after_copies;
+    p.mass = plan_weight(a, two);
+    ws.bytes = std::max(ws.bytes, two.bytes);
   }
   p.bytes = ws.bytes;
   return p;
@@ -279,16 +286,15 @@ GradPlan plan_grad(const sinkhorn_attention* a, const void* q, const void* k, co
 struct WeightPlan {
   MassPlan m;
   Operand q, k;
-  int64_t part_off, bytes;
+  int64_t bytes;
 };
 
 WeightPlan plan_mass(const sinkhorn_attention* a, const void* q, const void* k) {
   WeightPlan p{};
   Space ws;
-  p.m = split_mass(a);
   p.q = operand(a, q, a->q_stride, a->len_q, a->heads_q, a->d, ws);
   p.k = operand(a, k, a->k_stride, a->len_k, a->heads_kv, a->d, ws);
-  if (p.m.nsplit > 1) p.part_off = ws.take(4 * p.m.nsplit * (int64_t)a->batch * a->heads_kv * a->len_k);
+  p.m = plan_weight(a, ws);
   p.bytes = ws.bytes;
   return p;
 }
@@ -375,6 +381,17 @@ void check_workspace(const void* ws, int64_t have, int64_t need) {
 }
 
 // ---------------------------------------------------------------- gathered weight
+// Row statistics of k_mass (natural: as for mass_row).
+__global__ __launch_bounds__(256) void k_mass_stat(MassArgs A, bool natural) {
+  const Shape& S = A.S;
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (idx >= (int64_t)S.batch * S.hkv * A.rows_pad) return;
+  const int64_t pair = idx / A.rows_pad;
+  const int b = (int)(pair / S.hkv);
+  const f32x2 x = mass_row(A, b, (int)(pair - (int64_t)b * S.hkv), idx - pair * A.rows_pad, live_rows(S, b), natural);
+  A.stat[idx] = f32x2{-x[0], x[1]};
+}
+
 __global__ __launch_bounds__(256) void k_mass_join(MassArgs A) {
   const Shape& S = A.S;
   const int64_t n = (int64_t)S.batch * S.hkv * S.lk;
@@ -417,6 +434,11 @@ __global__ __launch_bounds__(256) void k_mass_scores(MassArgs A) {
 }
 
 void run_mass(const sinkhorn_attention* a, MassArgs& A, hipStream_t st) {
+  if (A.S.rows > 0) {
+    hipLaunchKernelGGL(k_mass_stat, grid1(ceil_div((int64_t)A.S.batch * A.S.hkv * A.rows_pad, 256), 256), dim3(256), 0,
+                       st, A, a->dtype == SINKHORN_F32);
+    SK_LAUNCH_CHECK();
+  }
   if (a->dtype == SINKHORN_BF16)
     attend_mass<__bf16>(A, st);
   else if (a->dtype == SINKHORN_F16)
@@ -513,9 +535,7 @@ int sinkhorn_cross_attention(const sinkhorn_attention* a, const void* q, const v
                            dim3(256), 0, st, M);
         SK_LAUNCH_CHECK();
       } else {
-        M.tiles = p.mass_tiles;
-        M.nsplit = p.mass_split;
-        M.part = p.mass_split > 1 ? (float*)(ws + p.mass_off) : nullptr;
+        use_plan(p.mass, ws, M);
         run_mass(a, M, st);
       }
     }
@@ -605,9 +625,7 @@ int sinkhorn_attention_mass(const sinkhorn_attention* a, const void* q, const vo
     M.weight = row_weight;
     M.mass_in = mass_in;
     M.mass_out = mass_out;
-    M.tiles = p.m.tiles;
-    M.nsplit = p.m.nsplit;
-    M.part = p.m.nsplit > 1 ? (float*)(ws + p.part_off) : nullptr;
+    use_plan(p.m, ws, M);
     run_mass(a, M, st);
     return SINKHORN_OK;
   });

@@ -14,8 +14,8 @@
 // Tiles of keys lie in a ring of LDS buffers, filled by loads to LDS while an
 // earlier one is computed on: one barrier per tile and no staging registers,
 // which for many rows (two buffers) leaves two waves a SIMD whose matrix and
-// vector work overlap. With few rows memory is the bound: four buffers keep up
-// to 96 KB per compute unit in flight.
+// vector work overlap. With few rows memory is the bound: three tiles of 48 KB,
+// two of them in flight while one is computed on.
 #pragma once
 
 #include "attention.h"
@@ -30,7 +30,7 @@ struct AttendArgs {
   float* lse;     // [batch][hq][lq]
   float* opart;   // [split][batch * hkv][rows][dvp] unnormalized, nullable
   f32x2* mlpart;  // [split][batch * hkv][rows] running maximum (log2) and sum
-  float* scores;  // [batch * hkv][rows][score_ld] scores in log2 units, nullable
+  float* scores;  // [batch * hkv][rows][score_ld] scores (fp32: natural, else log2 units), nullable
   int64_t score_ld;
   int32_t dvp;     // dv rounded up to 4
   int32_t nsplit;  // splits of the keys
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
       for (int n = 0; n < NB; ++n) sc[n] = s + 2 < NS ? mma(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n])
                            : mma_first(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n], S.d - 16 * s);
     float f = kExact ? (float)kLog2e : S.c;  // to log2 units
-    if (kExact || A.scores || keys.masked(it)) {
+    if (kExact || keys.masked(it)) {
       const float* const term = keys.term(it);
 #pragma unroll
       for (int n = 0; n < NB; ++n)
@@ -137,21 +137,22 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
           }
         }
       if (!kExact) f = 1.0f;
-      if constexpr (WK > 1) {
-        if (A.scores) {
-          // Through this wave's own rows of the k tile, which it is done with, so
-          // that a row's 32 scores go out as one 128-byte line (four 32-byte
-          // pieces of a line each cost 60 of 350 us at 16 x 8 x 32768 keys).
-          char* const mine = const_cast<char*>(tk) + kb0 * TL::RB;
+    }
+    if constexpr (WK > 1) {
+      if (A.scores) {
+        // Through this wave's own rows of the k tile, which it is done with, so
+        // that a row's 32 scores go out as one 128-byte line (361 -> 349 us at
+        // 16 x 8 x 32768 keys against four 32-byte pieces of a line each).
+        const float u = kExact ? 1.0f : f;
+        char* const mine = const_cast<char*>(tk) + kb0 * TL::RB;
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            *(f32x4*)(mine + 128 * r32 + 16 * ((2 * g + h) ^ (r32 & 7))) =
-                f32x4{sc[0][4 * g], sc[0][4 * g + 1], sc[0][4 * g + 2], sc[0][4 * g + 3]};
-          float* const dst = A.scores + pair * S.rows * A.score_ld + (t0 + it) * KT + kb0;
-          for (int r = lane >> 3; r < (int)S.rows; r += 8)
-            *(f32x4*)(dst + r * A.score_ld + 4 * (lane & 7)) =
-                *(const f32x4*)(mine + 128 * r + 16 * ((lane & 7) ^ (r & 7)));
-        }
+        for (int g = 0; g < 4; ++g)
+          *(f32x4*)(mine + 128 * r32 + 16 * ((2 * g + h) ^ (r32 & 7))) =
+              f32x4{sc[0][4 * g] * u, sc[0][4 * g + 1] * u, sc[0][4 * g + 2] * u, sc[0][4 * g + 3] * u};
+        float* const dst = A.scores + pair * S.rows * A.score_ld + (t0 + it) * KT + kb0;
+        for (int r = lane >> 3; r < (int)S.rows; r += 8)
+          *(f32x4*)(dst + r * A.score_ld + 4 * (lane & 7)) =
+              *(const f32x4*)(mine + 128 * r + 16 * ((lane & 7) ^ (r & 7)));
       }
     }
     float mx = -kInf;
@@ -288,8 +289,8 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
 // Joins the splits of a row: 32 lanes per column group of four; GR groups of
 // lanes take every GR-th split and are added in a fixed order, 8 / GR rows per
 // workgroup. Few rows with many splits (decoding) take GR = 8: their loads are
-// then all in flight at once instead of one after the other (15 against 6 us
-// for 15 rows a head and 33 splits).
+// then all in flight at once instead of one after the other (26 -> 4 us for 33
+// splits).
 template <class T, int GR>
 __global__ __launch_bounds__(256) void k_join(AttendArgs A) {
   __shared__ f32x4 so[GR > 1 ? 256 : 1];

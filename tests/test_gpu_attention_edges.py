@@ -1,0 +1,247 @@
+"""Cross attention, its gradient, the gathered weight and cache eviction where
+their launch plans, tiles and loads change: head widths, groups and numbers of
+heads, wide strides, long caches, values that are no numbers, two streams, and
+shapes drawn at random. Plain forms and tolerances: tests/attention_ref.py."""
+import math
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+from attention_ref import Ref, assert_close, evict_ref  # noqa: E402
+
+DEV = "cuda:0"
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+DTYPES = [BF, HF, F32]
+IDS = ["bf16", "fp16", "fp32"]
+
+
+@pytest.fixture(scope="module")
+def sk():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import log_domain_sinkhorn_amd as sk
+
+    return sk
+
+
+def _log(msg):
+    print(msg, file=sys.stderr, flush=True)
+
+
+def _rand(gen, *shape, dtype=F32):
+    return torch.randn(*shape, generator=gen).to(dtype).to(DEV)
+
+
+def _check_all(sk, q, k, v, dout, what, weight=None, mass=None, **kw):
+    """Every entry point on one set of inputs."""
+    B, Lk, Hkv, _ = k.shape
+    got = torch.empty(B, Hkv, Lk, device=DEV)
+    out, lse = sk.cross_attention(q, k, v, row_weight=weight, mass_in=mass, mass_out=got, **kw)
+    ref = Ref(q, k, v, **kw)
+    assert_close(out, ref.out, ref.out_tol, what + " out")
+    assert_close(lse, ref.lse, ref.lse_tol, what + " lse")
+    assert_close(got, *ref.mass(mass, weight), what + " weight")
+    o2, l2 = sk.cross_attention(q, k, v, **kw)
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
+    ref = Ref(q, k, v, lse=lse, **kw)
+    assert_close(sk.attention_mass(q, k, lse, row_weight=weight, mass_in=mass, **kw), *ref.mass(mass, weight),
+                 what + " own pass")
+    for g, (want, tol), name in zip(sk.cross_attention_grad(dout, q, k, v, out, lse, **kw), ref.grads(dout, out),
+                                    ("dq", "dk", "dv")):
+        assert_close(g, want, tol, f"{what} {name}")
+
+
+def _case(dtype, B, Lq, Hq, Hkv, Lk, d, dv, seed, ragged=True):
+    gen = torch.Generator().manual_seed(seed)
+    q, k = _rand(gen, B, Lq, Hq, d, dtype=dtype), _rand(gen, B, Lk, Hkv, d, dtype=dtype)
+    v, dout = _rand(gen, B, Lk, Hkv, dv, dtype=dtype), _rand(gen, B, Lq, Hq, dv, dtype=dtype)
+    kw = {}
+    if ragged:
+        bias = torch.randn(B, Lk, generator=gen)
+        bias[torch.rand(B, Lk, generator=gen) < 0.2] = -math.inf
+        kw = dict(key_bias=bias.to(DEV),
+                  key_lengths=torch.randint(0, Lk + 1, (B,), generator=gen, dtype=torch.int32).to(DEV),
+                  query_lengths=torch.randint(0, Lq + 1, (B,), generator=gen, dtype=torch.int32).to(DEV))
+    extra = dict(weight=torch.rand(B, Lq, generator=gen).to(DEV), mass=torch.rand(B, Hkv, Lk, generator=gen).to(DEV))
+    return (q, k, v, dout), kw, extra
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("d,dv", [(32, 24), (16, 32), (65, 96), (96, 80), (97, 1), (1, 128), (50, 50), (31, 63)])
+def test_head_widths(sk, dtype, d, dv):
+    for Lq in (1, 75):
+        _log(f"widths {dtype} {d} {dv} {Lq}")
+        args, kw, extra = _case(dtype, 2, Lq, 4, 2, 210, d, dv, seed=30)
+        _check_all(sk, *args, f"Lq {Lq}", **kw, **extra)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("Lq,Hq,Hkv", [(60, 5, 1), (45, 6, 2), (20, 48, 1), (3, 96, 1), (11, 33, 1), (1, 40, 1), (1, 64, 2)])
+def test_groups_across_tiles(sk, dtype, Lq, Hq, Hkv):
+    """Query heads a key head that do not divide the tiles of rows, and more of
+    them than a tile holds."""
+    _log(f"groups {dtype} {Lq} {Hq} {Hkv}")
+    args, kw, extra = _case(dtype, 2, Lq, Hq, Hkv, 140, 64, 64, seed=31)
+    _check_all(sk, *args, "group", **kw, **extra)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("B,Hkv", [(13, 5), (8, 1), (3, 3), (64, 1), (9, 8)])
+@pytest.mark.parametrize("Lq", [1, 36])
+def test_numbers_of_heads(sk, dtype, B, Hkv, Lq):
+    """Pairs of batch entry and key head: in eights, more than 64, fewer."""
+    _log(f"pairs {dtype} {B} {Hkv} {Lq}")
+    args, kw, extra = _case(dtype, B, Lq, Hkv, Hkv, 70, 64, 64, seed=32)
+    _check_all(sk, *args, "pairs", **kw, **extra)
+
+
+def _far(t, strides):
+    """t at the given strides (elements) in a buffer of its own."""
+    n = 1 + sum((s - 1) * x for s, x in zip(t.shape, strides))
+    x = torch.empty(n, dtype=t.dtype, device=DEV).as_strided(t.shape, strides)
+    x.copy_(t)
+    return x
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("Lq", [1, 40])
+def test_wide_strides(sk, dtype, Lq):
+    """Rows 16 MB and heads more than 1 GB apart: a tile's offsets would pass
+    31 bits."""
+    _log(f"strides {dtype} {Lq}")
+    (q, k, v, dout), kw, extra = _case(dtype, 1, Lq, 2, 1, 70, 64, 64, seed=33)
+    row = (16 << 20) // q.element_size()
+    want = sk.cross_attention(q, k, v, **kw)
+    grads = sk.cross_attention_grad(dout, q, k, v, *want, **kw)
+    far = lambda t: _far(t, (0, row, 64, 1))  # noqa: E731
+    heads = lambda t: _far(t, (0, 64, (5 << 28) // t.element_size(), 1))  # noqa: E731
+    for move in (far, heads):
+        a = [move(q), move(k), move(v)]
+        got = sk.cross_attention(*a, **kw)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        for x, y in zip(sk.cross_attention_grad(move(dout), *a, *got, **kw), grads):
+            assert torch.equal(x, y)
+        assert torch.equal(sk.attention_mass(a[0], a[1], got[1], **kw), sk.attention_mass(q, k, want[1], **kw))
+    out = far(torch.zeros_like(want[0]))
+    sk.cross_attention(q, k, v, out=out, **kw)
+    assert torch.equal(out, want[0])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_long_sequences_split(sk, dtype):
+    """Keys split over workgroups with sequences of every length, and rows
+    split over them in the backward pass."""
+    for B, Lq, Hq, Hkv, Lk in ((4, 1, 8, 2, 9000), (4, 40, 2, 1, 5000), (2, 3000, 2, 1, 33)):
+        _log(f"split {dtype} {B} {Lq} {Lk}")
+        args, kw, extra = _case(dtype, B, Lq, Hq, Hkv, Lk, 64, 64, seed=34)
+        kw["key_lengths"] = torch.tensor([Lk, 0, 1, Lk // 3][:B], dtype=torch.int32, device=DEV)
+        kw["query_lengths"] = torch.tensor([Lq, Lq, Lq, Lq - 1][:B], dtype=torch.int32, device=DEV)
+        _check_all(sk, *args, "split", **kw, **extra)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("Lq", [1, 50])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_live_values_that_are_no_numbers(sk, dtype, Lq, bad):
+    """What a live key or row holds reaches its own results and no others."""
+    (q, k, v, dout), _, _ = _case(dtype, 2, Lq, 4, 2, 150, 64, 64, seed=35, ragged=False)
+    good = sk.cross_attention(q, k, v)
+    k2 = k.clone()
+    k2[1, 70, 1] = math.nan  # every row of batch entry 1, heads 2 and 3
+    out, lse = sk.cross_attention(q, k2, v)
+    assert bool(torch.isnan(out[1, :, 2:]).all()) and bool(torch.isnan(lse[1, 2:]).all())
+    out[1, :, 2:], lse[1, 2:] = good[0][1, :, 2:], good[1][1, 2:]
+    assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+    v2 = v.clone()
+    v2[0, 149, 0, 5] = bad  # one column of heads 0 and 1
+    out, lse = sk.cross_attention(q, k, v2)
+    assert not bool(torch.isfinite(out[0, :, :2, 5]).any())
+    out[0, :, :2, 5] = good[0][0, :, :2, 5]
+    assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+    q2 = q.clone()
+    q2[0, Lq - 1, 3] = math.nan
+    out, lse = sk.cross_attention(q2, k, v)
+    assert bool(torch.isnan(out[0, Lq - 1, 3]).all()) and bool(torch.isnan(lse[0, 3, Lq - 1]))
+    out[0, Lq - 1, 3], lse[0, 3, Lq - 1] = good[0][0, Lq - 1, 3], good[1][0, 3, Lq - 1]
+    assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+    bias = torch.zeros(2, 150, device=DEV)
+    bias[1, 3] = math.nan  # not masked: it reaches the whole entry
+    out, lse = sk.cross_attention(q, k, v, key_bias=bias)
+    assert bool(torch.isnan(out[1]).all()) and bool(torch.isfinite(out[0]).all())
+
+
+@pytest.mark.parametrize("B,n,H,keep,first,recent", [
+    (2, 16384, 1, 3000, 7, 100), (2, 20001, 2, 9000, 4, 64), (1, 65536, 1, 1, 0, 0), (2, 65537, 1, 30000, 0, 1),
+    (1, 150001, 2, 149999, 11, 13), (3, 90000, 1, 40000, 40000, 0), (1, 70000, 1, 70000, 0, 0),
+])
+def test_evict_long(sk, B, n, H, keep, first, recent):
+    """Each way of selecting: keys in registers, several a thread, streamed."""
+    _log(f"evict {(B, n, H, keep, first, recent)}")
+    gen = torch.Generator().manual_seed(36)
+    k, v = _rand(gen, B, n, H, 8, dtype=BF), _rand(gen, B, n, H, 4, dtype=BF)
+    heavy = torch.exp(3 * torch.randn(B, H, n, generator=gen))
+    ties = torch.randint(0, 3, (B, H, n), generator=gen).float()
+    ties[ties == 0] = -0.0
+    sel = torch.rand(B, H, n, generator=gen)
+    heavy2 = heavy.clone()
+    heavy2[sel < 0.1], heavy2[sel > 0.9], heavy2[(sel > 0.5) & (sel < 0.6)] = math.nan, -math.inf, math.inf
+    lens = torch.randint(0, n + 1, (B,), generator=gen, dtype=torch.int32)
+    lens[-1] = n - 1
+    for mass, ln in ((heavy, None), (ties, lens), (heavy2, lens), (torch.zeros_like(heavy), None)):
+        got = sk.cache_evict(k, v, mass.to(DEV), keep, key_lengths=None if ln is None else ln.to(DEV), first=first,
+                             recent=recent)
+        ko, vo, mo, idx, left = (t.cpu() for t in got)
+        kept = evict_ref(k, v, mass, keep, ln, first, recent)
+        for b in range(B):
+            for h in range(H):
+                want = torch.from_numpy(kept[b][h])
+                c = want.numel()
+                assert int(left[b]) == c
+                assert torch.equal(idx[b, h, :c].long(), want)
+                assert torch.equal(ko[b, :c, h], k.cpu()[b, want, h]) and torch.equal(vo[b, :c, h], v.cpu()[b, want, h])
+                assert torch.equal(mo[b, h, :c].view(torch.int32), mass[b, h, want].view(torch.int32))
+                assert bool((idx[b, h, c:] == -1).all()) and bool((mo[b, h, c:] == 0).all())
+
+
+def test_two_streams_at_once(sk):
+    """Calls on two streams, each with its own workspace, do not meet."""
+    cases = [_case(BF, 2, 1, 8, 2, 6000, 64, 64, seed=37), _case(BF, 2, 90, 8, 2, 400, 64, 64, seed=38)]
+
+    def run(args, kw):
+        q, k, v, dout = args
+        mass = torch.empty(k.shape[0], k.shape[2], k.shape[1], device=DEV)
+        out, lse = sk.cross_attention(q, k, v, mass_out=mass, **kw)
+        return (out, lse, mass) + sk.cross_attention_grad(dout, q, k, v, out, lse, **kw) + tuple(
+            sk.cache_evict(k, v, mass, 150, key_lengths=kw["key_lengths"], recent=4))
+
+    want = [run(a, kw) for a, kw, _ in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(*cases[i][:2]))
+    torch.cuda.synchronize()
+    for w, rounds in zip(want, got):
+        for r in rounds:
+            # index_out and lengths are whole; rows behind a short sequence are zero from the binding
+            assert all(torch.equal(x, y) for x, y in zip(w, r))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn_shapes(sk, dtype, seed):
+    gen = torch.Generator().manual_seed(1000 + seed)
+    pick = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=gen))  # noqa: E731
+    Hkv, G, B = pick(1, 5), pick(1, 9), pick(1, 4)
+    Lq = (1, pick(2, 8), pick(9, 200))[pick(0, 2)]
+    Lk = (pick(1, 70), pick(71, 1500))[pick(0, 1)]
+    d, dv = pick(1, 128), pick(1, 128)
+    _log(f"drawn {dtype} {(B, Lq, Hkv * G, Hkv, Lk, d, dv)}")
+    args, kw, extra = _case(dtype, B, Lq, Hkv * G, Hkv, Lk, d, dv, seed=2000 + seed, ragged=bool(seed % 3))
+    _check_all(sk, *args, "drawn", **kw, **extra)

@@ -30,7 +30,7 @@ struct AttendArgs {
   float* lse;     // [batch][hq][lq]
   float* opart;   // [split][batch * hkv][rows][dvp] unnormalized, nullable
   f32x2* mlpart;  // [split][batch * hkv][rows] running maximum (log2) and sum
-  float* scores;  // [batch * hkv][rows][score_ld] scores (fp32: natural, else log2 units), nullable
+  float* scores;  // [batch * hkv][score_ld / 32][rows][32] scores (fp32: natural, else log2 units), nullable
   int64_t score_ld;
   int32_t dvp;     // dv rounded up to 4
   int32_t nsplit;  // splits of the keys
@@ -149,10 +149,9 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
         for (int g = 0; g < 4; ++g)
           *(f32x4*)(mine + 128 * r32 + 16 * ((2 * g + h) ^ (r32 & 7))) =
               f32x4{sc[0][4 * g] * u, sc[0][4 * g + 1] * u, sc[0][4 * g + 2] * u, sc[0][4 * g + 3] * u};
-        float* const dst = A.scores + pair * S.rows * A.score_ld + (t0 + it) * KT + kb0;
+        float* const dst = A.scores + S.rows * (pair * A.score_ld + (t0 + it) * KT + kb0);
         for (int r = lane >> 3; r < (int)S.rows; r += 8)
-          *(f32x4*)(dst + r * A.score_ld + 4 * (lane & 7)) =
-              *(const f32x4*)(mine + 128 * r + 16 * ((lane & 7) ^ (r & 7)));
+          *(f32x4*)(dst + 32 * r + 4 * (lane & 7)) = *(const f32x4*)(mine + 128 * r + 16 * ((lane & 7) ^ (r & 7)));
       }
     }
     float mx = -kInf;

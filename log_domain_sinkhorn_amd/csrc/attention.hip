@@ -417,9 +417,9 @@ __global__ __launch_bounds__(256) void k_mass_scores(MassArgs A) {
   const float f = A.exact ? (float)kLog2e : 1.0f;
   if (j < nkeys) {
     // the forward kernel wrote whole tiles of the live keys
-    const float* sc = A.scores + pair * S.rows * A.score_ld + j;
+    const float* sc = A.scores + S.rows * (pair * A.score_ld + (j & ~int64_t(31))) + (j & 31);
     for (int r = 0; r < (int)nrows; ++r) {
-      const f32x4 t = *(const f32x4*)(sc + r * A.score_ld);
+      const f32x4 t = *(const f32x4*)(sc + 32 * r);
       const f32x2 st = srow[r];
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = fmaf(st[1], ex2((t[e] - st[0]) * f), x[e]);

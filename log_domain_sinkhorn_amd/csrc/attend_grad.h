@@ -28,7 +28,7 @@ struct GradArgs {
   void* dq;
   void* dk;
   void* dv;
-  f32x2* stat;       // [batch * hkv][rows_pad]: minus lse (-inf: the row takes no part), D
+  f32x2* stat;       // [batch * hkv][rows_pad] from k_grad_q: minus lse (-inf: the row takes no part), D
   int64_t rows_pad;  // rows rounded up to 64
   float* part_q;  // [split][batch * hkv][rows][dp], nullable
   float* part_k;  // [split][batch * hkv][lk][dp], nullable
@@ -37,50 +37,8 @@ struct GradArgs {
   int32_t split_q, split_kv;
   int64_t tiles_q, tiles_kv;
   bool vec_q, vec_k, vec_v;  // dq, dk, dv may be written four elements at a time
-  bool stat_vec;             // out and dout may be read 16 bytes at a time
+  bool out_vec;              // out may be read 16 bytes at a time
 };
-
-// Row statistics: 16 lanes per row. The lse is kept in natural units for fp32
-// and in log2 units for the 16-bit types.
-template <class T>
-__global__ __launch_bounds__(256) void k_grad_stat(GradArgs A) {
-  const Shape& S = A.S;
-  const int64_t idx = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  if (idx >= (int64_t)S.batch * S.hkv * A.rows_pad) return;
-  const int64_t pair = idx / A.rows_pad, row = idx - pair * A.rows_pad;
-  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
-  const int64_t qi = row / S.group;
-  const int qh = hk * S.group + (int)(row - qi * S.group);
-  const int ln = threadIdx.x & 15;
-  if (row >= live_rows(S, b)) {
-    if (ln == 0) A.stat[idx] = f32x2{-kInf, 0.0f};
-    return;
-  }
-  const T* o = (const T*)A.out + b * A.os[0] + qi * A.os[1] + qh * A.os[2];
-  const T* g = (const T*)A.dout + b * A.dos[0] + qi * A.dos[1] + qh * A.dos[2];
-  float s = 0.0f;
-  if (A.stat_vec) {  // 16-byte chunks
-    constexpr int EPC = 16 / (int)sizeof(T);
-    for (int c = ln * EPC; c < S.dv; c += 16 * EPC) {
-      union {
-        u32x4 u;
-        T e[EPC];
-      } x, y;
-      x.u = *(const u32x4*)(o + c);
-      y.u = *(const u32x4*)(g + c);
-#pragma unroll
-      for (int e = 0; e < EPC; ++e) s = fmaf((float)x.e[e], (float)y.e[e], s);
-    }
-  } else {
-    for (int c = ln; c < S.dv; c += 16) s = fmaf((float)o[c], (float)g[c], s);
-  }
-#pragma unroll
-  for (int x = 8; x > 0; x >>= 1) s += __shfl_xor(s, x, 16);
-  if (ln == 0) {
-    const float e = A.lse[((int64_t)b * S.hq + qh) * S.lq + qi];
-    A.stat[idx] = e == -kInf ? f32x2{-kInf, 0.0f} : f32x2{sizeof(T) == 4 ? -e : -e * (float)kLog2e, s};
-  }
-}
 
 // exp(score - lse) of a product x, its column term (if it has one) and minus the
 // row's lse.
@@ -113,7 +71,11 @@ __device__ __forceinline__ void write_cols(const f32x16 (&x)[NDB], float f, floa
     }
 }
 
-// dQ: 4 waves of 32 rows, tiles of KT keys in two LDS buffers (as k_attend).
+// dQ: 4 waves of 32 rows, tiles of KT keys in two LDS buffers (as k_attend). It
+// also makes the rows' statistics for k_grad_kv, as it holds dout anyway: minus
+// the lse (natural units for fp32, log2 units for the 16-bit types) and D (a
+// kernel of its own took 7 of 110 us at 512 x 1000 x 16 heads x 8, bf16, and one
+// of seven launches).
 template <class T, int W>
 __global__ __launch_bounds__(256, sizeof(T) * row_width(W) <= 256 ? 2 : 1) void k_grad_q(GradArgs A) {
   constexpr int DP = row_width(W);
@@ -157,7 +119,30 @@ __global__ __launch_bounds__(256, sizeof(T) * row_width(W) <= 256 ? 2 : 1) void 
       gf[s] = global_frag<T>(grow, live_row && t0 < t1, s, h, S.dv);
     }
   }
-  const f32x2 st = live_row ? A.stat[pair * A.rows_pad + row] : f32x2{-kInf, 0.0f};
+  f32x2 st = {-kInf, 0.0f};
+  if (live_row && t0 < t1) {
+    const T* orow = (const T*)A.out + b * A.os[0] + qi * A.os[1] + qh * A.os[2];
+    const float e = A.lse[((int64_t)b * S.hq + qh) * S.lq + qi];
+    float dot = 0.0f;
+    if (A.out_vec) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const V8 x = global_frag<T>(orow, true, s, h, S.dv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot = fmaf((float)x[i], (float)gf[s][i], dot);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (16 * s + 8 * h + i < S.dv) dot = fmaf((float)orow[16 * s + 8 * h + i], (float)gf[s][i], dot);
+    }
+    dot = half_sum(dot);  // both lanes of a row are here
+    if (e != -kInf) st = f32x2{sizeof(T) == 4 ? -e : -e * (float)kLog2e, dot};
+  }
+  // for k_grad_kv; a tile without live rows or keys is not read there
+  if (split == 0 && h == 0 && row < A.rows_pad) A.stat[pair * A.rows_pad + row] = st;
   loads_done();
   f32x16 dq[NDB];
 #pragma unroll
@@ -397,7 +382,7 @@ __global__ __launch_bounds__(512, 2) void k_grad_kv(GradArgs A) {
 // The same for 64 columns of 16 bits, where one wave holds both operands and
 // both accumulators of its 32 keys in less than 256 registers: 4 waves, tiles of
 // 64 rows in two LDS buffers, half the barriers and nothing passed between
-// waves (512 x 1000 x 16 heads x 8, bf16: 5x us against 60).
+// waves (512 x 1000 x 16 heads x 8, bf16: 48 us against 60).
 template <class T, int W>
 __global__ __launch_bounds__(256, 2) void k_grad_kv_one(GradArgs A) {
   constexpr int DP = row_width(W);
@@ -577,10 +562,6 @@ void grad_launch(const GradArgs& A, hipStream_t st) {
 template <class T>
 void attend_grad(const GradArgs& A, hipStream_t st) {
   const int64_t pairs = (int64_t)A.S.batch * A.S.hkv;
-  if (A.S.rows > 0) {
-    hipLaunchKernelGGL((k_grad_stat<T>), grid1((pairs * A.rows_pad + 15) / 16, 256), dim3(256), 0, st, A);
-    SK_LAUNCH_CHECK();
-  }
   by_width(A.S.d, A.S.dv, [&](auto w) { grad_launch<T, decltype(w)::value>(A, st); });
   GradJoins all{};
   all.pairs = pairs;

@@ -595,7 +595,7 @@ int sinkhorn_cross_attention_grad(const sinkhorn_attention* a, const void* q, co
     A.vec_q = rows_aligned(dq, a->dq_stride, a->d, size, 4 * size);
     A.vec_k = rows_aligned(dk, a->dk_stride, a->d, size, 4 * size);
     A.vec_v = rows_aligned(dv, a->dv_stride, a->dv, size, 4 * size);
-    A.stat_vec = rows_aligned(out, A.os, a->dv, size, 16) && rows_aligned(A.dout, A.dos, a->dv, size, 16);
+    A.out_vec = rows_aligned(out, A.os, a->dv, size, 16);
     if (a->dtype == SINKHORN_BF16)
       attend_grad<__bf16>(A, st);
     else if (a->dtype == SINKHORN_F16)

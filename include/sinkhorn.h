@@ -509,7 +509,8 @@ int sinkhorn_attention_workspace(const sinkhorn_attention* at, int32_t what, con
  * (mass_in nullable: 0, and may be mass_out; row_weight nullable: 1). When all
  * rows of a key head (len_q * heads_q / heads_kv) are at most 32, as for single
  * tokens, the weight comes from the scores of the same pass and the keys are
- * read once. out may not be an input. */
+ * read once. out and lse may not overlap an input, nor mass_out one other than
+ * mass_in. */
 int sinkhorn_cross_attention(const sinkhorn_attention* at, const void* q, const void* k,
                              const void* v, void* out, float* lse, const float* row_weight,
                              const float* mass_in, float* mass_out, void* workspace,
@@ -550,8 +551,8 @@ typedef struct {
  * the kept rows, mass_out [batch][heads][cap] their weights and index_out
  * [batch][heads][cap] the positions they had; lengths_out [batch] the number
  * kept. Behind that number k_out and v_out are left as they were, mass_out is
- * 0 and index_out -1. Outputs may not overlap inputs or each other. d and dv
- * are not limited to 128. Asynchronous on `stream`. */
+ * 0 and index_out -1. Outputs may not overlap inputs or each other (lengths_out
+ * is no key_lengths). d and dv are not limited to 128. Asynchronous on `stream`. */
 int sinkhorn_cache_evict(const sinkhorn_cache* cache, const void* k, const void* v,
                          const float* mass, void* k_out, void* v_out, float* mass_out,
                          int32_t* index_out, int32_t* lengths_out, void* workspace,

@@ -569,7 +569,11 @@ inline bool rows_aligned(const void* p, const int64_t* stride, int64_t width, in
          width % q == 0;
 }
 
-
+// Have two arrays of n and m bytes no byte in common? (a null one has none)
+inline bool apart(const void* a, int64_t n, const void* b, int64_t m) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x == 0 || y == 0 || x + (uintptr_t)n <= y || y + (uintptr_t)m <= x;
+}
 
 }  // namespace attn
 }  // namespace sk

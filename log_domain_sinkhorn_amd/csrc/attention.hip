@@ -374,6 +374,15 @@ void place(const sinkhorn_attention* a, std::initializer_list<Placed> operands, 
   SK_LAUNCH_CHECK();
 }
 
+// The contiguous fp32 outputs against each other and their inputs.
+void check_mass(const sinkhorn_attention* a, const float* lse, const float* row_weight, const float* mass_in,
+                const float* mass_out) {
+  const int64_t rows = 4 * (int64_t)a->batch * a->len_q, mass = 4 * (int64_t)a->batch * a->heads_kv * a->len_k;
+  const int64_t stat = rows * a->heads_q;
+  require(mass_in == mass_out || apart(mass_in, mass, mass_out, mass), "mass_out overlaps mass_in without being it");
+  require(apart(row_weight, rows, mass_out, mass) && apart(lse, stat, mass_out, mass), "mass_out overlaps another argument");
+}
+
 void check_workspace(const void* ws, int64_t have, int64_t need) {
   if (need == 0) return;
   require(ws != nullptr && have >= need, "workspace too small (sinkhorn_attention_workspace)");
@@ -490,6 +499,11 @@ int sinkhorn_cross_attention(const sinkhorn_attention* a, const void* q, const v
             "mass_in and row_weight need mass_out");
     require(out == nullptr || (out != q && out != k && out != v), "output aliases an input");
     const bool mass = mass_out != nullptr && keys;
+    check_mass(a, lse, row_weight, mass_in, mass_out);
+    require(apart(lse, 4 * (int64_t)a->batch * a->heads_q * a->len_q, mass_in,
+                  4 * (int64_t)a->batch * a->heads_kv * a->len_k) &&
+                apart(lse, 4 * (int64_t)a->batch * a->heads_q * a->len_q, row_weight, 4 * (int64_t)a->batch * a->len_q),
+            "lse overlaps an input");
     const AttendPlan p = plan_attend(a, q, k, v, mass);
     check_workspace(workspace, workspace_bytes, p.bytes);
     const hipStream_t st = (hipStream_t)stream;
@@ -614,6 +628,7 @@ int sinkhorn_attention_mass(const sinkhorn_attention* a, const void* q, const vo
     if (a->batch == 0 || a->len_k == 0) return SINKHORN_OK;
     require(mass_out != nullptr, "null pointer");
     require(a->len_q == 0 || (q && k && lse), "null pointer");
+    check_mass(a, lse, row_weight, mass_in, mass_out);
     const WeightPlan p = plan_mass(a, q, k);
     check_workspace(workspace, workspace_bytes, p.bytes);
     const hipStream_t st = (hipStream_t)stream;

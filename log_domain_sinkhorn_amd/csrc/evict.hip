@@ -13,7 +13,8 @@
 // all that can be done by others is: k_evict_move (one workgroup per 256 keys)
 // takes the threshold and those counts, finds its kept keys' places and copies
 // their rows, bound by memory (4 x 8 x 65536 keys to 16384, rows of 128 bf16: with
-// the places found by k_evict_select it took 78 us in place of 3x).
+// the places found by k_evict_select that one took 78 us in place of 27; k_evict_move
+// takes 112).
 #include "attention.h"
 
 namespace sk {
@@ -295,15 +296,15 @@ void require(bool ok, const char* what) {
 }
 
 void check(const sinkhorn_cache* c) {
-    require(c != nullptr, "null cache description");
-    require(c->dtype == SINKHORN_F32 || c->dtype == SINKHORN_F16 || c->dtype == SINKHORN_BF16, "unknown dtype");
-    require(c->batch >= 0 && c->heads >= 1 && c->len >= 0 && c->d >= 1 && c->dv >= 1, "bad sizes");
-    require(c->len < (int64_t(1) << 31), "len must be below 2^31");
-    require(c->keep >= 1 && c->first >= 0 && c->recent >= 0, "keep must be >= 1, first and recent >= 0");
-    require(c->first <= c->keep && c->recent <= c->keep - c->first, "first + recent exceed keep");
-    for (int i = 0; i < 3; ++i)
-      require(c->k_stride[i] >= 0 && c->v_stride[i] >= 0 && c->k_out_stride[i] >= 0 && c->v_out_stride[i] >= 0,
-              "negative stride");
+  require(c != nullptr, "null cache description");
+  require(c->dtype == SINKHORN_F32 || c->dtype == SINKHORN_F16 || c->dtype == SINKHORN_BF16, "unknown dtype");
+  require(c->batch >= 0 && c->heads >= 1 && c->len >= 0 && c->d >= 1 && c->dv >= 1, "bad sizes");
+  require(c->len < (int64_t(1) << 31), "len must be below 2^31");
+  require(c->keep >= 1 && c->first >= 0 && c->recent >= 0, "keep must be >= 1, first and recent >= 0");
+  require(c->first <= c->keep && c->recent <= c->keep - c->first, "first + recent exceed keep");
+  for (int i = 0; i < 3; ++i)
+    require(c->k_stride[i] >= 0 && c->v_stride[i] >= 0 && c->k_out_stride[i] >= 0 && c->v_out_stride[i] >= 0,
+            "negative stride");
 }
 
 int64_t space(const sinkhorn_cache* c) {
@@ -337,7 +338,15 @@ int sinkhorn_cache_evict(const sinkhorn_cache* c, const void* k, const void* v, 
     require(lengths_out != nullptr, "null pointer");
     if (c->len > 0) {
       require(k && v && mass && k_out && v_out && mass_out && index_out, "null pointer");
-      require(k_out != k && v_out != v && k_out != v_out && mass_out != mass, "output aliases an input");
+      const int64_t pairs = (int64_t)c->batch * c->heads, in = 4 * pairs * c->len;
+      const int64_t out = 4 * pairs * (c->keep < c->len ? c->keep : c->len), lengths = 4 * (int64_t)c->batch;
+      require(k_out != k && k_out != v && v_out != v && v_out != k && k_out != v_out, "output aliases an input");
+      // all of them are read by workgroups that run while others write (lengths_out in place of key_lengths, say)
+      require(apart(mass, in, mass_out, out) && apart(mass, in, index_out, out) && apart(mass, in, lengths_out, lengths) &&
+                  apart(c->key_lengths, lengths, lengths_out, lengths) && apart(c->key_lengths, lengths, mass_out, out) &&
+                  apart(c->key_lengths, lengths, index_out, out) && apart(mass_out, out, index_out, out) &&
+                  apart(mass_out, out, lengths_out, lengths) && apart(index_out, out, lengths_out, lengths),
+              "an output overlaps an input or another output");
     }
     require(workspace_bytes >= space(c) && (space(c) == 0 || workspace != nullptr),
             "workspace too small (sinkhorn_cache_workspace)");

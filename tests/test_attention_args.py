@@ -191,3 +191,32 @@ def test_cache_descriptions_are_refused():
     for kw in (dict(ws=None), dict(n=need.value - 1), dict(ws=ctypes.c_void_p(4104))):
         assert call(_cache(), *p, **kw) == sk.ERR_INVALID_ARG and b"workspace" in L.sinkhorn_last_error()
     assert call(_cache(batch=0), *([None] * 8)) == sk.OK
+
+
+def test_overlapping_side_outputs_are_refused():
+    """Arrays that some workgroups read while others write."""
+    L = sk.lib()
+    at = lambda x: ctypes.c_void_p(x)  # noqa: E731
+    a = _desc()  # weights of 2 * 2 * 1000 floats, lse of 2 * 4 * 3, row weights of 2 * 3
+    for kw in (dict(mi=at(1 << 20), mo=at((1 << 20) + 16000 - 4)), dict(mi=at((1 << 20) + 4), mo=at(1 << 20)),
+               dict(mo=at(1 << 20), lse=at((1 << 20) + 15996)), dict(mo=at(1 << 20), lse=at((1 << 20) - 92)),
+               dict(mo=at(1 << 20), w=at((1 << 20) + 96)), dict(mo=at(1 << 20), mi=at(1 << 21), lse=at((1 << 21) + 32)),
+               dict(mo=at(1 << 20), w=at(1 << 21), lse=at((1 << 21) + 20))):
+        assert _forward(a, **kw) == sk.ERR_INVALID_ARG and b"overlaps" in L.sinkhorn_last_error(), kw
+    for kw in (dict(mi=at(1 << 20), mo=at(1 << 20)), dict(mi=at(1 << 20), mo=at((1 << 20) + 16000)),
+               dict(mo=at(1 << 20), lse=at((1 << 20) - 96), w=at((1 << 20) + 16000))):
+        assert _forward(a, **kw) == sk.ERR_INVALID_ARG and b"workspace" in L.sinkhorn_last_error(), kw
+    own = lambda lse, w, mi, mo: L.sinkhorn_attention_mass(ctypes.byref(a), FAKE, FAKE, lse, w, mi, mo, None, 0, None)  # noqa: E731
+    assert own(at(1 << 20), None, None, at(1 << 20)) == sk.ERR_INVALID_ARG and b"overlaps" in L.sinkhorn_last_error()
+    assert own(FAKE, None, at((1 << 20) + 64), at(1 << 20)) == sk.ERR_INVALID_ARG and b"overlaps" in L.sinkhorn_last_error()
+    # k, v, mass, k_out, v_out, mass_out, index_out, lengths_out
+    p = [at(1 << (20 + i)) for i in range(8)]
+    lens = at(1 << 30)
+    evict = lambda c, *x: L.sinkhorn_cache_evict(ctypes.byref(c), *x, None, 0, None)  # noqa: E731
+    for i, x in ((7, 1 << 30), (5, (1 << 22) + 796), (6, 1 << 22), (7, (1 << 22) + 8), (6, (1 << 25) + 76), (7, 1 << 25),
+                 (7, (1 << 26) + 40), (5, (1 << 30) - 76), (3, 1 << 21), (4, 1 << 20)):
+        q = list(p)
+        q[i] = at(x)
+        assert evict(_cache(key_lengths=lens), *q) == sk.ERR_INVALID_ARG, (i, x)
+        assert b"overlaps" in L.sinkhorn_last_error() or b"aliases" in L.sinkhorn_last_error(), (i, x)
+    assert evict(_cache(key_lengths=lens), *p) == sk.ERR_INVALID_ARG and b"workspace" in L.sinkhorn_last_error()

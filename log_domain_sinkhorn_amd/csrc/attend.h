@@ -18,6 +18,7 @@
 // two of them in flight while one is computed on.
 #pragma once
 
+#include "attend_mass.h"
 #include "attention.h"
 
 namespace sk {
@@ -291,13 +292,13 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
 // then all in flight at once instead of one after the other (26 -> 4 us for 33
 // splits).
 template <class T, int GR>
-__global__ __launch_bounds__(256) void k_join(AttendArgs A) {
+__device__ __forceinline__ void join_rows(const AttendArgs& A, int64_t blk) {
   __shared__ f32x4 so[GR > 1 ? 256 : 1];
   __shared__ f32x2 sml[GR > 1 ? 8 : 1];
   const Shape& S = A.S;
   const int64_t n = (int64_t)S.batch * S.hkv * S.rows;  // rows in all
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
-  const int64_t idx = (int64_t)blockIdx.x * (8 / GR) + grp / GR;
+  const int64_t idx = blk * (8 / GR) + grp / GR;
   const bool live = idx < n;
   const int c = 4 * lane;
   // maximum over this group's splits, then over the groups
@@ -373,6 +374,44 @@ __global__ __launch_bounds__(256) void k_join(AttendArgs A) {
   if (c == 0) A.lse[((int64_t)b * S.hq + qh) * S.lq + qi] = log_sum(mm, ll);
 }
 
+template <class T, int GR>
+__global__ __launch_bounds__(256) void k_join(AttendArgs A) {
+  join_rows<T, GR>(A, blockIdx.x);
+}
+
+// The join and, in the workgroups behind its `joins`, the gathered weight. These
+// take a row's reference and sum from the splits themselves: 8 lanes a row.
+template <class T, int GR>
+__global__ __launch_bounds__(256) void k_join_weight(AttendArgs A, MassArgs M, int64_t joins) {
+  if (blockIdx.x < joins) {
+    join_rows<T, GR>(A, blockIdx.x);
+    return;
+  }
+  weight_keys(M, blockIdx.x - joins, 0.0f, [&](f32x2* srow, int64_t pair, int b, int, int64_t nrows) {
+    const Shape& S = A.S;
+    const int r = threadIdx.x >> 3, ln = threadIdx.x & 7;
+    const int64_t n = (int64_t)S.batch * S.hkv * S.rows, idx = pair * S.rows + r;
+    const bool live = r < nrows;
+    float mm = -kInf, ll = 0.0f;
+    if (live)
+      for (int s = ln; s < A.nsplit; s += 8) mm = fmaxf(mm, A.mlpart[s * n + idx][0]);
+#pragma unroll
+    for (int x = 4; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor(mm, x, 8));
+    const float mu = mm == -kInf ? 0.0f : mm;
+    if (live)
+      for (int s = ln; s < A.nsplit; s += 8) {
+        const f32x2 p = A.mlpart[s * n + idx];
+        ll = fmaf(ex2(p[0] - mu), p[1], ll);
+      }
+#pragma unroll
+    for (int x = 4; x > 0; x >>= 1) ll += __shfl_xor(ll, x, 8);
+    if (ln == 0) {
+      const float w = live && M.weight ? M.weight[b * S.lq + r / S.group] : 1.0f;
+      srow[r] = f32x2{mu, ll == 0.0f ? 0.0f : w / ll};
+    }
+  });
+}
+
 // many: 128 rows per workgroup, else all rows in one tile of 32
 template <class T, int W>
 void attend_launch(const AttendArgs& A, bool many, hipStream_t st) {
@@ -391,18 +430,26 @@ void attend_launch(const AttendArgs& A, bool many, hipStream_t st) {
   SK_LAUNCH_CHECK();
 }
 
-// Instantiated once per element type (attend_*.hip).
+// Instantiated once per element type (attend_*.hip). M: the gathered weight from
+// the scores, where the keys are split (else null).
 template <class T>
-void attend(const AttendArgs& A, bool many, hipStream_t st) {
+void attend(const AttendArgs& A, bool many, const MassArgs* M, hipStream_t st) {
   by_width(A.S.d, A.S.dv, [&](auto w) { attend_launch<T, decltype(w)::value>(A, many, st); });
-  if (A.opart) {
-    const int64_t rows = (int64_t)A.S.batch * A.S.hkv * A.S.rows;
-    if (A.nsplit >= 8)
-      hipLaunchKernelGGL((k_join<T, 8>), grid1(rows, 256), dim3(256), 0, st, A);
+  if (!A.opart) return;
+  const int64_t rows = (int64_t)A.S.batch * A.S.hkv * A.S.rows;
+  auto join = [&](auto gr) {
+    constexpr int GR = decltype(gr)::value;
+    const int64_t blocks = GR == 8 ? rows : (rows + 7) / 8;
+    if (M)
+      hipLaunchKernelGGL((k_join_weight<T, GR>), grid1(blocks + weight_blocks(*M), 256), dim3(256), 0, st, A, *M, blocks);
     else
-      hipLaunchKernelGGL((k_join<T, 1>), grid1((rows + 7) / 8, 256), dim3(256), 0, st, A);
+      hipLaunchKernelGGL((k_join<T, GR>), grid1(blocks, 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
-  }
+  };
+  if (A.nsplit >= 8)
+    join(std::integral_constant<int, 8>{});
+  else
+    join(std::integral_constant<int, 1>{});
 }
 
 }  // namespace attn

@@ -7,8 +7,10 @@
 // sums are added in split order by k_mass_join. No atomics.
 //
 // For a single tile of rows (decoding) the forward kernel leaves its scores in
-// a workspace and k_mass_scores reads those: keys are then read once from
-// memory, by the forward pass.
+// a workspace and weight_keys reads those: keys are then read once from memory,
+// by the forward pass. Where that was split, it runs beside the join of the
+// splits (attend.h), from the splits' references and sums: one launch less
+// (24 -> 21 us for 5 x 4097 x 12 heads x 3).
 #pragma once
 
 #include <type_traits>
@@ -29,9 +31,10 @@ struct MassArgs {
   int64_t rows_pad;       // rows rounded up to 64
   int32_t nsplit;
   int64_t tiles;
-  const float* scores;    // of the forward kernel (k_mass_scores)
+  const float* scores;    // of the forward kernel, nullable
   int64_t score_ld;
   bool exact;             // scores in natural units (fp32), else log2 units
+  bool deal;              // weight_keys: 256 keys and four groups of rows a workgroup, else 1024 keys
 };
 
 // A row's log-sum-exp (+inf: the row takes no part) and weight. In log2 units
@@ -49,6 +52,61 @@ __device__ __forceinline__ f32x2 mass_row(const MassArgs& A, int b, int hk, int6
   const float t = e * (float)kLog2e;
   const float lost = fmaf(e, (float)kLog2e, -t) + e * (float)(kLog2e - (double)(float)kLog2e);
   return f32x2{t, w * ex2(-lost)};
+}
+
+// The weight of block `blk`'s keys from the forward kernel's scores of the pair's
+// rows (32 at most), four keys a thread: 1024 keys, or, where that leaves the chip
+// empty, 256 with the rows dealt to four groups of 64 threads (16 x 8 x 32768
+// keys, 4 rows: join and weight 21 us with 1024 keys, 30 with 256; 3 x 4 x 4097
+// keys, 15 rows: 5.3 us with 256, with 1024 the weight alone took 6.2). rows(...) puts each row's reference (log2 units)
+// and the factor of its weights into LDS. lo: what the fp32 log2e misses, where
+// the references were made without that loss (else it cancels).
+template <class F>
+__device__ __forceinline__ void weight_keys(const MassArgs& A, int64_t blk, float lo, F&& rows) {
+  __shared__ f32x2 srow[32];
+  __shared__ f32x4 sx[3][64];
+  const Shape& S = A.S;
+  const bool deal = A.deal;
+  const int64_t chunks = (S.lk + (deal ? 255 : 1023)) / (deal ? 256 : 1024);
+  const int64_t pair = blk / chunks;
+  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
+  const int t = threadIdx.x & 63, g = threadIdx.x >> 6, step = deal ? 4 : 1;
+  const int64_t j = (blk - pair * chunks) * (deal ? 256 : 1024) + 4 * (deal ? t : (int)threadIdx.x);
+  const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
+  rows(srow, pair, b, hk, nrows);
+  __syncthreads();
+  f32x4 x = {0, 0, 0, 0};
+  const float f = A.exact ? (float)kLog2e : 1.0f;
+  if (j < nkeys) {
+    // the forward kernel wrote whole tiles of the live keys
+    const float* sc = A.scores + S.rows * (pair * A.score_ld + (j & ~int64_t(31))) + (j & 31);
+    for (int r = deal ? g : 0; r < (int)nrows; r += step) {
+      const f32x4 v = *(const f32x4*)(sc + 32 * r);
+      const f32x2 st = srow[r];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = fmaf(st[1], ex2(fmaf(v[e], f, lo > 0.0f ? fmaf(v[e], lo, -st[0]) : -st[0])), x[e]);
+    }
+  }
+  if (deal) {
+    if (g > 0) sx[g - 1][t] = x;
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const f32x4 y = sx[k][t];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] += y[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (j + e < S.lk) {
+      const int64_t i = pair * S.lk + j + e;
+      A.mass_out[i] = (A.mass_in ? A.mass_in[i] : 0.0f) + (j + e < nkeys ? x[e] : 0.0f);
+    }
+}
+inline int64_t weight_blocks(const MassArgs& A) {
+  return (int64_t)A.S.batch * A.S.hkv * ((A.S.lk + (A.deal ? 255 : 1023)) / (A.deal ? 256 : 1024));
 }
 
 template <class T, int W>

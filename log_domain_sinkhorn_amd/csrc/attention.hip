@@ -11,9 +11,9 @@
 namespace sk {
 namespace attn {
 
-extern template void attend<__bf16>(const AttendArgs&, bool, hipStream_t);
-extern template void attend<_Float16>(const AttendArgs&, bool, hipStream_t);
-extern template void attend<float>(const AttendArgs&, bool, hipStream_t);
+extern template void attend<__bf16>(const AttendArgs&, bool, const MassArgs*, hipStream_t);
+extern template void attend<_Float16>(const AttendArgs&, bool, const MassArgs*, hipStream_t);
+extern template void attend<float>(const AttendArgs&, bool, const MassArgs*, hipStream_t);
 extern template void attend_grad<__bf16>(const GradArgs&, hipStream_t);
 extern template void attend_grad<_Float16>(const GradArgs&, hipStream_t);
 extern template void attend_grad<float>(const GradArgs&, hipStream_t);
@@ -411,35 +411,14 @@ __global__ __launch_bounds__(256) void k_mass_join(MassArgs A) {
   A.mass_out[i] = (A.mass_in ? A.mass_in[i] : 0.0f) + x;
 }
 
-// From the forward kernel's scores: rows <= 32, four keys a thread.
+// From the scores of a forward pass whose keys were not split, and its lse.
 __global__ __launch_bounds__(256) void k_mass_scores(MassArgs A) {
-  __shared__ f32x2 srow[32];
-  const Shape& S = A.S;
-  const int64_t chunks = (S.lk + 1023) / 1024;
-  const int64_t pair = blockIdx.x / chunks;
-  const int64_t j = (blockIdx.x - pair * chunks) * 1024 + 4 * threadIdx.x;
-  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
-  const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
-  if (threadIdx.x < 32) srow[threadIdx.x] = mass_row(A, b, hk, threadIdx.x, nrows, A.exact);
-  __syncthreads();
-  f32x4 x = {0, 0, 0, 0};
-  const float f = A.exact ? (float)kLog2e : 1.0f;
-  if (j < nkeys) {
-    // the forward kernel wrote whole tiles of the live keys
-    const float* sc = A.scores + S.rows * (pair * A.score_ld + (j & ~int64_t(31))) + (j & 31);
-    for (int r = 0; r < (int)nrows; ++r) {
-      const f32x4 t = *(const f32x4*)(sc + 32 * r);
-      const f32x2 st = srow[r];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = fmaf(st[1], ex2((t[e] - st[0]) * f), x[e]);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (j + e < S.lk) {
-      const int64_t i = pair * S.lk + j + e;
-      A.mass_out[i] = (A.mass_in ? A.mass_in[i] : 0.0f) + (j + e < nkeys ? x[e] : 0.0f);
-    }
+  const float lo = A.exact ? (float)(kLog2e - (double)(float)kLog2e) : 0.0f;
+  weight_keys(A, blockIdx.x, lo, [&](f32x2* srow, int64_t, int b, int hk, int64_t nrows) {
+    if (threadIdx.x >= 32) return;
+    f32x2 x = mass_row(A, b, hk, threadIdx.x, nrows, false);
+    srow[threadIdx.x] = x[0] == kInf ? f32x2{0.0f, 0.0f} : x;
+  });
 }
 
 void run_mass(const sinkhorn_attention* a, MassArgs& A, hipStream_t st) {
@@ -526,32 +505,31 @@ int sinkhorn_cross_attention(const sinkhorn_attention* a, const void* q, const v
       A.scores = (float*)(ws + p.score_off);
       A.score_ld = p.score_ld;
     }
+    MassArgs M{};
+    M.S = A.S;
+    M.lse = lse;
+    M.weight = row_weight;
+    M.mass_in = mass_in;
+    M.mass_out = mass_out;
+    M.scores = A.scores;
+    M.score_ld = A.score_ld;
+    M.exact = a->dtype == SINKHORN_F32;
+    M.deal = (int64_t)a->batch * a->heads_kv * ceil_div(a->len_k, 1024) < 512;  // two workgroups a compute unit
+    const MassArgs* with = p.scores && p.partial ? &M : nullptr;
     if (rows) {
       if (a->dtype == SINKHORN_BF16)
-        attend<__bf16>(A, p.many, st);
+        attend<__bf16>(A, p.many, with, st);
       else if (a->dtype == SINKHORN_F16)
-        attend<_Float16>(A, p.many, st);
+        attend<_Float16>(A, p.many, with, st);
       else
-        attend<float>(A, p.many, st);
+        attend<float>(A, p.many, with, st);
     }
-    if (mass) {
-      MassArgs M{};
-      M.S = A.S;
-      M.lse = lse;
-      M.weight = row_weight;
-      M.mass_in = mass_in;
-      M.mass_out = mass_out;
-      if (p.scores) {
-        M.scores = A.scores;
-        M.score_ld = A.score_ld;
-        M.exact = a->dtype == SINKHORN_F32;
-        hipLaunchKernelGGL(k_mass_scores, grid1((int64_t)a->batch * a->heads_kv * ceil_div(a->len_k, 1024), 256),
-                           dim3(256), 0, st, M);
-        SK_LAUNCH_CHECK();
-      } else {
-        use_plan(p.mass, ws, M);
-        run_mass(a, M, st);
-      }
+    if (mass && p.scores && !(rows && with)) {
+      hipLaunchKernelGGL(k_mass_scores, grid1(weight_blocks(M), 256), dim3(256), 0, st, M);
+      SK_LAUNCH_CHECK();
+    } else if (mass && !p.scores) {
+      use_plan(p.mass, ws, M);
+      run_mass(a, M, st);
     }
     return SINKHORN_OK;
   });

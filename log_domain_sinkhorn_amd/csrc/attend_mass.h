@@ -58,9 +58,10 @@ __device__ __forceinline__ f32x2 mass_row(const MassArgs& A, int b, int hk, int6
 // rows (32 at most), four keys a thread: 1024 keys, or, where that leaves the chip
 // empty, 256 with the rows dealt to four groups of 64 threads (16 x 8 x 32768
 // keys, 4 rows: join and weight 21 us with 1024 keys, 30 with 256; 3 x 4 x 4097
-// keys, 15 rows: 5.3 us with 256, with 1024 the weight alone took 6.2). rows(...) puts each row's reference (log2 units)
-// and the factor of its weights into LDS. lo: what the fp32 log2e misses, where
-// the references were made without that loss (else it cancels).
+// keys, 15 rows: 5.3 us with 256, with 1024 the weight alone took 6.2). rows(...)
+// puts each row's reference (log2 units) and the factor of its weights into LDS.
+// lo: what the fp32 log2e misses, where the references were made without that
+// loss (else it cancels).
 template <class F>
 __device__ __forceinline__ void weight_keys(const MassArgs& A, int64_t blk, float lo, F&& rows) {
   __shared__ f32x2 srow[32];

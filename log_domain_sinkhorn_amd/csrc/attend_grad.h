@@ -157,10 +157,25 @@ __global__ __launch_bounds__(256, sizeof(T) * row_width(W) <= 256 ? 2 : 1) void 
 #pragma unroll
     for (int n = 0; n < KT / 32; ++n) {
       f32x16 p = zero16(), g = zero16();
+      if constexpr (TL::RB == 128) {
+        V8 a[NS][2];  // all on their way before the first product, as in k_attend
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        p = mma(TL::row_frag(tk, 32 * n + r32, s, h), qf[s], p);
-        g = mma(TL::row_frag(tv, 32 * n + r32, s, h), gf[s], g);
+        for (int s = 0; s < NS; ++s) {
+          a[s][0] = TL::row_frag(tk, 32 * n + r32, s, h);
+          a[s][1] = TL::row_frag(tv, 32 * n + r32, s, h);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          p = mma(a[s][0], qf[s], p);
+          g = mma(a[s][1], gf[s], g);
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          p = mma(TL::row_frag(tk, 32 * n + r32, s, h), qf[s], p);
+          g = mma(TL::row_frag(tv, 32 * n + r32, s, h), gf[s], g);
+        }
       }
       auto weights = [&](auto terms) {
 #pragma unroll
@@ -454,10 +469,17 @@ __global__ __launch_bounds__(256, 2) void k_grad_kv_one(GradArgs A) {
 #pragma unroll
     for (int n = 0; n < RT / 32; ++n) {
       f32x16 p = zero16(), g = zero16();
+      V8 a[NS][2];  // all on their way before the first product, as in k_attend
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        p = mma(TL::row_frag(tq, 32 * n + r32, s, h), kf[s], p);
-        g = mma(TL::row_frag(tg, 32 * n + r32, s, h), vf[s], g);
+        a[s][0] = TL::row_frag(tq, 32 * n + r32, s, h);
+        a[s][1] = TL::row_frag(tg, 32 * n + r32, s, h);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        p = mma(a[s][0], kf[s], p);
+        g = mma(a[s][1], vf[s], g);
       }
       auto weights = [&](auto biased) {
 #pragma unroll

@@ -73,11 +73,13 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
   const int64_t pairs = (int64_t)S.batch * S.hkv;
   const int64_t item = xcd_item(pairs, A.tiles * A.nsplit);
   if (item < 0) return;
-  const int64_t pair = item / (A.tiles * A.nsplit);
+  int64_t pair = item / (A.tiles * A.nsplit);
   const int64_t rest = item - pair * (A.tiles * A.nsplit);
   const int64_t tile = rest / A.nsplit;
   const int split = (int)(rest - tile * A.nsplit);
-  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
+  const int pos = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)pos * S.hkv);
+  const int b = batch_entry(S, pos);
+  pair = (int64_t)b * S.hkv + hk;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r32 = lane & 31;

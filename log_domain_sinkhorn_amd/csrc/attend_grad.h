@@ -89,11 +89,13 @@ __global__ __launch_bounds__(256, sizeof(T) * row_width(W) <= 256 ? 2 : 1) void 
   const int64_t pairs = (int64_t)S.batch * S.hkv;
   const int64_t item = xcd_item(pairs, A.tiles_q * A.split_q);
   if (item < 0) return;
-  const int64_t pair = item / (A.tiles_q * A.split_q);
+  int64_t pair = item / (A.tiles_q * A.split_q);
   const int64_t rest = item - pair * (A.tiles_q * A.split_q);
   const int64_t tile = rest / A.split_q;
   const int split = (int)(rest - tile * A.split_q);
-  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
+  const int pos = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)pos * S.hkv);
+  const int b = batch_entry(S, pos);
+  pair = (int64_t)b * S.hkv + hk;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r32 = lane & 31;
 
@@ -234,11 +236,13 @@ __global__ __launch_bounds__(512, 2) void k_grad_kv(GradArgs A) {
   const int64_t pairs = (int64_t)S.batch * S.hkv;
   const int64_t item = xcd_item(pairs, A.tiles_kv * A.split_kv);
   if (item < 0) return;
-  const int64_t pair = item / (A.tiles_kv * A.split_kv);
+  int64_t pair = item / (A.tiles_kv * A.split_kv);
   const int64_t rest = item - pair * (A.tiles_kv * A.split_kv);
   const int64_t tile = rest / A.split_kv;
   const int split = (int)(rest - tile * A.split_kv);
-  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
+  const int pos = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)pos * S.hkv);
+  const int b = batch_entry(S, pos);
+  pair = (int64_t)b * S.hkv + hk;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r32 = lane & 31;
   const int wp = wave & 3;
@@ -412,11 +416,13 @@ __global__ __launch_bounds__(256, 2) void k_grad_kv_one(GradArgs A) {
   const int64_t pairs = (int64_t)S.batch * S.hkv;
   const int64_t item = xcd_item(pairs, A.tiles_kv * A.split_kv);
   if (item < 0) return;
-  const int64_t pair = item / (A.tiles_kv * A.split_kv);
+  int64_t pair = item / (A.tiles_kv * A.split_kv);
   const int64_t rest = item - pair * (A.tiles_kv * A.split_kv);
   const int64_t tile = rest / A.split_kv;
   const int split = (int)(rest - tile * A.split_kv);
-  const int b = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)b * S.hkv);
+  const int pos = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)pos * S.hkv);
+  const int b = batch_entry(S, pos);
+  pair = (int64_t)b * S.hkv + hk;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r32 = lane & 31;
 

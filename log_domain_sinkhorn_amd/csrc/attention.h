@@ -356,6 +356,26 @@ __device__ __forceinline__ int64_t live_rows(const Shape& S, int b) {
   return (n < 0 ? 0 : (n > S.lq ? S.lq : n)) * S.group;
 }
 
+// The batch entry that the workgroups at place `pos` of the batch work on. With
+// lengths of its own for each entry: the longer half first, longest at the front,
+// then the shorter half from its shortest up, so that of two workgroups that share
+// a compute unit one is short where the other is long (512 x 2000 x 16 heads x 8,
+// lengths from 1125 to 2000 in random order: 44.7 -> 40.9 us; from longest to
+// shortest 42.2, long and short in turn 44.6).
+__device__ __forceinline__ int batch_entry(const Shape& S, int pos) {
+  if (!S.klen || S.batch < 2 || S.batch > 64) return pos;
+  const int lane = threadIdx.x & 63;
+  const int mine = lane < S.batch ? S.klen[lane] : -1;
+  int rank = 0;
+  for (int b = 0; b < S.batch; ++b) {
+    const int other = __builtin_amdgcn_readlane(mine, b);
+    rank += other > mine || (other == mine && b < lane);
+  }
+  const int half = (S.batch + 1) / 2;
+  const int want = pos < half ? pos : S.batch - 1 - (pos - half);
+  return (int)__builtin_ctzll(__ballot(lane < S.batch && rank == want));
+}
+
 // Rows of the packed (query, head) side: byte offset of row r of a tile that
 // starts at head `rem` of its first query.
 __device__ __forceinline__ uint32_t packed_row(const Shape& S, int r, int rem, uint32_t row_bytes, uint32_t head_bytes) {

@@ -112,6 +112,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
   for (int n = 0; n < NDB; ++n) o[n] = zero16();
   float m = -kInf, l = 0.0f;  // the row's reference (log2 units) and this lane's part of the sum
 
+  if constexpr (WK == 1 && OCC == 2) one_ahead();
   for (int it = 0; it < keys.count; ++it) {
     // each of the last two tiles stored its scores with an instruction at least
     keys.template next<(D > 2 ? 2 : 0)>(it, D > 2 && A.scores && it >= 2);

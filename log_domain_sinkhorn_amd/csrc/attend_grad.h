@@ -150,6 +150,7 @@ __global__ __launch_bounds__(256, sizeof(T) * row_width(W) <= 256 ? 2 : 1) void 
 #pragma unroll
   for (int n = 0; n < NDB; ++n) dq[n] = zero16();
 
+  if constexpr (TL::RB == 256) one_ahead();
   for (int it = 0; it < keys.count; ++it) {
     keys.next(it);
     const char* const tk = keys.ktile(it);

@@ -439,8 +439,8 @@ void attend_launch(const AttendArgs& A, bool many, hipStream_t st) {
   constexpr int RB = row_width(W) * (int)sizeof(T);
   // many rows: two waves a SIMD (three for rows of 128 bytes); with fewer
   // registers a wave spills, and half tiles cost more in what each tile
-  // repeats than they gain in occupancy (8192 x 16384 x 32 heads of 128:
-  // 2180 us against 5200)
+  // repeats than they gain in occupancy (8192 x 16384 x 32 heads of 128: 2.2 ms
+  // against 5.2 when both were measured)
   constexpr int OCC = RB == 128 ? 3 : (RB == 256 ? 2 : 1);
   if (many)
     hipLaunchKernelGGL((k_attend<T, W, 4, 1, 2, 2, OCC>), grid1(blocks, 256), dim3(256), 0, st, A);

@@ -110,6 +110,10 @@ inline int64_t weight_blocks(const MassArgs& A) {
   return (int64_t)A.S.batch * A.S.hkv * ((A.S.lk + (A.deal ? 255 : 1023)) / (A.deal ? 256 : 1024));
 }
 
+// Bound by the vector work of a score (an exponential, two fma) beside its product:
+// 2 x 2048 x 8191 keys, 16 heads of 128 on 4, bf16: 158 us, 870 TFLOP/s. Three
+// waves a SIMD where the registers allow it without spilling (96 columns: two); the
+// products of both 32-row blocks ahead of the first's weights spill: 164 us.
 template <class T, int W>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? (W == 96 ? 2 : 3) : 1) void k_mass(MassArgs A) {
   constexpr int DP = row_width(W);

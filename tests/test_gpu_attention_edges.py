@@ -89,7 +89,7 @@ def test_groups_across_tiles(sk, dtype, Lq, Hq, Hkv):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
-@pytest.mark.parametrize("B,Hkv", [(13, 5), (8, 1), (3, 3), (64, 1), (9, 8)])
+@pytest.mark.parametrize("B,Hkv", [(13, 5), (8, 1), (3, 3), (64, 1), (9, 8), (70, 1)])
 @pytest.mark.parametrize("Lq", [1, 36])
 def test_numbers_of_heads(sk, dtype, B, Hkv, Lq):
     """Pairs of batch entry and key head: in eights, more than 64, fewer."""

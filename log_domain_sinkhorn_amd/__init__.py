@@ -423,11 +423,12 @@ def _head_tensor(t, name, dtype=None, shape=None):
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 4:
+    has = t.shape
+    if len(has) != 4:
         raise ValueError(f"{name} must be [batch, length, heads, width]")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    if shape is not None and has != shape:
+        raise ValueError(f"{name} has shape {tuple(has)}, expected {tuple(shape)}")
+    if t.stride(3) != 1 and has[3] > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires grad: these calls record no graph; detach it or use torch.no_grad(), "
@@ -438,10 +439,11 @@ def _head_tensor(t, name, dtype=None, shape=None):
 def _written(t, name):
     """An output: no two of its elements may share memory."""
     span = 1
-    for size, stride in sorted(((n, st) for n, st in zip(t.shape, t.stride()) if n > 1), key=lambda x: x[1]):
-        if stride < span:
-            raise ValueError(f"{name} has overlapping elements")
-        span = stride * size
+    for stride, size in sorted(zip(t.stride(), t.shape)):
+        if size > 1:
+            if stride < span:
+                raise ValueError(f"{name} has overlapping elements")
+            span = stride * size
     return t
 
 
@@ -451,7 +453,7 @@ def _plain(t, name, dtype, shape):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -489,9 +491,11 @@ def _at(t):
 
 def _strides3(t):
     """Element strides of batch, length and head (0 where there is one)."""
-    n0, n1, n2, _ = t.shape
     s0, s1, s2, _ = t.stride()
-    return _i64x3(s0 if n0 > 1 else 0, s1 if n1 > 1 else 0, s2 if n2 > 1 else 0)
+    shape = t.shape
+    if 1 in shape:
+        return _i64x3(s0 if shape[0] > 1 else 0, s1 if shape[1] > 1 else 0, s2 if shape[2] > 1 else 0)
+    return _i64x3(s0, s1, s2)
 
 
 def _attention(q, k, v, scale, key_bias, query_lengths, key_lengths):

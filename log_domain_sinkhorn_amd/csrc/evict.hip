@@ -43,6 +43,7 @@ constexpr int kGroup = 256;  // keys of a workgroup of k_evict_move
 constexpr int kSelThreads = 1024;
 constexpr int kSelPer = 16;  // keys of a thread in a chunk
 constexpr int kSelChunk = kSelThreads * kSelPer;
+constexpr int kSelFew = 4;  // the same where all keys fit kSelThreads * kSelFew
 // Copies of the counts, by lane: equal weights (keys that gathered none) would
 // otherwise make a wave's additions to one counter wait for each other.
 constexpr int kCopies = 8;
@@ -67,11 +68,13 @@ __device__ __forceinline__ uint32_t key_value(float x, int j, int n, int lo, int
   return j >= n ? kNone : (j < lo || j >= hi ? kAlways : order_key(x));
 }
 
-// C: chunks of keys held in registers; 0: any number, read in each pass.
-template <int C>
+// C: chunks of keys held in registers; 0: any number, read in each pass. P: keys of
+// a thread in a chunk.
+template <int C, int P>
 __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
-  constexpr int kSub = kSelChunk / kGroup;  // groups of a chunk: 64, four of a wave's
-  static_assert(kSub == 64 && kSelPer * 64 == 4 * kGroup, "a lane of one wave for each group");
+  constexpr int kChunk = kSelThreads * P;
+  constexpr int kSub = kChunk / kGroup, kOwn = 64 * P / kGroup;  // groups of a chunk, of a wave's part of it
+  static_assert(kSub <= 64 && kOwn * kGroup == 64 * P, "a lane of one wave for each group");
   __shared__ uint32_t hist[256][kCopies];
   __shared__ uint32_t scount[2][kSub];
   __shared__ uint32_t sdigit, sbefore;
@@ -89,18 +92,18 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
   if (n <= keep) return;  // all kept
   const float* w = A.mass + pair * A.len;
   const int lo = (int)A.first, hi = n - (int)A.recent;
-  // a wave's keys of a chunk: 1024 consecutive ones, 64 at a time
-  const int base = wave * (64 * kSelPer) + lane;
-  auto read = [&](int chunk, uint32_t (&u)[kSelPer]) {
-    const int j0 = chunk * kSelChunk + base;
-    float x[kSelPer];
+  // a wave's keys of a chunk: 64 P consecutive ones, 64 at a time
+  const int base = wave * (64 * P) + lane;
+  auto read = [&](int chunk, uint32_t (&u)[P]) {
+    const int j0 = chunk * kChunk + base;
+    float x[P];
 #pragma unroll
-    for (int i = 0; i < kSelPer; ++i) x[i] = j0 + 64 * i < n ? w[j0 + 64 * i] : 0.0f;
+    for (int i = 0; i < P; ++i) x[i] = j0 + 64 * i < n ? w[j0 + 64 * i] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < kSelPer; ++i) u[i] = key_value(x[i], j0 + 64 * i, n, lo, hi);
+    for (int i = 0; i < P; ++i) u[i] = key_value(x[i], j0 + 64 * i, n, lo, hi);
   };
-  const int chunks = (n - 1) / kSelChunk + 1;
-  uint32_t held[C > 0 ? C : 1][kSelPer];
+  const int chunks = (n - 1) / kChunk + 1;
+  uint32_t held[C > 0 ? C : 1][P];
   if constexpr (C > 0) {
 #pragma unroll
     for (int c = 0; c < C; ++c) read(c, held[c]);
@@ -123,9 +126,9 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
   for (int shift = 24; shift >= 0; shift -= 8) {
     for (int i = tid; i < 256 * kCopies; i += kSelThreads) ((uint32_t*)hist)[i] = 0;
     __syncthreads();
-    each([&](int, const uint32_t (&u)[kSelPer]) {
+    each([&](int, const uint32_t (&u)[P]) {
 #pragma unroll
-      for (int i = 0; i < kSelPer; ++i)
+      for (int i = 0; i < P; ++i)
         if ((u[i] & mask) == prefix) atomicAdd(&hist[(u[i] >> shift) & 255u][lane % kCopies], 1u);
     });
     __syncthreads();
@@ -166,9 +169,9 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
     A.limit[2 * pair + 1] = need;
   }
   uint32_t nsel = 0, neq = 0;  // before this chunk (the first wave's)
-  each([&](int chunk, const uint32_t (&u)[kSelPer]) {
+  each([&](int chunk, const uint32_t (&u)[P]) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < kOwn; ++g) {
       uint32_t s = 0, q = 0;
 #pragma unroll
       for (int i = 4 * g; i < 4 * g + 4; ++i) {
@@ -176,13 +179,13 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
         q += __popcll(__ballot(u[i] == prefix));
       }
       if (lane == 0) {
-        scount[0][4 * wave + g] = s;
-        scount[1][4 * wave + g] = q;
+        scount[0][kOwn * wave + g] = s;
+        scount[1][kOwn * wave + g] = q;
       }
     }
     __syncthreads();
     if (wave == 0) {
-      const uint32_t s = scount[0][lane], q = scount[1][lane];
+      const uint32_t s = lane < kSub ? scount[0][lane] : 0, q = lane < kSub ? scount[1][lane] : 0;
       uint32_t is = s, iq = q;
 #pragma unroll
       for (int x = 1; x < 64; x <<= 1) {
@@ -193,7 +196,7 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
         }
       }
       const int64_t group = (int64_t)chunk * kSub + lane;
-      if (group < A.groups) {
+      if (lane < kSub && group < A.groups) {
         A.before[2 * (pair * A.groups + group)] = nsel + is - s;
         A.before[2 * (pair * A.groups + group) + 1] = neq + iq - q;
       }
@@ -394,12 +397,15 @@ int sinkhorn_cache_evict(const sinkhorn_cache* c, const void* k, const void* v, 
     A.limit = (uint32_t*)workspace;
     A.before = (uint32_t*)workspace + 2 * pairs;
     const dim3 all = grid1(pairs, kSelThreads);
-    if (c->len <= kSelChunk)
-      hipLaunchKernelGGL((k_evict_select<1>), all, dim3(kSelThreads), 0, st, A);
+    // few keys spread over all waves (4 x 8 x 4096: 7.6 us in place of 11.5)
+    if (c->len <= kSelThreads * kSelFew)
+      hipLaunchKernelGGL((k_evict_select<1, kSelFew>), all, dim3(kSelThreads), 0, st, A);
+    else if (c->len <= kSelChunk)
+      hipLaunchKernelGGL((k_evict_select<1, kSelPer>), all, dim3(kSelThreads), 0, st, A);
     else if (c->len <= 4 * kSelChunk)
-      hipLaunchKernelGGL((k_evict_select<4>), all, dim3(kSelThreads), 0, st, A);
+      hipLaunchKernelGGL((k_evict_select<4, kSelPer>), all, dim3(kSelThreads), 0, st, A);
     else
-      hipLaunchKernelGGL((k_evict_select<0>), all, dim3(kSelThreads), 0, st, A);
+      hipLaunchKernelGGL((k_evict_select<0, kSelPer>), all, dim3(kSelThreads), 0, st, A);
     SK_LAUNCH_CHECK();
     if (A.cap == 0) return SINKHORN_OK;
     const dim3 grid = grid1(pairs * A.groups, kGroup);

@@ -174,7 +174,7 @@ def test_live_values_that_are_no_numbers(sk, dtype, Lq, bad):
 
 
 @pytest.mark.parametrize("B,n,H,keep,first,recent", [
-    (2, 16384, 1, 3000, 7, 100), (2, 20001, 2, 9000, 4, 64), (1, 65536, 1, 1, 0, 0), (2, 65537, 1, 30000, 0, 1),
+    (2, 4096, 3, 1024, 4, 128), (2, 4097, 1, 2000, 0, 9), (2, 16384, 1, 3000, 7, 100), (2, 20001, 2, 9000, 4, 64), (1, 65536, 1, 1, 0, 0), (2, 65537, 1, 30000, 0, 1),
     (1, 150001, 2, 149999, 11, 13), (3, 90000, 1, 40000, 40000, 0), (1, 70000, 1, 70000, 0, 0),
 ])
 def test_evict_long(sk, B, n, H, keep, first, recent):

@@ -85,7 +85,8 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictArgs A) {
   const int keep = (int)(A.keep < A.len ? A.keep : A.len);
   const int left = n < keep ? n : keep;
   if (tid == 0 && pair == (int64_t)b * A.heads) A.lengths_out[b] = left;
-  for (int j = left + tid; j < (int)A.cap; j += kSelThreads) {
+  // in 64 bits: a step from below cap, itself below 2^31, can lead past 2^31
+  for (int64_t j = left + tid; j < A.cap; j += kSelThreads) {
     A.index_out[pair * A.cap + j] = -1;
     A.mass_out[pair * A.cap + j] = 0.0f;
   }

@@ -245,3 +245,35 @@ def test_drawn_shapes(sk, dtype, seed):
     _log(f"drawn {dtype} {(B, Lq, Hkv * G, Hkv, Lk, d, dv)}")
     args, kw, extra = _case(dtype, B, Lq, Hkv * G, Hkv, Lk, d, dv, seed=2000 + seed, ragged=bool(seed % 3))
     _check_all(sk, *args, "drawn", **kw, **extra)
+
+
+def test_evict_at_the_largest_length(sk):
+    """2^31 - 1 keys, the most that are accepted: the places behind the kept
+    keys, and a selection among keys up to the last one."""
+    n = (1 << 31) - 1
+    _log("evict 2^31 - 1, all places filled")
+    row = torch.arange(1.0, 9.0, dtype=BF, device=DEV)
+    k = row[:1].view(1, 1, 1, 1).expand(1, n, 1, 1)  # one row for all keys
+    mass = torch.zeros(1, 1, n, device=DEV)
+    guard = 4096
+    index = torch.full((n + guard,), 7, dtype=torch.int32, device=DEV)
+    weight = torch.full((n + guard,), 7.0, device=DEV)
+    lens = torch.tensor([5], dtype=torch.int32, device=DEV)
+    k_out, v_out = (torch.full((1, n, 1, 1), 3.0, dtype=BF, device=DEV) for _ in range(2))
+    mass[0, 0, :6] = 2.0
+    left = sk.cache_evict(k, k, mass, n, key_lengths=lens, k_out=k_out, v_out=v_out, mass_out=weight[:n].view(1, 1, n),
+                          index_out=index[:n].view(1, 1, n))[4]
+    assert left.tolist() == [5] and index[:5].tolist() == [0, 1, 2, 3, 4] and weight[:5].tolist() == [2.0] * 5
+    assert int(index[5:n].max()) == -1 and int(index[5:n].min()) == -1
+    assert float(weight[5:n].max()) == 0.0 and float(weight[5:n].min()) == 0.0
+    assert bool((index[n:] == 7).all()) and bool((weight[n:] == 7.0).all())
+    for t in (k_out, v_out):
+        assert bool((t[0, :5] == 1.0).all()) and float(t[0, 5:].max()) == 3.0 and float(t[0, 5:].min()) == 3.0
+    del index, weight, k_out, v_out
+    _log("evict 2^31 - 1, selection")
+    at = [0, 3, n // 2, n - 20000, n - 300, n - 2, n - 1]
+    mass.zero_()
+    mass[0, 0, at] = 1.0
+    idx, left = sk.cache_evict(k, k, mass, 9)[3:]
+    # the rest weigh nothing: the lowest indices
+    assert left.tolist() == [9] and idx[0, 0].tolist() == sorted(at + [1, 2])

@@ -452,7 +452,10 @@ int sinkhorn_sparse_barycentric(sinkhorn_problem* p, double eps, const float* g,
  * (batch, row, head), the last dimension contiguous. Inputs may have any
  * strides >= 0 and any alignment (operands whose rows are not 16-byte aligned, or
  * no whole number of 16 bytes long, are first copied into the workspace); the
- * elements of an output may not overlap. Query head h reads key head
+ * elements of an output may not overlap, nor an output or the workspace another
+ * argument (refused; they may lie between another's rows, as the halves of one
+ * buffer do, unless strides without a common one leave that undecided). Query
+ * head h reads key head
  * h / (heads_q / heads_kv). lse is [batch][heads_q][len_q], gathered weights are
  * [batch][heads_kv][len_k], row weights [batch][len_q], contiguous fp32.
  *
@@ -510,8 +513,7 @@ int sinkhorn_attention_workspace(const sinkhorn_attention* at, int32_t what, con
  * (mass_in nullable: 0, and may be mass_out; row_weight nullable: 1). When all
  * rows of a key head (len_q * heads_q / heads_kv) are at most 32, as for single
  * tokens, the weight comes from the scores of the same pass and the keys are
- * read once. out and lse may not overlap an input, nor mass_out one other than
- * mass_in. */
+ * read once. */
 int sinkhorn_cross_attention(const sinkhorn_attention* at, const void* q, const void* k,
                              const void* v, void* out, float* lse, const float* row_weight,
                              const float* mass_in, float* mass_out, void* workspace,
@@ -553,7 +555,7 @@ typedef struct {
  * [batch][heads][cap] the positions they had; lengths_out [batch] the number
  * kept. Behind that number k_out and v_out are left as they were, mass_out is
  * 0 and index_out -1. Outputs may not overlap inputs or each other (lengths_out
- * is no key_lengths). d and dv are not limited to 128. Asynchronous on `stream`. */
+ * is no key_lengths; k_out may be rows of k's own buffer behind len). d and dv are not limited to 128. Asynchronous on `stream`. */
 int sinkhorn_cache_evict(const sinkhorn_cache* cache, const void* k, const void* v,
                          const float* mass, void* k_out, void* v_out, float* mass_out,
                          int32_t* index_out, int32_t* lengths_out, void* workspace,

@@ -7,6 +7,7 @@
 #include "attend.h"
 #include "attend_grad.h"
 #include "attend_mass.h"
+#include "overlap.h"
 
 namespace sk {
 namespace attn {
@@ -390,6 +391,32 @@ void check_workspace(const void* ws, int64_t have, int64_t need) {
   require((uintptr_t)ws % 16 == 0, "workspace must be 16-byte aligned");
 }
 
+// The arrays of a call, for the test that nothing is written that another
+// workgroup may be reading: by elements, as outputs may lie between the rows of
+// inputs (the halves of one buffer).
+Span row_heads(const sinkhorn_attention* a, const void* p, const int64_t* stride, int32_t width) {
+  return Span(p, stride, a->batch, a->len_q, a->heads_q, width, elem_size(a));
+}
+Span key_heads(const sinkhorn_attention* a, const void* p, const int64_t* stride, int32_t width) {
+  return Span(p, stride, a->batch, a->len_k, a->heads_kv, width, elem_size(a));
+}
+Span bias_rows(const sinkhorn_attention* a) {
+  const int64_t stride[3] = {a->bias_stride[0], a->bias_stride[1], 0};
+  return Span(a->key_bias, stride, a->batch, a->heads_kv, 1, a->len_k, 4);
+}
+Span per_row(const sinkhorn_attention* a, const void* p) { return Span(p, 4 * (int64_t)a->batch * a->len_q); }
+Span per_row_head(const sinkhorn_attention* a, const void* p) {
+  return Span(p, 4 * (int64_t)a->batch * a->heads_q * a->len_q);
+}
+Span per_key(const sinkhorn_attention* a, const void* p) {
+  return Span(p, 4 * (int64_t)a->batch * a->heads_kv * a->len_k);
+}
+Span per_entry(const sinkhorn_attention* a, const void* p) { return Span(p, 4 * (int64_t)a->batch); }
+
+void check_apart(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  require(!any_meet(written, read), "an output or the workspace overlaps another argument");
+}
+
 // ---------------------------------------------------------------- gathered weight
 // Row statistics of k_mass (natural: as for mass_row).
 __global__ __launch_bounds__(256) void k_mass_stat(MassArgs A, bool natural) {
@@ -486,6 +513,12 @@ int sinkhorn_cross_attention(const sinkhorn_attention* a, const void* q, const v
             "lse overlaps an input");
     const AttendPlan p = plan_attend(a, q, k, v, mass);
     check_workspace(workspace, workspace_bytes, p.bytes);
+    check_apart({row_heads(a, out, a->out_stride, a->dv), per_row_head(a, lse), per_key(a, mass_out),
+                 Span(workspace, p.bytes)},
+                {row_heads(a, q, a->q_stride, a->d), key_heads(a, k, a->k_stride, a->d),
+                 key_heads(a, v, a->v_stride, a->dv), bias_rows(a), per_entry(a, a->query_lengths),
+                 per_entry(a, a->key_lengths), per_row(a, row_weight),
+                 per_key(a, mass_in == mass_out ? nullptr : mass_in)});
     const hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
     AttendArgs A{};
@@ -551,6 +584,12 @@ int sinkhorn_cross_attention_grad(const sinkhorn_attention* a, const void* q, co
     require((!keys || dk != dv) && (!(rows && keys) || (dq != dk && dq != dv)), "outputs alias each other");
     const GradPlan p = plan_grad(a, q, k, v, dout);
     check_workspace(workspace, workspace_bytes, p.bytes);
+    check_apart({row_heads(a, dq, a->dq_stride, a->d), key_heads(a, dk, a->dk_stride, a->d),
+                 key_heads(a, dv, a->dv_stride, a->dv), Span(workspace, p.bytes)},
+                {row_heads(a, q, a->q_stride, a->d), key_heads(a, k, a->k_stride, a->d),
+                 key_heads(a, v, a->v_stride, a->dv), row_heads(a, out, a->out_stride, a->dv),
+                 row_heads(a, dout, a->dout_stride, a->dv), per_row_head(a, lse), bias_rows(a),
+                 per_entry(a, a->query_lengths), per_entry(a, a->key_lengths)});
     const hipStream_t st = (hipStream_t)stream;
     const int64_t size = elem_size(a);
     char* ws = (char*)workspace;
@@ -610,6 +649,10 @@ int sinkhorn_attention_mass(const sinkhorn_attention* a, const void* q, const vo
     check_mass(a, lse, row_weight, mass_in, mass_out);
     const WeightPlan p = plan_mass(a, q, k);
     check_workspace(workspace, workspace_bytes, p.bytes);
+    check_apart({per_key(a, mass_out), Span(workspace, p.bytes)},
+                {row_heads(a, q, a->q_stride, a->d), key_heads(a, k, a->k_stride, a->d), bias_rows(a),
+                 per_entry(a, a->query_lengths), per_entry(a, a->key_lengths), per_row_head(a, lse),
+                 per_row(a, row_weight), per_key(a, mass_in == mass_out ? nullptr : mass_in)});
     const hipStream_t st = (hipStream_t)stream;
     char* ws = (char*)workspace;
     MassArgs M{};

@@ -16,6 +16,7 @@
 // the places found by k_evict_select that one took 78 us in place of 27; k_evict_move
 // takes 112).
 #include "attention.h"
+#include "overlap.h"
 
 namespace sk {
 namespace attn {
@@ -356,11 +357,20 @@ int sinkhorn_cache_evict(const sinkhorn_cache* c, const void* k, const void* v, 
             "workspace too small (sinkhorn_cache_workspace)");
     require((uintptr_t)workspace % 16 == 0, "workspace must be 16-byte aligned");
     const int64_t size = c->dtype == SINKHORN_F32 ? 4 : 2;
+    const int64_t cap = c->keep < c->len ? c->keep : c->len, pairs = (int64_t)c->batch * c->heads;
+    require(!any_meet({Span(k_out, c->k_out_stride, c->batch, cap, c->heads, c->d, size),
+                       Span(v_out, c->v_out_stride, c->batch, cap, c->heads, c->dv, size), Span(mass_out, 4 * pairs * cap),
+                       Span(index_out, 4 * pairs * cap), Span(lengths_out, 4 * (int64_t)c->batch),
+                       Span(workspace, space(c))},
+                      {Span(k, c->k_stride, c->batch, c->len, c->heads, c->d, size),
+                       Span(v, c->v_stride, c->batch, c->len, c->heads, c->dv, size), Span(mass, 4 * pairs * c->len),
+                       Span(c->key_lengths, 4 * (int64_t)c->batch)}),
+            "an output or the workspace overlaps another argument");
     EvictArgs A{};
     A.batch = c->batch;
     A.heads = c->heads;
     A.len = c->len;
-    A.cap = c->keep < c->len ? c->keep : c->len;
+    A.cap = cap;
     A.keep = c->keep;
     A.first = c->first;
     A.recent = c->recent;
@@ -393,7 +403,6 @@ int sinkhorn_cache_evict(const sinkhorn_cache* c, const void* k, const void* v, 
       }
     }
     const hipStream_t st = (hipStream_t)stream;
-    const int64_t pairs = (int64_t)c->batch * c->heads;
     A.groups = (c->len + kGroup - 1) / kGroup;
     A.limit = (uint32_t*)workspace;
     A.before = (uint32_t*)workspace + 2 * pairs;

@@ -220,3 +220,87 @@ def test_overlapping_side_outputs_are_refused():
         assert evict(_cache(key_lengths=lens), *q) == sk.ERR_INVALID_ARG, (i, x)
         assert b"overlaps" in L.sinkhorn_last_error() or b"aliases" in L.sinkhorn_last_error(), (i, x)
     assert evict(_cache(key_lengths=lens), *p) == sk.ERR_INVALID_ARG and b"workspace" in L.sinkhorn_last_error()
+
+
+def _fill(a):
+    """Arguments of every entry point far apart from each other, and a workspace
+    that suffices: {name: address}."""
+    names = ("q", "k", "v", "out", "lse", "w", "mi", "mo", "dout", "dq", "dk", "dv", "bias", "qlen", "klen", "ws")
+    at = {n: (i + 1) << 36 for i, n in enumerate(names)}
+    a.key_bias, a.query_lengths, a.key_lengths = at["bias"], at["qlen"], at["klen"]
+    a.bias_stride = sk._i64x2(1000, 0)
+    return at
+
+
+def _call_all(a, at, n):
+    """What each entry point says: the launch itself fails where there is no device."""
+    L, r, res = sk.lib(), ctypes.byref(a), {}
+    p = lambda *names: [ctypes.c_void_p(at[x]) for x in names]  # noqa: E731
+    for name, code in (
+            ("forward", lambda: L.sinkhorn_cross_attention(r, *p("q", "k", "v", "out", "lse", "w", "mi", "mo", "ws"), n, None)),
+            ("grad", lambda: L.sinkhorn_cross_attention_grad(
+                r, *p("q", "k", "v", "out", "lse", "dout", "dq", "dk", "dv", "ws"), n, None)),
+            ("mass", lambda: L.sinkhorn_attention_mass(r, *p("q", "k", "lse", "w", "mi", "mo", "ws"), n, None))):
+        c = code()
+        res[name] = c == sk.ERR_INVALID_ARG and any(x in L.sinkhorn_last_error() for x in (b"overlap", b"alias"))
+    return res
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="addresses that are no memory: only where nothing can be launched")
+def test_arrays_that_share_memory_are_refused():
+    """By elements: [2][3 or 1000][4 or 2][64] of bf16, rows 512 bytes apart."""
+    n = 1 << 30
+    FW, GR, MA = {"forward"}, {"grad"}, {"mass"}
+    for change, want in (
+            (dict(), set()),
+            # a part of another array's elements
+            (dict(out="q", by=128), FW), (dict(out="k", by=512 * 999 + 128), FW), (dict(out="v", by=256 - 2), FW),
+            (dict(lse="q", by=512 * 2), FW), (dict(lse="k", by=4), FW), (dict(mo="q", by=0), FW | MA),
+            (dict(mo="k", by=512 * 900), FW | MA), (dict(mo="bias", by=7996), FW | MA), (dict(mo="klen", by=4), FW | MA),
+            (dict(mo="out", by=256), FW), (dict(lse="out", by=0), FW), (dict(lse="klen", by=4), FW),
+            (dict(out="bias", by=4000), FW), (dict(mo="mi", by=0), set()),
+            (dict(dq="q", by=384), GR), (dict(dk="k", by=128), GR), (dict(dv="k", by=512), GR), (dict(dk="dout", by=0), GR),
+            (dict(dv="dk", by=126), GR), (dict(dq="out", by=2), GR), (dict(dk="lse", by=92), GR), (dict(dv="bias", by=0), GR),
+            (dict(dq="qlen", by=0), GR),
+            # the workspace
+            (dict(ws="k", by=512 * 512), FW | GR | MA), (dict(ws="lse", by=0), FW | GR | MA), (dict(ws="dk", by=0), GR),
+            # between the others' rows
+            (dict(dv="dk", by=256), set()), (dict(dk="k", by=256), set()), (dict(out="v", by=256 + 512 * 997), FW),
+            (dict(dk="q", by=512 * 3), set()), (dict(out="q", by=512 * 3), set())):
+        a = _desc()
+        at = _fill(a)
+        by = change.pop("by", 0)
+        for x, y in change.items():
+            at[x] = at[y] + by
+        got = {x for x, refused in _call_all(a, at, n).items() if refused}
+        assert got == want, (change, by, got)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="addresses that are no memory: only where nothing can be launched")
+def test_rows_of_the_cache_itself_are_refused_as_outputs():
+    L = sk.lib()
+    row, B, n, H, keep = 128, 2, 100, 2, 10
+    names = ("k", "v", "mass", "k_out", "v_out", "mass_out", "index_out", "lengths_out", "ws")
+
+    def refused(k_first=None, total=200, **kw):
+        at = {x: (i + 1) << 36 for i, x in enumerate(names)}
+        c = sk._CacheC(dtype=1, batch=B, heads=H, d=64, dv=64, len=n, keep=keep, first=1, recent=2, key_lengths=1 << 50)
+        for x in ("k", "v", "k_out", "v_out"):
+            setattr(c, x + "_stride", sk._i64x3(total * H * 64, H * 64, 64))
+        if k_first is not None:
+            at["k_out"] = at["k"] + k_first * H * row
+        for x, (y, by) in kw.items():
+            at[x] = at[y] + by
+        code = L.sinkhorn_cache_evict(ctypes.byref(c), *[ctypes.c_void_p(at[x]) for x in names], 1 << 20, None)
+        return code == sk.ERR_INVALID_ARG and any(x in L.sinkhorn_last_error() for x in (b"overlap", b"alias"))
+
+    assert not refused()
+    for first in (1, 50, 99):
+        assert refused(first)
+    assert not refused(100) and not refused(190)  # rows behind the cache, between its batch entries
+    assert refused(191)  # its last row is the next entry's first
+    for kw in (dict(v_out=("k", row)), dict(v_out=("k_out", 0)), dict(v_out=("k_out", row)), dict(k_out=("mass", 796)),
+               dict(mass_out=("v", 0)), dict(index_out=("k_out", 0)), dict(lengths_out=("v", 8)), dict(ws=("mass", 0)),
+               dict(ws=("k_out", 16))):
+        assert refused(**kw), kw
+    assert not refused(mass_out=("v", n * H * row))  # behind the first entry

@@ -99,11 +99,14 @@ __device__ __forceinline__ void weight_keys(const MassArgs& A, int64_t blk, floa
       for (int e = 0; e < 4; ++e) x[e] += y[e];
     }
   }
+  // by the mask itself, as a masked key's weight is NaN under a row that is no number
+  const float* bias = S.bias ? S.bias + b * S.bs[0] + hk * S.bs[1] : nullptr;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (j + e < S.lk) {
       const int64_t i = pair * S.lk + j + e;
-      A.mass_out[i] = (A.mass_in ? A.mass_in[i] : 0.0f) + (j + e < nkeys ? x[e] : 0.0f);
+      const bool live = column_term(bias, j + e, nkeys, 1.0f) != -kInf;
+      A.mass_out[i] = (A.mass_in ? A.mass_in[i] : 0.0f) + (live ? x[e] : 0.0f);
     }
 }
 inline int64_t weight_blocks(const MassArgs& A) {

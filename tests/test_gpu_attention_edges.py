@@ -277,3 +277,29 @@ def test_evict_at_the_largest_length(sk):
     idx, left = sk.cache_evict(k, k, mass, 9)[3:]
     # the rest weigh nothing: the lowest indices
     assert left.tolist() == [9] and idx[0, 0].tolist() == sorted(at + [1, 2])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("Lk", [90, 6000])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_weight_of_masked_keys_under_rows_that_are_no_numbers(sk, dtype, Lk, d, bad):
+    """A key that takes no part gathers nothing, whatever a live row of q holds,
+    in the fused form as in the pass of its own."""
+    _log(f"masked weight {dtype} {Lk} {d} {bad}")
+    for Lq in (1, 5, 40):
+        (q, k, v, _), _, extra = _case(dtype, 2, Lq, 4, 2, Lk, d, d, seed=39, ragged=False)
+        bias = torch.zeros(2, Lk, device=DEV)
+        bias[:, ::3] = -math.inf
+        bias[:, 1::7] = torch.finfo(F32).min
+        lens = torch.tensor([Lk - 3, Lk - 40], dtype=torch.int32, device=DEV)
+        masked = (bias < -1e29) | (torch.arange(Lk, device=DEV)[None] >= lens[:, None])
+        masked = masked[:, None].expand(2, 2, Lk)
+        q[:, Lq - 1, ::2, 5] = bad
+        kw = dict(key_bias=bias, key_lengths=lens)
+        got = torch.empty(2, 2, Lk, device=DEV)
+        _, lse = sk.cross_attention(q, k, v, mass_in=extra["mass"], mass_out=got, **kw)
+        own = sk.attention_mass(q, k, lse, mass_in=extra["mass"], **kw)
+        for m in (got, own):
+            assert torch.equal(m[masked], extra["mass"][masked])
+            assert bool(torch.isnan(m[~masked]).all())

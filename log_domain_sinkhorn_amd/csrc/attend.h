@@ -60,7 +60,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
   constexpr float kTerm = kExact ? 1.0f : (float)kLog2e;
   constexpr bool AHEAD = WK == 1 && TL::RB == 128;
   static_assert(WK == 1 || (WQ == 1 && NB == 1), "few rows: one tile of 32, a wave's own 32 keys");
-  using KeyT = KeyTiles<T, DP, KT, NT, D, (WK > 1)>;  // few rows: each key is read by one workgroup
+  using KeyT = KeyTiles<T, DP, KT, NT, D, (WK > 1), true>;  // few rows: each key is read by one workgroup
   constexpr int kJoinBytes = WK > 1 ? WK * 32 * W * 4 : 0;
   union Memory {
     typename KeyT::Shared keys;
@@ -211,7 +211,11 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
       }
   }
   l = half_sum(l);
-  if (!live_row) {  // a row behind its sequence (its zero scores weigh nothing)
+  // rows behind their sequence (whose zero scores weigh nothing), and rows without
+  // any key, which masked ones would make NaN where the row is no number
+  const bool live_keys = keys.live();
+  const bool has = live_row && live_keys;
+  if (!has) {
     m = -kInf;
     l = 0.0f;
   }
@@ -226,7 +230,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
 #pragma unroll
     for (int x = 0; x < NDB; ++x)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) so[(wk * W + 32 * x + 8 * (e >> 2) + 4 * h + (e & 3)) * 32 + r32] = live_row ? o[x][e] : 0.0f;
+      for (int e = 0; e < 16; ++e) so[(wk * W + 32 * x + 8 * (e >> 2) + 4 * h + (e & 3)) * 32 + r32] = has ? o[x][e] : 0.0f;
     __syncthreads();
     // thread: row tid % 32, column groups tid / 32, + NT / 32, ...
     const int64_t jrow = row0 + (tid & 31);
@@ -285,7 +289,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
         const int c = 32 * n + 8 * g + 4 * h;
         f32x4 x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = live_row ? o[n][4 * g + e] : 0.0f;
+        for (int e = 0; e < 4; ++e) x[e] = has ? o[n][4 * g + e] : 0.0f;
         if (part) {
           if (c < A.dvp) *(f32x4*)(A.opart + prow_i * A.dvp + c) = x;
         } else {

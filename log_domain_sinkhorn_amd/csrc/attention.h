@@ -444,7 +444,8 @@ struct RowTiles {
 // started while tile n is computed on. Biases arrive D - 1 tiles before that,
 // in a ring of their own: when a tile is started they decide which of its rows
 // are loaded and become its column terms (times `unit`; -inf: masked).
-template <class T, int DP, int KT, int NT, int D, bool ONCE = false>
+// SOME: live() is asked for behind the last tile.
+template <class T, int DP, int KT, int NT, int D, bool ONCE = false, bool SOME = false>
 struct KeyTiles {
   using Ld = Loader<T, DP, KT, NT, ONCE>;
   static constexpr int kTileBytes = KT * Tile<T, DP>::RB;
@@ -453,6 +454,7 @@ struct KeyTiles {
   struct Shared {
     __attribute__((aligned(16))) char tiles[D][2][kTileBytes];
     __attribute__((aligned(16))) float term[D][KT], raw[D][KT];
+    int some;  // with a bias: has a key that takes part been seen? (in LDS: a register for it makes fp32 of 128 columns spill)
   };
   Ld lk, lv;
   Shared& sm;
@@ -490,7 +492,9 @@ struct KeyTiles {
         const float x = raw[tid];
         term = x <= kMasked ? -kInf : x * unit;
       }
-      sm.term[buf][tid] = tid < left ? term : -kInf;
+      if (tid >= left) term = -kInf;
+      sm.term[buf][tid] = term;
+      if (SOME && bias && term != -kInf) sm.some = 1;
     }
     auto both = [&](auto&& live) {
       lk.start(k + first * ks, sm.tiles[buf][0], live, wave, lane);
@@ -506,6 +510,7 @@ struct KeyTiles {
   // before the first tile
   __device__ __forceinline__ void begin() const {
     if (bias) {
+      if (SOME && wave == 0) sm.some = 0;
 #pragma unroll
       for (int n = 0; n < 2 * (D - 1) && n < D; ++n) fetch(n);
       dma_wait<0>();
@@ -548,6 +553,13 @@ struct KeyTiles {
   __device__ __forceinline__ const char* ktile(int n) const { return sm.tiles[n % D][0]; }
   __device__ __forceinline__ const char* vtile(int n) const { return sm.tiles[n % D][1]; }
   __device__ __forceinline__ const float* term(int n) const { return sm.term[n % D]; }
+  // behind the last tile, by all threads of the workgroup: does any of its keys take part?
+  __device__ __forceinline__ bool live() const {
+    static_assert(SOME, "kept where it is asked for");
+    if (!bias) return count > 0;
+    __syncthreads();
+    return sm.some != 0;
+  }
   // does tile n have masked columns? (without a bias only where the live keys end)
   __device__ __forceinline__ bool masked(int n) const { return bias != nullptr || (t0 + n + 1) * KT > nkeys; }
 };

@@ -303,3 +303,30 @@ def test_weight_of_masked_keys_under_rows_that_are_no_numbers(sk, dtype, Lk, d, 
         for m in (got, own):
             assert torch.equal(m[masked], extra["mass"][masked])
             assert bool(torch.isnan(m[~masked]).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("Lq", [1, 5, 40, 300])
+@pytest.mark.parametrize("Lk", [70, 5000])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_without_keys_that_are_no_numbers(sk, dtype, Lq, Lk, d):
+    """A row whose keys are all masked gives 0 and -infinity, whatever it holds,
+    by its length as by its bias."""
+    _log(f"rows without keys {dtype} {Lq} {Lk} {d}")
+    (q, k, v, dout), _, _ = _case(dtype, 3, Lq, 4, 2, Lk, d, d, seed=40, ragged=False)
+    bias = torch.zeros(3, 2, Lk, device=DEV)
+    bias[1] = -math.inf  # entry 1 by its bias, of entry 2 the heads 2 and 3
+    bias[2, 1] = torch.finfo(F32).min
+    lens = torch.tensor([0, Lk, Lk - 1], dtype=torch.int32, device=DEV)
+    kw = dict(key_bias=bias, key_lengths=lens)
+    good = sk.cross_attention(q, k, v, **kw)
+    for bad in (math.nan, math.inf, -math.inf):
+        q2 = q.clone()
+        q2[:2, Lq // 2:, :, 3] = bad
+        q2[2, 0, 2:, d - 1] = bad
+        got = torch.empty(3, 2, Lk, device=DEV)
+        out, lse = sk.cross_attention(q2, k, v, mass_out=got, **kw)
+        assert bool((out[:2] == 0).all()) and bool((lse[:2] == -math.inf).all())
+        assert bool((out[2, :, 2:] == 0).all()) and bool((lse[2, 2:] == -math.inf).all())
+        assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+        assert bool((got[:2] == 0).all()) and bool((got[2, 1] == 0).all())

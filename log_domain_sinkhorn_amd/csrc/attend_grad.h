@@ -205,6 +205,12 @@ __global__ __launch_bounds__(256, sizeof(T) * row_width(W) <= 256 ? 2 : 1) void 
     }
   }
   if (row >= S.rows) return;
+  // a row without keys has no gradient, whatever dout and q hold (0 dout is NaN
+  // where dout is no number)
+  if (st[0] == -kInf) {
+#pragma unroll
+    for (int n = 0; n < NDB; ++n) dq[n] = zero16();
+  }
   float* prow = A.part_q ? A.part_q + (((int64_t)split * pairs + pair) * S.rows + row) * A.dp : nullptr;
   T* orow = (T*)A.dq + b * A.dqs[0] + qi * A.dqs[1] + qh * A.dqs[2];
   write_cols<T, NDB>(dq, S.scale, prow, A.dp, orow, S.d, A.vec_q, h);

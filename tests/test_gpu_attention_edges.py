@@ -330,3 +330,29 @@ def test_rows_without_keys_that_are_no_numbers(sk, dtype, Lq, Lk, d):
         assert bool((out[2, :, 2:] == 0).all()) and bool((lse[2, 2:] == -math.inf).all())
         assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
         assert bool((got[:2] == 0).all()) and bool((got[2, 1] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("Lq,Lk", [(1, 70), (40, 300), (3, 5000)])
+@pytest.mark.parametrize("d,dv", [(64, 64), (128, 80)])
+def test_gradient_of_rows_without_keys_that_are_no_numbers(sk, dtype, Lq, Lk, d, dv):
+    """No gradient of a row whose keys are all masked by bias, whatever q, dout
+    and out hold there, and of its keys."""
+    _log(f"gradient without keys {dtype} {Lq} {Lk} {d} {dv}")
+    (q, k, v, dout), _, _ = _case(dtype, 2, Lq, 4, 2, Lk, d, dv, seed=41, ragged=False)
+    bias = torch.zeros(2, 2, Lk, device=DEV)
+    bias[1] = -math.inf
+    bias[0, 1] = torch.finfo(F32).min
+    kw = dict(key_bias=bias)
+    out, lse = sk.cross_attention(q, k, v, **kw)
+    good = sk.cross_attention_grad(dout, q, k, v, out, lse, **kw)
+    for g in good:
+        assert bool((g[1] == 0).all())
+    for bad in (math.nan, math.inf):
+        for which in range(3):
+            args = [dout.clone(), q.clone(), k, v, out.clone(), lse]
+            t = args[(0, 1, 4)[which]]
+            t[1, Lq // 2:, :, 1] = bad
+            t[0, 0, 2:, -1] = bad
+            for got, want in zip(sk.cross_attention_grad(*args, **kw), good):
+                assert torch.equal(got, want), (bad, which)

@@ -430,6 +430,11 @@ def _head_tensor(t, name, dtype=None, shape=None):
         raise ValueError(f"{name} has shape {tuple(has)}, expected {tuple(shape)}")
     if t.stride(3) != 1 and has[3] > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
+    return _ungraphed(t, name)
+
+
+def _ungraphed(t, name):
+    """No call here records a graph: a tensor whose gradient would be lost is refused."""
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires grad: these calls record no graph; detach it or use torch.no_grad(), "
                          "and take gradients from cross_attention_grad")
@@ -457,7 +462,7 @@ def _plain(t, name, dtype, shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
+    return _ungraphed(t, name)
 
 
 def _same_device(first, others):

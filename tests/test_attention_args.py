@@ -304,3 +304,33 @@ def test_rows_of_the_cache_itself_are_refused_as_outputs():
                dict(ws=("k_out", 16))):
         assert refused(**kw), kw
     assert not refused(mass_out=("v", n * H * row))  # behind the first entry
+
+
+def _side_calls():
+    """Every entry point and its fp32 side arguments."""
+    q, k, v = _qkv()
+    out, lse = torch.zeros(2, 3, 4, 8, dtype=BF), torch.zeros(2, 4, 3)
+    mass, w = torch.zeros(2, 2, 5), torch.ones(2, 3)
+    bias = torch.zeros(2, 5)
+    return [
+        (sk.cross_attention, dict(q=q, k=k, v=v, key_bias=bias, row_weight=w, mass_in=mass, mass_out=mass.clone(),
+                                  out=out, lse=lse)),
+        (sk.cross_attention_grad, dict(dout=out, q=q, k=k, v=v, out=out.clone(), lse=lse, key_bias=bias, dq=q.clone(),
+                                       dk=k.clone(), dv=v.clone())),
+        (sk.attention_mass, dict(q=q, k=k, lse=lse, key_bias=bias, row_weight=w, mass_in=mass, mass_out=mass.clone())),
+        (sk.cache_evict, dict(k=k, v=v, mass=mass, keep=3, k_out=k[:, :3].clone(), v_out=v[:, :3].clone(),
+                              mass_out=mass[..., :3].clone())),
+    ]
+
+
+@pytest.mark.parametrize("call,name", [(i, n) for i, (_, kw) in enumerate(_side_calls()) for n, t in kw.items()
+                                       if isinstance(t, torch.Tensor)])
+def test_gradients_are_not_lost_silently(call, name):
+    """What requires grad is refused in every place while a graph is recorded,
+    and gets past that check otherwise (to the one of the device)."""
+    fn, kw = _side_calls()[call]
+    kw[name] = kw[name].detach().clone().requires_grad_()
+    with pytest.raises(ValueError, match="grad"):
+        fn(**kw)
+    with torch.no_grad(), pytest.raises(ValueError, match="device tensors"):
+        fn(**kw)

@@ -18,6 +18,7 @@ import os
 from dataclasses import dataclass
 
 import torch  # loads the HIP runtime the library links against
+import torch.autograd.forward_ad as _forward_ad
 
 __all__ = [
     "SinkhornError",
@@ -438,6 +439,9 @@ def _ungraphed(t, name):
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires grad: these calls record no graph; detach it or use torch.no_grad(), "
                          "and take gradients from cross_attention_grad")
+    # a tangent does not show in requires_grad; asked for only inside a dual level
+    if getattr(_forward_ad, "_current_level", 0) >= 0 and _forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{name} carries a tangent: these calls have no forward derivative; pass its primal")
     return t
 
 
@@ -527,6 +531,7 @@ def _attention(q, k, v, scale, key_bias, query_lengths, key_lengths):
             raise TypeError("key_bias must be a float32 tensor")
         if key_bias.requires_grad and torch.is_grad_enabled():
             raise ValueError("key_bias is held fixed and takes no gradient")
+        _ungraphed(key_bias, "key_bias")
         if tuple(key_bias.shape) not in ((B, lk), (B, hkv, lk)):
             raise ValueError(f"key_bias has shape {tuple(key_bias.shape)}, expected ({B}, {lk}) or ({B}, {hkv}, {lk})")
         if lk > 1 and key_bias.stride(-1) != 1:

@@ -334,3 +334,31 @@ def test_gradients_are_not_lost_silently(call, name):
         fn(**kw)
     with torch.no_grad(), pytest.raises(ValueError, match="device tensors"):
         fn(**kw)
+
+
+@pytest.mark.parametrize("call,name", [(i, n) for i, (_, kw) in enumerate(_side_calls()) for n, t in kw.items()
+                                       if isinstance(t, torch.Tensor)])
+def test_tangents_are_not_lost_silently(call, name):
+    """Forward-mode tensors are refused in every place; others inside a dual
+    level are not."""
+    import torch.autograd.forward_ad as fw
+
+    fn, kw = _side_calls()[call]
+    with fw.dual_level():
+        with pytest.raises(ValueError, match="device tensors"):
+            fn(**kw)
+        kw[name] = fw.make_dual(kw[name].detach().clone(), torch.ones_like(kw[name]))
+        with pytest.raises(ValueError, match="tangent"):
+            fn(**kw)
+        kw[name] = fw.unpack_dual(kw[name]).primal
+        with pytest.raises(ValueError, match="device tensors"):
+            fn(**kw)
+
+
+def test_function_transforms_are_refused():
+    q, k, v = _qkv(dtype=torch.float32)
+    run = lambda x: sk.cross_attention(x, k, v)[0]  # noqa: E731
+    with pytest.raises(ValueError, match="tangent"):
+        torch.func.jvp(run, (q,), (torch.ones_like(q),))
+    with pytest.raises(ValueError, match="requires grad"):
+        torch.func.grad(lambda x: run(x).sum())(q)

@@ -247,7 +247,7 @@ __device__ __forceinline__ void dma_load(__amdgpu_buffer_rsrc_t rsrc, uint32_t l
         "buffer_load_dwordx4 %1, %2, 0 offen nt lds"
         :
         : "s"(lds), "v"(off), "s"(rsrc)
-        : "memory");
+        : "memory", "m0");
   else if constexpr (CH == 16)
     asm volatile(
         "s_mov_b32 m0, %0\n"
@@ -255,7 +255,7 @@ __device__ __forceinline__ void dma_load(__amdgpu_buffer_rsrc_t rsrc, uint32_t l
         "buffer_load_dwordx4 %1, %2, 0 offen lds"
         :
         : "s"(lds), "v"(off), "s"(rsrc)
-        : "memory");
+        : "memory", "m0");
   else
     asm volatile(
         "s_mov_b32 m0, %0\n"
@@ -263,7 +263,7 @@ __device__ __forceinline__ void dma_load(__amdgpu_buffer_rsrc_t rsrc, uint32_t l
         "buffer_load_dword %1, %2, 0 offen lds"
         :
         : "s"(lds), "v"(off), "s"(rsrc)
-        : "memory");
+        : "memory", "m0");
 }
 // base: the same for all lanes (the reads make that known to the compiler)
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t dma_rsrc(const void* base) {

@@ -86,3 +86,17 @@ def test_gpu_path_runs_with_the_oracle_and_torch_compute_forbidden(monkeypatch):
     monkeypatch.undo()
     assert rep["iters"] > 0 and rep5["fine_updates"] == 1
     assert torch.isfinite(f).all() and torch.isfinite(T).all() and torch.isfinite(f5).all()
+
+
+def test_assembly_names_the_registers_it_writes():
+    """A fixed register that a block of assembly moves to is among its clobbers
+    (the compiler may keep its own value there otherwise)."""
+    blocks = 0
+    csrc = os.path.join(PKG, "csrc")
+    for name in sorted(os.listdir(csrc)):
+        text = open(os.path.join(csrc, name)).read()
+        for block in re.findall(r"asm volatile\((.*?)\);", text, flags=re.S):
+            for reg in re.findall(r"s_mov_b32 (m0|s\d+|vcc_lo|vcc_hi)\b", block):
+                blocks += 1
+                assert f'"{reg}"' in block.rsplit(":", 1)[1], f"{name}: {reg} in {block.strip()}"
+    assert blocks >= 3

@@ -150,8 +150,10 @@ struct Operand {
   int64_t at = 0;  // place of the copy in the workspace
 };
 
-Operand operand(const sinkhorn_attention* a, const void* p, const int64_t* stride, int64_t len, int32_t heads, int32_t d,
-                Space& ws) {
+// group: heads that a tile takes side by side (rows of q and dout that share a
+// key head; 1 for keys). The stride of others only moves the tile's base.
+Operand operand(const sinkhorn_attention* a, const void* p, const int64_t* stride, int64_t len, int32_t heads,
+                int32_t group, int32_t d, Space& ws) {
   const int64_t size = elem_size(a);
   Operand o;
   o.p = p;
@@ -160,14 +162,16 @@ Operand operand(const sinkhorn_attention* a, const void* p, const int64_t* strid
   o.heads = heads;
   o.d = d;
   o.dp = (int32_t)(ceil_div(d * size, 16) * 16 / size);
-  o.copy = !rows_aligned(p, stride, d, size, 16) || stride[1] * size >= (int64_t(1) << 23) ||
-           stride[2] * size * heads >= (int64_t(1) << 30);
-  // keys of one head: its stride only moves the base
-  if (stride[1] * size < (int64_t(1) << 23) && rows_aligned(p, stride, d, size, 16) && heads == a->heads_kv &&
-      len == a->len_k)
-    o.copy = false;
+  o.copy = !rows_aligned(p, stride, d, size, 16) || stride[1] >= (int64_t(1) << 23) / size ||
+           (group > 1 && stride[2] >= (int64_t(1) << 30) / size / group);
   if (o.copy) o.at = ws.take(size * a->batch * len * heads * o.dp);
   return o;
+}
+Operand rows_operand(const sinkhorn_attention* a, const void* p, const int64_t* stride, int32_t d, Space& ws) {
+  return operand(a, p, stride, a->len_q, a->heads_q, a->heads_q / a->heads_kv, d, ws);
+}
+Operand keys_operand(const sinkhorn_attention* a, const void* p, const int64_t* stride, int32_t d, Space& ws) {
+  return operand(a, p, stride, a->len_k, a->heads_kv, 1, d, ws);
 }
 
 struct MassPlan {
@@ -228,9 +232,9 @@ AttendPlan plan_attend(const sinkhorn_attention* a, const void* q, const void* k
   p.nsplit = splits(pairs * p.tiles, steps, slots, p.many ? join_steps(a) : 7.0, !p.many);
   p.partial = p.nsplit > 1;
   p.scores = mass && !p.many;
-  p.q = operand(a, q, a->q_stride, a->len_q, a->heads_q, a->d, ws);
-  p.k = operand(a, k, a->k_stride, a->len_k, a->heads_kv, a->d, ws);
-  p.v = operand(a, v, a->v_stride, a->len_k, a->heads_kv, a->dv, ws);
+  p.q = rows_operand(a, q, a->q_stride, a->d, ws);
+  p.k = keys_operand(a, k, a->k_stride, a->d, ws);
+  p.v = keys_operand(a, v, a->v_stride, a->dv, ws);
   const int64_t after_copies = ws.bytes;
   if (p.partial) {
     p.o_off = ws.take(4 * p.nsplit * pairs * rows * ceil_div(a->dv, 4) * 4);
@@ -270,10 +274,10 @@ GradPlan plan_grad(const sinkhorn_attention* a, const void* q, const void* k, co
   p.split_q = splits(pairs * p.tiles_q, ceil_div(a->len_k, step), f32 && wide(a) ? 256 : 512, join_steps(a), false);
   p.split_kv = f32 || wide(a) ? splits(pairs * p.tiles_kv, ceil_div(rows, 32), 256, 4 * join_steps(a), false)
                               : splits(pairs * p.tiles_kv, ceil_div(rows, 64), 512, 2 * join_steps(a), false);
-  p.q = operand(a, q, a->q_stride, a->len_q, a->heads_q, a->d, ws);
-  p.k = operand(a, k, a->k_stride, a->len_k, a->heads_kv, a->d, ws);
-  p.v = operand(a, v, a->v_stride, a->len_k, a->heads_kv, a->dv, ws);
-  p.dout = operand(a, dout, a->dout_stride, a->len_q, a->heads_q, a->dv, ws);
+  p.q = rows_operand(a, q, a->q_stride, a->d, ws);
+  p.k = keys_operand(a, k, a->k_stride, a->d, ws);
+  p.v = keys_operand(a, v, a->v_stride, a->dv, ws);
+  p.dout = rows_operand(a, dout, a->dout_stride, a->dv, ws);
   const int64_t dp = ceil_div(a->d, 4) * 4, dvp = ceil_div(a->dv, 4) * 4;
   p.stat_off = ws.take(8 * pairs * p.rows_pad);
   if (p.split_q > 1) p.pq_off = ws.take(4 * p.split_q * pairs * rows * dp);
@@ -294,8 +298,8 @@ struct WeightPlan {
 WeightPlan plan_mass(const sinkhorn_attention* a, const void* q, const void* k) {
   WeightPlan p{};
   Space ws;
-  p.q = operand(a, q, a->q_stride, a->len_q, a->heads_q, a->d, ws);
-  p.k = operand(a, k, a->k_stride, a->len_k, a->heads_kv, a->d, ws);
+  p.q = rows_operand(a, q, a->q_stride, a->d, ws);
+  p.k = keys_operand(a, k, a->k_stride, a->d, ws);
   p.m = plan_weight(a, ws);
   p.bytes = ws.bytes;
   return p;

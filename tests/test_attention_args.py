@@ -362,3 +362,28 @@ def test_function_transforms_are_refused():
         torch.func.jvp(run, (q,), (torch.ones_like(q),))
     with pytest.raises(ValueError, match="requires grad"):
         torch.func.grad(lambda x: run(x).sum())(q)
+
+
+@pytest.mark.parametrize("dtype,size", [(0, 4), (1, 2), (2, 2)])
+def test_heads_far_apart_are_read_where_they_are(dtype, size):
+    """[B, H, L, d] operands whose heads lie 256 MB apart: only rows of q and
+    dout whose heads share a tile, and span 1 GB together, are copied. The lengths
+    do not matter."""
+    L = sk.lib()
+    far, row = (1 << 28) // size, 64
+
+    def need(what, hq, hkv, lq, lk, q_heads, k_heads):
+        a = sk._AttentionC(dtype=dtype, batch=1, heads_q=hq, heads_kv=hkv, d=64, dv=64, len_q=lq, len_k=lk, scale=0.125)
+        for n, s in (("q", q_heads), ("dout", q_heads), ("k", k_heads), ("v", k_heads)):
+            setattr(a, n + "_stride", sk._i64x3(0, row, s))
+        n = ctypes.c_int64()
+        assert L.sinkhorn_attention_workspace(ctypes.byref(a), what, FAKE, FAKE, FAKE, FAKE, ctypes.byref(n)) == sk.OK
+        return n.value
+
+    for lq, lk in ((1000, 1000), (1000, 999), (1, 4000), (40, 70)):
+        for what in range(4):
+            rows = 2 if what == 2 else 1  # q, and dout in the backward pass
+            for hq, hkv, copied in ((8, 8, 0), (8, 4, 0), (8, 2, rows), (8, 1, rows), (6, 2, 0)):
+                near = need(what, hq, hkv, lq, lk, 64 * lq, 64 * lk)
+                pad = -(-size * lq * hq * 64 // 256) * 256
+                assert need(what, hq, hkv, lq, lk, far, far) == near + copied * pad, (what, hq, hkv, lq, lk)

@@ -356,3 +356,25 @@ def test_gradient_of_rows_without_keys_that_are_no_numbers(sk, dtype, Lq, Lk, d,
             t[0, 0, 2:, -1] = bad
             for got, want in zip(sk.cross_attention_grad(*args, **kw), good):
                 assert torch.equal(got, want), (bad, which)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (4, 2), (3, 1)])
+def test_heads_more_than_4_gb_apart(sk, dtype, Hq, Hkv):
+    """Heads whose distance passes 32 bits, read where they are or (those that
+    share a tile) from a copy."""
+    _log(f"far heads {dtype} {Hq} {Hkv}")
+    for Lq in (1, 90):
+        (q, k, v, dout), kw, extra = _case(dtype, 1, Lq, Hq, Hkv, 70, 64, 64, seed=42)
+        kw["query_lengths"] = None
+        gap = ((1 << 32) + 4096) // q.element_size()
+        far = lambda t: _far(t, (0, 64, gap, 1))  # noqa: E731
+        q2, k2, v2, dout2 = far(q), far(k), far(v), far(dout)
+        mass, mass2 = (torch.empty(1, Hkv, 70, device=DEV) for _ in range(2))
+        want = sk.cross_attention(q, k, v, mass_out=mass, **kw)
+        got = sk.cross_attention(q2, k2, v2, mass_out=mass2, **kw)
+        assert all(torch.equal(x, y) for x, y in zip(got, want)) and torch.equal(mass, mass2)
+        assert torch.equal(sk.attention_mass(q2, k2, got[1], **kw), sk.attention_mass(q, k, want[1], **kw))
+        for x, y in zip(sk.cross_attention_grad(dout2, q2, k2, v2, *got, **kw),
+                        sk.cross_attention_grad(dout, q, k, v, *want, **kw)):
+            assert torch.equal(x, y)

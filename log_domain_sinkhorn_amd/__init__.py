@@ -661,7 +661,8 @@ def cache_evict(k, v, mass, keep: int, *, key_lengths=None, first: int = 0, rece
     if tuple(v.shape) != (B, n, h, dv):
         raise ValueError(f"v has shape {tuple(v.shape)}, expected ({B}, {n}, {h}, width)")
     _plain(mass, "mass", torch.float32, (B, h, n))
-    keep, first, recent = int(keep), int(first), int(recent)
+    # as large as the C side takes them: a longer one means the same
+    keep, first, recent = (max(-1, min(int(x), (1 << 63) - 1)) for x in (keep, first, recent))
     cap = min(keep, n)
     if keep < 1:
         raise ValueError("keep must be >= 1")

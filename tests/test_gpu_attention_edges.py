@@ -378,3 +378,17 @@ def test_heads_more_than_4_gb_apart(sk, dtype, Hq, Hkv):
         for x, y in zip(sk.cross_attention_grad(dout2, q2, k2, v2, *got, **kw),
                         sk.cross_attention_grad(dout, q, k, v, *want, **kw)):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("big", [(1 << 63) - 1, 1 << 63, (1 << 64) + 2, 1 << 100])
+def test_evict_keeps_more_than_64_bits_count(sk, big):
+    """A number of kept keys beyond 64 bits keeps all of them."""
+    (_, k, v, _), _, extra = _case(BF, 2, 1, 4, 2, 50, 64, 64, seed=43, ragged=False)
+    want = sk.cache_evict(k, v, extra["mass"], 50)
+    for kw in (dict(), dict(first=3, recent=4), dict(first=big), dict(recent=big)):
+        for got, x in zip(sk.cache_evict(k, v, extra["mass"], big, **kw), want):
+            assert torch.equal(got, x)
+    with pytest.raises(sk.SinkhornError):
+        sk.cache_evict(k, v, extra["mass"], 10, first=big)
+    with pytest.raises(sk.SinkhornError):
+        sk.cache_evict(k, v, extra["mass"], 10, recent=-big)

@@ -392,3 +392,28 @@ def test_evict_keeps_more_than_64_bits_count(sk, big):
         sk.cache_evict(k, v, extra["mass"], 10, first=big)
     with pytest.raises(sk.SinkhornError):
         sk.cache_evict(k, v, extra["mass"], 10, recent=-big)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("split", [False, True], ids=["whole", "split"])
+def test_few_rows_over_many_tiles(sk, dtype, d, split):
+    """Single tokens (and three) with the weight kept where a workgroup runs over
+    nine tiles of live keys and more, alone on its keys or with others: the ring
+    of tiles in its steady state."""
+    size = torch.finfo(dtype).bits // 8
+    keys = {128: 192, 256: 96, 512: 64}[size * (64 if d == 64 else 128)]  # of a tile
+    # 256 pairs fill the compute units, with twelve tiles each; 32 are split in nine, nine tiles each
+    B, Hkv, Lk, Lq, G = (16, 2, 79 * keys - 5, 1, 2) if split else (32, 8, 11 * keys + 7, 3, 1)
+    _log(f"many tiles {dtype} {d} {(B, Hkv, Lk)}")
+    (q, k, v, _), ragged, extra = _case(dtype, B, Lq, Hkv * G, Hkv, Lk, d, d, seed=44)
+    ragged["key_lengths"][:3] = torch.tensor([Lk, Lk - 1, Lk - keys], dtype=torch.int32, device=DEV)
+    for kw in (dict(), dict(key_bias=ragged["key_bias"]), ragged):
+        got = torch.empty(B, Hkv, Lk, device=DEV)
+        out, lse = sk.cross_attention(q, k, v, row_weight=extra["weight"], mass_in=extra["mass"], mass_out=got, **kw)
+        o2, l2 = sk.cross_attention(q, k, v, **kw)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+        ref = Ref(q, k, v, **kw)
+        assert_close(out, ref.out, ref.out_tol, "out")
+        assert_close(lse, ref.lse, ref.lse_tol, "lse")
+        assert_close(got, *ref.mass(extra["mass"], extra["weight"]), "weight")

@@ -417,3 +417,125 @@ def test_few_rows_over_many_tiles(sk, dtype, d, split):
         assert_close(out, ref.out, ref.out_tol, "out")
         assert_close(lse, ref.lse, ref.lse_tol, "lse")
         assert_close(got, *ref.mass(extra["mass"], extra["weight"]), "weight")
+
+
+def _place(shape, dtype, layout):
+    """(view, everything around it): room for an output in a layout of its own,
+    filled with 7."""
+    B, L, H, d = shape
+    if layout == "heads":  # [B, H, L, d]
+        x = torch.full((B, H, L, d), 7.0, dtype=dtype, device=DEV)
+        return x.transpose(1, 2), x
+    if layout == "half":  # one half of a wider projection
+        x = torch.full((B, L, H, 2 * d), 7.0, dtype=dtype, device=DEV)
+        return x[..., d:], x
+    if layout == "odd":  # neither base nor rows aligned
+        x = torch.full((B * L * H * (d + 3) + 1,), 7.0, dtype=dtype, device=DEV)
+        return x[1:].view(B, L, H, d + 3)[..., :d], x
+    x = torch.full((B, 2 * L, H, d), 7.0, dtype=dtype, device=DEV)  # behind other rows of each entry
+    return x[:, L:], x
+
+
+def _only(view, whole):
+    """Nothing beside the view was written (the view itself is cleared)."""
+    view.fill_(7.0)
+    return bool((whole == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("layout", ["heads", "half", "odd", "behind"])
+@pytest.mark.parametrize("shape", [(2, 33, 4, 2, 65, 64, 48), (1, 200, 4, 4, 300, 96, 128), (2, 3, 6, 2, 40, 40, 8),
+                                   (1, 1, 2, 1, 4000, 64, 32), (1, 3000, 2, 1, 5, 32, 64)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_gradients_in_the_callers_tensors(sk, dtype, layout, shape):
+    """dq, dk and dv of different widths in strided tensors, from whole and from
+    split passes: the same bits as in new ones, and nothing beside them."""
+    _log(f"own gradients {dtype} {layout} {shape}")
+    (q, k, v, dout), kw, _ = _case(dtype, *shape, seed=45)
+    out, lse = sk.cross_attention(q, k, v, **kw)
+    want = sk.cross_attention_grad(dout, q, k, v, out, lse, **kw)
+    own = [_place(t.shape, dtype, layout) for t in want]
+    got = sk.cross_attention_grad(dout, q, k, v, out, lse, dq=own[0][0], dk=own[1][0], dv=own[2][0], **kw)
+    for g, w, (view, whole) in zip(got, want, own):
+        assert g.data_ptr() == view.data_ptr() and torch.equal(g, w)
+    for view, whole in own:
+        assert _only(view, whole)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_gradients_side_by_side(sk, dtype):
+    """The gradients of one projection's parts (q, k and v of the same length) in
+    the parts of one tensor, and out in the place behind them."""
+    B, L, H, d = 2, 77, 3, 64
+    gen = torch.Generator().manual_seed(46)
+    qkv, dout = _rand(gen, B, L, 4, H, d, dtype=dtype), _rand(gen, B, L, H, d, dtype=dtype)
+    q, k, v = qkv[:, :, 0], qkv[:, :, 1], qkv[:, :, 2]
+    want = sk.cross_attention(q, k, v)
+    out, lse = sk.cross_attention(q, k, v, out=qkv[:, :, 3])  # between the rows of its inputs
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    grads = sk.cross_attention_grad(dout, q, k, v, out, lse)
+    whole = torch.full_like(qkv, 7.0)
+    sk.cross_attention_grad(dout, q, k, v, out, lse, dq=whole[:, :, 0], dk=whole[:, :, 1], dv=whole[:, :, 2])
+    for i in range(3):
+        assert torch.equal(whole[:, :, i], grads[i])
+    assert bool((whole[:, :, 3] == 7.0).all())
+    for bad in (q, k[:, :, :], qkv[:, :, 2]):
+        with pytest.raises(sk.SinkhornError):
+            sk.cross_attention_grad(dout, q, k, v, out, lse, dq=bad)
+    # parts that begin inside another
+    inside = whole.as_strided(q.shape, q.stride(), d)
+    with pytest.raises(sk.SinkhornError) as e:
+        sk.cross_attention_grad(dout, q, k, v, out, lse, dq=whole[:, :, 0], dk=inside)
+    assert "overlap" in str(e.value)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("Lq,Lk", [(1, 90), (1, 6000), (40, 500)])
+def test_forward_in_the_callers_tensors(sk, dtype, Lq, Lk):
+    (q, k, v, _), kw, extra = _case(dtype, 2, Lq, 4, 2, Lk, 64, 32, seed=47)
+    mass = torch.empty(2, 2, Lk, device=DEV)
+    want = sk.cross_attention(q, k, v, mass_out=mass, **kw)
+    side = torch.full((2 * 4 * Lq + 64,), 7.0, device=DEV)
+    weight = torch.full((2 * 2 * Lk + 64,), 7.0, device=DEV)
+    out, whole = _place(want[0].shape, dtype, "behind")
+    lse, got = side[32:-32].view(2, 4, Lq), weight[32:-32].view(2, 2, Lk)
+    res = sk.cross_attention(q, k, v, out=out, lse=lse, mass_out=got, **kw)
+    assert res[0].data_ptr() == out.data_ptr() and res[1].data_ptr() == lse.data_ptr()
+    for x, y in zip((out, lse, got), (*want, mass)):
+        assert torch.equal(x, y)
+    assert _only(out, whole) and _only(lse, side) and _only(got, weight)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("layout", ["heads", "half", "odd", "behind"])
+def test_evict_into_the_callers_tensors(sk, dtype, layout):
+    """Every output given, short sequences among them: the kept places written,
+    nothing beside them; and into rows of the cache's own buffer behind its keys."""
+    B, n, H, d, dv, keep = 3, 700, 2, 64, 24, 130
+    (_, k, v, _), kw, extra = _case(dtype, B, 1, H, H, n, d, dv, seed=48)
+    lens = torch.tensor([700, 60, 131], dtype=torch.int32, device=DEV)
+    want = sk.cache_evict(k, v, extra["mass"], keep, key_lengths=lens, first=3, recent=20)
+    (ko, kw_), (vo, vw) = _place((B, keep, H, d), dtype, layout), _place((B, keep, H, dv), dtype, layout)
+    mass, index = (torch.full((B * H * keep + 64,), 7, dtype=t, device=DEV) for t in (F32, torch.int32))
+    left = torch.full((B + 64,), 7, dtype=torch.int32, device=DEV)
+    views = (ko, vo, mass[32:-32].view(B, H, keep), index[32:-32].view(B, H, keep), left[32:-32])
+    got = sk.cache_evict(k, v, extra["mass"], keep, key_lengths=lens, first=3, recent=20, k_out=views[0], v_out=views[1],
+                         mass_out=views[2], index_out=views[3], lengths_out=views[4])
+    for g, x in zip(got, views):
+        assert g.data_ptr() == x.data_ptr()
+    for g, w in zip(got[2:], want[2:]):
+        assert torch.equal(g, w)
+    for g, w in zip(got[:2], want[:2]):
+        for b, c in enumerate(want[4].tolist()):
+            assert torch.equal(g[b, :c], w[b, :c]) and bool((g[b, c:] == 7.0).all())
+    for x, whole in zip(views, (kw_, vw, mass, index, left)):
+        assert _only(x, whole)
+    # one buffer for the cache and what is left of it
+    both = torch.zeros(B, n + keep, H, d, dtype=dtype, device=DEV)
+    both[:, :n] = k
+    sk.cache_evict(both[:, :n], v, extra["mass"], keep, key_lengths=lens, first=3, recent=20, k_out=both[:, n:])
+    assert torch.equal(both[:, :n], k) and torch.equal(both[:, n:], want[0])
+    for at in (1, n - 1):
+        with pytest.raises(sk.SinkhornError) as e:
+            sk.cache_evict(both[:, :n], v, extra["mass"], keep, k_out=both[:, at:at + keep])
+        assert "overlap" in str(e.value)

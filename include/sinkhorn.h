@@ -468,9 +468,10 @@ int sinkhorn_sparse_barycentric(sinkhorn_problem* p, double eps, const float* g,
  *
  * Arithmetic: scores, softmax statistics and all sums in fp32; with 16-bit
  * types the weights (and in the backward pass their derivatives) are rounded
- * to that type for the product that follows; fp16 gradients want a loss scale
- * that keeps weight x (dout . v) between 2^-14 and 65504 where it counts. fp32 products are fp32
- * throughout. Results do not depend on scheduling: no atomics on floating
+ * to that type for the product that follows, but where all rows of a key head
+ * are at most 32 the weights are held in two such parts, so that out is off by its
+ * own rounding; fp16 gradients want a loss scale that keeps weight x (dout . v)
+ * between 2^-14 and 65504 where it counts. fp32 products are fp32 throughout. Results do not depend on scheduling: no atomics on floating
  * point, splits are joined in a fixed order.
  *
  * All calls are asynchronous on `stream` (a hipStream_t of the current

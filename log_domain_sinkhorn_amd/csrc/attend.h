@@ -206,8 +206,19 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const V8 p = pack<T>(sc[n], s);
+        if constexpr (WK > 1 && sizeof(T) == 2) {
+          // few rows wait for memory, not for products: weights in two parts, so
+          // that a token's result is off by its own rounding alone
+          const V8 r = pack_rest<T>(sc[n], s, p);
 #pragma unroll
-        for (int x = 0; x < NDB; ++x) o[x] = mma(TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane), p, o[x]);
+          for (int x = 0; x < NDB; ++x) {
+            const V8 f = TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane);
+            o[x] = mma(f, r, mma(f, p, o[x]));
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < NDB; ++x) o[x] = mma(TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane), p, o[x]);
+        }
       }
   }
   l = half_sum(l);

@@ -137,6 +137,16 @@ __device__ __forceinline__ typename Vec<T>::V8 pack(const f32x16& x, int s) {
   return v;
 }
 
+// What that rounding left of them, rounded in its turn: both parts together
+// hold a weight to 2^-16 (bf16) or 2^-22 (fp16) of it.
+template <class T>
+__device__ __forceinline__ typename Vec<T>::V8 pack_rest(const f32x16& x, int s, typename Vec<T>::V8 first) {
+  typename Vec<T>::V8 v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = (T)(x[8 * s + e] - (float)first[e]);
+  return v;
+}
+
 // ---------------------------------------------------------------- LDS tiles
 // A tile of rows of DP elements, row-major in 16-byte chunks; chunk c of row r
 // sits at c ^ swz(r). swz takes 16 consecutive rows to 16 different chunks

@@ -539,3 +539,21 @@ def test_evict_into_the_callers_tensors(sk, dtype, layout):
         with pytest.raises(sk.SinkhornError) as e:
             sk.cache_evict(both[:, :n], v, extra["mass"], keep, k_out=both[:, at:at + keep])
         assert "overlap" in str(e.value)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("B,Lq,Hq,Hkv,Lk,d,dv", [(4, 1, 8, 8, 1000, 64, 64), (2, 1, 16, 4, 5000, 128, 128), (3, 5, 12, 4, 700, 80, 96),
+                                                 (1, 32, 1, 1, 333, 50, 7), (1, 1, 1, 1, 40, 32, 32)])
+def test_few_rows_are_off_by_their_own_rounding(sk, dtype, B, Lq, Hq, Hkv, Lk, d, dv):
+    """Where all rows fit one tile, weights enter their product in two parts,
+    each rounded to u of what it holds: off by u^2 of the weight, so out is off by
+    its own rounding u |out| and what fp32 leaves. (fp16: a part below the normal
+    range by 2^-25, against weights that sum to 1 at least.)"""
+    (q, k, v, _), ragged, _ = _case(dtype, B, Lq, Hq, Hkv, Lk, d, dv, seed=49)
+    ragged["key_lengths"].clamp_(min=1)
+    for kw in (dict(), dict(key_bias=ragged["key_bias"]), ragged):
+        out, _ = sk.cross_attention(q, k, v, **kw)
+        ref = Ref(q, k, v, **kw)
+        W = (ref.P @ ref.V.abs()).permute(0, 2, 1, 3)
+        weights = 1.01 * ref.u * W  # what out_tol holds for weights in one part
+        assert_close(out, ref.out, ref.out_tol - weights + ref.u * weights, "out")

@@ -7,8 +7,8 @@
 // registers and one exchange with the lane 32 away; the weights feed
 // O^T = V^T P^T from their registers. WQ waves take different rows of the
 // same keys and WK waves different keys of the same rows (joined through LDS
-// at the end): 4 x 1 for many rows, 1 x 2 when one tile of 32 rows holds them
-// all. The keys are split over workgroups when rows and heads alone do not fill
+// at the end): 4 x 1 for many rows, 1 x 6, 3 or 2 (few_waves, by the bytes of a
+// row) when one tile of 32 rows holds them all. The keys are split over workgroups when rows and heads alone do not fill
 // the chip; k_join then joins the partial results.
 //
 // Tiles of keys lie in a ring of LDS buffers, filled by loads to LDS while an
@@ -40,7 +40,8 @@ struct AttendArgs {
 };
 
 // Few rows: waves of a workgroup, each with 32 keys of a tile, and tiles in LDS
-// for rows of `bytes` bytes: 144 KB, two thirds of it in flight.
+// for rows of `bytes` bytes: 144 KB, two thirds of it in flight; for the widest
+// rows, of which three tiles do not fit, 128 KB and half of it.
 constexpr int few_waves(int64_t bytes) { return bytes <= 128 ? 6 : (bytes <= 256 ? 3 : 2); }
 constexpr int few_depth(int64_t bytes) { return bytes <= 256 ? 3 : 2; }
 

@@ -45,11 +45,13 @@ void require(bool ok, const char* what) {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Splits of the streamed side, `steps` tiles of it, for `blocks` workgroups of
-// which `slots` run at a time: the number with the least time in units of one
-// step, counting rounds of workgroups, two steps to begin and end each, and the
-// join (`join` steps and a little per split: a join takes 4 to 7 us, a step of 64
-// keys at 128 rows about 2 in 16-bit types and 6 in fp32, of few rows about 1). `fine`: at least four rounds, so
-// that sequences of different lengths even out.
+// which about `slots` run at a time (the chip holds more at up to 64 16-bit
+// columns, and fewer of the weight's own pass in fp32 above 64): the number with
+// the least time in units of one step, counting rounds of workgroups, two steps to
+// begin and end each, and the join (`join` steps and a little per split: a join
+// takes 4 to 7 us, a step of 64 keys at 128 rows about 2 in 16-bit types and 6 in
+// fp32, of few rows about 1). `fine`: at least four rounds, so that sequences of
+// different lengths even out.
 int32_t splits(int64_t blocks, int64_t steps, int64_t slots, double join, bool fine) {
   if (blocks <= 0 || steps <= 1 || blocks >= 4 * slots) return 1;
   const int64_t most = std::min<int64_t>(steps, 512);

@@ -578,7 +578,10 @@ def cross_attention(q, k, v, *, scale=None, key_bias=None, query_lengths=None, k
     heads, rows weighted by row_weight (float32 [B, Lq], default 1).
 
     For the squared-Euclidean cost at eps, q = x, k = y, scale = 2 s / eps and
-    key_bias = log b + (g - s |y|^2) / eps average v over the plan's rows."""
+    key_bias = log b + (g - s |y|^2) / eps average v over the plan's rows.
+
+    Outputs may lie between the rows of other arguments but share no element with
+    them (mass_out with mass_in apart)."""
     a = _attention(q, k, v, scale, key_bias, query_lengths, key_lengths)
     B, lq, hq, _ = q.shape
     shape = (B, lq, hq, v.shape[3])
@@ -653,7 +656,8 @@ def cache_evict(k, v, mass, keep: int, *, key_lengths=None, first: int = 0, rece
     kept rows [B, C, H, .] with C = min(keep, L), their weights and old positions
     [B, H, C] (0 and -1 behind the kept ones) and the counts [B] (int32). Rows of
     k_out and v_out behind the kept ones are left as they were (zero in buffers
-    made here)."""
+    made here). Outputs share no element with k, v, mass or each other; they may be
+    rows of the cache's own buffers behind its keys."""
     _head_tensor(k, "k")
     B, n, h, d = k.shape
     _head_tensor(v, "v", k.dtype)

@@ -407,7 +407,10 @@ int sinkhorn_cache_evict(const sinkhorn_cache* c, const void* k, const void* v, 
     A.limit = (uint32_t*)workspace;
     A.before = (uint32_t*)workspace + 2 * pairs;
     const dim3 all = grid1(pairs, kSelThreads);
-    // few keys spread over all waves (4 x 8 x 4096: 7.6 us in place of 11.5)
+    // The smallest form that holds all keys in registers, spread over all waves; none
+    // does above 65536. k_evict_select of 32 pairs, us, forms in this order:
+    //   4096 keys 7.4, 11.1, 13.0, 16.3 |  4097 and 16384 -, 11.0, 13.5, 16.7
+    //   16385 -, -, 18.2, 25.3 | 65536 -, -, 26.9, 45.6 | 65537 -, -, -, 54.6
     if (c->len <= kSelThreads * kSelFew)
       hipLaunchKernelGGL((k_evict_select<1, kSelFew>), all, dim3(kSelThreads), 0, st, A);
     else if (c->len <= kSelChunk)

@@ -116,12 +116,13 @@ def draw(rng):
     if op == "token":
         len_q, len_k = rng.choice([1, 1, 1, 2, 4, 7]), _log_int(rng, 64, 32768)
         batch = min(batch, 16)
-        while batch * heads * len_k > 16 * 8 * 32768 // 2:
+        while batch * heads * len_k > 16 * 8 * 32768 // 3:
             batch, len_k = max(1, batch // 2), len_k // 2 + 1
     else:
         len_q, len_k = _log_int(rng, 17, 4096), _log_int(rng, 64, 16384)
         cap = 1.0e11 if dtype != "fp32" else 3.0e9  # score elements x d that a drawn case may cost
-        while batch * heads * group * len_q * max(len_k, 2 * len_q) * max(d, dv) > cap:
+        while batch * heads * group * len_q * max(len_k, 2 * len_q) * max(d, dv) > cap \
+                or batch * heads * max(len_k, 2 * len_q) * (d + dv) > 5.0e8:
             if batch > 1:
                 batch = (batch + 1) // 2 if batch > 2 else 1
             elif heads * group > 8:

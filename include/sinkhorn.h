@@ -565,6 +565,105 @@ int sinkhorn_cache_evict(const sinkhorn_cache* cache, const void* k, const void*
 /* Bytes of device workspace (16-byte aligned) that sinkhorn_cache_evict needs. Host only. */
 int sinkhorn_cache_workspace(const sinkhorn_cache* cache, int64_t* bytes);
 
+/* ---------------------------------------------------------------------------
+ * Decoding over a paged cache: rotary positions with a norm of each head, new
+ * keys and values into the cache, and attention of new tokens over it.
+ *
+ * A head x of d elements at position p becomes
+ *   n = x / sqrt(mean x^2 + eps) * weight       (with `norm`; weight NULL: 1)
+ *   (a, b) -> gain (a cos t - b sin t, a sin t + b cos t),  t = p frequencies[i]
+ * for pair i < rotated / 2 of n: elements i and i + rotated / 2, or with
+ * `interleaved` 2 i and 2 i + 1; elements from `rotated` on stay as n has them.
+ * The angles are formed and reduced in 64 bits (so far positions lose nothing),
+ * the rest is fp32, and a result is rounded once.
+ *
+ * Layout: q [batch][len][heads_q][d] and k [batch][len][heads_kv][d], and their
+ * results and gradients, by strides in elements (batch, row, head), the last
+ * dimension contiguous; any strides >= 0 and any alignment. Strides that keep 16
+ * bytes aligned, and rotated / 2 a multiple of 16 bytes, are fastest. Rows at or
+ * behind lengths[batch] give zeros (and are not appended), whatever they hold,
+ * and take no part in a gradient.
+ *
+ * All calls are asynchronous on `stream`, allocate nothing, keep no state and may
+ * be captured in a graph. Outputs may not overlap inputs or each other, but for
+ * q_out = q and k_out = k with the same strides (in place).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t dtype;              /* SINKHORN_F32, _F16 or _BF16: of q, k, their results and gradients */
+  int32_t batch;
+  int32_t heads_q, heads_kv;  /* 0: no such tensor (its pointers and strides do not count) */
+  int32_t d;                  /* 1 .. 128 (SINKHORN_ERR_UNSUPPORTED above) */
+  int32_t rotated;            /* even, 0 (no rotation) .. d */
+  int32_t interleaved;        /* 0: pairs i, i + rotated / 2; 1: pairs 2 i, 2 i + 1 */
+  int32_t norm;               /* 0: no norm */
+  int32_t weight_dtype;       /* SINKHORN_F32 or dtype: q_weight, k_weight [d] */
+  int64_t len;                /* batch * len below 2^31 */
+  double gain;                /* finite; of the rotated elements */
+  double eps;                 /* with norm: finite and >= 0 */
+  int64_t q_stride[3], k_stride[3];          /* elements: batch, row, head */
+  int64_t q_out_stride[3], k_out_stride[3];  /* of the results; backward: of their gradients */
+  int64_t dq_stride[3], dk_stride[3];        /* backward only */
+  const double* frequencies;     /* device [rotated / 2], radians per position */
+  const int32_t* positions;      /* device [batch][len], nullable: 0, 1, .. (appending: the key's place) */
+  int64_t position_stride;       /* elements from one batch entry to the next (0: shared) */
+  const int32_t* lengths;        /* device [batch], nullable: len */
+} sinkhorn_rotation;
+
+/* Frequencies base^(-2 i / rotated) for i < rotated / 2 into `out` (host), for a
+ * context `factor` times longer than the original_length positions that they
+ * were meant for: a pair that makes at most `low` turns in original_length is
+ * slowed down by the factor, one that makes `high` or more is left as it is,
+ * and in between the two are mixed linearly in the turns. original_length 0:
+ * all are slowed down. Host only. */
+int sinkhorn_rotary_frequencies(int32_t rotated, double base, double factor, double original_length,
+                                double low, double high, double* out);
+
+/* Norm and rotation of q and k in one launch. */
+int sinkhorn_rotate_heads(const sinkhorn_rotation* rot, const void* q, const void* k,
+                          const void* q_weight, const void* k_weight, void* q_out, void* k_out,
+                          void* stream);
+
+/* Backward pass: dq and dk from the gradients dq_out, dk_out of the results, and
+ * with norm those of the weights, dq_weight and dk_weight [d] (fp32, nullable:
+ * not wanted), summed over rows and heads in a fixed order. q and k are read only
+ * with norm. dq may be dq_out and dk dk_out with the same strides. With norm it
+ * takes a workspace. */
+int sinkhorn_rotation_workspace(const sinkhorn_rotation* rot, int64_t* bytes);
+int sinkhorn_rotate_heads_grad(const sinkhorn_rotation* rot, const void* dq_out, const void* dk_out,
+                               const void* q, const void* k, const void* q_weight,
+                               const void* k_weight, void* dq, void* dk, float* dq_weight,
+                               float* dk_weight, void* workspace, int64_t workspace_bytes,
+                               void* stream);
+
+/* Keys and values of several sequences in pages of page_size: key j of entry b lies
+ * in page page_table[b][j / page_size], slot j % page_size. Places of the table
+ * behind a sequence's keys may hold anything. */
+typedef struct {
+  int32_t page_size;                /* a multiple of 8 */
+  int32_t table_len;                /* pages of a sequence at most; table_len * page_size below 2^31 */
+  int64_t pages;                    /* in the cache, below 2^31 */
+  int64_t table_stride;             /* elements from one entry's pages to the next's */
+  int64_t k_stride[3], v_stride[3]; /* elements: page, slot, head */
+  int32_t dv;                       /* width of a value head, 1 .. 128 */
+  const int32_t* page_table;        /* device */
+  const int32_t* lengths;           /* device [batch]: keys in the cache, taken as within
+                                     * [0, table_len * page_size]; before the call when appending */
+} sinkhorn_pages;
+
+/* Appends the tokens of rot->len rows (rot->lengths[b] of them where that is
+ * given) to the sequences: row i's key, normed and rotated, and value v
+ * [batch][len][heads_kv][dv] go to place lengths[b] + i of the cache, and their
+ * queries, normed and rotated, to q_out (heads_q 0: no queries). Without positions
+ * a token's position is its place. A place whose page is outside [0, pages), or
+ * behind the table, is not written. lengths_out [batch] (may not be the cache's
+ * lengths) receives the keys in the cache after the call. Everything else in the
+ * cache is left as it was. No two tokens may share a place; pages that several
+ * sequences share must lie before what they append. */
+int sinkhorn_cache_append(const sinkhorn_rotation* rot, const sinkhorn_pages* cache, const void* q,
+                          const void* k, const void* v, const int64_t* v_stride,
+                          const void* q_weight, const void* k_weight, void* q_out, void* k_cache,
+                          void* v_cache, int32_t* lengths_out, void* stream);
+
 /* Measurement hook. `kinds` is a bit set of the kernels to time: every later
  * launch of a selected kernel carries two HIP events that its own dispatch
  * records at the kernel's start and end (hipExtLaunchKernelGGL), so the time

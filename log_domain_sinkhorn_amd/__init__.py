@@ -31,6 +31,10 @@ __all__ = [
     "cross_attention_grad",
     "attention_mass",
     "cache_evict",
+    "rotary_frequencies",
+    "rotate_heads",
+    "rotate_heads_grad",
+    "cache_append",
     "lib",
     "LIB_PATH",
     "OK",
@@ -195,6 +199,47 @@ class _CacheC(ctypes.Structure):
     ]
 
 
+class _RotationC(ctypes.Structure):
+    _fields_ = [
+        ("dtype", _i32),
+        ("batch", _i32),
+        ("heads_q", _i32),
+        ("heads_kv", _i32),
+        ("d", _i32),
+        ("rotated", _i32),
+        ("interleaved", _i32),
+        ("norm", _i32),
+        ("weight_dtype", _i32),
+        ("len", _i64),
+        ("gain", _f64),
+        ("eps", _f64),
+        ("q_stride", _i64x3),
+        ("k_stride", _i64x3),
+        ("q_out_stride", _i64x3),
+        ("k_out_stride", _i64x3),
+        ("dq_stride", _i64x3),
+        ("dk_stride", _i64x3),
+        ("frequencies", _p),
+        ("positions", _p),
+        ("position_stride", _i64),
+        ("lengths", _p),
+    ]
+
+
+class _PagesC(ctypes.Structure):
+    _fields_ = [
+        ("page_size", _i32),
+        ("table_len", _i32),
+        ("pages", _i64),
+        ("table_stride", _i64),
+        ("k_stride", _i64x3),
+        ("v_stride", _i64x3),
+        ("dv", _i32),
+        ("page_table", _p),
+        ("lengths", _p),
+    ]
+
+
 # name -> argtypes (every entry point declared in include/sinkhorn.h)
 _SIGS = {
     "sinkhorn_strerror": ([_i32], ctypes.c_char_p),
@@ -229,6 +274,11 @@ _SIGS = {
     "sinkhorn_attention_mass": ([_p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
     "sinkhorn_cache_evict": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
     "sinkhorn_cache_workspace": ([_p, _p], _i32),
+    "sinkhorn_rotary_frequencies": ([_i32, _f64, _f64, _f64, _f64, _f64, _p], _i32),
+    "sinkhorn_rotate_heads": ([_p, _p, _p, _p, _p, _p, _p, _p], _i32),
+    "sinkhorn_rotation_workspace": ([_p, _p], _i32),
+    "sinkhorn_rotate_heads_grad": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
+    "sinkhorn_cache_append": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p], _i32),
     "sinkhorn_profile_enable": ([_p, _i32], _i32),
     "sinkhorn_profile_read": ([_p, _p, _p, _p], _i32),
     "sinkhorn_probe_issue_rate": ([_i32, _i32, _p, _p, _p, _p], _i32),
@@ -703,6 +753,226 @@ def cache_evict(k, v, mass, keep: int, *, key_lengths=None, first: int = 0, rece
             mass.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), mass_out.data_ptr(), index_out.data_ptr(),
             lengths_out.data_ptr(), _at(ws), size.value)
     return k_out, v_out, mass_out, index_out, lengths_out
+
+
+# ---------------------------------------------------------------- decoding over a paged cache
+def rotary_frequencies(rotated: int, base: float = 10000.0, *, factor: float = 1.0, original_length: float = 0.0,
+                       low: float = 1.0, high: float = 32.0, device="cuda:0"):
+    """Radians per position of each pair, float64 [rotated / 2] on `device`
+    (``sinkhorn_rotary_frequencies``): base ** (-2 i / rotated), slowed down by
+    `factor` for a context that much longer; with original_length only for pairs of
+    few turns in it (all of it up to `low` turns, none from `high` on, linearly
+    mixed in between)."""
+    buf = (_f64 * max(1, int(rotated) // 2))()
+    _check(lib().sinkhorn_rotary_frequencies(int(rotated), float(base), float(factor), float(original_length),
+                                             float(low), float(high), buf), "rotary_frequencies")
+    return torch.tensor(list(buf)[:int(rotated) // 2], dtype=torch.float64, device=device)
+
+
+def _rotation(q, k, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, lengths):
+    """The description of a call, and the tensors that it points to; q or k may be None."""
+    if q is None and k is None:
+        raise ValueError("q and k are both missing")
+    one = k if q is None else q
+    B, n, _, d = one.shape
+    r = _RotationC(_ATTN_DTYPES[one.dtype], B, 0, 0, d)
+    if q is not None:
+        r.heads_q = q.shape[2]
+        r.q_stride = _strides3(q)
+    if k is not None:
+        if k.dtype != one.dtype:
+            raise TypeError(f"k must be {one.dtype}, got {k.dtype}")
+        if k.shape[0] != B or k.shape[1] != n or k.shape[3] != d:
+            raise ValueError(f"k has shape {tuple(k.shape)}, expected ({B}, {n}, heads, {d})")
+        r.heads_kv = k.shape[2]
+        r.k_stride = _strides3(k)
+    r.len = n
+    if frequencies is not None:
+        if not isinstance(frequencies, torch.Tensor) or frequencies.dtype != torch.float64:
+            raise TypeError("frequencies must be a float64 tensor")
+        if frequencies.dim() != 1 or 2 * frequencies.shape[0] > d:
+            raise ValueError(f"frequencies have shape {tuple(frequencies.shape)}, expected at most ({d // 2},)")
+        if not frequencies.is_contiguous():
+            raise ValueError("frequencies must be contiguous")
+        r.rotated = 2 * _ungraphed(frequencies, "frequencies").shape[0]
+        r.frequencies = frequencies.data_ptr()
+        r.interleaved = bool(interleaved)
+        r.gain = float(gain)
+    elif positions is not None:
+        raise ValueError("positions need frequencies")
+    if norm_eps is not None:
+        r.norm = 1
+        r.eps = float(norm_eps)
+        kind = None
+        for w, t, name in ((q_weight, q, "q_weight"), (k_weight, k, "k_weight")):
+            if w is None:
+                continue
+            if t is None:
+                raise ValueError(f"{name} without its tensor")
+            if kind is None:
+                kind = w.dtype if isinstance(w, torch.Tensor) and w.dtype == one.dtype else torch.float32
+            _plain(w, name, kind, (d,))
+        r.weight_dtype = 0 if kind is None else _ATTN_DTYPES[kind]
+    elif q_weight is not None or k_weight is not None:
+        raise ValueError("weights need norm_eps")
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
+            raise TypeError("positions must be an int32 tensor")
+        if tuple(positions.shape) not in ((B, n), (n,)):
+            raise ValueError(f"positions have shape {tuple(positions.shape)}, expected ({B}, {n}) or ({n},)")
+        if n > 1 and positions.stride(-1) != 1:
+            raise ValueError("the last dimension of positions must be contiguous")
+        r.positions = positions.data_ptr()
+        r.position_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    if lengths is not None:
+        r.lengths = _plain(lengths, "lengths", torch.int32, (B,)).data_ptr()
+    return r
+
+
+def _result(t, like, name):
+    """An output like `like`: the caller's, or a new one."""
+    if like is None:
+        if t is not None:
+            raise ValueError(f"{name} without its tensor")
+        return None
+    if t is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    return _written(_head_tensor(t, name, like.dtype, like.shape), name)
+
+
+def rotate_heads(q, k=None, *, positions=None, frequencies=None, interleaved=False, gain=1.0, norm_eps=None,
+                 q_weight=None, k_weight=None, lengths=None, q_out=None, k_out=None):
+    """(q_out, k_out): the heads of q [B, L, Hq, d] and k [B, L, Hkv, d] normed and
+    rotated to their positions, in one launch (``sinkhorn_rotate_heads``).
+
+    With norm_eps each head is divided by sqrt(mean x^2 + norm_eps) and multiplied by
+    its weight (q_weight, k_weight [d], float32 or of q's type; default 1). With
+    frequencies (float64 [r / 2], see rotary_frequencies) its first r elements turn:
+    pairs (i, i + r / 2), or (2 i, 2 i + 1) if interleaved, by positions frequencies[i],
+    times gain. positions is int32 [B, L] or [L], default 0, 1, ... Rows >= lengths[b]
+    (int32 [B]) give zeros. q_out may be q and k_out k; k may be None."""
+    _head_tensor(q, "q")
+    if k is not None:
+        _head_tensor(k, "k")
+    r = _rotation(q, k, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, lengths)
+    q_out, k_out = _result(q_out, q, "q_out"), _result(k_out, k, "k_out")
+    index = _same_device(q, (k, frequencies, q_weight, k_weight, positions, lengths, q_out, k_out))
+    r.q_out_stride = _strides3(q_out)
+    if k is not None:
+        r.k_out_stride = _strides3(k_out)
+    _launch(index, "rotate_heads", lib().sinkhorn_rotate_heads, ctypes.byref(r), q.data_ptr(), _at(k), _at(q_weight),
+            _at(k_weight), q_out.data_ptr(), _at(k_out))
+    return q_out, k_out
+
+
+def rotate_heads_grad(dq_out, dk_out=None, q=None, k=None, *, positions=None, frequencies=None, interleaved=False,
+                      gain=1.0, norm_eps=None, q_weight=None, k_weight=None, lengths=None, dq=None, dk=None):
+    """(dq, dk, dq_weight, dk_weight) from the gradients of rotate_heads' results
+    for the same arguments (``sinkhorn_rotate_heads_grad``). q and k are needed with
+    norm_eps only; the weights' gradients (float32 [d], also where the weight is
+    left at 1) are None without it. dk_out and k may be None. dq may be dq_out and dk
+    dk_out."""
+    _head_tensor(dq_out, "dq_out")
+    if dk_out is not None:
+        _head_tensor(dk_out, "dk_out")
+    r = _rotation(dq_out, dk_out, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, lengths)
+    r.q_out_stride = r.q_stride
+    r.k_out_stride = r.k_stride
+    wq = wk = None
+    if norm_eps is not None:
+        if q is None or (k is None) != (dk_out is None):
+            raise ValueError("the gradient of a norm needs q and k")
+        _head_tensor(q, "q", dq_out.dtype, dq_out.shape)
+        r.q_stride = _strides3(q)
+        if k is not None:
+            _head_tensor(k, "k", dk_out.dtype, dk_out.shape)
+            r.k_stride = _strides3(k)
+    dq, dk = _result(dq, dq_out, "dq"), _result(dk, dk_out, "dk")
+    index = _same_device(dq_out, (dk_out, q, k, frequencies, q_weight, k_weight, positions, lengths, dq, dk))
+    r.dq_stride = _strides3(dq)
+    if dk is not None:
+        r.dk_stride = _strides3(dk)
+    ws, n = None, 0
+    if norm_eps is not None:
+        device, d = dq_out.device, dq_out.shape[3]
+        wq = torch.empty(d, dtype=torch.float32, device=device)
+        wk = None if dk is None else torch.empty(d, dtype=torch.float32, device=device)
+        size = _i64()
+        _check(lib().sinkhorn_rotation_workspace(ctypes.byref(r), ctypes.byref(size)), "rotation_workspace")
+        n = size.value
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+    _launch(index, "rotate_heads_grad", lib().sinkhorn_rotate_heads_grad, ctypes.byref(r), dq_out.data_ptr(),
+            _at(dk_out), _at(q), _at(k), _at(q_weight), _at(k_weight), dq.data_ptr(), _at(dk), _at(wq), _at(wk),
+            _at(ws), n)
+    return dq, dk, wq, wk
+
+
+def _pages(dtype, B, heads, d, k_cache, v_cache, page_table, lengths, name):
+    """The description of a paged cache of k [pages, page_size, heads, d] and v."""
+    _head_tensor(k_cache, "k_cache", dtype)
+    _head_tensor(v_cache, "v_cache", dtype)
+    pages, size, _, _ = k_cache.shape
+    dv = v_cache.shape[3]
+    if tuple(k_cache.shape) != (pages, size, heads, d):
+        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected (pages, page_size, {heads}, {d})")
+    if tuple(v_cache.shape) != (pages, size, heads, dv):
+        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected ({pages}, {size}, {heads}, width)")
+    if not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32:
+        raise TypeError("page_table must be an int32 tensor")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected ({B}, pages of a sequence)")
+    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+        raise ValueError("the last dimension of page_table must be contiguous")
+    _plain(lengths, name, torch.int32, (B,))
+    return _PagesC(size, page_table.shape[1], pages, page_table.stride(0) if B > 1 else 0, _strides3(k_cache),
+                   _strides3(v_cache), dv, page_table.data_ptr(), lengths.data_ptr())
+
+
+def cache_append(k, v, k_cache, v_cache, page_table, cache_lengths, *, new_lengths=None, positions=None,
+                 frequencies=None, interleaved=False, gain=1.0, norm_eps=None, k_weight=None, q=None, q_weight=None,
+                 q_out=None, lengths_out=None):
+    """Append new tokens to a paged cache (``sinkhorn_cache_append``).
+
+    The keys k [B, L, Hkv, d], normed and rotated as by rotate_heads (neither without
+    norm_eps and frequencies), and the values v [B, L, Hkv, dv] of the first
+    new_lengths[b] tokens (int32 [B], default L) go behind the cache_lengths[b] keys
+    (int32 [B]) that sequence b has. k_cache [pages, page_size, Hkv, d] and v_cache
+    [pages, page_size, Hkv, dv] hold key j in page page_table[b, j // page_size]
+    (int32 [B, pages of a sequence]), slot j % page_size; page_size is a multiple of 8.
+    A token's position is its place in the sequence, or positions (int32 [B, L] or
+    [L]). With q [B, L, Hq, d] the tokens' queries are normed and rotated on the way.
+
+    Returns (lengths_out, q_out): the keys in the cache now (int32 [B]) and the queries
+    (None without q; zeros behind new_lengths). Tokens whose page is outside the cache
+    or behind the table are not written. No two tokens may share a place."""
+    _head_tensor(k, "k")
+    B, n, h, d = k.shape
+    _head_tensor(v, "v", k.dtype)
+    if v.shape[:3] != k.shape[:3]:
+        raise ValueError(f"v has shape {tuple(v.shape)}, expected ({B}, {n}, {h}, width)")
+    if q is not None:
+        _head_tensor(q, "q", k.dtype)
+        if q.shape[0] != B or q.shape[1] != n or q.shape[3] != d:
+            raise ValueError(f"q has shape {tuple(q.shape)}, expected ({B}, {n}, heads, {d})")
+    r = _rotation(q, k, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, new_lengths)
+    c = _pages(k.dtype, B, h, d, k_cache, v_cache, page_table, cache_lengths, "cache_lengths")
+    if v.shape[3] != c.dv:
+        raise ValueError(f"v has shape {tuple(v.shape)}, expected ({B}, {n}, {h}, {c.dv})")
+    _written(k_cache, "k_cache")
+    _written(v_cache, "v_cache")
+    if lengths_out is not None:
+        _plain(lengths_out, "lengths_out", torch.int32, (B,))
+    q_out = _result(q_out, q, "q_out")
+    index = _same_device(k, (v, q, k_cache, v_cache, page_table, cache_lengths, new_lengths, positions, frequencies,
+                             k_weight, q_weight, q_out, lengths_out))
+    if q is not None:
+        r.q_out_stride = _strides3(q_out)
+    if lengths_out is None:
+        lengths_out = torch.empty(B, dtype=torch.int32, device=k.device)
+    _launch(index, "cache_append", lib().sinkhorn_cache_append, ctypes.byref(r), ctypes.byref(c), _at(q), k.data_ptr(),
+            v.data_ptr(), _strides3(v), _at(q_weight), _at(k_weight), _at(q_out), k_cache.data_ptr(),
+            v_cache.data_ptr(), lengths_out.data_ptr())
+    return lengths_out, q_out
 
 
 class Problem:

@@ -16,6 +16,7 @@
 // the places found by k_evict_select that one took 78 us in place of 27; k_evict_move
 // takes 112).
 #include "attention.h"
+#include "attention_host.h"
 #include "overlap.h"
 
 namespace sk {
@@ -280,24 +281,6 @@ __global__ __launch_bounds__(kGroup) void k_evict_move(EvictArgs A) {
       }
     }
   }
-}
-
-template <class F>
-int guarded(F&& body) {
-  try {
-    set_last_error("");
-    return body();
-  } catch (const Failure& f) {
-    set_last_error(f.msg);
-    return f.code;
-  } catch (...) {
-    set_last_error("unexpected exception");
-    return SINKHORN_ERR_HIP;
-  }
-}
-
-void require(bool ok, const char* what) {
-  if (!ok) fail(SINKHORN_ERR_INVALID_ARG, what);
 }
 
 void check(const sinkhorn_cache* c) {

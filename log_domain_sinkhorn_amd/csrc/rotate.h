@@ -1,0 +1,444 @@
+// Rotary positions with a norm of each head, and the same on the way into a
+// paged cache.
+//
+// A group of LPH lanes holds one head at a time, a lane two chunks of E elements
+// (16 bytes each where the layout allows it) whose pairs it has both elements of:
+// chunks u and u + rotated / (2 E) for pairs half of the rotated part apart, 2 u and
+// 2 u + 1 for neighbours. So the rotation is in registers, the norm takes one sum
+// over the group's lanes, and a lane's E angles serve all heads of its token: the
+// angles are formed in 64 bits, reduced to a quarter turn there, and their sine and
+// cosine are Taylor sums in fp32 (about 40 operations an angle against 14 bytes
+// and more of traffic for each head that uses it).
+//
+// Bound by memory: each element is read once and written once.
+#pragma once
+
+#include "attention.h"
+#include "attention_host.h"
+#include "pages.h"
+
+namespace sk {
+namespace attn {
+
+// The heads of one tensor.
+struct HeadRows {
+  const void* src;
+  void* dst;
+  const void* weight;  // of the norm, nullable
+  int64_t ss[3], ds[3];  // elements: batch, row, head; ds of a cache: page, slot, head
+  int32_t heads;
+};
+
+struct RotateArgs {
+  HeadRows q, k, v;  // v: appended as it is
+  int32_t batch, len, d, dv;
+  int32_t steps;   // rows of a batch entry that are visited: len, at least one where lengths are written
+  int32_t heads;   // of q, k and v
+  int32_t groups;  // log2 of the lane groups that share a token's heads
+  int32_t half;    // pairs of a head
+  bool interleaved, norm, weight_f32;
+  float gain, sign, eps, inv_d;  // sign: -1 turns back; 1 / d
+  const double* freq;
+  const int32_t* positions;  // nullable
+  int64_t position_stride;
+  const int32_t* lengths;  // nullable
+  Paging P;
+  int32_t* lengths_out;  // null: no cache
+  // backward
+  const void* dq_out;
+  const void* dk_out;
+  int64_t dqs[3], dks[3];  // of dq_out and dk_out
+  float* part;             // [workgroups][2][128] partial sums of the weights' gradients
+};
+
+// E elements as they lie in memory.
+template <class T, int E>
+struct Raw {
+  typedef T V __attribute__((ext_vector_type(E)));
+  __device__ __forceinline__ static float get(const V& v, int e) { return (float)v[e]; }
+  __device__ __forceinline__ static void set(V& v, int e, float x) { v[e] = (T)x; }
+};
+template <class T>
+struct Raw<T, 1> {
+  typedef T V;
+  __device__ __forceinline__ static float get(const V& v, int) { return (float)v; }
+  __device__ __forceinline__ static void set(V& v, int, float x) { v = (T)x; }
+};
+template <class T, int E>
+__device__ __forceinline__ void widen(const typename Raw<T, E>::V& v, float (&x)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = Raw<T, E>::get(v, e);
+}
+template <class T, int E>
+__device__ __forceinline__ typename Raw<T, E>::V narrow(const float (&x)[E]) {
+  typename Raw<T, E>::V v;
+#pragma unroll
+  for (int e = 0; e < E; ++e) Raw<T, E>::set(v, e, x[e]);
+  return v;
+}
+
+// cos and sin of `turns` whole turns. The reduction to x quarter turns, |x| <= 1/2,
+// is exact in 64 bits; sine and cosine of x pi / 2 by their Taylor sums, whose
+// first terms left out are below 2e-9 and 2e-10.
+__device__ __forceinline__ void cos_sin(double turns, float& c, float& s) {
+  const double f = turns - rint(turns);
+  const double n = rint(4.0 * f);
+  const float x = (float)fma(4.0, f, -n);
+  const int quarter = (int)n;
+  constexpr double h = 1.57079632679489661923;  // pi / 2
+  constexpr double h2 = h * h;
+  const float z = x * x;
+  const float sn = x * fmaf(fmaf(fmaf(fmaf(z, (float)(h2 * h2 * h2 * h2 * h / 362880), (float)(-h2 * h2 * h2 * h / 5040)),
+                                      z, (float)(h2 * h2 * h / 120)), z, (float)(-h2 * h / 6)), z, (float)h);
+  const float cs = fmaf(fmaf(fmaf(fmaf(fmaf(z, (float)(-h2 * h2 * h2 * h2 * h2 / 3628800), (float)(h2 * h2 * h2 * h2 / 40320)),
+                                       z, (float)(-h2 * h2 * h2 / 720)), z, (float)(h2 * h2 / 24)), z, (float)(-h2 / 2)), z, 1.0f);
+  const float a = quarter & 1 ? sn : cs, b = quarter & 1 ? cs : sn;
+  c = (quarter + 1) & 2 ? -a : a;
+  s = quarter & 2 ? -b : b;
+}
+
+// A lane's part of the heads of width d.
+template <int E>
+struct Lane {
+  int at[2];     // first element of its chunks
+  bool has[2];   // are they within the head?
+  bool turns;    // are they rotated?
+
+  // u: the lane's place in its group; half: rotated pairs
+  __device__ __forceinline__ Lane(int u, int half, bool interleaved, int d) {
+    const int n = half / E;  // lanes whose chunks are rotated
+    turns = u < n;
+    const int a = turns && !interleaved ? u : 2 * u, b = turns && !interleaved ? u + n : 2 * u + 1;
+    at[0] = a * E;
+    at[1] = b * E;
+    has[0] = at[0] < d;
+    has[1] = at[1] < d;
+  }
+};
+
+// (x, y) turned by the lane's angles: element pairs (x[e], y[e]), or with
+// `interleaved` neighbours in x, then in y.
+template <int E>
+__device__ __forceinline__ void turn(float (&x)[E], float (&y)[E], const float (&c)[E], const float (&s)[E], bool interleaved) {
+  if (E > 1 && interleaved) {
+    if constexpr (E > 1) {
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        const float a = x[2 * e], b = x[2 * e + 1], p = y[2 * e], q = y[2 * e + 1];
+        x[2 * e] = fmaf(a, c[e], -(b * s[e]));
+        x[2 * e + 1] = fmaf(a, s[e], b * c[e]);
+        y[2 * e] = fmaf(p, c[E / 2 + e], -(q * s[E / 2 + e]));
+        y[2 * e + 1] = fmaf(p, s[E / 2 + e], q * c[E / 2 + e]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float a = x[e], b = y[e];
+      x[e] = fmaf(a, c[e], -(b * s[e]));
+      y[e] = fmaf(a, s[e], b * c[e]);
+    }
+  }
+}
+
+// A lane's frequencies in turns per position.
+template <int E>
+__device__ __forceinline__ void lane_frequencies(const RotateArgs& A, const Lane<E>& l, int u, double (&w)[E]) {
+  constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
+#pragma unroll
+  for (int e = 0; e < E; ++e) w[e] = l.turns ? A.freq[u * E + e] * kTurn : 0.0;
+}
+template <int E>
+__device__ __forceinline__ void lane_angles(const RotateArgs& A, const Lane<E>& l, const double (&w)[E], int position,
+                                            float (&c)[E], float (&s)[E]) {
+  if (!l.turns) return;
+  const double p = (double)position;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    cos_sin(p * w[e], c[e], s[e]);
+    c[e] *= A.gain;
+    s[e] *= A.gain * A.sign;
+  }
+}
+
+template <class T, int E>
+__device__ __forceinline__ void lane_weight(const RotateArgs& A, const void* weight, const Lane<E>& l, int i, float (&x)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int c = l.at[i] + e;
+    x[e] = !weight || !l.has[i] ? 1.0f : (A.weight_f32 ? ((const float*)weight)[c] : (float)((const T*)weight)[c]);
+  }
+}
+
+// Sum over the LPH lanes of a group.
+template <int LPH>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+  for (int k = LPH / 2; k > 0; k >>= 1) x += __shfl_xor(x, k, 64);
+  return x;
+}
+
+__device__ __forceinline__ int live_tokens(const RotateArgs& A, int b) {
+  if (!A.lengths) return A.len;
+  const int n = A.lengths[b];
+  return n < 0 ? 0 : (n > A.len ? A.len : n);
+}
+
+// 1 / sqrt(mean + eps) from a head's sum of squares. fp32: rounded in full; else
+// to about one step of fp32.
+template <class T>
+__device__ __forceinline__ float inverse_rms(const RotateArgs& A, float sum) {
+  const float x = fmaf(sum, A.inv_d, A.eps);
+  if constexpr (sizeof(T) == 4)
+    return 1.0f / sqrtf(x);
+  else
+    return __builtin_amdgcn_rsqf(x);
+}
+
+// Forward (and the backward pass without a norm: the rotation the other way). A
+// token's heads are dealt to 1 << A.groups lane groups, neighbours to neighbours.
+// U heads of a group are loaded before the first is used.
+template <class T, int E, int LPH, int U>
+__global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
+  typedef typename Raw<T, E>::V V;
+  const int lane = threadIdx.x % LPH;
+  const int64_t item = (int64_t)blockIdx.x * (256 / LPH) + threadIdx.x / LPH;
+  const int64_t token = item >> A.groups;
+  const int g = (int)(item & ((1 << A.groups) - 1));
+  if (token >= (int64_t)A.batch * A.steps) return;
+  const int b = (int)((uint32_t)token / (uint32_t)A.steps), i = (int)((uint32_t)token - (uint32_t)b * (uint32_t)A.steps);
+  const int ntokens = live_tokens(A, b);
+  const bool live = i < ntokens;
+  const Lane<E> lt(lane, A.half, A.interleaved, A.d), lv(lane, 0, false, A.dv);
+  // where the token's key and value go
+  int64_t kto, vto = 0;
+  int place = i;
+  bool keys = true;
+  if (A.lengths_out) {
+    const int before = paged_keys(A.P, b);
+    const int64_t j = (int64_t)before + i, cap = (int64_t)A.P.len * A.P.size;
+    if (i == 0 && g == 0 && lane == 0) A.lengths_out[b] = (int)(before + ntokens < cap ? before + ntokens : cap);
+    if (i >= A.len) return;  // no rows at all
+    keys = live && j < cap;
+    place = (int)j;
+    kto = 0;
+    if (keys) {
+      const uint32_t page = page_of(A.P, (uint32_t)j);
+      const int64_t id = A.P.table[b * A.P.stride + page];
+      keys = id >= 0 && id < A.P.pages;
+      const int64_t slot = j - (int64_t)page * A.P.size;
+      kto = id * A.k.ds[0] + slot * A.k.ds[1];
+      vto = id * A.v.ds[0] + slot * A.v.ds[1];
+    }
+  } else {
+    kto = b * A.k.ds[0] + i * A.k.ds[1];
+  }
+  const int64_t qto = b * A.q.ds[0] + i * A.q.ds[1];
+  float c[E], s[E];
+  {
+    double w[E];
+    lane_frequencies<E>(A, lt, lane, w);
+    if (A.positions) place = A.positions[b * A.position_stride + i];
+    lane_angles<E>(A, lt, w, place, c, s);
+  }
+  float wq[2][E], wk[2][E];
+  if (A.norm)
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      lane_weight<T, E>(A, A.q.weight, lt, n, wq[n]);
+      lane_weight<T, E>(A, A.k.weight, lt, n, wk[n]);
+    }
+  const T* const qsrc = (const T*)A.q.src + b * A.q.ss[0] + i * A.q.ss[1];
+  const T* const ksrc = (const T*)A.k.src + b * A.k.ss[0] + i * A.k.ss[1];
+  const T* const vsrc = (const T*)A.v.src + b * A.v.ss[0] + i * A.v.ss[1];
+  const int hk = A.q.heads, hv = A.q.heads + A.k.heads;
+  for (int h0 = g; h0 < A.heads; h0 += U << A.groups) {
+    V raw[U][2];
+#pragma unroll
+    for (int n = 0; n < U; ++n) {
+      const int h = h0 + (n << A.groups);
+      const bool isq = h < hk, isv = h >= hv, ok = live && h < A.heads && (isq || keys);
+      const T* from = isq ? qsrc + h * A.q.ss[2] : (isv ? vsrc + (h - hv) * A.v.ss[2] : ksrc + (h - hk) * A.k.ss[2]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        raw[n][k] = V{};
+        if (ok && (isv ? lv.has[k] : lt.has[k])) raw[n][k] = *(const V*)(from + (isv ? lv.at[k] : lt.at[k]));
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < U; ++n) {
+      const int h = h0 + (n << A.groups);
+      const bool isq = h < hk, isv = h >= hv, ok = h < A.heads && (isq || keys);
+      float x[2][E];
+      widen<T, E>(raw[n][0], x[0]);
+      widen<T, E>(raw[n][1], x[1]);
+      if (A.norm) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum = fmaf(x[k][e], x[k][e], sum);
+        const float r = inverse_rms<T>(A, group_sum<LPH>(sum));
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[k][e] = x[k][e] * r * (isq ? wq[k][e] : wk[k][e]);
+      }
+      if (lt.turns) turn<E>(x[0], x[1], c, s, A.interleaved);
+      T* to = isq ? (T*)A.q.dst + qto + h * A.q.ds[2]
+                  : (isv ? (T*)A.v.dst + vto + (h - hv) * A.v.ds[2] : (T*)A.k.dst + kto + (h - hk) * A.k.ds[2]);
+      const bool changed = !isv && live && (A.norm || lt.turns);  // else as it is: values, zeros, the rest of a head
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (ok && (isv ? lv.has[k] : lt.has[k]))
+          *(V*)(to + (isv ? lv.at[k] : lt.at[k])) = changed ? narrow<T, E>(x[k]) : raw[n][k];
+    }
+  }
+}
+
+// Backward with a norm: with g = the rotation undone on the result's gradient,
+// xh = x r, r = 1 / rms, u = g w:  dx = r (u - xh mean(u xh)),  dw = sum g xh.
+// A lane adds up the weights' gradients of its chunks over all rows that it meets;
+// groups of a wave, waves and workgroups are then added in a fixed order.
+template <class T, int E, int LPH>
+__global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
+  typedef typename Raw<T, E>::V V;
+  __shared__ float sw[4][2][kMaxD];
+  const int lane = threadIdx.x % LPH, wave = threadIdx.x >> 6;
+  const Lane<E> l(lane, A.half, A.interleaved, A.d);
+  double w[E];
+  lane_frequencies<E>(A, l, lane, w);
+  float acc[2][2][E], weight[2][2][E];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    lane_weight<T, E>(A, A.q.weight, l, k, weight[0][k]);
+    lane_weight<T, E>(A, A.k.weight, l, k, weight[1][k]);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[p][k][e] = 0.0f;
+  }
+  const int64_t items = ((int64_t)A.batch * A.len) << A.groups, step = (int64_t)gridDim.x * (256 / LPH);
+  for (int64_t item = (int64_t)blockIdx.x * (256 / LPH) + threadIdx.x / LPH; item < items; item += step) {
+    const uint32_t token = (uint32_t)(item >> A.groups);
+    const int g = (int)(item & ((1 << A.groups) - 1));
+    const int b = (int)(token / (uint32_t)A.len), i = (int)(token - (uint32_t)b * (uint32_t)A.len);
+    const bool live = i < live_tokens(A, b);
+    float c[E], s[E];
+    lane_angles<E>(A, l, w, A.positions ? A.positions[b * A.position_stride + i] : i, c, s);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const HeadRows& R = p == 0 ? A.q : A.k;
+      const int64_t* ys = p == 0 ? A.dqs : A.dks;
+      const T* const src = (const T*)R.src + b * R.ss[0] + i * R.ss[1];
+      const T* const dy = (const T*)(p == 0 ? A.dq_out : A.dk_out) + b * ys[0] + i * ys[1];
+      T* const dst = (T*)R.dst + b * R.ds[0] + i * R.ds[1];
+      for (int h = g; h < R.heads; h += 1 << A.groups) {
+        V rx[2], ry[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          rx[k] = ry[k] = V{};
+          if (live && l.has[k]) {
+            rx[k] = *(const V*)(src + h * R.ss[2] + l.at[k]);
+            ry[k] = *(const V*)(dy + h * ys[2] + l.at[k]);
+          }
+        }
+        float x[2][E], y[2][E];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          widen<T, E>(rx[k], x[k]);
+          widen<T, E>(ry[k], y[k]);
+        }
+        if (l.turns) turn<E>(y[0], y[1], c, s, A.interleaved);
+        float sum = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            sum = fmaf(x[k][e], x[k][e], sum);
+            dot = fmaf(y[k][e] * weight[p][k][e], x[k][e], dot);
+          }
+        const float r = inverse_rms<T>(A, group_sum<LPH>(sum));
+        const float m = group_sum<LPH>(dot) * A.inv_d * r * r;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            if (live) acc[p][k][e] = fmaf(y[k][e], x[k][e] * r, acc[p][k][e]);
+            x[k][e] = live ? r * fmaf(-m, x[k][e], y[k][e] * weight[p][k][e]) : 0.0f;
+          }
+          if (l.has[k]) *(V*)(dst + h * R.ds[2] + l.at[k]) = narrow<T, E>(x[k]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float x = acc[p][k][e];
+#pragma unroll
+        for (int z = LPH; z < 64; z <<= 1) x += __shfl_xor(x, z, 64);
+        if ((threadIdx.x & 63) < LPH && l.has[k]) sw[wave][p][l.at[k] + e] = x;
+      }
+  __syncthreads();
+  const int p = threadIdx.x >> 7, col = threadIdx.x & 127;
+  if (col < A.d)
+    A.part[((int64_t)blockIdx.x * 2 + p) * kMaxD + col] = (sw[0][p][col] + sw[1][p][col]) + (sw[2][p][col] + sw[3][p][col]);
+}
+
+// ---------------------------------------------------------------- launches
+// Elements of a chunk: as many as 16 bytes hold, and the layout and the pairs allow.
+template <class T, class F>
+void by_chunk(int e, int width, F&& f) {
+  constexpr int most = 16 / (int)sizeof(T);
+  auto go = [&](auto chunk, auto lanes) { f(chunk, lanes); };
+  using std::integral_constant;
+  if (e == most && width <= kMaxD / 2)
+    go(integral_constant<int, most>{}, integral_constant<int, 32 / most>{});
+  else if (e == most)
+    go(integral_constant<int, most>{}, integral_constant<int, 64 / most>{});
+  else if (e == 4 && most == 8)
+    go(integral_constant<int, 4>{}, integral_constant<int, 16>{});
+  else if (e == 2)
+    go(integral_constant<int, 2>{}, integral_constant<int, 32>{});
+  else
+    go(integral_constant<int, 1>{}, integral_constant<int, 64>{});
+}
+
+// Lane groups of a token (log2): few tokens spread over the chip, many share their
+// angles among heads.
+inline int32_t rotate_groups(int64_t tokens, int32_t heads, int32_t lanes) {
+  int32_t g = 0;
+  while ((1 << g) < 64 / lanes && (1 << g) < heads) ++g;
+  while ((1 << g) < heads && (tokens << g) * lanes < (int64_t)256 * 1024) ++g;
+  return g;
+}
+
+// Instantiated once per element type (rotate_*.hip). e: elements of a chunk.
+template <class T>
+void rotate(RotateArgs& A, int e, hipStream_t st) {
+  by_chunk<T>(e, A.d > A.dv ? A.d : A.dv, [&](auto chunk, auto lanes) {
+    constexpr int E = decltype(chunk)::value, L = decltype(lanes)::value;
+    const int64_t tokens = (int64_t)A.batch * A.steps;
+    A.groups = rotate_groups(tokens, A.heads, L);
+    const int64_t blocks = ceil_div((tokens << A.groups) * L, 256);
+    hipLaunchKernelGGL((k_rotate<T, E, L, 2>), grid1(blocks, 256), dim3(256), 0, st, A);
+    SK_LAUNCH_CHECK();
+  });
+}
+
+template <class T>
+void rotate_grad(RotateArgs& A, int e, int blocks, hipStream_t st) {
+  by_chunk<T>(e, A.d, [&](auto chunk, auto lanes) {
+    constexpr int E = decltype(chunk)::value, L = decltype(lanes)::value;
+    A.groups = rotate_groups((int64_t)A.batch * A.len, A.heads, L);
+    hipLaunchKernelGGL((k_rotate_grad<T, E, L>), grid1(blocks, 256), dim3(256), 0, st, A);
+    SK_LAUNCH_CHECK();
+  });
+}
+
+}  // namespace attn
+}  // namespace sk

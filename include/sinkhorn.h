@@ -664,6 +664,30 @@ int sinkhorn_cache_append(const sinkhorn_rotation* rot, const sinkhorn_pages* ca
                           const void* q_weight, const void* k_weight, void* q_out, void* k_cache,
                           void* v_cache, int32_t* lengths_out, void* stream);
 
+/* Attention of new tokens over the cache that they were appended to. Of entry b the
+ * n = query_lengths[b] (or len_q) rows of q are the last n of its lengths[b] keys: row
+ * i is at place p = lengths[b] - n + i and sees key j <= p; with recent > 0 only
+ * those of p - recent < j and of j < first (the window `recent` long ends with the
+ * row itself). out and lse as of sinkhorn_cross_attention, by the fields of `at` for
+ * q, out, scale, widths and lengths of queries (dv that of the cache; key fields,
+ * bias and other strides do not count and must be 0 or NULL where they are pointers).
+ *
+ * Hidden keys have no influence on a row, whatever they hold, and neither have keys
+ * at or behind lengths[b] or on pages outside [0, pages). A row without any key (p
+ * < 0, say) and rows at or behind query_lengths give out = 0 and lse = -infinity.
+ * Pages wholly outside the windows of all rows are not read and may be gone.
+ *
+ * Rows of the cache must be whole, aligned units of 16 bytes (d and dv multiples of
+ * 8, of 4 in fp32; SINKHORN_ERR_UNSUPPORTED otherwise); any strides else, any size
+ * of the cache. The table should be as wide as the sequences need: the keys are
+ * split over the chip for as many as it has places for. */
+int sinkhorn_paged_workspace(const sinkhorn_attention* at, const sinkhorn_pages* cache,
+                             int64_t first, int64_t recent, int64_t* bytes);
+int sinkhorn_paged_attention(const sinkhorn_attention* at, const sinkhorn_pages* cache,
+                             int64_t first, int64_t recent, const void* q, const void* k_cache,
+                             const void* v_cache, void* out, float* lse, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
 /* Measurement hook. `kinds` is a bit set of the kernels to time: every later
  * launch of a selected kernel carries two HIP events that its own dispatch
  * records at the kernel's start and end (hipExtLaunchKernelGGL), so the time

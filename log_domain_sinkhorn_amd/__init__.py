@@ -35,6 +35,7 @@ __all__ = [
     "rotate_heads",
     "rotate_heads_grad",
     "cache_append",
+    "paged_attention",
     "lib",
     "LIB_PATH",
     "OK",
@@ -279,6 +280,8 @@ _SIGS = {
     "sinkhorn_rotation_workspace": ([_p, _p], _i32),
     "sinkhorn_rotate_heads_grad": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
     "sinkhorn_cache_append": ([_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p], _i32),
+    "sinkhorn_paged_workspace": ([_p, _p, _i64, _i64, _p], _i32),
+    "sinkhorn_paged_attention": ([_p, _p, _i64, _i64, _p, _p, _p, _p, _p, _p, _i64, _p], _i32),
     "sinkhorn_profile_enable": ([_p, _i32], _i32),
     "sinkhorn_profile_read": ([_p, _p, _p, _p], _i32),
     "sinkhorn_probe_issue_rate": ([_i32, _i32, _p, _p, _p, _p], _i32),
@@ -973,6 +976,59 @@ def cache_append(k, v, k_cache, v_cache, page_table, cache_lengths, *, new_lengt
             v.data_ptr(), _strides3(v), _at(q_weight), _at(k_weight), _at(q_out), k_cache.data_ptr(),
             v_cache.data_ptr(), lengths_out.data_ptr())
     return lengths_out, q_out
+
+
+def paged_attention(q, k_cache, v_cache, page_table, key_lengths, *, scale=None, query_lengths=None, first=0,
+                    recent=None, out=None, lse=None):
+    """(out, lse): causal attention of new tokens over the paged cache that they were
+    appended to (``sinkhorn_paged_attention``).
+
+    q [B, Lq, Hq, d] holds the queries of the last n = query_lengths[b] (int32 [B], default
+    Lq) of the key_lengths[b] keys (int32 [B]) of sequence b; the cache is laid out as for
+    cache_append, query head h reads key head h // (Hq / Hkv). The row at place p sees
+    key j <= p, and with `recent` only its `recent` last keys (itself among them) and the
+    `first` first of the sequence. scale defaults to d ** -0.5. out [B, Lq, Hq, dv] has q's
+    type, lse [B, Hq, Lq] is float32; rows without keys, and rows >= query_lengths[b], give
+    0 and -inf. Keys on pages outside the cache take no part. d and dv are multiples of 16
+    bytes, as are the cache's strides."""
+    _head_tensor(q, "q")
+    B, lq, hq, d = q.shape
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, page_size, heads, width]")
+    hkv = k_cache.shape[2]
+    if hkv < 1 or hq < 1 or hq % hkv:
+        raise ValueError(f"{hq} query heads are no multiple of {hkv} key heads")
+    c = _pages(q.dtype, B, hkv, d, k_cache, v_cache, page_table, key_lengths, "key_lengths")
+    shape = (B, lq, hq, c.dv)
+    a = _AttentionC(_ATTN_DTYPES[q.dtype], B, hq, hkv, d, c.dv, lq, 0,
+                    1.0 / math.sqrt(max(d, 1)) if scale is None else float(scale), _strides3(q))
+    if query_lengths is not None:
+        a.query_lengths = _plain(query_lengths, "query_lengths", torch.int32, (B,)).data_ptr()
+    if recent is None:
+        recent = 0
+        if first:
+            raise ValueError("first needs recent")
+    elif recent < 1:
+        raise ValueError("recent must be >= 1")
+    # as large as the C side takes them: a longer one means the same
+    first, recent = (max(-1, min(int(x), (1 << 63) - 1)) for x in (first, recent))
+    if out is not None:
+        _written(_head_tensor(out, "out", q.dtype, shape), "out")
+    if lse is not None:
+        _plain(lse, "lse", torch.float32, (B, hq, lq))
+    index = _same_device(q, (k_cache, v_cache, page_table, key_lengths, query_lengths, out, lse))
+    device = q.device
+    out = torch.empty(shape, dtype=q.dtype, device=device) if out is None else out
+    lse = torch.empty((B, hq, lq), dtype=torch.float32, device=device) if lse is None else lse
+    a.out_stride = _strides3(out)
+    size = _i64()
+    _check(lib().sinkhorn_paged_workspace(ctypes.byref(a), ctypes.byref(c), first, recent, ctypes.byref(size)),
+           "paged_workspace")
+    n = size.value
+    ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    _launch(index, "paged_attention", lib().sinkhorn_paged_attention, ctypes.byref(a), ctypes.byref(c), first, recent,
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), _at(ws), n)
+    return out, lse
 
 
 class Problem:

@@ -1,0 +1,400 @@
+// Attention of new tokens over a paged cache: row i of an entry's n new tokens is at
+// place p = keys - n + i of its sequence and sees key j <= p, and of these, with
+// `recent`, only j > p - recent or j < first.
+//
+// The tiles, the softmax and the split of the keys are those of k_attend (attend.h),
+// with three differences.
+//
+// Pages. A tile is loaded by instructions of 2, 4 or 8 rows, which lie in one page
+// because page sizes are multiples of 8: the page's address goes into the scalar base
+// of the load, so a lane's offsets are the same in every tile and a cache may be of
+// any size. A wave holds 256 page numbers of the sequence, four a lane, and takes
+// them from there by lane reads; loading the next 256 waits for the loads in
+// flight, once in 2048 keys or more.
+//
+// Masks are of the pair, but only in tiles at the rows' own places and at the
+// window's edge; tiles that no row of the workgroup sees are not loaded, and waves
+// leave out those that none of their rows sees. A hidden key's score becomes
+// -infinity, its weight 0; a value there that is no number must not reach the row
+// through 0 x infinity, so such a tile is first looked through for any (2
+// operations per 4 bytes), and if there is one, its finite part is multiplied as
+// usual, while infinities are counted by products with 0 and 1 in place of values
+// and weights and added to the rows that see them.
+//
+// Order. The rows at the end of a chunk see the most keys and come first.
+#pragma once
+
+#include "attend.h"
+#include "pages.h"
+
+namespace sk {
+namespace attn {
+
+struct PagedArgs {
+  AttendArgs A;  // S.k, S.v: the cache; S.ks, S.vs: page, slot, head; S.klen: P.lengths
+  Paging P;
+  int32_t first, recent;  // recent 0: all keys
+  bool qvec;              // q may be read 16 bytes a lane
+};
+
+// The tiles of KT keys that a workgroup runs over: `ns` from the sequence's start on,
+// then those from tile t_lo on; of all these, `count` from the n0-th on. In a ring
+// of D buffers as KeyTiles.
+template <class T, int DP, int KT, int NT, int D, bool ONCE>
+struct PageTiles {
+  using Ld = Loader<T, DP, KT, NT, ONCE>;
+  using TL = Tile<T, DP>;
+  static constexpr int kTileBytes = KT * TL::RB;
+  static constexpr int kOps = 2 * Ld::N;
+  static constexpr int kHeld = 4;  // page numbers of a lane
+  static_assert(D == 2 || Ld::TOTAL % Ld::NW == 0, "counted loads: the same of every wave");
+  static_assert(8 % Ld::RPI == 0, "the rows of an instruction lie in one page");
+  struct Shared {
+    __attribute__((aligned(16))) char tiles[D][2][kTileBytes];
+    __attribute__((aligned(16))) float term[D][KT];  // of a tile with bad pages: 0 or -inf by key
+  };
+  Shared& sm;
+  const Paging& P;
+  const char* k;
+  const char* v;
+  int64_t kpage, vpage;  // bytes
+  uint32_t kslot, vslot;
+  const int32_t* table;
+  uint32_t koff[Ld::N], voff[Ld::N];  // byte offset of this lane's chunk within an instruction's rows
+  int32_t id[kHeld];
+  uint32_t held;  // first page held
+  int nkeys, n0, count, ns, t_lo, wave, lane;
+  uint32_t npages;  // of the sequence
+  uint32_t bad;     // bit n % D: tile n has pages outside the cache
+  bool bad_held;
+
+  __device__ __forceinline__ PageTiles(Shared& sm_, const PagedArgs& A, int b, int hk, int nkeys_, int ns_, int t_lo_, int n0_,
+                                       int count_, int wave_, int lane_)
+      : sm(sm_), P(A.P), k((const char*)A.A.S.k + (int64_t)hk * A.A.S.ks[2] * sizeof(T)),
+        v((const char*)A.A.S.v + (int64_t)hk * A.A.S.vs[2] * sizeof(T)), kpage(A.A.S.ks[0] * sizeof(T)),
+        vpage(A.A.S.vs[0] * sizeof(T)), kslot((uint32_t)(A.A.S.ks[1] * sizeof(T))), vslot((uint32_t)(A.A.S.vs[1] * sizeof(T))),
+        table(A.P.table + b * A.P.stride), held(0), nkeys(nkeys_), n0(n0_), count(count_), ns(ns_), t_lo(t_lo_), wave(wave_),
+        lane(lane_), npages(nkeys_ > 0 ? page_of(A.P, (uint32_t)(nkeys_ - 1)) + 1 : 0), bad(0), bad_held(false) {
+#pragma unroll
+    for (int n = 0; n < Ld::N; ++n) {
+      const int c = (lane % TL::CPR) ^ TL::swz(Ld::row(n, wave, lane)), r = lane / TL::CPR;
+      koff[n] = c * TL::EPC < A.A.S.d ? r * kslot + 16 * c : kOutside;
+      voff[n] = c * TL::EPC < A.A.S.dv ? r * vslot + 16 * c : kOutside;
+    }
+#pragma unroll
+    for (int n = 0; n < kHeld; ++n) id[n] = -1;
+    if (count > 0) hold(page_of(P, (uint32_t)key(0)));
+  }
+  // first key of tile n
+  __device__ __forceinline__ int key(int n) const {
+    const int x = n0 + n;
+    return (x < ns ? x : x - ns + t_lo) * KT;
+  }
+  __device__ __forceinline__ void hold(uint32_t page) {
+    held = page;
+    bool out = false;
+#pragma unroll
+    for (int n = 0; n < kHeld; ++n) {
+      const uint32_t p = page + 64 * n + lane;
+      id[n] = p < npages ? table[p] : 0;
+    }
+#pragma unroll
+    for (int n = 0; n < kHeld; ++n) out = out || (uint32_t)id[n] >= (uint32_t)P.pages;
+    bad_held = __any(out);
+    loads_done();  // known to the compiler: it would otherwise wait for all loads at every use
+  }
+  __device__ __forceinline__ int32_t number(uint32_t page) const {
+    const uint32_t x = page - held, at = x & 63;
+    const int32_t a = __builtin_amdgcn_readlane(id[0], at), b = __builtin_amdgcn_readlane(id[1], at);
+    const int32_t c = __builtin_amdgcn_readlane(id[2], at), d = __builtin_amdgcn_readlane(id[3], at);
+    return x < 128 ? (x < 64 ? a : b) : (x < 192 ? c : d);
+  }
+  __device__ __forceinline__ void start(int n) {
+    if (n >= count) return;
+    const int buf = n % D;
+    const int first = __builtin_amdgcn_readfirstlane(key(n));
+    const int left = nkeys - first;  // keys from the tile's first on, at least one
+    {
+      const uint32_t p0 = page_of(P, (uint32_t)first), p1 = page_of(P, (uint32_t)(first + (left < KT ? left : KT) - 1));
+      if (p0 < held || p1 >= held + 64 * kHeld) hold(p0);
+    }
+    bad = (bad & ~(1u << buf)) | (bad_held ? 1u << buf : 0u);
+    const uint32_t klds = lds_offset(sm.tiles[buf][0]) + wave * 1024, vlds = lds_offset(sm.tiles[buf][1]) + wave * 1024;
+#pragma unroll
+    for (int i = 0; i < Ld::N; ++i)
+      if (Ld::has(i, wave)) {
+        const int r0 = (i * Ld::NW + wave) * Ld::RPI;
+        const uint32_t j = (uint32_t)(first + (r0 < left ? r0 : 0));  // rows behind the keys are not read
+        const uint32_t page = page_of(P, j), slot = j - page * (uint32_t)P.size;
+        const int32_t at = number(page);
+        const bool ok = r0 < left && (uint32_t)at < (uint32_t)P.pages;
+        const int64_t where = ok ? at : 0;
+        const bool live = ok && r0 + lane / TL::CPR < left;
+        dma_load<16, ONCE>(dma_rsrc(k + where * kpage + (uint64_t)slot * kslot), klds + i * Ld::NW * 1024, live ? koff[i] : kOutside);
+        dma_load<16, ONCE>(dma_rsrc(v + where * vpage + (uint64_t)slot * vslot), vlds + i * Ld::NW * 1024, live ? voff[i] : kOutside);
+        if (bad_held && lane < Ld::RPI) sm.term[buf][r0 + lane] = ok ? 0.0f : -kInf;
+      }
+  }
+  __device__ __forceinline__ void begin() {
+#pragma unroll
+    for (int n = 0; n < D - 1; ++n) start(n);
+  }
+  // Makes tile n readable and starts the one D - 1 further on.
+  __device__ __forceinline__ void next(int n) {
+    const int ahead = count - 1 - n;
+    if constexpr (D == 2)
+      dma_wait<0>();
+    else if (ahead >= D - 2)
+      dma_wait<(D - 2) * kOps>();
+    else
+      dma_wait<0>();
+    __syncthreads();
+    start(n + D - 1);
+  }
+  __device__ __forceinline__ const char* ktile(int n) const { return sm.tiles[n % D][0]; }
+  __device__ __forceinline__ const char* vtile(int n) const { return sm.tiles[n % D][1]; }
+  // of a tile with pages outside the cache: 0 or -inf for each key; else null
+  __device__ __forceinline__ const float* term(int n) const { return (bad >> (n % D)) & 1 ? sm.term[n % D] : nullptr; }
+};
+
+// Does any value of rows kb0 .. kb0 + ROWS - 1 of the tile fail to be a number? By all lanes of a wave.
+template <class T, int DP, int ROWS>
+__device__ __forceinline__ bool no_numbers(const char* tv, int kb0, int lane) {
+  using TL = Tile<T, DP>;
+  const char* p = tv + kb0 * TL::RB + 16 * lane;
+  if constexpr (sizeof(T) == 4) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < ROWS * TL::RB / 1024; ++i) {
+      const u32x4 x = *(const u32x4*)(p + 1024 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max(top, x[e] & 0x7fffffffu);
+    }
+    return __any(top >= 0x7f800000u);
+  } else {
+    typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
+    constexpr unsigned short inf = std::is_same<T, __bf16>::value ? 0x7f80 : 0x7c00;
+    u16x8 top = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < ROWS * TL::RB / 1024; ++i) {
+      const u16x8 x = *(const u16x8*)(p + 1024 * i) & (unsigned short)0x7fff;
+      top = __builtin_elementwise_max(top, x);
+    }
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) any = any || top[e] >= inf;
+    return __any(any);
+  }
+}
+
+// add_values where values may be no numbers and some keys are hidden: seen(i) tells
+// whether the lane's row sees key kb0 + i + 4 h (h: the lane's half).
+template <class T, int DP, bool MANY, int NB, int NDB, class F>
+__device__ __forceinline__ void add_seen_values(const char* tv, int kb0, int lane, const f32x16 (&sc)[NB], f32x16 (&o)[NDB],
+                                                F&& seen) {
+  using TL = Tile<T, DP>;
+  using V8 = typename Vec<T>::V8;
+#pragma unroll
+  for (int x = 0; x < NDB; ++x) {
+    f32x16 up = zero16(), down = zero16();  // how many +inf, -inf (a NaN counts as both) the row sees
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        V8 f = TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane), pos, neg, one;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float y = (float)f[e];
+          pos[e] = (T)(y < kInf ? 0.0f : 1.0f);
+          neg[e] = (T)(y > -kInf ? 0.0f : 1.0f);
+          f[e] = y < kInf && y > -kInf ? f[e] : (T)0.0f;
+          one[e] = (T)(seen(32 * n + 16 * s + 8 * (e >> 2) + (e & 3)) ? 1.0f : 0.0f);
+        }
+        const V8 p = pack<T>(sc[n], s);
+        o[x] = mma(f, p, o[x]);
+        if constexpr (!MANY && sizeof(T) == 2) o[x] = mma(f, pack_rest<T>(sc[n], s, p), o[x]);
+        up = mma(pos, one, up);
+        down = mma(neg, one, down);
+      }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      if (up[e] > 0.0f) o[x][e] += kInf;
+      if (down[e] > 0.0f) o[x][e] -= kInf;
+    }
+  }
+}
+
+template <class T, int W, int WQ, int WK, int NB, int D, int OCC>
+__global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G) {
+  constexpr int DP = row_width(W);
+  using TL = Tile<T, DP>;
+  using V8 = typename Vec<T>::V8;
+  constexpr int NT = 64 * WQ * WK;
+  constexpr int KT = 32 * NB * WK;  // keys per tile
+  constexpr int KW = 32 * NB;       // of them a wave's own
+  constexpr int NS = W / 16, NDB = W / 32;
+  constexpr bool kExact = sizeof(T) == 4;  // scores in natural units, as in k_attend
+  constexpr bool AHEAD = WK == 1 && TL::RB == 128;
+  static_assert(WK == 1 || (WQ == 1 && NB == 1), "few rows: one tile of 32, a wave's own 32 keys");
+  using KeyT = PageTiles<T, DP, KT, NT, D, (WK > 1)>;
+  constexpr int kJoinBytes = WK > 1 ? WK * 32 * W * 4 : 0;
+  union Memory {
+    typename KeyT::Shared keys;
+    float join[kJoinBytes / 4 + 1];
+  };
+  __shared__ Memory sm;
+  __shared__ f32x2 sml[WK > 1 ? WK * 32 : 1];
+
+  const AttendArgs& A = G.A;
+  const Shape& S = A.S;
+  const int64_t item = xcd_item((int64_t)S.batch * S.hkv, A.tiles * A.nsplit);
+  if (item < 0) return;
+  const int64_t place = item / (A.tiles * A.nsplit);
+  const int64_t rest = item - place * (A.tiles * A.nsplit);
+  const int64_t tile = A.tiles - 1 - rest / A.nsplit;  // the last rows see the most keys
+  const int split = (int)(rest % A.nsplit);
+  const int pos = (int)(place / S.hkv), hk = (int)(place - (int64_t)pos * S.hkv);
+  const int b = batch_entry(S, pos);
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5, r32 = lane & 31;
+  const int wq = wave % WQ, wk = wave / WQ;
+
+  const int nkeys = __builtin_amdgcn_readfirstlane(paged_keys(G.P, b));
+  const int64_t nrows = live_rows(S, b);
+  const int64_t row0 = tile * (32 * WQ);
+  const int64_t row = row0 + 32 * wq + r32;
+  const bool live_row = row < nrows;
+  const int64_t qi = row / S.group;
+  const int qh = hk * S.group + (int)(row - qi * S.group);
+
+  // keys that rows r0 .. r1 (live ones) may see end at `end`, and their window starts
+  // at the earliest at `from`
+  const int base = nkeys - (int)(nrows / S.group);  // place of the entry's first row
+  auto end_of = [&](int64_t r) {
+    const int x = base + (int)(r / S.group) + 1;
+    return x < 0 ? 0 : x;
+  };
+  auto from_of = [&](int end) {
+    const int x = end - G.recent;
+    return G.recent == 0 || x < 0 ? 0 : x;
+  };
+  int ns = 0, t_lo = 0, total = 0;
+  if (row0 < nrows) {
+    const int64_t last = row0 + 32 * WQ < nrows ? row0 + 32 * WQ - 1 : nrows - 1;
+    const int end = end_of(last), t_end = (end - 1 + KT) / KT;
+    t_lo = from_of(end_of(row0)) / KT;
+    const int f = G.first < end ? G.first : end, n = f > 0 ? (f - 1) / KT + 1 : 0;
+    ns = n < t_lo ? n : t_lo;
+    total = ns + t_end - t_lo;
+  }
+  const int per = (total + A.nsplit - 1) / A.nsplit;
+  const int n0 = split * per, count = total - n0 < per ? total - n0 : per;
+
+  KeyT keys(sm.keys, G, b, hk, nkeys, ns, t_lo, n0, count > 0 ? count : 0, wave, lane);
+  keys.begin();
+
+  V8 qf[NS];
+  {
+    const T* qrow = (const T*)S.q + b * S.qs[0] + qi * S.qs[1] + qh * S.qs[2];
+    const bool need = live_row && keys.count > 0;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      if (G.qvec) {
+        qf[s] = global_frag<T>(qrow, need, s, h, S.d);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) qf[s][e] = need && 16 * s + 8 * h + e < S.d ? qrow[16 * s + 8 * h + e] : (T)0.0f;
+      }
+    }
+  }
+  loads_done();
+  f32x16 o[NDB];
+#pragma unroll
+  for (int n = 0; n < NDB; ++n) o[n] = zero16();
+  float m = -kInf, l = 0.0f;
+
+  // this lane's row sees keys below `end`, and of these from `from` on or below G.first;
+  // over the wave's live rows these bounds run from e_lo to e_hi and f_lo to f_hi
+  const int end = end_of(row), from = from_of(end);
+  const int64_t w0 = row0 + 32 * wq, w1 = w0 + 31 < nrows ? w0 + 31 : nrows - 1;
+  const int e_lo = end_of(w0), e_hi = w0 < nrows ? end_of(w1) : 0, f_lo = from_of(e_lo), f_hi = from_of(e_hi);
+
+  if constexpr (WK == 1 && OCC == 2) one_ahead();
+  for (int it = 0; it < keys.count; ++it) {
+    keys.next(it);
+    const int kb0 = KW * wk;
+    const int j0 = __builtin_amdgcn_readfirstlane(keys.key(it) + kb0);
+    if (j0 >= e_hi || (j0 + KW <= f_lo && j0 >= G.first)) continue;  // no row of this wave sees any
+    const char* const tk = keys.ktile(it);
+    const char* const tv = keys.vtile(it);
+    f32x16 sc[NB];
+    score_tile<T, DP, AHEAD, NB, NS>(tk, kb0, lane, qf, S.d, sc);
+    const float f = kExact ? (float)kLog2e : S.c;  // to log2 units
+    if constexpr (kExact) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sc[n][e] = fmaf(sc[n][e], S.scale, sc[n][e] * S.scale_lo);
+    }
+    const float* const term = keys.term(it);
+    const bool all = j0 + KW <= e_lo && (j0 >= f_hi || j0 + KW <= G.first);  // every row sees every key
+    // does the row see key i + 4 h of this wave's own? Without branches: a select each.
+    const int f0 = from - j0 - 4 * h, g0 = (G.first < end ? G.first : end) - j0 - 4 * h;
+    const uint32_t span = (uint32_t)(end - from);
+    auto seen = [&](int i) { return ((uint32_t)(i - f0) < span) | (i < g0); };
+    if (!all) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sc[n][e] = seen(32 * n + 8 * (e >> 2) + (e & 3)) ? sc[n][e] : -kInf;
+    }
+    if (term) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 ct = *(const f32x4*)&term[kb0 + 32 * n + 8 * g + 4 * h];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[n][4 * g + e] = ct[e] == 0.0f ? sc[n][4 * g + e] : -kInf;
+        }
+    }
+    soften<NB, NDB>(sc, f, m, l, o);
+    if (!all && no_numbers<T, DP, KW>(tv, kb0, lane))
+      add_seen_values<T, DP, WK == 1, NB, NDB>(tv, kb0, lane, sc, o, seen);
+    else
+      add_values<T, DP, WK == 1, NB, NDB>(tv, kb0, lane, sc, o);
+  }
+  l = half_sum(l);
+  if (!live_row) {
+    m = -kInf;
+    l = 0.0f;
+  }
+  finish_rows<T, W, WQ, WK>(A, sm.join, sml, o, m, l, live_row, split, b, hk, row0);
+}
+
+// many: 128 rows per workgroup, else all rows in one tile of 32; waves and tiles as
+// for k_attend
+template <class T, int W>
+void attend_paged_launch(const PagedArgs& G, bool many, hipStream_t st) {
+  const int64_t blocks = xcd_blocks((int64_t)G.A.S.batch * G.A.S.hkv, G.A.tiles * G.A.nsplit);
+  constexpr int RB = row_width(W) * (int)sizeof(T);
+  constexpr int OCC = RB == 128 ? 3 : (RB == 256 ? 2 : 1);
+  if (many)
+    hipLaunchKernelGGL((k_attend_paged<T, W, 4, 1, 2, 2, OCC>), grid1(blocks, 256), dim3(256), 0, st, G);
+  else
+    hipLaunchKernelGGL((k_attend_paged<T, W, 1, few_waves(RB), 1, few_depth(RB), RB == 128 ? 2 : 1>),
+                       grid1(blocks, 64 * few_waves(RB)), dim3(64 * few_waves(RB)), 0, st, G);
+  SK_LAUNCH_CHECK();
+}
+
+// Instantiated once per element type (attend_paged_*.hip).
+template <class T>
+void attend_paged(const PagedArgs& G, bool many, hipStream_t st) {
+  const AttendArgs& A = G.A;
+  by_width(A.S.d, A.S.dv, [&](auto w) { attend_paged_launch<T, decltype(w)::value>(G, many, st); });
+  if (A.opart) join_splits<T>(A, nullptr, st);
+}
+
+}  // namespace attn
+}  // namespace sk

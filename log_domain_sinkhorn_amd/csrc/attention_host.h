@@ -4,7 +4,7 @@
 
 #include <algorithm>
 
-#include "internal.h"
+#include "attention.h"
 
 namespace sk {
 namespace attn {
@@ -55,6 +55,58 @@ inline int32_t splits(int64_t blocks, int64_t steps, int64_t slots, double join,
     if (n > best) best = (int32_t)n;
   }
   return best;
+}
+
+inline int64_t elem_size(const sinkhorn_attention* a) { return a->dtype == SINKHORN_F32 ? 4 : 2; }
+
+inline void check(const sinkhorn_attention* a) {
+  require(a != nullptr, "null attention description");
+  require(a->dtype == SINKHORN_F32 || a->dtype == SINKHORN_F16 || a->dtype == SINKHORN_BF16, "unknown dtype");
+  require(a->batch >= 0 && a->len_q >= 0 && a->len_k >= 0, "negative size");
+  require(a->heads_q >= 1 && a->heads_kv >= 1 && a->heads_q % a->heads_kv == 0,
+          "heads_q must be a multiple of heads_kv");
+  if (a->heads_q > 8192) fail(SINKHORN_ERR_UNSUPPORTED, "more than 8192 heads");
+  require(a->d >= 1 && a->dv >= 1, "head widths must be >= 1");
+  if (a->d > kMaxD || a->dv > kMaxD) fail(SINKHORN_ERR_UNSUPPORTED, "head widths above 128");
+  require(a->len_q * (a->heads_q / a->heads_kv) < (int64_t(1) << 31) && a->len_q < (int64_t(1) << 31) &&
+              a->len_k < (int64_t(1) << 31),
+          "lengths must be below 2^31");
+  require(std::isfinite(a->scale) && a->scale > 0.0 && std::isfinite((float)(a->scale * kLog2e)) &&
+              (float)a->scale > 0.0f,
+          "scale must be finite and > 0");
+  for (int i = 0; i < 3; ++i)
+    require(a->q_stride[i] >= 0 && a->k_stride[i] >= 0 && a->v_stride[i] >= 0 && a->out_stride[i] >= 0 &&
+                a->dout_stride[i] >= 0 && a->dq_stride[i] >= 0 && a->dk_stride[i] >= 0 && a->dv_stride[i] >= 0,
+            "negative stride");
+  require(a->bias_stride[0] >= 0 && a->bias_stride[1] >= 0, "negative stride");
+}
+
+inline Shape make_shape(const sinkhorn_attention* a) {
+  Shape S{};
+  S.batch = a->batch;
+  S.hq = a->heads_q;
+  S.hkv = a->heads_kv;
+  S.group = a->heads_q / a->heads_kv;
+  S.d = a->d;
+  S.dv = a->dv;
+  S.lq = a->len_q;
+  S.lk = a->len_k;
+  S.rows = a->len_q * S.group;
+  S.group_mul = S.group > 1 ? (uint32_t)(((uint64_t(1) << 32) + S.group - 1) / S.group) : 0;
+  for (int i = 0; i < 3; ++i) {
+    S.qs[i] = a->q_stride[i];
+    S.ks[i] = a->k_stride[i];
+    S.vs[i] = a->v_stride[i];
+  }
+  S.bias = a->key_bias;
+  S.bs[0] = a->bias_stride[0];
+  S.bs[1] = a->bias_stride[1];
+  S.qlen = a->query_lengths;
+  S.klen = a->key_lengths;
+  S.scale = (float)a->scale;
+  S.scale_lo = (float)(a->scale - (double)S.scale);
+  S.c = (float)(a->scale * kLog2e);
+  return S;
 }
 
 // Workspace layout: consecutive pieces of 256-byte multiples.

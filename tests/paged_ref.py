@@ -141,3 +141,61 @@ def table_of(lens, size, pages, gen, extra=0):
         t[b, :n] = torch.tensor(order[at:at + n], dtype=torch.int32)
         at += n
     return t
+
+
+class PagedRef:
+    """paged_attention in 64 bits, with tolerances as attention_ref.Ref derives them (two_parts: the
+    weights are held in two parts of the element type, which leaves 2^-16 (bf16) or 2^-22 of them)."""
+
+    def __init__(self, q, k_cache, v_cache, page_table, key_lengths, scale=None, query_lengths=None, first=0, recent=None):
+        dtype = q.dtype
+        u, f16 = half_step(dtype), dtype == torch.float16
+        B, m, Hq, d = q.shape
+        pages, size, H, dv = v_cache.shape
+        G = Hq // H
+        scale = d ** -0.5 if scale is None else scale
+        cap = page_table.shape[1] * size
+        first, recent = min(first, cap), None if recent is None else min(recent, cap + m)
+        self.out = torch.zeros(B, m, Hq, dv, dtype=torch.float64)
+        self.out_tol = torch.zeros(B, m, Hq, dv, dtype=torch.float64)
+        self.lse = torch.full((B, Hq, m), -float("inf"), dtype=torch.float64)
+        self.lse_tol = torch.zeros(B, Hq, m, dtype=torch.float64)
+        few = m * G <= 32 and dtype != torch.float32
+        weight_step = {torch.bfloat16: 2.0 ** -16, torch.float16: 2.0 ** -22, torch.float32: 0.0}[dtype] if few else u
+        for b in range(B):
+            n = min(max(int(key_lengths[b]), 0), cap)
+            rows = m if query_lengths is None else min(max(int(query_lengths[b]), 0), m)
+            ids = page_table[b].cpu().long()
+            ok = (ids >= 0) & (ids < pages)
+            ids = torch.where(ok, ids, torch.zeros_like(ids))
+            if pages == 0 or n == 0:
+                continue
+            need = (n + size - 1) // size
+            take = lambda c: c[ids[:need].to(c.device)].flatten(0, 1)[:n].cpu().double()  # noqa: E731
+            K, V = take(k_cache), take(v_cache)  # [n, H, .]
+            live = ok[:need].repeat_interleave(size)[:n]
+            j = torch.arange(n)
+            for i in range(rows):
+                p = n - rows + i
+                see = live & (j <= p)
+                if recent is not None:
+                    see = see & ((j > p - recent) | (j < first))
+                at = torch.nonzero(see)[:, 0]
+                if not len(at):
+                    continue
+                for h in range(Hq):
+                    x = q[b, i, h].cpu().double()
+                    k, v = K[at, h // G], V[at, h // G]
+                    s = (k @ x) * scale
+                    z = torch.logsumexp(s, 0)
+                    w = torch.exp(s - z)
+                    mag = (k.abs() @ x.abs()) * scale
+                    dw = E * ((d + 4) * mag.max() + 16)
+                    rel = dw + E * (len(at) + 64)
+                    y = w @ v
+                    self.lse[b, h, i] = z
+                    self.lse_tol[b, h, i] = rel + 4 * E * z.abs() + 4 * E
+                    self.out[b, i, h] = y
+                    W = w @ v.abs()
+                    small = 2.0 ** -25 * v.abs().sum(0) if f16 else 0.0
+                    self.out_tol[b, i, h] = u * y.abs() * 1.01 + (weight_step * 1.01 + 2 * rel) * W + small + tiny(dtype) * 4

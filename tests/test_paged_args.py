@@ -212,3 +212,81 @@ def test_append_refusals():
         assert _append(_desc(), _pages(), **kw) == sk.ERR_INVALID_ARG, kw
         assert b"overlaps" in L.sinkhorn_last_error(), kw
     assert _append(_desc(batch=0), _pages()) == sk.OK
+
+
+def _att(**kw):
+    a = dict(q=torch.zeros(2, 3, 4, 8, dtype=BF), k_cache=torch.zeros(4, 8, 2, 8, dtype=BF), v_cache=torch.zeros(4, 8, 2, 16, dtype=BF),
+             page_table=torch.zeros(2, 2, dtype=I32), key_lengths=torch.zeros(2, dtype=I32))
+    a.update(kw)
+    return a
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q=torch.zeros(2, 3, 4, 8)), dict(q=[1]), dict(k_cache=torch.zeros(4, 8, 2, 8)), dict(v_cache=None), dict(page_table=torch.zeros(2, 2)),
+    dict(key_lengths=torch.zeros(2)), dict(query_lengths=torch.zeros(2, dtype=torch.int64)), dict(out=torch.zeros(2, 3, 4, 16)),
+    dict(lse=torch.zeros(2, 4, 3, dtype=torch.float64)),
+])
+def test_paged_attention_types(bad):
+    with pytest.raises(TypeError):
+        sk.paged_attention(**_att(**bad))
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q=torch.zeros(2, 3, 8, dtype=BF)), dict(q=torch.zeros(2, 3, 3, 8, dtype=BF)), dict(q=torch.zeros(2, 3, 4, 16, dtype=BF)),
+    dict(k_cache=torch.zeros(4, 8, 16, dtype=BF)), dict(k_cache=torch.zeros(4, 8, 0, 8, dtype=BF)),
+    dict(v_cache=torch.zeros(4, 8, 1, 16, dtype=BF)), dict(page_table=torch.zeros(1, 2, dtype=I32)),
+    dict(key_lengths=torch.zeros(1, dtype=I32)), dict(query_lengths=torch.zeros(3, dtype=I32)), dict(recent=0), dict(recent=-1),
+    dict(first=2), dict(out=torch.zeros(2, 3, 4, 8, dtype=BF)), dict(out=torch.zeros(1, 3, 4, 16, dtype=BF).expand(2, 3, 4, 16)),
+    dict(lse=torch.zeros(2, 3, 4)), dict(q=torch.zeros(2, 3, 4, 8, dtype=BF, requires_grad=True)),
+    dict(k_cache=torch.zeros(4, 8, 2, 8, dtype=BF, requires_grad=True)), dict(),
+])
+def test_paged_attention_shapes_and_places(bad):
+    with pytest.raises(ValueError):
+        sk.paged_attention(**_att(**bad))
+
+
+def _adesc(**kw):
+    a = sk._AttentionC(dtype=2, batch=2, heads_q=4, heads_kv=2, d=64, dv=64, len_q=3, scale=0.125)
+    for n in ("q", "out"):
+        setattr(a, n + "_stride", sk._i64x3(4096, 512, 64))
+    for n, x in kw.items():
+        setattr(a, n, x)
+    return a
+
+
+def _attend(a, c, first=0, recent=0, q=AT[0], k=AT[1], v=AT[2], out=AT[3], lse=AT[4], ws=AT[5], n=1 << 30):
+    return sk.lib().sinkhorn_paged_attention(ctypes.byref(a) if a else None, ctypes.byref(c) if c else None, first, recent, q, k, v, out,
+                                             lse, ws, n, None)
+
+
+def test_paged_attention_refusals():
+    L = sk.lib()
+    assert _attend(None, _pages()) == sk.ERR_INVALID_ARG and _attend(_adesc(), None) == sk.ERR_INVALID_ARG
+    for kw, word in ((dict(dtype=5), b"dtype"), (dict(batch=-1), b"negative"), (dict(heads_kv=3), b"multiple"), (dict(d=0), b"width"),
+                     (dict(scale=0.0), b"scale"), (dict(dv=32), b"dv"), (dict(len_q=1 << 30), b"2^31"), (dict(key_bias=AT[9].value), b"key_bias"),
+                     (dict(key_lengths=AT[9].value), b"key_lengths")):
+        assert _attend(_adesc(**kw), _pages()) == sk.ERR_INVALID_ARG, kw
+        assert word in L.sinkhorn_last_error(), kw
+    for kw in (dict(page_size=20), dict(table_len=-1), dict(page_table=None), dict(lengths=None), dict(v_stride=sk._i64x3(-1, 1, 1))):
+        assert _attend(_adesc(), _pages(**kw)) == sk.ERR_INVALID_ARG, kw
+    for kw in (dict(first=-1), dict(recent=-1), dict(first=3), dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(lse=None)):
+        assert _attend(_adesc(), _pages(), **kw) == sk.ERR_INVALID_ARG, kw
+    # rows that are not whole, aligned units of 16 bytes, and slots too far apart
+    for at, c in ((_adesc(d=60), _pages()), (_adesc(dv=60), _pages(dv=60)), (_adesc(), _pages(k_stride=sk._i64x3(8192, 516, 64))),
+                  (_adesc(), _pages(v_stride=sk._i64x3(8192, 512, 68))), (_adesc(d=136), _pages()), (_adesc(), _pages(v_stride=sk._i64x3(0, 1 << 27, 64)))):
+        assert _attend(at, c) == sk.ERR_UNSUPPORTED
+    assert _attend(_adesc(), _pages(), k=ctypes.c_void_p(AT[1].value + 8)) == sk.ERR_UNSUPPORTED
+    for kw in (dict(out=AT[1]), dict(out=AT[0]), dict(lse=AT[3]), dict(lse=AT[11]), dict(out=AT[10])):
+        assert _attend(_adesc(), _pages(), **kw) == sk.ERR_INVALID_ARG, kw
+        assert b"overlaps" in L.sinkhorn_last_error(), kw
+    # a long table is split: it takes a workspace
+    c, n = _pages(table_len=4096, table_stride=4096), ctypes.c_int64()
+    assert L.sinkhorn_paged_workspace(ctypes.byref(_adesc()), ctypes.byref(c), 0, 0, ctypes.byref(n)) == sk.OK and n.value > 0
+    whole = n.value
+    assert L.sinkhorn_paged_workspace(ctypes.byref(_adesc()), ctypes.byref(c), 4, 100, ctypes.byref(n)) == sk.OK and n.value < whole
+    assert L.sinkhorn_paged_workspace(ctypes.byref(_adesc()), ctypes.byref(c), 0, 0, None) == sk.ERR_INVALID_ARG
+    for kw in (dict(ws=None), dict(n=whole - 1), dict(ws=ctypes.c_void_p(AT[5].value + 8))):
+        assert _attend(_adesc(), c, **kw) == sk.ERR_INVALID_ARG and b"workspace" in L.sinkhorn_last_error()
+    assert _attend(_adesc(), c, ws=AT[1]) == sk.ERR_INVALID_ARG and b"overlaps" in L.sinkhorn_last_error()
+    assert _attend(_adesc(batch=0), _pages()) == sk.OK
+    assert _attend(_adesc(len_q=0), _pages()) == sk.OK

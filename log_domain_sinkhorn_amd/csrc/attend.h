@@ -45,117 +45,198 @@ struct AttendArgs {
 constexpr int few_waves(int64_t bytes) { return bytes <= 128 ? 6 : (bytes <= 256 ? 3 : 2); }
 constexpr int few_depth(int64_t bytes) { return bytes <= 256 ? 3 : 2; }
 
-// sc = the products of keys kb0 .. of the tile (down) with the lane's row of q (across).
-template <class T, int DP, bool AHEAD, int NB, int NS>
-__device__ __forceinline__ void score_tile(const char* tk, int kb0, int lane, const typename Vec<T>::V8 (&qf)[NS], int d,
-                                           f32x16 (&sc)[NB]) {
+template <class T, int W, int WQ, int WK, int NB, int D, int OCC>
+__global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
+    AttendArgs A) {
+  constexpr int DP = row_width(W);
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
-  const int h = lane >> 5, r32 = lane & 31;
-#pragma unroll
-  for (int n = 0; n < NB; ++n) sc[n] = zero16();
-  if constexpr (AHEAD) {
-    // all fragments on their way before the first product: left alone, the
-    // compiler reads one or two ahead and each product waits for LDS (512 x
-    // 2000 x 16 heads of 64 x 8, fp16: 42.9 -> 41.6 us; of 128 columns no gain)
-    V8 kf[NS][NB];
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-      for (int n = 0; n < NB; ++n) kf[s][n] = TL::row_frag(tk, kb0 + 32 * n + r32, s, h);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-      for (int n = 0; n < NB; ++n) sc[n] = mma(kf[s][n], qf[s], sc[n]);
-  } else {
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-        sc[n] = s + 2 < NS ? mma(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n])
-                           : mma_first(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n], d - 16 * s);
-  }
-}
+  constexpr int NT = 64 * WQ * WK;
+  constexpr int KT = 32 * NB * WK;  // keys per tile
+  constexpr int NS = W / 16, NDB = W / 32;
+  // fp32: scores in natural units, rounded once, and 2^(log2e s - m) with the
+  // product inside an fma: a weight is off by what its score's own rounding
+  // makes it. 16-bit types: log2 units from the start, one operation less.
+  constexpr bool kExact = sizeof(T) == 4;
+  constexpr float kTerm = kExact ? 1.0f : (float)kLog2e;
+  constexpr bool AHEAD = WK == 1 && TL::RB == 128;
+  static_assert(WK == 1 || (WQ == 1 && NB == 1), "few rows: one tile of 32, a wave's own 32 keys");
+  using KeyT = KeyTiles<T, DP, KT, NT, D, (WK > 1), true>;  // few rows: each key is read by one workgroup
+  constexpr int kJoinBytes = WK > 1 ? WK * 32 * W * 4 : 0;
+  union Memory {
+    typename KeyT::Shared keys;
+    float join[kJoinBytes / 4 + 1];  // [WK][W][32]
+  };
+  __shared__ Memory sm;
+  __shared__ f32x2 sml[WK > 1 ? WK * 32 : 1];
 
-// One tile's scores of a row become weights 2^(f sc - m); m, the sum l and the
-// result o follow the running reference.
-template <int NB, int NDB>
-__device__ __forceinline__ void soften(f32x16 (&sc)[NB], float f, float& m, float& l, f32x16 (&o)[NDB]) {
-  float mx = -kInf;
-#pragma unroll
-  for (int n = 0; n < NB; ++n)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[n][e]);
-  mx = half_max(mx) * f;
-  // a new reference only where the maximum rose by more than 2^8: weights
-  // stay below 2^8 and the accumulators are seldom rescaled
-  if (__any(mx > m + 8.0f)) {
-    const float mn = fmaxf(m, mx);
-    const float a = mn == -kInf ? 1.0f : ex2(m - mn);
-    m = mn;
-    l *= a;
-#pragma unroll
-    for (int n = 0; n < NDB; ++n)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[n][e] *= a;
-  }
-  const float mu = m == -kInf ? 0.0f : m;  // a row with no live key yet: all weights 0
-#pragma unroll
-  for (int n = 0; n < NB; ++n)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      sc[n][e] = ex2(fmaf(sc[n][e], f, -mu));
-      l += sc[n][e];
-    }
-}
-
-// o += weights times the values of keys kb0 .. of the tile. MANY rows; with few,
-// which wait for memory, not for products, weights of 16-bit types go in two parts,
-// so that a token's result is off by its own rounding alone.
-template <class T, int DP, bool MANY, int NB, int NDB>
-__device__ __forceinline__ void add_values(const char* tv, int kb0, int lane, const f32x16 (&sc)[NB], f32x16 (&o)[NDB]) {
-  using TL = Tile<T, DP>;
-  using V8 = typename Vec<T>::V8;
-#pragma unroll
-  for (int n = 0; n < NB; ++n)
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const V8 p = pack<T>(sc[n], s);
-      if constexpr (!MANY && sizeof(T) == 2) {
-        const V8 r = pack_rest<T>(sc[n], s, p);
-#pragma unroll
-        for (int x = 0; x < NDB; ++x) {
-          const V8 f = TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane);
-          o[x] = mma(f, r, mma(f, p, o[x]));
-        }
-      } else {
-#pragma unroll
-        for (int x = 0; x < NDB; ++x) o[x] = mma(TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane), p, o[x]);
-      }
-    }
-}
-
-// Writes the rows of a workgroup: o (not divided by the sum), reference m and
-// sum l of this lane's row, or zeros without `has`; as a partial result where the
-// keys are split. With WK > 1 the waves' parts of the keys are joined through
-// so [WK][W][32] and sml [WK][32] first.
-template <class T, int W, int WQ, int WK>
-__device__ __forceinline__ void finish_rows(const AttendArgs& A, float* so, f32x2* sml, const f32x16 (&o)[W / 32], float m,
-                                            float l, bool has, int split, int b, int hk, int64_t row0) {
-  constexpr int NDB = W / 32, NT = 64 * WQ * WK;
   const Shape& S = A.S;
-  const int64_t pairs = (int64_t)S.batch * S.hkv, pair = (int64_t)b * S.hkv + hk;
+  const int64_t pairs = (int64_t)S.batch * S.hkv;
+  const int64_t item = xcd_item(pairs, A.tiles * A.nsplit);
+  if (item < 0) return;
+  int64_t pair = item / (A.tiles * A.nsplit);
+  const int64_t rest = item - pair * (A.tiles * A.nsplit);
+  const int64_t tile = rest / A.nsplit;
+  const int split = (int)(rest - tile * A.nsplit);
+  const int pos = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)pos * S.hkv);
+  const int b = batch_entry(S, pos);
+  pair = (int64_t)b * S.hkv + hk;
+
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r32 = lane & 31;
   const int wq = wave % WQ, wk = wave / WQ;
+
+  const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
+  const int64_t row0 = tile * (32 * WQ);
   const int64_t row = row0 + 32 * wq + r32;
+  const bool live_row = row < nrows;
   const int64_t qi = row / S.group;
   const int qh = hk * S.group + (int)(row - qi * S.group);
+
+  // this split's tiles of the live keys
+  const int64_t ntiles = row0 < nrows ? (nkeys + KT - 1) / KT : 0;
+  const int64_t per = (ntiles + A.nsplit - 1) / A.nsplit;
+  const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
+
+  KeyT keys(sm.keys, S, b, hk, t0, t1, nkeys, kTerm, wave, lane);
+  keys.begin();
+
+  V8 qf[NS];
+  {
+    const T* qrow = (const T*)S.q + b * S.qs[0] + qi * S.qs[1] + qh * S.qs[2];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) qf[s] = global_frag<T>(qrow, live_row && t0 < t1, s, h, S.d);
+  }
+  loads_done();
+  f32x16 o[NDB];
+#pragma unroll
+  for (int n = 0; n < NDB; ++n) o[n] = zero16();
+  float m = -kInf, l = 0.0f;  // the row's reference (log2 units) and this lane's part of the sum
+
+  if constexpr (WK == 1 && OCC == 2) one_ahead();
+  for (int it = 0; it < keys.count; ++it) {
+    // each of the last two tiles stored its scores with an instruction at least
+    keys.template next<(D > 2 ? 2 : 0)>(it, D > 2 && A.scores && it >= 2);
+    const char* const tk = keys.ktile(it);
+    const char* const tv = keys.vtile(it);
+    const int kb0 = 32 * NB * wk;
+    f32x16 sc[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) sc[n] = zero16();
+    if constexpr (AHEAD) {
+      // all fragments on their way before the first product: left alone, the
+      // compiler reads one or two ahead and each product waits for LDS (512 x
+      // 2000 x 16 heads of 64 x 8, fp16: 42.9 -> 41.6 us; of 128 columns no gain)
+      V8 kf[NS][NB];
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) kf[s][n] = TL::row_frag(tk, kb0 + 32 * n + r32, s, h);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) sc[n] = mma(kf[s][n], qf[s], sc[n]);
+    } else {
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) sc[n] = s + 2 < NS ? mma(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n])
+                           : mma_first(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n], S.d - 16 * s);
+    }
+    float f = kExact ? (float)kLog2e : S.c;  // to log2 units
+    if (kExact || keys.masked(it)) {
+      const float* const term = keys.term(it);
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 ct = *(const f32x4*)&term[kb0 + 32 * n + 8 * g + 4 * h];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = sc[n][4 * g + e];
+            sc[n][4 * g + e] = kExact ? fmaf(x, S.scale, fmaf(x, S.scale_lo, ct[e])) : fmaf(x, S.c, ct[e]);
+          }
+        }
+      if (!kExact) f = 1.0f;
+    }
+    if constexpr (WK > 1) {
+      if (A.scores) {
+        // Through this wave's own rows of the k tile, which it is done with, so
+        // that a row's 32 scores go out as one 128-byte line (361 -> 349 us at
+        // 16 x 8 x 32768 keys against four 32-byte pieces of a line each).
+        const float u = kExact ? 1.0f : f;
+        char* const mine = const_cast<char*>(tk) + kb0 * TL::RB;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *(f32x4*)(mine + 128 * r32 + 16 * ((2 * g + h) ^ (r32 & 7))) =
+              f32x4{sc[0][4 * g] * u, sc[0][4 * g + 1] * u, sc[0][4 * g + 2] * u, sc[0][4 * g + 3] * u};
+        float* const dst = A.scores + S.rows * (pair * A.score_ld + (t0 + it) * KT + kb0);
+        for (int r = lane >> 3; r < (int)S.rows; r += 8)
+          *(f32x4*)(dst + 32 * r + 4 * (lane & 7)) = *(const f32x4*)(mine + 128 * r + 16 * ((lane & 7) ^ (r & 7)));
+      }
+    }
+    float mx = -kInf;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[n][e]);
+    mx = half_max(mx) * f;
+    // a new reference only where the maximum rose by more than 2^8: weights
+    // stay below 2^8 and the accumulators are seldom rescaled
+    if (__any(mx > m + 8.0f)) {
+      const float mn = fmaxf(m, mx);
+      const float a = mn == -kInf ? 1.0f : ex2(m - mn);
+      m = mn;
+      l *= a;
+#pragma unroll
+      for (int n = 0; n < NDB; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[n][e] *= a;
+    }
+    const float mu = m == -kInf ? 0.0f : m;  // a row with no live key yet: all weights 0
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        sc[n][e] = ex2(fmaf(sc[n][e], f, -mu));
+        l += sc[n][e];
+      }
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const V8 p = pack<T>(sc[n], s);
+        if constexpr (WK > 1 && sizeof(T) == 2) {
+          // few rows wait for memory, not for products: weights in two parts, so
+          // that a token's result is off by its own rounding alone
+          const V8 r = pack_rest<T>(sc[n], s, p);
+#pragma unroll
+          for (int x = 0; x < NDB; ++x) {
+            const V8 f = TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane);
+            o[x] = mma(f, r, mma(f, p, o[x]));
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < NDB; ++x) o[x] = mma(TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane), p, o[x]);
+        }
+      }
+  }
+  l = half_sum(l);
+  // rows behind their sequence (whose zero scores weigh nothing), and rows without
+  // any key, which masked ones would make NaN where the row is no number
+  const bool live_keys = keys.live();
+  const bool has = live_row && live_keys;
+  if (!has) {
+    m = -kInf;
+    l = 0.0f;
+  }
+
   // the row's result, column group by column group: group index c4 of four
   // columns, value x (not divided by the sum)
   const bool part = A.opart != nullptr;
   if constexpr (WK > 1) {
+    float* const so = sm.join;
     __syncthreads();
     if (h == 0) sml[wk * 32 + r32] = f32x2{m, l};
 #pragma unroll
@@ -239,131 +320,6 @@ __device__ __forceinline__ void finish_rows(const AttendArgs& A, float* so, f32x
         A.lse[((int64_t)b * S.hq + qh) * S.lq + qi] = log_sum(m, l);
     }
   }
-}
-
-template <class T, int W, int WQ, int WK, int NB, int D, int OCC>
-__global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend(
-    AttendArgs A) {
-  constexpr int DP = row_width(W);
-  using TL = Tile<T, DP>;
-  using V8 = typename Vec<T>::V8;
-  constexpr int NT = 64 * WQ * WK;
-  constexpr int KT = 32 * NB * WK;  // keys per tile
-  constexpr int NS = W / 16, NDB = W / 32;
-  // fp32: scores in natural units, rounded once, and 2^(log2e s - m) with the
-  // product inside an fma: a weight is off by what its score's own rounding
-  // makes it. 16-bit types: log2 units from the start, one operation less.
-  constexpr bool kExact = sizeof(T) == 4;
-  constexpr float kTerm = kExact ? 1.0f : (float)kLog2e;
-  constexpr bool AHEAD = WK == 1 && TL::RB == 128;
-  static_assert(WK == 1 || (WQ == 1 && NB == 1), "few rows: one tile of 32, a wave's own 32 keys");
-  using KeyT = KeyTiles<T, DP, KT, NT, D, (WK > 1), true>;  // few rows: each key is read by one workgroup
-  constexpr int kJoinBytes = WK > 1 ? WK * 32 * W * 4 : 0;
-  union Memory {
-    typename KeyT::Shared keys;
-    float join[kJoinBytes / 4 + 1];  // [WK][W][32]
-  };
-  __shared__ Memory sm;
-  __shared__ f32x2 sml[WK > 1 ? WK * 32 : 1];
-
-  const Shape& S = A.S;
-  const int64_t pairs = (int64_t)S.batch * S.hkv;
-  const int64_t item = xcd_item(pairs, A.tiles * A.nsplit);
-  if (item < 0) return;
-  int64_t pair = item / (A.tiles * A.nsplit);
-  const int64_t rest = item - pair * (A.tiles * A.nsplit);
-  const int64_t tile = rest / A.nsplit;
-  const int split = (int)(rest - tile * A.nsplit);
-  const int pos = (int)(pair / S.hkv), hk = (int)(pair - (int64_t)pos * S.hkv);
-  const int b = batch_entry(S, pos);
-  pair = (int64_t)b * S.hkv + hk;
-
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int h = lane >> 5, r32 = lane & 31;
-  const int wq = wave % WQ, wk = wave / WQ;
-
-  const int64_t nkeys = live_keys(S, b), nrows = live_rows(S, b);
-  const int64_t row0 = tile * (32 * WQ);
-  const int64_t row = row0 + 32 * wq + r32;
-  const bool live_row = row < nrows;
-  const int64_t qi = row / S.group;
-  const int qh = hk * S.group + (int)(row - qi * S.group);
-
-  // this split's tiles of the live keys
-  const int64_t ntiles = row0 < nrows ? (nkeys + KT - 1) / KT : 0;
-  const int64_t per = (ntiles + A.nsplit - 1) / A.nsplit;
-  const int64_t t0 = split * per, t1 = t0 + per < ntiles ? t0 + per : ntiles;
-
-  KeyT keys(sm.keys, S, b, hk, t0, t1, nkeys, kTerm, wave, lane);
-  keys.begin();
-
-  V8 qf[NS];
-  {
-    const T* qrow = (const T*)S.q + b * S.qs[0] + qi * S.qs[1] + qh * S.qs[2];
-#pragma unroll
-    for (int s = 0; s < NS; ++s) qf[s] = global_frag<T>(qrow, live_row && t0 < t1, s, h, S.d);
-  }
-  loads_done();
-  f32x16 o[NDB];
-#pragma unroll
-  for (int n = 0; n < NDB; ++n) o[n] = zero16();
-  float m = -kInf, l = 0.0f;  // the row's reference (log2 units) and this lane's part of the sum
-
-  if constexpr (WK == 1 && OCC == 2) one_ahead();
-  for (int it = 0; it < keys.count; ++it) {
-    // each of the last two tiles stored its scores with an instruction at least
-    keys.template next<(D > 2 ? 2 : 0)>(it, D > 2 && A.scores && it >= 2);
-    const char* const tk = keys.ktile(it);
-    const char* const tv = keys.vtile(it);
-    const int kb0 = 32 * NB * wk;
-    f32x16 sc[NB];
-    score_tile<T, DP, AHEAD, NB, NS>(tk, kb0, lane, qf, S.d, sc);
-    float f = kExact ? (float)kLog2e : S.c;  // to log2 units
-    if (kExact || keys.masked(it)) {
-      const float* const term = keys.term(it);
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f32x4 ct = *(const f32x4*)&term[kb0 + 32 * n + 8 * g + 4 * h];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = sc[n][4 * g + e];
-            sc[n][4 * g + e] = kExact ? fmaf(x, S.scale, fmaf(x, S.scale_lo, ct[e])) : fmaf(x, S.c, ct[e]);
-          }
-        }
-      if (!kExact) f = 1.0f;
-    }
-    if constexpr (WK > 1) {
-      if (A.scores) {
-        // Through this wave's own rows of the k tile, which it is done with, so
-        // that a row's 32 scores go out as one 128-byte line (361 -> 349 us at
-        // 16 x 8 x 32768 keys against four 32-byte pieces of a line each).
-        const float u = kExact ? 1.0f : f;
-        char* const mine = const_cast<char*>(tk) + kb0 * TL::RB;
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *(f32x4*)(mine + 128 * r32 + 16 * ((2 * g + h) ^ (r32 & 7))) =
-              f32x4{sc[0][4 * g] * u, sc[0][4 * g + 1] * u, sc[0][4 * g + 2] * u, sc[0][4 * g + 3] * u};
-        float* const dst = A.scores + S.rows * (pair * A.score_ld + (t0 + it) * KT + kb0);
-        for (int r = lane >> 3; r < (int)S.rows; r += 8)
-          *(f32x4*)(dst + 32 * r + 4 * (lane & 7)) = *(const f32x4*)(mine + 128 * r + 16 * ((lane & 7) ^ (r & 7)));
-      }
-    }
-    soften<NB, NDB>(sc, f, m, l, o);
-    add_values<T, DP, WK == 1, NB, NDB>(tv, kb0, lane, sc, o);
-  }
-  l = half_sum(l);
-  // rows behind their sequence (whose zero scores weigh nothing), and rows without
-  // any key, which masked ones would make NaN where the row is no number
-  const bool live_keys = keys.live();
-  const bool has = live_row && live_keys;
-  if (!has) {
-    m = -kInf;
-    l = 0.0f;
-  }
-
-  finish_rows<T, W, WQ, WK>(A, sm.join, sml, o, m, l, has, split, b, hk, row0);
 }
 
 // Joins the splits of a row: 32 lanes per column group of four; GR groups of

@@ -3,7 +3,9 @@
 // `recent`, only j > p - recent or j < first.
 //
 // The tiles, the softmax and the split of the keys are those of k_attend (attend.h),
-// with three differences.
+// with the differences below. (Their code stands here as functions; k_attend keeps its
+// own in line: called as functions they cost it 1 to 3% in fp32, 20000 x 24001 at 50
+// columns 996 -> 1009 to 1033 us.)
 //
 // Pages. A tile is loaded by instructions of 2, 4 or 8 rows, which lie in one page
 // because page sizes are multiples of 8: the page's address goes into the scalar base
@@ -16,10 +18,9 @@
 // window's edge; tiles that no row of the workgroup sees are not loaded, and waves
 // leave out those that none of their rows sees. A hidden key's score becomes
 // -infinity, its weight 0; a value there that is no number must not reach the row
-// through 0 x infinity, so such a tile is first looked through for any (2
-// operations per 4 bytes), and if there is one, its finite part is multiplied as
-// usual, while infinities are counted by products with 0 and 1 in place of values
-// and weights and added to the rows that see them.
+// through 0 x infinity, so the workgroup first looks through such a tile for any (a
+// share each, 2 operations per 4 bytes, and a barrier). If there is one, those values
+// are added, key by key, to the rows that see them, and 0 takes their places.
 //
 // Order. The rows at the end of a chunk see the most keys and come first.
 #pragma once
@@ -52,6 +53,7 @@ struct PageTiles {
   struct Shared {
     __attribute__((aligned(16))) char tiles[D][2][kTileBytes];
     __attribute__((aligned(16))) float term[D][KT];  // of a tile with bad pages: 0 or -inf by key
+    int odd;  // the last tile, counted from 1, that was found to hold values that are no numbers
   };
   Shared& sm;
   const Paging& P;
@@ -136,6 +138,7 @@ struct PageTiles {
       }
   }
   __device__ __forceinline__ void begin() {
+    if (wave == 0) sm.odd = 0;  // read behind the first tile's barrier
 #pragma unroll
     for (int n = 0; n < D - 1; ++n) start(n);
   }
@@ -152,75 +155,269 @@ struct PageTiles {
     start(n + D - 1);
   }
   __device__ __forceinline__ const char* ktile(int n) const { return sm.tiles[n % D][0]; }
-  __device__ __forceinline__ const char* vtile(int n) const { return sm.tiles[n % D][1]; }
+  __device__ __forceinline__ char* vtile(int n) const { return sm.tiles[n % D][1]; }
   // of a tile with pages outside the cache: 0 or -inf for each key; else null
   __device__ __forceinline__ const float* term(int n) const { return (bad >> (n % D)) & 1 ? sm.term[n % D] : nullptr; }
 };
 
-// Does any value of rows kb0 .. kb0 + ROWS - 1 of the tile fail to be a number? By all lanes of a wave.
-template <class T, int DP, int ROWS>
-__device__ __forceinline__ bool no_numbers(const char* tv, int kb0, int lane) {
+// sc = the products of keys kb0 .. of the tile (down) with the lane's row of q (across).
+template <class T, int DP, bool AHEAD, int NB, int NS>
+__device__ __forceinline__ void score_tile(const char* tk, int kb0, int lane, const typename Vec<T>::V8 (&qf)[NS], int d,
+                                           f32x16 (&sc)[NB]) {
   using TL = Tile<T, DP>;
-  const char* p = tv + kb0 * TL::RB + 16 * lane;
+  using V8 = typename Vec<T>::V8;
+  const int h = lane >> 5, r32 = lane & 31;
+#pragma unroll
+  for (int n = 0; n < NB; ++n) sc[n] = zero16();
+  if constexpr (AHEAD) {
+    // all fragments on their way before the first product: left alone, the
+    // compiler reads one or two ahead and each product waits for LDS (512 x
+    // 2000 x 16 heads of 64 x 8, fp16: 42.9 -> 41.6 us; of 128 columns no gain)
+    V8 kf[NS][NB];
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) kf[s][n] = TL::row_frag(tk, kb0 + 32 * n + r32, s, h);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) sc[n] = mma(kf[s][n], qf[s], sc[n]);
+  } else {
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+        sc[n] = s + 2 < NS ? mma(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n])
+                           : mma_first(TL::row_frag(tk, kb0 + 32 * n + r32, s, h), qf[s], sc[n], d - 16 * s);
+  }
+}
+
+// One tile's scores of a row become weights 2^(f sc - m); m, the sum l and the
+// result o follow the running reference.
+template <int NB, int NDB>
+__device__ __forceinline__ void soften(f32x16 (&sc)[NB], float f, float& m, float& l, f32x16 (&o)[NDB]) {
+  float mx = -kInf;
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[n][e]);
+  mx = half_max(mx) * f;
+  // a new reference only where the maximum rose by more than 2^8: weights
+  // stay below 2^8 and the accumulators are seldom rescaled
+  if (__any(mx > m + 8.0f)) {
+    const float mn = fmaxf(m, mx);
+    const float a = mn == -kInf ? 1.0f : ex2(m - mn);
+    m = mn;
+    l *= a;
+#pragma unroll
+    for (int n = 0; n < NDB; ++n)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[n][e] *= a;
+  }
+  const float mu = m == -kInf ? 0.0f : m;  // a row with no live key yet: all weights 0
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      sc[n][e] = ex2(fmaf(sc[n][e], f, -mu));
+      l += sc[n][e];
+    }
+}
+
+// o += weights times the values of keys kb0 .. of the tile. MANY rows; with few,
+// which wait for memory, not for products, weights of 16-bit types go in two parts,
+// so that a token's result is off by its own rounding alone.
+template <class T, int DP, bool MANY, int NB, int NDB>
+__device__ __forceinline__ void add_values(const char* tv, int kb0, int lane, const f32x16 (&sc)[NB], f32x16 (&o)[NDB]) {
+  using V8 = typename Vec<T>::V8;
+  using TL = Tile<T, DP>;
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const V8 p = pack<T>(sc[n], s);
+      if constexpr (!MANY && sizeof(T) == 2) {
+        const V8 r = pack_rest<T>(sc[n], s, p);
+#pragma unroll
+        for (int x = 0; x < NDB; ++x) {
+          const V8 f = TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane);
+          o[x] = mma(f, r, mma(f, p, o[x]));
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < NDB; ++x) o[x] = mma(TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane), p, o[x]);
+      }
+    }
+}
+
+// Writes the rows of a workgroup: o (not divided by the sum), reference m and
+// sum l of this lane's row, or zeros without `has`; as a partial result where the
+// keys are split. With WK > 1 the waves' parts of the keys are joined through
+// so [WK][W][32] and sml [WK][32] first.
+template <class T, int W, int WQ, int WK>
+__device__ __forceinline__ void finish_rows(const AttendArgs& A, float* so, f32x2* sml, const f32x16 (&o)[W / 32], float m,
+                                            float l, bool has, int split, int b, int hk, int64_t row0) {
+  constexpr int NDB = W / 32, NT = 64 * WQ * WK;
+  const Shape& S = A.S;
+  const int64_t pairs = (int64_t)S.batch * S.hkv, pair = (int64_t)b * S.hkv + hk;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5, r32 = lane & 31;
+  const int wq = wave % WQ, wk = wave / WQ;
+  const int64_t row = row0 + 32 * wq + r32;
+  const int64_t qi = row / S.group;
+  const int qh = hk * S.group + (int)(row - qi * S.group);
+  // the row's result, column group by column group: group index c4 of four
+  // columns, value x (not divided by the sum)
+  const bool part = A.opart != nullptr;
+  if constexpr (WK > 1) {
+    __syncthreads();
+    if (h == 0) sml[wk * 32 + r32] = f32x2{m, l};
+#pragma unroll
+    for (int x = 0; x < NDB; ++x)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) so[(wk * W + 32 * x + 8 * (e >> 2) + 4 * h + (e & 3)) * 32 + r32] = has ? o[x][e] : 0.0f;
+    __syncthreads();
+    // thread: row tid % 32, column groups tid / 32, + NT / 32, ...
+    const int64_t jrow = row0 + (tid & 31);
+    float f[WK], mm = -kInf, ll = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) mm = fmaxf(mm, sml[w * 32 + (tid & 31)][0]);
+    const float mu = mm == -kInf ? 0.0f : mm;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) {
+      const f32x2 p = sml[w * 32 + (tid & 31)];
+      f[w] = ex2(p[0] - mu);
+      ll = fmaf(f[w], p[1], ll);
+    }
+    if (jrow >= S.rows) return;
+    const int64_t ji = jrow / S.group;
+    const int jh = hk * S.group + (int)(jrow - ji * S.group);
+    // a NaN sum is kept; only an empty row is 0
+    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+    T* orow = (T*)A.out + b * A.os[0] + ji * A.os[1] + jh * A.os[2];
+    float* prow = part ? A.opart + (((int64_t)split * pairs + pair) * S.rows + jrow) * A.dvp : nullptr;
+#pragma unroll
+    for (int it = 0; it < (W * 8 + NT - 1) / NT; ++it) {
+      const int c = 4 * ((tid >> 5) + it * (NT / 32));
+      if (c >= W) break;
+      f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < WK; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = fmaf(f[w], so[(w * W + c + e) * 32 + (tid & 31)], x[e]);
+      if (part) {
+        if (c < A.dvp) *(f32x4*)(prow + c) = x;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] *= inv;
+        if (A.vec)
+          store4<T, true>(orow, c, S.dv, x);
+        else
+          store4<T, false>(orow, c, S.dv, x);
+      }
+    }
+    if (tid < 32) {
+      if (part)
+        A.mlpart[((int64_t)split * pairs + pair) * S.rows + jrow] = f32x2{mm, ll};
+      else
+        A.lse[((int64_t)b * S.hq + jh) * S.lq + ji] = log_sum(mm, ll);
+    }
+  } else {
+    if (row >= S.rows) return;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    T* orow = (T*)A.out + b * A.os[0] + qi * A.os[1] + qh * A.os[2];
+    const int64_t prow_i = ((int64_t)split * pairs + pair) * S.rows + row;
+#pragma unroll
+    for (int n = 0; n < NDB; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = 32 * n + 8 * g + 4 * h;
+        f32x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = has ? o[n][4 * g + e] : 0.0f;
+        if (part) {
+          if (c < A.dvp) *(f32x4*)(A.opart + prow_i * A.dvp + c) = x;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] *= inv;
+          if (A.vec)
+            store4<T, true>(orow, c, S.dv, x);
+          else
+            store4<T, false>(orow, c, S.dv, x);
+        }
+      }
+    if (h == 0) {
+      if (part)
+        A.mlpart[prow_i] = f32x2{m, l};
+      else
+        A.lse[((int64_t)b * S.hq + qh) * S.lq + qi] = log_sum(m, l);
+    }
+  }
+}
+
+// Is any value of the tile no number? By the workgroup's threads, a share each;
+// the answer of this thread's.
+template <class T, int BYTES, int NT>
+__device__ __forceinline__ bool no_numbers(const char* tv) {
+  const char* p = tv + 16 * threadIdx.x;
+  constexpr int N = BYTES / 16 / NT;
+  static_assert(N * NT * 16 == BYTES, "whole shares");
   if constexpr (sizeof(T) == 4) {
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < ROWS * TL::RB / 1024; ++i) {
-      const u32x4 x = *(const u32x4*)(p + 1024 * i);
+    for (int i = 0; i < N; ++i) {
+      const u32x4 x = *(const u32x4*)(p + 16 * NT * i);
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = max(top, x[e] & 0x7fffffffu);
     }
-    return __any(top >= 0x7f800000u);
+    return top >= 0x7f800000u;
   } else {
     typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
     constexpr unsigned short inf = std::is_same<T, __bf16>::value ? 0x7f80 : 0x7c00;
     u16x8 top = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < ROWS * TL::RB / 1024; ++i) {
-      const u16x8 x = *(const u16x8*)(p + 1024 * i) & (unsigned short)0x7fff;
-      top = __builtin_elementwise_max(top, x);
-    }
+    for (int i = 0; i < N; ++i) top = __builtin_elementwise_max(top, *(const u16x8*)(p + 16 * NT * i) & (unsigned short)0x7fff);
     bool any = false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) any = any || top[e] >= inf;
-    return __any(any);
+    for (int e = 0; e < 8; ++e) any |= top[e] >= inf;
+    return any;
+  }
+}
+// Puts 0 in their places.
+template <class T, int BYTES, int NT>
+__device__ __forceinline__ void clear_no_numbers(char* tv) {
+  typedef typename Vec<T>::V4 V4;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < BYTES / (int)sizeof(V4); i += NT) {
+    V4 x = ((V4*)tv)[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = fabsf((float)x[e]) < kInf ? x[e] : (T)0.0f;
+    ((V4*)tv)[i] = x;
   }
 }
 
-// add_values where values may be no numbers and some keys are hidden: seen(i) tells
-// whether the lane's row sees key kb0 + i + 4 h (h: the lane's half).
-template <class T, int DP, bool MANY, int NB, int NDB, class F>
-__device__ __forceinline__ void add_seen_values(const char* tv, int kb0, int lane, const f32x16 (&sc)[NB], f32x16 (&o)[NDB],
-                                                F&& seen) {
+// Adds the values of keys kb0 .. that are no numbers to the rows that see them; seen(i)
+// tells whether the lane's row sees key kb0 + i + 4 h (h: the lane's half).
+template <class T, int DP, int KEYS, int NDB, class F>
+__device__ __forceinline__ void add_no_numbers(const char* tv, int kb0, int lane, f32x16 (&o)[NDB], F&& seen) {
   using TL = Tile<T, DP>;
-  using V8 = typename Vec<T>::V8;
+  typedef typename Vec<T>::V4 V4;
+  const int h = lane >> 5;
+#pragma unroll 1
+  for (int i = 0; i < KEYS; ++i) {
+    if (!seen(i - 4 * h)) continue;
 #pragma unroll
-  for (int x = 0; x < NDB; ++x) {
-    f32x16 up = zero16(), down = zero16();  // how many +inf, -inf (a NaN counts as both) the row sees
+    for (int x = 0; x < NDB; ++x)
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
+      for (int g = 0; g < 4; ++g) {
+        const int c = 32 * x + 8 * g + 4 * h;
+        const V4 y = *(const V4*)(tv + TL::at(kb0 + i, c / TL::EPC) + c % TL::EPC * (int)sizeof(T));
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        V8 f = TL::col_frag(tv, kb0 + 32 * n + 16 * s, 32 * x, lane), pos, neg, one;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y = (float)f[e];
-          pos[e] = (T)(y < kInf ? 0.0f : 1.0f);
-          neg[e] = (T)(y > -kInf ? 0.0f : 1.0f);
-          f[e] = y < kInf && y > -kInf ? f[e] : (T)0.0f;
-          one[e] = (T)(seen(32 * n + 16 * s + 8 * (e >> 2) + (e & 3)) ? 1.0f : 0.0f);
-        }
-        const V8 p = pack<T>(sc[n], s);
-        o[x] = mma(f, p, o[x]);
-        if constexpr (!MANY && sizeof(T) == 2) o[x] = mma(f, pack_rest<T>(sc[n], s, p), o[x]);
-        up = mma(pos, one, up);
-        down = mma(neg, one, down);
+        for (int e = 0; e < 4; ++e)
+          o[x][4 * g + e] += fabsf((float)y[e]) < kInf ? 0.0f : (float)y[e];
+        __builtin_amdgcn_sched_barrier(0);  // one at a time: few registers
       }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if (up[e] > 0.0f) o[x][e] += kInf;
-      if (down[e] > 0.0f) o[x][e] -= kInf;
-    }
   }
 }
 
@@ -316,18 +513,37 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
 
   // this lane's row sees keys below `end`, and of these from `from` on or below G.first;
   // over the wave's live rows these bounds run from e_lo to e_hi and f_lo to f_hi
+  // (over the workgroup's: b_lo and b_hi)
   const int end = end_of(row), from = from_of(end);
   const int64_t w0 = row0 + 32 * wq, w1 = w0 + 31 < nrows ? w0 + 31 : nrows - 1;
   const int e_lo = end_of(w0), e_hi = w0 < nrows ? end_of(w1) : 0, f_lo = from_of(e_lo), f_hi = from_of(e_hi);
+
+  const int b_lo = end_of(row0), b_hi = from_of(end_of(row0 + 32 * WQ < nrows ? row0 + 32 * WQ - 1 : nrows - 1));
 
   if constexpr (WK == 1 && OCC == 2) one_ahead();
   for (int it = 0; it < keys.count; ++it) {
     keys.next(it);
     const int kb0 = KW * wk;
     const int j0 = __builtin_amdgcn_readfirstlane(keys.key(it) + kb0);
-    if (j0 >= e_hi || (j0 + KW <= f_lo && j0 >= G.first)) continue;  // no row of this wave sees any
     const char* const tk = keys.ktile(it);
-    const char* const tv = keys.vtile(it);
+    char* const tv = keys.vtile(it);
+    // does every row of the workgroup see every key? If not, are there values that are no numbers?
+    bool odd = false;
+    const int t0 = j0 - kb0;
+    if (t0 + KT > b_lo || (t0 < b_hi && t0 + KT > G.first)) {
+      if (no_numbers<T, KeyT::kTileBytes, NT>(tv)) sm.keys.odd = it + 1;
+      __syncthreads();
+      odd = __builtin_amdgcn_readfirstlane(sm.keys.odd) == it + 1;
+    }
+    auto clear = [&] {
+      __syncthreads();
+      clear_no_numbers<T, KeyT::kTileBytes, NT>(tv);
+      __syncthreads();
+    };
+    if (j0 >= e_hi || (j0 + KW <= f_lo && j0 >= G.first)) {  // no row of this wave sees any
+      if (odd) clear();
+      continue;
+    }
     f32x16 sc[NB];
     score_tile<T, DP, AHEAD, NB, NS>(tk, kb0, lane, qf, S.d, sc);
     const float f = kExact ? (float)kLog2e : S.c;  // to log2 units
@@ -360,10 +576,11 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
         }
     }
     soften<NB, NDB>(sc, f, m, l, o);
-    if (!all && no_numbers<T, DP, KW>(tv, kb0, lane))
-      add_seen_values<T, DP, WK == 1, NB, NDB>(tv, kb0, lane, sc, o, seen);
-    else
-      add_values<T, DP, WK == 1, NB, NDB>(tv, kb0, lane, sc, o);
+    if (odd) {
+      add_no_numbers<T, DP, KW>(tv, kb0, lane, o, seen);
+      clear();
+    }
+    add_values<T, DP, WK == 1, NB, NDB>(tv, kb0, lane, sc, o);
   }
   l = half_sum(l);
   if (!live_row) {

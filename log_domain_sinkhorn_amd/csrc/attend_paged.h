@@ -7,12 +7,17 @@
 // own in line: called as functions they cost it 1 to 3% in fp32, 20000 x 24001 at 50
 // columns 996 -> 1009 to 1033 us.)
 //
-// Pages. A tile is loaded by instructions of 2, 4 or 8 rows, which lie in one page
-// because page sizes are multiples of 8: the page's address goes into the scalar base
-// of the load, so a lane's offsets are the same in every tile and a cache may be of
-// any size. A wave holds 256 page numbers of the sequence, four a lane, and takes
-// them from there by lane reads; loading the next 256 waits for the loads in
-// flight, once in 2048 keys or more.
+// Pages. A wave loads a tile's rows in groups of 8, which lie in one page because page
+// sizes are multiples of 8: a group's address goes into the scalar base of its loads,
+// so a lane's offsets are the same in every tile and a cache may be of any size. The
+// addresses of a tile's groups are made side by side in the lanes of a vector
+// register, a tile ahead, and read from there lane by lane (made one by one in
+// scalar registers they took the longer part of a tile's time with few rows: 16 x
+// 32768 keys x 8 heads 326 -> 276 us). A wave holds 256 page numbers of the sequence, four a lane;
+// loading the next 256 waits for the loads in flight, once in 2048 keys or more.
+//
+// Few rows: a wave loads the keys that it computes on itself, and the waves of a
+// workgroup meet only at the end.
 //
 // Masks are of the pair, but only in tiles at the rows' own places and at the
 // window's edge; tiles that no row of the workgroup sees are not loaded, and waves
@@ -39,17 +44,22 @@ struct PagedArgs {
 };
 
 // The tiles of KT keys that a workgroup runs over: `ns` from the sequence's start on,
-// then those from tile t_lo on; of all these, `count` from the n0-th on. In a ring
-// of D buffers as KeyTiles.
-template <class T, int DP, int KT, int NT, int D, bool ONCE>
+// then those from tile t_lo on; of all these, `count` from the n0-th on. In a ring of
+// D buffers (k, then v, in each): tile n + D - 1 is started while tile n is computed
+// on. A wave loads RW consecutive rows of a tile. OWN: these are the ones that it
+// computes on, so waves do not wait for each other.
+template <class T, int DP, int KT, int NT, int D, bool OWN>
 struct PageTiles {
-  using Ld = Loader<T, DP, KT, NT, ONCE>;
   using TL = Tile<T, DP>;
+  static constexpr int NW = NT / 64, RW = KT / NW;
   static constexpr int kTileBytes = KT * TL::RB;
-  static constexpr int kOps = 2 * Ld::N;
+  static constexpr int RPI = 64 / TL::CPR;               // rows of an instruction
+  static constexpr int IPO = 8 / RPI;                    // instructions for 8 rows, which lie in one page
+  static constexpr int N = RW / RPI;                     // instructions of a wave for k, and for v
+  static constexpr int KIND = N < 2 * IPO ? N : 2 * IPO;  // the chunks' permutation repeats after 16 rows
+  static constexpr int kOps = 2 * N;
   static constexpr int kHeld = 4;  // page numbers of a lane
-  static_assert(D == 2 || Ld::TOTAL % Ld::NW == 0, "counted loads: the same of every wave");
-  static_assert(8 % Ld::RPI == 0, "the rows of an instruction lie in one page");
+  static_assert(KT % NW == 0 && RW % 16 == 0 && IPO >= 1, "whole groups of 8 rows");
   struct Shared {
     __attribute__((aligned(16))) char tiles[D][2][kTileBytes];
     __attribute__((aligned(16))) float term[D][KT];  // of a tile with bad pages: 0 or -inf by key
@@ -62,12 +72,14 @@ struct PageTiles {
   int64_t kpage, vpage;  // bytes
   uint32_t kslot, vslot;
   const int32_t* table;
-  uint32_t koff[Ld::N], voff[Ld::N];  // byte offset of this lane's chunk within an instruction's rows
+  uint32_t koff[KIND], voff[KIND];  // byte offset of this lane's chunk from its 8 rows' start
   int32_t id[kHeld];
-  uint32_t held;  // first page held
+  uint32_t held;         // first page held
+  uint64_t kat, vat;     // of the next tile to be started: lane i: address of the wave's i-th 8 rows
+  uint64_t ok;           // bit i: they are in the cache
   int nkeys, n0, count, ns, t_lo, wave, lane;
   uint32_t npages;  // of the sequence
-  uint32_t bad;     // bit n % D: tile n has pages outside the cache
+  uint32_t bad;     // bit n % D: tile n may have pages outside the cache
   bool bad_held;
 
   __device__ __forceinline__ PageTiles(Shared& sm_, const PagedArgs& A, int b, int hk, int nkeys_, int ns_, int t_lo_, int n0_,
@@ -78,14 +90,17 @@ struct PageTiles {
         table(A.P.table + b * A.P.stride), held(0), nkeys(nkeys_), n0(n0_), count(count_), ns(ns_), t_lo(t_lo_), wave(wave_),
         lane(lane_), npages(nkeys_ > 0 ? page_of(A.P, (uint32_t)(nkeys_ - 1)) + 1 : 0), bad(0), bad_held(false) {
 #pragma unroll
-    for (int n = 0; n < Ld::N; ++n) {
-      const int c = (lane % TL::CPR) ^ TL::swz(Ld::row(n, wave, lane)), r = lane / TL::CPR;
-      koff[n] = c * TL::EPC < A.A.S.d ? r * kslot + 16 * c : kOutside;
-      voff[n] = c * TL::EPC < A.A.S.dv ? r * vslot + 16 * c : kOutside;
+    for (int i = 0; i < KIND; ++i) {
+      const int r = i * RPI + lane / TL::CPR, c = (lane % TL::CPR) ^ TL::swz(r);
+      koff[i] = c * TL::EPC < A.A.S.d ? r % 8 * kslot + 16 * c : kOutside;
+      voff[i] = c * TL::EPC < A.A.S.dv ? r % 8 * vslot + 16 * c : kOutside;
     }
 #pragma unroll
     for (int n = 0; n < kHeld; ++n) id[n] = -1;
-    if (count > 0) hold(page_of(P, (uint32_t)key(0)));
+    if (count > 0) {
+      hold(page_of(P, (uint32_t)key(0)));
+      locate(0);
+    }
   }
   // first key of tile n
   __device__ __forceinline__ int key(int n) const {
@@ -105,37 +120,54 @@ struct PageTiles {
     bad_held = __any(out);
     loads_done();  // known to the compiler: it would otherwise wait for all loads at every use
   }
-  __device__ __forceinline__ int32_t number(uint32_t page) const {
-    const uint32_t x = page - held, at = x & 63;
-    const int32_t a = __builtin_amdgcn_readlane(id[0], at), b = __builtin_amdgcn_readlane(id[1], at);
-    const int32_t c = __builtin_amdgcn_readlane(id[2], at), d = __builtin_amdgcn_readlane(id[3], at);
-    return x < 128 ? (x < 64 ? a : b) : (x < 192 ? c : d);
+  // Addresses for tile n, those of the wave's groups of 8 rows side by side in its lanes.
+  __device__ __forceinline__ void locate(int n) {
+    const int first = __builtin_amdgcn_readfirstlane(key(n));
+    const int left = nkeys - first;  // keys from the tile's first on, at least one
+    const uint32_t p0 = page_of(P, (uint32_t)first), p1 = page_of(P, (uint32_t)(first + (left < KT ? left : KT) - 1));
+    if (p0 < held || p1 >= held + 64 * kHeld) hold(p0);
+    const int r = wave * RW + 8 * (lane % (RW / 8));
+    const bool live = r < left;
+    const uint32_t j = (uint32_t)(first + (live ? r : 0));
+    const uint32_t page = page_of(P, j), slot = j - page * (uint32_t)P.size;
+    const uint32_t x = page - held;
+    int32_t at = 0;
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      const int32_t y = __builtin_amdgcn_ds_bpermute(4 * (x & 63), id[h]);
+      at = x >> 6 == (uint32_t)h ? y : at;
+    }
+    const bool in = live && (uint32_t)at < (uint32_t)P.pages;
+    at = in ? at : 0;
+    kat = (uint64_t)k + (uint64_t)at * (uint64_t)kpage + (uint64_t)slot * kslot;
+    vat = (uint64_t)v + (uint64_t)at * (uint64_t)vpage + (uint64_t)slot * vslot;
+    ok = __ballot(in);
+  }
+  __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rsrc_of(uint64_t at, int i) {
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)at, i), hi = __builtin_amdgcn_readlane((uint32_t)(at >> 32), i);
+    return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0, (int)kOutside, 0x00027000);
   }
   __device__ __forceinline__ void start(int n) {
     if (n >= count) return;
     const int buf = n % D;
-    const int first = __builtin_amdgcn_readfirstlane(key(n));
-    const int left = nkeys - first;  // keys from the tile's first on, at least one
-    {
-      const uint32_t p0 = page_of(P, (uint32_t)first), p1 = page_of(P, (uint32_t)(first + (left < KT ? left : KT) - 1));
-      if (p0 < held || p1 >= held + 64 * kHeld) hold(p0);
-    }
+    const int mine = nkeys - __builtin_amdgcn_readfirstlane(key(n)) - wave * RW;  // keys from this wave's first row on
     bad = (bad & ~(1u << buf)) | (bad_held ? 1u << buf : 0u);
-    const uint32_t klds = lds_offset(sm.tiles[buf][0]) + wave * 1024, vlds = lds_offset(sm.tiles[buf][1]) + wave * 1024;
+    const uint32_t klds = lds_offset(sm.tiles[buf][0]) + wave * (N * 1024), vlds = lds_offset(sm.tiles[buf][1]) + wave * (N * 1024);
+    const int lane_row = lane / TL::CPR;
 #pragma unroll
-    for (int i = 0; i < Ld::N; ++i)
-      if (Ld::has(i, wave)) {
-        const int r0 = (i * Ld::NW + wave) * Ld::RPI;
-        const uint32_t j = (uint32_t)(first + (r0 < left ? r0 : 0));  // rows behind the keys are not read
-        const uint32_t page = page_of(P, j), slot = j - page * (uint32_t)P.size;
-        const int32_t at = number(page);
-        const bool ok = r0 < left && (uint32_t)at < (uint32_t)P.pages;
-        const int64_t where = ok ? at : 0;
-        const bool live = ok && r0 + lane / TL::CPR < left;
-        dma_load<16, ONCE>(dma_rsrc(k + where * kpage + (uint64_t)slot * kslot), klds + i * Ld::NW * 1024, live ? koff[i] : kOutside);
-        dma_load<16, ONCE>(dma_rsrc(v + where * vpage + (uint64_t)slot * vslot), vlds + i * Ld::NW * 1024, live ? voff[i] : kOutside);
-        if (bad_held && lane < Ld::RPI) sm.term[buf][r0 + lane] = ok ? 0.0f : -kInf;
+    for (int g = 0; g < RW / 8; ++g) {
+      const __amdgpu_buffer_rsrc_t kr = rsrc_of(kat, g), vr = rsrc_of(vat, g);
+      const int end = (ok >> g) & 1 ? mine : 0;
+#pragma unroll
+      for (int s = 0; s < IPO; ++s) {
+        const int i = g * IPO + s;
+        const bool live = i * RPI + lane_row < end;
+        dma_load<16, OWN>(kr, klds + i * 1024, live ? koff[i % KIND] : kOutside);
+        dma_load<16, OWN>(vr, vlds + i * 1024, live ? voff[i % KIND] : kOutside);
       }
+      if (bad_held && lane < 8) sm.term[buf][wave * RW + 8 * g + lane] = (ok >> g) & 1 ? 0.0f : -kInf;
+    }
+    if (n + 1 < count) locate(n + 1);
   }
   __device__ __forceinline__ void begin() {
     if (wave == 0) sm.odd = 0;  // read behind the first tile's barrier
@@ -151,7 +183,7 @@ struct PageTiles {
       dma_wait<(D - 2) * kOps>();
     else
       dma_wait<0>();
-    __syncthreads();
+    if constexpr (!OWN) __syncthreads();
     start(n + D - 1);
   }
   __device__ __forceinline__ const char* ktile(int n) const { return sm.tiles[n % D][0]; }
@@ -356,11 +388,11 @@ __device__ __forceinline__ void finish_rows(const AttendArgs& A, float* so, f32x
   }
 }
 
-// Is any value of the tile no number? By the workgroup's threads, a share each;
-// the answer of this thread's.
+// Is any value of BYTES bytes no number? By NT threads, a share each; the answer of
+// this one's.
 template <class T, int BYTES, int NT>
-__device__ __forceinline__ bool no_numbers(const char* tv) {
-  const char* p = tv + 16 * threadIdx.x;
+__device__ __forceinline__ bool no_numbers(const char* tv, int thread) {
+  const char* p = tv + 16 * thread;
   constexpr int N = BYTES / 16 / NT;
   static_assert(N * NT * 16 == BYTES, "whole shares");
   if constexpr (sizeof(T) == 4) {
@@ -386,10 +418,10 @@ __device__ __forceinline__ bool no_numbers(const char* tv) {
 }
 // Puts 0 in their places.
 template <class T, int BYTES, int NT>
-__device__ __forceinline__ void clear_no_numbers(char* tv) {
+__device__ __forceinline__ void clear_no_numbers(char* tv, int thread) {
   typedef typename Vec<T>::V4 V4;
 #pragma unroll 1
-  for (int i = threadIdx.x; i < BYTES / (int)sizeof(V4); i += NT) {
+  for (int i = thread; i < BYTES / (int)sizeof(V4); i += NT) {
     V4 x = ((V4*)tv)[i];
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = fabsf((float)x[e]) < kInf ? x[e] : (T)0.0f;
@@ -433,7 +465,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
   constexpr bool kExact = sizeof(T) == 4;  // scores in natural units, as in k_attend
   constexpr bool AHEAD = WK == 1 && TL::RB == 128;
   static_assert(WK == 1 || (WQ == 1 && NB == 1), "few rows: one tile of 32, a wave's own 32 keys");
-  using KeyT = PageTiles<T, DP, KT, NT, D, (WK > 1)>;
+  using KeyT = PageTiles<T, DP, KT, NT, D, (WK > 1)>;  // few rows: a wave loads the keys that it computes on
   constexpr int kJoinBytes = WK > 1 ? WK * 32 * W * 4 : 0;
   union Memory {
     typename KeyT::Shared keys;
@@ -527,21 +559,30 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
     const int j0 = __builtin_amdgcn_readfirstlane(keys.key(it) + kb0);
     const char* const tk = keys.ktile(it);
     char* const tv = keys.vtile(it);
-    // does every row of the workgroup see every key? If not, are there values that are no numbers?
+    // does every row that computes on these values see every key? If not, are there any
+    // that are no numbers? With many rows the workgroup looks together.
     bool odd = false;
-    const int t0 = j0 - kb0;
-    if (t0 + KT > b_lo || (t0 < b_hi && t0 + KT > G.first)) {
-      if (no_numbers<T, KeyT::kTileBytes, NT>(tv)) sm.keys.odd = it + 1;
-      __syncthreads();
-      odd = __builtin_amdgcn_readfirstlane(sm.keys.odd) == it + 1;
+    if constexpr (WK > 1) {
+      if (j0 + KW > e_lo || (j0 < f_hi && j0 + KW > G.first))
+        odd = __any(no_numbers<T, KW * TL::RB, 64>(tv + kb0 * TL::RB, lane));
+    } else {
+      if (j0 + KT > b_lo || (j0 < b_hi && j0 + KT > G.first)) {
+        if (no_numbers<T, KeyT::kTileBytes, NT>(tv, tid)) sm.keys.odd = it + 1;
+        __syncthreads();
+        odd = __builtin_amdgcn_readfirstlane(sm.keys.odd) == it + 1;
+      }
     }
     auto clear = [&] {
-      __syncthreads();
-      clear_no_numbers<T, KeyT::kTileBytes, NT>(tv);
-      __syncthreads();
+      if constexpr (WK > 1) {
+        clear_no_numbers<T, KW * TL::RB, 64>(tv + kb0 * TL::RB, lane);
+      } else {
+        __syncthreads();
+        clear_no_numbers<T, KeyT::kTileBytes, NT>(tv, tid);
+        __syncthreads();
+      }
     };
     if (j0 >= e_hi || (j0 + KW <= f_lo && j0 >= G.first)) {  // no row of this wave sees any
-      if (odd) clear();
+      if (WK == 1 && odd) clear();
       continue;
     }
     f32x16 sc[NB];

@@ -13,6 +13,8 @@
 // Bound by memory: each element is read once and written once.
 #pragma once
 
+#include <algorithm>
+
 #include "attention.h"
 #include "attention_host.h"
 #include "pages.h"
@@ -20,21 +22,22 @@
 namespace sk {
 namespace attn {
 
-// The heads of one tensor.
+// The heads of one tensor: q, k, or v, which is appended as it is.
 struct HeadRows {
   const void* src;
   void* dst;
-  const void* weight;  // of the norm, nullable
-  int64_t ss[3], ds[3];  // elements: batch, row, head; ds of a cache: page, slot, head
+  const void* weight;    // of the norm, nullable
+  const void* dy;        // backward: gradient of the result
+  int64_t ss[3], ds[3], ys[3];  // elements: batch, row, head; ds of a cache: page, slot, head
   int32_t heads;
+  int32_t groups;  // log2 of the lane groups that share a token's heads
+  int32_t end;     // its workgroups end here (and start where the tensor's before it end)
 };
 
 struct RotateArgs {
-  HeadRows q, k, v;  // v: appended as it is
+  HeadRows part[3];  // q, k, v
   int32_t batch, len, d, dv;
   int32_t steps;   // rows of a batch entry that are visited: len, at least one where lengths are written
-  int32_t heads;   // of q, k and v
-  int32_t groups;  // log2 of the lane groups that share a token's heads
   int32_t half;    // pairs of a head
   bool interleaved, norm, weight_f32;
   float gain, sign, eps, inv_d;  // sign: -1 turns back; 1 / d
@@ -44,11 +47,7 @@ struct RotateArgs {
   const int32_t* lengths;  // nullable
   Paging P;
   int32_t* lengths_out;  // null: no cache
-  // backward
-  const void* dq_out;
-  const void* dk_out;
-  int64_t dqs[3], dks[3];  // of dq_out and dk_out
-  float* part;             // [workgroups][2][128] partial sums of the weights' gradients
+  float* sums;           // backward: [workgroups][128] partial sums of the weights' gradients
 };
 
 // E elements as they lie in memory.
@@ -196,83 +195,76 @@ __device__ __forceinline__ float inverse_rms(const RotateArgs& A, float sum) {
 }
 
 // Forward (and the backward pass without a norm: the rotation the other way). A
-// token's heads are dealt to 1 << A.groups lane groups, neighbours to neighbours.
-// U heads of a group are loaded before the first is used.
+// workgroup takes one of the tensors; a token's heads are dealt to 1 << groups lane
+// groups, neighbours to neighbours, and U heads of a group are loaded before the
+// first is used.
 template <class T, int E, int LPH, int U>
 __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
   typedef typename Raw<T, E>::V V;
+  const int which = (int)blockIdx.x < A.part[0].end ? 0 : ((int)blockIdx.x < A.part[1].end ? 1 : 2);
+  const HeadRows& R = A.part[which];
+  const bool value = which == 2, cache = A.lengths_out && which != 0;
   const int lane = threadIdx.x % LPH;
-  const int64_t item = (int64_t)blockIdx.x * (256 / LPH) + threadIdx.x / LPH;
-  const int64_t token = item >> A.groups;
-  const int g = (int)(item & ((1 << A.groups) - 1));
+  const int64_t item = (int64_t)(blockIdx.x - (which ? A.part[which - 1].end : 0)) * (256 / LPH) + threadIdx.x / LPH;
+  const int64_t token = item >> R.groups;
+  const int g = (int)(item & ((1 << R.groups) - 1));
   if (token >= (int64_t)A.batch * A.steps) return;
   const int b = (int)((uint32_t)token / (uint32_t)A.steps), i = (int)((uint32_t)token - (uint32_t)b * (uint32_t)A.steps);
   const int ntokens = live_tokens(A, b);
   const bool live = i < ntokens;
-  const Lane<E> lt(lane, A.half, A.interleaved, A.d), lv(lane, 0, false, A.dv);
-  // where the token's key and value go
-  int64_t kto, vto = 0;
+  const Lane<E> l(lane, value ? 0 : A.half, A.interleaved, value ? A.dv : A.d);
   int place = i;
-  bool keys = true;
+  int64_t to = b * R.ds[0] + i * R.ds[1];
   if (A.lengths_out) {
     const int before = paged_keys(A.P, b);
     const int64_t j = (int64_t)before + i, cap = (int64_t)A.P.len * A.P.size;
-    if (i == 0 && g == 0 && lane == 0) A.lengths_out[b] = (int)(before + ntokens < cap ? before + ntokens : cap);
-    if (i >= A.len) return;  // no rows at all
-    keys = live && j < cap;
+    if (which == 1 && i == 0 && g == 0 && lane == 0) A.lengths_out[b] = (int)(before + ntokens < cap ? before + ntokens : cap);
     place = (int)j;
-    kto = 0;
-    if (keys) {
+    if (cache) {
+      if (!live || j >= cap) return;
       const uint32_t page = page_of(A.P, (uint32_t)j);
       const int64_t id = A.P.table[b * A.P.stride + page];
-      keys = id >= 0 && id < A.P.pages;
-      const int64_t slot = j - (int64_t)page * A.P.size;
-      kto = id * A.k.ds[0] + slot * A.k.ds[1];
-      vto = id * A.v.ds[0] + slot * A.v.ds[1];
+      if (id < 0 || id >= A.P.pages) return;
+      to = id * R.ds[0] + (j - (int64_t)page * A.P.size) * R.ds[1];
+    } else if (i >= A.len) {
+      return;  // no rows at all
     }
-  } else {
-    kto = b * A.k.ds[0] + i * A.k.ds[1];
   }
-  const int64_t qto = b * A.q.ds[0] + i * A.q.ds[1];
   float c[E], s[E];
-  {
+  if (l.turns) {
     double w[E];
-    lane_frequencies<E>(A, lt, lane, w);
+    lane_frequencies<E>(A, l, lane, w);
     if (A.positions) place = A.positions[b * A.position_stride + i];
-    lane_angles<E>(A, lt, w, place, c, s);
+    lane_angles<E>(A, l, w, place, c, s);
   }
-  float wq[2][E], wk[2][E];
-  if (A.norm)
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      lane_weight<T, E>(A, A.q.weight, lt, n, wq[n]);
-      lane_weight<T, E>(A, A.k.weight, lt, n, wk[n]);
-    }
-  const T* const qsrc = (const T*)A.q.src + b * A.q.ss[0] + i * A.q.ss[1];
-  const T* const ksrc = (const T*)A.k.src + b * A.k.ss[0] + i * A.k.ss[1];
-  const T* const vsrc = (const T*)A.v.src + b * A.v.ss[0] + i * A.v.ss[1];
-  const int hk = A.q.heads, hv = A.q.heads + A.k.heads;
-  for (int h0 = g; h0 < A.heads; h0 += U << A.groups) {
+  const bool norm = A.norm && !value;
+  float weight[2][E];
+  if (norm) {
+    lane_weight<T, E>(A, R.weight, l, 0, weight[0]);
+    lane_weight<T, E>(A, R.weight, l, 1, weight[1]);
+  }
+  const bool changed = live && (norm || l.turns);  // else as it is: values, zeros, the rest of a head
+  const T* const src = (const T*)R.src + b * R.ss[0] + i * R.ss[1];
+  T* const dst = (T*)R.dst + to;
+  for (int h0 = g; h0 < R.heads; h0 += U << R.groups) {
     V raw[U][2];
 #pragma unroll
     for (int n = 0; n < U; ++n) {
-      const int h = h0 + (n << A.groups);
-      const bool isq = h < hk, isv = h >= hv, ok = live && h < A.heads && (isq || keys);
-      const T* from = isq ? qsrc + h * A.q.ss[2] : (isv ? vsrc + (h - hv) * A.v.ss[2] : ksrc + (h - hk) * A.k.ss[2]);
+      const int h = h0 + (n << R.groups);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         raw[n][k] = V{};
-        if (ok && (isv ? lv.has[k] : lt.has[k])) raw[n][k] = *(const V*)(from + (isv ? lv.at[k] : lt.at[k]));
+        if (live && h < R.heads && l.has[k]) raw[n][k] = *(const V*)(src + h * R.ss[2] + l.at[k]);
       }
     }
 #pragma unroll
     for (int n = 0; n < U; ++n) {
-      const int h = h0 + (n << A.groups);
-      const bool isq = h < hk, isv = h >= hv, ok = h < A.heads && (isq || keys);
+      const int h = h0 + (n << R.groups);
+      if (h >= R.heads) break;
       float x[2][E];
       widen<T, E>(raw[n][0], x[0]);
       widen<T, E>(raw[n][1], x[1]);
-      if (A.norm) {
+      if (norm) {
         float sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -282,72 +274,72 @@ __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int e = 0; e < E; ++e) x[k][e] = x[k][e] * r * (isq ? wq[k][e] : wk[k][e]);
+          for (int e = 0; e < E; ++e) x[k][e] = x[k][e] * r * weight[k][e];
       }
-      if (lt.turns) turn<E>(x[0], x[1], c, s, A.interleaved);
-      T* to = isq ? (T*)A.q.dst + qto + h * A.q.ds[2]
-                  : (isv ? (T*)A.v.dst + vto + (h - hv) * A.v.ds[2] : (T*)A.k.dst + kto + (h - hk) * A.k.ds[2]);
-      const bool changed = !isv && live && (A.norm || lt.turns);  // else as it is: values, zeros, the rest of a head
+      if (l.turns) turn<E>(x[0], x[1], c, s, A.interleaved);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (ok && (isv ? lv.has[k] : lt.has[k]))
-          *(V*)(to + (isv ? lv.at[k] : lt.at[k])) = changed ? narrow<T, E>(x[k]) : raw[n][k];
+        if (l.has[k]) *(V*)(dst + h * R.ds[2] + l.at[k]) = changed ? narrow<T, E>(x[k]) : raw[n][k];
     }
   }
 }
 
 // Backward with a norm: with g = the rotation undone on the result's gradient,
 // xh = x r, r = 1 / rms, u = g w:  dx = r (u - xh mean(u xh)),  dw = sum g xh.
-// A lane adds up the weights' gradients of its chunks over all rows that it meets;
-// groups of a wave, waves and workgroups are then added in a fixed order.
-template <class T, int E, int LPH>
+// A workgroup takes rows of one tensor; a lane adds up the weight's gradient of its
+// chunks over all that it meets; groups of a wave, waves and workgroups are then added
+// in a fixed order.
+template <class T, int E, int LPH, int U>
 __global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
   typedef typename Raw<T, E>::V V;
-  __shared__ float sw[4][2][kMaxD];
+  __shared__ float sw[4][kMaxD];
+  const int which = (int)blockIdx.x < A.part[0].end ? 0 : 1, first = which ? A.part[0].end : 0;
+  const HeadRows& R = A.part[which];
   const int lane = threadIdx.x % LPH, wave = threadIdx.x >> 6;
   const Lane<E> l(lane, A.half, A.interleaved, A.d);
   double w[E];
   lane_frequencies<E>(A, l, lane, w);
-  float acc[2][2][E], weight[2][2][E];
+  float acc[2][E], weight[2][E];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    lane_weight<T, E>(A, A.q.weight, l, k, weight[0][k]);
-    lane_weight<T, E>(A, A.k.weight, l, k, weight[1][k]);
+    lane_weight<T, E>(A, R.weight, l, k, weight[k]);
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[p][k][e] = 0.0f;
+    for (int e = 0; e < E; ++e) acc[k][e] = 0.0f;
   }
-  const int64_t items = ((int64_t)A.batch * A.len) << A.groups, step = (int64_t)gridDim.x * (256 / LPH);
-  for (int64_t item = (int64_t)blockIdx.x * (256 / LPH) + threadIdx.x / LPH; item < items; item += step) {
-    const uint32_t token = (uint32_t)(item >> A.groups);
-    const int g = (int)(item & ((1 << A.groups) - 1));
+  const int64_t items = ((int64_t)A.batch * A.len) << R.groups, step = (int64_t)(R.end - first) * (256 / LPH);
+  for (int64_t item = (int64_t)(blockIdx.x - first) * (256 / LPH) + threadIdx.x / LPH; item < items; item += step) {
+    const uint32_t token = (uint32_t)(item >> R.groups);
+    const int g = (int)(item & ((1 << R.groups) - 1));
     const int b = (int)(token / (uint32_t)A.len), i = (int)(token - (uint32_t)b * (uint32_t)A.len);
     const bool live = i < live_tokens(A, b);
+    const T* const src = (const T*)R.src + b * R.ss[0] + i * R.ss[1];
+    const T* const dy = (const T*)R.dy + b * R.ys[0] + i * R.ys[1];
+    T* const dst = (T*)R.dst + b * R.ds[0] + i * R.ds[1];
     float c[E], s[E];
     lane_angles<E>(A, l, w, A.positions ? A.positions[b * A.position_stride + i] : i, c, s);
+    for (int h0 = g; h0 < R.heads; h0 += U << R.groups) {
+      V rx[U][2], ry[U][2];
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const HeadRows& R = p == 0 ? A.q : A.k;
-      const int64_t* ys = p == 0 ? A.dqs : A.dks;
-      const T* const src = (const T*)R.src + b * R.ss[0] + i * R.ss[1];
-      const T* const dy = (const T*)(p == 0 ? A.dq_out : A.dk_out) + b * ys[0] + i * ys[1];
-      T* const dst = (T*)R.dst + b * R.ds[0] + i * R.ds[1];
-      for (int h = g; h < R.heads; h += 1 << A.groups) {
-        V rx[2], ry[2];
+      for (int n = 0; n < U; ++n) {
+        const int h = h0 + (n << R.groups);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          rx[k] = ry[k] = V{};
-          if (live && l.has[k]) {
-            rx[k] = *(const V*)(src + h * R.ss[2] + l.at[k]);
-            ry[k] = *(const V*)(dy + h * ys[2] + l.at[k]);
+          rx[n][k] = ry[n][k] = V{};
+          if (live && h < R.heads && l.has[k]) {
+            rx[n][k] = *(const V*)(src + h * R.ss[2] + l.at[k]);
+            ry[n][k] = *(const V*)(dy + h * R.ys[2] + l.at[k]);
           }
         }
+      }
+#pragma unroll
+      for (int n = 0; n < U; ++n) {
+        const int h = h0 + (n << R.groups);
+        if (h >= R.heads) break;
         float x[2][E], y[2][E];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          widen<T, E>(rx[k], x[k]);
-          widen<T, E>(ry[k], y[k]);
+          widen<T, E>(rx[n][k], x[k]);
+          widen<T, E>(ry[n][k], y[k]);
         }
         if (l.turns) turn<E>(y[0], y[1], c, s, A.interleaved);
         float sum = 0.0f, dot = 0.0f;
@@ -356,7 +348,7 @@ __global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             sum = fmaf(x[k][e], x[k][e], sum);
-            dot = fmaf(y[k][e] * weight[p][k][e], x[k][e], dot);
+            dot = fmaf(y[k][e] * weight[k][e], x[k][e], dot);
           }
         const float r = inverse_rms<T>(A, group_sum<LPH>(sum));
         const float m = group_sum<LPH>(dot) * A.inv_d * r * r;
@@ -364,8 +356,8 @@ __global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            if (live) acc[p][k][e] = fmaf(y[k][e], x[k][e] * r, acc[p][k][e]);
-            x[k][e] = live ? r * fmaf(-m, x[k][e], y[k][e] * weight[p][k][e]) : 0.0f;
+            if (live) acc[k][e] = fmaf(y[k][e], x[k][e] * r, acc[k][e]);
+            x[k][e] = live ? r * fmaf(-m, x[k][e], y[k][e] * weight[k][e]) : 0.0f;
           }
           if (l.has[k]) *(V*)(dst + h * R.ds[2] + l.at[k]) = narrow<T, E>(x[k]);
         }
@@ -373,20 +365,17 @@ __global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
     }
   }
 #pragma unroll
-  for (int p = 0; p < 2; ++p)
+  for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int e = 0; e < E; ++e) {
+      float x = acc[k][e];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float x = acc[p][k][e];
-#pragma unroll
-        for (int z = LPH; z < 64; z <<= 1) x += __shfl_xor(x, z, 64);
-        if ((threadIdx.x & 63) < LPH && l.has[k]) sw[wave][p][l.at[k] + e] = x;
-      }
+      for (int z = LPH; z < 64; z <<= 1) x += __shfl_xor(x, z, 64);
+      if ((threadIdx.x & 63) < LPH && l.has[k]) sw[wave][l.at[k] + e] = x;
+    }
   __syncthreads();
-  const int p = threadIdx.x >> 7, col = threadIdx.x & 127;
-  if (col < A.d)
-    A.part[((int64_t)blockIdx.x * 2 + p) * kMaxD + col] = (sw[0][p][col] + sw[1][p][col]) + (sw[2][p][col] + sw[3][p][col]);
+  const int col = threadIdx.x;
+  if (col < A.d) A.sums[(int64_t)blockIdx.x * kMaxD + col] = (sw[0][col] + sw[1][col]) + (sw[2][col] + sw[3][col]);
 }
 
 // ---------------------------------------------------------------- launches
@@ -408,11 +397,11 @@ void by_chunk(int e, int width, F&& f) {
     go(integral_constant<int, 1>{}, integral_constant<int, 64>{});
 }
 
-// Lane groups of a token (log2): few tokens spread over the chip, many share their
-// angles among heads.
+// Lane groups of a token (log2): of few tokens every head has its own; of many, four
+// heads share their token's angles.
 inline int32_t rotate_groups(int64_t tokens, int32_t heads, int32_t lanes) {
   int32_t g = 0;
-  while ((1 << g) < 64 / lanes && (1 << g) < heads) ++g;
+  while ((1 << g) < (heads + 3) / 4) ++g;
   while ((1 << g) < heads && (tokens << g) * lanes < (int64_t)256 * 1024) ++g;
   return g;
 }
@@ -423,19 +412,31 @@ void rotate(RotateArgs& A, int e, hipStream_t st) {
   by_chunk<T>(e, A.d > A.dv ? A.d : A.dv, [&](auto chunk, auto lanes) {
     constexpr int E = decltype(chunk)::value, L = decltype(lanes)::value;
     const int64_t tokens = (int64_t)A.batch * A.steps;
-    A.groups = rotate_groups(tokens, A.heads, L);
-    const int64_t blocks = ceil_div((tokens << A.groups) * L, 256);
-    hipLaunchKernelGGL((k_rotate<T, E, L, 2>), grid1(blocks, 256), dim3(256), 0, st, A);
+    int64_t blocks = 0;
+    for (HeadRows& R : A.part) {
+      if (R.heads > 0) {
+        R.groups = rotate_groups(tokens, R.heads, L);
+        blocks += ceil_div((tokens << R.groups) * L, 256);
+      }
+      R.end = (int32_t)std::min<int64_t>(blocks, INT32_MAX);
+    }
+    hipLaunchKernelGGL((k_rotate<T, E, L, 4>), grid1(blocks, 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   });
 }
 
+// blocks: workgroups for both tensors, dealt by their heads.
 template <class T>
-void rotate_grad(RotateArgs& A, int e, int blocks, hipStream_t st) {
+void rotate_grad(RotateArgs& A, int e, int32_t blocks, hipStream_t st) {
   by_chunk<T>(e, A.d, [&](auto chunk, auto lanes) {
     constexpr int E = decltype(chunk)::value, L = decltype(lanes)::value;
-    A.groups = rotate_groups((int64_t)A.batch * A.len, A.heads, L);
-    hipLaunchKernelGGL((k_rotate_grad<T, E, L>), grid1(blocks, 256), dim3(256), 0, st, A);
+    HeadRows &q = A.part[0], &k = A.part[1];
+    for (HeadRows* R : {&q, &k}) R->groups = rotate_groups((int64_t)A.batch * A.len, R->heads, L);
+    q.end = (int32_t)((int64_t)blocks * q.heads / (q.heads + k.heads));
+    if (q.heads > 0 && q.end == 0) q.end = 1;
+    if (k.heads > 0 && q.end == blocks) --q.end;
+    k.end = blocks;
+    hipLaunchKernelGGL((k_rotate_grad<T, E, L, 2>), grid1(blocks, 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   });
 }

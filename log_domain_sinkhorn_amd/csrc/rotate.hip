@@ -13,28 +13,33 @@ namespace attn {
 extern template void rotate<__bf16>(RotateArgs&, int, hipStream_t);
 extern template void rotate<_Float16>(RotateArgs&, int, hipStream_t);
 extern template void rotate<float>(RotateArgs&, int, hipStream_t);
-extern template void rotate_grad<__bf16>(RotateArgs&, int, int, hipStream_t);
+extern template void rotate_grad<__bf16>(RotateArgs&, int, int32_t, hipStream_t);
 extern template void rotate_grad<_Float16>(RotateArgs&, int, int, hipStream_t);
 extern template void rotate_grad<float>(RotateArgs&, int, int, hipStream_t);
 
 namespace {
 
-// The weights' gradients from `blocks` partial sums: 16 columns of one tensor a
-// workgroup, 16 threads a column.
-__global__ __launch_bounds__(256) void k_weight_join(const float* part, int blocks, int d, float* dq, float* dk) {
-  __shared__ float s[16][17];
-  const int c = threadIdx.x & 15, r = threadIdx.x >> 4, p = blockIdx.x & 1, col = (blockIdx.x >> 1) * 16 + c;
-  float* const out = p ? dk : dq;
+// The weights' gradients from the workgroups' sums: one workgroup per tensor and four
+// columns, thread t adding up rows t, t + 256, ...; then a tree over the threads.
+__global__ __launch_bounds__(256) void k_weight_join(RotateArgs A, float* dq, float* dk) {
+  __shared__ f32x4 s[256];
+  const int which = blockIdx.x & 1, col = 4 * (blockIdx.x >> 1), tid = threadIdx.x;
+  float* const out = which ? dk : dq;
   if (!out) return;
-  float x = 0.0f;
-  if (col < d)
-    for (int n = r; n < blocks; n += 16) x += part[((int64_t)n * 2 + p) * kMaxD + col];
-  s[r][c] = x;
-  __syncthreads();
-  if (r != 0 || col >= d) return;
+  f32x4 x = {0, 0, 0, 0};
+  for (int n = (which ? A.part[0].end : 0) + tid; n < A.part[which].end; n += 256) {
+    const f32x4 y = *(const f32x4*)(A.sums + (int64_t)n * kMaxD + col);
 #pragma unroll
-  for (int n = 1; n < 16; ++n) x += s[n][c];
-  out[col] = x;
+    for (int e = 0; e < 4; ++e) x[e] += y[e];
+  }
+  s[tid] = x;
+  for (int k = 128; k > 0; k >>= 1) {
+    __syncthreads();
+    if (tid < k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[tid][e] += s[tid + k][e];
+  }
+  if (tid < 4 && col + tid < A.d) out[col + tid] = s[0][tid];
 }
 
 int64_t elem_size(int32_t dtype) { return dtype == SINKHORN_F32 ? 4 : 2; }
@@ -104,7 +109,6 @@ RotateArgs arguments(const sinkhorn_rotation* r) {
   A.batch = r->batch;
   A.len = A.steps = (int32_t)r->len;
   A.d = r->d;
-  A.heads = r->heads_q + r->heads_kv;
   A.half = r->rotated / 2;
   A.interleaved = r->interleaved != 0;
   A.norm = r->norm != 0;
@@ -129,13 +133,13 @@ void run(const sinkhorn_rotation* r, RotateArgs& A, int e, hipStream_t st) {
     rotate<float>(A, e, st);
 }
 
-// Workgroups of the backward pass with a norm: four a compute unit, at most one
-// for 8 tokens.
-int grad_blocks(const sinkhorn_rotation* r) {
-  const int64_t n = ceil_div(r->batch * r->len, 8);
-  return (int)(n < 1 ? 1 : (n > 1024 ? 1024 : n));
+// Workgroups of the backward pass with a norm: four a compute unit, fewer where a
+// wave would not find four heads; two at least, one for each tensor.
+int32_t grad_blocks(const sinkhorn_rotation* r) {
+  const int64_t n = ceil_div(r->batch * r->len * (r->heads_q + r->heads_kv), 16);
+  return (int32_t)(n < 2 ? 2 : (n > 1024 ? 1024 : n));
 }
-int64_t grad_space(const sinkhorn_rotation* r) { return r->norm ? (int64_t)grad_blocks(r) * 2 * kMaxD * 4 : 0; }
+int64_t grad_space(const sinkhorn_rotation* r) { return r->norm ? (int64_t)grad_blocks(r) * kMaxD * 4 : 0; }
 
 }  // namespace
 }  // namespace attn
@@ -181,8 +185,8 @@ int sinkhorn_rotate_heads(const sinkhorn_rotation* r, const void* q, const void*
                        weight_of(r, k_weight), positions_of(r), per_entry(r, r->lengths), frequencies_of(r)}),
             "an output overlaps another argument");
     RotateArgs A = arguments(r);
-    set(A.q, q, r->q_stride, q_out, r->q_out_stride, q_weight, r->heads_q);
-    set(A.k, k, r->k_stride, k_out, r->k_out_stride, k_weight, r->heads_kv);
+    set(A.part[0], q, r->q_stride, q_out, r->q_out_stride, q_weight, r->heads_q);
+    set(A.part[1], k, r->k_stride, k_out, r->k_out_stride, k_weight, r->heads_kv);
     Unit u(r);
     if (r->heads_q) u.fit(q, r->q_stride, r->d), u.fit(q_out, r->q_out_stride, r->d);
     if (r->heads_kv) u.fit(k, r->k_stride, r->d), u.fit(k_out, r->k_out_stride, r->d);
@@ -232,23 +236,23 @@ int sinkhorn_rotate_heads_grad(const sinkhorn_rotation* r, const void* dq_out, c
     if (r->heads_q) u.fit(dq_out, r->q_out_stride, r->d), u.fit(dq, r->dq_stride, r->d);
     if (r->heads_kv) u.fit(dk_out, r->k_out_stride, r->d), u.fit(dk, r->dk_stride, r->d);
     if (!r->norm) {
-      set(A.q, dq_out, r->q_out_stride, dq, r->dq_stride, nullptr, r->heads_q);
-      set(A.k, dk_out, r->k_out_stride, dk, r->dk_stride, nullptr, r->heads_kv);
+      set(A.part[0], dq_out, r->q_out_stride, dq, r->dq_stride, nullptr, r->heads_q);
+      set(A.part[1], dk_out, r->k_out_stride, dk, r->dk_stride, nullptr, r->heads_kv);
       run(r, A, u.e, st);
       return SINKHORN_OK;
     }
     if (r->heads_q) u.fit(q, r->q_stride, r->d);
     if (r->heads_kv) u.fit(k, r->k_stride, r->d);
-    set(A.q, q, r->q_stride, dq, r->dq_stride, q_weight, r->heads_q);
-    set(A.k, k, r->k_stride, dk, r->dk_stride, k_weight, r->heads_kv);
-    A.dq_out = dq_out;
-    A.dk_out = dk_out;
+    set(A.part[0], q, r->q_stride, dq, r->dq_stride, q_weight, r->heads_q);
+    set(A.part[1], k, r->k_stride, dk, r->dk_stride, k_weight, r->heads_kv);
+    A.part[0].dy = dq_out;
+    A.part[1].dy = dk_out;
     for (int i = 0; i < 3; ++i) {
-      A.dqs[i] = r->q_out_stride[i];
-      A.dks[i] = r->k_out_stride[i];
+      A.part[0].ys[i] = r->q_out_stride[i];
+      A.part[1].ys[i] = r->k_out_stride[i];
     }
-    A.part = (float*)workspace;
-    const int blocks = grad_blocks(r);
+    A.sums = (float*)workspace;
+    const int32_t blocks = grad_blocks(r);
     if (r->dtype == SINKHORN_BF16)
       rotate_grad<__bf16>(A, u.e, blocks, st);
     else if (r->dtype == SINKHORN_F16)
@@ -256,8 +260,7 @@ int sinkhorn_rotate_heads_grad(const sinkhorn_rotation* r, const void* dq_out, c
     else
       rotate_grad<float>(A, u.e, blocks, st);
     if (dq_weight || dk_weight) {
-      hipLaunchKernelGGL(k_weight_join, grid1(2 * ceil_div(r->d, 16), 256), dim3(256), 0, st, A.part, blocks, r->d, dq_weight,
-                         dk_weight);
+      hipLaunchKernelGGL(k_weight_join, grid1(2 * ceil_div(r->d, 4), 256), dim3(256), 0, st, A, dq_weight, dk_weight);
       SK_LAUNCH_CHECK();
     }
     return SINKHORN_OK;
@@ -288,10 +291,9 @@ int sinkhorn_cache_append(const sinkhorn_rotation* r, const sinkhorn_pages* c, c
                        Span(c->page_table, table, r->batch, 1, 1, c->table_len, 4), per_entry(r, c->lengths)}),
             "an output overlaps another argument");
     RotateArgs A = arguments(r);
-    set(A.q, q, r->q_stride, q_out, r->q_out_stride, q_weight, r->heads_q);
-    set(A.k, k, r->k_stride, k_cache, c->k_stride, k_weight, r->heads_kv);
-    set(A.v, v, v_stride, v_cache, c->v_stride, nullptr, r->heads_kv);
-    A.heads += r->heads_kv;
+    set(A.part[0], q, r->q_stride, q_out, r->q_out_stride, q_weight, r->heads_q);
+    set(A.part[1], k, r->k_stride, k_cache, c->k_stride, k_weight, r->heads_kv);
+    set(A.part[2], v, v_stride, v_cache, c->v_stride, nullptr, r->heads_kv);
     A.dv = c->dv;
     A.steps = rows ? A.len : 1;
     A.P = paging(c);

@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from dataclasses import dataclass
 
 import torch  # loads the HIP runtime the library links against
@@ -240,6 +241,17 @@ class _PagesC(ctypes.Structure):
         ("lengths", _p),
     ]
 
+
+def _packer(cls):
+    """pack(*values) -> the bytes of a `cls`, arrays as their elements and pointers as
+    integers (a third of the time that filling the fields takes)."""
+    codes = {_i32: "i", _i64: "q", _f64: "d", _p: "P", _i64x2: "2q", _i64x3: "3q"}
+    s = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_) + "0q")
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_attention, _pack_rotation, _pack_pages = (_packer(c) for c in (_AttentionC, _RotationC, _PagesC))
 
 # name -> argtypes (every entry point declared in include/sinkhorn.h)
 _SIGS = {
@@ -772,24 +784,34 @@ def rotary_frequencies(rotated: int, base: float = 10000.0, *, factor: float = 1
     return torch.tensor(list(buf)[:int(rotated) // 2], dtype=torch.float64, device=device)
 
 
+_NO_STRIDES = (0, 0, 0)
+
+
+def _strides(t):
+    """Element strides of batch, length and head (0 where there is one)."""
+    s0, s1, s2, _ = t.stride()
+    shape = t.shape
+    if 1 in shape:
+        return (s0 if shape[0] > 1 else 0, s1 if shape[1] > 1 else 0, s2 if shape[2] > 1 else 0)
+    return s0, s1, s2
+
+
 def _rotation(q, k, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, lengths):
-    """The description of a call, and the tensors that it points to; q or k may be None."""
-    if q is None and k is None:
-        raise ValueError("q and k are both missing")
+    """What a call's description holds before its strides and behind them; q or k may be None."""
     one = k if q is None else q
-    B, n, _, d = one.shape
-    r = _RotationC(_ATTN_DTYPES[one.dtype], B, 0, 0, d)
-    if q is not None:
-        r.heads_q = q.shape[2]
-        r.q_stride = _strides3(q)
-    if k is not None:
-        if k.dtype != one.dtype:
-            raise TypeError(f"k must be {one.dtype}, got {k.dtype}")
-        if k.shape[0] != B or k.shape[1] != n or k.shape[3] != d:
+    dtype = one.dtype
+    B, n, heads_q, d = one.shape
+    heads_kv = 0
+    if q is None:
+        heads_q, heads_kv = 0, heads_q
+    elif k is not None:
+        if k.dtype != dtype:
+            raise TypeError(f"k must be {dtype}, got {k.dtype}")
+        kb, kn, heads_kv, kd = k.shape
+        if kb != B or kn != n or kd != d:
             raise ValueError(f"k has shape {tuple(k.shape)}, expected ({B}, {n}, heads, {d})")
-        r.heads_kv = k.shape[2]
-        r.k_stride = _strides3(k)
-    r.len = n
+    rotated = at = place = stride = norm = kind = count = 0
+    eps = 0.0
     if frequencies is not None:
         if not isinstance(frequencies, torch.Tensor) or frequencies.dtype != torch.float64:
             raise TypeError("frequencies must be a float64 tensor")
@@ -797,25 +819,22 @@ def _rotation(q, k, frequencies, interleaved, gain, norm_eps, q_weight, k_weight
             raise ValueError(f"frequencies have shape {tuple(frequencies.shape)}, expected at most ({d // 2},)")
         if not frequencies.is_contiguous():
             raise ValueError("frequencies must be contiguous")
-        r.rotated = 2 * _ungraphed(frequencies, "frequencies").shape[0]
-        r.frequencies = frequencies.data_ptr()
-        r.interleaved = bool(interleaved)
-        r.gain = float(gain)
+        rotated = 2 * _ungraphed(frequencies, "frequencies").shape[0]
+        at = frequencies.data_ptr()
     elif positions is not None:
         raise ValueError("positions need frequencies")
     if norm_eps is not None:
-        r.norm = 1
-        r.eps = float(norm_eps)
-        kind = None
+        norm, eps = 1, float(norm_eps)
+        of = None
         for w, t, name in ((q_weight, q, "q_weight"), (k_weight, k, "k_weight")):
             if w is None:
                 continue
             if t is None:
                 raise ValueError(f"{name} without its tensor")
-            if kind is None:
-                kind = w.dtype if isinstance(w, torch.Tensor) and w.dtype == one.dtype else torch.float32
-            _plain(w, name, kind, (d,))
-        r.weight_dtype = 0 if kind is None else _ATTN_DTYPES[kind]
+            if of is None:
+                of = dtype if isinstance(w, torch.Tensor) and w.dtype == dtype else torch.float32
+                kind = _ATTN_DTYPES[of]
+            _plain(w, name, of, (d,))
     elif q_weight is not None or k_weight is not None:
         raise ValueError("weights need norm_eps")
     if positions is not None:
@@ -825,11 +844,12 @@ def _rotation(q, k, frequencies, interleaved, gain, norm_eps, q_weight, k_weight
             raise ValueError(f"positions have shape {tuple(positions.shape)}, expected ({B}, {n}) or ({n},)")
         if n > 1 and positions.stride(-1) != 1:
             raise ValueError("the last dimension of positions must be contiguous")
-        r.positions = positions.data_ptr()
-        r.position_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+        place = positions.data_ptr()
+        stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
     if lengths is not None:
-        r.lengths = _plain(lengths, "lengths", torch.int32, (B,)).data_ptr()
-    return r
+        count = _plain(lengths, "lengths", torch.int32, (B,)).data_ptr()
+    head = (_ATTN_DTYPES[dtype], B, heads_q, heads_kv, d, rotated, 1 if interleaved else 0, norm, kind, n, float(gain), eps)
+    return head, (at, place, stride, count)
 
 
 def _result(t, like, name):
@@ -839,7 +859,7 @@ def _result(t, like, name):
             raise ValueError(f"{name} without its tensor")
         return None
     if t is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     return _written(_head_tensor(t, name, like.dtype, like.shape), name)
 
 
@@ -857,14 +877,13 @@ def rotate_heads(q, k=None, *, positions=None, frequencies=None, interleaved=Fal
     _head_tensor(q, "q")
     if k is not None:
         _head_tensor(k, "k")
-    r = _rotation(q, k, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, lengths)
+    head, tail = _rotation(q, k, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, lengths)
     q_out, k_out = _result(q_out, q, "q_out"), _result(k_out, k, "k_out")
     index = _same_device(q, (k, frequencies, q_weight, k_weight, positions, lengths, q_out, k_out))
-    r.q_out_stride = _strides3(q_out)
-    if k is not None:
-        r.k_out_stride = _strides3(k_out)
-    _launch(index, "rotate_heads", lib().sinkhorn_rotate_heads, ctypes.byref(r), q.data_ptr(), _at(k), _at(q_weight),
-            _at(k_weight), q_out.data_ptr(), _at(k_out))
+    ks, ko = (_NO_STRIDES, _NO_STRIDES) if k is None else (_strides(k), _strides(k_out))
+    r = _pack_rotation(*head, *_strides(q), *ks, *_strides(q_out), *ko, *_NO_STRIDES, *_NO_STRIDES, *tail)
+    _launch(index, "rotate_heads", lib().sinkhorn_rotate_heads, r, q.data_ptr(), _at(k), _at(q_weight), _at(k_weight),
+            q_out.data_ptr(), _at(k_out))
     return q_out, k_out
 
 
@@ -878,57 +897,56 @@ def rotate_heads_grad(dq_out, dk_out=None, q=None, k=None, *, positions=None, fr
     _head_tensor(dq_out, "dq_out")
     if dk_out is not None:
         _head_tensor(dk_out, "dk_out")
-    r = _rotation(dq_out, dk_out, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, lengths)
-    r.q_out_stride = r.q_stride
-    r.k_out_stride = r.k_stride
-    wq = wk = None
-    if norm_eps is not None:
+    head, tail = _rotation(dq_out, dk_out, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, lengths)
+    norm = norm_eps is not None
+    qs = ks = yk = dks = _NO_STRIDES
+    if norm:
         if q is None or (k is None) != (dk_out is None):
             raise ValueError("the gradient of a norm needs q and k")
-        _head_tensor(q, "q", dq_out.dtype, dq_out.shape)
-        r.q_stride = _strides3(q)
+        qs = _strides(_head_tensor(q, "q", dq_out.dtype, dq_out.shape))
         if k is not None:
-            _head_tensor(k, "k", dk_out.dtype, dk_out.shape)
-            r.k_stride = _strides3(k)
+            ks = _strides(_head_tensor(k, "k", dk_out.dtype, dk_out.shape))
     dq, dk = _result(dq, dq_out, "dq"), _result(dk, dk_out, "dk")
     index = _same_device(dq_out, (dk_out, q, k, frequencies, q_weight, k_weight, positions, lengths, dq, dk))
-    r.dq_stride = _strides3(dq)
     if dk is not None:
-        r.dk_stride = _strides3(dk)
-    ws, n = None, 0
-    if norm_eps is not None:
+        yk, dks = _strides(dk_out), _strides(dk)
+    r = _pack_rotation(*head, *qs, *ks, *_strides(dq_out), *yk, *_strides(dq), *dks, *tail)
+    wq = wk = ws = None
+    n = 0
+    if norm:
         device, d = dq_out.device, dq_out.shape[3]
         wq = torch.empty(d, dtype=torch.float32, device=device)
         wk = None if dk is None else torch.empty(d, dtype=torch.float32, device=device)
         size = _i64()
-        _check(lib().sinkhorn_rotation_workspace(ctypes.byref(r), ctypes.byref(size)), "rotation_workspace")
+        _check(lib().sinkhorn_rotation_workspace(r, ctypes.byref(size)), "rotation_workspace")
         n = size.value
         ws = torch.empty(n, dtype=torch.uint8, device=device)
-    _launch(index, "rotate_heads_grad", lib().sinkhorn_rotate_heads_grad, ctypes.byref(r), dq_out.data_ptr(),
-            _at(dk_out), _at(q), _at(k), _at(q_weight), _at(k_weight), dq.data_ptr(), _at(dk), _at(wq), _at(wk),
-            _at(ws), n)
+    _launch(index, "rotate_heads_grad", lib().sinkhorn_rotate_heads_grad, r, dq_out.data_ptr(), _at(dk_out), _at(q), _at(k),
+            _at(q_weight), _at(k_weight), dq.data_ptr(), _at(dk), _at(wq), _at(wk), _at(ws), n)
     return dq, dk, wq, wk
 
 
 def _pages(dtype, B, heads, d, k_cache, v_cache, page_table, lengths, name):
-    """The description of a paged cache of k [pages, page_size, heads, d] and v."""
+    """The bytes that describe a paged cache of k [pages, page_size, heads, d] and v, and v's width."""
     _head_tensor(k_cache, "k_cache", dtype)
     _head_tensor(v_cache, "v_cache", dtype)
-    pages, size, _, _ = k_cache.shape
-    dv = v_cache.shape[3]
-    if tuple(k_cache.shape) != (pages, size, heads, d):
+    pages, size, kh, kd = k_cache.shape
+    vp, vsize, vh, dv = v_cache.shape
+    if kh != heads or kd != d:
         raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected (pages, page_size, {heads}, {d})")
-    if tuple(v_cache.shape) != (pages, size, heads, dv):
+    if vp != pages or vsize != size or vh != heads:
         raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected ({pages}, {size}, {heads}, width)")
     if not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32:
         raise TypeError("page_table must be an int32 tensor")
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected ({B}, pages of a sequence)")
-    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+    row, one = page_table.stride()
+    width = page_table.shape[1]
+    if width > 1 and one != 1:
         raise ValueError("the last dimension of page_table must be contiguous")
     _plain(lengths, name, torch.int32, (B,))
-    return _PagesC(size, page_table.shape[1], pages, page_table.stride(0) if B > 1 else 0, _strides3(k_cache),
-                   _strides3(v_cache), dv, page_table.data_ptr(), lengths.data_ptr())
+    return _pack_pages(size, width, pages, row if B > 1 else 0, *_strides(k_cache), *_strides(v_cache), dv,
+                       page_table.data_ptr(), lengths.data_ptr()), dv
 
 
 def cache_append(k, v, k_cache, v_cache, page_table, cache_lengths, *, new_lengths=None, positions=None,
@@ -951,30 +969,31 @@ def cache_append(k, v, k_cache, v_cache, page_table, cache_lengths, *, new_lengt
     _head_tensor(k, "k")
     B, n, h, d = k.shape
     _head_tensor(v, "v", k.dtype)
-    if v.shape[:3] != k.shape[:3]:
+    vb, vn, vh, dv = v.shape
+    if vb != B or vn != n or vh != h:
         raise ValueError(f"v has shape {tuple(v.shape)}, expected ({B}, {n}, {h}, width)")
     if q is not None:
         _head_tensor(q, "q", k.dtype)
         if q.shape[0] != B or q.shape[1] != n or q.shape[3] != d:
             raise ValueError(f"q has shape {tuple(q.shape)}, expected ({B}, {n}, heads, {d})")
-    r = _rotation(q, k, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, new_lengths)
-    c = _pages(k.dtype, B, h, d, k_cache, v_cache, page_table, cache_lengths, "cache_lengths")
-    if v.shape[3] != c.dv:
-        raise ValueError(f"v has shape {tuple(v.shape)}, expected ({B}, {n}, {h}, {c.dv})")
+    head, tail = _rotation(q, k, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, new_lengths)
+    c, width = _pages(k.dtype, B, h, d, k_cache, v_cache, page_table, cache_lengths, "cache_lengths")
+    if dv != width:
+        raise ValueError(f"v has shape {tuple(v.shape)}, expected ({B}, {n}, {h}, {width})")
     _written(k_cache, "k_cache")
     _written(v_cache, "v_cache")
-    if lengths_out is not None:
+    if lengths_out is None:
+        lengths_out = cache_lengths.new_empty(B)
+    else:
         _plain(lengths_out, "lengths_out", torch.int32, (B,))
     q_out = _result(q_out, q, "q_out")
     index = _same_device(k, (v, q, k_cache, v_cache, page_table, cache_lengths, new_lengths, positions, frequencies,
                              k_weight, q_weight, q_out, lengths_out))
-    if q is not None:
-        r.q_out_stride = _strides3(q_out)
-    if lengths_out is None:
-        lengths_out = torch.empty(B, dtype=torch.int32, device=k.device)
-    _launch(index, "cache_append", lib().sinkhorn_cache_append, ctypes.byref(r), ctypes.byref(c), _at(q), k.data_ptr(),
-            v.data_ptr(), _strides3(v), _at(q_weight), _at(k_weight), _at(q_out), k_cache.data_ptr(),
-            v_cache.data_ptr(), lengths_out.data_ptr())
+    qs, qo = (_NO_STRIDES, _NO_STRIDES) if q is None else (_strides(q), _strides(q_out))
+    r = _pack_rotation(*head, *qs, *_strides(k), *qo, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *tail)
+    _launch(index, "cache_append", lib().sinkhorn_cache_append, r, c, _at(q), k.data_ptr(), v.data_ptr(),
+            _strides3(v), _at(q_weight), _at(k_weight), _at(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+            lengths_out.data_ptr())
     return lengths_out, q_out
 
 
@@ -998,12 +1017,8 @@ def paged_attention(q, k_cache, v_cache, page_table, key_lengths, *, scale=None,
     hkv = k_cache.shape[2]
     if hkv < 1 or hq < 1 or hq % hkv:
         raise ValueError(f"{hq} query heads are no multiple of {hkv} key heads")
-    c = _pages(q.dtype, B, hkv, d, k_cache, v_cache, page_table, key_lengths, "key_lengths")
-    shape = (B, lq, hq, c.dv)
-    a = _AttentionC(_ATTN_DTYPES[q.dtype], B, hq, hkv, d, c.dv, lq, 0,
-                    1.0 / math.sqrt(max(d, 1)) if scale is None else float(scale), _strides3(q))
-    if query_lengths is not None:
-        a.query_lengths = _plain(query_lengths, "query_lengths", torch.int32, (B,)).data_ptr()
+    c, dv = _pages(q.dtype, B, hkv, d, k_cache, v_cache, page_table, key_lengths, "key_lengths")
+    count = 0 if query_lengths is None else _plain(query_lengths, "query_lengths", torch.int32, (B,)).data_ptr()
     if recent is None:
         recent = 0
         if first:
@@ -1011,23 +1026,26 @@ def paged_attention(q, k_cache, v_cache, page_table, key_lengths, *, scale=None,
     elif recent < 1:
         raise ValueError("recent must be >= 1")
     # as large as the C side takes them: a longer one means the same
-    first, recent = (max(-1, min(int(x), (1 << 63) - 1)) for x in (first, recent))
+    first, recent = max(-1, min(int(first), (1 << 63) - 1)), min(int(recent), (1 << 63) - 1)
     if out is not None:
-        _written(_head_tensor(out, "out", q.dtype, shape), "out")
-    if lse is not None:
+        _written(_head_tensor(out, "out", q.dtype, (B, lq, hq, dv)), "out")
+    elif dv == d:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        out = q.new_empty((B, lq, hq, dv))
+    if lse is None:
+        lse = torch.empty((B, hq, lq), dtype=torch.float32, device=q.device)
+    else:
         _plain(lse, "lse", torch.float32, (B, hq, lq))
     index = _same_device(q, (k_cache, v_cache, page_table, key_lengths, query_lengths, out, lse))
-    device = q.device
-    out = torch.empty(shape, dtype=q.dtype, device=device) if out is None else out
-    lse = torch.empty((B, hq, lq), dtype=torch.float32, device=device) if lse is None else lse
-    a.out_stride = _strides3(out)
+    a = _pack_attention(_ATTN_DTYPES[q.dtype], B, hq, hkv, d, dv, lq, 0, 1.0 / math.sqrt(max(d, 1)) if scale is None else float(scale),
+                        *_strides(q), *_NO_STRIDES, *_NO_STRIDES, *_strides(out), *(_NO_STRIDES * 4), 0, 0, 0, count, 0)
     size = _i64()
-    _check(lib().sinkhorn_paged_workspace(ctypes.byref(a), ctypes.byref(c), first, recent, ctypes.byref(size)),
-           "paged_workspace")
+    _check(lib().sinkhorn_paged_workspace(a, c, first, recent, ctypes.byref(size)), "paged_workspace")
     n = size.value
-    ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
-    _launch(index, "paged_attention", lib().sinkhorn_paged_attention, ctypes.byref(a), ctypes.byref(c), first, recent,
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), _at(ws), n)
+    ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    _launch(index, "paged_attention", lib().sinkhorn_paged_attention, a, c, first, recent, q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), _at(ws), n)
     return out, lse
 
 

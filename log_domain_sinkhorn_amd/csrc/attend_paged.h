@@ -40,6 +40,8 @@ struct PagedArgs {
   AttendArgs A;  // S.k, S.v: the cache; S.ks, S.vs: page, slot, head; S.klen: P.lengths
   Paging P;
   int32_t first, recent;  // recent 0: all keys
+  int32_t rows, tiles, per;  // rows and row tiles of a pair, tiles times splits
+  Divide by_group, by_heads, by_per, by_split;
   bool qvec;              // q may be read 16 bytes a lane
 };
 
@@ -88,7 +90,7 @@ struct PageTiles {
         v((const char*)A.A.S.v + (int64_t)hk * A.A.S.vs[2] * sizeof(T)), kpage(A.A.S.ks[0] * sizeof(T)),
         vpage(A.A.S.vs[0] * sizeof(T)), kslot((uint32_t)(A.A.S.ks[1] * sizeof(T))), vslot((uint32_t)(A.A.S.vs[1] * sizeof(T))),
         table(A.P.table + b * A.P.stride), held(0), nkeys(nkeys_), n0(n0_), count(count_), ns(ns_), t_lo(t_lo_), wave(wave_),
-        lane(lane_), npages(nkeys_ > 0 ? page_of(A.P, (uint32_t)(nkeys_ - 1)) + 1 : 0), bad(0), bad_held(false) {
+        lane(lane_), npages(nkeys_ > 0 ? A.P.page((uint32_t)(nkeys_ - 1)) + 1 : 0), bad(0), bad_held(false) {
 #pragma unroll
     for (int i = 0; i < KIND; ++i) {
       const int r = i * RPI + lane / TL::CPR, c = (lane % TL::CPR) ^ TL::swz(r);
@@ -98,7 +100,7 @@ struct PageTiles {
 #pragma unroll
     for (int n = 0; n < kHeld; ++n) id[n] = -1;
     if (count > 0) {
-      hold(page_of(P, (uint32_t)key(0)));
+      hold(P.page((uint32_t)key(0)));
       locate(0);
     }
   }
@@ -124,12 +126,12 @@ struct PageTiles {
   __device__ __forceinline__ void locate(int n) {
     const int first = __builtin_amdgcn_readfirstlane(key(n));
     const int left = nkeys - first;  // keys from the tile's first on, at least one
-    const uint32_t p0 = page_of(P, (uint32_t)first), p1 = page_of(P, (uint32_t)(first + (left < KT ? left : KT) - 1));
+    const uint32_t p0 = P.page((uint32_t)first), p1 = P.page((uint32_t)(first + (left < KT ? left : KT) - 1));
     if (p0 < held || p1 >= held + 64 * kHeld) hold(p0);
     const int r = wave * RW + 8 * (lane % (RW / 8));
     const bool live = r < left;
     const uint32_t j = (uint32_t)(first + (live ? r : 0));
-    const uint32_t page = page_of(P, j), slot = j - page * (uint32_t)P.size;
+    const uint32_t page = P.page(j), slot = j - page * (uint32_t)P.size;
     const uint32_t x = page - held;
     int32_t at = 0;
 #pragma unroll
@@ -288,17 +290,16 @@ __device__ __forceinline__ void add_values(const char* tv, int kb0, int lane, co
 // keys are split. With WK > 1 the waves' parts of the keys are joined through
 // so [WK][W][32] and sml [WK][32] first.
 template <class T, int W, int WQ, int WK>
-__device__ __forceinline__ void finish_rows(const AttendArgs& A, float* so, f32x2* sml, const f32x16 (&o)[W / 32], float m,
-                                            float l, bool has, int split, int b, int hk, int64_t row0) {
+__device__ __forceinline__ void finish_rows(const PagedArgs& G, float* so, f32x2* sml, const f32x16 (&o)[W / 32], float m,
+                                            float l, bool has, int split, int b, int hk, int row0) {
   constexpr int NDB = W / 32, NT = 64 * WQ * WK;
+  const AttendArgs& A = G.A;
   const Shape& S = A.S;
-  const int64_t pairs = (int64_t)S.batch * S.hkv, pair = (int64_t)b * S.hkv + hk;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r32 = lane & 31;
   const int wq = wave % WQ, wk = wave / WQ;
-  const int64_t row = row0 + 32 * wq + r32;
-  const int64_t qi = row / S.group;
-  const int qh = hk * S.group + (int)(row - qi * S.group);
+  // partial results of this split and pair start at this row
+  const int64_t part0 = ((int64_t)split * (S.batch * S.hkv) + b * S.hkv + hk) * G.rows;
   // the row's result, column group by column group: group index c4 of four
   // columns, value x (not divided by the sum)
   const bool part = A.opart != nullptr;
@@ -311,7 +312,7 @@ __device__ __forceinline__ void finish_rows(const AttendArgs& A, float* so, f32x
       for (int e = 0; e < 16; ++e) so[(wk * W + 32 * x + 8 * (e >> 2) + 4 * h + (e & 3)) * 32 + r32] = has ? o[x][e] : 0.0f;
     __syncthreads();
     // thread: row tid % 32, column groups tid / 32, + NT / 32, ...
-    const int64_t jrow = row0 + (tid & 31);
+    const int jrow = row0 + (tid & 31);
     float f[WK], mm = -kInf, ll = 0.0f;
 #pragma unroll
     for (int w = 0; w < WK; ++w) mm = fmaxf(mm, sml[w * 32 + (tid & 31)][0]);
@@ -322,13 +323,12 @@ __device__ __forceinline__ void finish_rows(const AttendArgs& A, float* so, f32x
       f[w] = ex2(p[0] - mu);
       ll = fmaf(f[w], p[1], ll);
     }
-    if (jrow >= S.rows) return;
-    const int64_t ji = jrow / S.group;
-    const int jh = hk * S.group + (int)(jrow - ji * S.group);
+    if (jrow >= G.rows) return;
+    const int ji = (int)G.by_group((uint32_t)jrow), jh = hk * S.group + jrow - ji * S.group;
     // a NaN sum is kept; only an empty row is 0
     const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
     T* orow = (T*)A.out + b * A.os[0] + ji * A.os[1] + jh * A.os[2];
-    float* prow = part ? A.opart + (((int64_t)split * pairs + pair) * S.rows + jrow) * A.dvp : nullptr;
+    float* prow = part ? A.opart + (part0 + jrow) * A.dvp : nullptr;
 #pragma unroll
     for (int it = 0; it < (W * 8 + NT - 1) / NT; ++it) {
       const int c = 4 * ((tid >> 5) + it * (NT / 32));
@@ -351,15 +351,17 @@ __device__ __forceinline__ void finish_rows(const AttendArgs& A, float* so, f32x
     }
     if (tid < 32) {
       if (part)
-        A.mlpart[((int64_t)split * pairs + pair) * S.rows + jrow] = f32x2{mm, ll};
+        A.mlpart[part0 + jrow] = f32x2{mm, ll};
       else
         A.lse[((int64_t)b * S.hq + jh) * S.lq + ji] = log_sum(mm, ll);
     }
   } else {
-    if (row >= S.rows) return;
+    const int row = row0 + 32 * wq + r32;
+    if (row >= G.rows) return;
+    const int qi = (int)G.by_group((uint32_t)row), qh = hk * S.group + row - qi * S.group;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     T* orow = (T*)A.out + b * A.os[0] + qi * A.os[1] + qh * A.os[2];
-    const int64_t prow_i = ((int64_t)split * pairs + pair) * S.rows + row;
+    const int64_t prow_i = part0 + row;
 #pragma unroll
     for (int n = 0; n < NDB; ++n)
 #pragma unroll
@@ -476,13 +478,27 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
 
   const AttendArgs& A = G.A;
   const Shape& S = A.S;
-  const int64_t item = xcd_item((int64_t)S.batch * S.hkv, A.tiles * A.nsplit);
-  if (item < 0) return;
-  const int64_t place = item / (A.tiles * A.nsplit);
-  const int64_t rest = item - place * (A.tiles * A.nsplit);
-  const int64_t tile = A.tiles - 1 - rest / A.nsplit;  // the last rows see the most keys
-  const int split = (int)(rest % A.nsplit);
-  const int pos = (int)(place / S.hkv), hk = (int)(place - (int64_t)pos * S.hkv);
+  // workgroup -> (pair, row tile, split), as xcd_item deals them
+  const int pairs = S.batch * S.hkv;
+  int place, rest;
+  {
+    const int x = blockIdx.x & 7, i = blockIdx.x >> 3;
+    if (xcd_by_pair(pairs)) {
+      const int p = (int)G.by_per((uint32_t)i);
+      place = 8 * p + x;
+      rest = i - p * G.per;
+    } else {
+      const int run = (pairs * G.per + 7) >> 3, item = x * run + i;
+      if (i >= run) return;
+      place = (int)G.by_per((uint32_t)item);
+      rest = item - place * G.per;
+    }
+    if (place >= pairs) return;
+  }
+  int tile = (int)G.by_split((uint32_t)rest);
+  const int split = rest - tile * A.nsplit;
+  tile = G.tiles - 1 - tile;  // the last rows see the most keys
+  const int pos = (int)G.by_heads((uint32_t)place), hk = place - pos * S.hkv;
   const int b = batch_entry(S, pos);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -490,18 +506,21 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
   const int wq = wave % WQ, wk = wave / WQ;
 
   const int nkeys = __builtin_amdgcn_readfirstlane(paged_keys(G.P, b));
-  const int64_t nrows = live_rows(S, b);
-  const int64_t row0 = tile * (32 * WQ);
-  const int64_t row = row0 + 32 * wq + r32;
+  int nq = (int)S.lq;  // live queries
+  if (S.qlen) {
+    const int n = __builtin_amdgcn_readfirstlane(S.qlen[b]);
+    nq = n < 0 ? 0 : (n < nq ? n : nq);
+  }
+  const int nrows = nq * S.group;
+  const int row0 = tile * (32 * WQ), row = row0 + 32 * wq + r32;
   const bool live_row = row < nrows;
-  const int64_t qi = row / S.group;
-  const int qh = hk * S.group + (int)(row - qi * S.group);
+  const int qi = (int)G.by_group((uint32_t)row), qh = hk * S.group + row - qi * S.group;
 
-  // keys that rows r0 .. r1 (live ones) may see end at `end`, and their window starts
-  // at the earliest at `from`
-  const int base = nkeys - (int)(nrows / S.group);  // place of the entry's first row
-  auto end_of = [&](int64_t r) {
-    const int x = base + (int)(r / S.group) + 1;
+  // keys that row r (a live one) may see end at end_of(r), and its window starts at
+  // from_of(that)
+  const int base = nkeys - nq;  // place of the entry's first row
+  auto end_of = [&](int r) {
+    const int x = base + (int)G.by_group((uint32_t)r) + 1;
     return x < 0 ? 0 : x;
   };
   auto from_of = [&](int end) {
@@ -509,15 +528,15 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
     return G.recent == 0 || x < 0 ? 0 : x;
   };
   int ns = 0, t_lo = 0, total = 0;
+  const int last = row0 + 32 * WQ < nrows ? row0 + 32 * WQ - 1 : nrows - 1;
   if (row0 < nrows) {
-    const int64_t last = row0 + 32 * WQ < nrows ? row0 + 32 * WQ - 1 : nrows - 1;
-    const int end = end_of(last), t_end = (end - 1 + KT) / KT;
+    const int end = end_of(last), t_end = (end + KT - 1) / KT;
     t_lo = from_of(end_of(row0)) / KT;
     const int f = G.first < end ? G.first : end, n = f > 0 ? (f - 1) / KT + 1 : 0;
     ns = n < t_lo ? n : t_lo;
     total = ns + t_end - t_lo;
   }
-  const int per = (total + A.nsplit - 1) / A.nsplit;
+  const int per = (int)G.by_split((uint32_t)(total + A.nsplit - 1));
   const int n0 = split * per, count = total - n0 < per ? total - n0 : per;
 
   KeyT keys(sm.keys, G, b, hk, nkeys, ns, t_lo, n0, count > 0 ? count : 0, wave, lane);
@@ -547,10 +566,10 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
   // over the wave's live rows these bounds run from e_lo to e_hi and f_lo to f_hi
   // (over the workgroup's: b_lo and b_hi)
   const int end = end_of(row), from = from_of(end);
-  const int64_t w0 = row0 + 32 * wq, w1 = w0 + 31 < nrows ? w0 + 31 : nrows - 1;
+  const int w0 = row0 + 32 * wq, w1 = w0 + 31 < nrows ? w0 + 31 : nrows - 1;
   const int e_lo = end_of(w0), e_hi = w0 < nrows ? end_of(w1) : 0, f_lo = from_of(e_lo), f_hi = from_of(e_hi);
 
-  const int b_lo = end_of(row0), b_hi = from_of(end_of(row0 + 32 * WQ < nrows ? row0 + 32 * WQ - 1 : nrows - 1));
+  const int b_lo = end_of(row0), b_hi = from_of(end_of(last));
 
   if constexpr (WK == 1 && OCC == 2) one_ahead();
   for (int it = 0; it < keys.count; ++it) {
@@ -628,7 +647,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
     m = -kInf;
     l = 0.0f;
   }
-  finish_rows<T, W, WQ, WK>(A, sm.join, sml, o, m, l, live_row, split, b, hk, row0);
+  finish_rows<T, W, WQ, WK>(G, sm.join, sml, o, m, l, live_row, split, b, hk, row0);
 }
 
 // many: 128 rows per workgroup, else all rows in one tile of 32; waves and tiles as

@@ -137,6 +137,13 @@ int sinkhorn_paged_attention(const sinkhorn_attention* a, const sinkhorn_pages* 
     const int64_t most = INT32_MAX;
     G.first = (int32_t)std::min(first, most);
     G.recent = (int32_t)std::min(recent, most);
+    G.rows = (int32_t)p.rows;
+    G.tiles = (int32_t)p.tiles;
+    G.per = (int32_t)(p.tiles * p.nsplit);
+    G.by_group = Divide(A.S.group);
+    G.by_heads = Divide(A.S.hkv);
+    G.by_per = Divide(G.per);
+    G.by_split = Divide(p.nsplit);
     G.qvec = rows_aligned(q, a->q_stride, a->d, size, 16);
     const hipStream_t st = (hipStream_t)stream;
     if (a->dtype == SINKHORN_BF16)

@@ -38,6 +38,7 @@ struct RotateArgs {
   HeadRows part[3];  // q, k, v
   int32_t batch, len, d, dv;
   int32_t steps;   // rows of a batch entry that are visited: len, at least one where lengths are written
+  Divide by_steps;
   int32_t half;    // pairs of a head
   bool interleaved, norm, weight_f32;
   float gain, sign, eps, inv_d;  // sign: -1 turns back; 1 / d
@@ -209,7 +210,7 @@ __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
   const int64_t token = item >> R.groups;
   const int g = (int)(item & ((1 << R.groups) - 1));
   if (token >= (int64_t)A.batch * A.steps) return;
-  const int b = (int)((uint32_t)token / (uint32_t)A.steps), i = (int)((uint32_t)token - (uint32_t)b * (uint32_t)A.steps);
+  const int b = (int)A.by_steps((uint32_t)token), i = (int)token - b * A.steps;
   const int ntokens = live_tokens(A, b);
   const bool live = i < ntokens;
   const Lane<E> l(lane, value ? 0 : A.half, A.interleaved, value ? A.dv : A.d);
@@ -222,7 +223,7 @@ __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
     place = (int)j;
     if (cache) {
       if (!live || j >= cap) return;
-      const uint32_t page = page_of(A.P, (uint32_t)j);
+      const uint32_t page = A.P.page((uint32_t)j);
       const int64_t id = A.P.table[b * A.P.stride + page];
       if (id < 0 || id >= A.P.pages) return;
       to = id * R.ds[0] + (j - (int64_t)page * A.P.size) * R.ds[1];
@@ -310,7 +311,7 @@ __global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
   for (int64_t item = (int64_t)(blockIdx.x - first) * (256 / LPH) + threadIdx.x / LPH; item < items; item += step) {
     const uint32_t token = (uint32_t)(item >> R.groups);
     const int g = (int)(item & ((1 << R.groups) - 1));
-    const int b = (int)(token / (uint32_t)A.len), i = (int)(token - (uint32_t)b * (uint32_t)A.len);
+    const int b = (int)A.by_steps(token), i = (int)token - b * A.len;
     const bool live = i < live_tokens(A, b);
     const T* const src = (const T*)R.src + b * R.ss[0] + i * R.ss[1];
     const T* const dy = (const T*)R.dy + b * R.ys[0] + i * R.ys[1];
@@ -409,6 +410,7 @@ inline int32_t rotate_groups(int64_t tokens, int32_t heads, int32_t lanes) {
 // Instantiated once per element type (rotate_*.hip). e: elements of a chunk.
 template <class T>
 void rotate(RotateArgs& A, int e, hipStream_t st) {
+  A.by_steps = Divide(A.steps);
   by_chunk<T>(e, A.d > A.dv ? A.d : A.dv, [&](auto chunk, auto lanes) {
     constexpr int E = decltype(chunk)::value, L = decltype(lanes)::value;
     const int64_t tokens = (int64_t)A.batch * A.steps;
@@ -428,6 +430,7 @@ void rotate(RotateArgs& A, int e, hipStream_t st) {
 // blocks: workgroups for both tensors, dealt by their heads.
 template <class T>
 void rotate_grad(RotateArgs& A, int e, int32_t blocks, hipStream_t st) {
+  A.by_steps = Divide(A.len);
   by_chunk<T>(e, A.d, [&](auto chunk, auto lanes) {
     constexpr int E = decltype(chunk)::value, L = decltype(lanes)::value;
     HeadRows &q = A.part[0], &k = A.part[1];

@@ -287,11 +287,12 @@ __device__ __forceinline__ void add_values(const char* tv, int kb0, int lane, co
 
 // Writes the rows of a workgroup: o (not divided by the sum), reference m and
 // sum l of this lane's row, or zeros without `has`; as a partial result where the
-// keys are split. With WK > 1 the waves' parts of the keys are joined through
+// keys are split. With few rows the waves' parts of the keys are joined through
 // so [WK][W][32] and sml [WK][32] first.
 template <class T, int W, int WQ, int WK>
 __device__ __forceinline__ void finish_rows(const PagedArgs& G, float* so, f32x2* sml, const f32x16 (&o)[W / 32], float m,
                                             float l, bool has, int split, int b, int hk, int row0) {
+  constexpr bool MANY = WQ > 1;
   constexpr int NDB = W / 32, NT = 64 * WQ * WK;
   const AttendArgs& A = G.A;
   const Shape& S = A.S;
@@ -303,7 +304,7 @@ __device__ __forceinline__ void finish_rows(const PagedArgs& G, float* so, f32x2
   // the row's result, column group by column group: group index c4 of four
   // columns, value x (not divided by the sum)
   const bool part = A.opart != nullptr;
-  if constexpr (WK > 1) {
+  if constexpr (!MANY) {
     __syncthreads();
     if (h == 0) sml[wk * 32 + r32] = f32x2{m, l};
 #pragma unroll
@@ -458,6 +459,7 @@ __device__ __forceinline__ void add_no_numbers(const char* tv, int kb0, int lane
 template <class T, int W, int WQ, int WK, int NB, int D, int OCC>
 __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G) {
   constexpr int DP = row_width(W);
+  constexpr bool MANY = WQ > 1;
   using TL = Tile<T, DP>;
   using V8 = typename Vec<T>::V8;
   constexpr int NT = 64 * WQ * WK;
@@ -465,16 +467,16 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
   constexpr int KW = 32 * NB;       // of them a wave's own
   constexpr int NS = W / 16, NDB = W / 32;
   constexpr bool kExact = sizeof(T) == 4;  // scores in natural units, as in k_attend
-  constexpr bool AHEAD = WK == 1 && TL::RB == 128;
-  static_assert(WK == 1 || (WQ == 1 && NB == 1), "few rows: one tile of 32, a wave's own 32 keys");
-  using KeyT = PageTiles<T, DP, KT, NT, D, (WK > 1)>;  // few rows: a wave loads the keys that it computes on
-  constexpr int kJoinBytes = WK > 1 ? WK * 32 * W * 4 : 0;
+  constexpr bool AHEAD = MANY && TL::RB == 128;
+  static_assert(WQ > 1 || (WQ == 1 && NB == 1), "few rows: one tile of 32, a wave's own 32 keys");
+  using KeyT = PageTiles<T, DP, KT, NT, D, !MANY>;  // few rows: a wave loads the keys that it computes on
+  constexpr int kJoinBytes = !MANY ? WK * 32 * W * 4 : 0;
   union Memory {
     typename KeyT::Shared keys;
     float join[kJoinBytes / 4 + 1];
   };
   __shared__ Memory sm;
-  __shared__ f32x2 sml[WK > 1 ? WK * 32 : 1];
+  __shared__ f32x2 sml[MANY ? 1 : WK * 32];
 
   const AttendArgs& A = G.A;
   const Shape& S = A.S;
@@ -571,7 +573,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
 
   const int b_lo = end_of(row0), b_hi = from_of(end_of(last));
 
-  if constexpr (WK == 1 && OCC == 2) one_ahead();
+  if constexpr (MANY && OCC == 2) one_ahead();
   for (int it = 0; it < keys.count; ++it) {
     keys.next(it);
     const int kb0 = KW * wk;
@@ -581,7 +583,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
     // does every row that computes on these values see every key? If not, are there any
     // that are no numbers? With many rows the workgroup looks together.
     bool odd = false;
-    if constexpr (WK > 1) {
+    if constexpr (!MANY) {
       if (j0 + KW > e_lo || (j0 < f_hi && j0 + KW > G.first))
         odd = __any(no_numbers<T, KW * TL::RB, 64>(tv + kb0 * TL::RB, lane));
     } else {
@@ -592,7 +594,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
       }
     }
     auto clear = [&] {
-      if constexpr (WK > 1) {
+      if constexpr (!MANY) {
         clear_no_numbers<T, KW * TL::RB, 64>(tv + kb0 * TL::RB, lane);
       } else {
         __syncthreads();
@@ -601,7 +603,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
       }
     };
     if (j0 >= e_hi || (j0 + KW <= f_lo && j0 >= G.first)) {  // no row of this wave sees any
-      if (WK == 1 && odd) clear();
+      if (MANY && odd) clear();
       continue;
     }
     f32x16 sc[NB];
@@ -640,7 +642,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
       add_no_numbers<T, DP, KW>(tv, kb0, lane, o, seen);
       clear();
     }
-    add_values<T, DP, WK == 1, NB, NDB>(tv, kb0, lane, sc, o);
+    add_values<T, DP, MANY, NB, NDB>(tv, kb0, lane, sc, o);
   }
   l = half_sum(l);
   if (!live_row) {
@@ -650,8 +652,18 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
   finish_rows<T, W, WQ, WK>(G, sm.join, sml, o, m, l, live_row, split, b, hk, row0);
 }
 
-// many: 128 rows per workgroup, else all rows in one tile of 32; waves and tiles as
-// for k_attend
+// Few rows: waves of a workgroup, each with two tiles of 32 keys in LDS, one of them
+// in flight, for rows of `bytes` bytes; workgroups of a compute unit. A wave for each
+// SIMD or two, because a wave takes 1.4 us (rows of 256 bytes) for a tile that its
+// loads could bring in 1.8. Against the three waves of three tiles that k_attend
+// has there: 16 x 32768 keys x 8 heads of 128 271 -> 263 us, 8 x 4096 x 8 36 -> 27.5,
+// fp32 of 64 179 -> 145; waves of two workgroups of two: 268, 27.5, 143. Rows of 128
+// bytes, six waves of three tiles: 16 x 32768 x 8 of 64 173 -> 165 us, 4 x 1000 x 8
+// 10.7 -> 9.9; eight of two 165, 12.0.
+constexpr int paged_waves(int64_t bytes) { return bytes <= 256 ? 4 : 2; }
+constexpr int paged_groups(int64_t bytes) { return bytes <= 128 ? 2 : 1; }
+
+// many: 128 rows per workgroup, else all rows in one tile of 32
 template <class T, int W>
 void attend_paged_launch(const PagedArgs& G, bool many, hipStream_t st) {
   const int64_t blocks = xcd_blocks((int64_t)G.A.S.batch * G.A.S.hkv, G.A.tiles * G.A.nsplit);
@@ -660,8 +672,8 @@ void attend_paged_launch(const PagedArgs& G, bool many, hipStream_t st) {
   if (many)
     hipLaunchKernelGGL((k_attend_paged<T, W, 4, 1, 2, 2, OCC>), grid1(blocks, 256), dim3(256), 0, st, G);
   else
-    hipLaunchKernelGGL((k_attend_paged<T, W, 1, few_waves(RB), 1, few_depth(RB), RB == 128 ? 2 : 1>),
-                       grid1(blocks, 64 * few_waves(RB)), dim3(64 * few_waves(RB)), 0, st, G);
+    hipLaunchKernelGGL((k_attend_paged<T, W, 1, paged_waves(RB), 1, 2, paged_groups(RB)>), grid1(blocks, 64 * paged_waves(RB)),
+                       dim3(64 * paged_waves(RB)), 0, st, G);
   SK_LAUNCH_CHECK();
 }
 

@@ -32,15 +32,18 @@ PagedPlan plan_paged(const sinkhorn_attention* a, const sinkhorn_pages* c, int64
   p.rows = a->len_q * group;
   p.many = p.rows > 32;
   p.tiles = ceil_div(p.rows, p.many ? 128 : 32);
-  const int64_t keys = p.many ? 64 : 32 * few_waves((wide ? 128 : 64) * elem_size(a));  // of a tile
+  const int64_t size = elem_size(a), keys = p.many ? 64 : 32 * paged_waves((wide ? 128 : 64) * size);  // of a tile
   int64_t seen = c->table_len * (int64_t)c->page_size;
   if (recent > 0) {
     // the window of a tile's rows and the first keys, each with a tile cut at both ends
     const int64_t rows = std::min<int64_t>(a->len_q, (p.many ? 128 : 32) / group + 2);
     seen = std::min(seen, std::min(first, seen) + std::min(recent, seen) + rows + 2 * keys);
   }
-  const int64_t slots = !p.many || (f32 && wide) ? 256 : 512;
-  p.nsplit = splits(pairs * p.tiles, ceil_div(seen, keys), slots, p.many ? (f32 ? 1.0 : 3.0) : 7.0, !p.many);
+  // a step of few rows takes 1.4 us, a join with its launch 4 to 5 (at 7 steps, as a
+  // step of k_attend's tokens seems: 4 x 1000 keys x 8 heads of 64 14.9 -> 9.9 us, 32768 x
+  // 8 of 128 46 -> 30.5)
+  const int64_t slots = p.many ? (f32 && wide ? 256 : 512) : 256 * paged_groups((wide ? 128 : 64) * size);
+  p.nsplit = splits(pairs * p.tiles, ceil_div(seen, keys), slots, f32 && p.many ? 1.0 : 3.0, !p.many);
   Space ws;
   if (p.nsplit > 1) {
     p.o_off = ws.take(4 * p.nsplit * pairs * p.rows * ceil_div(a->dv, 4) * 4);

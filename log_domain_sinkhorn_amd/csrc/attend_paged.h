@@ -10,11 +10,11 @@
 // Pages. A wave loads a tile's rows in groups of 8, which lie in one page because page
 // sizes are multiples of 8: a group's address goes into the scalar base of its loads,
 // so a lane's offsets are the same in every tile and a cache may be of any size. The
-// addresses of a tile's groups are made side by side in the lanes of a vector
-// register, a tile ahead, and read from there lane by lane (made one by one in
-// scalar registers they took the longer part of a tile's time with few rows: 16 x
-// 32768 keys x 8 heads 326 -> 276 us). A wave holds 256 page numbers of the sequence, four a lane;
-// loading the next 256 waits for the loads in flight, once in 2048 keys or more.
+// addresses of 64 groups, of the next 16 tiles or 32, are made side by side in the
+// lanes of a vector register and read from there lane by lane. (Made one by one in
+// scalar registers for each tile they took the longer part of a tile's time with few
+// rows, 16 x 32768 keys x 8 heads 326 -> 276 us side by side; tile by tile, ahead of its
+// loads, they cost the chunk of 2048 over 16384 keys x 32 heads 574 -> 548 us.)
 //
 // Few rows: a wave loads the keys that it computes on itself, and the waves of a
 // workgroup meet only at the end.
@@ -46,11 +46,11 @@ struct PagedArgs {
 };
 
 // The tiles of KT keys that a workgroup runs over: `ns` from the sequence's start on,
-// then those from tile t_lo on; of all these, `count` from the n0-th on. In a ring of
-// D buffers (k, then v, in each): tile n + D - 1 is started while tile n is computed
-// on. A wave loads RW consecutive rows of a tile. OWN: these are the ones that it
-// computes on, so waves do not wait for each other.
-template <class T, int DP, int KT, int NT, int D, bool OWN>
+// then those from tile t_lo on; of all these, `count` from the n0-th on. Two buffers (k
+// and v in each): tile n + 1 is started while tile n is computed on. A wave loads RW
+// consecutive rows of a tile. OWN: these are the ones that it computes on, so waves
+// do not wait for each other.
+template <class T, int DP, int KT, int NT, bool OWN>
 struct PageTiles {
   using TL = Tile<T, DP>;
   static constexpr int NW = NT / 64, RW = KT / NW;
@@ -59,12 +59,12 @@ struct PageTiles {
   static constexpr int IPO = 8 / RPI;                    // instructions for 8 rows, which lie in one page
   static constexpr int N = RW / RPI;                     // instructions of a wave for k, and for v
   static constexpr int KIND = N < 2 * IPO ? N : 2 * IPO;  // the chunks' permutation repeats after 16 rows
-  static constexpr int kOps = 2 * N;
-  static constexpr int kHeld = 4;  // page numbers of a lane
-  static_assert(KT % NW == 0 && RW % 16 == 0 && IPO >= 1, "whole groups of 8 rows");
+  static constexpr int GROUPS = RW / 8;                  // of 8 rows, of a wave
+  static constexpr int BATCH = 64 / GROUPS;              // tiles whose groups fill a wave's lanes
+  static_assert(KT % NW == 0 && RW % 16 == 0 && IPO >= 1 && BATCH * GROUPS == 64, "whole groups of 8 rows");
   struct Shared {
-    __attribute__((aligned(16))) char tiles[D][2][kTileBytes];
-    __attribute__((aligned(16))) float term[D][KT];  // of a tile with bad pages: 0 or -inf by key
+    __attribute__((aligned(16))) char tiles[2][2][kTileBytes];
+    uint64_t fine[2][NW];  // `fine` of each wave, of this batch of tiles and the next
     int odd;  // the last tile, counted from 1, that was found to hold values that are no numbers
   };
   Shared& sm;
@@ -75,33 +75,24 @@ struct PageTiles {
   uint32_t kslot, vslot;
   const int32_t* table;
   uint32_t koff[KIND], voff[KIND];  // byte offset of this lane's chunk from its 8 rows' start
-  int32_t id[kHeld];
-  uint32_t held;         // first page held
-  uint64_t kat, vat;     // of the next tile to be started: lane i: address of the wave's i-th 8 rows
-  uint64_t ok;           // bit i: they are in the cache
+  uint64_t kat, vat;  // lane i: address of the wave's group i % GROUPS of the batch's tile i / GROUPS
+  uint64_t ok;        // bit i: it lies in the cache
+  uint64_t fine;      // bit i: it does, or is behind the keys
+  bool bad;           // of the batch that is computed on: some wave's is not fine
   int nkeys, n0, count, ns, t_lo, wave, lane;
-  uint32_t npages;  // of the sequence
-  uint32_t bad;     // bit n % D: tile n may have pages outside the cache
-  bool bad_held;
 
   __device__ __forceinline__ PageTiles(Shared& sm_, const PagedArgs& A, int b, int hk, int nkeys_, int ns_, int t_lo_, int n0_,
                                        int count_, int wave_, int lane_)
       : sm(sm_), P(A.P), k((const char*)A.A.S.k + (int64_t)hk * A.A.S.ks[2] * sizeof(T)),
         v((const char*)A.A.S.v + (int64_t)hk * A.A.S.vs[2] * sizeof(T)), kpage(A.A.S.ks[0] * sizeof(T)),
         vpage(A.A.S.vs[0] * sizeof(T)), kslot((uint32_t)(A.A.S.ks[1] * sizeof(T))), vslot((uint32_t)(A.A.S.vs[1] * sizeof(T))),
-        table(A.P.table + b * A.P.stride), held(0), nkeys(nkeys_), n0(n0_), count(count_), ns(ns_), t_lo(t_lo_), wave(wave_),
-        lane(lane_), npages(nkeys_ > 0 ? A.P.page((uint32_t)(nkeys_ - 1)) + 1 : 0), bad(0), bad_held(false) {
+        table(A.P.table + b * A.P.stride), bad(false), nkeys(nkeys_), n0(n0_), count(count_), ns(ns_), t_lo(t_lo_), wave(wave_),
+        lane(lane_) {
 #pragma unroll
     for (int i = 0; i < KIND; ++i) {
       const int r = i * RPI + lane / TL::CPR, c = (lane % TL::CPR) ^ TL::swz(r);
       koff[i] = c * TL::EPC < A.A.S.d ? r % 8 * kslot + 16 * c : kOutside;
       voff[i] = c * TL::EPC < A.A.S.dv ? r % 8 * vslot + 16 * c : kOutside;
-    }
-#pragma unroll
-    for (int n = 0; n < kHeld; ++n) id[n] = -1;
-    if (count > 0) {
-      hold(P.page((uint32_t)key(0)));
-      locate(0);
     }
   }
   // first key of tile n
@@ -109,89 +100,92 @@ struct PageTiles {
     const int x = n0 + n;
     return (x < ns ? x : x - ns + t_lo) * KT;
   }
-  __device__ __forceinline__ void hold(uint32_t page) {
-    held = page;
-    bool out = false;
-#pragma unroll
-    for (int n = 0; n < kHeld; ++n) {
-      const uint32_t p = page + 64 * n + lane;
-      id[n] = p < npages ? table[p] : 0;
-    }
-#pragma unroll
-    for (int n = 0; n < kHeld; ++n) out = out || (uint32_t)id[n] >= (uint32_t)P.pages;
-    bad_held = __any(out);
-    loads_done();  // known to the compiler: it would otherwise wait for all loads at every use
-  }
-  // Addresses for tile n, those of the wave's groups of 8 rows side by side in its lanes.
+  // Addresses for the batch of tiles that begins with tile n. No loads to LDS are in flight.
   __device__ __forceinline__ void locate(int n) {
-    const int first = __builtin_amdgcn_readfirstlane(key(n));
-    const int left = nkeys - first;  // keys from the tile's first on, at least one
-    const uint32_t p0 = P.page((uint32_t)first), p1 = P.page((uint32_t)(first + (left < KT ? left : KT) - 1));
-    if (p0 < held || p1 >= held + 64 * kHeld) hold(p0);
-    const int r = wave * RW + 8 * (lane % (RW / 8));
-    const bool live = r < left;
-    const uint32_t j = (uint32_t)(first + (live ? r : 0));
-    const uint32_t page = P.page(j), slot = j - page * (uint32_t)P.size;
-    const uint32_t x = page - held;
+    const int t = n + lane / GROUPS;
+    const int j = key(t) + wave * RW + 8 * (lane % GROUPS);
+    const bool live = t < count && j < nkeys;
+    uint32_t slot = 0;
     int32_t at = 0;
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
-      const int32_t y = __builtin_amdgcn_ds_bpermute(4 * (x & 63), id[h]);
-      at = x >> 6 == (uint32_t)h ? y : at;
+    if (live) {
+      const uint32_t page = P.page((uint32_t)j);
+      slot = (uint32_t)j - page * (uint32_t)P.size;
+      at = table[page];
     }
     const bool in = live && (uint32_t)at < (uint32_t)P.pages;
     at = in ? at : 0;
     kat = (uint64_t)k + (uint64_t)at * (uint64_t)kpage + (uint64_t)slot * kslot;
     vat = (uint64_t)v + (uint64_t)at * (uint64_t)vpage + (uint64_t)slot * vslot;
     ok = __ballot(in);
+    fine = __ballot(in || !live);
+    if constexpr (!OWN)
+      if (lane == 0) sm.fine[n / BATCH % 2][wave] = fine;
   }
-  __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rsrc_of(uint64_t at, int i) {
-    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)at, i), hi = __builtin_amdgcn_readlane((uint32_t)(at >> 32), i);
-    return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0, (int)kOutside, 0x00027000);
+  // A scalar register that a vector instruction has written may be read by a memory
+  // instruction five wait states later; the compiler does not see the loads in assembly.
+  __device__ __forceinline__ static void rsrcs_of(uint64_t kat, uint64_t vat, int i, __amdgpu_buffer_rsrc_t& kr,
+                                                  __amdgpu_buffer_rsrc_t& vr) {
+    uint32_t a = __builtin_amdgcn_readlane((uint32_t)kat, i), b = __builtin_amdgcn_readlane((uint32_t)(kat >> 32), i);
+    uint32_t c = __builtin_amdgcn_readlane((uint32_t)vat, i), d = __builtin_amdgcn_readlane((uint32_t)(vat >> 32), i);
+    asm volatile("s_nop 4" : "+s"(a), "+s"(b), "+s"(c), "+s"(d));
+    kr = __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)b << 32 | a), 0, (int)kOutside, 0x00027000);
+    vr = __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)d << 32 | c), 0, (int)kOutside, 0x00027000);
   }
   __device__ __forceinline__ void start(int n) {
     if (n >= count) return;
-    const int buf = n % D;
+    if (n % BATCH == 0) locate(n);
+    const int buf = n % 2, at = n % BATCH * GROUPS;
     const int mine = nkeys - __builtin_amdgcn_readfirstlane(key(n)) - wave * RW;  // keys from this wave's first row on
-    bad = (bad & ~(1u << buf)) | (bad_held ? 1u << buf : 0u);
     const uint32_t klds = lds_offset(sm.tiles[buf][0]) + wave * (N * 1024), vlds = lds_offset(sm.tiles[buf][1]) + wave * (N * 1024);
-    const int lane_row = lane / TL::CPR;
+    constexpr uint64_t kAll = (uint64_t(1) << GROUPS) - 1;
+    auto load = [&](auto&& live) {
 #pragma unroll
-    for (int g = 0; g < RW / 8; ++g) {
-      const __amdgpu_buffer_rsrc_t kr = rsrc_of(kat, g), vr = rsrc_of(vat, g);
-      const int end = (ok >> g) & 1 ? mine : 0;
+      for (int g = 0; g < GROUPS; ++g) {
+        __amdgpu_buffer_rsrc_t kr, vr;
+        rsrcs_of(kat, vat, at + g, kr, vr);
 #pragma unroll
-      for (int s = 0; s < IPO; ++s) {
-        const int i = g * IPO + s;
-        const bool live = i * RPI + lane_row < end;
-        dma_load<16, OWN>(kr, klds + i * 1024, live ? koff[i % KIND] : kOutside);
-        dma_load<16, OWN>(vr, vlds + i * 1024, live ? voff[i % KIND] : kOutside);
+        for (int s = 0; s < IPO; ++s) {
+          const int i = g * IPO + s;
+          const bool in = live(g, i * RPI + lane / TL::CPR);
+          dma_load<16, OWN>(kr, klds + i * 1024, in ? koff[i % KIND] : kOutside);
+          dma_load<16, OWN>(vr, vlds + i * 1024, in ? voff[i % KIND] : kOutside);
+        }
       }
-      if (bad_held && lane < 8) sm.term[buf][wave * RW + 8 * g + lane] = (ok >> g) & 1 ? 0.0f : -kInf;
-    }
-    if (n + 1 < count) locate(n + 1);
+    };
+    if (mine >= RW && (ok >> at & kAll) == kAll)
+      load([](int, int) { return true; });
+    else
+      load([&](int g, int r) { return (ok >> (at + g) & 1) != 0 && r < mine; });
   }
   __device__ __forceinline__ void begin() {
     if (wave == 0) sm.odd = 0;  // read behind the first tile's barrier
-#pragma unroll
-    for (int n = 0; n < D - 1; ++n) start(n);
+    start(0);
   }
-  // Makes tile n readable and starts the one D - 1 further on.
+  // Makes tile n readable and starts the next one.
   __device__ __forceinline__ void next(int n) {
-    const int ahead = count - 1 - n;
-    if constexpr (D == 2)
-      dma_wait<0>();
-    else if (ahead >= D - 2)
-      dma_wait<(D - 2) * kOps>();
-    else
-      dma_wait<0>();
-    if constexpr (!OWN) __syncthreads();
-    start(n + D - 1);
+    dma_wait<0>();
+    if constexpr (OWN) {
+      if (n % BATCH == 0) bad = fine != ~uint64_t(0);
+    } else {
+      __syncthreads();
+      if (n % BATCH == 0) {
+        uint64_t all = ~uint64_t(0);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) all &= sm.fine[n / BATCH % 2][w];
+        bad = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)all & (uint32_t)(all >> 32)) != ~0u;
+      }
+    }
+    start(n + 1);
   }
-  __device__ __forceinline__ const char* ktile(int n) const { return sm.tiles[n % D][0]; }
-  __device__ __forceinline__ char* vtile(int n) const { return sm.tiles[n % D][1]; }
-  // of a tile with pages outside the cache: 0 or -inf for each key; else null
-  __device__ __forceinline__ const float* term(int n) const { return (bad >> (n % D)) & 1 ? sm.term[n % D] : nullptr; }
+  // Of a batch that has bad pages: are the 8 keys from row r of tile n on in the cache
+  // (or behind the keys)? In the OWN form r is one of the wave's own.
+  __device__ __forceinline__ bool in_cache(int n, int r, uint64_t own) const {
+    const int bit = n % BATCH * GROUPS + r % RW / 8;
+    if constexpr (OWN) return (own >> bit & 1) != 0;
+    return (sm.fine[n / BATCH % 2][r / RW] >> bit & 1) != 0;
+  }
+  __device__ __forceinline__ const char* ktile(int n) const { return sm.tiles[n % 2][0]; }
+  __device__ __forceinline__ char* vtile(int n) const { return sm.tiles[n % 2][1]; }
 };
 
 // sc = the products of keys kb0 .. of the tile (down) with the lane's row of q (across).
@@ -456,7 +450,7 @@ __device__ __forceinline__ void add_no_numbers(const char* tv, int kb0, int lane
   }
 }
 
-template <class T, int W, int WQ, int WK, int NB, int D, int OCC>
+template <class T, int W, int WQ, int WK, int NB, int OCC>
 __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G) {
   constexpr int DP = row_width(W);
   constexpr bool MANY = WQ > 1;
@@ -469,7 +463,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
   constexpr bool kExact = sizeof(T) == 4;  // scores in natural units, as in k_attend
   constexpr bool AHEAD = MANY && TL::RB == 128;
   static_assert(WQ > 1 || (WQ == 1 && NB == 1), "few rows: one tile of 32, a wave's own 32 keys");
-  using KeyT = PageTiles<T, DP, KT, NT, D, !MANY>;  // few rows: a wave loads the keys that it computes on
+  using KeyT = PageTiles<T, DP, KT, NT, !MANY>;  // few rows: a wave loads the keys that it computes on
   constexpr int kJoinBytes = !MANY ? WK * 32 * W * 4 : 0;
   union Memory {
     typename KeyT::Shared keys;
@@ -574,7 +568,9 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
   const int b_lo = end_of(row0), b_hi = from_of(end_of(last));
 
   if constexpr (MANY && OCC == 2) one_ahead();
+  uint64_t fine = 0;  // keys.fine of the batch that is computed on
   for (int it = 0; it < keys.count; ++it) {
+    if (it % KeyT::BATCH == 0) fine = keys.fine;
     keys.next(it);
     const int kb0 = KW * wk;
     const int j0 = __builtin_amdgcn_readfirstlane(keys.key(it) + kb0);
@@ -615,7 +611,6 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
 #pragma unroll
         for (int e = 0; e < 16; ++e) sc[n][e] = fmaf(sc[n][e], S.scale, sc[n][e] * S.scale_lo);
     }
-    const float* const term = keys.term(it);
     const bool all = j0 + KW <= e_lo && (j0 >= f_hi || j0 + KW <= G.first);  // every row sees every key
     // does the row see key i + 4 h of this wave's own? Without branches: a select each.
     const int f0 = from - j0 - 4 * h, g0 = (G.first < end ? G.first : end) - j0 - 4 * h;
@@ -627,14 +622,14 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
 #pragma unroll
         for (int e = 0; e < 16; ++e) sc[n][e] = seen(32 * n + 8 * (e >> 2) + (e & 3)) ? sc[n][e] : -kInf;
     }
-    if (term) {
+    if (keys.bad) {
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x4 ct = *(const f32x4*)&term[kb0 + 32 * n + 8 * g + 4 * h];
+          const bool in = keys.in_cache(it, kb0 + 32 * n + 8 * g, fine);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[n][4 * g + e] = ct[e] == 0.0f ? sc[n][4 * g + e] : -kInf;
+          for (int e = 0; e < 4; ++e) sc[n][4 * g + e] = in ? sc[n][4 * g + e] : -kInf;
         }
     }
     soften<NB, NDB>(sc, f, m, l, o);
@@ -670,9 +665,9 @@ void attend_paged_launch(const PagedArgs& G, bool many, hipStream_t st) {
   constexpr int RB = row_width(W) * (int)sizeof(T);
   constexpr int OCC = RB == 128 ? 3 : (RB == 256 ? 2 : 1);
   if (many)
-    hipLaunchKernelGGL((k_attend_paged<T, W, 4, 1, 2, 2, OCC>), grid1(blocks, 256), dim3(256), 0, st, G);
+    hipLaunchKernelGGL((k_attend_paged<T, W, 4, 1, 2, OCC>), grid1(blocks, 256), dim3(256), 0, st, G);
   else
-    hipLaunchKernelGGL((k_attend_paged<T, W, 1, paged_waves(RB), 1, 2, paged_groups(RB)>), grid1(blocks, 64 * paged_waves(RB)),
+    hipLaunchKernelGGL((k_attend_paged<T, W, 1, paged_waves(RB), 1, paged_groups(RB)>), grid1(blocks, 64 * paged_waves(RB)),
                        dim3(64 * paged_waves(RB)), 0, st, G);
   SK_LAUNCH_CHECK();
 }

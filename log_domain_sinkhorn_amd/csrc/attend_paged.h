@@ -402,15 +402,16 @@ __device__ __forceinline__ bool no_numbers(const char* tv, int thread) {
     }
     return top >= 0x7f800000u;
   } else {
-    typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
     constexpr unsigned short inf = std::is_same<T, __bf16>::value ? 0x7f80 : 0x7c00;
-    u16x8 top = {0, 0, 0, 0, 0, 0, 0, 0};
+    u16x2 top = {0, 0};
 #pragma unroll
-    for (int i = 0; i < N; ++i) top = __builtin_elementwise_max(top, *(const u16x8*)(p + 16 * NT * i) & (unsigned short)0x7fff);
-    bool any = false;
+    for (int i = 0; i < N; ++i) {
+      const u32x4 x = *(const u32x4*)(p + 16 * NT * i);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) any |= top[e] >= inf;
-    return any;
+      for (int e = 0; e < 4; ++e) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x[e] & 0x7fff7fffu));
+    }
+    return (top[0] >= inf) | (top[1] >= inf);
   }
 }
 // Puts 0 in their places.
@@ -616,13 +617,13 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
     const int f0 = from - j0 - 4 * h, g0 = (G.first < end ? G.first : end) - j0 - 4 * h;
     const uint32_t span = (uint32_t)(end - from);
     auto seen = [&](int i) { return ((uint32_t)(i - f0) < span) | (i < g0); };
-    if (!all) {
+    if (__builtin_expect(!all, 0)) {
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int e = 0; e < 16; ++e) sc[n][e] = seen(32 * n + 8 * (e >> 2) + (e & 3)) ? sc[n][e] : -kInf;
     }
-    if (keys.bad) {
+    if (__builtin_expect(keys.bad, 0)) {
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -633,7 +634,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
         }
     }
     soften<NB, NDB>(sc, f, m, l, o);
-    if (odd) {
+    if (__builtin_expect(odd, 0)) {
       add_no_numbers<T, DP, KW>(tv, kb0, lane, o, seen);
       clear();
     }

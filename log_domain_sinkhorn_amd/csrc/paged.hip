@@ -23,27 +23,79 @@ struct PagedPlan {
   int64_t o_off, ml_off, bytes;
 };
 
-// As plan_attend, for as many keys as the table has places for or the rows of a
-// tile may see.
+// The two forms of the kernel: 128 rows against 64 keys a step, or 32 rows against 32
+// keys of each wave. step: microseconds of a step with `slots` workgroups on the
+// chip, by width (32, 64, 96, 128 columns), measured at 256 to 768 pairs of 4096 keys
+// that share their pages.
+struct Form {
+  bool many;
+  int64_t rows, keys, slots;
+  double step;
+};
+Form form_of(const sinkhorn_attention* a, bool many) {
+  const bool f32 = a->dtype == SINKHORN_F32;
+  const int w = head_width(a->d, a->dv) / 32 - 1;
+  const int64_t bytes = row_width(32 * (w + 1)) * elem_size(a);
+  static const double steps[2][2][4] = {{{1.2, 1.26, 1.1, 1.2}, {2.0, 3.2, 4.3, 5.4}}, {{1.5, 2.1, 1.9, 2.2}, {5.3, 9.1, 7.7, 10.1}}};
+  if (many) return Form{true, 128, 64, bytes <= 128 ? 768 : (bytes <= 256 ? 512 : 256), steps[1][f32][w]};
+  return Form{false, 32, 32 * paged_waves(bytes), 256 * paged_groups(bytes), steps[0][f32][w]};
+}
+
+// Microseconds of a call: rounds of workgroups, each with 4 to begin and end, and the
+// join: 4, and its partial results written and read at 4.5 TB/s. With fewer workgroups
+// on a compute unit than it holds a step is shorter.
+double cost_of(const Form& f, int64_t tiles, int64_t steps, int64_t n, double partial) {
+  const int64_t blocks = tiles * n, rounds = ceil_div(blocks, f.slots), most = f.slots / 256;
+  const int64_t held = std::min(ceil_div(blocks, 256), most);
+  const double step = f.step * (0.4 + 0.6 * (double)held / (double)most);
+  return (double)rounds * ((double)ceil_div(steps, n) * step + 4.0) + (n > 1 ? 4.0 + (double)n * partial / 2.25e6 : 0.0);
+}
+
+// The form and the number of splits of the keys that cost least, for as many keys as
+// the table has places for or the rows of a tile may see. More than 32 rows of a pair
+// take the form of few rows where its smaller tiles spread over more of the chip:
+// 14 pairs of 170 rows against 2123 keys of 128 bf16 26.3 us of many rows, 20.7 of few;
+// 24 x 180 against 199 of 96 13.3, 10.1; 10 x 3928 against 491 of 72 22.5, 43.7; over 40
+// drawn chunks what this takes is 0.7% above the better one.
 PagedPlan plan_paged(const sinkhorn_attention* a, const sinkhorn_pages* c, int64_t first, int64_t recent) {
   PagedPlan p{};
-  const bool f32 = a->dtype == SINKHORN_F32, wide = a->d > 64 || a->dv > 64;
   const int64_t group = a->heads_q / a->heads_kv, pairs = (int64_t)a->batch * a->heads_kv;
   p.rows = a->len_q * group;
-  p.many = p.rows > 32;
-  p.tiles = ceil_div(p.rows, p.many ? 128 : 32);
-  const int64_t size = elem_size(a), keys = p.many ? 64 : 32 * paged_waves((wide ? 128 : 64) * size);  // of a tile
-  int64_t seen = c->table_len * (int64_t)c->page_size;
-  if (recent > 0) {
-    // the window of a tile's rows and the first keys, each with a tile cut at both ends
-    const int64_t rows = std::min<int64_t>(a->len_q, (p.many ? 128 : 32) / group + 2);
-    seen = std::min(seen, std::min(first, seen) + std::min(recent, seen) + rows + 2 * keys);
+  const double partial = 4.0 * (double)(pairs * p.rows) * (double)(ceil_div(a->dv, 4) * 4 + 2);
+  double least = 0.0;
+  for (int form = p.rows > 32; form >= 0; --form) {
+    const Form f = form_of(a, form != 0);
+    const int64_t tiles = ceil_div(p.rows, f.rows);
+    int64_t seen = c->table_len * (int64_t)c->page_size;
+    if (recent > 0) {
+      // the window of a tile's rows and the first keys, each with a tile cut at both ends
+      const int64_t rows = std::min<int64_t>(a->len_q, f.rows / group + 2);
+      seen = std::min(seen, std::min(first, seen) + std::min(recent, seen) + rows + 2 * f.keys);
+    }
+    const int64_t steps = ceil_div(seen, f.keys), most = std::min<int64_t>(steps, 512);
+    int64_t n = 1, best = 1;
+    double cost = 0.0;
+    do {  // the fewest splits for each number of steps
+      const double x = cost_of(f, pairs * tiles, steps, n, partial);
+      if (n == 1 || x < cost) {
+        cost = x;
+        best = n;
+      }
+      const int64_t each = ceil_div(steps, n);
+      if (each <= 1) break;
+      n = ceil_div(steps, each - 1);
+    } while (n <= most);
+    // tokens: at least four rounds where there are several, so that sequences of
+    // different lengths even out
+    if (p.rows <= 32 && best > 1)
+      best = std::max(best, std::min(ceil_div(4 * f.slots, pairs * tiles), std::max<int64_t>(1, steps / 8)));
+    if (p.tiles == 0 || cost < least) {
+      least = cost;
+      p.many = f.many;
+      p.tiles = tiles;
+      p.nsplit = (int32_t)best;
+    }
   }
-  // a step of few rows takes 1.4 us, a join with its launch 4 to 5 (at 7 steps, as a
-  // step of k_attend's tokens seems: 4 x 1000 keys x 8 heads of 64 14.9 -> 9.9 us, 32768 x
-  // 8 of 128 46 -> 30.5)
-  const int64_t slots = p.many ? (f32 && wide ? 256 : 512) : 256 * paged_groups((wide ? 128 : 64) * size);
-  p.nsplit = splits(pairs * p.tiles, ceil_div(seen, keys), slots, f32 && p.many ? 1.0 : 3.0, !p.many);
   Space ws;
   if (p.nsplit > 1) {
     p.o_off = ws.take(4 * p.nsplit * pairs * p.rows * ceil_div(a->dv, 4) * 4);

@@ -97,41 +97,46 @@ __device__ __forceinline__ void cos_sin(double turns, float& c, float& s) {
   s = quarter & 2 ? -b : b;
 }
 
-// A lane's part of the heads of width d.
-template <int E>
+// A lane's part of the heads of width d. PAIRS: neighbours turn together (for chunks
+// of one element as for pairs apart, with other places).
+template <int E, bool PAIRS>
 struct Lane {
-  int at[2];     // first element of its chunks
-  bool has[2];   // are they within the head?
-  bool turns;    // are they rotated?
+  int at[2];      // first element of its chunks
+  bool has[2];    // are they within the head?
+  bool turns[2];  // are they rotated?
 
   // u: the lane's place in its group; half: rotated pairs
-  __device__ __forceinline__ Lane(int u, int half, bool interleaved, int d) {
-    const int n = half / E;  // lanes whose chunks are rotated
-    turns = u < n;
-    const int a = turns && !interleaved ? u : 2 * u, b = turns && !interleaved ? u + n : 2 * u + 1;
-    at[0] = a * E;
-    at[1] = b * E;
-    has[0] = at[0] < d;
-    has[1] = at[1] < d;
+  __device__ __forceinline__ Lane(int u, int half, bool pairs, int d) {
+    const int n = half / E;  // lanes whose chunks are rotated, for pairs apart
+    const bool apart = !pairs && u < n;
+    at[0] = (apart ? u : 2 * u) * E;
+    at[1] = (apart ? u + n : 2 * u + 1) * E;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      has[k] = at[k] < d;
+      turns[k] = PAIRS ? at[k] < 2 * half : u < n;
+    }
   }
 };
 
-// (x, y) turned by the lane's angles: element pairs (x[e], y[e]), or with
-// `interleaved` neighbours in x, then in y.
-template <int E>
-__device__ __forceinline__ void turn(float (&x)[E], float (&y)[E], const float (&c)[E], const float (&s)[E], bool interleaved) {
-  if (E > 1 && interleaved) {
-    if constexpr (E > 1) {
+// (x, y) turned by the lane's angles: element pairs (x[e], y[e]), or with PAIRS
+// neighbours in x, then in y.
+template <int E, bool PAIRS>
+__device__ __forceinline__ void turn(float (&x)[E], float (&y)[E], const float (&c)[E], const float (&s)[E],
+                                     const Lane<E, PAIRS>& l) {
+  if constexpr (PAIRS && E > 1) {
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        const float a = x[2 * e], b = x[2 * e + 1], p = y[2 * e], q = y[2 * e + 1];
-        x[2 * e] = fmaf(a, c[e], -(b * s[e]));
-        x[2 * e + 1] = fmaf(a, s[e], b * c[e]);
-        y[2 * e] = fmaf(p, c[E / 2 + e], -(q * s[E / 2 + e]));
-        y[2 * e + 1] = fmaf(p, s[E / 2 + e], q * c[E / 2 + e]);
-      }
+    for (int k = 0; k < 2; ++k) {
+      float(&z)[E] = k ? y : x;
+      if (l.turns[k])
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          const float a = z[2 * e], b = z[2 * e + 1], cs = c[k * E / 2 + e], sn = s[k * E / 2 + e];
+          z[2 * e] = fmaf(a, cs, -(b * sn));
+          z[2 * e + 1] = fmaf(a, sn, b * cs);
+        }
     }
-  } else {
+  } else if (l.turns[0]) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float a = x[e], b = y[e];
@@ -142,16 +147,23 @@ __device__ __forceinline__ void turn(float (&x)[E], float (&y)[E], const float (
 }
 
 // A lane's frequencies in turns per position.
-template <int E>
-__device__ __forceinline__ void lane_frequencies(const RotateArgs& A, const Lane<E>& l, int u, double (&w)[E]) {
+template <int E, bool PAIRS>
+__device__ __forceinline__ void lane_frequencies(const RotateArgs& A, const Lane<E, PAIRS>& l, int u, double (&w)[E]) {
   constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
+  constexpr int kFirst = PAIRS && E > 1 ? E / 2 : E;  // of the first chunk
 #pragma unroll
-  for (int e = 0; e < E; ++e) w[e] = l.turns ? A.freq[u * E + e] * kTurn : 0.0;
+  for (int e = 0; e < E; ++e) w[e] = 0.0;
+  if (l.turns[0])
+#pragma unroll
+    for (int e = 0; e < kFirst; ++e) w[e] = A.freq[u * E + e] * kTurn;
+  if (l.turns[1])
+#pragma unroll
+    for (int e = kFirst; e < E; ++e) w[e] = A.freq[u * E + e] * kTurn;
 }
-template <int E>
-__device__ __forceinline__ void lane_angles(const RotateArgs& A, const Lane<E>& l, const double (&w)[E], int position,
+template <int E, bool PAIRS>
+__device__ __forceinline__ void lane_angles(const RotateArgs& A, const Lane<E, PAIRS>& l, const double (&w)[E], int position,
                                             float (&c)[E], float (&s)[E]) {
-  if (!l.turns) return;
+  if (!l.turns[0]) return;
   const double p = (double)position;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -161,8 +173,8 @@ __device__ __forceinline__ void lane_angles(const RotateArgs& A, const Lane<E>& 
   }
 }
 
-template <class T, int E>
-__device__ __forceinline__ void lane_weight(const RotateArgs& A, const void* weight, const Lane<E>& l, int i, float (&x)[E]) {
+template <class T, int E, bool PAIRS>
+__device__ __forceinline__ void lane_weight(const RotateArgs& A, const void* weight, const Lane<E, PAIRS>& l, int i, float (&x)[E]) {
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int c = l.at[i] + e;
@@ -199,7 +211,7 @@ __device__ __forceinline__ float inverse_rms(const RotateArgs& A, float sum) {
 // workgroup takes one of the tensors; a token's heads are dealt to 1 << groups lane
 // groups, neighbours to neighbours, and U heads of a group are loaded before the
 // first is used.
-template <class T, int E, int LPH, int U>
+template <class T, int E, int LPH, int U, bool PAIRS>
 __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
   typedef typename Raw<T, E>::V V;
   const int which = (int)blockIdx.x < A.part[0].end ? 0 : ((int)blockIdx.x < A.part[1].end ? 1 : 2);
@@ -213,7 +225,7 @@ __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
   const int b = (int)A.by_steps((uint32_t)token), i = (int)token - b * A.steps;
   const int ntokens = live_tokens(A, b);
   const bool live = i < ntokens;
-  const Lane<E> l(lane, value ? 0 : A.half, A.interleaved, value ? A.dv : A.d);
+  const Lane<E, PAIRS> l(lane, value ? 0 : A.half, A.interleaved, value ? A.dv : A.d);
   int place = i;
   int64_t to = b * R.ds[0] + i * R.ds[1];
   if (A.lengths_out) {
@@ -232,19 +244,19 @@ __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
     }
   }
   float c[E], s[E];
-  if (l.turns) {
+  if (l.turns[0]) {
     double w[E];
-    lane_frequencies<E>(A, l, lane, w);
+    lane_frequencies(A, l, lane, w);
     if (A.positions) place = A.positions[b * A.position_stride + i];
-    lane_angles<E>(A, l, w, place, c, s);
+    lane_angles(A, l, w, place, c, s);
   }
   const bool norm = A.norm && !value;
+  const bool turned[2] = {live && (norm || l.turns[0]), live && (norm || l.turns[1])};  // else as it is
   float weight[2][E];
   if (norm) {
-    lane_weight<T, E>(A, R.weight, l, 0, weight[0]);
-    lane_weight<T, E>(A, R.weight, l, 1, weight[1]);
+    lane_weight<T>(A, R.weight, l, 0, weight[0]);
+    lane_weight<T>(A, R.weight, l, 1, weight[1]);
   }
-  const bool changed = live && (norm || l.turns);  // else as it is: values, zeros, the rest of a head
   const T* const src = (const T*)R.src + b * R.ss[0] + i * R.ss[1];
   T* const dst = (T*)R.dst + to;
   for (int h0 = g; h0 < R.heads; h0 += U << R.groups) {
@@ -277,10 +289,10 @@ __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
 #pragma unroll
           for (int e = 0; e < E; ++e) x[k][e] = x[k][e] * r * weight[k][e];
       }
-      if (l.turns) turn<E>(x[0], x[1], c, s, A.interleaved);
+      turn(x[0], x[1], c, s, l);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (l.has[k]) *(V*)(dst + h * R.ds[2] + l.at[k]) = changed ? narrow<T, E>(x[k]) : raw[n][k];
+        if (l.has[k]) *(V*)(dst + h * R.ds[2] + l.at[k]) = turned[k] ? narrow<T, E>(x[k]) : raw[n][k];
     }
   }
 }
@@ -290,20 +302,20 @@ __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
 // A workgroup takes rows of one tensor; a lane adds up the weight's gradient of its
 // chunks over all that it meets; groups of a wave, waves and workgroups are then added
 // in a fixed order.
-template <class T, int E, int LPH, int U>
+template <class T, int E, int LPH, int U, bool PAIRS>
 __global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
   typedef typename Raw<T, E>::V V;
   __shared__ float sw[4][kMaxD];
   const int which = (int)blockIdx.x < A.part[0].end ? 0 : 1, first = which ? A.part[0].end : 0;
   const HeadRows& R = A.part[which];
   const int lane = threadIdx.x % LPH, wave = threadIdx.x >> 6;
-  const Lane<E> l(lane, A.half, A.interleaved, A.d);
+  const Lane<E, PAIRS> l(lane, A.half, A.interleaved, A.d);
   double w[E];
-  lane_frequencies<E>(A, l, lane, w);
+  lane_frequencies(A, l, lane, w);
   float acc[2][E], weight[2][E];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    lane_weight<T, E>(A, R.weight, l, k, weight[k]);
+    lane_weight<T>(A, R.weight, l, k, weight[k]);
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[k][e] = 0.0f;
   }
@@ -317,7 +329,7 @@ __global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
     const T* const dy = (const T*)R.dy + b * R.ys[0] + i * R.ys[1];
     T* const dst = (T*)R.dst + b * R.ds[0] + i * R.ds[1];
     float c[E], s[E];
-    lane_angles<E>(A, l, w, A.positions ? A.positions[b * A.position_stride + i] : i, c, s);
+    lane_angles(A, l, w, A.positions ? A.positions[b * A.position_stride + i] : i, c, s);
     for (int h0 = g; h0 < R.heads; h0 += U << R.groups) {
       V rx[U][2], ry[U][2];
 #pragma unroll
@@ -342,7 +354,7 @@ __global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
           widen<T, E>(rx[n][k], x[k]);
           widen<T, E>(ry[n][k], y[k]);
         }
-        if (l.turns) turn<E>(y[0], y[1], c, s, A.interleaved);
+        turn(y[0], y[1], c, s, l);
         float sum = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -380,30 +392,43 @@ __global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
 }
 
 // ---------------------------------------------------------------- launches
-// Elements of a chunk: as many as 16 bytes hold, and the layout and the pairs allow.
+// f(chunk, lanes, pairs): elements of a chunk (e: as many as 16 bytes hold, and the
+// layout and the pairs allow), lanes for heads of up to 64 or 128 elements, neighbours.
 template <class T, class F>
-void by_chunk(int e, int width, F&& f) {
-  constexpr int most = 16 / (int)sizeof(T);
-  auto go = [&](auto chunk, auto lanes) { f(chunk, lanes); };
+void by_chunk(int e, int width, bool interleaved, F&& f) {
   using std::integral_constant;
-  if (e == most && width <= kMaxD / 2)
-    go(integral_constant<int, most>{}, integral_constant<int, 32 / most>{});
-  else if (e == most)
-    go(integral_constant<int, most>{}, integral_constant<int, 64 / most>{});
-  else if (e == 4 && most == 8)
-    go(integral_constant<int, 4>{}, integral_constant<int, 16>{});
-  else if (e == 2)
-    go(integral_constant<int, 2>{}, integral_constant<int, 32>{});
-  else
-    go(integral_constant<int, 1>{}, integral_constant<int, 64>{});
+  auto go = [&](auto chunk) {
+    constexpr int E = decltype(chunk)::value;
+    auto wide = [&](auto pairs) {
+      if (width <= kMaxD / 2)
+        f(chunk, integral_constant<int, 32 / E>{}, pairs);
+      else
+        f(chunk, integral_constant<int, 64 / E>{}, pairs);
+    };
+    if (interleaved)
+      wide(std::true_type{});
+    else
+      wide(std::false_type{});
+  };
+  if (e == 8) {
+    if constexpr (sizeof(T) == 2) go(integral_constant<int, 8>{});
+  } else if (e == 4) {
+    go(integral_constant<int, 4>{});
+  } else if (e == 2) {
+    go(integral_constant<int, 2>{});
+  } else {
+    go(integral_constant<int, 1>{});
+  }
 }
 
-// Lane groups of a token (log2): of few tokens every head has its own; of many, four
-// heads share their token's angles.
+// Lane groups of a token (log2): up to four heads share their token's angles, fewer
+// where that leaves a compute unit fewer than 256 lanes (with 1024 as the bound more
+// groups make the same angles: 6978 tokens x 16 heads of 32 bf16 13.1 us in place of 7.5,
+// 635 x 45 of 96 9.9 of 6.9; 16384 x 40 of 128 takes four heads either way).
 inline int32_t rotate_groups(int64_t tokens, int32_t heads, int32_t lanes) {
   int32_t g = 0;
   while ((1 << g) < (heads + 3) / 4) ++g;
-  while ((1 << g) < heads && (tokens << g) * lanes < (int64_t)256 * 1024) ++g;
+  while ((1 << g) < heads && (tokens << g) * lanes < (int64_t)256 * 256) ++g;
   return g;
 }
 
@@ -411,8 +436,9 @@ inline int32_t rotate_groups(int64_t tokens, int32_t heads, int32_t lanes) {
 template <class T>
 void rotate(RotateArgs& A, int e, hipStream_t st) {
   A.by_steps = Divide(A.steps);
-  by_chunk<T>(e, A.d > A.dv ? A.d : A.dv, [&](auto chunk, auto lanes) {
+  by_chunk<T>(e, A.d > A.dv ? A.d : A.dv, A.interleaved, [&](auto chunk, auto lanes, auto pairs) {
     constexpr int E = decltype(chunk)::value, L = decltype(lanes)::value;
+    constexpr bool P = decltype(pairs)::value;
     const int64_t tokens = (int64_t)A.batch * A.steps;
     int64_t blocks = 0;
     for (HeadRows& R : A.part) {
@@ -422,7 +448,7 @@ void rotate(RotateArgs& A, int e, hipStream_t st) {
       }
       R.end = (int32_t)std::min<int64_t>(blocks, INT32_MAX);
     }
-    hipLaunchKernelGGL((k_rotate<T, E, L, 4>), grid1(blocks, 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_rotate<T, E, L, 4, P>), grid1(blocks, 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   });
 }
@@ -431,15 +457,16 @@ void rotate(RotateArgs& A, int e, hipStream_t st) {
 template <class T>
 void rotate_grad(RotateArgs& A, int e, int32_t blocks, hipStream_t st) {
   A.by_steps = Divide(A.len);
-  by_chunk<T>(e, A.d, [&](auto chunk, auto lanes) {
+  by_chunk<T>(e, A.d, A.interleaved, [&](auto chunk, auto lanes, auto pairs) {
     constexpr int E = decltype(chunk)::value, L = decltype(lanes)::value;
+    constexpr bool P = decltype(pairs)::value;
     HeadRows &q = A.part[0], &k = A.part[1];
     for (HeadRows* R : {&q, &k}) R->groups = rotate_groups((int64_t)A.batch * A.len, R->heads, L);
     q.end = (int32_t)((int64_t)blocks * q.heads / (q.heads + k.heads));
     if (q.heads > 0 && q.end == 0) q.end = 1;
     if (k.heads > 0 && q.end == blocks) --q.end;
     k.end = blocks;
-    hipLaunchKernelGGL((k_rotate_grad<T, E, L, 2>), grid1(blocks, 256), dim3(256), 0, st, A);
+    hipLaunchKernelGGL((k_rotate_grad<T, E, L, 2, P>), grid1(blocks, 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   });
 }

@@ -97,7 +97,9 @@ struct Unit {
   int64_t size;
   int e;
   explicit Unit(const sinkhorn_rotation* r) : size(elem_size(r->dtype)), e((int)(16 / elem_size(r->dtype))) {
-    while (r->d % e != 0 || (r->rotated / 2) % e != 0) e /= 2;
+    // both elements of a pair in a chunk, or in two chunks of one lane
+    const int32_t turn = r->interleaved ? r->rotated : r->rotated / 2;
+    while (r->d % e != 0 || turn % e != 0) e /= 2;
   }
   void fit(const void* p, const int64_t* stride, int32_t width) {
     while (e > 1 && !rows_aligned(p, stride, width, size, e * size)) e /= 2;
@@ -133,11 +135,12 @@ void run(const sinkhorn_rotation* r, RotateArgs& A, int e, hipStream_t st) {
     rotate<float>(A, e, st);
 }
 
-// Workgroups of the backward pass with a norm: four a compute unit, fewer where a
-// wave would not find four heads; two at least, one for each tensor.
+// Workgroups of the backward pass with a norm: as many as the chip holds at a time,
+// three a compute unit (16384 tokens x 40 heads of 128 bf16: 768 108 us, 1024 114, 1536 109),
+// fewer where a wave would not find four heads; two at least, one for each tensor.
 int32_t grad_blocks(const sinkhorn_rotation* r) {
   const int64_t n = ceil_div(r->batch * r->len * (r->heads_q + r->heads_kv), 16);
-  return (int32_t)(n < 2 ? 2 : (n > 1024 ? 1024 : n));
+  return (int32_t)(n < 2 ? 2 : (n > 768 ? 768 : n));
 }
 int64_t grad_space(const sinkhorn_rotation* r) { return r->norm ? (int64_t)grad_blocks(r) * kMaxD * 4 : 0; }
 

@@ -1012,9 +1012,7 @@ def paged_attention(q, k_cache, v_cache, page_table, key_lengths, *, scale=None,
     bytes, as are the cache's strides."""
     _head_tensor(q, "q")
     B, lq, hq, d = q.shape
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [pages, page_size, heads, width]")
-    hkv = k_cache.shape[2]
+    hkv = _head_tensor(k_cache, "k_cache", q.dtype).shape[2]
     if hkv < 1 or hq < 1 or hq % hkv:
         raise ValueError(f"{hq} query heads are no multiple of {hkv} key heads")
     c, dv = _pages(q.dtype, B, hkv, d, k_cache, v_cache, page_table, key_lengths, "key_lengths")

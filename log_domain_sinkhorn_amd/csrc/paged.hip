@@ -199,6 +199,7 @@ int sinkhorn_paged_attention(const sinkhorn_attention* a, const sinkhorn_pages* 
     G.by_heads = Divide(A.S.hkv);
     G.by_per = Divide(G.per);
     G.by_split = Divide(p.nsplit);
+    G.pair_up = p.many && p.nsplit == 1 && (int64_t)a->batch * a->heads_kv * p.tiles <= form_of(a, true).slots;
     G.qvec = rows_aligned(q, a->q_stride, a->d, size, 16);
     const hipStream_t st = (hipStream_t)stream;
     if (a->dtype == SINKHORN_BF16)

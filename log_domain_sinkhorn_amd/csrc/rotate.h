@@ -161,10 +161,9 @@ __device__ __forceinline__ void lane_frequencies(const RotateArgs& A, const Lane
     for (int e = kFirst; e < E; ++e) w[e] = A.freq[u * E + e] * kTurn;
 }
 template <int E, bool PAIRS>
-__device__ __forceinline__ void lane_angles(const RotateArgs& A, const Lane<E, PAIRS>& l, const double (&w)[E], int position,
+__device__ __forceinline__ void lane_angles(const RotateArgs& A, const Lane<E, PAIRS>& l, const double (&w)[E], double p,
                                             float (&c)[E], float (&s)[E]) {
   if (!l.turns[0]) return;
-  const double p = (double)position;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     cos_sin(p * w[e], c[e], s[e]);
@@ -226,13 +225,13 @@ __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
   const int ntokens = live_tokens(A, b);
   const bool live = i < ntokens;
   const Lane<E, PAIRS> l(lane, value ? 0 : A.half, A.interleaved, value ? A.dv : A.d);
-  int place = i;
+  int64_t place = i;
   int64_t to = b * R.ds[0] + i * R.ds[1];
   if (A.lengths_out) {
     const int before = paged_keys(A.P, b);
     const int64_t j = (int64_t)before + i, cap = (int64_t)A.P.len * A.P.size;
     if (which == 1 && i == 0 && g == 0 && lane == 0) A.lengths_out[b] = (int)(before + ntokens < cap ? before + ntokens : cap);
-    place = (int)j;
+    place = j;
     if (cache) {
       if (!live || j >= cap) return;
       const uint32_t page = A.P.page((uint32_t)j);
@@ -248,7 +247,7 @@ __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
     double w[E];
     lane_frequencies(A, l, lane, w);
     if (A.positions) place = A.positions[b * A.position_stride + i];
-    lane_angles(A, l, w, place, c, s);
+    lane_angles(A, l, w, (double)place, c, s);
   }
   const bool norm = A.norm && !value;
   const bool turned[2] = {live && (norm || l.turns[0]), live && (norm || l.turns[1])};  // else as it is
@@ -329,7 +328,7 @@ __global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
     const T* const dy = (const T*)R.dy + b * R.ys[0] + i * R.ys[1];
     T* const dst = (T*)R.dst + b * R.ds[0] + i * R.ds[1];
     float c[E], s[E];
-    lane_angles(A, l, w, A.positions ? A.positions[b * A.position_stride + i] : i, c, s);
+    lane_angles(A, l, w, (double)(A.positions ? A.positions[b * A.position_stride + i] : i), c, s);
     for (int h0 = g; h0 < R.heads; h0 += U << R.groups) {
       V rx[U][2], ry[U][2];
 #pragma unroll

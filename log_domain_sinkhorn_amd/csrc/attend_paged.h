@@ -16,8 +16,8 @@
 // rows, 16 x 32768 keys x 8 heads 326 -> 276 us side by side; tile by tile, ahead of its
 // loads, they cost the chunk of 2048 over 16384 keys x 32 heads 574 -> 548 us.)
 //
-// Few rows: a wave loads the keys that it computes on itself, and the waves of a
-// workgroup meet only at the end.
+// Few rows: a wave loads the keys that it computes on itself, k and v in turn, and the
+// waves of a workgroup meet only at the end.
 //
 // Masks are of the pair, but only in tiles at the rows' own places and at the
 // window's edge; tiles that no row of the workgroup sees are not loaded, and waves
@@ -47,24 +47,29 @@ struct PagedArgs {
 };
 
 // The tiles of KT keys that a workgroup runs over: `ns` from the sequence's start on,
-// then those from tile t_lo on; of all these, `count` from the n0-th on. Two buffers (k
-// and v in each): tile n + 1 is started while tile n is computed on. A wave loads RW
-// consecutive rows of a tile. OWN: these are the ones that it computes on, so waves
-// do not wait for each other.
-template <class T, int DP, int KT, int NT, bool OWN>
+// then those from tile t_lo on; of all these, `count` from the n0-th on. A wave loads
+// RW consecutive rows of a tile.
+//
+// Many rows: two buffers, k and v in each; tile n + 1 is started while all waves
+// compute on tile n. Few rows (PLACES > 0): a wave's rows are those that it computes on,
+// so waves do not wait for each other, and k and v take turns in a ring of PLACES places
+// of the wave's own: k of tile n is half 2 n of the run, v half 2 n + 1, and while one
+// is computed on, those behind it are in flight.
+template <class T, int DP, int KT, int NT, int PLACES>
 struct PageTiles {
+  static constexpr bool OWN = PLACES > 0;
   using TL = Tile<T, DP>;
   static constexpr int NW = NT / 64, RW = KT / NW;
-  static constexpr int kTileBytes = KT * TL::RB;
+  static constexpr int kTileBytes = KT * TL::RB, kOwnBytes = RW * TL::RB;
   static constexpr int RPI = 64 / TL::CPR;               // rows of an instruction
   static constexpr int IPO = 8 / RPI;                    // instructions for 8 rows, which lie in one page
   static constexpr int N = RW / RPI;                     // instructions of a wave for k, and for v
   static constexpr int KIND = N < 2 * IPO ? N : 2 * IPO;  // the chunks' permutation repeats after 16 rows
   static constexpr int GROUPS = RW / 8;                  // of 8 rows, of a wave
   static constexpr int BATCH = 64 / GROUPS;              // tiles whose groups fill a wave's lanes
-  static_assert(KT % NW == 0 && RW % 16 == 0 && IPO >= 1 && BATCH * GROUPS == 64, "whole groups of 8 rows");
+  static_assert(KT % NW == 0 && RW % 16 == 0 && IPO >= 1 && BATCH * GROUPS == 64 && BATCH > 2, "whole groups of 8 rows");
   struct Shared {
-    __attribute__((aligned(16))) char tiles[2][2][kTileBytes];
+    __attribute__((aligned(16))) char tiles[(OWN ? PLACES : 4) * kTileBytes];
     uint64_t fine[2][NW];  // `fine` of each wave, of this batch of tiles and the next
     int odd;  // the last tile, counted from 1, that was found to hold values that are no numbers
   };
@@ -79,7 +84,6 @@ struct PageTiles {
   uint64_t kat, vat;  // lane i: address of the wave's group i % GROUPS of the batch's tile i / GROUPS
   uint64_t ok;        // bit i: it lies in the cache
   uint64_t fine;      // bit i: it does, or is behind the keys
-  bool bad;           // of the batch that is computed on: some wave's is not fine
   int nkeys, n0, count, ns, t_lo, wave, lane;
 
   __device__ __forceinline__ PageTiles(Shared& sm_, const PagedArgs& A, int b, int hk, int nkeys_, int ns_, int t_lo_, int n0_,
@@ -87,8 +91,7 @@ struct PageTiles {
       : sm(sm_), P(A.P), k((const char*)A.A.S.k + (int64_t)hk * A.A.S.ks[2] * sizeof(T)),
         v((const char*)A.A.S.v + (int64_t)hk * A.A.S.vs[2] * sizeof(T)), kpage(A.A.S.ks[0] * sizeof(T)),
         vpage(A.A.S.vs[0] * sizeof(T)), kslot((uint32_t)(A.A.S.ks[1] * sizeof(T))), vslot((uint32_t)(A.A.S.vs[1] * sizeof(T))),
-        table(A.P.table + b * A.P.stride), bad(false), nkeys(nkeys_), n0(n0_), count(count_), ns(ns_), t_lo(t_lo_), wave(wave_),
-        lane(lane_) {
+        table(A.P.table + b * A.P.stride), nkeys(nkeys_), n0(n0_), count(count_), ns(ns_), t_lo(t_lo_), wave(wave_), lane(lane_) {
 #pragma unroll
     for (int i = 0; i < KIND; ++i) {
       const int r = i * RPI + lane / TL::CPR, c = (lane % TL::CPR) ^ TL::swz(r);
@@ -101,7 +104,7 @@ struct PageTiles {
     const int x = n0 + n;
     return (x < ns ? x : x - ns + t_lo) * KT;
   }
-  // Addresses for the batch of tiles that begins with tile n. No loads to LDS are in flight.
+  // Addresses for the batch of tiles that begins with tile n.
   __device__ __forceinline__ void locate(int n) {
     const int t = n + lane / GROUPS;
     const int j = key(t) + wave * RW + 8 * (lane % GROUPS);
@@ -124,70 +127,112 @@ struct PageTiles {
   }
   // A scalar register that a vector instruction has written may be read by a memory
   // instruction five wait states later; the compiler does not see the loads in assembly.
-  __device__ __forceinline__ static void rsrcs_of(uint64_t kat, uint64_t vat, int i, __amdgpu_buffer_rsrc_t& kr,
-                                                  __amdgpu_buffer_rsrc_t& vr) {
-    uint32_t a = __builtin_amdgcn_readlane((uint32_t)kat, i), b = __builtin_amdgcn_readlane((uint32_t)(kat >> 32), i);
-    uint32_t c = __builtin_amdgcn_readlane((uint32_t)vat, i), d = __builtin_amdgcn_readlane((uint32_t)(vat >> 32), i);
-    asm volatile("s_nop 4" : "+s"(a), "+s"(b), "+s"(c), "+s"(d));
-    kr = __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)b << 32 | a), 0, (int)kOutside, 0x00027000);
-    vr = __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)d << 32 | c), 0, (int)kOutside, 0x00027000);
+  __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rsrc_of(uint64_t at, int i) {
+    uint32_t a = __builtin_amdgcn_readlane((uint32_t)at, i), b = __builtin_amdgcn_readlane((uint32_t)(at >> 32), i);
+    asm volatile("s_nop 4" : "+s"(a), "+s"(b));
+    return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)b << 32 | a), 0, (int)kOutside, 0x00027000);
   }
-  __device__ __forceinline__ void start(int n) {
-    if (n >= count) return;
-    if (n % BATCH == 0) locate(n);
-    const int buf = n % 2, at = n % BATCH * GROUPS;
+  // Starts the wave's rows of k or v of tile n, whose batch is located, to the wave's part at `to`.
+  __device__ __forceinline__ void load(int n, uint64_t base, const uint32_t (&off)[KIND], const char* to) const {
+    const int at = n % BATCH * GROUPS;
     const int mine = nkeys - __builtin_amdgcn_readfirstlane(key(n)) - wave * RW;  // keys from this wave's first row on
-    const uint32_t klds = lds_offset(sm.tiles[buf][0]) + wave * (N * 1024), vlds = lds_offset(sm.tiles[buf][1]) + wave * (N * 1024);
+    const uint32_t lds = lds_offset(to);
     constexpr uint64_t kAll = (uint64_t(1) << GROUPS) - 1;
-    auto load = [&](auto&& live) {
+    auto all = [&](auto&& live) {
 #pragma unroll
       for (int g = 0; g < GROUPS; ++g) {
-        __amdgpu_buffer_rsrc_t kr, vr;
-        rsrcs_of(kat, vat, at + g, kr, vr);
+        const __amdgpu_buffer_rsrc_t r = rsrc_of(base, at + g);
 #pragma unroll
         for (int s = 0; s < IPO; ++s) {
           const int i = g * IPO + s;
-          const bool in = live(g, i * RPI + lane / TL::CPR);
-          dma_load<16, OWN>(kr, klds + i * 1024, in ? koff[i % KIND] : kOutside);
-          dma_load<16, OWN>(vr, vlds + i * 1024, in ? voff[i % KIND] : kOutside);
+          dma_load<16, OWN>(r, lds + i * 1024, live(g, i * RPI + lane / TL::CPR) ? off[i % KIND] : kOutside);
         }
       }
     };
     if (mine >= RW && (ok >> at & kAll) == kAll)
-      load([](int, int) { return true; });
+      all([](int, int) { return true; });
     else
-      load([&](int g, int r) { return (ok >> (at + g) & 1) != 0 && r < mine; });
+      all([&](int g, int r) { return (ok >> (at + g) & 1) != 0 && r < mine; });
+  }
+  __device__ __forceinline__ char* place(int half) const { return sm.tiles + (PLACES * wave + half % (OWN ? PLACES : 1)) * kOwnBytes; }
+  // Where k and v of tile n lie: with OWN the wave's rows of it.
+  __device__ __forceinline__ const char* ktile(int n) const {
+    return OWN ? place(2 * n) : sm.tiles + n % 2 * 2 * kTileBytes;
+  }
+  __device__ __forceinline__ char* vtile(int n) const {
+    return OWN ? place(2 * n + 1) : sm.tiles + (n % 2 * 2 + 1) * kTileBytes;
+  }
+  __device__ __forceinline__ void start_k(int n) {
+    if (n >= count) return;
+    if (n % BATCH == 0) locate(n);
+    load(n, kat, koff, ktile(n) + (OWN ? 0 : wave * kOwnBytes));
+  }
+  __device__ __forceinline__ void start_v(int n) {
+    if (n < count) load(n, vat, voff, vtile(n) + (OWN ? 0 : wave * kOwnBytes));
   }
   __device__ __forceinline__ void begin() {
     if (wave == 0) sm.odd = 0;  // read behind the first tile's barrier
-    start(0);
-  }
-  // Makes tile n readable and starts the next one.
-  __device__ __forceinline__ void next(int n) {
-    dma_wait<0>();
-    if constexpr (OWN) {
-      if (n % BATCH == 0) bad = fine != ~uint64_t(0);
-    } else {
-      __syncthreads();
-      if (n % BATCH == 0) {
-        uint64_t all = ~uint64_t(0);
+    start_k(0);
+    start_v(0);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) all &= sm.fine[n / BATCH % 2][w];
-        bad = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)all & (uint32_t)(all >> 32)) != ~0u;
-      }
+    for (int half = 2; half < PLACES; ++half) start(half);
+  }
+  // Few rows: starts a half of the run.
+  __device__ __forceinline__ void start(int half) {
+    if (half & 1)
+      start_v(half >> 1);
+    else
+      start_k(half >> 1);
+  }
+  // Waits for the wave's reads of LDS, before a load goes to where they were.
+  __device__ __forceinline__ static void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+  // Many rows: makes tile n readable and starts the next one. Returns whether the
+  // batch has pages outside the cache, asked at its first tile.
+  __device__ __forceinline__ bool next(int n, bool bad) {
+    dma_wait<0>();
+    __syncthreads();
+    if (n % BATCH == 0) {
+      uint64_t all = ~uint64_t(0);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) all &= sm.fine[n / BATCH % 2][w];
+      bad = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)all & (uint32_t)(all >> 32)) != ~0u;
     }
-    start(n + 1);
+    start_k(n + 1);
+    start_v(n + 1);
+    return bad;
+  }
+  // Few rows: waits for a half; those behind it, of which PLACES - 1 are started, stay in flight.
+  __device__ __forceinline__ void wait(int half) const {
+    const int behind = 2 * count - 1 - half;
+    if (PLACES > 2 && behind >= 2)
+      dma_wait<2 * N>();
+    else if (behind >= 1)
+      dma_wait<N>();
+    else
+      dma_wait<0>();
   }
   // Of a batch that has bad pages: are the 8 keys from row r of tile n on in the cache
-  // (or behind the keys)? In the OWN form r is one of the wave's own.
+  // (or behind the keys)? With OWN r is the wave's own and `own` its `fine`.
   __device__ __forceinline__ bool in_cache(int n, int r, uint64_t own) const {
     const int bit = n % BATCH * GROUPS + r % RW / 8;
     if constexpr (OWN) return (own >> bit & 1) != 0;
     return (sm.fine[n / BATCH % 2][r / RW] >> bit & 1) != 0;
   }
-  __device__ __forceinline__ const char* ktile(int n) const { return sm.tiles[n % 2][0]; }
-  __device__ __forceinline__ char* vtile(int n) const { return sm.tiles[n % 2][1]; }
 };
+
+// Few rows: waves of a workgroup, one for each SIMD; by the bytes of a row, workgroups
+// of a compute unit that the keys are split for, and places of a wave's ring. With 32
+// keys a place, two places leave room for four waves of the widest rows and a second
+// workgroup of 256-byte ones; three keep more in flight for rows of 128 bytes, which are
+// done with sooner. Against k and v of whole tiles in two buffers (two waves of the
+// widest rows): 8 x 16384 keys x 8 heads of 128 fp32 387 -> 205 us, of 64 134 -> 106,
+// 64 x 2048 x 8 of 128 bf16 78 -> 71, 16 x 32768 x 8 265 -> 262 (three places 264), of 64
+// 163 -> 157 (two places 163). Splits for a second workgroup of 256-byte rows: 26.0 for
+// 27.1 us and 0.4 less for the least calls, 20.8 for 17.9 of 64 columns, 265 for 262.
+constexpr int kPagedWaves = 4;
+constexpr int paged_groups(int64_t bytes) { return bytes <= 128 ? 2 : 1; }
+constexpr int paged_places(int64_t bytes) { return bytes <= 128 ? 3 : 2; }
 
 // sc = the products of keys kb0 .. of the tile (down) with the lane's row of q (across).
 template <class T, int DP, bool AHEAD, int NB, int NS>
@@ -465,7 +510,8 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
   constexpr bool kExact = sizeof(T) == 4;  // scores in natural units, as in k_attend
   constexpr bool AHEAD = MANY && TL::RB == 128;
   static_assert(WQ > 1 || (WQ == 1 && NB == 1), "few rows: one tile of 32, a wave's own 32 keys");
-  using KeyT = PageTiles<T, DP, KT, NT, !MANY>;  // few rows: a wave loads the keys that it computes on
+  constexpr int kPlaces = MANY ? 0 : paged_places(TL::RB);
+  using KeyT = PageTiles<T, DP, KT, NT, kPlaces>;
   constexpr int kJoinBytes = !MANY ? WK * 32 * W * 4 : 0;
   union Memory {
     typename KeyT::Shared keys;
@@ -576,20 +622,25 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
 
   if constexpr (MANY && OCC == 2) one_ahead();
   uint64_t fine = 0;  // keys.fine of the batch that is computed on
+  bool bad = false;   // the batch has pages outside the cache
   for (int it = 0; it < keys.count; ++it) {
-    if (it % KeyT::BATCH == 0) fine = keys.fine;
-    keys.next(it);
-    const int kb0 = KW * wk;
+    const int kb0 = KW * wk;  // this wave's keys of the tile
     const int j0 = __builtin_amdgcn_readfirstlane(keys.key(it) + kb0);
+    if constexpr (MANY) {
+      bad = keys.next(it, bad);
+    } else {
+      if (it % KeyT::BATCH == 0) {
+        fine = keys.fine;
+        bad = fine != ~uint64_t(0);
+      }
+      keys.wait(2 * it);
+    }
     const char* const tk = keys.ktile(it);
     char* const tv = keys.vtile(it);
     // does every row that computes on these values see every key? If not, are there any
     // that are no numbers? With many rows the workgroup looks together.
     bool odd = false;
-    if constexpr (!MANY) {
-      if (j0 + KW > e_lo || (j0 < f_hi && j0 + KW > G.first))
-        odd = __any(no_numbers<T, KW * TL::RB, 64>(tv + kb0 * TL::RB, lane));
-    } else {
+    if constexpr (MANY) {
       if (j0 + KT > b_lo || (j0 < b_hi && j0 + KT > G.first)) {
         if (no_numbers<T, KeyT::kTileBytes, NT>(tv, tid)) sm.keys.odd = it + 1;
         __syncthreads();
@@ -597,20 +648,30 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
       }
     }
     auto clear = [&] {
-      if constexpr (!MANY) {
-        clear_no_numbers<T, KW * TL::RB, 64>(tv + kb0 * TL::RB, lane);
-      } else {
+      if constexpr (MANY) {
         __syncthreads();
         clear_no_numbers<T, KeyT::kTileBytes, NT>(tv, tid);
         __syncthreads();
+      } else {
+        clear_no_numbers<T, KeyT::kOwnBytes, 64>(tv, lane);
       }
     };
     if (j0 >= e_hi || (j0 + KW <= f_lo && j0 >= G.first)) {  // no row of this wave sees any
-      if (MANY && odd) clear();
+      if constexpr (MANY) {
+        if (odd) clear();
+      } else {
+        keys.start(2 * it + kPlaces);
+        keys.wait(2 * it + 1);
+        keys.start(2 * it + 1 + kPlaces);
+      }
       continue;
     }
     f32x16 sc[NB];
-    score_tile<T, DP, AHEAD, NB, NS>(tk, kb0, lane, qf, S.d, sc);
+    score_tile<T, DP, AHEAD, NB, NS>(tk, 0, lane, qf, S.d, sc);
+    if constexpr (!MANY) {
+      keys.reads_done();
+      keys.start(2 * it + kPlaces);
+    }
     const float f = kExact ? (float)kLog2e : S.c;  // to log2 units
     if constexpr (kExact) {
 #pragma unroll
@@ -629,7 +690,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
 #pragma unroll
         for (int e = 0; e < 16; ++e) sc[n][e] = seen(32 * n + 8 * (e >> 2) + (e & 3)) ? sc[n][e] : -kInf;
     }
-    if (__builtin_expect(keys.bad, 0)) {
+    if (__builtin_expect(bad, 0)) {
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -640,11 +701,19 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
         }
     }
     soften<NB, NDB>(sc, f, m, l, o);
+    if constexpr (!MANY) {
+      keys.wait(2 * it + 1);
+      if (__builtin_expect(!all, 0)) odd = __any(no_numbers<T, KeyT::kOwnBytes, 64>(tv, lane));
+    }
     if (__builtin_expect(odd, 0)) {
-      add_no_numbers<T, DP, KW>(tv, kb0, lane, o, seen);
+      add_no_numbers<T, DP, KW>(tv, 0, lane, o, seen);
       clear();
     }
-    add_values<T, DP, MANY, NB, NDB>(tv, kb0, lane, sc, o);
+    add_values<T, DP, MANY, NB, NDB>(tv, 0, lane, sc, o);
+    if constexpr (!MANY) {
+      keys.reads_done();
+      keys.start(2 * it + 1 + kPlaces);
+    }
   }
   l = half_sum(l);
   if (!live_row) {
@@ -653,17 +722,6 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
   }
   finish_rows<T, W, WQ, WK>(G, sm.join, sml, o, m, l, live_row, split, b, hk, row0);
 }
-
-// Few rows: waves of a workgroup, each with two tiles of 32 keys in LDS, one of them
-// in flight, for rows of `bytes` bytes; workgroups of a compute unit. A wave for each
-// SIMD or two, because a wave takes 1.4 us (rows of 256 bytes) for a tile that its
-// loads could bring in 1.8. Against the three waves of three tiles that k_attend
-// has there: 16 x 32768 keys x 8 heads of 128 271 -> 263 us, 8 x 4096 x 8 36 -> 27.5,
-// fp32 of 64 179 -> 145; waves of two workgroups of two: 268, 27.5, 143. Rows of 128
-// bytes, six waves of three tiles: 16 x 32768 x 8 of 64 173 -> 165 us, 4 x 1000 x 8
-// 10.7 -> 9.9; eight of two 165, 12.0.
-constexpr int paged_waves(int64_t bytes) { return bytes <= 256 ? 4 : 2; }
-constexpr int paged_groups(int64_t bytes) { return bytes <= 128 ? 2 : 1; }
 
 // many: 128 rows per workgroup, else all rows in one tile of 32
 template <class T, int W>
@@ -674,8 +732,8 @@ void attend_paged_launch(const PagedArgs& G, bool many, hipStream_t st) {
   if (many)
     hipLaunchKernelGGL((k_attend_paged<T, W, 4, 1, 2, OCC>), grid1(blocks, 256), dim3(256), 0, st, G);
   else
-    hipLaunchKernelGGL((k_attend_paged<T, W, 1, paged_waves(RB), 1, paged_groups(RB)>), grid1(blocks, 64 * paged_waves(RB)),
-                       dim3(64 * paged_waves(RB)), 0, st, G);
+    hipLaunchKernelGGL((k_attend_paged<T, W, 1, kPagedWaves, 1, (paged_groups(RB) * kPagedWaves + 3) / 4>), grid1(blocks, 64 * kPagedWaves),
+                       dim3(64 * kPagedWaves), 0, st, G);
   SK_LAUNCH_CHECK();
 }
 

@@ -36,9 +36,9 @@ Form form_of(const sinkhorn_attention* a, bool many) {
   const bool f32 = a->dtype == SINKHORN_F32;
   const int w = head_width(a->d, a->dv) / 32 - 1;
   const int64_t bytes = row_width(32 * (w + 1)) * elem_size(a);
-  static const double steps[2][2][4] = {{{1.2, 1.26, 1.1, 1.2}, {2.0, 3.2, 4.3, 5.4}}, {{1.5, 2.1, 1.9, 2.2}, {5.3, 9.1, 7.7, 10.1}}};
+  static const double steps[2][2][4] = {{{1.4, 1.4, 1.1, 1.2}, {2.8, 2.8, 3.8, 4.8}}, {{1.5, 2.1, 1.9, 2.2}, {5.3, 9.1, 7.7, 10.1}}};
   if (many) return Form{true, 128, 64, bytes <= 128 ? 768 : (bytes <= 256 ? 512 : 256), steps[1][f32][w]};
-  return Form{false, 32, 32 * paged_waves(bytes), 256 * paged_groups(bytes), steps[0][f32][w]};
+  return Form{false, 32, 32 * kPagedWaves, 256 * paged_groups(bytes), steps[0][f32][w]};
 }
 
 // Microseconds of a call: rounds of workgroups, each with 4 to begin and end, and the

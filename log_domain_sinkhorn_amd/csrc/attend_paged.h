@@ -620,7 +620,6 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
 
   const int b_lo = end_of(row0), b_hi = from_of(end_of(last));
 
-  if constexpr (MANY && OCC == 2) one_ahead();
   uint64_t fine = 0;  // keys.fine of the batch that is computed on
   bool bad = false;   // the batch has pages outside the cache
   for (int it = 0; it < keys.count; ++it) {
@@ -668,6 +667,12 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
     }
     f32x16 sc[NB];
     score_tile<T, DP, AHEAD, NB, NS>(tk, 0, lane, qf, S.d, sc);
+    // the products of a tile stay together, and so do its vector instructions: two
+    // waves of a SIMD then take turns of themselves (without, and with one of two
+    // workgroups ahead by priority as k_attend has it: 2048 rows over 16384 keys of 128
+    // 526 us for 509, 4 x 512 over 4096 129 for 115, 2048 x 4096 fp32 of 64 143 for 138;
+    // 4096 of 96 under a window 53 for 54.6). With three waves it costs 1%.
+    if constexpr (MANY && OCC < 3) __builtin_amdgcn_sched_barrier(0);
     if constexpr (!MANY) {
       keys.reads_done();
       keys.start(2 * it + kPlaces);

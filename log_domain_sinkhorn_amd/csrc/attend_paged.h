@@ -36,6 +36,10 @@
 namespace sk {
 namespace attn {
 
+// Rows of a workgroup: 128, or 32 with the keys of a step dealt to its waves; these alone
+// on a compute unit with all keys.
+enum class PagedForm { kMany, kFew, kAlone };
+
 struct PagedArgs {
   AttendArgs A;  // S.k, S.v: the cache; S.ks, S.vs: page, slot, head; S.klen: P.lengths
   Paging P;
@@ -230,7 +234,11 @@ struct PageTiles {
 // 64 x 2048 x 8 of 128 bf16 78 -> 71, 16 x 32768 x 8 265 -> 262 (three places 264), of 64
 // 163 -> 157 (two places 163). Splits for a second workgroup of 256-byte rows: 26.0 for
 // 27.1 us and 0.4 less for the least calls, 20.8 for 17.9 of 64 columns, 265 for 262.
+// A workgroup that has a compute unit and all keys of its rows to itself takes twice the
+// waves where LDS holds their rings: 32 pairs of 64 columns bf16 over 500 keys 8.7 us
+// (four waves 9.9), over 1000 11.3 (14.3), of 128 14.2 (16.7).
 constexpr int kPagedWaves = 4;
+constexpr int alone_waves(int64_t bytes) { return bytes <= 256 ? 2 * kPagedWaves : kPagedWaves; }
 constexpr int paged_groups(int64_t bytes) { return bytes <= 128 ? 2 : 1; }
 constexpr int paged_places(int64_t bytes) { return bytes <= 128 ? 3 : 2; }
 
@@ -728,25 +736,28 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
   finish_rows<T, W, WQ, WK>(G, sm.join, sml, o, m, l, live_row, split, b, hk, row0);
 }
 
-// many: 128 rows per workgroup, else all rows in one tile of 32
 template <class T, int W>
-void attend_paged_launch(const PagedArgs& G, bool many, hipStream_t st) {
+void attend_paged_launch(const PagedArgs& G, PagedForm form, hipStream_t st) {
   const int64_t blocks = xcd_blocks((int64_t)G.A.S.batch * G.A.S.hkv, G.A.tiles * G.A.nsplit);
   constexpr int RB = row_width(W) * (int)sizeof(T);
   constexpr int OCC = RB == 128 ? 3 : (RB == 256 ? 2 : 1);
-  if (many)
+  constexpr int FEW = kPagedWaves, ALONE = alone_waves(RB);
+  if (form == PagedForm::kMany) {
     hipLaunchKernelGGL((k_attend_paged<T, W, 4, 1, 2, OCC>), grid1(blocks, 256), dim3(256), 0, st, G);
-  else
-    hipLaunchKernelGGL((k_attend_paged<T, W, 1, kPagedWaves, 1, (paged_groups(RB) * kPagedWaves + 3) / 4>), grid1(blocks, 64 * kPagedWaves),
-                       dim3(64 * kPagedWaves), 0, st, G);
+  } else if (ALONE == FEW || form == PagedForm::kFew) {
+    hipLaunchKernelGGL((k_attend_paged<T, W, 1, FEW, 1, (paged_groups(RB) * FEW + 3) / 4>), grid1(blocks, 64 * FEW), dim3(64 * FEW),
+                       0, st, G);
+  } else {
+    hipLaunchKernelGGL((k_attend_paged<T, W, 1, ALONE, 1, ALONE / 4>), grid1(blocks, 64 * ALONE), dim3(64 * ALONE), 0, st, G);
+  }
   SK_LAUNCH_CHECK();
 }
 
 // Instantiated once per element type (attend_paged_*.hip).
 template <class T>
-void attend_paged(const PagedArgs& G, bool many, hipStream_t st) {
+void attend_paged(const PagedArgs& G, PagedForm form, hipStream_t st) {
   const AttendArgs& A = G.A;
-  by_width(A.S.d, A.S.dv, [&](auto w) { attend_paged_launch<T, decltype(w)::value>(G, many, st); });
+  by_width(A.S.d, A.S.dv, [&](auto w) { attend_paged_launch<T, decltype(w)::value>(G, form, st); });
   if (A.opart) join_splits<T>(A, nullptr, st);
 }
 

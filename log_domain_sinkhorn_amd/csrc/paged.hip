@@ -10,45 +10,54 @@
 namespace sk {
 namespace attn {
 
-extern template void attend_paged<__bf16>(const PagedArgs&, bool, hipStream_t);
-extern template void attend_paged<_Float16>(const PagedArgs&, bool, hipStream_t);
-extern template void attend_paged<float>(const PagedArgs&, bool, hipStream_t);
+extern template void attend_paged<__bf16>(const PagedArgs&, PagedForm, hipStream_t);
+extern template void attend_paged<_Float16>(const PagedArgs&, PagedForm, hipStream_t);
+extern template void attend_paged<float>(const PagedArgs&, PagedForm, hipStream_t);
 
 namespace {
 
 struct PagedPlan {
-  bool many;
+  PagedForm form;
   int32_t nsplit;
   int64_t tiles, rows;
   int64_t o_off, ml_off, bytes;
 };
 
-// The two forms of the kernel: 128 rows against 64 keys a step, or 32 rows against 32
-// keys of each wave. step: microseconds of a step with `slots` workgroups on the
-// chip, by width (32, 64, 96, 128 columns), measured at 256 to 768 pairs of 4096 keys
-// that share their pages.
+// The forms of the kernel: 128 rows against 64 keys a step, or 32 rows against 32 keys
+// of each wave. step: microseconds of a step with `slots` workgroups on the chip, by
+// width (32, 64, 96, 128 columns), measured at 256 to 768 pairs of 4096 keys that share
+// their pages; of the form that is alone on its compute unit at 8 and 32 pairs of 250
+// to 2000 keys.
 struct Form {
-  bool many;
+  PagedForm form;
   int64_t rows, keys, slots;
   double step;
 };
-Form form_of(const sinkhorn_attention* a, bool many) {
+Form form_of(const sinkhorn_attention* a, PagedForm form) {
   const bool f32 = a->dtype == SINKHORN_F32;
   const int w = head_width(a->d, a->dv) / 32 - 1;
   const int64_t bytes = row_width(32 * (w + 1)) * elem_size(a);
-  static const double steps[2][2][4] = {{{1.4, 1.4, 1.1, 1.2}, {2.8, 2.8, 3.8, 4.8}}, {{1.5, 2.1, 1.9, 2.2}, {5.3, 9.1, 7.7, 10.1}}};
-  if (many) return Form{true, 128, 64, bytes <= 128 ? 768 : (bytes <= 256 ? 512 : 256), steps[1][f32][w]};
-  return Form{false, 32, 32 * kPagedWaves, 256 * paged_groups(bytes), steps[0][f32][w]};
+  static const double steps[3][2][4] = {{{1.5, 2.1, 1.9, 2.2}, {5.3, 9.1, 7.7, 10.1}},
+                                        {{1.4, 1.4, 1.1, 1.2}, {1.8, 2.8, 3.8, 4.8}},
+                                        {{1.6, 1.6, 2.2, 2.4}, {4.0, 6.0, 3.8, 4.8}}};
+  const double step = steps[(int)form][f32][w];
+  if (form == PagedForm::kMany) return Form{form, 128, 64, bytes <= 128 ? 768 : (bytes <= 256 ? 512 : 256), step};
+  if (form == PagedForm::kAlone) return Form{form, 32, 32 * alone_waves(bytes), 256, step};
+  return Form{form, 32, 32 * kPagedWaves, 256 * paged_groups(bytes), step};
 }
 
-// Microseconds of a call: rounds of workgroups, each with 4 to begin and end, and the
-// join: 4, and its partial results written and read at 4.5 TB/s. With fewer workgroups
-// on a compute unit than it holds a step is shorter.
+// Microseconds of a call on the device: rounds of workgroups, each with 4 to begin and
+// end, and the join: 4, and its partial results written and read at 4.5 TB/s. With fewer
+// workgroups on a compute unit than it holds a step is shorter. The least calls take
+// longer on the host, 12.5 and with a join's launch and workspace 16.5: what counts is
+// the mean of a call that waits for the host and one that is replayed (32 pairs of 64
+// columns bf16 over 1000 keys: split 9.9 and 16.6, not split 11.3 and 12.8).
 double cost_of(const Form& f, int64_t tiles, int64_t steps, int64_t n, double partial) {
   const int64_t blocks = tiles * n, rounds = ceil_div(blocks, f.slots), most = f.slots / 256;
   const int64_t held = std::min(ceil_div(blocks, 256), most);
   const double step = f.step * (0.4 + 0.6 * (double)held / (double)most);
-  return (double)rounds * ((double)ceil_div(steps, n) * step + 4.0) + (n > 1 ? 4.0 + (double)n * partial / 2.25e6 : 0.0);
+  const double device = (double)rounds * ((double)ceil_div(steps, n) * step + 4.0) + (n > 1 ? 4.0 + (double)n * partial / 2.25e6 : 0.0);
+  return 0.5 * (device + std::max(device, n > 1 ? 16.5 : 12.5));
 }
 
 // The form and the number of splits of the keys that cost least, for as many keys as
@@ -63,16 +72,18 @@ PagedPlan plan_paged(const sinkhorn_attention* a, const sinkhorn_pages* c, int64
   p.rows = a->len_q * group;
   const double partial = 4.0 * (double)(pairs * p.rows) * (double)(ceil_div(a->dv, 4) * 4 + 2);
   double least = 0.0;
-  for (int form = p.rows > 32; form >= 0; --form) {
-    const Form f = form_of(a, form != 0);
+  for (const PagedForm form : {PagedForm::kAlone, PagedForm::kFew, PagedForm::kMany}) {
+    if (form == PagedForm::kMany && p.rows <= 32) continue;
+    const Form f = form_of(a, form);
     const int64_t tiles = ceil_div(p.rows, f.rows);
+    if (form == PagedForm::kAlone && pairs * tiles > f.slots) continue;
     int64_t seen = c->table_len * (int64_t)c->page_size;
     if (recent > 0) {
       // the window of a tile's rows and the first keys, each with a tile cut at both ends
       const int64_t rows = std::min<int64_t>(a->len_q, f.rows / group + 2);
       seen = std::min(seen, std::min(first, seen) + std::min(recent, seen) + rows + 2 * f.keys);
     }
-    const int64_t steps = ceil_div(seen, f.keys), most = std::min<int64_t>(steps, 512);
+    const int64_t steps = ceil_div(seen, f.keys), most = form == PagedForm::kAlone ? 1 : std::min<int64_t>(steps, 512);
     int64_t n = 1, best = 1;
     double cost = 0.0;
     do {  // the fewest splits for each number of steps
@@ -91,7 +102,7 @@ PagedPlan plan_paged(const sinkhorn_attention* a, const sinkhorn_pages* c, int64
       best = std::max(best, std::min(ceil_div(4 * f.slots, pairs * tiles), std::max<int64_t>(1, steps / 8)));
     if (p.tiles == 0 || cost < least) {
       least = cost;
-      p.many = f.many;
+      p.form = form;
       p.tiles = tiles;
       p.nsplit = (int32_t)best;
     }
@@ -199,15 +210,16 @@ int sinkhorn_paged_attention(const sinkhorn_attention* a, const sinkhorn_pages* 
     G.by_heads = Divide(A.S.hkv);
     G.by_per = Divide(G.per);
     G.by_split = Divide(p.nsplit);
-    G.pair_up = p.many && p.nsplit == 1 && (int64_t)a->batch * a->heads_kv * p.tiles <= form_of(a, true).slots;
+    G.pair_up = p.form == PagedForm::kMany && p.nsplit == 1 &&
+                (int64_t)a->batch * a->heads_kv * p.tiles <= form_of(a, p.form).slots;
     G.qvec = rows_aligned(q, a->q_stride, a->d, size, 16);
     const hipStream_t st = (hipStream_t)stream;
     if (a->dtype == SINKHORN_BF16)
-      attend_paged<__bf16>(G, p.many, st);
+      attend_paged<__bf16>(G, p.form, st);
     else if (a->dtype == SINKHORN_F16)
-      attend_paged<_Float16>(G, p.many, st);
+      attend_paged<_Float16>(G, p.form, st);
     else
-      attend_paged<float>(G, p.many, st);
+      attend_paged<float>(G, p.form, st);
     return SINKHORN_OK;
   });
 }

@@ -255,6 +255,21 @@ def test_sharp_scores(sk, dtype, m):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("d,dv", [(32, 32), (64, 40), (96, 72), (128, 128)])
+@pytest.mark.parametrize("m", [1, 6, 37])
+@pytest.mark.parametrize("window", [{}, {"recent": 300, "first": 5}])
+def test_narrow_and_wide_tables(sk, dtype, d, dv, m, window):
+    # short sequences: a table with places for them alone is worked through by one workgroup
+    # a row tile, one with places for many more by several
+    _log(f"tables {dtype} {d} {dv} {m} {window}")
+    for extra in (0, 1000):
+        q, kc, vc, t, n = _make(dtype, [255, 0, 257, 512, 31, 700][:4 if m > 6 else 6], m, 4, 2, d, dv, 16, seed=d + m, extra=extra)
+        _check(sk, (q, kc, vc, t, n), f"{extra} places behind", **window)
+        t[3, 2], t[2, 16], t[0, 0] = -1, kc.shape[0], 1 << 30
+        _check(sk, (q, kc, vc, t, n), f"bad pages, {extra} places behind", **window)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 @pytest.mark.parametrize("d", [64, 128])
 def test_long_sequences_split(sk, dtype, d):
     """Many tiles a workgroup and many splits, page numbers beyond what a wave holds at a time."""

@@ -230,7 +230,8 @@ __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
   if (A.lengths_out) {
     const int before = paged_keys(A.P, b);
     const int64_t j = (int64_t)before + i, cap = (int64_t)A.P.len * A.P.size;
-    if (which == 1 && i == 0 && g == 0 && lane == 0) A.lengths_out[b] = (int)(before + ntokens < cap ? before + ntokens : cap);
+    const int64_t after = (int64_t)before + ntokens;
+    if (which == 1 && i == 0 && g == 0 && lane == 0) A.lengths_out[b] = (int)(after < cap ? after : cap);
     place = j;
     if (cache) {
       if (!live || j >= cap) return;

@@ -214,3 +214,13 @@ def test_graph_of_a_growing_cache(sk):
         torch.cuda.synchronize()
         assert torch.equal(lens, eager) and torch.equal(qo, qe)
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_lengths_next_to_2_31(sk):
+    """The new length stays within the table where the sum would pass 2^31 (no page: nothing is written)."""
+    _log("lengths next to 2^31")
+    size = 2 ** 31 - 8
+    kc = torch.empty(0, size, 1, 8, dtype=BF, device=DEV)
+    k = torch.ones(3, 20, 1, 8, dtype=BF, device=DEV)
+    lens, _ = sk.cache_append(k, k, kc, kc.clone(), _ints([[0], [0], [0]]), _ints([size - 5, 2 ** 31 - 1, size - 30]))
+    assert lens.tolist() == [size, size, size - 10]

@@ -106,18 +106,18 @@ struct PageTiles {
   // first key of tile n
   __device__ __forceinline__ int key(int n) const {
     const int x = n0 + n;
-    return (x < ns ? x : x - ns + t_lo) * KT;
+    return (int)((uint32_t)(x < ns ? x : x - ns + t_lo) * KT);
   }
   // Addresses for the batch of tiles that begins with tile n.
   __device__ __forceinline__ void locate(int n) {
     const int t = n + lane / GROUPS;
-    const int j = key(t) + wave * RW + 8 * (lane % GROUPS);
-    const bool live = t < count && j < nkeys;
+    const uint32_t j = (uint32_t)key(t) + wave * RW + 8 * (lane % GROUPS);  // behind the last tile it may pass 2^31
+    const bool live = t < count && j < (uint32_t)nkeys;
     uint32_t slot = 0;
     int32_t at = 0;
     if (live) {
-      const uint32_t page = P.page((uint32_t)j);
-      slot = (uint32_t)j - page * (uint32_t)P.size;
+      const uint32_t page = P.page(j);
+      slot = j - page * (uint32_t)P.size;
       at = table[page];
     }
     const bool in = live && (uint32_t)at < (uint32_t)P.pages;
@@ -584,10 +584,11 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
     const int x = end - G.recent;
     return G.recent == 0 || x < 0 ? 0 : x;
   };
+  // (a tile's end may pass 2^31: bounds are compared with its first key)
   int ns = 0, t_lo = 0, total = 0;
   const int last = row0 + 32 * WQ < nrows ? row0 + 32 * WQ - 1 : nrows - 1;
   if (row0 < nrows) {
-    const int end = end_of(last), t_end = (end + KT - 1) / KT;
+    const int end = end_of(last), t_end = end / KT + (end % KT != 0);
     t_lo = from_of(end_of(row0)) / KT;
     const int f = G.first < end ? G.first : end, n = f > 0 ? (f - 1) / KT + 1 : 0;
     ns = n < t_lo ? n : t_lo;
@@ -648,7 +649,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
     // that are no numbers? With many rows the workgroup looks together.
     bool odd = false;
     if constexpr (MANY) {
-      if (j0 + KT > b_lo || (j0 < b_hi && j0 + KT > G.first)) {
+      if (j0 > b_lo - KT || (j0 < b_hi && j0 > G.first - KT)) {
         if (no_numbers<T, KeyT::kTileBytes, NT>(tv, tid)) sm.keys.odd = it + 1;
         __syncthreads();
         odd = __builtin_amdgcn_readfirstlane(sm.keys.odd) == it + 1;
@@ -663,7 +664,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
         clear_no_numbers<T, KeyT::kOwnBytes, 64>(tv, lane);
       }
     };
-    if (j0 >= e_hi || (j0 + KW <= f_lo && j0 >= G.first)) {  // no row of this wave sees any
+    if (j0 >= e_hi || (j0 <= f_lo - KW && j0 >= G.first)) {  // no row of this wave sees any
       if constexpr (MANY) {
         if (odd) clear();
       } else {
@@ -692,11 +693,11 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
 #pragma unroll
         for (int e = 0; e < 16; ++e) sc[n][e] = fmaf(sc[n][e], S.scale, sc[n][e] * S.scale_lo);
     }
-    const bool all = j0 + KW <= e_lo && (j0 >= f_hi || j0 + KW <= G.first);  // every row sees every key
+    const bool all = j0 <= e_lo - KW && (j0 >= f_hi || j0 <= G.first - KW);  // every row sees every key
     // does the row see key i + 4 h of this wave's own? Without branches: a select each.
     const int f0 = from - j0 - 4 * h, g0 = (G.first < end ? G.first : end) - j0 - 4 * h;
     const uint32_t span = (uint32_t)(end - from);
-    auto seen = [&](int i) { return ((uint32_t)(i - f0) < span) | (i < g0); };
+    auto seen = [&](int i) { return ((uint32_t)i - (uint32_t)f0 < span) | (i < g0); };
     if (__builtin_expect(!all, 0)) {
 #pragma unroll
       for (int n = 0; n < NB; ++n)

@@ -330,13 +330,40 @@ def test_caches_beyond_32_bits(sk):
     small = _make(BF, [250, 300], 5, 4, 2, d, d, size, seed=16)
     ids = _ints([274999, 3, 1, 0, 9, 7, 70000, 270000, 5, 11, 2])[:small[1].shape[0]]
     kh[ids.long()] = small[1]
-    vh = kh.clone() if False else torch.empty(2, 275000, size, d, dtype=BF, device=DEV).permute(1, 2, 0, 3)
+    vh = torch.empty(2, 275000, size, d, dtype=BF, device=DEV).permute(1, 2, 0, 3)
     vh[ids.long()] = small[2]
     t = small[3].clone()
     ok = (t >= 0) & (t < small[1].shape[0])
     t[ok] = ids[t[ok].long()]
     want, got = sk.paged_attention(*small), sk.paged_attention(small[0], kh, vh, t, small[4])
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("m", [1, 70])
+@pytest.mark.parametrize("back", [0, 3, 100])
+def test_sequences_that_end_next_to_2_31(sk, dtype, m, back):
+    """One page of 2^31 - 8 slots that all lie in the same place: out is the value, lse the
+    score plus the log of the visible keys' number."""
+    _log(f"2^31 {dtype} {m} {back}")
+    size, d = 2 ** 31 - 8, 64
+    n = size - back
+    k = torch.full((1, 1, 1, d), 0.25, dtype=dtype, device=DEV).expand(1, size, 1, d)
+    v = torch.linspace(-8, 8, 64, device=DEV).round().to(dtype).view(1, 1, 1, d).expand(1, size, 1, d)
+    q = torch.full((1, m, 2, d), 0.5, dtype=dtype, device=DEV)
+    for kw in ({"recent": 100}, {"recent": 100, "first": 7}, {"recent": 2 ** 31 - 200}, {}):
+        out, lse = sk.paged_attention(q, k, v, _ints([[0]]), _ints([n]), scale=0.125, **kw)
+        p = n - m + torch.arange(m, dtype=torch.float64)  # places
+        recent = float(kw.get("recent", 2 ** 31))
+        seen = torch.minimum(p + 1, torch.full_like(p, recent + kw.get("first", 0)))
+        want = (1.0 + seen.log()).view(1, 1, m).expand(1, 2, m)
+        # scores are 1; weights 1 and their sums, whole numbers, are rounded to 24 bits
+        # when lanes and splits are joined, ten times at most; then a logarithm and a sum
+        assert_close(lse, want, torch.full_like(want, 2.0 ** -24 * (10 + 8 * 32)), f"lse {kw}")
+        # split 512 times a lane's sums are whole numbers below 2^24 times the value, exact; the
+        # bound leaves room for splits 2^11 times longer, then the joins' roundings and the result's
+        tol = (v[0, 0, 0].double().abs() * (2.0 ** -13 + (2.0 ** -8 if dtype == BF else 0.0)) + 2.0 ** -40).cpu()
+        assert_close(out, v[0, 0, 0].double().cpu().expand(1, m, 2, d), tol.expand(1, m, 2, d), f"out {kw}")
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)

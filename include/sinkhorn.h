@@ -576,6 +576,8 @@ int sinkhorn_cache_workspace(const sinkhorn_cache* cache, int64_t* bytes);
  * `interleaved` 2 i and 2 i + 1; elements from `rotated` on stay as n has them.
  * The angles are formed and reduced in 64 bits (so far positions lose nothing),
  * the rest is fp32, and a result is rounded once.
+ * Squares are fp32 numbers too: of a head with elements above 2^60, or with eps 0 of
+ * one with none above 2^-60, the norm passes fp32's range.
  *
  * Layout: q [batch][len][heads_q][d] and k [batch][len][heads_kv][d], and their
  * results and gradients, by strides in elements (batch, row, head), the last

@@ -503,7 +503,7 @@ def _ungraphed(t, name):
     """No call here records a graph: a tensor whose gradient would be lost is refused."""
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires grad: these calls record no graph; detach it or use torch.no_grad(), "
-                         "and take gradients from cross_attention_grad")
+                         "and take gradients from cross_attention_grad or rotate_heads_grad")
     # a tangent does not show in requires_grad; asked for only inside a dual level
     if getattr(_forward_ad, "_current_level", 0) >= 0 and _forward_ad.unpack_dual(t).tangent is not None:
         raise ValueError(f"{name} carries a tangent: these calls have no forward derivative; pass its primal")
@@ -927,11 +927,14 @@ def rotate_heads_grad(dq_out, dk_out=None, q=None, k=None, *, positions=None, fr
 
 
 def _pages(dtype, B, heads, d, k_cache, v_cache, page_table, lengths, name):
-    """The bytes that describe a paged cache of k [pages, page_size, heads, d] and v, and v's width."""
+    """The bytes that describe a paged cache of k [pages, page_size, heads, d] and v, v's width
+    and the heads (None: k's)."""
     _head_tensor(k_cache, "k_cache", dtype)
     _head_tensor(v_cache, "v_cache", dtype)
     pages, size, kh, kd = k_cache.shape
     vp, vsize, vh, dv = v_cache.shape
+    if heads is None:
+        heads = kh
     if kh != heads or kd != d:
         raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected (pages, page_size, {heads}, {d})")
     if vp != pages or vsize != size or vh != heads:
@@ -946,7 +949,7 @@ def _pages(dtype, B, heads, d, k_cache, v_cache, page_table, lengths, name):
         raise ValueError("the last dimension of page_table must be contiguous")
     _plain(lengths, name, torch.int32, (B,))
     return _pack_pages(size, width, pages, row if B > 1 else 0, *_strides(k_cache), *_strides(v_cache), dv,
-                       page_table.data_ptr(), lengths.data_ptr()), dv
+                       page_table.data_ptr(), lengths.data_ptr()), dv, heads
 
 
 def cache_append(k, v, k_cache, v_cache, page_table, cache_lengths, *, new_lengths=None, positions=None,
@@ -977,7 +980,7 @@ def cache_append(k, v, k_cache, v_cache, page_table, cache_lengths, *, new_lengt
         if q.shape[0] != B or q.shape[1] != n or q.shape[3] != d:
             raise ValueError(f"q has shape {tuple(q.shape)}, expected ({B}, {n}, heads, {d})")
     head, tail = _rotation(q, k, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, new_lengths)
-    c, width = _pages(k.dtype, B, h, d, k_cache, v_cache, page_table, cache_lengths, "cache_lengths")
+    c, width, _ = _pages(k.dtype, B, h, d, k_cache, v_cache, page_table, cache_lengths, "cache_lengths")
     if dv != width:
         raise ValueError(f"v has shape {tuple(v.shape)}, expected ({B}, {n}, {h}, {width})")
     _written(k_cache, "k_cache")
@@ -1012,10 +1015,9 @@ def paged_attention(q, k_cache, v_cache, page_table, key_lengths, *, scale=None,
     bytes, as are the cache's strides."""
     _head_tensor(q, "q")
     B, lq, hq, d = q.shape
-    hkv = _head_tensor(k_cache, "k_cache", q.dtype).shape[2]
+    c, dv, hkv = _pages(q.dtype, B, None, d, k_cache, v_cache, page_table, key_lengths, "key_lengths")
     if hkv < 1 or hq < 1 or hq % hkv:
         raise ValueError(f"{hq} query heads are no multiple of {hkv} key heads")
-    c, dv = _pages(q.dtype, B, hkv, d, k_cache, v_cache, page_table, key_lengths, "key_lengths")
     count = 0 if query_lengths is None else _plain(query_lengths, "query_lengths", torch.int32, (B,)).data_ptr()
     if recent is None:
         recent = 0

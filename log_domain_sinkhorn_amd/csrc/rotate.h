@@ -77,6 +77,19 @@ __device__ __forceinline__ typename Raw<T, E>::V narrow(const float (&x)[E]) {
   return v;
 }
 
+// Results of calls that move more than the last cache holds are written past it: written
+// into it they drive out each other and what is still to be read. 16384 tokens x 40 heads
+// of 128 bf16 (336 MB) 71 -> 58 us, with the backward pass 172 -> 145, a call and the next
+// reader of its results 95 either way, at 640 MB 204 -> 184; calls of 154 and 234 MB lose,
+// 28 -> 41 and with the reader 66 -> 70.
+template <bool PAST, class V>
+__device__ __forceinline__ void put(V* p, const V& x) {
+  if constexpr (PAST)
+    __builtin_nontemporal_store(x, p);
+  else
+    *p = x;
+}
+
 // cos and sin of `turns` whole turns. The reduction to x quarter turns, |x| <= 1/2,
 // is exact in 64 bits; sine and cosine of x pi / 2 by their Taylor sums, whose
 // first terms left out are below 2e-9 and 2e-10.
@@ -219,7 +232,7 @@ __device__ __forceinline__ float inverse_rms(const RotateArgs& A, float sum) {
 // workgroup takes one of the tensors; a token's heads are dealt to 1 << groups lane
 // groups, neighbours to neighbours, and U heads of a group are loaded before the
 // first is used.
-template <class T, int E, int LPH, int U, bool PAIRS>
+template <class T, int E, int LPH, int U, bool PAIRS, bool PAST>
 __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
   typedef typename Raw<T, E>::V V;
   const int which = (int)blockIdx.x < A.part[0].end ? 0 : ((int)blockIdx.x < A.part[1].end ? 1 : 2);
@@ -301,7 +314,7 @@ __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
       turn(x[0], x[1], c, s, l);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (l.has[k]) *(V*)(dst + h * R.ds[2] + l.at[k]) = turned[k] ? narrow<T, E>(x[k]) : raw[n][k];
+        if (l.has[k]) put<PAST>((V*)(dst + h * R.ds[2] + l.at[k]), turned[k] ? narrow<T, E>(x[k]) : raw[n][k]);
     }
   }
 }
@@ -311,7 +324,7 @@ __global__ __launch_bounds__(256) void k_rotate(RotateArgs A) {
 // A workgroup takes rows of one tensor; a lane adds up the weight's gradient of its
 // chunks over all that it meets; groups of a wave, waves and workgroups are then added
 // in a fixed order.
-template <class T, int E, int LPH, int U, bool PAIRS>
+template <class T, int E, int LPH, int U, bool PAIRS, bool PAST>
 __global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
   typedef typename Raw<T, E>::V V;
   __shared__ float sw[4][kMaxD];
@@ -381,7 +394,7 @@ __global__ __launch_bounds__(256) void k_rotate_grad(RotateArgs A) {
             if (live) acc[k][e] = fmaf(y[k][e], x[k][e] * r, acc[k][e]);
             x[k][e] = live ? r * fmaf(-m, x[k][e], y[k][e] * weight[k][e]) : 0.0f;
           }
-          if (l.has[k]) *(V*)(dst + h * R.ds[2] + l.at[k]) = narrow<T, E>(x[k]);
+          if (l.has[k]) put<PAST>((V*)(dst + h * R.ds[2] + l.at[k]), narrow<T, E>(x[k]));
         }
       }
     }
@@ -441,10 +454,18 @@ inline int32_t rotate_groups(int64_t tokens, int32_t heads, int32_t lanes) {
   return g;
 }
 
+// Do `arrays` read or written for each of q, k and v hold more than the last cache, 256 MB?
+// (Chunks of less than 16 bytes stay with plain stores, which join them in the caches.)
+inline bool beyond_cache(const RotateArgs& A, int arrays, size_t size) {
+  const int64_t row = (int64_t)(A.part[0].heads + A.part[1].heads) * A.d + (int64_t)A.part[2].heads * A.dv;
+  return (int64_t)A.batch * A.len * row * arrays * (int64_t)size > (int64_t(1) << 28);
+}
+
 // Instantiated once per element type (rotate_*.hip). e: elements of a chunk.
 template <class T>
 void rotate(RotateArgs& A, int e, hipStream_t st) {
   A.by_steps = Divide(A.steps);
+  const bool past = beyond_cache(A, 2, sizeof(T));
   by_chunk<T>(e, A.d > A.dv ? A.d : A.dv, A.interleaved, [&](auto chunk, auto lanes, auto pairs) {
     constexpr int E = decltype(chunk)::value, L = decltype(lanes)::value;
     constexpr bool P = decltype(pairs)::value;
@@ -457,7 +478,10 @@ void rotate(RotateArgs& A, int e, hipStream_t st) {
       }
       R.end = (int32_t)std::min<int64_t>(blocks, INT32_MAX);
     }
-    hipLaunchKernelGGL((k_rotate<T, E, L, 4, P>), grid1(blocks, 256), dim3(256), 0, st, A);
+    if (past && E * sizeof(T) == 16)
+      hipLaunchKernelGGL((k_rotate<T, E, L, 4, P, E * sizeof(T) == 16>), grid1(blocks, 256), dim3(256), 0, st, A);
+    else
+      hipLaunchKernelGGL((k_rotate<T, E, L, 4, P, false>), grid1(blocks, 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   });
 }
@@ -466,6 +490,7 @@ void rotate(RotateArgs& A, int e, hipStream_t st) {
 template <class T>
 void rotate_grad(RotateArgs& A, int e, int32_t blocks, hipStream_t st) {
   A.by_steps = Divide(A.len);
+  const bool past = beyond_cache(A, 3, sizeof(T));
   by_chunk<T>(e, A.d, A.interleaved, [&](auto chunk, auto lanes, auto pairs) {
     constexpr int E = decltype(chunk)::value, L = decltype(lanes)::value;
     constexpr bool P = decltype(pairs)::value;
@@ -475,7 +500,10 @@ void rotate_grad(RotateArgs& A, int e, int32_t blocks, hipStream_t st) {
     if (q.heads > 0 && q.end == 0) q.end = 1;
     if (k.heads > 0 && q.end == blocks) --q.end;
     k.end = blocks;
-    hipLaunchKernelGGL((k_rotate_grad<T, E, L, 2, P>), grid1(blocks, 256), dim3(256), 0, st, A);
+    if (past && E * sizeof(T) == 16)
+      hipLaunchKernelGGL((k_rotate_grad<T, E, L, 2, P, E * sizeof(T) == 16>), grid1(blocks, 256), dim3(256), 0, st, A);
+    else
+      hipLaunchKernelGGL((k_rotate_grad<T, E, L, 2, P, false>), grid1(blocks, 256), dim3(256), 0, st, A);
     SK_LAUNCH_CHECK();
   });
 }

@@ -224,3 +224,22 @@ def test_lengths_next_to_2_31(sk):
     k = torch.ones(3, 20, 1, 8, dtype=BF, device=DEV)
     lens, _ = sk.cache_append(k, k, kc, kc.clone(), _ints([[0], [0], [0]]), _ints([size - 5, 2 ** 31 - 1, size - 30]))
     assert lens.tolist() == [size, size, size - 10]
+
+
+def test_calls_beyond_the_last_cache(sk):
+    """More than 256 MB in a call (written past the caches) as in parts: the same bits."""
+    _log("beyond the cache")
+    B, L, H, d, size = 4, 6000, 16, 128, 32
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    k, v, q = (torch.randn(B, L, h, d, generator=gen, device=DEV).to(BF) for h in (H, H, 8))
+    assert 4 * k.numel() * 2 > 1 << 28 > 4 * (2 * k[0].numel() + q[0].numel())
+    pages = B * (L // size + 1)
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(5)).to(torch.int32).view(B, -1).to(DEV)
+    before = _ints([0, 5, 31, 32])
+    a, b = (torch.zeros(2, pages, size, H, d, dtype=BF, device=DEV) for _ in range(2))
+    kw = dict(frequencies=sk.rotary_frequencies(d, device=DEV))
+    lens, out = sk.cache_append(k, v, a[0], a[1], table, before, q=q, **kw)
+    for i in range(B):
+        n, o = sk.cache_append(k[i:i + 1], v[i:i + 1], b[0], b[1], table[i:i + 1], before[i:i + 1], q=q[i:i + 1], **kw)
+        assert torch.equal(n, lens[i:i + 1]) and torch.equal(o, out[i:i + 1])
+    assert torch.equal(a, b)

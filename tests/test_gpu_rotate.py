@@ -321,3 +321,25 @@ def test_graph_streams_and_repeats(sk):
         dq.copy_(dq.roll(1, 0))
         dk.copy_(dk.roll(1, 0))
         want = [t.clone() for t in step()]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("interleaved", [False, True], ids=["half", "pairs"])
+def test_calls_beyond_the_last_cache(sk, dtype, interleaved):
+    """More than 256 MB in a call (results go past the caches) as in parts: the same bits."""
+    _log(f"beyond the cache {dtype} {interleaved}")
+    B, L, H, d = 4, (6000 if dtype != torch.float32 else 3000), 24, 128
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    q, k, dq, dk = (torch.randn(B, L, h, d, generator=gen, device=DEV).to(dtype) for h in (H, 8, H, 8))
+    kw = dict(frequencies=sk.rotary_frequencies(96, device=DEV), interleaved=interleaved, norm_eps=1e-6)
+    assert 2 * q.numel() * q.element_size() > 1 << 28 > 3 * (q[0].numel() + k[0].numel()) * q.element_size()
+    got, grads = sk.rotate_heads(q, k, **kw), sk.rotate_heads_grad(dq, dk, q, k, **kw)
+    plain = sk.rotate_heads(q, k, frequencies=kw["frequencies"], interleaved=interleaved)
+    for b in range(B):
+        part = [x[b:b + 1] for x in (q, k, dq, dk)]
+        for x, y in zip(got, sk.rotate_heads(*part[:2], **kw)):
+            assert torch.equal(x[b:b + 1], y)
+        for x, y in zip(grads[:2], sk.rotate_heads_grad(part[2], part[3], part[0], part[1], **kw)[:2]):
+            assert torch.equal(x[b:b + 1], y)
+        for x, y in zip(plain, sk.rotate_heads(*part[:2], frequencies=kw["frequencies"], interleaved=interleaved)):
+            assert torch.equal(x[b:b + 1], y)

@@ -136,8 +136,9 @@ void run(const sinkhorn_rotation* r, RotateArgs& A, int e, hipStream_t st) {
 }
 
 // Workgroups of the backward pass with a norm: as many as the chip holds at a time,
-// three a compute unit (16384 tokens x 40 heads of 128 bf16: 768 108 us, 1024 114, 1536 109),
-// fewer where a wave would not find four heads; two at least, one for each tensor.
+// three a compute unit (16384 tokens x 40 heads of 128 bf16: 768 103 us, 1024 110, 1536
+// 103; 8192 x 40 of 64 29.6, 32.6, 31.7), fewer where a wave would not find four heads;
+// two at least, one for each tensor.
 int32_t grad_blocks(const sinkhorn_rotation* r) {
   const int64_t n = ceil_div(r->batch * r->len * (r->heads_q + r->heads_kv), 16);
   return (int32_t)(n < 2 ? 2 : (n > 768 ? 768 : n));

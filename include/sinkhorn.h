@@ -647,7 +647,8 @@ typedef struct {
   int64_t table_stride;             /* elements from one entry's pages to the next's */
   int64_t k_stride[3], v_stride[3]; /* elements: page, slot, head */
   int32_t dv;                       /* width of a value head, 1 .. 128 */
-  const int32_t* page_table;        /* device */
+  const int32_t* page_table;        /* device; may be NULL where table_len is 0, and where there are
+                                     * no pages and no token is appended */
   const int32_t* lengths;           /* device [batch]: keys in the cache, taken as within
                                      * [0, table_len * page_size]; before the call when appending */
 } sinkhorn_pages;

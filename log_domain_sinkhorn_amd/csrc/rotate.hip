@@ -282,7 +282,9 @@ int sinkhorn_cache_append(const sinkhorn_rotation* r, const sinkhorn_pages* c, c
     const bool rows = r->len > 0, places = c->table_len > 0 && c->pages > 0;
     require(v_stride != nullptr && c->lengths && lengths_out, "null pointer");
     require(!rows || (k && v && (r->heads_q == 0 || (q && q_out))), "null pointer");
-    require(!places || (k_cache && v_cache && c->page_table), "null pointer");
+    require(!places || (k_cache && v_cache), "null pointer");
+    // a token looks its place up before it knows that there are no pages
+    require(!(places || (rows && c->table_len > 0)) || c->page_table, "null page table");
     for (int i = 0; i < 3; ++i) require(v_stride[i] >= 0, "negative stride");
     const bool qsame = in_place(q_out, r->q_out_stride, q, r->q_stride);
     const int64_t size = elem_size(r->dtype), table[3] = {c->table_stride, 0, 0};

@@ -214,6 +214,15 @@ def test_append_refusals():
     assert _append(_desc(batch=0), _pages()) == sk.OK
 
 
+def test_append_without_a_table():
+    """A cache of no pages needs a table too where a token is appended: its places are looked up there."""
+    L = sk.lib()
+    for kw in (dict(pages=0), dict(pages=0, table_len=1), dict()):
+        assert _append(_desc(), _pages(page_table=None, **kw)) == sk.ERR_INVALID_ARG, kw
+        assert b"page table" in L.sinkhorn_last_error(), kw
+    assert _append(_desc(batch=0), _pages(pages=0, page_table=None)) == sk.OK
+
+
 def _att(**kw):
     a = dict(q=torch.zeros(2, 3, 4, 8, dtype=BF), k_cache=torch.zeros(4, 8, 2, 8, dtype=BF), v_cache=torch.zeros(4, 8, 2, 16, dtype=BF),
              page_table=torch.zeros(2, 2, dtype=I32), key_lengths=torch.zeros(2, dtype=I32))

@@ -286,11 +286,13 @@ __device__ __forceinline__ void soften(f32x16 (&sc)[NB], float f, float& m, floa
     for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[n][e]);
   mx = half_max(mx) * f;
   // a new reference only where the maximum rose by more than 2^8: weights
-  // stay below 2^8 and the accumulators are seldom rescaled
-  if (__any(mx > m + 8.0f)) {
-    const float mn = fmaxf(m, mx);
-    const float a = mn == -kInf ? 1.0f : ex2(m - mn);
-    m = mn;
+  // stay below 2^8 and the accumulators are seldom rescaled. Each row by its own
+  // maximum: the others of the wave keep their reference, and so their roundings,
+  // whatever this row's keys, which they may not see, hold
+  const bool rose = mx > m + 8.0f;
+  if (__any(rose)) {
+    const float a = rose ? ex2(m - mx) : 1.0f;
+    m = rose ? mx : m;
     l *= a;
 #pragma unroll
     for (int n = 0; n < NDB; ++n)

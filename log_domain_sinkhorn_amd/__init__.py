@@ -356,6 +356,18 @@ def _dev(t: torch.Tensor, dtype, name: str, shape=None) -> torch.Tensor:
     return t
 
 
+_increment_version = torch.autograd.graph.increment_version
+
+
+def _changed(*outputs):
+    """Tells autograd that a call wrote these tensors of the caller's (None: it had no such
+    one): a graph that saved one before then refuses its backward pass, as it does after
+    torch's own operations in place."""
+    for t in outputs:
+        if t is not None:
+            _increment_version(t)
+
+
 def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
@@ -659,12 +671,14 @@ def cross_attention(q, k, v, *, scale=None, key_bias=None, query_lengths=None, k
     _mass_args(a, row_weight, mass_in, mass_out)
     index = _same_device(q, (k, v, key_bias, query_lengths, key_lengths, row_weight, mass_in, mass_out, out, lse))
     device = q.device
+    given = out, lse, mass_out
     out = torch.empty(shape, dtype=q.dtype, device=device) if out is None else out
     lse = torch.empty((B, hq, lq), dtype=torch.float32, device=device) if lse is None else lse
     a.out_stride = _strides3(out)
     ws, n = _workspace(a, _ATTEND if mass_out is None else _ATTEND_MASS, device, q, k, v)
     _launch(index, "cross_attention", lib().sinkhorn_cross_attention, ctypes.byref(a), q.data_ptr(), k.data_ptr(),
             v.data_ptr(), out.data_ptr(), lse.data_ptr(), _at(row_weight), _at(mass_in), _at(mass_out), _at(ws), n)
+    _changed(*given)
     return out, lse
 
 
@@ -684,6 +698,7 @@ def cross_attention_grad(dout, q, k, v, out, lse, *, scale=None, key_bias=None, 
             _written(_head_tensor(t, name, q.dtype, like.shape), name)
     index = _same_device(q, (k, v, key_bias, query_lengths, key_lengths, dout, out, lse, dq, dk, dv))
     device = q.device
+    given = dq, dk, dv
     dq, dk, dv = (torch.empty(like.shape, dtype=q.dtype, device=device) if t is None else t
                   for t, like in ((dq, q), (dk, k), (dv, v)))
     a.out_stride, a.dout_stride = _strides3(out), _strides3(dout)
@@ -692,6 +707,7 @@ def cross_attention_grad(dout, q, k, v, out, lse, *, scale=None, key_bias=None, 
     _launch(index, "cross_attention_grad", lib().sinkhorn_cross_attention_grad, ctypes.byref(a), q.data_ptr(),
             k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
             dv.data_ptr(), _at(ws), n)
+    _changed(*given)
     return dq, dk, dv
 
 
@@ -704,11 +720,13 @@ def attention_mass(q, k, lse, *, scale=None, key_bias=None, query_lengths=None, 
     _plain(lse, "lse", torch.float32, (a.batch, a.heads_q, a.len_q))
     _mass_args(a, row_weight, mass_in, mass_out)
     index = _same_device(q, (k, key_bias, query_lengths, key_lengths, lse, row_weight, mass_in, mass_out))
+    given = mass_out
     if mass_out is None:
         mass_out = torch.empty((a.batch, a.heads_kv, a.len_k), dtype=torch.float32, device=q.device)
     ws, n = _workspace(a, _ATTENTION_MASS, q.device, q, k)
     _launch(index, "attention_mass", lib().sinkhorn_attention_mass, ctypes.byref(a), q.data_ptr(), k.data_ptr(),
             lse.data_ptr(), _at(row_weight), _at(mass_in), mass_out.data_ptr(), _at(ws), n)
+    _changed(given)
     return mass_out
 
 
@@ -749,6 +767,7 @@ def cache_evict(k, v, mass, keep: int, *, key_lengths=None, first: int = 0, rece
         _plain(lengths_out, "lengths_out", torch.int32, (B,))
     index = _same_device(k, (v, mass, key_lengths, k_out, v_out, mass_out, index_out, lengths_out))
     device = k.device
+    given = k_out, v_out, mass_out, index_out, lengths_out
     # without key_lengths every row of the outputs is written
     new = torch.empty if key_lengths is None else torch.zeros
     k_out = new((B, cap, h, d), dtype=k.dtype, device=device) if k_out is None else k_out
@@ -767,6 +786,7 @@ def cache_evict(k, v, mass, keep: int, *, key_lengths=None, first: int = 0, rece
     _launch(index, "cache_evict", lib().sinkhorn_cache_evict, ctypes.byref(c), k.data_ptr(), v.data_ptr(),
             mass.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), mass_out.data_ptr(), index_out.data_ptr(),
             lengths_out.data_ptr(), _at(ws), size.value)
+    _changed(*given)
     return k_out, v_out, mass_out, index_out, lengths_out
 
 
@@ -878,12 +898,14 @@ def rotate_heads(q, k=None, *, positions=None, frequencies=None, interleaved=Fal
     if k is not None:
         _head_tensor(k, "k")
     head, tail = _rotation(q, k, frequencies, interleaved, gain, norm_eps, q_weight, k_weight, positions, lengths)
+    given = q_out, k_out
     q_out, k_out = _result(q_out, q, "q_out"), _result(k_out, k, "k_out")
     index = _same_device(q, (k, frequencies, q_weight, k_weight, positions, lengths, q_out, k_out))
     ks, ko = (_NO_STRIDES, _NO_STRIDES) if k is None else (_strides(k), _strides(k_out))
     r = _pack_rotation(*head, *_strides(q), *ks, *_strides(q_out), *ko, *_NO_STRIDES, *_NO_STRIDES, *tail)
     _launch(index, "rotate_heads", lib().sinkhorn_rotate_heads, r, q.data_ptr(), _at(k), _at(q_weight), _at(k_weight),
             q_out.data_ptr(), _at(k_out))
+    _changed(*given)
     return q_out, k_out
 
 
@@ -906,6 +928,7 @@ def rotate_heads_grad(dq_out, dk_out=None, q=None, k=None, *, positions=None, fr
         qs = _strides(_head_tensor(q, "q", dq_out.dtype, dq_out.shape))
         if k is not None:
             ks = _strides(_head_tensor(k, "k", dk_out.dtype, dk_out.shape))
+    given = dq, dk
     dq, dk = _result(dq, dq_out, "dq"), _result(dk, dk_out, "dk")
     index = _same_device(dq_out, (dk_out, q, k, frequencies, q_weight, k_weight, positions, lengths, dq, dk))
     if dk is not None:
@@ -923,6 +946,7 @@ def rotate_heads_grad(dq_out, dk_out=None, q=None, k=None, *, positions=None, fr
         ws = torch.empty(n, dtype=torch.uint8, device=device)
     _launch(index, "rotate_heads_grad", lib().sinkhorn_rotate_heads_grad, r, dq_out.data_ptr(), _at(dk_out), _at(q), _at(k),
             _at(q_weight), _at(k_weight), dq.data_ptr(), _at(dk), _at(wq), _at(wk), _at(ws), n)
+    _changed(*given)
     return dq, dk, wq, wk
 
 
@@ -985,6 +1009,7 @@ def cache_append(k, v, k_cache, v_cache, page_table, cache_lengths, *, new_lengt
         raise ValueError(f"v has shape {tuple(v.shape)}, expected ({B}, {n}, {h}, {width})")
     _written(k_cache, "k_cache")
     _written(v_cache, "v_cache")
+    given = q_out, lengths_out
     if lengths_out is None:
         lengths_out = cache_lengths.new_empty(B)
     else:
@@ -997,6 +1022,7 @@ def cache_append(k, v, k_cache, v_cache, page_table, cache_lengths, *, new_lengt
     _launch(index, "cache_append", lib().sinkhorn_cache_append, r, c, _at(q), k.data_ptr(), v.data_ptr(),
             _strides3(v), _at(q_weight), _at(k_weight), _at(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
             lengths_out.data_ptr())
+    _changed(k_cache, v_cache, *given)
     return lengths_out, q_out
 
 
@@ -1027,6 +1053,7 @@ def paged_attention(q, k_cache, v_cache, page_table, key_lengths, *, scale=None,
         raise ValueError("recent must be >= 1")
     # as large as the C side takes them: a longer one means the same
     first, recent = max(-1, min(int(first), (1 << 63) - 1)), min(int(recent), (1 << 63) - 1)
+    given = out, lse
     if out is not None:
         _written(_head_tensor(out, "out", q.dtype, (B, lq, hq, dv)), "out")
     elif dv == d:
@@ -1046,6 +1073,7 @@ def paged_attention(q, k_cache, v_cache, page_table, key_lengths, *, scale=None,
     ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
     _launch(index, "paged_attention", lib().sinkhorn_paged_attention, a, c, first, recent, q.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), _at(ws), n)
+    _changed(*given)
     return out, lse
 
 
@@ -1111,6 +1139,7 @@ class Problem:
             self._pot(f_prev, self.n, "f_prev")
         _check(lib().sinkhorn_halfstep_f(self._h, float(eps), _ptr(g), _ptr(out), _ptr(f_prev),
                                          ctypes.byref(res) if res is not None else None), "halfstep_f")
+        _changed(out)
         return out, (res.value if res is not None else None)
 
     def halfstep_g(self, eps, f, out=None, g_prev=None):
@@ -1122,6 +1151,7 @@ class Problem:
             self._pot(g_prev, self.m, "g_prev")
         _check(lib().sinkhorn_halfstep_g(self._h, float(eps), _ptr(f), _ptr(out), _ptr(g_prev),
                                          ctypes.byref(res) if res is not None else None), "halfstep_g")
+        _changed(out)
         return out, (res.value if res is not None else None)
 
     def marginal_residual(self, eps, f, g):
@@ -1145,6 +1175,7 @@ class Problem:
         rep.history_cap = int(history)
         st = _check(lib().sinkhorn_solve(self._h, ctypes.byref(sc), _ptr(f), _ptr(g), ctypes.byref(rep)),
                     "solve")
+        _changed(f, g)
         out = _struct_dict(rep)
         out["history"] = list(buf[:min(rep.history_len, history)])
         out["status"] = st
@@ -1162,6 +1193,7 @@ class Problem:
             _dev(row_max, torch.float32, "row_max", (k,))
         _check(lib().sinkhorn_materialize_rows(self._h, float(eps), _ptr(f), _ptr(g), _ptr(rows), k,
                                                _ptr(T), _ptr(row_max)), "materialize_rows")
+        _changed(T, row_max)
         return T, row_max
 
     def materialize_rows_noalloc(self, eps, f, g, rows, T, row_max=None):
@@ -1177,6 +1209,7 @@ class Problem:
         _check(lib().sinkhorn_materialize_rows_noalloc(self._h, float(eps), _ptr(f), _ptr(g), _ptr(rows),
                                                        k, _ptr(T), _ptr(row_max)),
                "materialize_rows_noalloc")
+        _changed(T, row_max)
         return T, row_max
 
     def min_row(self, eps, f, g) -> float:
@@ -1246,6 +1279,7 @@ class Problem:
                                                 _ptr(out), _ptr(f_prev),
                                                 ctypes.byref(res) if res is not None else None),
                "sparse_halfstep_f")
+        _changed(out)
         return out, (res.value if res is not None else None)
 
     def sparse_halfstep_g(self, eps, f, B, ptr, idx, out=None, g_prev=None):
@@ -1256,6 +1290,7 @@ class Problem:
                                                 _ptr(out), _ptr(g_prev),
                                                 ctypes.byref(res) if res is not None else None),
                "sparse_halfstep_g")
+        _changed(out)
         return out, (res.value if res is not None else None)
 
     def sparsify(self, eps, f, g, threshold: float, batch: int = 1024, cap=None):
@@ -1289,6 +1324,7 @@ class Problem:
         T, grad = self._bary_out(T, grad, want_T, want_grad)
         _check(lib().sinkhorn_barycentric(self._h, float(eps), _ptr(g), _ptr(f_hint), _ptr(T), _ptr(grad)),
                "barycentric")
+        _changed(T, grad)
         return T, grad
 
     def sparse_barycentric(self, eps, g, B, ptr, idx, f_hint=None, T=None, grad=None, want_T=True,
@@ -1300,6 +1336,7 @@ class Problem:
         T, grad = self._bary_out(T, grad, want_T, want_grad)
         _check(lib().sinkhorn_sparse_barycentric(self._h, float(eps), _ptr(g), _ptr(f_hint), int(B), _ptr(ptr),
                                                  _ptr(idx), _ptr(T), _ptr(grad)), "sparse_barycentric")
+        _changed(T, grad)
         return T, grad
 
     def _bary_out(self, T, grad, want_T, want_grad):
@@ -1344,6 +1381,7 @@ class Problem:
         rep = _MultiscaleReportC()
         st = _check(lib().sinkhorn_solve_multiscale(self._h, ctypes.byref(c), _ptr(f), _ptr(g),
                                                     ctypes.byref(rep)), "solve_multiscale")
+        _changed(f, g)
         out = _struct_dict(rep)
         out["status"] = st
         return f, g, out

@@ -69,3 +69,63 @@ def test_rows_of_a_wave_are_independent(sk, dtype, m, lens, d, window):
                 o[b, see, :2], z[b, :2, see] = out[b, see, :2], lse[b, :2, see]
                 same = torch.equal(o, out), torch.equal(z, lse)
                 assert same == (True, True), (size, b, j)
+
+
+def test_written_tensors_raise_their_version(sk):
+    """What a call writes of the caller's is marked as changed, what it reads is not."""
+    _log("versions")
+    B, L, H, d, size = 2, 4, 2, 32, 8
+    mk = lambda *s: torch.randn(*s, device=DEV)  # noqa: E731
+    q, k, v, y = (mk(B, L, H, d) for _ in range(4))
+    f, table, have = sk.rotary_frequencies(d, device=DEV), _ints([[0, 1], [2, 3]]), _ints([5, 9])
+    kc, vc = mk(4, size, H, d), mk(4, size, H, d)
+    new = lambda *s, t=F32: torch.zeros(*s, dtype=t, device=DEV)  # noqa: E731
+    I32 = torch.int32
+    out, lse = sk.cross_attention(q, k, v)
+    mass = mk(B, H, L).abs()
+    P = sk.Problem(mk(9, 2), mk(7, 2), None, None, 1.0)
+    g, rows = torch.zeros(7, device=DEV), torch.arange(3, device=DEV)
+    f0 = P.halfstep_f(0.1, g)[0]
+    calls = [
+        (lambda o: sk.rotate_heads(q, k, frequencies=f, **o), dict(q_out=new(B, L, H, d), k_out=new(B, L, H, d)), (q, k)),
+        (lambda o: sk.rotate_heads(o["q_out"], None, frequencies=f, q_out=o["q_out"]), dict(q_out=q.clone()), (f,)),
+        (lambda o: sk.rotate_heads_grad(y, k, q, v, frequencies=f, norm_eps=1e-6, **o), dict(dq=new(B, L, H, d), dk=new(B, L, H, d)), (q, k, v, y)),
+        (lambda o: sk.rotate_heads_grad(o["dq"], frequencies=f, dq=o["dq"]), dict(dq=y.clone()), (f,)),
+        (lambda o: sk.cache_append(k, v, o["kc"], o["vc"], table, have, q=q, q_out=o["q"], lengths_out=o["n"], frequencies=f),
+         dict(kc=kc.clone(), vc=vc.clone(), q=new(B, L, H, d), n=new(B, t=I32)), (q, k, v, table, have)),
+        (lambda o: sk.paged_attention(q, kc, vc, table, have, **o), dict(out=new(B, L, H, d), lse=new(B, H, L)), (q, kc, vc)),
+        (lambda o: sk.cross_attention(q, k, v, **o), dict(out=new(B, L, H, d), lse=new(B, H, L), mass_out=new(B, H, L)), (q, k, v)),
+        (lambda o: sk.cross_attention_grad(y, q, k, v, out, lse, **o), {n: new(B, L, H, d) for n in ("dq", "dk", "dv")}, (q, k, v, y, out, lse)),
+        (lambda o: sk.attention_mass(q, k, lse, **o), dict(mass_out=new(B, H, L)), (q, k, lse)),
+        (lambda o: sk.cache_evict(k, v, mass, 3, **o), dict(k_out=new(B, 3, H, d), v_out=new(B, 3, H, d), mass_out=new(B, H, 3),
+                                                            index_out=new(B, H, 3, t=I32), lengths_out=new(B, t=I32)), (k, v, mass)),
+        (lambda o: P.halfstep_f(0.1, g, **o), dict(out=new(9)), (g,)),
+        (lambda o: P.halfstep_g(0.1, f0, **o), dict(out=new(7)), (f0,)),
+        (lambda o: P.solve(sk.Schedule(1.0, 0.5, fixed_iters=2), **o), dict(f=new(9), g=new(7)), ()),
+        (lambda o: P.materialize_rows(0.1, f0, g, rows, **o), dict(T=new(3, 7), row_max=new(3)), (f0, g)),
+        (lambda o: P.materialize_rows_noalloc(0.1, f0, g, rows, **o), dict(T=new(3, 7), row_max=new(3)), (f0, g)),
+        (lambda o: P.barycentric(0.1, g, **o), dict(T=new(9, 2), grad=new(9, 2)), (g,)),
+    ]
+    for i, (call, outputs, inputs) in enumerate(calls):
+        before, read = {n: t._version for n, t in outputs.items()}, [t._version for t in inputs]
+        call(outputs)
+        assert all(t._version > before[n] for n, t in outputs.items()), i
+        assert [t._version for t in inputs] == read, i
+    P.close()
+
+
+def test_a_graph_that_saved_a_written_tensor_refuses(sk):
+    """In place on an intermediate, without a graph: the backward pass that saved it raises
+    instead of going on with other values."""
+    _log("saved")
+    f = sk.rotary_frequencies(32, device=DEV)
+    x = torch.randn(3, 8, 4, 32, device=DEV, requires_grad=True)
+    one, other = torch.ones(1, 1, 4, 32, device=DEV), torch.zeros(3, 8, 4, 32, device=DEV)
+    for write in (lambda t: sk.rotate_heads(t, frequencies=f, q_out=t), lambda t: sk.rotate_heads_grad(t, frequencies=f, dq=t),
+                  lambda t: sk.cache_append(one, one, t, other, _ints([[1]]), _ints([0]))):
+        y = x * 2.0
+        loss = (y * y).sum()
+        with torch.no_grad():
+            write(y)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()

@@ -275,9 +275,16 @@ __device__ __forceinline__ void score_tile(const char* tk, int kb0, int lane, co
   }
 }
 
+// fp16 holds weights below 2^-14 in steps of 2^-24, and none below 2^-25: thousands of
+// them that together matter would be lost. Its reference lies 2^7 below the maximum,
+// so that they begin at 2^-21 and 2^-32 of it (the largest weight, 2^15, is within
+// fp16); a power of two moves nothing else. bf16 has fp32's range.
+template <class T>
+constexpr float kLift = std::is_same<T, _Float16>::value ? 7.0f : 0.0f;
+
 // One tile's scores of a row become weights 2^(f sc - m); m, the sum l and the
 // result o follow the running reference.
-template <int NB, int NDB>
+template <class T, int NB, int NDB>
 __device__ __forceinline__ void soften(f32x16 (&sc)[NB], float f, float& m, float& l, f32x16 (&o)[NDB]) {
   float mx = -kInf;
 #pragma unroll
@@ -285,14 +292,15 @@ __device__ __forceinline__ void soften(f32x16 (&sc)[NB], float f, float& m, floa
 #pragma unroll
     for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[n][e]);
   mx = half_max(mx) * f;
-  // a new reference only where the maximum rose by more than 2^8: weights
-  // stay below 2^8 and the accumulators are seldom rescaled. Each row by its own
-  // maximum: the others of the wave keep their reference, and so their roundings,
-  // whatever this row's keys, which they may not see, hold
-  const bool rose = mx > m + 8.0f;
+  // a new reference only where the maximum rose by more than 2^8: weights stay
+  // below 2^8 (2^15 with kLift) and the accumulators are seldom rescaled. Each row by
+  // its own maximum: the others of the wave keep their reference, and so their
+  // roundings, whatever this row's keys, which they may not see, hold
+  const bool rose = mx - m > 8.0f + kLift<T>;  // (an exact difference where it is that small)
   if (__any(rose)) {
-    const float a = rose ? ex2(m - mx) : 1.0f;
-    m = rose ? mx : m;
+    const float mn = rose ? mx - kLift<T> : m;
+    const float a = rose ? ex2(m - mn) : 1.0f;
+    m = mn;
     l *= a;
 #pragma unroll
     for (int n = 0; n < NDB; ++n)
@@ -716,7 +724,7 @@ __global__ __launch_bounds__(64 * WQ * WK, OCC) void k_attend_paged(PagedArgs G)
           for (int e = 0; e < 4; ++e) sc[n][4 * g + e] = in ? sc[n][4 * g + e] : -kInf;
         }
     }
-    soften<NB, NDB>(sc, f, m, l, o);
+    soften<T, NB, NDB>(sc, f, m, l, o);
     if constexpr (!MANY) {
       keys.wait(2 * it + 1);
       if (__builtin_expect(!all, 0)) odd = __any(no_numbers<T, KeyT::kOwnBytes, 64>(tv, lane));

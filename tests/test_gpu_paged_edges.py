@@ -129,3 +129,45 @@ def test_a_graph_that_saved_a_written_tensor_refuses(sk):
             write(y)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             loss.backward()
+
+
+@pytest.mark.parametrize("m", [1, 16, 40, 200])
+@pytest.mark.parametrize("apart", [10.0, 16.0, 18.0, 20.0])
+@pytest.mark.parametrize("at", [0, 300])
+def test_many_small_weights_in_fp16(sk, m, apart, at):
+    """One key takes nearly all of a row's weight and holds zeros; the result is what the
+    thousands of others add up to, whose weights fp16 alone could not hold."""
+    _log(f"small weights {m} {apart} {at}")
+    n, d = 3000, 64
+    gen = torch.Generator().manual_seed(22)
+    q, kc, vc, table, _ = _make(HF, [n], m, 1, 1, d, 16, seed=22)
+    q.zero_()
+    q[..., 0] = 1.0
+    kc.zero_()
+    value = (64.0 + 64.0 * torch.rand(n, d, generator=gen)).to(HF)
+    value[at] = 0.0
+    ids = table[0, :(n + 15) // 16].long()
+    places = torch.zeros(len(ids) * 16, 1, d, dtype=HF)
+    places[:n, 0] = value
+    vc[ids] = places.view(-1, 16, 1, d).to(DEV)
+    kc[ids[at // 16], at % 16, 0, 0] = apart
+    # the same for 4 x 64 heads: as many pairs as do not need their keys split
+    kc, vc = (x.expand(-1, -1, 64, -1) for x in (kc, vc))
+    out, lse = sk.paged_attention(q.expand(4, m, 64, d), kc, vc, table.expand(4, -1), _ints([n] * 4), scale=1.0)
+    for x, axes in ((out, (0, 2)), (lse, (0, 1))):
+        assert torch.equal(x, x.narrow(axes[0], 0, 1).narrow(axes[1], 0, 1).expand_as(x))
+    v, E = value.double(), 2.0 ** -24
+    for i in {0, m // 2, m - 1}:
+        see = n - m + i + 1
+        s = torch.zeros(see, dtype=torch.float64)
+        s[at] = apart
+        z = torch.logsumexp(s, 0)
+        w = torch.exp(s - z)
+        y, W = w @ v[:see], w @ v[:see].abs()
+        # a held weight is off by half a step, 2^-11 of it or 2^-25 where it is small, and the
+        # largest is held as 2^7 or more: 2^-32 of the sum. fp32: the score (one product), the
+        # exponential and sums of `see` terms. The result is rounded once
+        rel = E * (apart + 16 + see + 64)
+        tol = (2.0 ** -11 * 1.01 + 2 * rel) * W + 2.0 ** -32 * 1.01 * v[:see].abs().sum(0) + 2.0 ** -11 * 1.01 * y.abs() + 2.0 ** -25
+        assert_close(out[0, i, 0], y, tol, f"row {i}")
+        assert abs(float(lse[0, 0, i]) - float(z)) <= rel + 4 * E * float(z) + 4 * E, i

@@ -39,6 +39,7 @@ __global__ __launch_bounds__(256) void k_weight_join(RotateArgs A, float* dq, fl
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[tid][e] += s[tid + k][e];
   }
+  __syncthreads();
   if (tid < 4 && col + tid < A.d) out[col + tid] = s[0][tid];
 }
 

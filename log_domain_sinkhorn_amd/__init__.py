@@ -248,7 +248,14 @@ def _packer(cls):
     codes = {_i32: "i", _i64: "q", _f64: "d", _p: "P", _i64x2: "2q", _i64x3: "3q"}
     s = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_) + "0q")
     assert s.size == ctypes.sizeof(cls)
-    return s.pack
+
+    def pack(*values):
+        try:
+            return s.pack(*values)
+        except struct.error as e:
+            raise ValueError(f"a size or stride is out of range ({e})") from None
+
+    return pack
 
 
 _pack_attention, _pack_rotation, _pack_pages = (_packer(c) for c in (_AttentionC, _RotationC, _PagesC))

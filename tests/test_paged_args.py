@@ -299,3 +299,18 @@ def test_paged_attention_refusals():
     assert _attend(_adesc(), c, ws=AT[1]) == sk.ERR_INVALID_ARG and b"overlaps" in L.sinkhorn_last_error()
     assert _attend(_adesc(batch=0), _pages()) == sk.OK
     assert _attend(_adesc(len_q=0), _pages()) == sk.OK
+
+
+def test_sizes_beyond_the_descriptions():
+    """Sizes that the C side's fields do not hold are the caller's error like any other."""
+    many = 1 << 31
+    with pytest.raises(ValueError, match="size"):  # slots of a page
+        wide = torch.zeros(1, 1, 2, 8, dtype=BF).expand(1, many, 2, 8)
+        sk.paged_attention(**_att(k_cache=wide, v_cache=wide))
+    with pytest.raises(ValueError, match="size"):  # pages of a sequence
+        sk.cache_append(**_app(page_table=torch.empty(0, many, dtype=I32), k=torch.zeros(0, 3, 2, 8, dtype=BF),
+                               v=torch.zeros(0, 3, 2, 16, dtype=BF), cache_lengths=torch.zeros(0, dtype=I32)))
+    # sequences (on the device: here the descriptions alone)
+    for pack, n in ((sk._pack_rotation, 34), (sk._pack_attention, 38)):
+        with pytest.raises(ValueError, match="size"):
+            pack(0, many, *[0] * (n - 2))

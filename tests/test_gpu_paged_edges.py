@@ -171,3 +171,149 @@ def test_many_small_weights_in_fp16(sk, m, apart, at):
         tol = (2.0 ** -11 * 1.01 + 2 * rel) * W + 2.0 ** -32 * 1.01 * v[:see].abs().sum(0) + 2.0 ** -11 * 1.01 * y.abs() + 2.0 ** -25
         assert_close(out[0, i, 0], y, tol, f"row {i}")
         assert abs(float(lse[0, 0, i]) - float(z)) <= rel + 4 * E * float(z) + 4 * E, i
+
+
+def _far(t, axis):
+    """t's values in memory where `axis` (of two places) lies 2^32 elements and a little apart."""
+    shape, d = t.shape, t.shape[3]
+    far, near = (1 << 32) + 8 * d, [0, 0, 0]
+    n = d
+    for a in (2, 1, 0):
+        near[a] = far if a == axis else n
+        n *= 1 if a == axis else shape[a]
+    x = torch.empty(far + n, dtype=t.dtype, device=DEV).as_strided(shape, (*near, 1))
+    x.copy_(t)
+    assert torch.equal(x, t)
+    return x
+
+
+@pytest.mark.parametrize("axis", [0, 1, 2], ids=["sequences", "rows", "heads"])
+@pytest.mark.parametrize("interleaved", [False, True], ids=["half", "pairs"])
+def test_rotation_beyond_32_bits(sk, axis, interleaved):
+    """Operands, results and gradients whose elements lie beyond 2^32, as in one piece."""
+    _log(f"far {axis} {interleaved}")
+    gen = torch.Generator().manual_seed(23)
+    shape = [3, 3, 3, 128]
+    shape[axis] = 2
+    q, k, dq, dk = (torch.randn(shape, generator=gen).to(BF).to(DEV) for _ in range(4))
+    kw = dict(frequencies=sk.rotary_frequencies(96, device=DEV), interleaved=interleaved)
+    for norm in (None, 1e-6):
+        kw["norm_eps"] = norm
+        want, grads = sk.rotate_heads(q, k, **kw), sk.rotate_heads_grad(dq, dk, q, k, **kw)
+        a, b = _far(q, axis), _far(torch.zeros_like(q), axis)
+        got = sk.rotate_heads(a, k, q_out=b, **kw)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        got = sk.rotate_heads(q, a, k_out=b, **kw)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[0])
+        c = _far(dq, axis)
+        got = sk.rotate_heads_grad(c, dk, a, k, dq=b, **kw)
+        assert all(torch.equal(x, y) for x, y in zip(got, grads) if y is not None)
+        c.copy_(dk)
+        a.copy_(k)
+        got = sk.rotate_heads_grad(dq, c, q, a, dk=b, **kw)
+        assert all(torch.equal(x, y) for x, y in zip(got, grads) if y is not None)
+        del a, b, c
+
+
+@pytest.mark.parametrize("axis", [0, 1, 2], ids=["sequences", "rows", "heads"])
+def test_appending_from_beyond_32_bits(sk, axis):
+    _log(f"append far {axis}")
+    gen = torch.Generator().manual_seed(24)
+    shape = [3, 3, 3, 128]
+    shape[axis] = 2
+    q, k, v = (torch.randn(shape, generator=gen).to(BF).to(DEV) for _ in range(3))
+    B, L, H, d = shape
+    table = torch.arange(B, dtype=torch.int32, device=DEV).view(B, 1)
+    kw = dict(frequencies=sk.rotary_frequencies(d, device=DEV), norm_eps=1e-6)
+    near, far = ([torch.zeros(B, 8, H, d, dtype=BF, device=DEV) for _ in range(2)] for _ in range(2))
+    _, want = sk.cache_append(k, v, *near, table, _ints([2] * B), q=q, **kw)
+    _, got = sk.cache_append(_far(k, axis), _far(v, axis), *far, table, _ints([2] * B), q=q, q_out=_far(torch.zeros_like(q), axis), **kw)
+    assert torch.equal(got, want) and all(torch.equal(x, y) for x, y in zip(far, near))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("m", [1, 4, 50])
+@pytest.mark.parametrize("window", [{}, {"recent": 20, "first": 3}])
+def test_lengths_beyond_the_table(sk, dtype, m, window):
+    """A length beyond the table's places is taken as their number, below 0 as none."""
+    _log(f"beyond the table {dtype} {m} {window}")
+    args = _make(dtype, [96, 96, 96, 96], m, 4, 2, 64, 16, seed=25)
+    args[4] = _ints([2 ** 31 - 1, 97, -7, 95])
+    out, lse = sk.paged_attention(*args, **window)
+    ref = PagedRef(*args, **window)
+    assert_close(out, ref.out, ref.out_tol, "out")
+    assert_close(lse, ref.lse, ref.lse_tol, "lse")
+    want = sk.paged_attention(*args[:4], _ints([96, 96, 0, 95]), **window)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("d,dv,r", [(50, 33, 26), (64, 128, 64), (80, 8, 40), (1, 1, 0), (127, 126, 126)])
+@pytest.mark.parametrize("interleaved", [False, True], ids=["half", "pairs"])
+def test_appending_leaves_what_lies_around_a_row(sk, dtype, d, dv, r, interleaved):
+    """Rows that start anywhere, with other data in front of, between and behind them."""
+    _log(f"around {dtype} {d} {dv} {r}")
+    gen = torch.Generator().manual_seed(26)
+    pages, size, H, B, L = 6, 8, 3, 2, 11
+    whole, views = [], []
+    for w in (d, dv):
+        t = torch.randn(pages * size * H * (w + 3) + 4, generator=gen).to(dtype).to(DEV)
+        whole.append(t)
+        views.append(t[1:-3].view(pages, size, H, w + 3)[..., :w])
+    before = [t.clone() for t in whole]
+    table = _ints([[4, 0, 7], [-1, 5, 2]])  # pages 1 and 3 are nobody's, 7 and -1 are none
+    k, v, q = (torch.randn(B, L, H, w, generator=gen).to(dtype).to(DEV) for w in (d, dv, d))
+    qw = torch.randn(B * L * H * (d + 3) + 4, generator=gen).to(dtype).to(DEV)
+    qo, qb = qw[1:-3].view(B, L, H, d + 3)[..., :d], qw.clone()
+    new = [9, 11]
+    sk.cache_append(k, v, *views, table, _ints([3, 6]), new_lengths=_ints(new), q=q, q_out=qo, interleaved=interleaved, norm_eps=1e-6,
+                    frequencies=sk.rotary_frequencies(r, device=DEV))
+    places = [(4, s) for s in range(3, 8)] + [(0, s) for s in range(4)] + [(5, s) for s in range(8)] + [(2, 0)]
+    for x, t, b in zip(views, whole, before):
+        assert not torch.equal(t, b)
+        old = b[1:-3].view(pages, size, H, -1)[..., :x.shape[3]]
+        for at in places:
+            x[at] = old[at]
+        assert torch.equal(t, b)
+    assert not torch.equal(qw, qb)
+    qo.copy_(qb[1:-3].view(B, L, H, d + 3)[..., :d])
+    assert torch.equal(qw, qb)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("new", [1, 5])
+def test_evicted_cache_as_pages_of_one_sequence(sk, dtype, new):
+    """The contiguous cache's operators and the paged ones together: keys are appended to a cache in
+    one piece (a page a sequence), weighed and pruned; tokens that follow go behind those kept,
+    at the positions they have in the text, and see all that is left."""
+    _log(f"evicted {dtype} {new}")
+    B, Hq, H, d, size, keep = 2, 4, 2, 64, 128, 40
+    gen = torch.Generator().manual_seed(27)
+    mk = lambda n, h: torch.randn(B, n, h, d, generator=gen).to(dtype).to(DEV)  # noqa: E731
+    table, lens = torch.arange(B, dtype=torch.int32, device=DEV).view(B, 1), [100, 77]
+    kw = dict(frequencies=sk.rotary_frequencies(d, device=DEV), norm_eps=1e-6)
+    kc, vc, k2, v2 = (torch.zeros(B, size, H, d, dtype=dtype, device=DEV) for _ in range(4))
+    have, q = sk.cache_append(mk(100, H), mk(100, H), kc, vc, table, _ints([0] * B), new_lengths=_ints(lens), q=mk(100, Hq), **kw)
+    out, lse = sk.cross_attention(q[:, -1:], kc, vc, key_lengths=have)
+    mass = sk.attention_mass(q[:, -1:], kc, lse, key_lengths=have)
+    _, _, _, index, kept = sk.cache_evict(kc, vc, mass, keep, key_lengths=have, first=4, recent=8, k_out=k2[:, :keep], v_out=v2[:, :keep])
+    assert kept.tolist() == [keep] * B
+    for b in range(B):
+        for h in range(H):
+            at = index[b, h].long()
+            assert torch.equal(k2[b, :keep, h], kc[b, at, h]) and torch.equal(v2[b, :keep, h], vc[b, at, h])
+    k, v, x = mk(new, H), mk(new, H), mk(new, Hq)
+    places = (have[:, None] + torch.arange(new, device=DEV)).int()  # in the text, not in the cache
+    total, q = sk.cache_append(k, v, k2, v2, table, kept, positions=places, q=x, **kw)
+    assert total.tolist() == [keep + new] * B
+    qr, kr = sk.rotate_heads(x, k, positions=places, **kw)
+    assert torch.equal(q, qr) and torch.equal(k2[:, keep:keep + new], kr) and torch.equal(v2[:, keep:keep + new], v)
+    assert not k2[:, keep + new:].any() and not v2[:, keep + new:].any()
+    got, z = sk.paged_attention(q, k2, v2, table, total)
+    ref = PagedRef(q, k2, v2, table, total)
+    assert_close(got, ref.out, ref.out_tol, "out")
+    assert_close(z, ref.lse, ref.lse_tol, "lse")
+    # the last token sees all keys, as in the contiguous operator
+    o, y = sk.cross_attention(q[:, -1:], k2, v2, key_lengths=total)
+    assert_close(o, ref.out[:, -1:], ref.out_tol[:, -1:], "contiguous out")
+    assert_close(y, ref.lse[:, :, -1:], ref.lse_tol[:, :, -1:], "contiguous lse")

@@ -466,13 +466,14 @@ int sinkhorn_sparse_barycentric(sinkhorn_problem* p, double eps, const float* g,
  * gradient or weight. Lengths outside [0, len] are taken as the nearest bound.
  * Anything non-finite elsewhere gives non-finite results.
  *
- * Arithmetic: scores, softmax statistics and all sums in fp32; with 16-bit
- * types the weights (and in the backward pass their derivatives) are rounded
- * to that type for the product that follows, but where all rows of a key head
- * are at most 32 the weights are held in two such parts, so that out is off by its
- * own rounding (fp16: weights below 2^-25 of a row's largest are lost either way);
- * fp16 gradients want a loss scale that keeps weight x (dout . v)
- * between 2^-14 and 65504 where it counts. fp32 products are fp32 throughout. Results
+ * Arithmetic: scores, softmax statistics and all sums in fp32; with 16-bit types the
+ * weights (and in the backward pass their derivatives) are rounded to that type for
+ * the product that follows, but where all rows of a key head are at most 32 the
+ * weights are held in two such parts, so that out is off by its own rounding (fp16:
+ * weights below 2^-25 of a row's largest are lost either way); fp16 gradients want a
+ * loss scale that keeps weight x (dout . v) between 2^-14 and 65504 where it counts.
+ * fp32 products are fp32 throughout. Scores should stay below 2^24 in size: above it
+ * fp32's steps are larger than 1, and from 2^26 on results may be no numbers. Results
  * do not depend on scheduling: no atomics on floating point, splits are joined in a
  * fixed order.
  *
@@ -682,9 +683,9 @@ int sinkhorn_cache_append(const sinkhorn_rotation* rot, const sinkhorn_pages* ca
  * < 0, say) and rows at or behind query_lengths give out = 0 and lse = -infinity.
  * Pages wholly outside the windows of all rows are not read and may be gone.
  *
- * Arithmetic as of sinkhorn_cross_attention: 16-bit weights are rounded once with more
- * than 32 rows of a key head, which adds about as much as out's own rounding (bf16
- * 0.0022 relative in place of 0.0017), and held in two parts with at most 32. In fp16
+ * Arithmetic as of sinkhorn_cross_attention: with at most 32 rows of a key head 16-bit
+ * weights are held in two parts; with more they may be rounded once, which adds about
+ * as much as out's own rounding (bf16 0.0022 relative in place of 0.0017). In fp16
  * weights count down to 2^-32 of a row's largest.
  *
  * Rows of the cache must be whole, aligned units of 16 bytes (d and dv multiples of

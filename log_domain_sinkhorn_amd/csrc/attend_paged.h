@@ -317,9 +317,13 @@ __device__ __forceinline__ void soften(f32x16 (&sc)[NB], float f, float& m, floa
     }
 }
 
-// o += weights times the values of keys kb0 .. of the tile. MANY rows; with few,
-// which wait for memory, not for products, weights of 16-bit types go in two parts,
-// so that a token's result is off by its own rounding alone.
+// o += weights times the values of keys kb0 .. of the tile. With few rows, which wait for
+// memory, not for products, weights of 16-bit types go in two parts, so that a token's
+// result is off by its own rounding alone. With MANY a weight is rounded once, to the
+// type: half a step each (2^-9 to 2^-8 of it in bf16), which over a row adds about as much
+// as the result's own rounding (bf16 0.0022 relative to 64 bits in place of 0.0017). A
+// second part costs a third: 2048 rows over 16384 keys x 32 heads of 128 567 -> 753 us,
+// prompts of 8192 x 32 heads of 64 under a window 115 -> 151, 4 x 512 over 4096 158 -> 204.
 template <class T, int DP, bool MANY, int NB, int NDB>
 __device__ __forceinline__ void add_values(const char* tv, int kb0, int lane, const f32x16 (&sc)[NB], f32x16 (&o)[NDB]) {
   using V8 = typename Vec<T>::V8;
